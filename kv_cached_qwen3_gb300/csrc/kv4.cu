@@ -1,0 +1,340 @@
+// Rows written to and read from the 4-bit paged cache, and streams reordered by sharing pages.
+#include "kv4.cuh"
+
+using namespace talker_dev;
+
+namespace talker_k {
+
+namespace {
+
+constexpr int kRowThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, bool vec, float (&x)[8]);
+template <>
+__device__ __forceinline__ void load8<float>(const float *p, bool vec, float (&x)[8]) {
+    if (vec) {
+        const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = p[i];
+    }
+}
+template <>
+__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16 *p, bool vec, float (&x)[8]) {
+    if (vec) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[2 * i] = bf16lo(w[i]), x[2 * i + 1] = bf16hi(w[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __bfloat162float(p[i]);
+    }
+}
+__device__ __forceinline__ void store8(float *p, bool vec, const float (&x)[8]) {
+    if (vec) {
+        *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4 *>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = x[i];
+    }
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, bool vec, const float (&x)[8]) {
+    if (vec) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = __float2bfloat16_rn(x[i]);
+    }
+}
+
+// Grid (items, streams, layers * 2): thread = 8 dims of one (row, head) of K or V; the 4 * NB
+// threads of a head row are neighbours, rows of a head follow one another.
+template <int HD, typename T, bool READ>
+__global__ void __launch_bounds__(kRowThreads) k_kv4_rows(const Kv4Rows r, const bool vec) {
+    using Tile = Kv4Tile<HD>;
+    constexpr int NB = Tile::NB, TPR = 4 * NB;
+    const int s = blockIdx.y, l = blockIdx.z >> 1;
+    const bool is_v = blockIdx.z & 1;
+    const int sub = threadIdx.x % TPR, b = sub >> 2, c = sub & 3;
+    const unsigned item = blockIdx.x * (kRowThreads / TPR) + threadIdx.x / TPR;
+    const int h = (int)(item / (unsigned)r.T), i = (int)(item - (unsigned)h * r.T);
+    bool on = h < r.c.n_kv_heads && (r.count == nullptr || i < r.count[s]);
+    T *dense = static_cast<T *>(is_v ? r.v : r.k) + (l * r.st.layer + s * r.st.stream + i * r.st.row + h * r.st.head) +
+               b * 32 + c * 8;
+    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (!READ && on) load8<T>(dense, vec, x);
+    unsigned char *tile = nullptr;
+    int prow = 0;
+    if (on) {
+        const long long pos = (r.start != nullptr ? (long long)r.start[s] : 0) + i;
+        if (pos < 0 || pos >= (long long)r.c.pages_per_stream * kPage) {
+            if (sub == 0 && r.c.status != nullptr) atomicOr(r.c.status, ST_BAD_POSITION);
+            on = false;
+        } else {
+            const int page = r.c.page_table[(size_t)(r.stream0 + s) * r.c.pages_per_stream + (int)(pos / kPage)];
+            prow = (int)(pos % kPage);
+            if (page < 0 || page >= r.c.n_pages) {
+                if (sub == 0 && r.c.status != nullptr) atomicOr(r.c.status, ST_BAD_ARG);
+                on = false;
+            } else {
+                tile = static_cast<unsigned char *>(is_v ? r.c.v : r.c.k) +
+                       (((size_t)page * r.c.n_layers + r.layer0 + l) * r.c.n_kv_heads + h) * Tile::kBytes;
+            }
+        }
+    }
+    if constexpr (!READ) {
+        unsigned short d;
+        const uint32_t w = q4_codes8(x, d);
+        if (!on) return;
+        q4_store_codes<NB>(tile + prow * Tile::kRow, is_v, b, c, w);
+        if (c == 0) *reinterpret_cast<unsigned short *>(tile + Tile::kScales + (prow * NB + b) * 2) = d;
+    } else {
+        if (!on) return;
+        const uint32_t w = q4_load_codes<NB>(tile + prow * Tile::kRow, is_v, b, c);
+        const float d = __half2float(*reinterpret_cast<const __half *>(tile + Tile::kScales + (prow * NB + b) * 2));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = (float)((int)((w >> (4 * e)) & 15u) - 8) * d;
+        store8(dense, vec, x);
+    }
+}
+
+template <int HD, typename T, bool READ>
+cudaError_t launch_rows_t(const Kv4Rows &r, bool vec, cudaStream_t s) {
+    const long long items = (long long)r.T * r.c.n_kv_heads;
+    const int per = kRowThreads / (HD / 8);
+    const dim3 grid((unsigned)((items + per - 1) / per), r.n_streams, 2 * r.n_layers);
+    k_kv4_rows<HD, T, READ><<<grid, kRowThreads, 0, s>>>(r, vec);
+    return cudaGetLastError();
+}
+
+// ---- reorder
+
+// One warp per page-table column j. Row i of the new table keeps its parent's page where that is
+// full (shared) or, at the parent's tail page, where i is the parent's first child; every other
+// row needs a page of its own, and takes the pages of the column's set {r * pps + j} that no
+// kept entry uses, in order. A row refers to one page of a column, so there are always enough.
+__global__ void __launch_bounds__(256) k_reorder_table(const KvReorder r) {
+    __shared__ uint32_t used_s[8][32], seen_s[8][32], need_s[8][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int j = blockIdx.x * 8 + warp;
+    const bool first = blockIdx.x == 0 && warp == 0;
+    if (j >= r.pps) return;
+    uint32_t *used = used_s[warp], *seen = seen_s[warp], *need = need_s[warp];
+    used[lane] = seen[lane] = need[lane] = 0;
+    __syncwarp();
+    const int cap = r.pps * kPage;
+    for (int base = 0; base < r.n_streams; base += 32) {
+        const int i = base + lane;
+        const bool in = i < r.n_streams;
+        int p = in ? (i < r.R ? r.parents[i] : i) : -1 - lane, keep = -1;
+        bool own = false;
+        if (in) {
+            if (p < 0 || p >= r.n_streams) {
+                if (first && r.status != nullptr) atomicOr(r.status, ST_BAD_ARG);
+                p = i;
+            }
+            int len = r.lens[p];
+            if (len < 0 || len > cap) {
+                if (first && r.status != nullptr) atomicOr(r.status, ST_BAD_POSITION);
+                len = min(max(len, 0), cap);
+            }
+            if (first) r.lens_out[i] = len;
+            const int tail = len / kPage;
+            const int entry = r.table[(size_t)p * r.pps + j];
+            const int er = entry / r.pps;
+            const bool ok = entry >= 0 && entry - er * r.pps == j && er < r.n_streams;
+            if (!ok && j <= tail && r.status != nullptr) atomicOr(r.status, ST_BAD_ARG);
+            if (ok && j < tail) keep = er;
+            own = ok && j == tail;
+            if (own) keep = er;
+        }
+        // the first child of a parent takes its tail page over
+        const uint32_t same = __match_any_sync(0xffffffffu, p);
+        if (own && ((same & ((1u << lane) - 1)) != 0 || (seen[p >> 5] >> (p & 31) & 1u))) keep = -1;
+        __syncwarp();
+        if (in) atomicOr(&seen[p >> 5], 1u << (p & 31));
+        if (keep >= 0) {
+            atomicOr(&used[keep >> 5], 1u << (keep & 31));
+            r.table_out[(size_t)i * r.pps + j] = keep * r.pps + j;
+        }
+        const uint32_t wants = __ballot_sync(0xffffffffu, in && keep < 0);
+        if (lane == 0) need[base >> 5] = wants;
+        __syncwarp();
+    }
+    // free pages of the column: lane holds word `lane` of their set and how many lie before it
+    uint32_t fw = ~used[lane];
+    const int left = r.n_streams - 32 * lane;
+    fw &= left >= 32 ? 0xffffffffu : (left > 0 ? (1u << left) - 1 : 0u);
+    int before = __popc(fw);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += t;
+    }
+    before -= __popc(fw);
+    int taken = 0;
+    for (int base = 0; base < r.n_streams; base += 32) {
+        const uint32_t wants = need[base >> 5];
+        const bool mine = wants >> lane & 1u;
+        int k = taken + __popc(wants & ((1u << lane) - 1));
+        taken += __popc(wants);
+        int word = 0;   // the last word with at most k free pages before it
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            if (__shfl_sync(0xffffffffu, before, word + o) <= k) word += o;
+        uint32_t bits = __shfl_sync(0xffffffffu, fw, word);
+        k -= __shfl_sync(0xffffffffu, before, word);
+        if (mine) {
+            while (k-- > 0) bits &= bits - 1;
+            r.table_out[(size_t)(base + lane) * r.pps + j] = (32 * word + __ffs(bits) - 1) * r.pps + j;
+        }
+    }
+}
+
+// The rows of tail pages whose stream did not take its parent's page over: one warp per tile.
+// Sources are pages that stay in use, destinations pages that nothing in use refers to.
+__global__ void __launch_bounds__(256) k_reorder_copy(const KvReorder r) {
+    const int i = blockIdx.y;
+    int p = i < r.R ? r.parents[i] : i;
+    if (p < 0 || p >= r.n_streams) p = i;
+    const int len = min(max(r.lens[p], 0), r.pps * kPage);
+    const int col = len / kPage, rows = len % kPage;
+    if (rows == 0) return;
+    const int src = r.table[(size_t)p * r.pps + col], dst = r.table_out[(size_t)i * r.pps + col];
+    const int sr = src / r.pps;
+    if (src == dst || src < 0 || src - sr * r.pps != col || sr >= r.n_streams) return;
+    const int t = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (t >= 2 * r.n_tiles) return;
+    unsigned char *pool = t < r.n_tiles ? r.k : r.v;
+    const size_t off = (size_t)(t < r.n_tiles ? t : t - r.n_tiles) * r.tile_bytes;
+    const uint4 *from = reinterpret_cast<const uint4 *>(pool + src * r.page_bytes + off);
+    uint4 *to = reinterpret_cast<uint4 *>(pool + dst * r.page_bytes + off);
+    const int codes = rows * r.row_bytes / 16, scales = (rows * r.scale_bytes + 15) / 16, sc0 = kPage * r.row_bytes / 16;
+    for (int e = lane; e < codes; e += 32) to[e] = from[e];
+    for (int e = lane; e < scales; e += 32) to[sc0 + e] = from[sc0 + e];
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_rows(const Kv4Rows &r, int dtype, bool read, cudaStream_t s) {
+    if (r.T == 0 || r.n_streams == 0 || r.n_layers == 0) return cudaSuccess;
+    const int size = dtype == TALKER_DTYPE_BF16 ? 2 : 4, v = 16 / size;
+    // 16-byte accesses where every head row starts on a 16-byte boundary
+    const bool vec = !((reinterpret_cast<uintptr_t>(r.k) | reinterpret_cast<uintptr_t>(r.v)) & 15u) &&
+                     r.st.layer % v == 0 && r.st.stream % v == 0 && r.st.row % v == 0 && r.st.head % v == 0;
+    const bool bf16 = dtype == TALKER_DTYPE_BF16;
+    if (r.c.head_dim == 128) {
+        if (read) return bf16 ? launch_rows_t<128, __nv_bfloat16, true>(r, vec, s) : launch_rows_t<128, float, true>(r, vec, s);
+        return bf16 ? launch_rows_t<128, __nv_bfloat16, false>(r, vec, s) : launch_rows_t<128, float, false>(r, vec, s);
+    }
+    if (read) return bf16 ? launch_rows_t<64, __nv_bfloat16, true>(r, vec, s) : launch_rows_t<64, float, true>(r, vec, s);
+    return bf16 ? launch_rows_t<64, __nv_bfloat16, false>(r, vec, s) : launch_rows_t<64, float, false>(r, vec, s);
+}
+
+cudaError_t launch_kv_reorder(const KvReorder &r, cudaStream_t s) {
+    k_reorder_table<<<(r.pps + 7) / 8, 256, 0, s>>>(r);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    k_reorder_copy<<<dim3((2 * r.n_tiles + 7) / 8, r.n_streams), 256, 0, s>>>(r);
+    return cudaGetLastError();
+}
+
+}  // namespace talker_k
+
+// ---- C-ABI
+
+using namespace talker_k;
+
+namespace {
+
+bool sizes_ok(int n_layers, int n_kv, int hd) {
+    return n_layers >= 1 && n_kv >= 1 && (hd == 64 || hd == 128) &&
+           (long long)n_layers * n_kv <= 0x7fffffffll / kv4_tile_bytes(hd);
+}
+
+struct Span {
+    const int32_t *p;
+    size_t n;
+};
+
+talker_status status_of(cudaError_t e) {
+    if (e == cudaSuccess) return TALKER_OK;
+    cudaGetLastError();
+    return TALKER_ECUDA;
+}
+
+talker_status rows_call(const talker_kv4 *c, int layer0, int n_layers, int stream0, int n_streams,
+                        const int32_t *start, const int32_t *count, int T, void *k, void *v, int dtype,
+                        const talker_kv4_strides *st, bool read, void *cuda_stream) {
+    if (!kv4_cache_ok(c) || !k || !v || !st || T < 0 || n_layers < 0 || n_streams < 0) return TALKER_EINVAL;
+    if (layer0 < 0 || layer0 > c->n_layers - n_layers || stream0 < 0 || stream0 > c->n_streams - n_streams)
+        return TALKER_EINVAL;
+    if (n_layers > 32767 || n_streams > 65535 || (long long)T * c->n_kv_heads > 0x7fffffffll) return TALKER_EINVAL;
+    if (dtype != TALKER_DTYPE_F32 && dtype != TALKER_DTYPE_BF16) return TALKER_EINVAL;
+    if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) % (dtype == TALKER_DTYPE_F32 ? 4 : 2))
+        return TALKER_EINVAL;
+    const Kv4Rows r{*c, layer0, n_layers, stream0, n_streams, start, count, T, k, v, *st};
+    return status_of(launch_kv4_rows(r, dtype, read, static_cast<cudaStream_t>(cuda_stream)));
+}
+
+}  // namespace
+
+namespace talker_k {
+
+bool kv4_cache_ok(const talker_kv4 *c) {
+    return c && c->k && c->v && c->page_table && sizes_ok(c->n_layers, c->n_kv_heads, c->head_dim) && c->n_pages >= 1 &&
+           c->n_streams >= 1 && c->pages_per_stream >= 1 && c->pages_per_stream <= 0x7fffffff / talker_dev::kPage &&
+           !((reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v)) & 15u);
+}
+
+}  // namespace talker_k
+
+extern "C" {
+
+size_t talker_kv4_page_bytes(int n_layers, int n_kv_heads, int head_dim) {
+    return sizes_ok(n_layers, n_kv_heads, head_dim) ? (size_t)n_layers * n_kv_heads * kv4_tile_bytes(head_dim) : 0;
+}
+
+talker_status talker_kv4_write(const talker_kv4 *c, int layer0, int n_layers, int stream0, int n_streams,
+                               const int32_t *start, const int32_t *count, int T, const void *k, const void *v,
+                               int dtype, const talker_kv4_strides *strides, void *cuda_stream) {
+    return rows_call(c, layer0, n_layers, stream0, n_streams, start, count, T, const_cast<void *>(k),
+                     const_cast<void *>(v), dtype, strides, false, cuda_stream);
+}
+
+talker_status talker_kv4_read(const talker_kv4 *c, int layer0, int n_layers, int stream0, int n_streams,
+                              const int32_t *start, const int32_t *count, int T, void *k, void *v, int dtype,
+                              const talker_kv4_strides *strides, void *cuda_stream) {
+    return rows_call(c, layer0, n_layers, stream0, n_streams, start, count, T, k, v, dtype, strides, true, cuda_stream);
+}
+
+talker_status talker_kv4_reorder(const talker_kv4 *c, const int32_t *parents, int R, const int32_t *lens,
+                                 int32_t *table_out, int32_t *lens_out, void *cuda_stream) {
+    if (!kv4_cache_ok(c) || !lens || !table_out || !lens_out || R < 0 || R > c->n_streams || (R > 0 && !parents))
+        return TALKER_EINVAL;
+    if (c->n_streams > kReorderMaxStreams || (long long)c->n_streams * c->pages_per_stream > c->n_pages)
+        return TALKER_EINVAL;
+    const size_t nt = (size_t)c->n_streams * c->pages_per_stream, ns = c->n_streams;
+    const Span in[3] = {{c->page_table, nt}, {lens, ns}, {parents, (size_t)R}}, out[2] = {{table_out, nt}, {lens_out, ns}};
+    for (const Span &o : out)
+        for (const Span &i : in)
+            if (o.p < i.p + i.n && i.p < o.p + o.n) return TALKER_EINVAL;
+    if (table_out < lens_out + ns && lens_out < table_out + nt) return TALKER_EINVAL;
+    const int tile = kv4_tile_bytes(c->head_dim), tiles = c->n_layers * c->n_kv_heads;
+    const KvReorder r{static_cast<unsigned char *>(c->k), static_cast<unsigned char *>(c->v), (size_t)tiles * tile,
+                      tiles, c->head_dim / 2, c->head_dim / 16, tile, c->page_table, lens, parents, table_out, lens_out,
+                      c->status, c->n_streams, c->pages_per_stream, R};
+    return status_of(launch_kv_reorder(r, static_cast<cudaStream_t>(cuda_stream)));
+}
+
+}  // extern "C"

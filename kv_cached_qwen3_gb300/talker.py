@@ -91,6 +91,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "talker_test_gemm_bf16": (st, [vp, ctypes.c_int, ctypes.c_int, vp, ctypes.c_int, vp, ctypes.c_int,
                                        ctypes.c_int, vp]),
         "talker_test_gemm_swiglu_bf16": (st, [vp, ctypes.c_int, ctypes.c_int, vp, ctypes.c_int, vp, vp]),
+        "talker_kv4_page_bytes": (ctypes.c_size_t, [ctypes.c_int] * 3),
+        "talker_kv4_write": (st, [vp] + [ctypes.c_int] * 4 + [vp, vp, ctypes.c_int, vp, vp, ctypes.c_int, vp, vp]),
+        "talker_kv4_read": (st, [vp] + [ctypes.c_int] * 4 + [vp, vp, ctypes.c_int, vp, vp, ctypes.c_int, vp, vp]),
+        "talker_kv4_attend_scratch": (ctypes.c_size_t, [vp] + [ctypes.c_int] * 3),
+        "talker_kv4_attend": (st, [vp, ctypes.c_int, ctypes.c_int, vp, ctypes.c_int, ctypes.c_int, ctypes.c_float, vp,
+                                   i64, vp, vp, i64, ctypes.c_int, vp, vp, ctypes.c_size_t, vp]),
+        "talker_kv4_reorder": (st, [vp, vp, ctypes.c_int, vp, vp, vp, vp]),
+        "talker_beam_scratch": (ctypes.c_size_t, [ctypes.c_int] * 3),
+        "talker_beam_select": (st, [vp, i64, ctypes.c_int, vp, vp] + [ctypes.c_int] * 4 + [vp] * 5 +
+                               [ctypes.c_size_t, vp]),
     }
     for name, (res, args) in proto.items():
         fn = getattr(lib, name)
