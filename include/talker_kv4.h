@@ -26,7 +26,8 @@
  * Argument checks run before anything is enqueued. What only the device can see
  * (lengths, page numbers, parents) is checked there: what is out of range is
  * skipped as described and sets a bit of *status (when status is not NULL):
- * 1 << 0 a position or length outside the stream's pages, 1 << 3 a page number
+ * 1 << 0 a position or length outside the stream's pages, 1 << 1 a copy that did
+ * not arrive within a second (the row is NaN), 1 << 3 a page number
  * or parent out of range. Nothing is allocated; every call may be captured into
  * a CUDA graph; scratch need not hold anything on entry, and calls that may run
  * at the same time need scratch of their own.
