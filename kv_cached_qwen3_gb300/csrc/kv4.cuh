@@ -101,11 +101,15 @@ struct Kv4Attend {
     int64_t q_row, new_row;
     void *out;
     float scale;
-    int splits;
+    int grid, one_unit;   // Kv4AttendShape
     float *scratch;
 };
-int kv4_attend_splits(int B, int n_kv, int head_dim, int max_len, int n_sm);
-size_t kv4_attend_scratch(int B, int n_q, int head_dim, int splits);
+// CTAs of a launch, and whether each (stream, KV head) row is one CTA's work (no scratch then).
+struct Kv4AttendShape {
+    int grid, one_unit;
+};
+Kv4AttendShape kv4_attend_shape(int B, int n_kv, int max_len, int n_sm);
+size_t kv4_attend_scratch(const Kv4AttendShape &p, int head_dim);
 cudaError_t launch_kv4_attend(const Kv4Attend &a, int in_bf16, int out_bf16, cudaStream_t s);
 
 // Streams reordered by sharing pages (talker_kv4_reorder), for any page layout of n_tiles tiles a

@@ -11,11 +11,12 @@ namespace talker_k {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kSlots = 2;                 // pages (K and V tile) a warp has in shared memory
+constexpr int kCtas = 3;                  // CTAs a multiprocessor holds: 12 warps, 168 registers
+constexpr int kSlots = 3;                 // tiles (a page's K, its V, the next page's K ...) a warp has in shared memory
 constexpr int kMaxG = 8;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kSlack = 4.f;             // how far (base 2) scores may pass the reference before O is rescaled
-constexpr float kTop = 1024.f;            // scaled value scales stay below this
+constexpr int kTopBits = 14;              // probabilities times value scales stay below 2^14 (fp16) ...
+constexpr int kNewBits = 9;               // ... and are brought below 2^9 when they would pass it
 
 __device__ __forceinline__ float ex2(float x) {   // relative error about 2^-22, 0 at -inf
     float y;
@@ -27,57 +28,117 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// d = a b
+__device__ __forceinline__ void mma16816_new(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 // (lo, hi) as an fp16 pair, rounded towards zero
 __device__ __forceinline__ uint32_t pack_rz(float lo, float hi) {
     uint32_t r;
     asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// what is left of x after its first 11 bits (the fp16 part that pack_rz keeps)
-__device__ __forceinline__ float rest11(float x, uint32_t mask) { return x - __uint_as_float(__float_as_uint(x) & mask); }
+// ... and to nearest
+__device__ __forceinline__ uint32_t pack_rn(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 __device__ __forceinline__ uint32_t pack_half(__half lo, __half hi) {
     return (uint32_t)__half_as_ushort(lo) | ((uint32_t)__half_as_ushort(hi) << 16);
 }
 __device__ __forceinline__ float half_lo(uint32_t u) { return __half2float(__ushort_as_half((unsigned short)u)); }
 __device__ __forceinline__ float half_hi(uint32_t u) { return __half2float(__ushort_as_half((unsigned short)(u >> 16))); }
 
-// Nibbles 0 and 4 of u as an fp16 pair of (code - 8), and nibbles 1 and 5: the code goes under the
-// exponent of 1024 (or as 16 code), where fp16 holds it exactly.
-__device__ __forceinline__ uint32_t codes_even(uint32_t u) {
-    const uint32_t x = (u & 0x000f000fu) | 0x64006400u;
+// Two codes share a byte, and both operands made of it are the byte's low part: the low nibble n0 by
+// one AND, and the whole byte n0 + 16 n1, whose product takes n0's part along (the other operand, or
+// the result, takes it off again). As fp16 subnormals both are exact, times 2^-24.
+__device__ __forceinline__ uint32_t bytes02(uint32_t w) { return w & 0x00ff00ffu; }
+__device__ __forceinline__ uint32_t bytes13(uint32_t w) { return __byte_perm(w, 0, 0x4341); }
+__device__ __forceinline__ uint32_t nibbles(uint32_t bytes) { return bytes & 0x000f000fu; }
+// x - 8 of nibbles or x - 136 of bytes (8 + 16 8) as fp16 values: they go under the exponent of 1024.
+__device__ __forceinline__ uint32_t centred(uint32_t x, uint32_t mid) {
     uint32_t r;
-    asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x64086408u));           // - 1032
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x | 0x64006400u), "r"(mid));
     return r;
 }
-__device__ __forceinline__ uint32_t codes_odd(uint32_t u) {
-    const uint32_t x = (u & 0x00f000f0u) | 0x64006400u;
-    uint32_t r;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0x2c002c00u), "r"(0xd480d480u));   // / 16 - 72
-    return r;
-}
+constexpr uint32_t kMidNibble = 0x64086408u, kMidByte = 0x64886488u;   // 1032, 1160
 
+// Two f32 values in one 64-bit register, each instruction computing both.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float f2_lo(F2 x) { return __uint_as_float((uint32_t)x.v); }
+__device__ __forceinline__ float f2_hi(F2 x) { return __uint_as_float((uint32_t)(x.v >> 32)); }
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+// What is left of x after its first 11 bits (the fp16 part that pack_rz keeps), or x where mask is 0.
+__device__ __forceinline__ F2 rest11(F2 x, uint32_t mask) {
+    const F2 first = f2(__uint_as_float((uint32_t)x.v & mask), __uint_as_float((uint32_t)(x.v >> 32) & mask));
+    return fma2(first, f2(-1.f, -1.f), x);
+}
+// Transposes an 8 x 8 matrix of fp16 pairs: from row r, columns 2 c and 2 c + 1 to rows 2 c and 2 c + 1, column r.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// Half i of the words of a key's scales.
+__device__ __forceinline__ float scale_at(const uint32_t *w, int i) { return i & 1 ? half_hi(w[i / 2]) : half_lo(w[i / 2]); }
+
+__device__ __forceinline__ uint32_t lds_u1(uint32_t at) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
 template <int N>
 struct Words;
 template <>
 struct Words<4> {
     uint32_t w[4];
     __device__ __forceinline__ void load(uint32_t at) {
-        const uint4 u = lds_u4(at);
-        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
     }
 };
 template <>
 struct Words<2> {
     uint32_t w[2];
     __device__ __forceinline__ void load(uint32_t at) {
-        const uint2 u = lds_u2(at);
-        w[0] = u.x, w[1] = u.y;
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
     }
 };
 template <>
 struct Words<1> {
     uint32_t w[1];
-    __device__ __forceinline__ void load(uint32_t at) { asm("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(at)); }
+    __device__ __forceinline__ void load(uint32_t at) {
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(at) : "memory");
+    }
 };
 
 __device__ __forceinline__ bool bounded_wait(uint64_t *bar, uint32_t parity) {
@@ -89,7 +150,7 @@ __device__ __forceinline__ bool bounded_wait(uint64_t *bar, uint32_t parity) {
 }
 
 constexpr size_t attend_smem(int hd) {
-    const size_t ring = (size_t)kWarps * kSlots * 2 * kv4_tile_bytes(hd), merge = (size_t)kWarps * kMaxG * hd * 4;
+    const size_t ring = (size_t)kWarps * kSlots * kv4_tile_bytes(hd), merge = (size_t)kWarps * kMaxG * hd * 4;
     return ring > merge ? ring : merge;
 }
 
@@ -99,367 +160,533 @@ __device__ __forceinline__ void load_dims8(const T *p, float (&x)[8]) {
     for (int i = 0; i < 8; ++i) x[i] = (float)p[i];
 }
 
-// Pages of one stream per split: at least one for each warp.
-__device__ __forceinline__ int pages_per_split(int npages, int splits) {
-    return max(kWarps, (npages + splits - 1) / splits);
-}
-__device__ __forceinline__ int checked_len(const Kv4Attend &a, int b, bool report) {
+// The work of a call in units of one page for every warp of a CTA: each (stream, KV head) row has
+// a unit for every kWarps pages, at least one, or (one_unit) a single unit of all its pages. Rows
+// lie behind one another, streams outermost, and CTA i of n takes units [i U / n, (i + 1) U / n).
+__device__ __forceinline__ int checked_len(const Kv4Attend &a, int b) {
     const int len = a.lens[b];
-    if (len >= 0 && len <= a.c.pages_per_stream * kPage) return len;
-    if (report && a.c.status != nullptr) atomicOr(a.c.status, ST_BAD_POSITION);
-    return -1;
+    return len >= 0 && len <= a.c.pages_per_stream * kPage ? len : -1;
+}
+__device__ __forceinline__ int pages_of(int len) { return len > 0 ? (len + kPage - 1) / kPage : 0; }
+__device__ __forceinline__ int units_of(const Kv4Attend &a, int len) {
+    return a.one_unit ? 1 : max(1, (pages_of(len) + kWarps - 1) / kWarps);
+}
+// Units of one KV head of all streams, and of those before stream `upto` (one warp).
+__device__ __forceinline__ long long count_units(const Kv4Attend &a, int upto, long long &before) {
+    const int lane = threadIdx.x & 31;
+    long long all = 0, part = 0;
+    for (int b = lane; b < a.B; b += 32) {
+        const int u = units_of(a, checked_len(a, b));
+        all += u;
+        if (b < upto) part += u;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+        part += __shfl_xor_sync(0xffffffffu, part, o);
+    }
+    before = part;
+    return all;
+}
+// The stream of unit x and the number of units before its first row.
+__device__ __forceinline__ int stream_of(const Kv4Attend &a, long long x, long long &first) {
+    const int lane = threadIdx.x & 31;
+    long long sum = 0;
+    for (int base = 0; base < a.B; base += 32) {
+        const long long u = base + lane < a.B ? (long long)units_of(a, checked_len(a, base + lane)) * a.c.n_kv_heads : 0;
+        long long to = u;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long t = __shfl_up_sync(0xffffffffu, to, o);
+            if (lane >= o) to += t;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, sum + to > x);
+        if (past != 0) {
+            const int at = __ffs(past) - 1;
+            first = sum + __shfl_sync(0xffffffffu, to - u, at);
+            return base + at;
+        }
+        sum += __shfl_sync(0xffffffffu, to, 31);
+    }
+    first = sum;
+    return a.B;
 }
 
-// Grid (splits, n_kv, B). Each warp of CTA (s, g, b) takes every fourth page of the CTA's range of
-// stream b and KV head g through a ring of its own: bulk copies, no barrier between warps.
+// Each CTA walks its units row by row. Within a row, each warp takes every kWarps-th page through a
+// ring of its own: bulk copies, no barrier between warps; the warps' parts are merged at the row's
+// (or the range's) end. A row that lies in one CTA's range is finished there, else its parts go to
+// scratch: a CTA has at most two such parts, one that begins its range and one that ends it.
 //
-// A lane is (r = lane / 4, c = lane % 4). Scores of 8 keys, S[16 x 8] = Q K^T by m16n8k16: rows
-// r and r + 8 of Q are the two fp16 parts of one query head, scaled by a power of two so that its
-// largest value lies in [2^13, 2^14). K codes n enter as the fp16 subnormals n 2^-24 (and 16 n
-// 2^-24, against q / 16): a nibble is its own operand after one AND. The accumulator starts at
-// -8 sum(q) 2^-24 per block of 32 dims, and its two rows, added and multiplied by the key's scale,
-// make the block's part of the score in f32.
-// Values, O^T[dims x heads] += V^T P^T: V codes are centred in fp16 ((n - 8) exactly: with n as it
-// is, 8 sum(p) would cancel), and the probabilities, times the value's scale of each block and a
-// power of two, enter as two fp16 parts: with up to 4 query heads in columns h and h + 4 of one
-// MMA (SPLIT 1), else by two MMAs. The score's layout is the P operand's: a lane keeps its keys.
+// A lane is (r = lane / 4, c = lane % 4). Scores of 16 keys, S[keys x 8] = K Q^T by m16n8k16 per
+// block of 32 dims. K codes enter as they are (nibbles and bytes, below), q is scaled by a power of
+// two so that its largest value lies in [2^13, 2^14). The results times the key's scales are added
+// in f32; the codes' offset, -8 sum(q) of each block times its scale, is one more MMA, over blocks.
+// Values, O^T[dims x 8] += V^T P^T, P being the probabilities times the value's scale of each block,
+// transposed between lanes as fp16. The exponents' reference m keeps P in fp16's range: it follows
+// the largest score plus log2 of the largest value scale, and O and l are rescaled when P would
+// pass 2^14, to below 2^9. An accumulator's columns are its lane's heads throughout.
+// f32 results (PREC): q and P in two fp16 parts (22 bits), for up to 4 query heads in columns h and
+// h + 4 of one MMA, above that (WIDE) by two MMAs; V codes centred in fp16. bf16 results: one part
+// of q (exact where q is bf16), of p and of P, each 2^-12 of a term at most, an eighth of half a
+// step of the result; V codes as they are, and one more MMA (A = -8 everywhere) takes off what they
+// are too large by, 16 keys at a time: a sum over all keys would cancel too much in f32.
 template <int HD, bool WIDE, typename TI, typename TO>
-__global__ void __launch_bounds__(kWarps * 32, 3) k_kv4_attend(const Kv4Attend a) {
+__global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Attend a) {
     using Tile = Kv4Tile<HD>;
+    constexpr bool PREC = sizeof(TO) == 4;
     constexpr int NB = Tile::NB;
-    constexpr int kSlotBytes = 2 * Tile::kBytes;
+    constexpr int kParts = PREC && !WIDE ? 2 : 1;       // columns of P per query head
+    constexpr int kCorrBits = 10;
     extern __shared__ __align__(128) unsigned char ring_all[];
     __shared__ __align__(8) uint64_t bars[kWarps][kSlots];
     __shared__ float wm[kWarps + 1][kMaxG], wl[kWarps + 1][kMaxG];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    const int s = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
     const int G = a.n_q / a.c.n_kv_heads;
     pdl_launch_dependents();
-    const int len = checked_len(a, b, threadIdx.x == 0 && s == 0);
-    const int npages = len > 0 ? (len + kPage - 1) / kPage : 0;
-    const int per = pages_per_split(npages, a.splits);
-    const int pb = s * per, pe = min(pb + per, npages);
-    if (s > 0 && pb >= pe) return;   // not among the stream's splits
-
-    unsigned char *ring = ring_all + warp * kSlots * kSlotBytes;
-    const int *ptab = a.c.page_table + (size_t)b * a.c.pages_per_stream;
-    const size_t head_off = ((size_t)a.layer * a.c.n_kv_heads + g) * Tile::kBytes;
-    const size_t page_bytes = (size_t)a.c.n_layers * a.c.n_kv_heads * Tile::kBytes;
-    const int n_it = pb + warp < pe ? (pe - pb - warp + kWarps - 1) / kWarps : 0;
-    // lane i holds the page number of iteration 32 j + i
-    auto page_of = [&](int it) { return it < n_it ? ptab[pb + warp + it * kWarps] : 0; };
-    auto good = [&](int page) { return page >= 0 && page < a.c.n_pages; };
-    auto issue = [&](int slot, int page) {   // one lane; a bad page number copies page 0, which is not used
-        const size_t off = (good(page) ? page : 0) * page_bytes + head_off;
-        unsigned char *dst = ring + slot * kSlotBytes;
-        mbar_arrive_expect_tx(&bars[warp][slot], kSlotBytes);
-        bulk_g2s(dst, static_cast<const unsigned char *>(a.c.k) + off, Tile::kBytes, &bars[warp][slot]);
-        bulk_g2s(dst + Tile::kBytes, static_cast<const unsigned char *>(a.c.v) + off, Tile::kBytes, &bars[warp][slot]);
-    };
-    int pages = page_of(lane), ahead = page_of(32 + lane);
+    unsigned char *ring = ring_all + warp * kSlots * Tile::kBytes;
     if (lane == 0) {
         for (int i = 0; i < kSlots; ++i) mbar_init(&bars[warp][i], 1);
         fence_barrier_init();
     }
     __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i) {
-        const int page = __shfl_sync(0xffffffffu, pages, i);
-        if (lane == 0 && i < n_it) issue(i, page);
-    }
+    long long before;
+    const long long U = count_units(a, 0, before) * a.c.n_kv_heads;
+    const long long n = min(U, (long long)gridDim.x);
+    if (blockIdx.x >= n) return;
+    const long long x_begin = blockIdx.x * U / n, x_end = (blockIdx.x + 1) * U / n;
+    int b = stream_of(a, x_begin, before);
+    int len = checked_len(a, b), nu = units_of(a, len);
+    int g = (int)((x_begin - before) / nu), u0 = (int)((x_begin - before) % nu);
+    int slot = 0, phase = 0;   // where the next K tile goes, and the parity that each slot's next wait has
+    const uint32_t lo_mask = kParts == 1 || c >= 2 ? 0xffffe000u : 0u;
+    const uint32_t eight[4] = {0x80088008u, 0x80888088u, 0x80088008u, 0x80888088u};   // -8 2^-24 (nibbles), -136 2^-24 (bytes)
+    // Of 8 keys, row 2 c of the scores (and so slot 2 c of P) is key c and row 2 c + 1 key c2: the
+    // two rows of codes that eight lanes load together lie in other banks.
+    const int c2 = 4 + (c ^ 1), key_r = r & 1 ? 4 + ((r >> 1) ^ 1) : r >> 1;
 
-    // this lane's query head (rows beyond G compute on zeros)
-    const int hq = WIDE ? r : r & 3;
-    const float cs = a.scale * kLog2e;
-    uint32_t qf[NB][2][4];
-    float corr[NB][2], fs;
-    {
-        float x[NB][8], top = 0.f;
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            if (hq < G) {
-                load_dims8(static_cast<const TI *>(a.q) + b * a.q_row + (size_t)(g * G + hq) * HD + nb * 32 + c * 8, x[nb]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[nb][i] = 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[nb][i]));
-        }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = min((int)(__float_as_uint(top) >> 23), 254);        // biased exponent of the largest
-        const int up = min(13 + 127 - e, 120);                            // 2^up brings it to [2^13, 2^14)
-        const float qs = __uint_as_float((uint32_t)(up + 127) << 23);
-        fs = cs * exp2f((float)(24 - up));
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            float sh = 0.f, sl = 0.f;
-            __half hi[8], lo[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float y = x[nb][i] * qs * (i & 1 ? 0.0625f : 1.f);
-                hi[i] = __float2half_rn(y);
-                lo[i] = __float2half_rn(y - __half2float(hi[i]));
-                sh = fmaf(__half2float(hi[i]), i & 1 ? 16.f : 1.f, sh);
-                sl = fmaf(__half2float(lo[i]), i & 1 ? 16.f : 1.f, sl);
-            }
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                qf[nb][t][0] = pack_half(hi[2 * t], hi[2 * t + 4]);
-                qf[nb][t][1] = pack_half(lo[2 * t], lo[2 * t + 4]);
-                qf[nb][t][2] = pack_half(hi[2 * t + 1], hi[2 * t + 5]);
-                qf[nb][t][3] = pack_half(lo[2 * t + 1], lo[2 * t + 5]);
-            }
-            sh += __shfl_xor_sync(0xffffffffu, sh, 1);
-            sl += __shfl_xor_sync(0xffffffffu, sl, 1);
-            sh += __shfl_xor_sync(0xffffffffu, sh, 2);
-            sl += __shfl_xor_sync(0xffffffffu, sl, 2);
-            corr[nb][0] = sh * (-8.f / 16777216.f);
-            corr[nb][1] = sl * (-8.f / 16777216.f);
-        }
-    }
+    for (long long x = x_begin; x < x_end;) {
+        const int u1 = (int)min((long long)nu, u0 + (x_end - x));
+        const int npages = pages_of(len);
+        const int pb = u0 * kWarps, pe = u1 == nu ? npages : u1 * kWarps;
+        if (len < 0 && threadIdx.x == 0 && a.c.status != nullptr) atomicOr(a.c.status, ST_BAD_POSITION);
+        const int *ptab = a.c.page_table + (size_t)b * a.c.pages_per_stream;
+        const size_t head_off = ((size_t)a.layer * a.c.n_kv_heads + g) * Tile::kBytes;
+        const size_t page_bytes = (size_t)a.c.n_layers * a.c.n_kv_heads * Tile::kBytes;
+        const int n_it = pb + warp < pe ? (pe - pb - warp + kWarps - 1) / kWarps : 0;
+        // lane i holds the page number of iteration 32 j + i
+        auto page_of = [&](int it) { return it < n_it ? ptab[pb + warp + it * kWarps] : 0; };
+        auto good = [&](int page) { return page >= 0 && page < a.c.n_pages; };
+        // a tile to a slot, by one lane; a bad page number copies page 0, which is not used
+        auto issue = [&](int to, const void *pool, int page) {
+            mbar_arrive_expect_tx(&bars[warp][to], Tile::kBytes);
+            bulk_g2s(ring + to * Tile::kBytes, static_cast<const unsigned char *>(pool) + (good(page) ? page : 0) * page_bytes + head_off,
+                     Tile::kBytes, &bars[warp][to]);
+        };
+        auto wait = [&](int at) {
+            const bool ok = bounded_wait(&bars[warp][at], phase >> at & 1);
+            phase ^= 1 << at;
+            return !__any_sync(0xffffffffu, !ok);
+        };
+        auto after = [](int at) { return at == kSlots - 1 ? 0 : at + 1; };
+        int pages = page_of(lane), ahead = page_of(32 + lane);
+        int page = __shfl_sync(0xffffffffu, pages, 0), page1 = __shfl_sync(0xffffffffu, pages, 1);
+        if (lane == 0 && n_it > 0) issue(slot, a.c.k, page), issue(after(slot), a.c.v, page);
+        if (lane == 0 && n_it > 1) issue(after(after(slot)), a.c.k, page1);
 
-    float m = -INFINITY, l = 0.f;             // reference of the exponents, this lane's part of the sum
-    float vs = 274877906944.f;                // 2^38: the power of two on value scales
-    float o[2 * NB][4];                       // dims 32 (t / 2) + 4 r + 2 (t % 2) (+ 1 in the upper pair), heads 2 c, 2 c + 1
+        // this lane's query head (rows beyond G compute on zeros)
+        const int hq = kParts == 2 ? r & 3 : r;
+        const float cs = a.scale * kLog2e;
+        uint32_t qf[NB][2][2], ql[NB][2][2];       // (ql: WIDE only)
+        uint32_t qc[2];                            // -8 sum(q) of the blocks, in two parts, times 2^kCorrBits
+        F2 fs;                                     // from these units to scores in base 2, of this lane's columns 2 c, 2 c + 1
+        {
+            float x[NB][8], top = 0.f;
 #pragma unroll
-    for (int t = 0; t < 2 * NB; ++t)
+            for (int nb = 0; nb < NB; ++nb) {
+                if (hq < G) {
+                    load_dims8(static_cast<const TI *>(a.q) + b * a.q_row + (size_t)(g * G + hq) * HD + nb * 32 + c * 8, x[nb]);
+                } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
-    const uint32_t lo_mask = WIDE || r >= 4 ? 0xffffe000u : 0u;
-    const int krow = (r >> 1) + 4 * (r & 1);   // the key whose codes this lane loads, of the 8 of a score tile
-
-    bool failed = false;
-    for (int it = 0; it < n_it; ++it) {
-        const int slot = it % kSlots;
-        if (it > 0 && it % 32 == 0) {
-            pages = ahead;
-            ahead = page_of(it + 32 + lane);
-        }
-        if (__any_sync(0xffffffffu, !bounded_wait(&bars[warp][slot], (it / kSlots) & 1))) {
-            // report, give the copies in flight their chance to land, and leave with a NaN
-            if (lane == 0 && a.c.status != nullptr) atomicOr(a.c.status, ST_WAIT_TIMEOUT);
-            for (int j = it; j < it + kSlots && j < n_it; ++j) bounded_wait(&bars[warp][j % kSlots], (j / kSlots) & 1);
-            failed = true;
-            m = __int_as_float(0x7fc00000);
-            break;
-        }
-        const int page = __shfl_sync(0xffffffffu, pages, it % 32);
-        const int valid = min(kPage, len - (pb + warp + it * kWarps) * kPage);
-        if (!good(page)) {
-            if (lane == 0 && a.c.status != nullptr) atomicOr(a.c.status, ST_BAD_ARG);
-        } else {
-            const uint32_t kt = smem_u32(ring + slot * kSlotBytes), vt = kt + Tile::kBytes;
-            if (valid < kPage) {   // value scales past the length: zero (a stream's last page: never refilled)
-                for (int i = valid * NB + lane; i < kPage * NB; i += 32)
-                    *reinterpret_cast<unsigned short *>(ring + slot * kSlotBytes + Tile::kBytes + Tile::kScales + 2 * i) = 0;
-                __syncwarp();
+                    for (int i = 0; i < 8; ++i) x[nb][i] = 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[nb][i]));
             }
-            // scores, in base 2: key 8 j + c and 8 j + 4 + c
-            float sc[8][2];
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int e = min((int)(__float_as_uint(top) >> 23), 254);        // biased exponent of the largest
+            const int up = min(13 + 127 - e, 120);                            // 2^up brings it to [2^13, 2^14)
+            const float qs = __uint_as_float((uint32_t)(up + 127) << 23);
+            const float unit = cs * exp2f((float)(24 - up));
+            fs = f2(__shfl_sync(0xffffffffu, unit, 8 * c), __shfl_sync(0xffffffffu, unit, 8 * c + 4));
+            float corr[NB];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                Words<NB> k;
-                k.load(kt + (8 * j + krow) * Tile::kRow + c * 4 * NB);
-                Words<NB / 2> d0, d1;
-                d0.load(kt + Tile::kScales + (8 * j + c) * NB * 2);
-                d1.load(kt + Tile::kScales + (8 * j + 4 + c) * NB * 2);
-                float s0 = 0.f, s1 = 0.f;
+            for (int nb = 0; nb < NB; ++nb) {
+                float sum = 0.f;
+                __half hi[8], lo[8];
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    float acc[4] = {corr[nb][0], corr[nb][0], corr[nb][1], corr[nb][1]};
-                    const uint32_t w = k.w[nb], w8 = w >> 8;
-                    mma16816(acc, qf[nb][0], w & 0x000f000fu, w & 0x00f000f0u);
-                    mma16816(acc, qf[nb][1], w8 & 0x000f000fu, w8 & 0x00f000f0u);
-                    s0 = fmaf(nb & 1 ? half_hi(d0.w[nb / 2]) : half_lo(d0.w[nb / 2]), acc[0] + acc[2], s0);
-                    s1 = fmaf(nb & 1 ? half_hi(d1.w[nb / 2]) : half_lo(d1.w[nb / 2]), acc[1] + acc[3], s1);
-                }
-                sc[j][0] = s0 * fs;
-                sc[j][1] = s1 * fs;
-            }
-            if (valid < kPage) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (8 * j + c >= valid) sc[j][0] = -INFINITY;
-                    if (8 * j + 4 + c >= valid) sc[j][1] = -INFINITY;
-                }
-            }
-            float mx = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fmaxf(sc[j][0], sc[j][1]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            // the largest value scale of the page (a NaN is no size)
-            float dmax;
-            {
-                Words<NB / 2> d;
-                __half2 h = __float2half2_rn(0.f);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    d.load(vt + Tile::kScales + (2 * lane + i) * NB * 2);
-#pragma unroll
-                    for (int u = 0; u < NB / 2; ++u) h = __hmax2(h, __habs2(*reinterpret_cast<__half2 *>(&d.w[u])));
-                }
-                const float t = fmaxf(__low2float(h), __high2float(h));
-                dmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(t)));
-            }
-            const bool grow = mx > m + kSlack, wider = dmax * vs >= kTop;
-            if (__any_sync(0xffffffffu, grow) || wider) {
-                const float mn = fmaxf(m, mx);
-                float al = m == mn ? 1.f : ex2(m - mn);
-                m = mn;
-                l *= al;
-                if (wider) {   // dmax vs goes to [2^9, 2^10)
-                    const float nv = __uint_as_float((uint32_t)(127 + 9 + 127 - (int)(__float_as_uint(dmax) >> 23)) << 23);
-                    al *= nv / vs;
-                    vs = nv;
-                }
-                const float a0 = __shfl_sync(0xffffffffu, al, 8 * c), a1 = __shfl_sync(0xffffffffu, al, 8 * c + 4);
-#pragma unroll
-                for (int t = 0; t < 2 * NB; ++t) {
-                    o[t][0] *= a0, o[t][1] *= a1;
-                    o[t][2] *= a0, o[t][3] *= a1;
-                }
-            }
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {   // 16 keys: c, c + 4, c + 8, c + 12
-                float p[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    p[i] = ex2(sc[2 * ks + (i >> 1)][i & 1] - m);
-                    l += p[i];
-                    p[i] *= vs;
-                }
-                Words<NB / 2> v[4], d[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    v[i].load(vt + (16 * ks + 4 * i + c) * Tile::kRow + r * 2 * NB);
-                    d[i].load(vt + Tile::kScales + (16 * ks + 4 * i + c) * NB * 2);
+                for (int i = 0; i < 8; ++i) {
+                    // of the byte that holds dims i and i + 1: the part of n0 alone, and that of n0 + 16 n1
+                    const float y = i & 1 ? x[nb][i] * qs * 0.0625f : fmaf(x[nb][i + 1], qs * -0.0625f, x[nb][i] * qs);
+                    hi[i] = __float2half_rn(y);
+                    lo[i] = __float2half_rn(y - __half2float(hi[i]));
+                    if (kParts == 2 && r >= 4) hi[i] = lo[i];
+                    sum = fmaf(__half2float(hi[i]) + (WIDE ? __half2float(lo[i]) : 0.f), i & 1 ? 17.f : 1.f, sum);
                 }
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    float y[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) y[i] = p[i] * (nb & 1 ? half_hi(d[i].w[nb / 2]) : half_lo(d[i].w[nb / 2]));
-                    uint32_t ph[2], pl[2];
+                for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        if (WIDE) ph[i] = pack_rz(y[2 * i], y[2 * i + 1]);
-                        pl[i] = pack_rz(rest11(y[2 * i], lo_mask), rest11(y[2 * i + 1], lo_mask));
+                        qf[nb][t][i] = pack_half(hi[2 * t + i], hi[2 * t + 4 + i]);
+                        ql[nb][t][i] = pack_half(lo[2 * t + i], lo[2 * t + 4 + i]);
                     }
-                    // bytes 2 (nb % 2) and the next of the four keys' words
-                    const uint32_t sel = nb & 1 ? 0x7632 : 0x5410;
-                    uint32_t u0 = __byte_perm(v[0].w[nb / 2], v[1].w[nb / 2], sel);
-                    uint32_t u1 = __byte_perm(v[2].w[nb / 2], v[3].w[nb / 2], sel);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                corr[nb] = sum * (-8.f / 16777216.f * (1 << kCorrBits));
+            }
+            qc[0] = qc[1] = 0;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t va[4] = {codes_even(u0), codes_odd(u0), codes_even(u1), codes_odd(u1)};
-                        if (WIDE) mma16816(o[2 * nb + e], va, ph[0], ph[1]);
-                        mma16816(o[2 * nb + e], va, pl[0], pl[1]);
-                        u0 >>= 8;
-                        u1 >>= 8;
+            for (int i = 0; i < NB / 2; ++i)
+                if (c == i) {
+                    const __half h0 = __float2half_rn(corr[2 * i]), h1 = __float2half_rn(corr[2 * i + 1]);
+                    qc[0] = pack_half(h0, h1);
+                    qc[1] = pack_half(__float2half_rn(corr[2 * i] - __half2float(h0)), __float2half_rn(corr[2 * i + 1] - __half2float(h1)));
+                }
+        }
+
+        float m0 = -INFINITY, m1 = -INFINITY;     // references of the exponents of this lane's columns
+        F2 l2 = f2(0.f, 0.f);                     // its keys' parts of their sums
+        // dim 32 (t / 2) + 4 r + 2 (t % 2), and it plus 16 times the next one (e >= 2), of heads 2 c, 2 c + 1;
+        // with V codes as they are, times 2^-24
+        float o[2 * NB][4];
+#pragma unroll
+        for (int t = 0; t < 2 * NB; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
+
+        bool failed = false;
+        for (int it = 0; it < n_it; ++it) {
+            if ((it + 2) % 32 == 0) {
+                pages = ahead;
+                ahead = page_of(it + 34 + lane);
+            }
+            const int page2 = __shfl_sync(0xffffffffu, pages, (it + 2) % 32), vslot = after(slot);
+            const int valid = min(kPage, len - (pb + warp + it * kWarps) * kPage);
+            constexpr int H = NB / 2;
+            const uint32_t kt = smem_u32(ring) + slot * Tile::kBytes, vt = smem_u32(ring) + vslot * Tile::kBytes;
+            failed = !wait(slot);
+            if (failed) break;
+            F2 sc[4][2];   // scores in base 2: of keys 16 i + key_r and 16 i + 8 + key_r
+            if (!good(page)) {
+                if (lane == 0 && a.c.status != nullptr) atomicOr(a.c.status, ST_BAD_ARG);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    Words<NB> k0, k1;
+                    Words<H> d0, d1;
+                    k0.load(kt + (16 * i + key_r) * Tile::kRow + c * 4 * NB);
+                    k1.load(kt + (16 * i + 8 + key_r) * Tile::kRow + c * 4 * NB);
+                    d0.load(kt + Tile::kScales + (16 * i + key_r) * NB * 2);
+                    d1.load(kt + Tile::kScales + (16 * i + 8 + key_r) * NB * 2);
+                    F2 s0, s1;
+                    {
+                        uint32_t e[4];   // scales of blocks 2 c and 2 c + 1 (columns past the blocks meet zeros)
+                        e[0] = lds_u1(kt + Tile::kScales + (16 * i + key_r) * NB * 2 + 4 * (c & (H - 1)));
+                        e[1] = lds_u1(kt + Tile::kScales + (16 * i + 8 + key_r) * NB * 2 + 4 * (c & (H - 1)));
+                        e[2] = e[0], e[3] = e[1];
+                        float acc[4];
+                        mma16816_new(acc, e, qc[0], qc[1]);
+                        const F2 down = f2(1.f / (1 << kCorrBits), 1.f / (1 << kCorrBits));
+                        s0 = f2(acc[0], acc[1]) * down, s1 = f2(acc[2], acc[3]) * down;
+                    }
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        float acc[4];
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            const uint32_t w0 = t ? bytes13(k0.w[nb]) : bytes02(k0.w[nb]), w1 = t ? bytes13(k1.w[nb]) : bytes02(k1.w[nb]);
+                            const uint32_t codes[4] = {nibbles(w0), nibbles(w1), w0, w1};
+                            if (t == 0) mma16816_new(acc, codes, qf[nb][0][0], qf[nb][0][1]);
+                            else mma16816(acc, codes, qf[nb][1][0], qf[nb][1][1]);
+                            if (WIDE) mma16816(acc, codes, ql[nb][t][0], ql[nb][t][1]);
+                        }
+                        const float e0 = scale_at(d0.w, nb), e1 = scale_at(d1.w, nb);
+                        s0 = f2(fmaf(e0, acc[0], f2_lo(s0)), fmaf(e0, acc[1], f2_hi(s0)));
+                        s1 = f2(fmaf(e1, acc[2], f2_lo(s1)), fmaf(e1, acc[3], f2_hi(s1)));
+                    }
+                    sc[i][0] = s0, sc[i][1] = s1;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        F2 &x = sc[i][u];
+                        if (kParts == 2)   // the parts of head h: columns h and h + 4
+                            x = x + f2(__shfl_xor_sync(0xffffffffu, f2_lo(x), 2), __shfl_xor_sync(0xffffffffu, f2_hi(x), 2));
+                        x = x * fs;
+                    }
+                if (valid < kPage) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (8 * i + key_r >= valid) sc[i >> 1][i & 1] = f2(-INFINITY, -INFINITY);
+                }
+            }
+            __syncwarp();
+            if (lane == 0 && it + 1 < n_it) {   // the next page's V over this K
+                fence_proxy_async();
+                issue(slot, a.c.v, page1);
+            }
+            failed = !wait(vslot);
+            if (failed) break;
+            if (good(page)) {
+                if (valid < kPage) {   // value scales past the length: zero (a row's last page: never refilled)
+                    unsigned char *d = ring + vslot * Tile::kBytes + Tile::kScales;
+                    for (int i = valid * NB + lane; i < kPage * NB; i += 32) reinterpret_cast<unsigned short *>(d)[i] = 0;
+                    __syncwarp();
+                }
+                // exponent of the largest value scale (a NaN is no size), at least that of the smallest fp16, or 0
+                // where p itself is held in fp16
+                int de;
+                {
+                    __half2 top = __float2half2_rn(0.f);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        Words<H> d;
+                        d.load(vt + Tile::kScales + (2 * lane + u) * NB * 2);
+#pragma unroll
+                        for (int i = 0; i < H; ++i)
+                            top = __hmax2(top, __habs2(*reinterpret_cast<__half2 *>(&d.w[i])));
+                    }
+                    const uint32_t dmax = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(__low2float(top), __high2float(top))));
+                    de = max((int)(dmax >> 23) - 126, PREC ? -24 : 0);
+                }
+                F2 mx = f2(-INFINITY, -INFINITY);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) mx = f2(fmaxf(f2_lo(mx), f2_lo(sc[i][u])), fmaxf(f2_hi(mx), f2_hi(sc[i][u])));
+#pragma unroll
+                for (int j = 4; j < 32; j <<= 1)
+                    mx = f2(fmaxf(f2_lo(mx), __shfl_xor_sync(0xffffffffu, f2_lo(mx), j)),
+                            fmaxf(f2_hi(mx), __shfl_xor_sync(0xffffffffu, f2_hi(mx), j)));
+                if (__any_sync(0xffffffffu, f2_lo(mx) + de > m0 + kTopBits || f2_hi(mx) + de > m1 + kTopBits)) {
+                    const float n0 = fmaxf(m0, f2_lo(mx) + (de - kNewBits)), n1 = fmaxf(m1, f2_hi(mx) + (de - kNewBits));
+                    const F2 al = f2(m0 == n0 ? 1.f : ex2(m0 - n0), m1 == n1 ? 1.f : ex2(m1 - n1));
+                    m0 = n0;
+                    m1 = n1;
+                    l2 = l2 * al;
+#pragma unroll
+                    for (int t = 0; t < 2 * NB; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2) {
+                            const F2 x = f2(o[t][e], o[t][e + 1]) * al;
+                            o[t][e] = f2_lo(x), o[t][e + 1] = f2_hi(x);
+                        }
+                }
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) {
+                    F2 p[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const F2 x = sc[ks][i] + f2(-m0, -m1);
+                        p[i] = f2(ex2(f2_lo(x)), ex2(f2_hi(x)));
+                        l2 = l2 + p[i];
+                    }
+                    Words<H> v[4], d[4];   // of slots 2 c, 2 c + 1 and 8 further
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int key = 16 * ks + 8 * (i >> 1) + (i & 1 ? c2 : c);
+                        v[i].load(vt + key * Tile::kRow + r * 2 * NB);
+                        if (!PREC) d[i].load(vt + Tile::kScales + key * NB * 2);
+                    }
+                    uint32_t pt[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (PREC) d[i].load(vt + Tile::kScales + (16 * ks + 8 * i + key_r) * NB * 2);   // of p's keys
+                        else pt[i] = transpose8(pack_rn(f2_lo(p[i]), f2_hi(p[i])));
+                    }
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        const uint32_t sel = nb & 1 ? 0x7632 : 0x5410;   // halves nb % 2 of two keys' words
+                        uint32_t ph[2], pl[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if (!PREC) {
+                                ph[i] = mul_half2(pt[i], __byte_perm(d[2 * i].w[nb / 2], d[2 * i + 1].w[nb / 2], sel));
+                            } else {
+                                const float e = scale_at(d[i].w, nb);
+                                const F2 y = f2(f2_lo(p[i]) * e, f2_hi(p[i]) * e), z = rest11(y, lo_mask);
+                                if (WIDE) ph[i] = transpose8(pack_rz(f2_lo(y), f2_hi(y)));
+                                pl[i] = transpose8(pack_rz(f2_lo(z), f2_hi(z)));
+                            }
+                        }
+                        const uint32_t u0 = __byte_perm(v[0].w[nb / 2], v[1].w[nb / 2], sel);
+                        const uint32_t u1 = __byte_perm(v[2].w[nb / 2], v[3].w[nb / 2], sel);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float(&acc)[4] = o[2 * nb + e];
+                            const uint32_t x0 = e ? bytes13(u0) : bytes02(u0), x1 = e ? bytes13(u1) : bytes02(u1);
+                            if (PREC) {
+                                const uint32_t codes[4] = {centred(nibbles(x0), kMidNibble), centred(x0, kMidByte),
+                                                           centred(nibbles(x1), kMidNibble), centred(x1, kMidByte)};
+                                if (WIDE) mma16816(acc, codes, ph[0], ph[1]);
+                                mma16816(acc, codes, pl[0], pl[1]);
+                            } else {
+                                const uint32_t codes[4] = {nibbles(x0), x0, nibbles(x1), x1};
+                                mma16816(acc, eight, ph[0], ph[1]);
+                                mma16816(acc, codes, ph[0], ph[1]);
+                            }
+                        }
                     }
                 }
             }
+            __syncwarp();
+            if (lane == 0 && it + 2 < n_it) {   // the K after the next over this V
+                fence_proxy_async();
+                issue(vslot, a.c.k, page2);
+            }
+            slot = after(vslot);
+            page = page1;
+            page1 = page2;
         }
-        __syncwarp();
-        const int next = it + kSlots;
-        const int np = __shfl_sync(0xffffffffu, next / 32 == it / 32 ? pages : ahead, next % 32);
-        if (lane == 0 && next < n_it) {
-            fence_proxy_async();
-            issue(slot, np);
+        if (failed) {   // report, and give the copies in flight their chance to land
+            if (lane == 0 && a.c.status != nullptr) atomicOr(a.c.status, ST_WAIT_TIMEOUT);
+            for (int i = 0; i < kSlots; ++i) bounded_wait(&bars[warp][i], phase >> i & 1);
         }
-    }
 
-    // the warp's (m, l, O) to shared memory, over the ring
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
-    if (failed) l = m;
-    __syncthreads();
-    float *wo = reinterpret_cast<float *>(ring_all);   // [kWarps][kMaxG][HD]
-    const float down = 1.f / vs;
-    if (c == 0 && r == hq) wm[warp][hq] = m, wl[warp][hq] = l;
+        // the warp's (m, l, O) to shared memory, over the ring
 #pragma unroll
-    for (int t = 0; t < 2 * NB; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float x = o[t][e] * down;
-            if (!WIDE) x += __shfl_xor_sync(0xffffffffu, x, 2);   // the parts of head h: columns h and h + 4
-            const int h = 2 * c + (e & 1), dim = 32 * (t >> 1) + 4 * r + 2 * (t & 1) + (e >> 1);
-            if (WIDE || c < 2) wo[(warp * kMaxG + h) * HD + dim] = x;
+        for (int j = 4; j < 32; j <<= 1)
+            l2 = l2 + f2(__shfl_xor_sync(0xffffffffu, f2_lo(l2), j), __shfl_xor_sync(0xffffffffu, f2_hi(l2), j));
+        if (failed) {
+            m0 = m1 = __int_as_float(0x7fc00000);
+            l2 = f2(m0, m0);
         }
-    // the step's own row, as one more part of split 0
-    const bool fresh = s == 0 && len >= 0 && a.k_new != nullptr;
-    if (fresh) {
-        const TI *kn = static_cast<const TI *>(a.k_new) + b * a.new_row + (size_t)g * HD;
-        for (int h = warp; h < G; h += kWarps) {
-            const TI *q = static_cast<const TI *>(a.q) + b * a.q_row + (size_t)(g * G + h) * HD;
-            float t = 0.f;
-#pragma unroll
-            for (int i = 0; i < HD / 32; ++i) t = fmaf((float)q[32 * i + lane], (float)kn[32 * i + lane], t);
-            t = warp_sum(t);
-            if (lane == 0) wm[kWarps][h] = t * cs, wl[kWarps][h] = 1.f;
+        __syncthreads();
+        float *wo = reinterpret_cast<float *>(ring_all);   // [kWarps][kMaxG][HD]
+        if (r == 0 && (kParts == 1 || c < 2)) {
+            wm[warp][2 * c] = m0, wm[warp][2 * c + 1] = m1;
+            wl[warp][2 * c] = f2_lo(l2), wl[warp][2 * c + 1] = f2_hi(l2);
         }
-    }
-    __syncthreads();
-    const int nact = (npages + per - 1) / per;
-    for (int idx = threadIdx.x; idx < G * HD; idx += kWarps * 32) {
-        const int h = idx / HD, d = idx % HD;
-        float M = fresh ? wm[kWarps][h] : -INFINITY, L = 0.f, O = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wm[w][h]);
+        for (int t = 0; t < 2 * NB; ++t)
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float e = wm[w][h] == -INFINITY ? 0.f : ex2(wm[w][h] - M);
-            L = fmaf(wl[w][h], e, L);
-            O = fmaf(wo[(w * kMaxG + h) * HD + d], e, O);
-        }
+            for (int e = 0; e < 4; ++e) {
+                float y = e < 2 ? o[t][e] : (o[t][e] - o[t][e - 2]) * 0.0625f;
+                if (!PREC) y *= 16777216.f;
+                if (kParts == 2) y += __shfl_xor_sync(0xffffffffu, y, 2);   // the parts of head h: columns h and h + 4
+                const int h = 2 * c + (e & 1), dim = 32 * (t >> 1) + 4 * r + 2 * (t & 1) + (e >> 1);
+                if (kParts == 1 || c < 2) wo[(warp * kMaxG + h) * HD + dim] = y;
+            }
+        // the step's own row, as one more part of the row's first units
+        const bool fresh = u0 == 0 && len >= 0 && a.k_new != nullptr;
         if (fresh) {
-            const float e = ex2(wm[kWarps][h] - M);
-            L += e;
-            O = fmaf((float)static_cast<const TI *>(a.v_new)[b * a.new_row + (size_t)g * HD + d], e, O);
+            const TI *kn = static_cast<const TI *>(a.k_new) + b * a.new_row + (size_t)g * HD;
+            for (int h = warp; h < G; h += kWarps) {
+                const TI *q = static_cast<const TI *>(a.q) + b * a.q_row + (size_t)(g * G + h) * HD;
+                float t = 0.f;
+#pragma unroll
+                for (int i = 0; i < HD / 32; ++i) t = fmaf((float)q[32 * i + lane], (float)kn[32 * i + lane], t);
+                t = warp_sum(t);
+                if (lane == 0) wm[kWarps][h] = t * cs, wl[kWarps][h] = 1.f;
+            }
         }
-        const size_t row = (size_t)b * a.n_q + g * G + h;
-        if (nact <= 1) {
-            static_cast<TO *>(a.out)[row * HD + d] = (TO)(L == 0.f ? 0.f : O / L);
-        } else {
-            float *ws = a.scratch + (row * a.splits + s) * (HD + 4);
-            ws[4 + d] = O;
-            if (d == 0) ws[0] = M, ws[1] = L;
+        __syncthreads();
+        const bool whole = u0 == 0 && u1 == nu;
+        for (int idx = threadIdx.x; idx < G * HD; idx += kWarps * 32) {
+            const int h = idx / HD, d = idx % HD;
+            float M = fresh ? wm[kWarps][h] : -INFINITY, L = 0.f, O = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wm[w][h]);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float e = wm[w][h] == -INFINITY ? 0.f : ex2(wm[w][h] - M);
+                L = fmaf(wl[w][h], e, L);
+                O = fmaf(wo[(w * kMaxG + h) * HD + d], e, O);
+            }
+            if (fresh) {
+                const float e = ex2(wm[kWarps][h] - M);
+                L += e;
+                O = fmaf((float)static_cast<const TI *>(a.v_new)[b * a.new_row + (size_t)g * HD + d], e, O);
+            }
+            if (whole) {
+                static_cast<TO *>(a.out)[((size_t)b * a.n_q + g * G + h) * HD + d] = (TO)(L == 0.f ? 0.f : O / L);
+            } else {
+                float *ws = a.scratch + (((size_t)blockIdx.x * 2 + (x != x_begin)) * kMaxG + h) * (HD + 4);
+                ws[4 + d] = O;
+                if (d == 0) ws[0] = M, ws[1] = L;
+            }
+        }
+        x += u1 - u0;
+        u0 = 0;
+        if (x < x_end) {
+            if (++g == a.c.n_kv_heads) {
+                g = 0;
+                ++b;
+                len = checked_len(a, b);
+                nu = units_of(a, len);
+            }
+            __syncthreads();       // the ring is free again ...
+            fence_proxy_async();   // ... for copies behind these reads and writes
+            __syncwarp();
         }
     }
 }
 
-// Grid (n_q, B), HD threads: the splits' partials joined in split order.
+// Grid (n_q, B), HD threads: the parts of rows that several CTAs shared, joined in order.
 template <int HD, typename TO>
-__global__ void __launch_bounds__(HD) k_kv4_combine(const Kv4Attend a) {
+__global__ void __launch_bounds__(HD) k_kv4_combine(const Kv4Attend a, const int grid) {
+    constexpr int kAhead = 8;   // parts requested at a time
+    const int b = blockIdx.y, G = a.n_q / a.c.n_kv_heads, g = blockIdx.x / G, h = blockIdx.x % G;
     pdl_wait();
-    const int b = blockIdx.y;
-    const int npages = (max(checked_len(a, b, false), 0) + kPage - 1) / kPage;
-    const int per = pages_per_split(npages, a.splits), nact = (npages + per - 1) / per;
-    if (nact <= 1) return;   // written by its only split
-    const size_t row = (size_t)b * a.n_q + blockIdx.x;
-    const float *ws = a.scratch + row * a.splits * (HD + 4);
+    long long before;
+    const long long U = count_units(a, b, before) * a.c.n_kv_heads;
+    const int nu = units_of(a, checked_len(a, b));
+    const long long n = min(U, (long long)grid), x0 = before * a.c.n_kv_heads + (long long)g * nu;
+    const int first = (int)(((x0 + 1) * n - 1) / U), last = (int)(((x0 + nu) * n - 1) / U);   // CTAs of the row's ends
+    if (first == last) return;
+    auto part = [&](int i) {
+        const int slot = i == first && i * U / n != x0;
+        return a.scratch + (((size_t)i * 2 + slot) * kMaxG + h) * (HD + 4);
+    };
     float M = -INFINITY, L = 0.f, O = 0.f;
-    for (int s = 0; s < nact; ++s) M = fmaxf(M, ws[s * (HD + 4)]);
-    for (int s = 0; s < nact; ++s) {
-        const float m = ws[s * (HD + 4)], e = m == -INFINITY ? 0.f : ex2(m - M);
-        L = fmaf(ws[s * (HD + 4) + 1], e, L);
-        O = fmaf(ws[s * (HD + 4) + 4 + threadIdx.x], e, O);
+    for (int i0 = first; i0 <= last; i0 += kAhead) {
+        float m[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) m[i] = i0 + i <= last ? part(i0 + i)[0] : -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) M = fmaxf(M, m[i]);
     }
-    static_cast<TO *>(a.out)[row * HD + threadIdx.x] = (TO)(L == 0.f ? 0.f : O / L);
+    for (int i0 = first; i0 <= last; i0 += kAhead) {
+        float m[kAhead], l[kAhead], o[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const bool in = i0 + i <= last;
+            const float *ws = part(in ? i0 + i : last);
+            m[i] = in ? ws[0] : -INFINITY;
+            l[i] = in ? ws[1] : 0.f;
+            o[i] = in ? ws[4 + threadIdx.x] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const float e = m[i] == -INFINITY ? 0.f : ex2(m[i] - M);
+            L = fmaf(l[i], e, L);
+            O = fmaf(o[i], e, O);
+        }
+    }
+    static_cast<TO *>(a.out)[((size_t)b * a.n_q + blockIdx.x) * HD + threadIdx.x] = (TO)(L == 0.f ? 0.f : O / L);
 }
 
 template <int HD, typename TI, typename TO>
 cudaError_t launch_t(const Kv4Attend &a, cudaStream_t s) {
-    const bool wide = a.n_q / a.c.n_kv_heads > 4;
-    void (*kernel)(Kv4Attend) = wide ? k_kv4_attend<HD, true, TI, TO> : k_kv4_attend<HD, false, TI, TO>;
+    const bool wide = a.n_q / a.c.n_kv_heads > 4 && sizeof(TO) == 4;
+    void (*kernel)(Kv4Attend) = k_kv4_attend<HD, false, TI, TO>;
+    if constexpr (sizeof(TO) == 4) kernel = wide ? k_kv4_attend<HD, true, TI, TO> : kernel;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attend_smem(HD));
     if (e != cudaSuccess) return e;
-    kernel<<<dim3(a.splits, a.c.n_kv_heads, a.B), kWarps * 32, attend_smem(HD), s>>>(a);
+    kernel<<<a.grid, kWarps * 32, attend_smem(HD), s>>>(a);
     e = cudaGetLastError();
-    if (e != cudaSuccess || a.splits == 1) return e;
+    if (e != cudaSuccess || a.one_unit) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.n_q, a.B);
     cfg.blockDim = dim3(HD);
@@ -469,7 +696,7 @@ cudaError_t launch_t(const Kv4Attend &a, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_kv4_combine<HD, TO>, a);
+    return cudaLaunchKernelEx(&cfg, k_kv4_combine<HD, TO>, a, a.grid);
 }
 
 template <int HD>
@@ -480,14 +707,21 @@ cudaError_t launch_hd(const Kv4Attend &a, int in_bf16, int out_bf16, cudaStream_
 
 }  // namespace
 
-int kv4_attend_splits(int B, int n_kv, int head_dim, int max_len, int n_sm) {
-    const long long rows = (long long)B * n_kv;
-    const int pages = std::max(1, (int)(((long long)max_len + kPage - 1) / kPage));
-    return (int)std::min<long long>(std::min(64, pages), std::max<long long>(1, (4ll * n_sm + rows - 1) / rows));
+// CTAs of a launch and whether rows are left whole: with at most kWholePages pages (one or two per
+// warp) the second launch costs more than splitting wins.
+constexpr int kWholePages = 8;
+
+Kv4AttendShape kv4_attend_shape(int B, int n_kv, int max_len, int n_sm) {
+    const long long rows = (long long)B * n_kv, pages = ((long long)max_len + kPage - 1) / kPage;
+    Kv4AttendShape p;
+    p.one_unit = pages <= kWholePages;
+    const long long units = p.one_unit ? rows : rows * ((pages + kWarps - 1) / kWarps);
+    p.grid = (int)std::max<long long>(1, std::min<long long>(units, (long long)kCtas * n_sm));
+    return p;
 }
 
-size_t kv4_attend_scratch(int B, int n_q, int head_dim, int splits) {
-    return splits > 1 ? (size_t)B * n_q * splits * (head_dim + 4) * sizeof(float) : 0;
+size_t kv4_attend_scratch(const Kv4AttendShape &p, int head_dim) {
+    return p.one_unit ? 0 : (size_t)p.grid * 2 * kMaxG * (head_dim + 4) * sizeof(float);
 }
 
 cudaError_t launch_kv4_attend(const Kv4Attend &a, int in_bf16, int out_bf16, cudaStream_t s) {
@@ -506,13 +740,13 @@ bool attend_sizes_ok(const talker_kv4 *c, int B, int n_q, int max_len) {
            n_q % c->n_kv_heads == 0 && n_q / c->n_kv_heads <= kMaxG;
 }
 
-int splits_here(const talker_kv4 *c, int B, int max_len) {
+Kv4AttendShape shape_here(const talker_kv4 *c, int B, int max_len) {
     int dev = 0, n_sm = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
         cudaGetLastError();
         n_sm = 152;
     }
-    return kv4_attend_splits(std::max(B, 1), c->n_kv_heads, c->head_dim, std::min(max_len, c->pages_per_stream * kPage), n_sm);
+    return kv4_attend_shape(B, c->n_kv_heads, std::min(max_len, c->pages_per_stream * kPage), n_sm);
 }
 
 }  // namespace
@@ -521,7 +755,7 @@ extern "C" {
 
 size_t talker_kv4_attend_scratch(const talker_kv4 *c, int B, int n_q_heads, int max_len) {
     if (!attend_sizes_ok(c, B, n_q_heads, max_len)) return 0;
-    return kv4_attend_scratch(B, n_q_heads, c->head_dim, splits_here(c, B, max_len));
+    return kv4_attend_scratch(shape_here(c, B, max_len), c->head_dim);
 }
 
 talker_status talker_kv4_attend(const talker_kv4 *c, int layer, int B, const int32_t *lens, int max_len, int n_q_heads,
@@ -535,10 +769,10 @@ talker_status talker_kv4_attend(const talker_kv4 *c, int layer, int B, const int
     if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(k_new) |
          reinterpret_cast<uintptr_t>(v_new)) % size)
         return TALKER_EINVAL;
-    const int splits = splits_here(c, B, max_len);
-    const size_t need = kv4_attend_scratch(B, n_q_heads, c->head_dim, splits);
+    const Kv4AttendShape shape = shape_here(c, B, max_len);
+    const size_t need = kv4_attend_scratch(shape, c->head_dim);
     if (need > 0 && (!scratch || scratch_bytes < need || (reinterpret_cast<uintptr_t>(scratch) & 15u))) return TALKER_EINVAL;
-    const Kv4Attend a{*c, layer, B, n_q_heads, lens, q, k_new, v_new, q_row, new_row, out, scale, splits,
+    const Kv4Attend a{*c, layer, B, n_q_heads, lens, q, k_new, v_new, q_row, new_row, out, scale, shape.grid, shape.one_unit,
                       static_cast<float *>(scratch)};
     const int bf16 = dtype == TALKER_DTYPE_BF16;
     if (launch_kv4_attend(a, bf16, bf16, static_cast<cudaStream_t>(cuda_stream)) != cudaSuccess) {
