@@ -137,8 +137,9 @@ talker_status talker_kv4_reorder(const talker_kv4 *c, const int32_t *parents, in
  * NULL (eos_id may then be negative: no token ends a beam). Outputs
  * [n_seq][width]: tokens, parents (the row seq * width + w that is continued),
  * scores_out, and ended_out (may be NULL): the parent had ended, or the token is
- * eos_id. Outputs must not overlap the inputs. width <= 32, width <= vocab.
- * scratch: talker_beam_scratch bytes, 16-byte aligned.
+ * eos_id. Outputs must not overlap the inputs. width <= 32, width <= vocab,
+ * n_seq * width < 2^26.
+ * scratch: talker_beam_scratch bytes, 16-byte aligned (may be NULL when that is 0).
  * Errors: EINVAL, ECUDA. */
 size_t talker_beam_scratch(int n_seq, int width, int vocab);
 talker_status talker_beam_select(const void *logits, int64_t row_stride, int dtype, const float *scores,

@@ -3,7 +3,7 @@ from __future__ import annotations
 
 import torch
 
-from .kv4 import _DTYPE, _check
+from .kv4 import _DTYPE, launch
 from .talker import load_library
 
 
@@ -28,18 +28,14 @@ def beam_select(logits, scores, ended=None, eos_id: int = -1):
     if logits.stride(2) != 1 or stride < vocab or (n_seq > 1 and logits.stride(0) != width * stride):
         logits = logits.contiguous()
         stride = vocab
-    out = torch.empty((3, n_seq, width), dtype=torch.int32, device=device)
-    tokens, parents, done = out.unbind(0)
-    best = torch.empty((n_seq, width), dtype=torch.float32, device=device)
+    tokens, parents, done, best = torch.empty((4, n_seq, width), dtype=torch.int32, device=device).unbind(0)
+    best = best.view(torch.float32)
     if n_seq == 0:
         return tokens, parents, best, done
     lib = load_library()
     need = lib.talker_beam_scratch(n_seq, width, vocab)
-    with torch.cuda.device(device):
-        scratch = torch.empty(need, dtype=torch.uint8, device=device)
-        _check(lib.talker_beam_select(logits.data_ptr(), stride, _DTYPE[logits.dtype], scores.data_ptr(),
-                                      None if ended is None else ended.data_ptr(), n_seq, width, vocab, eos_id,
-                                      tokens.data_ptr(), parents.data_ptr(), best.data_ptr(), done.data_ptr(),
-                                      scratch.data_ptr(), need, torch.cuda.current_stream(device).cuda_stream),
-               "talker_beam_select")
+    scratch = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    launch(device.index, lib.talker_beam_select, "talker_beam_select", logits.data_ptr(), stride, _DTYPE[logits.dtype],
+           scores.data_ptr(), None if ended is None else ended.data_ptr(), n_seq, width, vocab, eos_id, tokens.data_ptr(),
+           parents.data_ptr(), best.data_ptr(), done.data_ptr(), scratch.data_ptr() if need else None, need)
     return tokens, parents, best, done

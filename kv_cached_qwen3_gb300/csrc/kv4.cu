@@ -119,60 +119,57 @@ cudaError_t launch_rows_t(const Kv4Rows &r, bool vec, cudaStream_t s) {
 
 // ---- reorder
 
-// One warp per page-table column j. Row i of the new table keeps its parent's page where that is
-// full (shared) or, at the parent's tail page, where i is the parent's first child; every other
-// row needs a page of its own, and takes the pages of the column's set {r * pps + j} that no
-// kept entry uses, in order. A row refers to one page of a column, so there are always enough.
-__global__ void __launch_bounds__(256) k_reorder_table(const KvReorder r) {
-    __shared__ uint32_t used_s[8][32], seen_s[8][32], need_s[8][32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int j = blockIdx.x * 8 + warp;
-    const bool first = blockIdx.x == 0 && warp == 0;
-    if (j >= r.pps) return;
-    uint32_t *used = used_s[warp], *seen = seen_s[warp], *need = need_s[warp];
-    used[lane] = seen[lane] = need[lane] = 0;
+struct ReorderScratch {   // one warp's sets of streams
+    uint32_t used[32], seen[32], need[32];
+};
+
+__device__ __forceinline__ int parent_of(const KvReorder &r, int i) {
+    const int p = i < r.R ? r.parents[i] : i;
+    return p >= 0 && p < r.n_streams ? p : i;
+}
+__device__ __forceinline__ int length_of(const KvReorder &r, int p) { return min(max(r.lens[p], 0), r.pps * kPage); }
+
+// One warp finds column j of the new table. Row i keeps its parent's page where that is full
+// (shared) or, at the parent's tail page, where i is the parent's first child; every other row needs
+// a page of its own, and takes the pages of the column's set {r * pps + j} that no kept entry uses,
+// in order. A row refers to one page of a column, so there are always enough. Writes the column when
+// `store`; returns row `ask`'s entry.
+__device__ int reorder_column(const KvReorder &r, int j, int ask, bool store, bool report, ReorderScratch &w) {
+    const int lane = threadIdx.x & 31;
+    w.used[lane] = w.seen[lane] = w.need[lane] = 0;
     __syncwarp();
-    const int cap = r.pps * kPage;
+    int answer = -1;
     for (int base = 0; base < r.n_streams; base += 32) {
         const int i = base + lane;
         const bool in = i < r.n_streams;
-        int p = in ? (i < r.R ? r.parents[i] : i) : -1 - lane, keep = -1;
+        int p = -1 - lane, keep = -1;
         bool own = false;
         if (in) {
-            if (p < 0 || p >= r.n_streams) {
-                if (first && r.status != nullptr) atomicOr(r.status, ST_BAD_ARG);
-                p = i;
-            }
-            int len = r.lens[p];
-            if (len < 0 || len > cap) {
-                if (first && r.status != nullptr) atomicOr(r.status, ST_BAD_POSITION);
-                len = min(max(len, 0), cap);
-            }
-            if (first) r.lens_out[i] = len;
-            const int tail = len / kPage;
+            p = parent_of(r, i);
+            const int tail = length_of(r, p) / kPage;
             const int entry = r.table[(size_t)p * r.pps + j];
             const int er = entry / r.pps;
             const bool ok = entry >= 0 && entry - er * r.pps == j && er < r.n_streams;
-            if (!ok && j <= tail && r.status != nullptr) atomicOr(r.status, ST_BAD_ARG);
-            if (ok && j < tail) keep = er;
+            if (report && !ok && j <= tail && r.status != nullptr) atomicOr(r.status, ST_BAD_ARG);
             own = ok && j == tail;
-            if (own) keep = er;
+            if (ok && j <= tail) keep = er;
         }
         // the first child of a parent takes its tail page over
         const uint32_t same = __match_any_sync(0xffffffffu, p);
-        if (own && ((same & ((1u << lane) - 1)) != 0 || (seen[p >> 5] >> (p & 31) & 1u))) keep = -1;
+        if (own && ((same & ((1u << lane) - 1)) != 0 || (w.seen[p >> 5] >> (p & 31) & 1u))) keep = -1;
         __syncwarp();
-        if (in) atomicOr(&seen[p >> 5], 1u << (p & 31));
+        if (in) atomicOr(&w.seen[p >> 5], 1u << (p & 31));
         if (keep >= 0) {
-            atomicOr(&used[keep >> 5], 1u << (keep & 31));
-            r.table_out[(size_t)i * r.pps + j] = keep * r.pps + j;
+            atomicOr(&w.used[keep >> 5], 1u << (keep & 31));
+            if (store) r.table_out[(size_t)i * r.pps + j] = keep * r.pps + j;
+            if (i == ask) answer = keep * r.pps + j;
         }
         const uint32_t wants = __ballot_sync(0xffffffffu, in && keep < 0);
-        if (lane == 0) need[base >> 5] = wants;
+        if (lane == 0) w.need[base >> 5] = wants;
         __syncwarp();
     }
     // free pages of the column: lane holds word `lane` of their set and how many lie before it
-    uint32_t fw = ~used[lane];
+    uint32_t fw = ~w.used[lane];
     const int left = r.n_streams - 32 * lane;
     fw &= left >= 32 ? 0xffffffffu : (left > 0 ? (1u << left) - 1 : 0u);
     int before = __popc(fw);
@@ -184,8 +181,7 @@ __global__ void __launch_bounds__(256) k_reorder_table(const KvReorder r) {
     before -= __popc(fw);
     int taken = 0;
     for (int base = 0; base < r.n_streams; base += 32) {
-        const uint32_t wants = need[base >> 5];
-        const bool mine = wants >> lane & 1u;
+        const uint32_t wants = w.need[base >> 5];
         int k = taken + __popc(wants & ((1u << lane) - 1));
         taken += __popc(wants);
         int word = 0;   // the last word with at most k free pages before it
@@ -194,32 +190,59 @@ __global__ void __launch_bounds__(256) k_reorder_table(const KvReorder r) {
             if (__shfl_sync(0xffffffffu, before, word + o) <= k) word += o;
         uint32_t bits = __shfl_sync(0xffffffffu, fw, word);
         k -= __shfl_sync(0xffffffffu, before, word);
-        if (mine) {
+        if (wants >> lane & 1u) {
             while (k-- > 0) bits &= bits - 1;
-            r.table_out[(size_t)(base + lane) * r.pps + j] = (32 * word + __ffs(bits) - 1) * r.pps + j;
+            const int entry = (32 * word + __ffs(bits) - 1) * r.pps + j;
+            if (store) r.table_out[(size_t)(base + lane) * r.pps + j] = entry;
+            if (base + lane == ask) answer = entry;
         }
     }
+    return __shfl_sync(0xffffffffu, answer, ask & 31);
 }
 
-// The rows of tail pages whose stream did not take its parent's page over: one warp per tile.
-// Sources are pages that stay in use, destinations pages that nothing in use refers to.
-__global__ void __launch_bounds__(256) k_reorder_copy(const KvReorder r) {
-    const int i = blockIdx.y;
-    int p = i < r.R ? r.parents[i] : i;
-    if (p < 0 || p >= r.n_streams) p = i;
-    const int len = min(max(r.lens[p], 0), r.pps * kPage);
+// The first table_blocks CTAs write the table, a warp per column, and the lengths. The others copy
+// the rows of a tail page that its stream did not take over from its parent: copy_blocks CTAs per
+// stream, a warp per tile. Each finds its destination itself (the column is a few hundred bytes), so
+// that one launch does it all. Sources are pages that stay in use, destinations pages that nothing
+// in use refers to, so copies need no order.
+__global__ void __launch_bounds__(256) k_reorder(const KvReorder r, int table_blocks, int copy_blocks) {
+    __shared__ ReorderScratch scratch[8];
+    __shared__ int to_s;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (blockIdx.x < table_blocks) {
+        const int j = blockIdx.x * 8 + warp;
+        if (blockIdx.x == 0)
+            for (int i = threadIdx.x; i < r.n_streams; i += 256) {
+                const int asked = i < r.R ? r.parents[i] : i, p = parent_of(r, i);
+                r.lens_out[i] = length_of(r, p);
+                if (r.status != nullptr && asked != p) atomicOr(r.status, ST_BAD_ARG);
+                if (r.status != nullptr && r.lens[p] != length_of(r, p)) atomicOr(r.status, ST_BAD_POSITION);
+            }
+        if (j < r.pps) reorder_column(r, j, 0, true, true, scratch[warp]);
+        return;
+    }
+    const int i = (blockIdx.x - table_blocks) / copy_blocks, part = (blockIdx.x - table_blocks) % copy_blocks;
+    const int p = parent_of(r, i), len = length_of(r, p);
     const int col = len / kPage, rows = len % kPage;
     if (rows == 0) return;
-    const int src = r.table[(size_t)p * r.pps + col], dst = r.table_out[(size_t)i * r.pps + col];
-    const int sr = src / r.pps;
-    if (src == dst || src < 0 || src - sr * r.pps != col || sr >= r.n_streams) return;
-    const int t = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int src = r.table[(size_t)p * r.pps + col], sr = src / r.pps;
+    if (src < 0 || src - sr * r.pps != col || sr >= r.n_streams) return;
+    int first = 0;   // whether another child of p comes before i
+    for (int k = threadIdx.x; k < i; k += 256) first |= parent_of(r, k) == p;
+    if (!__syncthreads_or(first)) return;
+    if (warp == 0) {
+        const int dst = reorder_column(r, col, i, false, false, scratch[0]);
+        if (lane == 0) to_s = dst;
+    }
+    __syncthreads();
+    const int dst = to_s, t = part * 8 + warp;
     if (t >= 2 * r.n_tiles) return;
     unsigned char *pool = t < r.n_tiles ? r.k : r.v;
     const size_t off = (size_t)(t < r.n_tiles ? t : t - r.n_tiles) * r.tile_bytes;
     const uint4 *from = reinterpret_cast<const uint4 *>(pool + src * r.page_bytes + off);
     uint4 *to = reinterpret_cast<uint4 *>(pool + dst * r.page_bytes + off);
     const int codes = rows * r.row_bytes / 16, scales = (rows * r.scale_bytes + 15) / 16, sc0 = kPage * r.row_bytes / 16;
+#pragma unroll 4
     for (int e = lane; e < codes; e += 32) to[e] = from[e];
     for (int e = lane; e < scales; e += 32) to[sc0 + e] = from[sc0 + e];
 }
@@ -242,10 +265,10 @@ cudaError_t launch_kv4_rows(const Kv4Rows &r, int dtype, bool read, cudaStream_t
 }
 
 cudaError_t launch_kv_reorder(const KvReorder &r, cudaStream_t s) {
-    k_reorder_table<<<(r.pps + 7) / 8, 256, 0, s>>>(r);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    k_reorder_copy<<<dim3((2 * r.n_tiles + 7) / 8, r.n_streams), 256, 0, s>>>(r);
+    const int table_blocks = (r.pps + 7) / 8, copy_blocks = (2 * r.n_tiles + 7) / 8;
+    const long long blocks = table_blocks + (long long)copy_blocks * r.n_streams;
+    if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+    k_reorder<<<(unsigned)blocks, 256, 0, s>>>(r, table_blocks, copy_blocks);
     return cudaGetLastError();
 }
 

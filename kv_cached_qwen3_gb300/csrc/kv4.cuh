@@ -110,6 +110,8 @@ struct Kv4AttendShape {
 };
 Kv4AttendShape kv4_attend_shape(int B, int n_kv, int max_len, int n_sm);
 size_t kv4_attend_scratch(const Kv4AttendShape &p, int head_dim);
+cudaError_t prepare_kv4_attend();   // shared-memory limits, on the current device
+int kv4_multiprocessors();          // of the current device, prepared as above (0: an error)
 cudaError_t launch_kv4_attend(const Kv4Attend &a, int in_bf16, int out_bf16, cudaStream_t s);
 
 // Streams reordered by sharing pages (talker_kv4_reorder), for any page layout of n_tiles tiles a

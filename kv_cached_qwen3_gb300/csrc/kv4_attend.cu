@@ -1,5 +1,6 @@
 // Decode attention over the 4-bit paged cache (talker_kv4_attend).
 #include <algorithm>
+#include <atomic>
 #include <math.h>
 
 #include "kv4.cuh"
@@ -682,10 +683,8 @@ cudaError_t launch_t(const Kv4Attend &a, cudaStream_t s) {
     const bool wide = a.n_q / a.c.n_kv_heads > 4 && sizeof(TO) == 4;
     void (*kernel)(Kv4Attend) = k_kv4_attend<HD, false, TI, TO>;
     if constexpr (sizeof(TO) == 4) kernel = wide ? k_kv4_attend<HD, true, TI, TO> : kernel;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attend_smem(HD));
-    if (e != cudaSuccess) return e;
     kernel<<<a.grid, kWarps * 32, attend_smem(HD), s>>>(a);
-    e = cudaGetLastError();
+    cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || a.one_unit) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.n_q, a.B);
@@ -724,6 +723,41 @@ size_t kv4_attend_scratch(const Kv4AttendShape &p, int head_dim) {
     return p.one_unit ? 0 : (size_t)p.grid * 2 * kMaxG * (head_dim + 4) * sizeof(float);
 }
 
+template <int HD, bool WIDE, typename TI, typename TO>
+cudaError_t raise_one() {
+    return cudaFuncSetAttribute(k_kv4_attend<HD, WIDE, TI, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attend_smem(HD));
+}
+template <int HD>
+cudaError_t raise_hd() {
+    cudaError_t e = raise_one<HD, false, float, float>();
+    e = e ? e : raise_one<HD, true, float, float>();
+    e = e ? e : raise_one<HD, false, float, __nv_bfloat16>();
+    return e ? e : raise_one<HD, false, __nv_bfloat16, __nv_bfloat16>();
+}
+
+cudaError_t prepare_kv4_attend() {
+    cudaError_t e = raise_hd<128>();
+    return e ? e : raise_hd<64>();
+}
+
+int kv4_multiprocessors() {
+    // once per device: the kernels' shared-memory limits and the number of multiprocessors
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        cudaGetLastError();
+        return 0;
+    }
+    n = known[dev].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || prepare_kv4_attend() != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 cudaError_t launch_kv4_attend(const Kv4Attend &a, int in_bf16, int out_bf16, cudaStream_t s) {
     if (a.B == 0) return cudaSuccess;
     return a.c.head_dim == 128 ? launch_hd<128>(a, in_bf16, out_bf16, s) : launch_hd<64>(a, in_bf16, out_bf16, s);
@@ -741,11 +775,7 @@ bool attend_sizes_ok(const talker_kv4 *c, int B, int n_q, int max_len) {
 }
 
 Kv4AttendShape shape_here(const talker_kv4 *c, int B, int max_len) {
-    int dev = 0, n_sm = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        cudaGetLastError();
-        n_sm = 152;
-    }
+    const int n_sm = std::max(kv4_multiprocessors(), 1);
     return kv4_attend_shape(B, c->n_kv_heads, std::min(max_len, c->pages_per_stream * kPage), n_sm);
 }
 

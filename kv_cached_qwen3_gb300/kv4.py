@@ -13,6 +13,7 @@ import torch
 from .talker import TalkerError, load_library
 
 PAGE = 64
+_raw_stream = torch._C._cuda_getCurrentRawStream   # torch.cuda.current_stream(device).cuda_stream, without the object
 _DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 
 
@@ -26,7 +27,13 @@ class _Strides(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("layer", "stream", "row", "head")]
 
 
-def _check(status, what):
+def launch(device: int, fn, what, *args):
+    """fn(*args, stream) on the current stream of a device, with that device current."""
+    if torch.cuda.current_device() == device:
+        status = fn(*args, _raw_stream(device))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _raw_stream(device))
     if status != 0:
         raise TalkerError(status, what)
 
@@ -81,6 +88,7 @@ class KV4Cache:
         self._c = _Cache(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), status.data_ptr(), self.n_pages,
                          self.n_streams, self.pages_per_stream, self.n_layers, self.n_kv_heads, head_dim)
         self._ref = ctypes.addressof(self._c)
+        self._scratch = {}     # attend's scratch bytes by (B, n_q_heads, max_len)
 
     def _ints(self, name, t, n):
         if t.dtype != torch.int32 or t.device != self.device or not t.is_contiguous() or \
@@ -89,15 +97,8 @@ class KV4Cache:
                              (name, "" if n is None else " of %d" % n, self.device))
         return t.data_ptr()
 
-    def _stream(self):
-        return torch.cuda.current_stream(self.device).cuda_stream
-
     def _call(self, fn, what, *args):
-        if torch.cuda.current_device() == self.device.index:
-            _check(fn(*args, self._stream()), what)
-        else:
-            with torch.cuda.device(self.device):
-                _check(fn(*args, self._stream()), what)
+        launch(self.device.index, fn, what, *args)
 
     def _rows(self, fn, what, k, v, start, count, layer0, stream0):
         for name, t in (("k", k), ("v", v)):
@@ -163,7 +164,10 @@ class KV4Cache:
             return out
         if max_len is None:
             max_len = self.pages_per_stream * PAGE
-        need = self._lib.talker_kv4_attend_scratch(self._ref, B, n_q, max_len)
+        max_len = min(-(-max_len // PAGE), self.pages_per_stream) * PAGE      # whole pages: few different calls
+        need = self._scratch.get((B, n_q, max_len))
+        if need is None:
+            need = self._scratch[(B, n_q, max_len)] = self._lib.talker_kv4_attend_scratch(self._ref, B, n_q, max_len)
         scratch = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
         self._call(self._lib.talker_kv4_attend, "talker_kv4_attend", self._ref, layer, B, lens_at, max_len, n_q,
                    1.0 / math.sqrt(hd) if scale is None else scale, q.data_ptr(), q.stride(0), kn, vn, new_row,

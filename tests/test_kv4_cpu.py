@@ -89,15 +89,15 @@ def test_reorder_refusals(lib):
 
 
 def test_beam_refusals(lib):
-    def call(x=4096, stride=100, dtype=0, scores=64, ended=None, S=1, W=4, V=100, eos=-1, tok=256, par=512, best=768,
+    def call(x=4096, stride=200000, dtype=0, scores=64, ended=None, S=1, W=4, V=100, eos=-1, tok=256, par=512, best=768,
              done=None, scratch=1024, n=1 << 20):
         return lib.talker_beam_select(x, stride, dtype, scores, ended, S, W, V, eos, tok, par, best, done, scratch, n, None)
-    need = lib.talker_beam_scratch(1, 4, 100)
-    assert need > 0
+    need = lib.talker_beam_scratch(1, 4, 200000)
+    assert need > 0 and lib.talker_beam_scratch(1, 4, 100) == 0
     for kw in (dict(x=None), dict(scores=None), dict(tok=None), dict(par=None), dict(best=None), dict(stride=99),
                dict(dtype=2), dict(W=0), dict(W=33), dict(V=3), dict(S=-1), dict(eos=100), dict(ended=64, eos=-1),
-               dict(best=64), dict(ended=64, done=64, eos=1), dict(scratch=None), dict(scratch=1032), dict(n=need - 1),
-               dict(x=4098)):
+               dict(best=64), dict(ended=64, done=64, eos=1), dict(V=200000, scratch=None), dict(V=200000, scratch=1032),
+               dict(V=200000, n=need - 1), dict(x=4098)):
         assert call(**kw) == 1, kw
     assert call(S=0) == 0
     for bad in ((-1, 4, 100), (1, 0, 100), (1, 33, 100), (1, 4, 3), (1 << 30, 4, 100)):
