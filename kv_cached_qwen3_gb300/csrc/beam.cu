@@ -19,34 +19,41 @@ constexpr int kCluster = 8;
 constexpr int kClusterTasks = kWarps * kCluster + kMaxWidth;
 constexpr float kMasked = -1e30f;   // at or below: counts as -inf
 constexpr float kLog2e = 1.4426950408889634f;
-typedef unsigned long long Key;
 
 // Masked values as -inf, and -0 as 0 (equal values are ordered by their index).
 __device__ __forceinline__ float unmask(float x) { return x > kMasked ? x + 0.f : -INFINITY; }
 
-// Order of (value, index): the larger value first, then the lower index. No key is 0.
-__device__ __forceinline__ Key key_of(float x, unsigned i) {
+// A logit and where it is in its row. rank: its value as a whole number of the same order, above 0.
+struct Entry {
+    uint32_t rank, index;
+};
+__device__ __forceinline__ uint32_t rank_of(float x) {
     const uint32_t u = __float_as_uint(x);
-    return (Key)(u & 0x80000000u ? ~u : u | 0x80000000u) << 32 | (0xffffffffu - i);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
-__device__ __forceinline__ float key_value(Key k) {
-    const uint32_t u = (uint32_t)(k >> 32);
-    return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
-}
-__device__ __forceinline__ unsigned key_index(Key k) { return 0xffffffffu - (uint32_t)k; }
-
-__device__ __forceinline__ Key warp_max_key(Key k) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const Key t = __shfl_xor_sync(0xffffffffu, k, o);
-        k = t > k ? t : k;
-    }
-    return k;
+__device__ __forceinline__ float value_of(uint32_t rank) {
+    return __uint_as_float(rank & 0x80000000u ? rank & 0x7fffffffu : ~rank);
 }
 __device__ __forceinline__ float ex2(float x) {   // relative error about 2^-22, 0 at -inf
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// log(x) for a normal x, to about 1e-10: x = 2^k f with f in [0.7, 1.5), log f = 2 atanh(z) by its
+// series in z = (f - 1) / (f + 1), |z| < 0.2. (Sums of exponentials meet here; scores next to one
+// another are told apart in 64 bits, in which the general logarithm would take most of a small call.)
+__device__ __forceinline__ double log_near(float x) {
+    const int bits = __float_as_int(x), k = (bits - 0x3f333333) >> 23;
+    const double f = (double)__int_as_float(bits - (k << 23)), z = (f - 1.0) / (f + 1.0), q = z * z;
+    double t = 1.0 / 15.0;
+    t = fma(t, q, 1.0 / 13.0);
+    t = fma(t, q, 1.0 / 11.0);
+    t = fma(t, q, 1.0 / 9.0);
+    t = fma(t, q, 1.0 / 7.0);
+    t = fma(t, q, 1.0 / 5.0);
+    t = fma(t, q, 1.0 / 3.0);
+    t = fma(t, q, 1.0);
+    return fma((double)k, 0.693147180559945309, 2.0 * z * t);
 }
 
 struct Args {
@@ -58,22 +65,33 @@ struct Args {
     int32_t *tokens, *parents, *ended_out;
     float *scores_out;
     int chunks;       // parts of a row
-    Key *keys;        // scratch: [row][chunk][width], best first
+    Entry *best;      // scratch: [row][chunk][width], best first
     float2 *sums;     // scratch: [row][chunk] (maximum, sum of exp(x - maximum))
 };
 
-// What a warp has seen of a row: lane i < width holds the i-th best logit, lanes apart their part of
-// the maximum and of the sum of exponentials.
+// What a warp has seen of a row: lane i < width holds the i-th best logit (rank 0: none yet); every
+// lane has its part of the maximum and of the sum of exponentials. What ranks `least` or lower is
+// not among the best any more.
 struct Seen {
-    Key mine;
-    float m, sum, least;   // least: the logit a new one has to pass (-inf and not `full` at first)
-    bool full;
+    Entry mine;
+    uint32_t least;
+    float m, sum;
+
+    __device__ __forceinline__ void insert(uint32_t rank, uint32_t index, int width) {   // the same in all lanes
+        const int lane = threadIdx.x & 31;
+        const int at = __popc(__ballot_sync(0xffffffffu, mine.rank > rank || (mine.rank == rank && mine.index < index)));
+        const uint32_t r = __shfl_up_sync(0xffffffffu, mine.rank, 1), i = __shfl_up_sync(0xffffffffu, mine.index, 1);
+        if (lane > at) mine = {r, i};
+        if (lane == at) mine = {rank, index};
+        if (lane >= width) mine.rank = 0;
+        least = max(least, __shfl_sync(0xffffffffu, mine.rank, width - 1));
+    }
 };
 
-// Values x of consecutive indexes: lane l holds those from at + l * N on, in order; on: how many of
-// them exist. Logits come in the order of their indexes, so an equal one never replaces another.
-template <int N>
-__device__ __forceinline__ void take(Seen &s, const float (&x)[N], unsigned at, int on, int width) {
+// N values per lane; the logit x[i] has index at(i), -inf where there is none (exists(i) false).
+// Logits come in the order of their indexes, so a later equal one never replaces another.
+template <int N, typename At, typename Exists>
+__device__ __forceinline__ void take(Seen &s, const float (&x)[N], At at, Exists exists, int width) {
     const int lane = threadIdx.x & 31;
     float top = x[0];
 #pragma unroll
@@ -86,31 +104,40 @@ __device__ __forceinline__ void take(Seen &s, const float (&x)[N], unsigned at, 
 #pragma unroll
         for (int i = 0; i < N; ++i) s.sum += ex2((x[i] - s.m) * kLog2e);
     }
-    if (!__any_sync(0xffffffffu, on > 0 && (top > s.least || !s.full))) return;
-    uint32_t left = 0;
+    uint32_t left = 0, best = 0;   // values not taken yet, the highest rank among them
 #pragma unroll
-    for (int i = 0; i < N; ++i) left |= (uint32_t)(i < on) << i;
+    for (int i = 0; i < N; ++i) left |= (uint32_t)exists(i) << i;
+    if (left != 0) best = rank_of(top);
+    if (s.least == 0) {
+        // The first values: `width` lanes have a value of at least the width-th of the lanes' highest
+        // ranks, so nothing below it is among the best. Without this, most of the first values would
+        // be inserted and pushed out again.
+        uint32_t lanes = best, floor = 0;
+        for (int j = 0; j < width; ++j) {
+            floor = __reduce_max_sync(0xffffffffu, lanes);
+            if (lane == __ffs(__ballot_sync(0xffffffffu, lanes == floor)) - 1) lanes = 0;
+        }
+        if (floor > 0) s.least = floor - 1;
+    }
     while (true) {
-        uint32_t pass = 0;
+        const uint32_t rank = __reduce_max_sync(0xffffffffu, best);
+        if (rank <= s.least || rank == 0) return;
+        uint32_t index = 0xffffffffu;
+        int e = -1;
+        if (best == rank) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) pass |= (uint32_t)(x[i] > s.least || !s.full) << i;
-        left &= pass;
-        const uint32_t lanes = __ballot_sync(0xffffffffu, left != 0);
-        if (lanes == 0) return;
-        const int from = __ffs(lanes) - 1, e = __ffs(left) - 1;
-        float v = x[0];
+            for (int i = N - 1; i >= 0; --i)
+                if ((left >> i & 1u) && rank_of(x[i]) == rank) index = at(i), e = i;
+        }
+        const uint32_t first = __reduce_min_sync(0xffffffffu, index);
+        s.insert(rank, first, width);
+        if (index == first) {
+            left &= ~(1u << e);
+            best = 0;
 #pragma unroll
-        for (int i = 1; i < N; ++i) v = e == i ? x[i] : v;
-        const Key k = __shfl_sync(0xffffffffu, key_of(v, at + lane * N + e), from);
-        if (lane == from) left &= left - 1;
-        const int pos = __popc(__ballot_sync(0xffffffffu, s.mine > k));
-        const Key up = __shfl_up_sync(0xffffffffu, s.mine, 1);
-        if (lane > pos) s.mine = up;
-        if (lane == pos) s.mine = k;
-        if (lane >= width) s.mine = 0;
-        const Key last = __shfl_sync(0xffffffffu, s.mine, width - 1);
-        s.full = last != 0;
-        s.least = s.full ? key_value(last) : -INFINITY;
+            for (int i = 0; i < N; ++i)
+                if (left >> i & 1u) best = max(best, rank_of(x[i]));
+        }
     }
 }
 
@@ -139,41 +166,45 @@ struct Vec<__nv_bfloat16> {
 // come from the same pass as its best logits.
 template <typename T>
 __device__ Seen read_part(const Args &a, int row, int chunk) {
-    constexpr int N = Vec<T>::N, kAhead = 4;
+    constexpr int N = Vec<T>::N, kAhead = 16 / N;
     const int lane = threadIdx.x & 31;
     const T *x = static_cast<const T *>(a.logits) + row * a.row_stride;
     const int head = min((int)((16 - (reinterpret_cast<uintptr_t>(x) & 15u)) % 16 / sizeof(T)), a.vocab);
     const int vectors = (a.vocab - head) / N;                   // whole ones
     const int v0 = (int)((long long)vectors * chunk / a.chunks), v1 = (int)((long long)vectors * (chunk + 1) / a.chunks);
-    Seen s{0, -INFINITY, 0.f, -INFINITY, false};
-    if (chunk == 0) {
+    Seen s{{0, 0}, 0, -INFINITY, 0.f};
+    if (chunk == 0 && head > 0) {
         const float one[1] = {lane < head ? unmask((float)x[lane]) : -INFINITY};
-        take<1>(s, one, 0, lane < head, a.width);
+        take<1>(s, one, [&](int) { return (uint32_t)lane; }, [&](int) { return lane < head; }, a.width);
     }
     const uint4 *vec = reinterpret_cast<const uint4 *>(x + head);
+    uint4 next[kAhead];
+    auto request = [&](int v) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (v + 32 * i + lane < v1) next[i] = ldg_stream(vec + v + 32 * i + lane);
+    };
+    request(v0);
     for (int v = v0; v < v1; v += 32 * kAhead) {
         uint4 u[kAhead];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (v + 32 * i + lane < v1) u[i] = ldg_stream(vec + v + 32 * i + lane);
+        for (int i = 0; i < kAhead; ++i) u[i] = next[i];
+        request(v + 32 * kAhead);
+        float f[kAhead * N];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            if (v + 32 * i >= v1) break;
-            const bool in = v + 32 * i + lane < v1;
-            float f[N];
-            if (in) {
-                Vec<T>::get(u[i], f);
-            } else {
+            float g[N];
+            Vec<T>::get(u[i], g);
 #pragma unroll
-                for (int e = 0; e < N; ++e) f[e] = -INFINITY;
-            }
-            take<N>(s, f, head + (v + 32 * i) * N, in ? N : 0, a.width);
+            for (int e = 0; e < N; ++e) f[i * N + e] = v + 32 * i + lane < v1 ? g[e] : -INFINITY;
         }
+        take<kAhead * N>(s, f, [&](int i) { return (uint32_t)(head + (v + 32 * (i / N) + lane) * N + i % N); },
+                         [&](int i) { return v + 32 * (i / N) + lane < v1; }, a.width);
     }
-    if (chunk == a.chunks - 1) {
-        const int t = head + vectors * N, n = a.vocab - t;       // fewer than a vector
-        const float one[1] = {lane < n ? unmask((float)x[t + lane]) : -INFINITY};
-        take<1>(s, one, t, lane < n, a.width);
+    const int t = head + vectors * N;
+    if (chunk == a.chunks - 1 && t < a.vocab) {
+        const float one[1] = {t + lane < a.vocab ? unmask((float)x[t + lane]) : -INFINITY};
+        take<1>(s, one, [&](int) { return (uint32_t)(t + lane); }, [&](int) { return t + lane < a.vocab; }, a.width);
     }
     const float m = warp_max(s.m);
     s.sum = warp_sum(s.m == -INFINITY ? 0.f : s.sum * ex2((s.m - m) * kLog2e));
@@ -182,73 +213,80 @@ __device__ Seen read_part(const Args &a, int row, int chunk) {
 }
 
 // The parts of a sequence's rows joined and its continuations chosen, by one CTA of kWarps warps.
-// keys, sums: [row of the sequence][part]. A warp joins a row's parts, lane = part; then lane w of
-// one warp walks beam w's best logits, and the best of the lanes' heads is chosen `width` times.
-// Candidates are compared in 64 bits.
-__device__ void choose(const Args &a, int seq, const Key *keys, const float2 *sums, Key *rows, float2 *lse) {
+// best, sums: [row of the sequence][part]. Where a sequence has more than a warp's lists, a warp
+// joins each row's first (into rows). Then one warp, a lane to a list, takes the best of the lists'
+// heads `width` times; candidates are compared in 64 bits, as whole numbers of the same order.
+__device__ void choose(const Args &a, int seq, const Entry *best, const float2 *sums, Entry *rows, float2 *lse) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int lists = a.chunks;   // of a row
     for (int w = warp; w < a.width; w += kWarps) {
         const bool part = lane < a.chunks;
-        const Key *list = keys + ((size_t)w * a.chunks + lane) * a.width;
         const float2 ms = part ? sums[w * a.chunks + lane] : make_float2(-INFINITY, 0.f);
         const float m = warp_max(ms.x), sum = warp_sum(ms.x == -INFINITY ? 0.f : ms.y * ex2((ms.x - m) * kLog2e));
         if (lane == 0) lse[w] = make_float2(m, sum);
+        if (a.width * a.chunks <= 32) continue;
+        const Entry *list = best + ((size_t)w * a.chunks + lane) * a.width;
         int at = 0;
-        Key head = part ? list[0] : 0;
+        Entry head = part ? list[0] : Entry{0, 0};
         for (int j = 0; j < a.width; ++j) {
-            const Key best = warp_max_key(head);
-            if (lane == 0) rows[w * a.width + j] = best;
-            if (head == best && best != 0) head = ++at < a.width ? list[at] : 0;
+            const uint32_t rank = __reduce_max_sync(0xffffffffu, head.rank);
+            const uint32_t index = __reduce_min_sync(0xffffffffu, head.rank == rank ? head.index : 0xffffffffu);
+            if (lane == 0) rows[w * a.width + j] = {rank, index};
+            if (head.rank == rank && head.index == index && rank != 0) head = ++at < a.width ? list[at] : Entry{0, 0};
         }
     }
+    if (a.width * a.chunks > 32) best = rows, lists = 1;
     __syncthreads();
     if (warp != 0) return;
-    const int row = seq * a.width + lane;
-    const bool on = lane < a.width;
+    const int w = lane / lists, row = seq * a.width + w;   // lists in the order of rows and indexes
+    const bool on = w < a.width;
     float score = -INFINITY;
     bool old = false, dead = true;
     double base = 0.0;
     if (on) {
         score = unmask(a.scores[row]);
         old = a.ended != nullptr && a.ended[row] != 0;
-        const float2 ms = lse[lane];
+        const float2 ms = lse[w];
         // no candidate above -inf: a masked score, or a row without a finite maximum
         dead = score == -INFINITY || score == INFINITY || (!old && !(fabsf(ms.x) < INFINITY));
-        if (!dead && !old) base = (double)ms.x + log((double)ms.y);
+        if (!dead && !old) base = (double)ms.x + log_near(ms.y);
     }
-    int at = 0;   // of this beam's candidates, in order
+    const Entry *list = best + (size_t)lane * a.width;
+    // The candidate `at` of this lane's list: its token and its score's rank (0: none left). Beams that
+    // are dead or have ended have one list, in order of tokens.
+    int at = 0, token = 0;
+    double c = 0.0;
+    unsigned long long rank = 0;
+    auto next = [&]() {
+        rank = 0;
+        if (!on || at >= a.width) return;
+        c = -INFINITY;
+        if (dead || old) {
+            if (lane % lists != 0) return;
+            token = dead ? at : at == 0 ? a.eos : at - 1 + (at - 1 >= a.eos);
+            if (!dead && at == 0) c = score;
+        } else {
+            const Entry e = list[at];
+            if (e.rank == 0) return;
+            token = (int)e.index;
+            c = (double)value_of(e.rank) - base + (double)score;
+        }
+        const unsigned long long u = (unsigned long long)__double_as_longlong(c + 0.0);
+        rank = u >> 63 ? ~u : u | 1ull << 63;
+    };
+    next();
     for (int j = 0; j < a.width; ++j) {
-        double c = -INFINITY;
-        int v = 0x7fffffff;
-        if (on && at < a.width) {
-            if (dead) {
-                v = at;
-            } else if (old) {   // eos, then the others in order
-                v = at == 0 ? a.eos : at - 1 + (at - 1 >= a.eos);
-                if (at == 0) c = score;
-            } else {
-                const Key k = rows[lane * a.width + at];
-                v = (int)key_index(k);
-                c = (double)key_value(k) - base + (double)score;
-            }
-        }
-        double bc = c;
-        int bw = lane;
-        bool bon = v != 0x7fffffff;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const double tc = __shfl_xor_sync(0xffffffffu, bc, o);
-            const int tw = __shfl_xor_sync(0xffffffffu, bw, o);
-            const bool ton = __shfl_xor_sync(0xffffffffu, (int)bon, o) != 0;
-            if (ton && (!bon || tc > bc || (tc == bc && tw < bw))) bc = tc, bw = tw, bon = true;
-        }
-        if (bw == lane) {
+        const uint32_t hi = (uint32_t)(rank >> 32), top = __reduce_max_sync(0xffffffffu, hi);
+        const uint32_t lo = hi == top ? (uint32_t)rank : 0, low = __reduce_max_sync(0xffffffffu, lo);
+        const int from = __ffs(__ballot_sync(0xffffffffu, hi == top && lo == low)) - 1;
+        if (lane == from) {
             const int out = seq * a.width + j;
-            a.tokens[out] = v;
+            a.tokens[out] = token;
             a.parents[out] = row;
             a.scores_out[out] = (float)c;
-            if (a.ended_out != nullptr) a.ended_out[out] = old || v == a.eos;
+            if (a.ended_out != nullptr) a.ended_out[out] = old || token == a.eos;
             ++at;
+            next();
         }
     }
 }
@@ -257,21 +295,21 @@ __device__ void choose(const Args &a, int seq, const Key *keys, const float2 *su
 // the first CTA's shared memory, which joins them. No scratch, one launch.
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32) k_beam_cluster(const Args a) {
-    __shared__ Key keys[kClusterTasks * kMaxWidth], rows[kMaxWidth * kMaxWidth];
+    __shared__ Entry best[kClusterTasks * kMaxWidth], rows[kMaxWidth * kMaxWidth];
     __shared__ float2 sums[kClusterTasks], lse[kMaxWidth];
     cg::cluster_group cluster = cg::this_cluster();
     const int ctas = cluster.num_blocks(), rank = cluster.block_rank(), seq = blockIdx.x / ctas;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    Key *keys0 = cluster.map_shared_rank(keys, 0);
+    Entry *best0 = cluster.map_shared_rank(best, 0);
     float2 *sums0 = cluster.map_shared_rank(sums, 0);
     cluster.sync();   // every CTA's shared memory is there
     for (int t = rank * kWarps + warp; t < a.width * a.chunks; t += ctas * kWarps) {
         const Seen s = read_part<T>(a, seq * a.width + t / a.chunks, t % a.chunks);
-        if (lane < a.width) keys0[(size_t)t * a.width + lane] = s.mine;
+        if (lane < a.width) best0[(size_t)t * a.width + lane] = s.mine;
         if (lane == 0) sums0[t] = make_float2(s.m, s.sum);
     }
     cluster.sync();
-    if (rank == 0) choose(a, seq, keys, sums, rows, lse);
+    if (rank == 0) choose(a, seq, best, sums, rows, lse);
 }
 
 // Larger calls: a warp per part over the whole GPU, the results in scratch; then a CTA per sequence.
@@ -282,15 +320,15 @@ __global__ void __launch_bounds__(kWarps * 32) k_beam_parts(const Args a, long l
     const long long t = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (t >= parts) return;
     const Seen s = read_part<T>(a, (int)(t / a.chunks), (int)(t % a.chunks));
-    if (lane < a.width) a.keys[t * a.width + lane] = s.mine;
+    if (lane < a.width) a.best[t * a.width + lane] = s.mine;
     if (lane == 0) a.sums[t] = make_float2(s.m, s.sum);
 }
 __global__ void __launch_bounds__(kWarps * 32) k_beam_choose(const Args a) {
-    __shared__ Key rows[kMaxWidth * kMaxWidth];
+    __shared__ Entry rows[kMaxWidth * kMaxWidth];
     __shared__ float2 lse[kMaxWidth];
     pdl_wait();
     const size_t first = (size_t)blockIdx.x * a.width * a.chunks;
-    choose(a, blockIdx.x, a.keys + first * a.width, a.sums + first, rows, lse);
+    choose(a, blockIdx.x, a.best + first * a.width, a.sums + first, rows, lse);
 }
 
 // How a call runs. A cluster serves a sequence until its CTAs would read over kClusterLogits each;
@@ -300,7 +338,7 @@ struct Shape {
     int chunks;
 };
 constexpr int kClusterLogits = 32768, kPartLogits = 1024;
-constexpr int kTargetParts = 152 * 24;
+constexpr int kTargetParts = 152 * 12;
 
 Shape shape_of(int n_seq, int width, int vocab) {
     const long long logits = (long long)width * vocab;
@@ -330,7 +368,7 @@ size_t talker_beam_scratch(int n_seq, int width, int vocab) {
     if (!sizes_ok(n_seq, width, vocab)) return 0;
     const Shape p = shape_of(n_seq, width, vocab);
     const size_t parts = (size_t)n_seq * width * p.chunks;
-    return p.ctas > 0 ? 0 : align16(parts * width * sizeof(Key)) + parts * sizeof(float2);
+    return p.ctas > 0 ? 0 : align16(parts * width * sizeof(Entry)) + parts * sizeof(float2);
 }
 
 talker_status talker_beam_select(const void *logits, int64_t row_stride, int dtype, const float *scores,
@@ -360,11 +398,12 @@ talker_status talker_beam_select(const void *logits, int64_t row_stride, int dty
         attr[0].val.clusterDim.x = p.ctas;
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.gridDim = dim3((unsigned)(n_seq * p.ctas));
+        cfg.numAttrs = p.ctas > 1;
         e = cudaLaunchKernelEx(&cfg, f32 ? k_beam_cluster<float> : k_beam_cluster<__nv_bfloat16>, a);
     } else {
         const long long parts = (long long)n_seq * width * p.chunks;
-        a.keys = static_cast<Key *>(scratch);
-        a.sums = reinterpret_cast<float2 *>(static_cast<char *>(scratch) + align16((size_t)parts * width * sizeof(Key)));
+        a.best = static_cast<Entry *>(scratch);
+        a.sums = reinterpret_cast<float2 *>(static_cast<char *>(scratch) + align16((size_t)parts * width * sizeof(Entry)));
         cfg.gridDim = dim3((unsigned)((parts + kWarps - 1) / kWarps));
         cfg.numAttrs = 0;
         e = cudaLaunchKernelEx(&cfg, f32 ? k_beam_parts<float> : k_beam_parts<__nv_bfloat16>, a, parts);

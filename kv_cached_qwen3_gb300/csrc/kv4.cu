@@ -57,63 +57,132 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, bool vec, const float (
     }
 }
 
-// Grid (items, streams, layers * 2): thread = 8 dims of one (row, head) of K or V; the 4 * NB
-// threads of a head row are neighbours, rows of a head follow one another.
+// Rows of one (stream, head) in one page, RP at a time, `passes` times: thread = 8 dims, the 4 * NB
+// threads of a row are neighbours. A lane's row: position pos(u) of the stream, row i(u) of the call.
+struct RowPlace {
+    unsigned char *tile;   // null: nothing to do
+    int prow;
+};
+
+__device__ __forceinline__ RowPlace place_of(const Kv4Rows &r, int tile_bytes, int s, int l, int h, bool is_v, long long pos,
+                                             bool report) {
+    if (pos < 0 || pos >= (long long)r.c.pages_per_stream * kPage) {
+        if (report && r.c.status != nullptr) atomicOr(r.c.status, ST_BAD_POSITION);
+        return {nullptr, 0};
+    }
+    const int page = r.c.page_table[(size_t)(r.stream0 + s) * r.c.pages_per_stream + (int)(pos / kPage)];
+    if (page < 0 || page >= r.c.n_pages) {
+        if (report && r.c.status != nullptr) atomicOr(r.c.status, ST_BAD_ARG);
+        return {nullptr, 0};
+    }
+    return {static_cast<unsigned char *>(is_v ? r.c.v : r.c.k) +
+                (((size_t)page * r.c.n_layers + r.layer0 + l) * r.c.n_kv_heads + h) * tile_bytes,
+            (int)(pos % kPage)};
+}
+
+// One row's eight dims between the tile and x; every lane of the warp takes part.
+template <int HD, bool READ>
+__device__ __forceinline__ void move8(unsigned char *tile, int prow, bool is_v, int b, int c, float (&x)[8]) {
+    using Tile = Kv4Tile<HD>;
+    constexpr int NB = Tile::NB;
+    unsigned char *word = tile + prow * Tile::kRow + q4_word_at<NB>(is_v, b, c);
+    unsigned char *scale = tile + Tile::kScales + (prow * NB + b) * 2;
+    if (READ) {
+        uint32_t w = tile != nullptr ? *reinterpret_cast<const uint32_t *>(word) : 0;
+        const float d = tile != nullptr ? __half2float(*reinterpret_cast<const __half *>(scale)) : 0.f;
+        if (is_v) w = v_word(w, b);
+        q4_values8(w, d, x);
+    } else {
+        unsigned short d;
+        uint32_t w = q4_codes8(x, d);
+        if (is_v) w = v_word(w, b);
+        if (tile == nullptr) return;
+        *reinterpret_cast<uint32_t *>(word) = w;
+        if (c == 0) *reinterpret_cast<unsigned short *>(scale) = d;
+    }
+}
+
+// Few rows: grid (items, streams, layers * 2), a head row per 4 * NB threads, rows of a head behind
+// one another.
 template <int HD, typename T, bool READ>
 __global__ void __launch_bounds__(kRowThreads) k_kv4_rows(const Kv4Rows r, const bool vec) {
     using Tile = Kv4Tile<HD>;
-    constexpr int NB = Tile::NB, TPR = 4 * NB;
+    constexpr int TPR = 4 * Tile::NB;
     const int s = blockIdx.y, l = blockIdx.z >> 1;
     const bool is_v = blockIdx.z & 1;
     const int sub = threadIdx.x % TPR, b = sub >> 2, c = sub & 3;
     const unsigned item = blockIdx.x * (kRowThreads / TPR) + threadIdx.x / TPR;
     const int h = (int)(item / (unsigned)r.T), i = (int)(item - (unsigned)h * r.T);
-    bool on = h < r.c.n_kv_heads && (r.count == nullptr || i < r.count[s]);
+    const bool on = h < r.c.n_kv_heads && (r.count == nullptr || i < r.count[s]);
     T *dense = static_cast<T *>(is_v ? r.v : r.k) + (l * r.st.layer + s * r.st.stream + i * r.st.row + h * r.st.head) +
                b * 32 + c * 8;
     float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (!READ && on) load8<T>(dense, vec, x);
-    unsigned char *tile = nullptr;
-    int prow = 0;
-    if (on) {
-        const long long pos = (r.start != nullptr ? (long long)r.start[s] : 0) + i;
-        if (pos < 0 || pos >= (long long)r.c.pages_per_stream * kPage) {
-            if (sub == 0 && r.c.status != nullptr) atomicOr(r.c.status, ST_BAD_POSITION);
-            on = false;
-        } else {
-            const int page = r.c.page_table[(size_t)(r.stream0 + s) * r.c.pages_per_stream + (int)(pos / kPage)];
-            prow = (int)(pos % kPage);
-            if (page < 0 || page >= r.c.n_pages) {
-                if (sub == 0 && r.c.status != nullptr) atomicOr(r.c.status, ST_BAD_ARG);
-                on = false;
+    RowPlace p{nullptr, 0};
+    if (on) p = place_of(r, Tile::kBytes, s, l, h, is_v, (r.start != nullptr ? (long long)r.start[s] : 0) + i, sub == 0);
+    move8<HD, READ>(p.tile, p.prow, is_v, b, c, x);
+    if (READ && p.tile != nullptr) store8(dense, vec, x);
+}
+
+// Many rows: grid (pages * heads, streams, layers * 2), a CTA per (page, head), whose rows it takes
+// kRowThreads / (4 * NB) at a time: one look-up of the page, and every load of the page in flight.
+// Bound by the dense rows' traffic (32 of 36.5 bytes a block of f32).
+template <int HD, typename T, bool READ>
+__global__ void __launch_bounds__(kRowThreads) k_kv4_pages(const Kv4Rows r, const bool vec) {
+    using Tile = Kv4Tile<HD>;
+    constexpr int TPR = 4 * Tile::NB, RP = kRowThreads / TPR, kPasses = kPage / RP;
+    const int s = blockIdx.y, l = blockIdx.z >> 1;
+    const bool is_v = blockIdx.z & 1;
+    const int h = blockIdx.x % r.c.n_kv_heads, slot = blockIdx.x / r.c.n_kv_heads;
+    const int sub = threadIdx.x % TPR, b = sub >> 2, c = sub & 3;
+    const long long start = r.start != nullptr ? (long long)r.start[s] : 0;
+    const int n = r.count != nullptr ? min(r.count[s], r.T) : r.T;
+    const long long first = (start >= 0 ? start / kPage : -((kPage - 1 - start) / kPage)) * kPage + (long long)slot * kPage;
+    const int lo = (int)max(0ll, start - first), hi = (int)min((long long)kPage, start + n - first);   // rows of this page
+    if (lo >= hi) return;
+    const RowPlace p = place_of(r, Tile::kBytes, s, l, h, is_v, first, threadIdx.x == 0);
+    if (p.tile == nullptr) return;
+    T *dense = static_cast<T *>(is_v ? r.v : r.k) + (l * r.st.layer + s * r.st.stream + h * r.st.head) + b * 32 + c * 8;
+    float x[kPasses][8];
+    if (!READ) {
+#pragma unroll
+        for (int u = 0; u < kPasses; ++u) {
+            const int row = u * RP + threadIdx.x / TPR;
+            if (row >= lo && row < hi) {
+                load8<T>(dense + (first + row - start) * r.st.row, vec, x[u]);
             } else {
-                tile = static_cast<unsigned char *>(is_v ? r.c.v : r.c.k) +
-                       (((size_t)page * r.c.n_layers + r.layer0 + l) * r.c.n_kv_heads + h) * Tile::kBytes;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[u][e] = 0.f;
             }
         }
     }
-    if constexpr (!READ) {
-        unsigned short d;
-        const uint32_t w = q4_codes8(x, d);
-        if (!on) return;
-        q4_store_codes<NB>(tile + prow * Tile::kRow, is_v, b, c, w);
-        if (c == 0) *reinterpret_cast<unsigned short *>(tile + Tile::kScales + (prow * NB + b) * 2) = d;
-    } else {
-        if (!on) return;
-        const uint32_t w = q4_load_codes<NB>(tile + prow * Tile::kRow, is_v, b, c);
-        const float d = __half2float(*reinterpret_cast<const __half *>(tile + Tile::kScales + (prow * NB + b) * 2));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = (float)((int)((w >> (4 * e)) & 15u) - 8) * d;
-        store8(dense, vec, x);
+    for (int u = 0; u < kPasses; ++u) {
+        const int row = u * RP + threadIdx.x / TPR;
+        move8<HD, READ>(row >= lo && row < hi ? p.tile : nullptr, row, is_v, b, c, x[u]);
+    }
+    if (READ) {
+#pragma unroll
+        for (int u = 0; u < kPasses; ++u) {
+            const int row = u * RP + threadIdx.x / TPR;
+            if (row >= lo && row < hi) store8(dense + (first + row - start) * r.st.row, vec, x[u]);
+        }
     }
 }
 
+// From this many rows a stream on, a CTA per page is faster.
+constexpr int kPageRowsMin = 16;
+
 template <int HD, typename T, bool READ>
 cudaError_t launch_rows_t(const Kv4Rows &r, bool vec, cudaStream_t s) {
-    const long long items = (long long)r.T * r.c.n_kv_heads;
-    const int per = kRowThreads / (HD / 8);
-    const dim3 grid((unsigned)((items + per - 1) / per), r.n_streams, 2 * r.n_layers);
-    k_kv4_rows<HD, T, READ><<<grid, kRowThreads, 0, s>>>(r, vec);
+    if (r.T >= kPageRowsMin) {
+        const long long slots = ((long long)r.T + kPage - 2) / kPage + 1;   // pages that T rows can touch
+        k_kv4_pages<HD, T, READ><<<dim3((unsigned)(slots * r.c.n_kv_heads), r.n_streams, 2 * r.n_layers), kRowThreads, 0, s>>>(r, vec);
+    } else {
+        const long long items = (long long)r.T * r.c.n_kv_heads;
+        const int per = kRowThreads / (HD / 8);
+        k_kv4_rows<HD, T, READ><<<dim3((unsigned)((items + per - 1) / per), r.n_streams, 2 * r.n_layers), kRowThreads, 0, s>>>(r, vec);
+    }
     return cudaGetLastError();
 }
 

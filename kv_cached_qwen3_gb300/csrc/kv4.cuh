@@ -25,16 +25,15 @@ constexpr int kv4_tile_bytes(int hd) { return hd * 36; }
 // codes (dim i in bits 4 i ..) and the block's scale bits.
 //
 // code = clamp(floor(8.5 - 8 x / m), 0, 15) has to be exact (a neighbouring code is off by a
-// whole step): with y = -x sign(m), M = |m| the code is at least k iff 16 y >= (2 k - 17) M.
-// fp32 finds the nearest such border k, and the sign of one fma, which rounds 16 y - (2 k - 17) M
-// only once, says on which side y lies. Blocks with tiny M are scaled by 2^60 first (exact), so
-// that neither 8 / M nor the sign can be lost.
+// whole step). t = 8.5 - 8 x / m in fp32 is off by less than 2e-6, so its floor is the code unless
+// t lies within 1e-5 of a whole number k; then the code is at least k iff 16 y >= (2 k - 17) M with
+// y = -x sign(m), M = |m|: the sign of one fma, which rounds 16 y - (2 k - 17) M only once. Blocks
+// with tiny M are scaled by 2^60 first (exact), so that neither 8 / M nor that sign can be lost.
 __device__ __forceinline__ uint32_t q4_codes8(const float (&x)[8], unsigned short &d_bits) {
-    float m = x[0];
-    bool bad = false;
+    float m = x[0], zero = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        bad |= !(fabsf(x[i]) <= 3.402823466e38f);
+        zero = fmaf(x[i], 0.f, zero);   // NaN if a value is not finite
         if (fabsf(x[i]) > fabsf(m)) m = x[i];
     }
     const int lane = threadIdx.x & 31;
@@ -42,42 +41,55 @@ __device__ __forceinline__ uint32_t q4_codes8(const float (&x)[8], unsigned shor
     for (int o = 1; o <= 2; o <<= 1) {
         const float other = __shfl_xor_sync(0xffffffffu, m, o);
         if (fabsf(other) > fabsf(m) || (fabsf(other) == fabsf(m) && (lane & o))) m = other;
-        bad |= __shfl_xor_sync(0xffffffffu, (int)bad, o) != 0;
     }
+    // the warp's bits of "not finite", of this group of four
+    const bool bad = (__ballot_sync(0xffffffffu, !(zero == 0.f)) >> (lane & ~3) & 15u) != 0;
     m = fminf(fmaxf(m, -524032.f), 524032.f);
     d_bits = bad ? 0x7e00 : __half_as_ushort(__float2half_rn(m * -0.125f));
-    const float up = fabsf(m) < 1e-30f ? 1152921504606846976.f : 1.f;   // 2^60
-    const float M = fabsf(m) * up;
-    if (bad || M == 0.f) return 0x88888888u;
-    const float s = m > 0.f ? -up : up, id = 8.f / M;
+    if (bad || m == 0.f) return 0x88888888u;
+    const bool tiny = fabsf(m) < 1e-30f;
+    const float id = -8.f / (tiny ? m * 1152921504606846976.f : m);   // 2^60
     uint32_t w = 0;
+    bool near = tiny;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float y = x[i] * s;
-        const float k = rintf(fminf(fmaxf(fmaf(y, id, 8.5f), 0.f), 17.f));
-        const float side = fmaf(fmaf(-2.f, k, 17.f), M, 16.f * y);
-        const int n = (int)k - (side < 0.f ? 1 : 0);
-        w |= (uint32_t)min(max(n, 0), 15) << (4 * i);
+    for (int i = 7; i >= 0; --i) {
+        // t in [0, 16): its floor is the mantissa's end of t + 2^23 rounded down
+        const float t = fminf(fmaxf(fmaf(x[i], id, 8.5f), 0.f), 15.9f), f = __fadd_rd(t, 8388608.f);
+        near |= fabsf((f - 8388608.f) + 0.5f - t) > 0.49999f;
+        w = w * 16 + (uint32_t)(__float_as_int(f) - 0x4b000000);
+    }
+    if (near) {
+        const float up = tiny ? 1152921504606846976.f : 1.f, M = fabsf(m) * up, s = m > 0.f ? -up : up, ip = 8.f / M;
+        w = 0;
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+            float v = x[0];
+#pragma unroll
+            for (int j = 1; j < 8; ++j) v = i == j ? x[j] : v;
+            const float y = v * s, k = rintf(fminf(fmaxf(fmaf(y, ip, 8.5f), 0.f), 17.f));
+            const float side = fmaf(fmaf(-2.f, k, 17.f), M, 16.f * y);
+            w |= (uint32_t)min(max((int)k - (side < 0.f ? 1 : 0), 0), 15) << (4 * i);
+        }
     }
     return w;
 }
 
-// The eight codes of dims 8 c .. 8 c + 7 of block b of a row, in the order of the K and V rows
-// (the K row keeps them in one word, the V row in two halves).
+// The 32-bit word of a row that lane (b, c), four lanes to a block, writes or reads. K: its own
+// eight codes. V: the codes of two neighbouring blocks for group g = 2 c + b % 2, which lanes b and
+// b ^ 1 (lane ^ 4) exchange: v_word turns a lane's codes into its word, and back.
 template <int NB>
-__device__ __forceinline__ void q4_store_codes(unsigned char *row, bool is_v, int b, int c, uint32_t w) {
-    if (!is_v) {
-        *reinterpret_cast<uint32_t *>(row + c * 4 * NB + 4 * b) = w;
-    } else {
-        *reinterpret_cast<uint16_t *>(row + (2 * c) * 2 * NB + 2 * b) = (uint16_t)w;
-        *reinterpret_cast<uint16_t *>(row + (2 * c + 1) * 2 * NB + 2 * b) = (uint16_t)(w >> 16);
-    }
+__device__ __forceinline__ int q4_word_at(bool is_v, int b, int c) {
+    return is_v ? (2 * c + (b & 1)) * 2 * NB + 2 * (b & ~1) : c * 4 * NB + 4 * b;
 }
-template <int NB>
-__device__ __forceinline__ uint32_t q4_load_codes(const unsigned char *row, bool is_v, int b, int c) {
-    if (!is_v) return *reinterpret_cast<const uint32_t *>(row + c * 4 * NB + 4 * b);
-    return (uint32_t)*reinterpret_cast<const uint16_t *>(row + (2 * c) * 2 * NB + 2 * b) |
-           (uint32_t)*reinterpret_cast<const uint16_t *>(row + (2 * c + 1) * 2 * NB + 2 * b) << 16;
+__device__ __forceinline__ uint32_t v_word(uint32_t w, int b) {
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, w, 4);
+    return b & 1 ? __byte_perm(other, w, 0x7632) : __byte_perm(w, other, 0x5410);
+}
+// The eight values of a lane's codes.
+__device__ __forceinline__ void q4_values8(uint32_t w, float d, float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)   // the code goes under the exponent of 2^23
+        x[i] = (__int_as_float((int)((w >> (4 * i) & 15u) | 0x4b000000u)) - 8388616.f) * d;
 }
 
 // Rows of a call to the cache (or back), see talker_kv4_write.

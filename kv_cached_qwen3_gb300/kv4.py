@@ -190,7 +190,17 @@ class KV4Cache:
         self._call(self._lib.talker_kv4_reorder, "talker_kv4_reorder", self._ref, at, R, lens_at,
                    self._ints("table_out", table_out, self.page_table.numel()),
                    self._ints("lens_out", lens_out, self.n_streams))
-        return KV4Cache.over(self.k, self.v, table_out.view(self.page_table.shape), self.head_dim, self.status), lens_out
+        return self._with_table(table_out.view(self.page_table.shape)), lens_out
+
+    def _with_table(self, page_table) -> "KV4Cache":
+        """This cache under another page table of the same shape."""
+        other = KV4Cache.__new__(KV4Cache)
+        other.__dict__.update(self.__dict__)
+        other.page_table = page_table
+        other._c = _Cache.from_buffer_copy(self._c)
+        other._c.page_table = page_table.data_ptr()
+        other._ref = ctypes.addressof(other._c)
+        return other
 
     def sync_status(self) -> int:
         """Wait for the device and return the status word, which is cleared (0: nothing to report)."""
