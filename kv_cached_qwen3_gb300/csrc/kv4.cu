@@ -9,13 +9,15 @@ namespace {
 
 constexpr int kRowThreads = 256;
 
+// Eight dims by one access of 32 bytes (f32) or 16 (bf16), or dim by dim.
 template <typename T>
 __device__ __forceinline__ void load8(const T *p, bool vec, float (&x)[8]);
 template <>
 __device__ __forceinline__ void load8<float>(const float *p, bool vec, float (&x)[8]) {
     if (vec) {
-        const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+        asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+                     : "l"(p));
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = p[i];
@@ -35,8 +37,9 @@ __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16 *p, boo
 }
 __device__ __forceinline__ void store8(float *p, bool vec, const float (&x)[8]) {
     if (vec) {
-        *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
-        *reinterpret_cast<float4 *>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+        asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]),
+                     "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                     : "memory");
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) p[i] = x[i];
@@ -320,9 +323,9 @@ __global__ void __launch_bounds__(256) k_reorder(const KvReorder r, int table_bl
 
 cudaError_t launch_kv4_rows(const Kv4Rows &r, int dtype, bool read, cudaStream_t s) {
     if (r.T == 0 || r.n_streams == 0 || r.n_layers == 0) return cudaSuccess;
-    const int size = dtype == TALKER_DTYPE_BF16 ? 2 : 4, v = 16 / size;
-    // 16-byte accesses where every head row starts on a 16-byte boundary
-    const bool vec = !((reinterpret_cast<uintptr_t>(r.k) | reinterpret_cast<uintptr_t>(r.v)) & 15u) &&
+    const int size = dtype == TALKER_DTYPE_BF16 ? 2 : 4, v = 8;
+    // one access for eight dims where every head row starts on its boundary
+    const bool vec = (reinterpret_cast<uintptr_t>(r.k) | reinterpret_cast<uintptr_t>(r.v)) % (v * size) == 0 &&
                      r.st.layer % v == 0 && r.st.stream % v == 0 && r.st.row % v == 0 && r.st.head % v == 0;
     const bool bf16 = dtype == TALKER_DTYPE_BF16;
     if (r.c.head_dim == 128) {

@@ -25,10 +25,10 @@ constexpr int kv4_tile_bytes(int hd) { return hd * 36; }
 // codes (dim i in bits 4 i ..) and the block's scale bits.
 //
 // code = clamp(floor(8.5 - 8 x / m), 0, 15) has to be exact (a neighbouring code is off by a
-// whole step). t = 8.5 - 8 x / m in fp32 is off by less than 2e-6, so its floor is the code unless
-// t lies within 1e-5 of a whole number k; then the code is at least k iff 16 y >= (2 k - 17) M with
-// y = -x sign(m), M = |m|: the sign of one fma, which rounds 16 y - (2 k - 17) M only once. Blocks
-// with tiny M are scaled by 2^60 first (exact), so that neither 8 / M nor that sign can be lost.
+// whole step, and values exactly between two codes are common in bf16). The whole number k nearest to
+// 8.5 - 8 x / m comes from fp32, off by less than 2e-6; the code is k, or k - 1 where
+// (17 - 2 k) |m| < 16 x sign(m): the sign of one fma, which rounds that difference only once. Blocks
+// with tiny |m| are scaled by 2^60 first (exact), so that neither 8 / m nor the sign can be lost.
 __device__ __forceinline__ uint32_t q4_codes8(const float (&x)[8], unsigned short &d_bits) {
     float m = x[0], zero = 0.f;
 #pragma unroll
@@ -44,32 +44,26 @@ __device__ __forceinline__ uint32_t q4_codes8(const float (&x)[8], unsigned shor
     }
     // the warp's bits of "not finite", of this group of four
     const bool bad = (__ballot_sync(0xffffffffu, !(zero == 0.f)) >> (lane & ~3) & 15u) != 0;
-    m = fminf(fmaxf(m, -524032.f), 524032.f);
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = x[i];
+    if (fabsf(m) > 524032.f) {
+        m = fminf(fmaxf(m, -524032.f), 524032.f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = fminf(fmaxf(y[i], -524032.f), 524032.f);
+    }
     d_bits = bad ? 0x7e00 : __half_as_ushort(__float2half_rn(m * -0.125f));
     if (bad || m == 0.f) return 0x88888888u;
-    const bool tiny = fabsf(m) < 1e-30f;
-    const float id = -8.f / (tiny ? m * 1152921504606846976.f : m);   // 2^60
+    const float up = fabsf(m) < 1e-30f ? 1152921504606846976.f : 1.f;   // 2^60
+    const float M = fabsf(m) * up, s = m > 0.f ? -16.f * up : 16.f * up, id = 0.5f / M;
+    constexpr float kRound = 12582912.f;   // 1.5 2^23: x + kRound holds the nearest whole number to x
     uint32_t w = 0;
-    bool near = tiny;
 #pragma unroll
     for (int i = 7; i >= 0; --i) {
-        // t in [0, 16): its floor is the mantissa's end of t + 2^23 rounded down
-        const float t = fminf(fmaxf(fmaf(x[i], id, 8.5f), 0.f), 15.9f), f = __fadd_rd(t, 8388608.f);
-        near |= fabsf((f - 8388608.f) + 0.5f - t) > 0.49999f;
-        w = w * 16 + (uint32_t)(__float_as_int(f) - 0x4b000000);
-    }
-    if (near) {
-        const float up = tiny ? 1152921504606846976.f : 1.f, M = fabsf(m) * up, s = m > 0.f ? -up : up, ip = 8.f / M;
-        w = 0;
-#pragma unroll 1
-        for (int i = 0; i < 8; ++i) {
-            float v = x[0];
-#pragma unroll
-            for (int j = 1; j < 8; ++j) v = i == j ? x[j] : v;
-            const float y = v * s, k = rintf(fminf(fmaxf(fmaf(y, ip, 8.5f), 0.f), 17.f));
-            const float side = fmaf(fmaf(-2.f, k, 17.f), M, 16.f * y);
-            w |= (uint32_t)min(max((int)k - (side < 0.f ? 1 : 0), 0), 15) << (4 * i);
-        }
+        const float z = y[i] * s, r = fmaf(z, id, 8.5f) + kRound;
+        const float side = fmaf(fmaf(-2.f, r - kRound, 17.f), M, z);
+        const int n = __float_as_int(r) - __float_as_int(kRound) + (__float_as_int(side) >> 31);
+        w = w * 16 + (uint32_t)min(n, 15);
     }
     return w;
 }
