@@ -15,6 +15,7 @@ constexpr int kWarps = 4;
 constexpr int kCtas = 3;                  // CTAs a multiprocessor holds: 12 warps, 168 registers
 constexpr int kSlots = 3;                 // tiles (a page's K, its V, the next page's K ...) a warp has in shared memory
 constexpr int kMaxG = 8;
+constexpr int kMaxGrid = 1024;            // CTAs of a launch
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTopBits = 14;              // probabilities times value scales stay below 2^14 (fp16) ...
 constexpr int kNewBits = 9;               // ... and are brought below 2^9 when they would pass it
@@ -151,14 +152,29 @@ __device__ __forceinline__ bool bounded_wait(uint64_t *bar, uint32_t parity) {
 }
 
 constexpr size_t attend_smem(int hd) {
-    const size_t ring = (size_t)kWarps * kSlots * kv4_tile_bytes(hd), merge = (size_t)kWarps * kMaxG * hd * 4;
-    return ring > merge ? ring : merge;
+    return (size_t)kWarps * kSlots * kv4_tile_bytes(hd) + (size_t)kWarps * kMaxG * hd * 4;
 }
 
-template <typename T>
-__device__ __forceinline__ void load_dims8(const T *p, float (&x)[8]) {
+// Eight dims of a query head; vec: rows lie on 16-byte boundaries.
+__device__ __forceinline__ void load_dims8(const float *p, bool vec, float (&x)[8]) {
+    if (vec) {
+        const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = (float)p[i];
+        for (int i = 0; i < 8; ++i) x[i] = p[i];
+    }
+}
+__device__ __forceinline__ void load_dims8(const __nv_bfloat16 *p, bool vec, float (&x)[8]) {
+    if (vec) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[2 * i] = bf16lo(w[i]), x[2 * i + 1] = bf16hi(w[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __bfloat162float(p[i]);
+    }
 }
 
 // The work of a call in units of one page for every warp of a CTA: each (stream, KV head) row has
@@ -255,9 +271,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
     const long long n = min(U, (long long)gridDim.x);
     if (blockIdx.x >= n) return;
     const long long x_begin = blockIdx.x * U / n, x_end = (blockIdx.x + 1) * U / n;
-    int b = stream_of(a, x_begin, before);
-    int len = checked_len(a, b), nu = units_of(a, len);
-    int g = (int)((x_begin - before) / nu), u0 = (int)((x_begin - before) % nu);
+    const int b0 = stream_of(a, x_begin, before), len0 = checked_len(a, b0), nu0 = units_of(a, len0);
     int slot = 0, phase = 0;   // where the next K tile goes, and the parity that each slot's next wait has
     const uint32_t lo_mask = kParts == 1 || c >= 2 ? 0xffffe000u : 0u;
     const uint32_t eight[4] = {0x80088008u, 0x80888088u, 0x80088008u, 0x80888088u};   // -8 2^-24 (nibbles), -136 2^-24 (bytes)
@@ -265,37 +279,55 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
     // two rows of codes that eight lanes load together lie in other banks.
     const int c2 = 4 + (c ^ 1), key_r = r & 1 ? 4 + ((r >> 1) ^ 1) : r >> 1;
 
-    for (long long x = x_begin; x < x_end;) {
-        const int u1 = (int)min((long long)nu, u0 + (x_end - x));
-        const int npages = pages_of(len);
-        const int pb = u0 * kWarps, pe = u1 == nu ? npages : u1 * kWarps;
-        if (len < 0 && threadIdx.x == 0 && a.c.status != nullptr) atomicOr(a.c.status, ST_BAD_POSITION);
-        const int *ptab = a.c.page_table + (size_t)b * a.c.pages_per_stream;
-        const size_t head_off = ((size_t)a.layer * a.c.n_kv_heads + g) * Tile::kBytes;
-        const size_t page_bytes = (size_t)a.c.n_layers * a.c.n_kv_heads * Tile::kBytes;
-        const int n_it = pb + warp < pe ? (pe - pb - warp + kWarps - 1) / kWarps : 0;
-        // lane i holds the page number of iteration 32 j + i
-        auto page_of = [&](int it) { return it < n_it ? ptab[pb + warp + it * kWarps] : 0; };
-        auto good = [&](int page) { return page >= 0 && page < a.c.n_pages; };
-        // a tile to a slot, by one lane; a bad page number copies page 0, which is not used
-        auto issue = [&](int to, const void *pool, int page) {
-            mbar_arrive_expect_tx(&bars[warp][to], Tile::kBytes);
-            bulk_g2s(ring + to * Tile::kBytes, static_cast<const unsigned char *>(pool) + (good(page) ? page : 0) * page_bytes + head_off,
-                     Tile::kBytes, &bars[warp][to]);
-        };
-        auto wait = [&](int at) {
-            const bool ok = bounded_wait(&bars[warp][at], phase >> at & 1);
-            phase ^= 1 << at;
-            return !__any_sync(0xffffffffu, !ok);
-        };
-        auto after = [](int at) { return at == kSlots - 1 ? 0 : at + 1; };
-        int pages = page_of(lane), ahead = page_of(32 + lane);
-        int page = __shfl_sync(0xffffffffu, pages, 0), page1 = __shfl_sync(0xffffffffu, pages, 1);
-        if (lane == 0 && n_it > 0) issue(slot, a.c.k, page), issue(after(slot), a.c.v, page);
-        if (lane == 0 && n_it > 1) issue(after(after(slot)), a.c.k, page1);
+    // Units [u0, u1) of the row of stream b and KV head g, which has nu; `left` units of the CTA's follow.
+    // Kept in shared memory, a copy for each warp, so that the loop over pages has the registers.
+    struct Range {
+        int b, g, len, nu, u0, u1;
+        long long left;
+    };
+    __shared__ Range ranges[kWarps];
+    Range &at = ranges[warp];
+    auto good = [&](int page) { return page >= 0 && page < a.c.n_pages; };
+    // a tile to a slot, by one lane; a bad page number copies page 0, which is not used
+    auto issue = [&](int to, const void *pool, int page, int g) {
+        const size_t tile = ((size_t)(good(page) ? page : 0) * a.c.n_layers + a.layer) * a.c.n_kv_heads + g;
+        mbar_arrive_expect_tx(&bars[warp][to], Tile::kBytes);
+        bulk_g2s(ring + to * Tile::kBytes, static_cast<const unsigned char *>(pool) + tile * Tile::kBytes, Tile::kBytes,
+                 &bars[warp][to]);
+    };
+    auto wait = [&](int at) {
+        const bool ok = bounded_wait(&bars[warp][at], phase >> at & 1);
+        phase ^= 1 << at;
+        return !__any_sync(0xffffffffu, !ok);
+    };
+    auto after = [](int at) { return at == kSlots - 1 ? 0 : at + 1; };
+    // of the warp's pages: how many, the numbers of 32 j + lane, of this one and of the next
+    int n_it = 0, rows = 0, pages = 0, ahead = 0, page = 0, page1 = 0;
+    auto page_of = [&](int it) {
+        const int *p = a.c.page_table + (size_t)at.b * a.c.pages_per_stream + at.u0 * kWarps + warp;
+        return it < n_it ? p[it * kWarps] : 0;
+    };
+    auto open = [&](int b, int g, int len, int nu, int u0, long long left) {   // ... and its first copies
+        const int u1 = (int)min((long long)nu, u0 + left), pb = u0 * kWarps + warp, pe = u1 == nu ? pages_of(len) : u1 * kWarps;
+        n_it = pb < pe ? (pe - pb + kWarps - 1) / kWarps : 0;
+        rows = len - pb * kPage;
+        if (lane == 0) at = {b, g, len, nu, u0, u1, left - (u1 - u0)};
+        __syncwarp();
+        pages = page_of(lane);
+        ahead = page_of(32 + lane);
+        page = __shfl_sync(0xffffffffu, pages, 0);
+        page1 = __shfl_sync(0xffffffffu, pages, 1);
+        if (lane == 0 && n_it > 0) issue(slot, a.c.k, page, g), issue(after(slot), a.c.v, page, g);
+        if (lane == 0 && n_it > 1) issue(after(after(slot)), a.c.k, page1, g);
+    };
+    open(b0, (int)((x_begin - before) / nu0), len0, nu0, (int)((x_begin - before) % nu0), x_end - x_begin);
+
+    for (bool begins = true;; begins = false) {
+        if (at.len < 0 && threadIdx.x == 0 && a.c.status != nullptr) atomicOr(a.c.status, ST_BAD_POSITION);
 
         // this lane's query head (rows beyond G compute on zeros)
         const int hq = kParts == 2 ? r & 3 : r;
+        const bool q_vec = (reinterpret_cast<uintptr_t>(a.q) & 15u) == 0 && a.q_row * sizeof(TI) % 16 == 0;
         const float cs = a.scale * kLog2e;
         uint32_t qf[NB][2][2], ql[NB][2][2];       // (ql: WIDE only)
         uint32_t qc[2];                            // -8 sum(q) of the blocks, in two parts, times 2^kCorrBits
@@ -305,7 +337,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
                 if (hq < G) {
-                    load_dims8(static_cast<const TI *>(a.q) + b * a.q_row + (size_t)(g * G + hq) * HD + nb * 32 + c * 8, x[nb]);
+                    load_dims8(static_cast<const TI *>(a.q) + at.b * a.q_row + (size_t)(at.g * G + hq) * HD + nb * 32 + c * 8, q_vec, x[nb]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) x[nb][i] = 0.f;
@@ -372,7 +404,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
                 ahead = page_of(it + 34 + lane);
             }
             const int page2 = __shfl_sync(0xffffffffu, pages, (it + 2) % 32), vslot = after(slot);
-            const int valid = min(kPage, len - (pb + warp + it * kWarps) * kPage);
+            const int valid = min(kPage, rows - it * kWarps * kPage);
             constexpr int H = NB / 2;
             const uint32_t kt = smem_u32(ring) + slot * Tile::kBytes, vt = smem_u32(ring) + vslot * Tile::kBytes;
             failed = !wait(slot);
@@ -435,7 +467,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
             __syncwarp();
             if (lane == 0 && it + 1 < n_it) {   // the next page's V over this K
                 fence_proxy_async();
-                issue(slot, a.c.v, page1);
+                issue(slot, a.c.v, page1, at.g);
             }
             failed = !wait(vslot);
             if (failed) break;
@@ -544,7 +576,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
             __syncwarp();
             if (lane == 0 && it + 2 < n_it) {   // the K after the next over this V
                 fence_proxy_async();
-                issue(vslot, a.c.k, page2);
+                issue(vslot, a.c.k, page2, at.g);
             }
             slot = after(vslot);
             page = page1;
@@ -555,7 +587,18 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
             for (int i = 0; i < kSlots; ++i) bounded_wait(&bars[warp][i], phase >> i & 1);
         }
 
-        // the warp's (m, l, O) to shared memory, over the ring
+        // The next range's first copies go out now. (This warp's reads and writes of its ring lie behind it.)
+        const Range done = at;
+        const int b = done.b, g = done.g;
+        if (done.left > 0) {
+            const bool row_ends = g == a.c.n_kv_heads - 1;
+            const int nb = row_ends ? b + 1 : b, nl = row_ends ? checked_len(a, nb) : done.len;
+            fence_proxy_async();
+            __syncwarp();
+            open(nb, row_ends ? 0 : g + 1, nl, row_ends ? units_of(a, nl) : done.nu, 0, done.left);
+        }
+
+        // the warp's (m, l, O) to shared memory
 #pragma unroll
         for (int j = 4; j < 32; j <<= 1)
             l2 = l2 + f2(__shfl_xor_sync(0xffffffffu, f2_lo(l2), j), __shfl_xor_sync(0xffffffffu, f2_hi(l2), j));
@@ -564,7 +607,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
             l2 = f2(m0, m0);
         }
         __syncthreads();
-        float *wo = reinterpret_cast<float *>(ring_all);   // [kWarps][kMaxG][HD]
+        float *wo = reinterpret_cast<float *>(ring_all + kWarps * kSlots * Tile::kBytes);   // [kWarps][kMaxG][HD]
         if (r == 0 && (kParts == 1 || c < 2)) {
             wm[warp][2 * c] = m0, wm[warp][2 * c + 1] = m1;
             wl[warp][2 * c] = f2_lo(l2), wl[warp][2 * c + 1] = f2_hi(l2);
@@ -580,7 +623,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
                 if (kParts == 1 || c < 2) wo[(warp * kMaxG + h) * HD + dim] = y;
             }
         // the step's own row, as one more part of the row's first units
-        const bool fresh = u0 == 0 && len >= 0 && a.k_new != nullptr;
+        const bool fresh = done.u0 == 0 && done.len >= 0 && a.k_new != nullptr;
         if (fresh) {
             const TI *kn = static_cast<const TI *>(a.k_new) + b * a.new_row + (size_t)g * HD;
             for (int h = warp; h < G; h += kWarps) {
@@ -593,7 +636,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
             }
         }
         __syncthreads();
-        const bool whole = u0 == 0 && u1 == nu;
+        const bool whole = done.u0 == 0 && done.u1 == done.nu;
         for (int idx = threadIdx.x; idx < G * HD; idx += kWarps * 32) {
             const int h = idx / HD, d = idx % HD;
             float M = fresh ? wm[kWarps][h] : -INFINITY, L = 0.f, O = 0.f;
@@ -613,69 +656,70 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
             if (whole) {
                 static_cast<TO *>(a.out)[((size_t)b * a.n_q + g * G + h) * HD + d] = (TO)(L == 0.f ? 0.f : O / L);
             } else {
-                float *ws = a.scratch + (((size_t)blockIdx.x * 2 + (x != x_begin)) * kMaxG + h) * (HD + 4);
+                float *ws = a.scratch + (((size_t)blockIdx.x * 2 + !begins) * kMaxG + h) * (HD + 4);
                 ws[4 + d] = O;
                 if (d == 0) ws[0] = M, ws[1] = L;
             }
         }
-        x += u1 - u0;
-        u0 = 0;
-        if (x < x_end) {
-            if (++g == a.c.n_kv_heads) {
-                g = 0;
-                ++b;
-                len = checked_len(a, b);
-                nu = units_of(a, len);
-            }
-            __syncthreads();       // the ring is free again ...
-            fence_proxy_async();   // ... for copies behind these reads and writes
-            __syncwarp();
-        }
+        if (done.left == 0) break;
     }
 }
 
-// Grid (n_q, B), HD threads: the parts of rows that several CTAs shared, joined in order.
-template <int HD, typename TO>
-__global__ void __launch_bounds__(HD) k_kv4_combine(const Kv4Attend a, const int grid) {
-    constexpr int kAhead = 8;   // parts requested at a time
+// Grid (n_q, B): the parts of rows that several CTAs shared, joined. The maxima and sums of all parts
+// are read at once, then each group of HD threads adds up every kGroups-th part, several in flight.
+// A few rows have many parts each (512 threads: their reads in few steps); many rows have about two.
+constexpr int kFewThreads = 128, kManyThreads = 512;
+template <int HD, typename TO, int kThreads>
+__global__ void __launch_bounds__(kThreads) k_kv4_combine(const Kv4Attend a, const int grid) {
+    constexpr int kGroups = kThreads / HD, kAhead = 8, kWarpsHere = kThreads / 32;
+    __shared__ float weight[kMaxGrid], red[2][kWarpsHere], sums[kGroups][HD];
     const int b = blockIdx.y, G = a.n_q / a.c.n_kv_heads, g = blockIdx.x / G, h = blockIdx.x % G;
-    pdl_wait();
-    long long before;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = threadIdx.x % HD, group = threadIdx.x / HD;
+    long long before;   // (lengths were there before the kernel that this one follows)
     const long long U = count_units(a, b, before) * a.c.n_kv_heads;
     const int nu = units_of(a, checked_len(a, b));
     const long long n = min(U, (long long)grid), x0 = before * a.c.n_kv_heads + (long long)g * nu;
     const int first = (int)(((x0 + 1) * n - 1) / U), last = (int)(((x0 + nu) * n - 1) / U);   // CTAs of the row's ends
+    pdl_wait();
     if (first == last) return;
-    auto part = [&](int i) {
-        const int slot = i == first && i * U / n != x0;
-        return a.scratch + (((size_t)i * 2 + slot) * kMaxG + h) * (HD + 4);
-    };
-    float M = -INFINITY, L = 0.f, O = 0.f;
-    for (int i0 = first; i0 <= last; i0 += kAhead) {
-        float m[kAhead];
+    const int tail = first * U / n != x0;   // the first CTA begins with another row
+    auto part = [&](int i) { return a.scratch + (((size_t)i * 2 + (i == first ? tail : 0)) * kMaxG + h) * (HD + 4); };
+    float m = -INFINITY;
+    for (int i = first + threadIdx.x; i <= last; i += kThreads) m = fmaxf(m, part(i)[0]);
+    m = warp_max(m);
+    if (lane == 0) red[0][warp] = m;
+    __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) m[i] = i0 + i <= last ? part(i0 + i)[0] : -INFINITY;
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) M = fmaxf(M, m[i]);
+    for (int w = 0; w < kWarpsHere; ++w) m = fmaxf(m, red[0][w]);
+    float L = 0.f;
+    for (int i = first + threadIdx.x; i <= last; i += kThreads) {
+        const float2 ml = *reinterpret_cast<const float2 *>(part(i));
+        const float e = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
+        weight[i - first] = e;
+        L = fmaf(ml.y, e, L);
     }
-    for (int i0 = first; i0 <= last; i0 += kAhead) {
-        float m[kAhead], l[kAhead], o[kAhead];
+    L = warp_sum(L);
+    if (lane == 0) red[1][warp] = L;
+    __syncthreads();
+    L = 0.f;
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const bool in = i0 + i <= last;
-            const float *ws = part(in ? i0 + i : last);
-            m[i] = in ? ws[0] : -INFINITY;
-            l[i] = in ? ws[1] : 0.f;
-            o[i] = in ? ws[4 + threadIdx.x] : 0.f;
-        }
+    for (int w = 0; w < kWarpsHere; ++w) L += red[1][w];
+    float O = 0.f;
+    for (int i0 = first + group; i0 <= last; i0 += kGroups * kAhead) {
+        float o[kAhead];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const float e = m[i] == -INFINITY ? 0.f : ex2(m[i] - M);
-            L = fmaf(l[i], e, L);
-            O = fmaf(o[i], e, O);
-        }
+        for (int i = 0; i < kAhead; ++i) o[i] = i0 + i * kGroups <= last ? part(i0 + i * kGroups)[4 + d] : 0.f;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (i0 + i * kGroups <= last) O = fmaf(o[i], weight[i0 + i * kGroups - first], O);
     }
-    static_cast<TO *>(a.out)[((size_t)b * a.n_q + blockIdx.x) * HD + threadIdx.x] = (TO)(L == 0.f ? 0.f : O / L);
+    sums[group][d] = O;
+    __syncthreads();
+    if (group != 0) return;
+    O = 0.f;
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) O += sums[i][d];
+    static_cast<TO *>(a.out)[((size_t)b * a.n_q + blockIdx.x) * HD + d] = (TO)(L == 0.f ? 0.f : O / L);
 }
 
 template <int HD, typename TI, typename TO>
@@ -688,14 +732,15 @@ cudaError_t launch_t(const Kv4Attend &a, cudaStream_t s) {
     if (e != cudaSuccess || a.one_unit) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.n_q, a.B);
-    cfg.blockDim = dim3(HD);
+    const bool many = a.grid >= 8ll * a.B * a.c.n_kv_heads;   // parts per row
+    cfg.blockDim = dim3(many ? kManyThreads : kFewThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_kv4_combine<HD, TO>, a, a.grid);
+    return cudaLaunchKernelEx(&cfg, many ? k_kv4_combine<HD, TO, kManyThreads> : k_kv4_combine<HD, TO, kFewThreads>, a, a.grid);
 }
 
 template <int HD>
@@ -715,7 +760,7 @@ Kv4AttendShape kv4_attend_shape(int B, int n_kv, int max_len, int n_sm) {
     Kv4AttendShape p;
     p.one_unit = pages <= kWholePages;
     const long long units = p.one_unit ? rows : rows * ((pages + kWarps - 1) / kWarps);
-    p.grid = (int)std::max<long long>(1, std::min<long long>(units, (long long)kCtas * n_sm));
+    p.grid = (int)std::max<long long>(1, std::min<long long>(units, std::min(kCtas * n_sm, kMaxGrid)));
     return p;
 }
 
