@@ -56,8 +56,10 @@ typedef enum {
  * ggml Q8_0 blocks): per head row, blocks of 32 int8 codes with an fp16 scale max|x|/127.
  * A call attends the rows cached by earlier calls dequantized and its own rows exactly.
  * It needs bf16 weights and head_dim 64 or 128; talker_prefill_append with it needs
- * head_dim 128 (EINVAL otherwise). */
-typedef enum { TALKER_DTYPE_F32 = 0, TALKER_DTYPE_BF16 = 1, TALKER_DTYPE_Q8_0 = 2 } talker_dtype;
+ * head_dim 128 (EINVAL otherwise).
+ * TALKER_DTYPE_Q4_0 likewise, with blocks of 32 4-bit codes and an fp16 scale as
+ * talker_kv4.h defines them: 4.5 bits an element. */
+typedef enum { TALKER_DTYPE_F32 = 0, TALKER_DTYPE_BF16 = 1, TALKER_DTYPE_Q8_0 = 2, TALKER_DTYPE_Q4_0 = 3 } talker_dtype;
 
 /* Geometry and storage formats (names as in the rightkit-qts TtsTransformerConfig).
  * Supported: head_dim in {32, 64, 128}; n_q_heads a multiple of n_kv_heads with
@@ -114,6 +116,18 @@ talker_status talker_kv_init_batched(talker_t *t, int n_streams, int max_seq_len
 /* Set stream's length to new_len (0 <= new_len <= current length). Rows past
  * new_len become stale and are never read again. Errors: EINVAL, ESTATE. */
 talker_status talker_kv_rewind(talker_t *t, int stream, int new_len);
+
+/* Reorder the streams of a beam search: for the n_seq groups of `width`
+ * consecutive streams (streams 0 .. n_seq * width - 1), stream i afterwards holds
+ * what stream parents[i] of the same group held (parents: device int32
+ * [n_seq * width], as talker_beam_select writes them). Any storage type. Full
+ * pages are shared and only the page that is being filled is copied, by one
+ * kernel; a stream that is later rewound, prefilled or imported into gets pages
+ * of its own again. The streams of a group must have the same length (EINVAL
+ * otherwise), which they keep. A parent outside its group sets the device status
+ * word (ST bad argument) and counts as the stream itself. Errors: EINVAL (null
+ * parents, sizes, n_streams > 1024), ESTATE, ECUDA. */
+talker_status talker_kv_reorder(talker_t *t, const int32_t *parents, int n_seq, int width);
 
 /* Current length of a stream (host int). Errors: EINVAL, ESTATE. */
 talker_status talker_cur_len(const talker_t *t, int stream, int *out_len);
@@ -216,7 +230,7 @@ talker_status talker_prefill_all_rows(talker_t *t, int stream, const float *emb,
 /* Test support, modelled on the state import/export of
  * "audio.cpp/src/models/vibevoice/decoder.cpp" (TransformerKVState):
  * copy `len` rows of a stream's cache in or out. k and v are device buffers
- * [n_layers][n_kv_heads][len][head_dim] in kv_dtype (f32 for Q8_0 storage: import
+ * [n_layers][n_kv_heads][len][head_dim] in kv_dtype (f32 for Q8_0 and Q4_0 storage: import
  * quantizes, export writes the dequantized values). Import sets the stream's
  * length to len. Errors: EINVAL, EOVERFLOW (len > max_seq_len), ESTATE, ECUDA. */
 talker_status talker_kv_import(talker_t *t, int stream, const void *k, const void *v, int len);

@@ -315,9 +315,9 @@ cudaError_t prepare_attn_prefill() {
     return e ? e : raise_ap<64, 2>();
 }
 
-// bf16 cache, or Q8_0 storage (whose prefill reads the call's rows from the dense bf16 copy)
+// bf16 cache, or Q8_0 / Q4_0 storage (whose prefill reads the call's rows from the dense bf16 copy)
 bool attn_prefill_supported(int kv_kind, int head_dim) {
-    return (kv_kind == 1 || kv_kind == 2) && (head_dim == 64 || head_dim == 128);
+    return kv_kind >= 1 && kv_kind <= 3 && (head_dim == 64 || head_dim == 128);
 }
 
 cudaError_t launch_attn_prefill(int head_dim, const AttnParams &a, int T, cudaStream_t st) {
@@ -325,7 +325,7 @@ cudaError_t launch_attn_prefill(int head_dim, const AttnParams &a, int T, cudaSt
     if (a.rowmap.rows_per_stream > 0 && T % a.rowmap.rows_per_stream) return cudaErrorInvalidValue;
     if ((a.dense_k != nullptr) != (a.dense_v != nullptr) || (a.dense_k != nullptr && a.rowmap.pos0 != 0))
         return cudaErrorInvalidValue;
-    if (a.cache.kv_q8 && a.dense_k == nullptr) return cudaErrorInvalidValue;
+    if ((a.cache.kv_q8 || a.cache.kv_q4) && a.dense_k == nullptr) return cudaErrorInvalidValue;
     const bool pair = a.group % 2 == 0;   // two q heads of a KV group share each staged page
     if (head_dim == 128) return pair ? launch_ap<128, 2>(a, T, st) : launch_ap<128, 1>(a, T, st);
     if (head_dim == 64) return pair ? launch_ap<64, 2>(a, T, st) : launch_ap<64, 1>(a, T, st);

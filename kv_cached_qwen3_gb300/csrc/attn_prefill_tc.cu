@@ -32,6 +32,7 @@
 
 #include "common.cuh"
 #include "kernels.cuh"
+#include "kv4.cuh"
 #include "tcgen05.cuh"
 
 using namespace talker_dev;
@@ -359,6 +360,22 @@ __device__ __forceinline__ uint4 q8_chunk_bf16(const unsigned char *tile, int ro
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// The same of a Q4_0 tile: chunk ch is lane (b, c) = (ch / 4, ch % 4)'s word of a K row, two halves of a V row.
+__device__ __forceinline__ uint4 q4_chunk_bf16(const unsigned char *tile, int row, int ch, bool is_v) {
+    using Tile = Kv4Tile<HD>;
+    const int b = ch >> 2, c = ch & 3;
+    const unsigned char *r = tile + row * Tile::kRow;
+    uint32_t w;
+    if (is_v)
+        w = (uint32_t)*reinterpret_cast<const uint16_t *>(r + 2 * c * 2 * Tile::NB + 2 * b) |
+            (uint32_t)*reinterpret_cast<const uint16_t *>(r + (2 * c + 1) * 2 * Tile::NB + 2 * b) << 16;
+    else
+        w = *reinterpret_cast<const uint32_t *>(r + c * 4 * Tile::NB + 4 * b);
+    float x[8];
+    q4_values8(w, __half2float(*reinterpret_cast<const __half *>(tile + Tile::kScales + (row * Tile::NB + b) * 2)), x);
+    return make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+}
+
 // Dense K rows and transposed V rows of one (64-key block, KV head); keys at or past
 // nkeys are written as zeros. Sources: the paged bf16 cache of `stream`; with Q8_0 storage,
 // the dense bf16 copy of the call's rows [rows][n_kv][HD] for keys >= pos0 and the cache's
@@ -382,6 +399,11 @@ __global__ void __launch_bounds__(256) k_kv_dense_tc(const CacheView c, int laye
                                    (size_t)(layer * c.n_kv + kvh) * tile;
                 kx = q8_chunk_bf16(static_cast<const unsigned char *>(c.k) + off, key % kPage, ch);
                 vx = q8_chunk_bf16(static_cast<const unsigned char *>(c.v) + off, key % kPage, ch);
+            } else if (c.kv_q4) {
+                const size_t off = (size_t)c.page_table[stream * c.pages_per_stream + key / kPage] * c.page_elems +
+                                   (size_t)(layer * c.n_kv + kvh) * Kv4Tile<HD>::kBytes;
+                kx = q4_chunk_bf16(static_cast<const unsigned char *>(c.k) + off, key % kPage, ch, false);
+                vx = q4_chunk_bf16(static_cast<const unsigned char *>(c.v) + off, key % kPage, ch, true);
             } else {
                 const size_t off = (size_t)c.page_table[stream * c.pages_per_stream + key / kPage] * c.page_elems +
                                    ((size_t)(layer * c.n_kv + kvh) * kPage + key % kPage) * HD;
@@ -411,10 +433,10 @@ int attn_prefill_tc_lpad(int nkeys) { return (nkeys + atc::BN - 1) / atc::BN * a
 
 bool attn_prefill_tc_supported(const AttnParams &a, int T) {
     const bool one_stream = a.rowmap.rows_per_stream == 0 || a.rowmap.rows_per_stream == T;
-    // bf16 cache: the dense copy reads every key from the pages; Q8_0: the call's own rows from
+    // bf16 cache: the dense copy reads every key from the pages; Q8_0 and Q4_0: the call's own rows from
     // their dense bf16 copy, earlier rows dequantized from the cache (any start position)
     return a.rowmap.mode == 1 && one_stream && a.out_bf16 && a.cache.head_dim == atc::HD && T >= 1 &&
-           (a.cache.kv_bf16 || (a.cache.kv_q8 && a.dense_k != nullptr));
+           (a.cache.kv_bf16 || ((a.cache.kv_q8 || a.cache.kv_q4) && a.dense_k != nullptr));
 }
 
 cudaError_t prepare_attn_prefill_tc() {

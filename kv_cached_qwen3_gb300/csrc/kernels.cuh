@@ -60,6 +60,7 @@ struct CacheView {
     int head_dim;
     int kv_bf16;        // 1: bf16 cache, 0: f32 (Q8_0 storage: kv_q8 = 1, kv_bf16 = 0)
     int kv_q8;          // 1: Q8_0 tiles ([64][hd] int8 codes + [64][hd/32] fp16 scales); page_elems in bytes
+    int kv_q4;          // 1: Q4_0 tiles (kv4.cuh); page_elems in bytes
     size_t page_elems;
 };
 
@@ -256,11 +257,13 @@ cudaError_t launch_gemm_tc_swiglu(const void *A, int M, int K, const void *B, in
 cudaError_t launch_rmsnorm_bf16(float *x, int ld, const float *w, float eps, int rows, int H, void *out,
                                 cudaStream_t st, const CodeGather *gather = nullptr, int *status = nullptr,
                                 float *zero = nullptr, size_t zero_n = 0);
-// dense_kv (Q8_0 storage only, else null): the rows' k / v also go to bf16 [2][rows][n_kv][hd]
+// dense_kv (Q8_0 and Q4_0 storage only, else null): the rows' k / v also go to bf16 [2][rows][n_kv][hd].
+// Q4_0 storage: they go to f32 [2][rows][n_kv][hd] at rows_f32 (dense_kv may then be null), from where
+// they are quantized by another launch.
 cudaError_t launch_qkv_post(const float *raw, int rows, int n_q, int n_kv, int hd, const float *q_norm,
                             const float *k_norm, const float2 *rope, float eps, float *q_out, const CacheView &cache,
                             int layer, const RowMap &rm, int *status, cudaStream_t st,
-                            __nv_bfloat16 *dense_kv = nullptr);
+                            __nv_bfloat16 *dense_kv = nullptr, float *rows_f32 = nullptr);
 // silu(gate) * up of a split-K [gate; up] sum; gu is zeroed behind the read (its split-K
 // accumulation always starts from zeros).
 cudaError_t launch_swiglu_bf16(float *gu, int rows, int I, void *out, cudaStream_t st);

@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kRowThreads) k_kv4_rows(const Kv4Rows r, const
     float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (!READ && on) load8<T>(dense, vec, x);
     RowPlace p{nullptr, 0};
-    if (on) p = place_of(r, Tile::kBytes, s, l, h, is_v, (r.start != nullptr ? (long long)r.start[s] : 0) + i, sub == 0);
+    if (on) p = place_of(r, Tile::kBytes, s, l, h, is_v, (r.start != nullptr ? (long long)r.start[s] : 0) + r.start0 + i, sub == 0);
     move8<HD, READ>(p.tile, p.prow, is_v, b, c, x);
     if (READ && p.tile != nullptr) store8(dense, vec, x);
 }
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kRowThreads) k_kv4_pages(const Kv4Rows r, cons
     const bool is_v = blockIdx.z & 1;
     const int h = blockIdx.x % r.c.n_kv_heads, slot = blockIdx.x / r.c.n_kv_heads;
     const int sub = threadIdx.x % TPR, b = sub >> 2, c = sub & 3;
-    const long long start = r.start != nullptr ? (long long)r.start[s] : 0;
+    const long long start = (r.start != nullptr ? (long long)r.start[s] : 0) + r.start0;
     const int n = r.count != nullptr ? min(r.count[s], r.T) : r.T;
     const long long first = (start >= 0 ? start / kPage : -((kPage - 1 - start) / kPage)) * kPage + (long long)slot * kPage;
     const int lo = (int)max(0ll, start - first), hi = (int)min((long long)kPage, start + n - first);   // rows of this page
@@ -192,51 +192,59 @@ cudaError_t launch_rows_t(const Kv4Rows &r, bool vec, cudaStream_t s) {
 // ---- reorder
 
 struct ReorderScratch {   // one warp's sets of streams
-    uint32_t used[32], seen[32], need[32];
+    uint32_t used[32], need[32];
 };
 
 __device__ __forceinline__ int parent_of(const KvReorder &r, int i) {
     const int p = i < r.R ? r.parents[i] : i;
-    return p >= 0 && p < r.n_streams ? p : i;
+    return p >= 0 && p < r.n_streams && (r.group == 0 || p / r.group == i / r.group) ? p : i;
 }
 __device__ __forceinline__ int length_of(const KvReorder &r, int p) { return min(max(r.lens[p], 0), r.pps * kPage); }
 
 // One warp finds column j of the new table. Row i keeps its parent's page where that is full
-// (shared) or, at the parent's tail page, where i is the parent's first child; every other row needs
-// a page of its own, and takes the pages of the column's set {r * pps + j} that no kept entry uses,
-// in order. A row refers to one page of a column, so there are always enough. Writes the column when
-// `store`; returns row `ask`'s entry.
+// (shared), and takes it over at the parent's tail page, unless a row before it did (another child) or a
+// stream shares the page (as one may after this one was cut shorter); every other row needs a page of
+// its own, and gets the pages of the column's set {r * pps + j} that no kept entry uses, in order. A row
+// refers to one page of a column, so there are always enough. Writes the column when `store`; returns
+// row `ask`'s entry.
 __device__ int reorder_column(const KvReorder &r, int j, int ask, bool store, bool report, ReorderScratch &w) {
     const int lane = threadIdx.x & 31;
-    w.used[lane] = w.seen[lane] = w.need[lane] = 0;
+    w.used[lane] = w.need[lane] = 0;
     __syncwarp();
+    // the page of the column that row i's parent holds (its r), and whether it is full (1) or the tail (0)
+    auto entry_of = [&](int i, int &p, int &full) {
+        p = parent_of(r, i);
+        const int tail = length_of(r, p) / kPage, entry = r.table[(size_t)p * r.pps + j], er = entry / r.pps;
+        const bool ok = entry >= 0 && entry - er * r.pps == j && er < r.n_streams;
+        if (report && !ok && j <= tail && r.status != nullptr) atomicOr(r.status, ST_BAD_ARG);
+        full = j < tail;
+        return ok && j <= tail ? er : -1;
+    };
     int answer = -1;
+    for (int i = lane; i < r.n_streams; i += 32) {
+        int p, full;
+        const int er = entry_of(i, p, full);
+        if (er < 0 || !full) continue;
+        atomicOr(&w.used[er >> 5], 1u << (er & 31));
+        if (store) r.table_out[(size_t)i * r.pps + j] = er * r.pps + j;
+        if (i == ask) answer = er * r.pps + j;
+    }
+    __syncwarp();
     for (int base = 0; base < r.n_streams; base += 32) {
         const int i = base + lane;
         const bool in = i < r.n_streams;
-        int p = -1 - lane, keep = -1;
-        bool own = false;
-        if (in) {
-            p = parent_of(r, i);
-            const int tail = length_of(r, p) / kPage;
-            const int entry = r.table[(size_t)p * r.pps + j];
-            const int er = entry / r.pps;
-            const bool ok = entry >= 0 && entry - er * r.pps == j && er < r.n_streams;
-            if (report && !ok && j <= tail && r.status != nullptr) atomicOr(r.status, ST_BAD_ARG);
-            own = ok && j == tail;
-            if (ok && j <= tail) keep = er;
-        }
-        // the first child of a parent takes its tail page over
-        const uint32_t same = __match_any_sync(0xffffffffu, p);
-        if (own && ((same & ((1u << lane) - 1)) != 0 || (w.seen[p >> 5] >> (p & 31) & 1u))) keep = -1;
+        int p = 0, full = 0;
+        const int er = in ? entry_of(i, p, full) : -1;
+        const bool tail = er >= 0 && !full;
+        const uint32_t same = __match_any_sync(0xffffffffu, tail ? er : -1 - lane);
+        const bool takes = tail && (same & ((1u << lane) - 1)) == 0 && !(w.used[er >> 5] >> (er & 31) & 1u);
         __syncwarp();
-        if (in) atomicOr(&w.seen[p >> 5], 1u << (p & 31));
-        if (keep >= 0) {
-            atomicOr(&w.used[keep >> 5], 1u << (keep & 31));
-            if (store) r.table_out[(size_t)i * r.pps + j] = keep * r.pps + j;
-            if (i == ask) answer = keep * r.pps + j;
+        if (takes) {
+            atomicOr(&w.used[er >> 5], 1u << (er & 31));
+            if (store) r.table_out[(size_t)i * r.pps + j] = er * r.pps + j;
+            if (i == ask) answer = er * r.pps + j;
         }
-        const uint32_t wants = __ballot_sync(0xffffffffu, in && keep < 0);
+        const uint32_t wants = __ballot_sync(0xffffffffu, in && !takes && !(er >= 0 && full));
         if (lane == 0) w.need[base >> 5] = wants;
         __syncwarp();
     }
@@ -299,9 +307,12 @@ __global__ void __launch_bounds__(256) k_reorder(const KvReorder r, int table_bl
     if (rows == 0) return;
     const int src = r.table[(size_t)p * r.pps + col], sr = src / r.pps;
     if (src < 0 || src - sr * r.pps != col || sr >= r.n_streams) return;
-    int first = 0;   // whether another child of p comes before i
-    for (int k = threadIdx.x; k < i; k += 256) first |= parent_of(r, k) == p;
-    if (!__syncthreads_or(first)) return;
+    int other = 0;   // whether a row before i takes the page over, or a stream shares it
+    for (int k = threadIdx.x; k < r.n_streams; k += 256) {
+        const int pk = parent_of(r, k), tail = length_of(r, pk) / kPage;
+        other |= (tail > col || (tail == col && k < i)) && r.table[(size_t)pk * r.pps + col] == src;
+    }
+    if (!__syncthreads_or(other)) return;
     if (warp == 0) {
         const int dst = reorder_column(r, col, i, false, false, scratch[0]);
         if (lane == 0) to_s = dst;
@@ -378,7 +389,7 @@ talker_status rows_call(const talker_kv4 *c, int layer0, int n_layers, int strea
     if (dtype != TALKER_DTYPE_F32 && dtype != TALKER_DTYPE_BF16) return TALKER_EINVAL;
     if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) % (dtype == TALKER_DTYPE_F32 ? 4 : 2))
         return TALKER_EINVAL;
-    const Kv4Rows r{*c, layer0, n_layers, stream0, n_streams, start, count, T, k, v, *st};
+    const Kv4Rows r{*c, layer0, n_layers, stream0, n_streams, start, count, T, k, v, *st, 0};
     return status_of(launch_kv4_rows(r, dtype, read, static_cast<cudaStream_t>(cuda_stream)));
 }
 
@@ -428,7 +439,7 @@ talker_status talker_kv4_reorder(const talker_kv4 *c, const int32_t *parents, in
     const int tile = kv4_tile_bytes(c->head_dim), tiles = c->n_layers * c->n_kv_heads;
     const KvReorder r{static_cast<unsigned char *>(c->k), static_cast<unsigned char *>(c->v), (size_t)tiles * tile,
                       tiles, c->head_dim / 2, c->head_dim / 16, tile, c->page_table, lens, parents, table_out, lens_out,
-                      c->status, c->n_streams, c->pages_per_stream, R};
+                      c->status, c->n_streams, c->pages_per_stream, R, 0};
     return status_of(launch_kv_reorder(r, static_cast<cudaStream_t>(cuda_stream)));
 }
 

@@ -94,6 +94,7 @@ struct Kv4Rows {
     int T;
     void *k, *v;
     talker_kv4_strides st;
+    int start0;   // added to start
 };
 bool kv4_cache_ok(const talker_kv4 *c);   // the host-side checks of a caller-owned cache
 cudaError_t launch_kv4_rows(const Kv4Rows &r, int dtype, bool read, cudaStream_t s);
@@ -115,6 +116,7 @@ struct Kv4AttendShape {
     int grid, one_unit;
 };
 Kv4AttendShape kv4_attend_shape(int B, int n_kv, int max_len, int n_sm);
+int kv4_attend_full_grid(int n_sm);   // the largest such grid
 size_t kv4_attend_scratch(const Kv4AttendShape &p, int head_dim);
 cudaError_t prepare_kv4_attend();   // shared-memory limits, on the current device
 int kv4_multiprocessors();          // of the current device, prepared as above (0: an error)
@@ -129,6 +131,7 @@ struct KvReorder {
     const int32_t *table, *lens, *parents;
     int32_t *table_out, *lens_out, *status;
     int n_streams, pps, R;
+    int group;    // > 0: a parent lies in its stream's group of this many consecutive streams
 };
 constexpr int kReorderMaxStreams = 1024;
 cudaError_t launch_kv_reorder(const KvReorder &r, cudaStream_t s);

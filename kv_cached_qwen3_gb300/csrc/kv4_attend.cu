@@ -760,9 +760,11 @@ Kv4AttendShape kv4_attend_shape(int B, int n_kv, int max_len, int n_sm) {
     Kv4AttendShape p;
     p.one_unit = pages <= kWholePages;
     const long long units = p.one_unit ? rows : rows * ((pages + kWarps - 1) / kWarps);
-    p.grid = (int)std::max<long long>(1, std::min<long long>(units, std::min(kCtas * n_sm, kMaxGrid)));
+    p.grid = (int)std::max<long long>(1, std::min<long long>(units, kv4_attend_full_grid(n_sm)));
     return p;
 }
+
+int kv4_attend_full_grid(int n_sm) { return std::min(kCtas * n_sm, kMaxGrid); }
 
 size_t kv4_attend_scratch(const Kv4AttendShape &p, int head_dim) {
     return p.one_unit ? 0 : (size_t)p.grid * 2 * kMaxG * (head_dim + 4) * sizeof(float);

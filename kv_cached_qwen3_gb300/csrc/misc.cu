@@ -1,6 +1,7 @@
 // Small bookkeeping kernels: per-stream length writes and dense <-> paged KV copies.
 #include "common.cuh"
 #include "kernels.cuh"
+#include "kv4.cuh"
 
 using namespace talker_dev;
 
@@ -87,6 +88,8 @@ cudaError_t prepare_kernels() {
     e = prepare_attn_prefill_tc();
     if (e != cudaSuccess) return e;
     e = prepare_attn_prefill();
+    if (e != cudaSuccess) return e;
+    e = prepare_kv4_attend();
     if (e != cudaSuccess) return e;
     return prepare_attn();
 }

@@ -139,7 +139,7 @@ __global__ void k_rmsnorm_bf16_rows(float *x, int ld, const float *w, float eps,
 // (prefill: stream0 at pos0 + r; decode: stream r at cur_len[r]).
 __global__ void k_qkv_post(const float *raw, int rows, int n_q, int n_kv, int hd, const float *q_norm,
                            const float *k_norm, const float2 *rope, float eps, float *q_out, CacheView cache, int layer,
-                           RowMap rm, int *status, __nv_bfloat16 *dense_kv) {
+                           RowMap rm, int *status, __nv_bfloat16 *dense_kv, float *rows_f32) {
     const int n_heads = n_q + 2 * n_kv;
     const int item = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
     pdl_launch_dependents();
@@ -191,6 +191,20 @@ __global__ void k_qkv_post(const float *raw, int rows, int n_q, int n_kv, int hd
         return;
     }
     const int kvh = is_k ? h - n_q : h - n_q - n_kv;
+    const size_t dense = ((size_t)(is_k ? 0 : rows) * n_kv + (size_t)r * n_kv + kvh) * hd;
+    if (cache.kv_q4) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int i = lane + 32 * j;
+            if (i >= half) continue;
+            rows_f32[dense + i] = a[j];
+            rows_f32[dense + i + half] = b[j];
+            if (dense_kv == nullptr) continue;
+            dense_kv[dense + i] = __float2bfloat16_rn(a[j]);
+            dense_kv[dense + i + half] = __float2bfloat16_rn(b[j]);
+        }
+        return;
+    }
     const int page = cache.page_table[(size_t)stream * cache.pages_per_stream + pos / kPage];
     if (cache.kv_q8) {
         // Q8_0 tile of (page, layer, head): [64][hd] codes, then [64][hd/32] fp16 scales; each valid
@@ -208,7 +222,7 @@ __global__ void k_qkv_post(const float *raw, int rows, int n_q, int n_kv, int hd
                 q8_store_block(t, row * hd + d0, kPage * hd + (row * (hd / 32) + d0 / 32) * 2, u ? b[j] : a[j], lane);
             }
         // the call itself attends its rows unquantized
-        __nv_bfloat16 *dk = dense_kv + ((size_t)(is_k ? 0 : rows) * n_kv + (size_t)r * n_kv + kvh) * hd;
+        __nv_bfloat16 *dk = dense_kv + dense;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int i = lane + 32 * j;
@@ -329,15 +343,17 @@ cudaError_t launch_rmsnorm_bf16(float *x, int ld, const float *w, float eps, int
 
 cudaError_t launch_qkv_post(const float *raw, int rows, int n_q, int n_kv, int hd, const float *q_norm,
                             const float *k_norm, const float2 *rope, float eps, float *q_out, const CacheView &cache,
-                            int layer, const RowMap &rm, int *status, cudaStream_t st, __nv_bfloat16 *dense_kv) {
-    if (cache.kv_q8 && dense_kv == nullptr) return cudaErrorInvalidValue;
+                            int layer, const RowMap &rm, int *status, cudaStream_t st, __nv_bfloat16 *dense_kv,
+                            float *rows_f32) {
+    if ((cache.kv_q8 && dense_kv == nullptr) || (cache.kv_q4 && rows_f32 == nullptr)) return cudaErrorInvalidValue;
     const long long items = (long long)rows * (n_q + 2 * n_kv);
     const int per_block = 8;
-    if (!cache.kv_q8 && hd == 128)
+    if (!cache.kv_q8 && !cache.kv_q4 && hd == 128)
         return launch_pdl(k_qkv_post_v, dim3((unsigned)((items + per_block - 1) / per_block)), dim3(per_block * 32), st,
                           raw, rows, n_q, n_kv, q_norm, k_norm, rope, eps, q_out, cache, layer, rm, status);
     return launch_pdl(k_qkv_post, dim3((unsigned)((items + per_block - 1) / per_block)), dim3(per_block * 32), st,
-                      raw, rows, n_q, n_kv, hd, q_norm, k_norm, rope, eps, q_out, cache, layer, rm, status, dense_kv);
+                      raw, rows, n_q, n_kv, hd, q_norm, k_norm, rope, eps, q_out, cache, layer, rm, status, dense_kv,
+                      rows_f32);
 }
 
 cudaError_t launch_swiglu_bf16(float *gu, int rows, int I, void *out, cudaStream_t st) {

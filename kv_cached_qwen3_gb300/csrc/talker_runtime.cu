@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "kernels.cuh"
+#include "kv4.cuh"
 #include "talker.h"
 
 using namespace talker_k;
@@ -76,7 +77,8 @@ struct talker {
     cudaStream_t cap_st = nullptr;  // private stream for graph capture (the caller's may be the legacy stream)
     int dev = 0, n_sm = 0;
     int H = 0, nq = 0, nkv = 0, hd = 0, qd = 0, kvd = 0, qkv_n = 0, I = 0, V = 0, G = 0;
-    int w_bf16 = 0, kv_bf16 = 0, kv_q8 = 0, kv_kind = 0;   // kv_kind: 0 f32, 1 bf16, 2 Q8_0
+    int w_bf16 = 0, kv_bf16 = 0, kv_q8 = 0, kv_q4 = 0, kv_kind = 0;   // kv_kind: 0 f32, 1 bf16, 2 Q8_0, 3 Q4_0
+    bool kv_quant = false;                                            // Q8_0 or Q4_0
     size_t wsz = 0, kvsz = 0;
     char *wstore = nullptr;
     std::vector<LayerDev> L;
@@ -89,6 +91,10 @@ struct talker {
     bool kv_maps_ok = false;
     void *kpool = nullptr, *vpool = nullptr;
     int *d_pt = nullptr, *d_len = nullptr;
+    int *d_reorder = nullptr;            // the page table and lengths that a reordering writes
+    bool pages_shared = false;           // streams may share full pages (talker_kv_reorder)
+    float *q4_ws = nullptr;              // Q4_0 storage: parts of rows that several CTAs attend
+    float *kv_rows = nullptr;            // Q4_0 storage: a call's own k / v rows, f32 [2][rows][n_kv][hd]
     float2 *d_rope = nullptr;
     std::vector<int> len;
     // activations, sized for cap_rows rows
@@ -152,7 +158,7 @@ void free_ptr(void *p) {
 
 void free_workspaces(talker *t) {
     float **fl[] = {&t->x, &t->raw, &t->q, &t->attn, &t->act, &t->attn_ws, &t->head_val, &t->frame_logits,
-                    &t->x2};
+                    &t->x2, &t->kv_rows};
     for (auto pp : fl) {
         free_ptr(*pp);
         *pp = nullptr;
@@ -185,8 +191,12 @@ void free_cache(talker *t) {
     free_ptr(t->d_pt);
     free_ptr(t->d_len);
     free_ptr(t->d_rope);
+    free_ptr(t->d_reorder);
+    free_ptr(t->q4_ws);
     t->kpool = t->vpool = nullptr;
-    t->d_pt = t->d_len = nullptr;
+    t->d_pt = t->d_len = t->d_reorder = nullptr;
+    t->q4_ws = nullptr;
+    t->pages_shared = false;
     t->d_rope = nullptr;
     t->kv_maps_ok = false;
     t->n_streams = t->max_seq = t->pps = 0;
@@ -219,6 +229,13 @@ int decode_splits(const talker *t, int B) {
 constexpr int kAttnMmMinPages = 3;
 
 void attn_config(const talker *t, int B, int max_len, int *splits, int *cluster, int *mm) {
+    if (t->kv_q4) {   // its own attention: a CTA per (row, KV group), or balanced ranges of pages over the GPU
+        const Kv4AttendShape shape = kv4_attend_shape(B, t->nkv, max_len, t->n_sm);
+        *splits = shape.one_unit ? shape.grid : kv4_attend_full_grid(t->n_sm);
+        *cluster = shape.one_unit;
+        *mm = 0;
+        return;
+    }
     const int pages_max = (max_len + 1 + kPageRows - 1) / kPageRows;
     if (B <= 2 && pages_max <= 3) {
         *splits = 1;
@@ -251,6 +268,11 @@ talker_status ensure_capacity(talker *t, int rows, int splits) {
         const int cap = std::max(rows, 16);
         float **fl[] = {&t->x, &t->raw, &t->q, &t->attn, &t->act, &t->x2};
         const int widths[] = {t->H, t->qkv_n, t->qd, t->qd, t->I, t->H};
+        if (t->kv_q4) {
+            free_ptr(t->kv_rows);
+            t->kv_rows = nullptr;
+            TRY_CUDA(cudaMalloc(&t->kv_rows, (size_t)2 * cap * t->kvd * sizeof(float)));
+        }
         for (int i = 0; i < 6; ++i) {
             free_ptr(*fl[i]);
             *fl[i] = nullptr;
@@ -296,10 +318,11 @@ talker_status validate_config(const talker_config *c) {
     if (c->vocab < 8 || c->vocab % 8) return TALKER_EINVAL;
     if (!(c->rms_eps >= 0.f) || !(c->rope_theta > 0.f)) return TALKER_EINVAL;
     if ((c->weight_dtype != TALKER_DTYPE_F32 && c->weight_dtype != TALKER_DTYPE_BF16) ||
-        (c->kv_dtype != TALKER_DTYPE_F32 && c->kv_dtype != TALKER_DTYPE_BF16 && c->kv_dtype != TALKER_DTYPE_Q8_0))
+        (c->kv_dtype != TALKER_DTYPE_F32 && c->kv_dtype != TALKER_DTYPE_BF16 && c->kv_dtype != TALKER_DTYPE_Q8_0 &&
+         c->kv_dtype != TALKER_DTYPE_Q4_0))
         return TALKER_EINVAL;
-    // Q8_0 storage: bf16 weights (its prefill runs on the tensor-core path), blocks of 32 in a head
-    if (c->kv_dtype == TALKER_DTYPE_Q8_0 && (c->weight_dtype != TALKER_DTYPE_BF16 || c->head_dim < 64))
+    // Q8_0 and Q4_0 storage: bf16 weights (its prefill runs on the tensor-core path), blocks of 32 in a head
+    if ((c->kv_dtype == TALKER_DTYPE_Q8_0 || c->kv_dtype == TALKER_DTYPE_Q4_0) && (c->weight_dtype != TALKER_DTYPE_BF16 || c->head_dim < 64))
         return TALKER_EINVAL;
     // the widest GEMV input must fit one staged row in shared memory
     const int kmax = std::max(std::max(c->hidden, c->n_q_heads * c->head_dim), c->intermediate);
@@ -387,6 +410,7 @@ CacheView cache_view(const talker *t) {
     c.head_dim = t->hd;
     c.kv_bf16 = t->kv_bf16;
     c.kv_q8 = t->kv_q8;
+    c.kv_q4 = t->kv_q4;
     c.page_elems = t->page_elems;
     return c;
 }
@@ -416,6 +440,37 @@ void set_raw_heads(const talker *t, const LayerDev &d, AttnParams &a) {
     a.k_norm = d.k_norm;
     a.rope = t->d_rope;
     a.eps = t->c.rms_eps;
+}
+
+// The cache as the 4-bit entry points see it (Q4_0 storage).
+talker_kv4 kv4_view(const talker *t) {
+    return {t->kpool, t->vpool, t->d_pt, t->d_status, t->n_streams * t->pps, t->n_streams, t->pps, t->c.n_layers, t->nkv, t->hd};
+}
+
+// Q4_0 storage: the call's rows (kv_rows, of n_streams streams of T rows) quantized into the cache at
+// start[s] + start0.
+talker_status enqueue_q4_write(talker *t, cudaStream_t st, int layer, int stream0, int n_streams, int T, const int *start,
+                               int start0, int *nk) {
+    const size_t rows = (size_t)n_streams * T;
+    const talker_kv4_strides strides{0, (int64_t)T * t->kvd, t->kvd, t->hd};
+    const Kv4Rows r{kv4_view(t), layer, 1, stream0, n_streams, start, nullptr, T, t->kv_rows, t->kv_rows + rows * t->kvd,
+                    strides, start0};
+    TRY_CUDA(launch_kv4_rows(r, TALKER_DTYPE_F32, false, st));
+    ++*nk;
+    return TALKER_OK;
+}
+
+// Q4_0 storage, decode: the heads finished from the raw projections, attention over the cached rows and
+// the step's own (exact, from kv_rows), which is then quantized into the cache.
+talker_status enqueue_q4_decode(talker *t, cudaStream_t st, int B, int layer, const LayerDev &d, const RowMap &rm, int grid,
+                                void *out, bool out_bf16, int *nk) {
+    TRY_CUDA(launch_qkv_post(t->raw, B, t->nq, t->nkv, t->hd, d.q_norm, d.k_norm, t->d_rope, t->c.rms_eps, t->q, cache_view(t),
+                             layer, rm, t->d_status, st, nullptr, t->kv_rows));
+    const Kv4Attend a{kv4_view(t), layer, B, t->nq, t->d_len, t->q, t->kv_rows, t->kv_rows + (size_t)B * t->kvd, t->qd, t->kvd,
+                      out, 1.0f / sqrtf((float)t->hd), grid, t->attn_cluster, t->q4_ws};
+    TRY_CUDA(launch_kv4_attend(a, 0, out_bf16, st));
+    *nk += t->attn_cluster ? 2 : 3;
+    return enqueue_q4_write(t, st, layer, 0, B, 1, t->d_len, 0, nk);
 }
 
 // Enqueue the whole forward for `rows` rows on the GEMV kernels: per layer QKV (+QK-norm,
@@ -483,8 +538,12 @@ talker_status enqueue_forward(talker *t, cudaStream_t st, int rows, const RowMap
         a.cnt = t->attn_cnt;
         a.status = t->d_status;
         if (rm.mode == 0) set_raw_heads(t, d, a);
-        TRY_CUDA(launch_attn(t->kv_kind, t->hd, a, rows, st, pdl));
-        ++nk;
+        if (t->kv_q4) {
+            TRY(enqueue_q4_decode(t, st, rows, l, d, rm, splits, t->attn, false, &nk));
+        } else {
+            TRY_CUDA(launch_attn(t->kv_kind, t->hd, a, rows, st, pdl));
+            ++nk;
+        }
         // 3) o_proj + residual
         GemvParams o{};
         o.rows = rows;
@@ -604,7 +663,7 @@ talker_status ensure_tc(talker *t, int rows) {
     TRY_CUDA(cudaMemset(t->gu, 0, (size_t)cap * 2 * t->I * sizeof(float)));
     TRY_CUDA(cudaMalloc(&t->gemm_cnt, (size_t)(2 * t->I / 128 + 1) * sizeof(int)));
     TRY_CUDA(cudaMemset(t->gemm_cnt, 0, (size_t)(2 * t->I / 128 + 1) * sizeof(int)));
-    if (t->kv_q8) TRY_CUDA(cudaMalloc(&t->kv_dense, (size_t)2 * cap * t->nkv * t->hd * 2));
+    if (t->kv_quant) TRY_CUDA(cudaMalloc(&t->kv_dense, (size_t)2 * cap * t->nkv * t->hd * 2));
     if (t->hd == 128) {   // keys of a call: up to the whole cache (an appended chunk reads every earlier key)
         const size_t lp = (size_t)attn_prefill_tc_lpad(std::max(cap, t->max_seq));
         TRY_CUDA(cudaMalloc(&t->kd_tc, lp * t->nkv * t->hd * 2));
@@ -647,8 +706,12 @@ talker_status enqueue_tc(talker *t, cudaStream_t st, int T, const RowMap &rm, co
         TRY(tc_gemm(t, st, t->hb, T, t->H, d.qkv, t->qkv_n, t->raw, t->qkv_n, false, &nk));
         if (rm.mode != 0) {   // prefill rows; decode rows are finished inside the attention kernel
             TRY_CUDA(launch_qkv_post(t->raw, T, t->nq, t->nkv, t->hd, d.q_norm, d.k_norm, t->d_rope, t->c.rms_eps,
-                                     t->q, cv, l, rm, t->d_status, st, t->kv_q8 ? t->kv_dense : nullptr));
+                                     t->q, cv, l, rm, t->d_status, st, t->kv_quant ? t->kv_dense : nullptr, t->kv_rows));
             ++nk;
+            if (t->kv_q4) {
+                const int per = rm.rows_per_stream > 0 ? rm.rows_per_stream : T;
+                TRY(enqueue_q4_write(t, st, l, rm.stream0, T / per, per, nullptr, rm.pos0, &nk));
+            }
         }
         AttnParams a{};
         a.q = t->q;
@@ -668,16 +731,16 @@ talker_status enqueue_tc(talker *t, cudaStream_t st, int T, const RowMap &rm, co
         a.cnt = t->attn_cnt;
         a.status = t->d_status;
         if (rm.mode == 0) set_raw_heads(t, d, a);
-        if (rm.mode == 1 && t->kv_q8) {   // the call's own rows from their dense copy, exact up to bf16
+        if (rm.mode == 1 && t->kv_quant) {   // the call's own rows from their dense copy, exact up to bf16
             a.dense_k = t->kv_dense;
             a.dense_v = t->kv_dense + (size_t)T * t->nkv * t->hd;
         }
         // rows of one stream: all T, or T / B in a batched prefill (B streams of rows_per_stream rows)
         const int Ts = rm.rows_per_stream > 0 ? rm.rows_per_stream : T;
         const int n_str = T / Ts;
-        // (an appended chunk over Q8_0 storage attends earlier rows dequantized: tcgen05 only)
+        // (an appended chunk over quantized storage attends earlier rows dequantized: tcgen05 only)
         const bool attn_tc = t->prefill_mode == 4 || (t->prefill_mode != 3 && Ts >= kAttnTcMinRows) ||
-                             (t->kv_q8 && rm.pos0 > 0);
+                             (t->kv_quant && rm.pos0 > 0);
         AttnParams a1 = a;   // the first stream's rows as a one-stream call
         a1.rowmap.rows_per_stream = 0;
         if (rm.mode == 1 && attn_tc && t->kd_tc != nullptr && rm.pos0 + Ts <= t->cap_kd_keys &&
@@ -699,6 +762,8 @@ talker_status enqueue_tc(talker *t, cudaStream_t st, int T, const RowMap &rm, co
         } else if (rm.mode == 1 && attn_prefill_supported(t->kv_kind, t->hd)) {
             TRY_CUDA(launch_attn_prefill(t->hd, a, T, st));   // causal tiles on mma.sync
             ++nk;
+        } else if (t->kv_q4) {
+            TRY(enqueue_q4_decode(t, st, T, l, d, rm, attn_splits, t->ab, true, &nk));
         } else {
             TRY_CUDA(launch_attn(t->kv_kind, t->hd, a, T, st, false));
             ++nk;
@@ -795,22 +860,63 @@ talker_status run_graph(talker *t, const std::vector<long long> &key, F enqueue)
     return TALKER_OK;
 }
 
+// The streams reordered by sharing pages (parents null: every stream stays as it is).
+talker_status reorder_pages(talker *t, const int32_t *parents, int R, int group) {
+    const size_t n_pages = (size_t)t->n_streams * t->pps;
+    KvReorder r{};
+    r.k = static_cast<unsigned char *>(t->kpool);
+    r.v = static_cast<unsigned char *>(t->vpool);
+    r.page_bytes = t->page_elems * t->kvsz;
+    r.n_tiles = t->c.n_layers * t->nkv;
+    r.row_bytes = t->kv_q4 ? t->hd / 2 : t->kv_q8 ? t->hd : t->hd * (int)t->kvsz;
+    r.scale_bytes = t->kv_quant ? t->hd / 16 : 0;
+    r.tile_bytes = (int)(r.page_bytes / r.n_tiles);
+    r.table = t->d_pt;
+    r.lens = t->d_len;
+    r.parents = parents;
+    r.table_out = t->d_reorder;
+    r.lens_out = t->d_reorder + n_pages;
+    r.status = t->d_status;
+    r.n_streams = t->n_streams;
+    r.pps = t->pps;
+    r.R = R;
+    r.group = group;
+    TRY_CUDA(launch_kv_reorder(r, t->st));
+    TRY_CUDA(cudaMemcpyAsync(t->d_pt, r.table_out, n_pages * sizeof(int), cudaMemcpyDeviceToDevice, t->st));
+    TRY_CUDA(cudaMemcpyAsync(t->d_len, r.lens_out, t->n_streams * sizeof(int), cudaMemcpyDeviceToDevice, t->st));
+    t->launches += 1;
+    return TALKER_OK;
+}
+
+// After lengths were cut: once streams share pages, every page that a stream may write next has to be
+// its own again.
+talker_status own_pages(talker *t) { return t->pages_shared ? reorder_pages(t, nullptr, 0, 0) : TALKER_OK; }
+
+// The same before a call that writes streams [s0, s0 + n) from position 0.
+talker_status own_pages_from_0(talker *t, int s0, int n) {
+    if (!t->pages_shared) return TALKER_OK;
+    for (int s = s0; s < s0 + n; ++s) TRY_CUDA(launch_set_len(t->d_len, s, 0, t->st));
+    t->launches += n;
+    return reorder_pages(t, nullptr, 0, 0);
+}
+
 // Prefill rows at positions pos0 .. pos0 + T - 1 of `stream` (pos0 = 0: talker_prefill;
 // pos0 = cur_len: talker_prefill_append).
 talker_status prefill_impl(talker *t, int stream, const float *emb, int T, float *hidden, float *logits,
                            int32_t *argmax, bool all_rows, bool append) {
     TRY(check_stream(t, stream));
     if (!emb || !logits || T < 1) return TALKER_EINVAL;
-    if (append && t->kv_q8 && t->hd != 128) return TALKER_EINVAL;   // Q8_0 appends: the tcgen05 attention
+    if (append && t->kv_quant && t->hd != 128) return TALKER_EINVAL;   // appends over quantized rows: the tcgen05 attention
     const int pos0 = append ? t->len[stream] : 0;
     if (T > t->max_seq - pos0) return TALKER_EOVERFLOW;
     TRY_CUDA(cudaSetDevice(t->dev));
     TRY(ensure_capacity(t, T, 1));
     RowMap rm{1, stream, pos0, t->d_len};
     ForwardOut out{logits, hidden, all_rows ? nullptr : argmax, all_rows, 0};
-    if (t->kv_q8 && !tc_usable(t)) return TALKER_EINVAL;
-    const bool tc = t->kv_q8 || (T >= kTcMinRows && t->prefill_mode != 2 && tc_usable(t));   // Q8_0: always tc
+    if (t->kv_quant && !tc_usable(t)) return TALKER_EINVAL;
+    const bool tc = t->kv_quant || (T >= kTcMinRows && t->prefill_mode != 2 && tc_usable(t));   // quantized rows: always tc
     if (tc) TRY(ensure_tc(t, T));
+    if (!append) TRY(own_pages_from_0(t, stream, 1));
     const std::vector<long long> key = {0, tc, T, stream, pos0, all_rows, t->prefill_mode,
                                         (long long)(uintptr_t)emb, (long long)(uintptr_t)hidden,
                                         (long long)(uintptr_t)logits, (long long)(uintptr_t)out.argmax};
@@ -864,9 +970,11 @@ talker_status talker_create(const talker_config *cfg, const talker_weight_ptrs *
     t->w_bf16 = cfg->weight_dtype == TALKER_DTYPE_BF16;
     t->kv_bf16 = cfg->kv_dtype == TALKER_DTYPE_BF16;
     t->kv_q8 = cfg->kv_dtype == TALKER_DTYPE_Q8_0;
-    t->kv_kind = t->kv_q8 ? 2 : (t->kv_bf16 ? 1 : 0);
+    t->kv_q4 = cfg->kv_dtype == TALKER_DTYPE_Q4_0;
+    t->kv_quant = t->kv_q8 || t->kv_q4;
+    t->kv_kind = t->kv_q4 ? 3 : t->kv_q8 ? 2 : (t->kv_bf16 ? 1 : 0);
     t->wsz = t->w_bf16 ? 2 : 4;
-    t->kvsz = t->kv_q8 ? 1 : (t->kv_bf16 ? 2 : 4);   // bytes per pool unit
+    t->kvsz = t->kv_quant ? 1 : (t->kv_bf16 ? 2 : 4);   // bytes per pool unit
     talker_status s = from_cuda(cudaGetDevice(&t->dev));
     if (s == TALKER_OK) s = from_cuda(cudaDeviceGetAttribute(&t->n_sm, cudaDevAttrMultiProcessorCount, t->dev));
     if (s == TALKER_OK) s = from_cuda(prepare_kernels());
@@ -906,8 +1014,9 @@ talker_status talker_kv_init_batched(talker_t *t, int n_streams, int max_seq_len
     drop_graphs(t);
     free_cache(t);
     const int pps = (max_seq_len + kPageRows - 1) / kPageRows;
-    // pool units per page: elements, or bytes for Q8_0 tiles ([64][hd] codes + [64][hd/32] fp16 scales)
-    const size_t tile_units = t->kv_q8 ? (size_t)kPageRows * t->hd + (size_t)kPageRows * (t->hd / 32) * 2
+    // pool units per page: elements, or bytes for Q8_0 tiles ([64][hd] codes + [64][hd/32] fp16 scales) and Q4_0 tiles
+    const size_t tile_units = t->kv_q4 ? (size_t)kv4_tile_bytes(t->hd) :
+                              t->kv_q8 ? (size_t)kPageRows * t->hd + (size_t)kPageRows * (t->hd / 32) * 2
                                        : (size_t)kPageRows * t->hd;
     const size_t page_elems = (size_t)t->c.n_layers * t->nkv * tile_units;
     const size_t n_pages = (size_t)n_streams * pps;
@@ -920,6 +1029,8 @@ talker_status talker_kv_init_batched(talker_t *t, int n_streams, int max_seq_len
     for (size_t i = 0; i < n_pages; ++i) pt[i] = (int)i;  // stream s owns pages [s*pps, (s+1)*pps)
     TRY_CUDA(cudaMalloc(&t->d_pt, n_pages * sizeof(int)));
     TRY_CUDA(cudaMemcpy(t->d_pt, pt.data(), n_pages * sizeof(int), cudaMemcpyHostToDevice));
+    TRY_CUDA(cudaMalloc(&t->d_reorder, (n_pages + n_streams) * sizeof(int)));
+    if (t->kv_q4) TRY_CUDA(cudaMalloc(&t->q4_ws, kv4_attend_scratch({kv4_attend_full_grid(t->n_sm), 0}, t->hd)));
     TRY_CUDA(cudaMalloc(&t->d_len, n_streams * sizeof(int)));
     TRY_CUDA(cudaMemsetAsync(t->d_len, 0, n_streams * sizeof(int), t->st));
     // RoPE table: angle p * theta^(-2i/hd) evaluated in double on the host, stored as f32 (cos, sin)
@@ -956,7 +1067,19 @@ talker_status talker_kv_rewind(talker_t *t, int stream, int new_len) {
     TRY_CUDA(launch_set_len(t->d_len, stream, new_len, t->st));
     t->launches += 1;
     t->len[stream] = new_len;
-    return TALKER_OK;
+    return own_pages(t);
+}
+
+talker_status talker_kv_reorder(talker_t *t, const int32_t *parents, int n_seq, int width) {
+    if (!t) return TALKER_EINVAL;
+    if (t->n_streams == 0) return TALKER_ESTATE;
+    if (!parents || n_seq < 1 || width < 1 || (long long)n_seq * width > t->n_streams || t->n_streams > kReorderMaxStreams)
+        return TALKER_EINVAL;
+    for (int i = 0; i < n_seq * width; ++i)
+        if (t->len[i] != t->len[i / width * width]) return TALKER_EINVAL;
+    TRY_CUDA(cudaSetDevice(t->dev));
+    t->pages_shared = true;
+    return reorder_pages(t, parents, n_seq * width, width);
 }
 
 talker_status talker_cur_len(const talker_t *t, int stream, int *out_len) {
@@ -992,6 +1115,7 @@ talker_status talker_prefill_batched(talker_t *t, int B, const float *emb, int T
     const int rows = B * T;
     TRY(ensure_capacity(t, rows, 1));
     TRY(ensure_tc(t, rows));
+    TRY(own_pages_from_0(t, 0, B));
     RowMap rm{1, 0, 0, t->d_len, T};
     ForwardOut out{logits_last, hidden_last, argmax_last, false, 0, T};
     const std::vector<long long> key = {1, B, T, t->prefill_mode, (long long)(uintptr_t)emb,
@@ -1023,7 +1147,7 @@ static talker_status decode_impl(talker *t, const float *emb, const CodeGather *
     for (int b = 0; b < B; ++b) max_len = std::max(max_len, t->len[b]);
     int splits = 0, cluster = 0, mm = 0;
     attn_config(t, B, max_len, &splits, &cluster, &mm);
-    TRY(ensure_capacity(t, B, splits));
+    TRY(ensure_capacity(t, B, t->kv_q4 ? 1 : splits));
     if (kind == 1) TRY(ensure_tc(t, B));
     GraphEntry *ge = nullptr;
     const int32_t *ids = gather ? gather->ids : nullptr;
@@ -1069,12 +1193,20 @@ talker_status talker_decode(talker_t *t, const float *emb, int B, float *logits,
     return decode_impl(t, emb, nullptr, B, logits, hidden, argmax);
 }
 
+static talker_status kv_copy(const talker *t, int stream, void *k, void *v, int len, bool to_cache) {
+    if (!t->kv_q4 || len == 0) return from_cuda(launch_kv_copy(cache_view(t), stream, k, v, len, to_cache, t->st));
+    const talker_kv4_strides strides{(int64_t)t->nkv * len * t->hd, 0, t->hd, (int64_t)len * t->hd};
+    const Kv4Rows r{kv4_view(t), 0, t->c.n_layers, stream, 1, nullptr, nullptr, len, k, v, strides, 0};
+    return from_cuda(launch_kv4_rows(r, TALKER_DTYPE_F32, !to_cache, t->st));
+}
+
 talker_status talker_kv_import(talker_t *t, int stream, const void *k, const void *v, int len) {
     TRY(check_stream(t, stream));
     if (!k || !v || len < 0) return TALKER_EINVAL;
     if (len > t->max_seq) return TALKER_EOVERFLOW;
     TRY_CUDA(cudaSetDevice(t->dev));
-    TRY_CUDA(launch_kv_copy(cache_view(t), stream, const_cast<void *>(k), const_cast<void *>(v), len, 1, t->st));
+    TRY(own_pages_from_0(t, stream, 1));
+    TRY(kv_copy(t, stream, const_cast<void *>(k), const_cast<void *>(v), len, true));
     TRY_CUDA(launch_set_len(t->d_len, stream, len, t->st));
     t->launches += (len > 0) + 1;
     t->len[stream] = len;
@@ -1086,7 +1218,7 @@ talker_status talker_kv_export(const talker_t *t, int stream, void *k, void *v, 
     if (!k || !v || len < 0) return TALKER_EINVAL;
     if (len > t->max_seq) return TALKER_EOVERFLOW;
     TRY_CUDA(cudaSetDevice(t->dev));
-    TRY_CUDA(launch_kv_copy(cache_view(t), stream, k, v, len, 0, t->st));
+    TRY(kv_copy(t, stream, k, v, len, false));
     const_cast<talker *>(t)->launches += (len > 0);
     return TALKER_OK;
 }
@@ -1219,8 +1351,8 @@ talker_status talker_frame(talker_t *t, const float *emb, int T0, int n_steps, c
     auto head_of = [&](int i) -> const void * { return heads ? heads[i] : t->head; };
     if (T0 > t->max_seq || n_steps > t->max_seq - T0) return TALKER_EOVERFLOW;
     TRY_CUDA(cudaSetDevice(t->dev));
-    const bool tc_pre = t->kv_q8 || (T0 >= kTcMinRows && t->prefill_mode != 2 && tc_usable(t));
-    if (t->kv_q8 && !tc_usable(t)) return TALKER_EINVAL;
+    const bool tc_pre = t->kv_quant || (T0 >= kTcMinRows && t->prefill_mode != 2 && tc_usable(t));
+    if (t->kv_quant && !tc_usable(t)) return TALKER_EINVAL;
     // every buffer the frame touches, sized before capture (growing drops captured graphs)
     const int splits_max = std::max(kAttnClusterMax, decode_splits(t, 1));
     TRY(ensure_capacity(t, T0, splits_max));
@@ -1284,6 +1416,7 @@ talker_status talker_frame(talker_t *t, const float *emb, int T0, int n_steps, c
         t->frame_key = key;
         t->frame_kernels = nk;
     }
+    TRY(own_pages_from_0(t, 0, 1));
     TRY_CUDA(cudaGraphLaunch(t->frame_exec, t->st));
     t->launches += t->frame_kernels;
     t->len[0] = T0 + n_steps;

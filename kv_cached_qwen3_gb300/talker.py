@@ -16,7 +16,7 @@ LIB_PATH = os.path.join(_HERE, "libtalker_gb300.so")
 
 STATUS = {0: "TALKER_OK", 1: "TALKER_EINVAL", 2: "TALKER_EOVERFLOW", 3: "TALKER_ENOMEM", 4: "TALKER_ECUDA",
           5: "TALKER_ESTATE", 6: "TALKER_EDEVICE"}
-DTYPE = {"f32": 0, "bf16": 1, "q8_0": 2}
+DTYPE = {"f32": 0, "bf16": 1, "q8_0": 2, "q4_0": 3}
 LAYER_FIELDS = ("input_norm", "q_proj", "k_proj", "v_proj", "q_norm", "k_norm", "o_proj", "post_norm",
                 "gate_proj", "up_proj", "down_proj")
 
@@ -66,6 +66,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "talker_destroy": (None, [vp]),
         "talker_kv_init_batched": (st, [vp, ctypes.c_int, ctypes.c_int]),
         "talker_kv_rewind": (st, [vp, ctypes.c_int, ctypes.c_int]),
+        "talker_kv_reorder": (st, [vp, vp, ctypes.c_int, ctypes.c_int]),
         "talker_cur_len": (st, [vp, ctypes.c_int, ctypes.POINTER(ctypes.c_int)]),
         "talker_prefill": (st, [vp, ctypes.c_int, vp, ctypes.c_int, vp, vp, vp]),
         "talker_prefill_append": (st, [vp, ctypes.c_int, vp, ctypes.c_int, vp, vp, vp]),
@@ -173,6 +174,14 @@ class Talker:
 
     def rewind(self, stream: int, new_len: int):
         self._check(self.lib.talker_kv_rewind(self.h, stream, new_len), "talker_kv_rewind")
+
+    def kv_reorder(self, parents, n_seq: int, width: int):
+        """Beam reordering: stream i of the n_seq groups of `width` streams holds what stream parents[i] held.
+        parents: int32 cuda [n_seq * width] (as beam_select returns them)."""
+        if parents.dtype != self.torch.int32 or not parents.is_cuda or not parents.is_contiguous() or \
+                parents.numel() != n_seq * width:
+            raise ValueError("kv_reorder: parents must be a contiguous int32 CUDA tensor of n_seq * width")
+        self._check(self.lib.talker_kv_reorder(self.h, _ptr(parents), n_seq, width), "talker_kv_reorder")
 
     def cur_len(self, stream: int) -> int:
         out = ctypes.c_int()

@@ -239,6 +239,27 @@ def q8_0_roundtrip(x):
     return q8_0_dequantize(*q8_0_quantize(x))
 
 
+# ----------------------------------------------------------------------------- Q4_0 KV storage
+
+def q4_0_quantize(x):
+    """Blocks of 32 along the last axis: m = the value of largest magnitude (the first on ties), d = fp16(-m / 8),
+    code = clamp(floor(8.5 - 8 x / m), 0, 15), 8 where m = 0. Returns (codes uint8 [..., n], d fp16 [..., n / 32]).
+    f64 decides exactly between codes of f32 inputs (the borders 16 x = (17 - 2 k) m have 24 + 5 bits)."""
+    b = np.asarray(x, F64)
+    shp = b.shape
+    b = b.reshape(shp[:-1] + (shp[-1] // 32, 32))
+    m = np.take_along_axis(b, np.argmax(np.abs(b), axis=-1)[..., None], axis=-1)
+    safe = np.where(m == 0, 1.0, m)
+    codes = np.where(m == 0, 8.0, np.clip(np.floor(8.5 - 8.0 * b / safe), 0, 15))
+    return codes.astype(np.uint8).reshape(shp), (m[..., 0] * -0.125).astype(np.float32).astype(np.float16)
+
+
+def q4_0_roundtrip(x):
+    codes, d = q4_0_quantize(x)
+    c = codes.astype(F64) - 8.0
+    return (c.reshape(c.shape[:-1] + (-1, 32)) * d.astype(F64)[..., None]).reshape(c.shape)
+
+
 class OracleCache:
     """Mode B: the incremental KV-cached forward over n_streams independent streams.
 
@@ -246,7 +267,8 @@ class OracleCache:
     counts the valid rows. Errors raise ValueError and leave the state unchanged.
     """
 
-    def __init__(self, oracle: Oracle, n_streams: int, max_seq_len: int, round_kv=None, kv_q8=False):
+    def __init__(self, oracle: Oracle, n_streams: int, max_seq_len: int, round_kv=None, kv_q8=False,
+                 kv_q4=False):
         g = oracle.g
         self.o = oracle
         self.max_seq_len = max_seq_len
@@ -259,12 +281,16 @@ class OracleCache:
         # Q8_0 storage (qwen3-tts talker, TurboQuantQ8_0): rows are stored as Q8_0; a call
         # attends the rows cached by earlier calls dequantized and its own rows exactly.
         self.kv_q8 = kv_q8
+        # Q4_0 storage, with the same reading
+        self.kv_q4 = kv_q4
 
     def _store(self, s, l, rows, k, v):
         if self.round_kv is not None:
             k, v = self.round_kv(k), self.round_kv(v)
         if self.kv_q8:
             k, v = q8_0_roundtrip(k), q8_0_roundtrip(v)
+        if self.kv_q4:
+            k, v = q4_0_roundtrip(k), q4_0_roundtrip(v)
         self.K[s][l][:, rows, :] = np.transpose(k, (1, 0, 2))
         self.V[s][l][:, rows, :] = np.transpose(v, (1, 0, 2))
 
@@ -280,6 +306,8 @@ class OracleCache:
         k, v = np.asarray(k, F64), np.asarray(v, F64)
         if self.kv_q8:
             k, v = q8_0_roundtrip(k), q8_0_roundtrip(v)
+        if self.kv_q4:
+            k, v = q4_0_roundtrip(k), q4_0_roundtrip(v)
         self.K[s][:, :, :length] = k
         self.V[s][:, :, :length] = v
         self.cur_len[s] = length
