@@ -19,16 +19,17 @@ constexpr int kCluster = 8;
 constexpr int kClusterTasks = kWarps * kCluster + kMaxWidth;
 constexpr float kMasked = -1e30f;   // at or below: counts as -inf
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLeastRef = -1.4426e30f;   // reference of a row's exponents without a logit: over kLog2e kMasked
 
-// Masked values as -inf, and -0 as 0 (equal values are ordered by their index).
-__device__ __forceinline__ float unmask(float x) { return x > kMasked ? x + 0.f : -INFINITY; }
+// Masked values (and NaN) as kMasked, the lowest value that is told apart.
+__device__ __forceinline__ float unmask(float x) { return fmaxf(x, kMasked); }
 
 // A logit and where it is in its row. rank: its value as a whole number of the same order, above 0.
 struct Entry {
     uint32_t rank, index;
 };
 __device__ __forceinline__ uint32_t rank_of(float x) {
-    const uint32_t u = __float_as_uint(x);
+    const uint32_t u = __float_as_uint(x + 0.f);   // (-0 ranks as 0: equal values are ordered by their index)
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 __device__ __forceinline__ float value_of(uint32_t rank) {
@@ -39,10 +40,10 @@ __device__ __forceinline__ float ex2(float x) {   // relative error about 2^-22,
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// log(x) for a normal x, to about 1e-10: x = 2^k f with f in [0.7, 1.5), log f = 2 atanh(z) by its
+// log2(x) for a normal x, to about 1e-10: x = 2^k f with f in [0.7, 1.5), log f = 2 atanh(z) by its
 // series in z = (f - 1) / (f + 1), |z| < 0.2. (Sums of exponentials meet here; scores next to one
 // another are told apart in 64 bits, in which the general logarithm would take most of a small call.)
-__device__ __forceinline__ double log_near(float x) {
+__device__ __forceinline__ double log2_near(float x) {
     const int bits = __float_as_int(x), k = (bits - 0x3f333333) >> 23;
     const double f = (double)__int_as_float(bits - (k << 23)), z = (f - 1.0) / (f + 1.0), q = z * z;
     double t = 1.0 / 15.0;
@@ -53,7 +54,7 @@ __device__ __forceinline__ double log_near(float x) {
     t = fma(t, q, 1.0 / 5.0);
     t = fma(t, q, 1.0 / 3.0);
     t = fma(t, q, 1.0);
-    return fma((double)k, 0.693147180559945309, 2.0 * z * t);
+    return fma(2.885390081777926814 * z, t, (double)k);   // 2 / log 2
 }
 
 struct Args {
@@ -66,16 +67,18 @@ struct Args {
     float *scores_out;
     int chunks;       // parts of a row
     Entry *best;      // scratch: [row][chunk][width], best first
-    float2 *sums;     // scratch: [row][chunk] (maximum, sum of exp(x - maximum))
+    float2 *sums;     // scratch: [row][chunk] (reference c, sum of 2^(kLog2e x - c))
 };
 
 // What a warp has seen of a row: lane i < width holds the i-th best logit (rank 0: none yet); every
-// lane has its part of the maximum and of the sum of exponentials. What ranks `least` or lower is
-// not among the best any more.
+// lane has its part of the sum of 2^(kLog2e x - c) and its reference c, kLog2e times its largest logit
+// (at least kLeastRef, below which masked values, and lanes that have none, add nothing).
+// (With one multiply-add per exponent: the same rounded factor in every term, and in the end.) What ranks
+// `least` or lower is not among the best any more.
 struct Seen {
     Entry mine;
     uint32_t least;
-    float m, sum;
+    float c, sum;
 
     __device__ __forceinline__ void insert(uint32_t rank, uint32_t index, int width) {   // the same in all lanes
         const int lane = threadIdx.x & 31;
@@ -88,26 +91,28 @@ struct Seen {
     }
 };
 
-// N values per lane; the logit x[i] has index at(i), -inf where there is none (exists(i) false).
-// Logits come in the order of their indexes, so a later equal one never replaces another.
-template <int N, typename At, typename Exists>
-__device__ __forceinline__ void take(Seen &s, const float (&x)[N], At at, Exists exists, int width) {
+// kVecs vectors of N values per lane; the logit x[i] has index at(i); `exist`: a bit for each that there
+// is (the others are kMasked). Logits come in the order of their indexes, so a later equal one never
+// replaces another.
+template <int N, int kVecs, typename At>
+__device__ __forceinline__ void take(Seen &s, const float (&x)[N * kVecs], At at, uint32_t exist, int width) {
     const int lane = threadIdx.x & 31;
-    float top = x[0];
+    float tops[kVecs], top = kMasked;   // the largest value of each vector, and of all
 #pragma unroll
-    for (int i = 1; i < N; ++i) top = fmaxf(top, x[i]);
-    if (top > s.m) {
-        s.sum = s.m == -INFINITY ? 0.f : s.sum * ex2((s.m - top) * kLog2e);
-        s.m = top;
+    for (int v = 0; v < kVecs; ++v) {
+        tops[v] = x[v * N];
+#pragma unroll
+        for (int i = 1; i < N; ++i) tops[v] = fmaxf(tops[v], x[v * N + i]);
+        top = fmaxf(top, tops[v]);
     }
-    if (s.m != -INFINITY) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) s.sum += ex2((x[i] - s.m) * kLog2e);
+    const float c = top * kLog2e;
+    if (c > s.c) {
+        s.sum *= ex2(s.c - c);
+        s.c = c;
     }
-    uint32_t left = 0, best = 0;   // values not taken yet, the highest rank among them
 #pragma unroll
-    for (int i = 0; i < N; ++i) left |= (uint32_t)exists(i) << i;
-    if (left != 0) best = rank_of(top);
+    for (int i = 0; i < N * kVecs; ++i) s.sum += ex2(fmaf(x[i], kLog2e, -s.c));
+    uint32_t best = exist != 0 ? rank_of(top) : 0;   // of the values not taken yet
     if (s.least == 0) {
         // The first values: `width` lanes have a value of at least the width-th of the lanes' highest
         // ranks, so nothing below it is among the best. Without this, most of the first values would
@@ -122,21 +127,33 @@ __device__ __forceinline__ void take(Seen &s, const float (&x)[N], At at, Exists
     while (true) {
         const uint32_t rank = __reduce_max_sync(0xffffffffu, best);
         if (rank <= s.least || rank == 0) return;
-        uint32_t index = 0xffffffffu;
         int e = -1;
-        if (best == rank) {
+        if (best == rank) {   // its lowest index here
+            const float value = value_of(rank);
 #pragma unroll
-            for (int i = N - 1; i >= 0; --i)
-                if ((left >> i & 1u) && rank_of(x[i]) == rank) index = at(i), e = i;
+            for (int v = 0; v < kVecs; ++v)
+                if (e < 0 && tops[v] == value) {
+#pragma unroll
+                    for (int i = N - 1; i >= 0; --i)
+                        if ((exist >> (v * N + i) & 1u) && x[v * N + i] == value) e = v * N + i;
+                }
         }
-        const uint32_t first = __reduce_min_sync(0xffffffffu, index);
+        const uint32_t index = e >= 0 ? at(e) : 0xffffffffu, first = __reduce_min_sync(0xffffffffu, index);
         s.insert(rank, first, width);
         if (index == first) {
-            left &= ~(1u << e);
-            best = 0;
+            exist &= ~(1u << e);
+            float next = kMasked;
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (left >> i & 1u) best = max(best, rank_of(x[i]));
+            for (int v = 0; v < kVecs; ++v) {
+                if (e / N == v) {   // (an empty vector's kMasked may equal a masked logit: no bit, no match)
+                    tops[v] = kMasked;
+#pragma unroll
+                    for (int i = 0; i < N; ++i)
+                        if (exist >> (v * N + i) & 1u) tops[v] = fmaxf(tops[v], x[v * N + i]);
+                }
+                next = fmaxf(next, tops[v]);
+            }
+            best = exist != 0 ? rank_of(next) : 0;
         }
     }
 }
@@ -172,10 +189,10 @@ __device__ Seen read_part(const Args &a, int row, int chunk) {
     const int head = min((int)((16 - (reinterpret_cast<uintptr_t>(x) & 15u)) % 16 / sizeof(T)), a.vocab);
     const int vectors = (a.vocab - head) / N;                   // whole ones
     const int v0 = (int)((long long)vectors * chunk / a.chunks), v1 = (int)((long long)vectors * (chunk + 1) / a.chunks);
-    Seen s{{0, 0}, 0, -INFINITY, 0.f};
+    Seen s{{0, 0}, 0, kLeastRef, 0.f};
     if (chunk == 0 && head > 0) {
-        const float one[1] = {lane < head ? unmask((float)x[lane]) : -INFINITY};
-        take<1>(s, one, [&](int) { return (uint32_t)lane; }, [&](int) { return lane < head; }, a.width);
+        const float one[1] = {lane < head ? unmask((float)x[lane]) : kMasked};
+        take<1, 1>(s, one, [&](int) { return (uint32_t)lane; }, lane < head, a.width);
     }
     const uint4 *vec = reinterpret_cast<const uint4 *>(x + head);
     uint4 next[kAhead];
@@ -191,24 +208,33 @@ __device__ Seen read_part(const Args &a, int row, int chunk) {
         for (int i = 0; i < kAhead; ++i) u[i] = next[i];
         request(v + 32 * kAhead);
         float f[kAhead * N];
+        uint32_t exist = (1ull << (kAhead * N)) - 1;
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             float g[N];
             Vec<T>::get(u[i], g);
 #pragma unroll
-            for (int e = 0; e < N; ++e) f[i * N + e] = v + 32 * i + lane < v1 ? g[e] : -INFINITY;
+            for (int e = 0; e < N; ++e) f[i * N + e] = g[e];
         }
-        take<kAhead * N>(s, f, [&](int i) { return (uint32_t)(head + (v + 32 * (i / N) + lane) * N + i % N); },
-                         [&](int i) { return v + 32 * (i / N) + lane < v1; }, a.width);
+        if (v + 32 * kAhead > v1) {   // the last ones
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (v + 32 * i + lane >= v1) {
+                    exist &= (1u << (i * N)) - 1;
+#pragma unroll
+                    for (int e = 0; e < N; ++e) f[i * N + e] = kMasked;
+                }
+        }
+        take<N, kAhead>(s, f, [&](int i) { return (uint32_t)(head + (v + 32 * (i / N) + lane) * N + i % N); }, exist, a.width);
     }
     const int t = head + vectors * N;
-    if (chunk == a.chunks - 1 && t < a.vocab) {
-        const float one[1] = {t + lane < a.vocab ? unmask((float)x[t + lane]) : -INFINITY};
-        take<1>(s, one, [&](int) { return (uint32_t)(t + lane); }, [&](int) { return t + lane < a.vocab; }, a.width);
+    if (chunk == a.chunks - 1 && t < a.vocab) {   // fewer than a vector
+        const float one[1] = {t + lane < a.vocab ? unmask((float)x[t + lane]) : kMasked};
+        take<1, 1>(s, one, [&](int) { return (uint32_t)(t + lane); }, t + lane < a.vocab, a.width);
     }
-    const float m = warp_max(s.m);
-    s.sum = warp_sum(s.m == -INFINITY ? 0.f : s.sum * ex2((s.m - m) * kLog2e));
-    s.m = m;
+    const float c = warp_max(s.c);
+    s.sum = warp_sum(s.sum * ex2(s.c - c));
+    s.c = c;
     return s;
 }
 
@@ -221,9 +247,9 @@ __device__ void choose(const Args &a, int seq, const Entry *best, const float2 *
     int lists = a.chunks;   // of a row
     for (int w = warp; w < a.width; w += kWarps) {
         const bool part = lane < a.chunks;
-        const float2 ms = part ? sums[w * a.chunks + lane] : make_float2(-INFINITY, 0.f);
-        const float m = warp_max(ms.x), sum = warp_sum(ms.x == -INFINITY ? 0.f : ms.y * ex2((ms.x - m) * kLog2e));
-        if (lane == 0) lse[w] = make_float2(m, sum);
+        const float2 cs = part ? sums[w * a.chunks + lane] : make_float2(kLeastRef, 0.f);
+        const float ref = warp_max(cs.x), sum = warp_sum(cs.y * ex2(cs.x - ref));
+        if (lane == 0) lse[w] = make_float2(ref, sum);
         if (a.width * a.chunks <= 32) continue;
         const Entry *list = best + ((size_t)w * a.chunks + lane) * a.width;
         int at = 0;
@@ -240,16 +266,16 @@ __device__ void choose(const Args &a, int seq, const Entry *best, const float2 *
     if (warp != 0) return;
     const int w = lane / lists, row = seq * a.width + w;   // lists in the order of rows and indexes
     const bool on = w < a.width;
-    float score = -INFINITY;
+    float score = 0.f;
     bool old = false, dead = true;
     double base = 0.0;
     if (on) {
-        score = unmask(a.scores[row]);
+        score = a.scores[row];
         old = a.ended != nullptr && a.ended[row] != 0;
-        const float2 ms = lse[w];
-        // no candidate above -inf: a masked score, or a row without a finite maximum
-        dead = score == -INFINITY || score == INFINITY || (!old && !(fabsf(ms.x) < INFINITY));
-        if (!dead && !old) base = (double)ms.x + log_near(ms.y);
+        const float2 cs = lse[w];
+        // no candidate above -inf: a masked score, or a row of masked logits or with an infinite one
+        dead = !(score > kMasked && score < INFINITY) || (!old && !(cs.x > kLeastRef && cs.x < INFINITY));
+        if (!dead && !old) base = ((double)cs.x + log2_near(cs.y)) / (double)kLog2e;
     }
     const Entry *list = best + (size_t)lane * a.width;
     // The candidate `at` of this lane's list: its token and its score's rank (0: none left). Beams that
@@ -269,7 +295,8 @@ __device__ void choose(const Args &a, int seq, const Entry *best, const float2 *
             const Entry e = list[at];
             if (e.rank == 0) return;
             token = (int)e.index;
-            c = (double)value_of(e.rank) - base + (double)score;
+            const float x = value_of(e.rank);
+            if (x > kMasked) c = (double)x - base + (double)score;
         }
         const unsigned long long u = (unsigned long long)__double_as_longlong(c + 0.0);
         rank = u >> 63 ? ~u : u | 1ull << 63;
@@ -306,7 +333,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_beam_cluster(const Args a) {
     for (int t = rank * kWarps + warp; t < a.width * a.chunks; t += ctas * kWarps) {
         const Seen s = read_part<T>(a, seq * a.width + t / a.chunks, t % a.chunks);
         if (lane < a.width) best0[(size_t)t * a.width + lane] = s.mine;
-        if (lane == 0) sums0[t] = make_float2(s.m, s.sum);
+        if (lane == 0) sums0[t] = make_float2(s.c, s.sum);
     }
     cluster.sync();
     if (rank == 0) choose(a, seq, best, sums, rows, lse);
@@ -321,7 +348,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_beam_parts(const Args a, long l
     if (t >= parts) return;
     const Seen s = read_part<T>(a, (int)(t / a.chunks), (int)(t % a.chunks));
     if (lane < a.width) a.best[t * a.width + lane] = s.mine;
-    if (lane == 0) a.sums[t] = make_float2(s.m, s.sum);
+    if (lane == 0) a.sums[t] = make_float2(s.c, s.sum);
 }
 __global__ void __launch_bounds__(kWarps * 32) k_beam_choose(const Args a) {
     __shared__ Entry rows[kMaxWidth * kMaxWidth];

@@ -60,8 +60,7 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, bool vec, const float (
     }
 }
 
-// Rows of one (stream, head) in one page, RP at a time, `passes` times: thread = 8 dims, the 4 * NB
-// threads of a row are neighbours. A lane's row: position pos(u) of the stream, row i(u) of the call.
+// A thread has 8 dims of a row; the 4 * NB threads of a head row are neighbours.
 struct RowPlace {
     unsigned char *tile;   // null: nothing to do
     int prow;
@@ -83,26 +82,32 @@ __device__ __forceinline__ RowPlace place_of(const Kv4Rows &r, int tile_bytes, i
             (int)(pos % kPage)};
 }
 
-// One row's eight dims between the tile and x; every lane of the warp takes part.
-template <int HD, bool READ>
-__device__ __forceinline__ void move8(unsigned char *tile, int prow, bool is_v, int b, int c, float (&x)[8]) {
+// A row's word and scale of a lane; where tile is null, none.
+struct Codes {
+    uint32_t w;
+    unsigned short d;
+};
+template <int HD>
+__device__ __forceinline__ Codes load_codes(const unsigned char *tile, int prow, bool is_v, int b, int c) {
     using Tile = Kv4Tile<HD>;
-    constexpr int NB = Tile::NB;
-    unsigned char *word = tile + prow * Tile::kRow + q4_word_at<NB>(is_v, b, c);
-    unsigned char *scale = tile + Tile::kScales + (prow * NB + b) * 2;
-    if (READ) {
-        uint32_t w = tile != nullptr ? *reinterpret_cast<const uint32_t *>(word) : 0;
-        const float d = tile != nullptr ? __half2float(*reinterpret_cast<const __half *>(scale)) : 0.f;
-        if (is_v) w = v_word(w, b);
-        q4_values8(w, d, x);
-    } else {
-        unsigned short d;
-        uint32_t w = q4_codes8(x, d);
-        if (is_v) w = v_word(w, b);
-        if (tile == nullptr) return;
-        *reinterpret_cast<uint32_t *>(word) = w;
-        if (c == 0) *reinterpret_cast<unsigned short *>(scale) = d;
-    }
+    if (tile == nullptr) return {0, 0};
+    return {*reinterpret_cast<const uint32_t *>(tile + prow * Tile::kRow + q4_word_at<Tile::NB>(is_v, b, c)),
+            *reinterpret_cast<const unsigned short *>(tile + Tile::kScales + (prow * Tile::NB + b) * 2)};
+}
+// The values they stand for; every lane of the warp takes part.
+__device__ __forceinline__ void values_of(const Codes &k, bool is_v, int b, float (&x)[8]) {
+    q4_values8(is_v ? v_word(k.w, b) : k.w, __half2float(__ushort_as_half(k.d)), x);
+}
+// A lane's eight dims quantized into the tile; every lane of the warp takes part.
+template <int HD>
+__device__ __forceinline__ void store_codes(unsigned char *tile, int prow, bool is_v, int b, int c, const float (&x)[8]) {
+    using Tile = Kv4Tile<HD>;
+    unsigned short d;
+    uint32_t w = q4_codes8(x, d);
+    if (is_v) w = v_word(w, b);
+    if (tile == nullptr) return;
+    *reinterpret_cast<uint32_t *>(tile + prow * Tile::kRow + q4_word_at<Tile::NB>(is_v, b, c)) = w;
+    if (c == 0) *reinterpret_cast<unsigned short *>(tile + Tile::kScales + (prow * Tile::NB + b) * 2) = d;
 }
 
 // Few rows: grid (items, streams, layers * 2), a head row per 4 * NB threads, rows of a head behind
@@ -123,54 +128,92 @@ __global__ void __launch_bounds__(kRowThreads) k_kv4_rows(const Kv4Rows r, const
     if (!READ && on) load8<T>(dense, vec, x);
     RowPlace p{nullptr, 0};
     if (on) p = place_of(r, Tile::kBytes, s, l, h, is_v, (r.start != nullptr ? (long long)r.start[s] : 0) + r.start0 + i, sub == 0);
-    move8<HD, READ>(p.tile, p.prow, is_v, b, c, x);
-    if (READ && p.tile != nullptr) store8(dense, vec, x);
+    if (READ) {
+        values_of(load_codes<HD>(p.tile, p.prow, is_v, b, c), is_v, b, x);
+        if (p.tile != nullptr) store8(dense, vec, x);
+    } else {
+        store_codes<HD>(p.tile, p.prow, is_v, b, c, x);
+    }
 }
 
-// Many rows: grid (pages * heads, streams, layers * 2), a CTA per (page, head), whose rows it takes
-// kRowThreads / (4 * NB) at a time: one look-up of the page, and every load of the page in flight.
-// Bound by the dense rows' traffic (32 of 36.5 bytes a block of f32).
-template <int HD, typename T, bool READ>
-__global__ void __launch_bounds__(kRowThreads) k_kv4_pages(const Kv4Rows r, const bool vec) {
+// The rows [lo, hi) of one page that a call has of a stream, and where they lie.
+struct PageRows {
+    long long first;   // position of the page's row 0, counted from the call's row 0
+    int lo, hi;
+};
+__device__ __forceinline__ PageRows page_rows(const Kv4Rows &r, int s, int slot, long long &pos) {
+    const long long start = (r.start != nullptr ? (long long)r.start[s] : 0) + r.start0;
+    const int n = r.count != nullptr ? min(r.count[s], r.T) : r.T;
+    pos = (start >= 0 ? start / kPage : -((kPage - 1 - start) / kPage)) * kPage + (long long)slot * kPage;
+    return {pos - start, (int)max(0ll, start - pos), (int)min((long long)kPage, start + n - pos)};
+}
+
+// Many rows: a CTA per (page, head), kRowThreads / (4 * NB) rows at a time: one look-up of the page, and
+// all its loads in flight. Bound by the dense rows' traffic (f32: 128 of 146 bytes a block).
+// Grid (pages * heads, streams, layers * 2) to write and (pages * heads, streams, layers) to read, where a
+// CTA takes K and V, whose loads are small.
+template <int HD, typename T>
+__global__ void __launch_bounds__(kRowThreads) k_kv4_write_pages(const Kv4Rows r, const bool vec) {
     using Tile = Kv4Tile<HD>;
     constexpr int TPR = 4 * Tile::NB, RP = kRowThreads / TPR, kPasses = kPage / RP;
     const int s = blockIdx.y, l = blockIdx.z >> 1;
     const bool is_v = blockIdx.z & 1;
     const int h = blockIdx.x % r.c.n_kv_heads, slot = blockIdx.x / r.c.n_kv_heads;
     const int sub = threadIdx.x % TPR, b = sub >> 2, c = sub & 3;
-    const long long start = (r.start != nullptr ? (long long)r.start[s] : 0) + r.start0;
-    const int n = r.count != nullptr ? min(r.count[s], r.T) : r.T;
-    const long long first = (start >= 0 ? start / kPage : -((kPage - 1 - start) / kPage)) * kPage + (long long)slot * kPage;
-    const int lo = (int)max(0ll, start - first), hi = (int)min((long long)kPage, start + n - first);   // rows of this page
-    if (lo >= hi) return;
-    const RowPlace p = place_of(r, Tile::kBytes, s, l, h, is_v, first, threadIdx.x == 0);
-    if (p.tile == nullptr) return;
-    T *dense = static_cast<T *>(is_v ? r.v : r.k) + (l * r.st.layer + s * r.st.stream + h * r.st.head) + b * 32 + c * 8;
+    long long pos;
+    const PageRows at = page_rows(r, s, slot, pos);
+    if (at.lo >= at.hi) return;
+    const T *dense = static_cast<const T *>(is_v ? r.v : r.k) + (l * r.st.layer + s * r.st.stream + h * r.st.head) + b * 32 + c * 8;
     float x[kPasses][8];
-    if (!READ) {
-#pragma unroll
-        for (int u = 0; u < kPasses; ++u) {
-            const int row = u * RP + threadIdx.x / TPR;
-            if (row >= lo && row < hi) {
-                load8<T>(dense + (first + row - start) * r.st.row, vec, x[u]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[u][e] = 0.f;
-            }
-        }
-    }
 #pragma unroll
     for (int u = 0; u < kPasses; ++u) {
         const int row = u * RP + threadIdx.x / TPR;
-        move8<HD, READ>(row >= lo && row < hi ? p.tile : nullptr, row, is_v, b, c, x[u]);
+        if (row >= at.lo && row < at.hi) {
+            load8<T>(dense + (at.first + row) * r.st.row, vec, x[u]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[u][e] = 0.f;
+        }
     }
-    if (READ) {
+    const RowPlace p = place_of(r, Tile::kBytes, s, l, h, is_v, pos, threadIdx.x == 0);
+    if (p.tile == nullptr) return;
+#pragma unroll
+    for (int u = 0; u < kPasses; ++u) {
+        const int row = u * RP + threadIdx.x / TPR;
+        store_codes<HD>(row >= at.lo && row < at.hi ? p.tile : nullptr, row, is_v, b, c, x[u]);
+    }
+}
+template <int HD, typename T>
+__global__ void __launch_bounds__(kRowThreads) k_kv4_read_pages(const Kv4Rows r, const bool vec) {
+    using Tile = Kv4Tile<HD>;
+    constexpr int TPR = 4 * Tile::NB, RP = kRowThreads / TPR, kPasses = kPage / RP;
+    const int s = blockIdx.y, l = blockIdx.z;
+    const int h = blockIdx.x % r.c.n_kv_heads, slot = blockIdx.x / r.c.n_kv_heads;
+    const int sub = threadIdx.x % TPR, b = sub >> 2, c = sub & 3;
+    long long pos;
+    const PageRows at = page_rows(r, s, slot, pos);
+    if (at.lo >= at.hi) return;
+    const RowPlace p = place_of(r, Tile::kBytes, s, l, h, false, pos, threadIdx.x == 0);
+    if (p.tile == nullptr) return;
+    unsigned char *tiles[2] = {p.tile, static_cast<unsigned char *>(r.c.v) + (p.tile - static_cast<unsigned char *>(r.c.k))};
+    Codes k[2][kPasses];
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
 #pragma unroll
         for (int u = 0; u < kPasses; ++u) {
             const int row = u * RP + threadIdx.x / TPR;
-            if (row >= lo && row < hi) store8(dense + (first + row - start) * r.st.row, vec, x[u]);
+            k[v][u] = load_codes<HD>(row >= at.lo && row < at.hi ? tiles[v] : nullptr, row, v, b, c);
         }
-    }
+    const int64_t off = l * r.st.layer + s * r.st.stream + h * r.st.head + b * 32 + c * 8;
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+#pragma unroll
+        for (int u = 0; u < kPasses; ++u) {
+            const int row = u * RP + threadIdx.x / TPR;
+            float x[8];
+            values_of(k[v][u], v, b, x);
+            if (row >= at.lo && row < at.hi) store8(static_cast<T *>(v ? r.v : r.k) + off + (at.first + row) * r.st.row, vec, x);
+        }
 }
 
 // From this many rows a stream on, a CTA per page is faster.
@@ -180,7 +223,9 @@ template <int HD, typename T, bool READ>
 cudaError_t launch_rows_t(const Kv4Rows &r, bool vec, cudaStream_t s) {
     if (r.T >= kPageRowsMin) {
         const long long slots = ((long long)r.T + kPage - 2) / kPage + 1;   // pages that T rows can touch
-        k_kv4_pages<HD, T, READ><<<dim3((unsigned)(slots * r.c.n_kv_heads), r.n_streams, 2 * r.n_layers), kRowThreads, 0, s>>>(r, vec);
+        const dim3 grid((unsigned)(slots * r.c.n_kv_heads), r.n_streams, READ ? r.n_layers : 2 * r.n_layers);
+        if (READ) k_kv4_read_pages<HD, T><<<grid, kRowThreads, 0, s>>>(r, vec);
+        else k_kv4_write_pages<HD, T><<<grid, kRowThreads, 0, s>>>(r, vec);
     } else {
         const long long items = (long long)r.T * r.c.n_kv_heads;
         const int per = kRowThreads / (HD / 8);

@@ -20,6 +20,33 @@ struct Kv4Tile {
 };
 constexpr int kv4_tile_bytes(int hd) { return hd * 36; }
 
+// Two f32 values in one 64-bit register, each instruction computing both.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float f2_lo(F2 x) { return __uint_as_float((uint32_t)x.v); }
+__device__ __forceinline__ float f2_hi(F2 x) { return __uint_as_float((uint32_t)(x.v >> 32)); }
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
 // Quantizes one block of 32 values. The four lanes of an aligned group hold dims 8 c .. 8 c + 7
 // of the block, c = lane & 3; every lane of the warp has to take part. Returns the lane's eight
 // codes (dim i in bits 4 i ..) and the block's scale bits.
@@ -30,10 +57,11 @@ constexpr int kv4_tile_bytes(int hd) { return hd * 36; }
 // (17 - 2 k) |m| < 16 x sign(m): the sign of one fma, which rounds that difference only once. Blocks
 // with tiny |m| are scaled by 2^60 first (exact), so that neither 8 / m nor the sign can be lost.
 __device__ __forceinline__ uint32_t q4_codes8(const float (&x)[8], unsigned short &d_bits) {
-    float m = x[0], zero = 0.f;
+    float m = x[0];
+    F2 zero = f2(0.f, 0.f);   // NaN if a value is not finite
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        zero = fmaf(x[i], 0.f, zero);   // NaN if a value is not finite
+        if (i % 2 == 0) zero = fma2(f2(x[i], x[i + 1]), f2(0.f, 0.f), zero);
         if (fabsf(x[i]) > fabsf(m)) m = x[i];
     }
     const int lane = threadIdx.x & 31;
@@ -43,7 +71,7 @@ __device__ __forceinline__ uint32_t q4_codes8(const float (&x)[8], unsigned shor
         if (fabsf(other) > fabsf(m) || (fabsf(other) == fabsf(m) && (lane & o))) m = other;
     }
     // the warp's bits of "not finite", of this group of four
-    const bool bad = (__ballot_sync(0xffffffffu, !(zero == 0.f)) >> (lane & ~3) & 15u) != 0;
+    const bool bad = (__ballot_sync(0xffffffffu, !(f2_lo(zero) + f2_hi(zero) == 0.f)) >> (lane & ~3) & 15u) != 0;
     float y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = x[i];
@@ -59,11 +87,12 @@ __device__ __forceinline__ uint32_t q4_codes8(const float (&x)[8], unsigned shor
     constexpr float kRound = 12582912.f;   // 1.5 2^23: x + kRound holds the nearest whole number to x
     uint32_t w = 0;
 #pragma unroll
-    for (int i = 7; i >= 0; --i) {
-        const float z = y[i] * s, r = fmaf(z, id, 8.5f) + kRound;
-        const float side = fmaf(fmaf(-2.f, r - kRound, 17.f), M, z);
-        const int n = __float_as_int(r) - __float_as_int(kRound) + (__float_as_int(side) >> 31);
-        w = w * 16 + (uint32_t)min(n, 15);
+    for (int i = 6; i >= 0; i -= 2) {
+        const F2 z = f2(y[i], y[i + 1]) * f2(s, s), r = fma2(z, f2(id, id), f2(8.5f, 8.5f)) + f2(kRound, kRound);
+        const F2 side = fma2(fma2(f2(-2.f, -2.f), r + f2(-kRound, -kRound), f2(17.f, 17.f)), f2(M, M), z);
+        const int n1 = __float_as_int(f2_hi(r)) - __float_as_int(kRound) + (__float_as_int(f2_hi(side)) >> 31);
+        const int n0 = __float_as_int(f2_lo(r)) - __float_as_int(kRound) + (__float_as_int(f2_lo(side)) >> 31);
+        w = w * 256 + (uint32_t)(min(n1, 15) * 16 + min(n0, 15));
     }
     return w;
 }

@@ -68,32 +68,6 @@ __device__ __forceinline__ uint32_t centred(uint32_t x, uint32_t mid) {
 }
 constexpr uint32_t kMidNibble = 0x64086408u, kMidByte = 0x64886488u;   // 1032, 1160
 
-// Two f32 values in one 64-bit register, each instruction computing both.
-struct F2 {
-    uint64_t v;
-};
-__device__ __forceinline__ F2 f2(float a, float b) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float f2_lo(F2 x) { return __uint_as_float((uint32_t)x.v); }
-__device__ __forceinline__ float f2_hi(F2 x) { return __uint_as_float((uint32_t)(x.v >> 32)); }
-__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
 // What is left of x after its first 11 bits (the fp16 part that pack_rz keeps), or x where mask is 0.
 __device__ __forceinline__ F2 rest11(F2 x, uint32_t mask) {
     const F2 first = f2(__uint_as_float((uint32_t)x.v & mask), __uint_as_float((uint32_t)(x.v >> 32) & mask));
