@@ -16,7 +16,8 @@ constexpr int kWarps = 8;
 constexpr int kMaxWidth = 32;
 constexpr int kMaxChunks = 32;      // parts of a row: the lists that one warp joins, a lane each
 constexpr int kCluster = 8;
-constexpr int kClusterTasks = kWarps * kCluster + kMaxWidth;
+constexpr int kRowEntries = 600;    // best logits of a row's parts, at most (k_beam_choose holds a row's for each warp)
+constexpr int kClusterTasks = 128, kClusterEntries = 3072;   // parts of a sequence and their best logits, in a cluster
 constexpr float kMasked = -1e30f;   // at or below: counts as -inf
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLeastRef = -1.4426e30f;   // reference of a row's exponents without a logit: over kLog2e kMasked
@@ -70,33 +71,33 @@ struct Args {
     float2 *sums;     // scratch: [row][chunk] (reference c, sum of 2^(kLog2e x - c))
 };
 
-// What a warp has seen of a row: lane i < width holds the i-th best logit (rank 0: none yet); every
-// lane has its part of the sum of 2^(kLog2e x - c) and its reference c, kLog2e times its largest logit
-// (at least kLeastRef, below which masked values, and lanes that have none, add nothing).
-// (With one multiply-add per exponent: the same rounded factor in every term, and in the end.) What ranks
-// `least` or lower is not among the best any more.
+// What a warp has seen of a row: lane i < width holds the i-th best logit (-inf: none yet); every lane
+// has its part of the sum of 2^(kLog2e x - c) and its reference c, kLog2e times its largest logit (at
+// least kLeastRef, below which masked values, and lanes that have none, add nothing). With one multiply-
+// add per exponent: the same rounded factor in every term, and in the end. A logit that is not above
+// `least` is not among the best any more.
 struct Seen {
-    Entry mine;
-    uint32_t least;
-    float c, sum;
+    float value;
+    uint32_t index;
+    float least, c, sum;
 
-    __device__ __forceinline__ void insert(uint32_t rank, uint32_t index, int width) {   // the same in all lanes
+    __device__ __forceinline__ Entry entry() const { return {value == -INFINITY ? 0 : rank_of(value), index}; }
+    __device__ __forceinline__ void insert(float x, uint32_t i, int width) {   // the same in all lanes
         const int lane = threadIdx.x & 31;
-        const int at = __popc(__ballot_sync(0xffffffffu, mine.rank > rank || (mine.rank == rank && mine.index < index)));
-        const uint32_t r = __shfl_up_sync(0xffffffffu, mine.rank, 1), i = __shfl_up_sync(0xffffffffu, mine.index, 1);
-        if (lane > at) mine = {r, i};
-        if (lane == at) mine = {rank, index};
-        if (lane >= width) mine.rank = 0;
-        least = max(least, __shfl_sync(0xffffffffu, mine.rank, width - 1));
+        const int at = __popc(__ballot_sync(0xffffffffu, value > x || (value == x && index < i)));
+        const float v = __shfl_up_sync(0xffffffffu, value, 1);
+        const uint32_t k = __shfl_up_sync(0xffffffffu, index, 1);
+        if (lane > at) value = v, index = k;
+        if (lane == at) value = x, index = i;
+        if (lane >= width) value = -INFINITY, index = 0xffffffffu;
+        least = fmaxf(least, __shfl_sync(0xffffffffu, value, width - 1));
     }
 };
 
-// kVecs vectors of N values per lane; the logit x[i] has index at(i); `exist`: a bit for each that there
-// is (the others are kMasked). Logits come in the order of their indexes, so a later equal one never
-// replaces another.
-template <int N, int kVecs, typename At>
-__device__ __forceinline__ void take(Seen &s, const float (&x)[N * kVecs], At at, uint32_t exist, int width) {
-    const int lane = threadIdx.x & 31;
+// kVecs vectors of N logits per lane, of which vector v exists if on(v); at(v, l): the index of lane l's
+// first. They are taken in the order of their indexes, so a later equal one never replaces another.
+template <int N, int kVecs, typename On, typename At>
+__device__ __forceinline__ void take(Seen &s, const float (&x)[N * kVecs], On on, At at, int width) {
     float tops[kVecs], top = kMasked;   // the largest value of each vector, and of all
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
@@ -104,6 +105,7 @@ __device__ __forceinline__ void take(Seen &s, const float (&x)[N * kVecs], At at
 #pragma unroll
         for (int i = 1; i < N; ++i) tops[v] = fmaxf(tops[v], x[v * N + i]);
         top = fmaxf(top, tops[v]);
+        if (!on(v)) tops[v] = -INFINITY;
     }
     const float c = top * kLog2e;
     if (c > s.c) {
@@ -112,48 +114,18 @@ __device__ __forceinline__ void take(Seen &s, const float (&x)[N * kVecs], At at
     }
 #pragma unroll
     for (int i = 0; i < N * kVecs; ++i) s.sum += ex2(fmaf(x[i], kLog2e, -s.c));
-    uint32_t best = exist != 0 ? rank_of(top) : 0;   // of the values not taken yet
-    if (s.least == 0) {
-        // The first values: `width` lanes have a value of at least the width-th of the lanes' highest
-        // ranks, so nothing below it is among the best. Without this, most of the first values would
-        // be inserted and pushed out again.
-        uint32_t lanes = best, floor = 0;
-        for (int j = 0; j < width; ++j) {
-            floor = __reduce_max_sync(0xffffffffu, lanes);
-            if (lane == __ffs(__ballot_sync(0xffffffffu, lanes == floor)) - 1) lanes = 0;
-        }
-        if (floor > 0) s.least = floor - 1;
-    }
-    while (true) {
-        const uint32_t rank = __reduce_max_sync(0xffffffffu, best);
-        if (rank <= s.least || rank == 0) return;
-        int e = -1;
-        if (best == rank) {   // its lowest index here
-            const float value = value_of(rank);
 #pragma unroll
-            for (int v = 0; v < kVecs; ++v)
-                if (e < 0 && tops[v] == value) {
+    for (int v = 0; v < kVecs; ++v) {
+        uint32_t lanes = __ballot_sync(0xffffffffu, tops[v] > s.least);
+        while (lanes != 0) {
+            const int from = __ffs(lanes) - 1;
 #pragma unroll
-                    for (int i = N - 1; i >= 0; --i)
-                        if ((exist >> (v * N + i) & 1u) && x[v * N + i] == value) e = v * N + i;
-                }
-        }
-        const uint32_t index = e >= 0 ? at(e) : 0xffffffffu, first = __reduce_min_sync(0xffffffffu, index);
-        s.insert(rank, first, width);
-        if (index == first) {
-            exist &= ~(1u << e);
-            float next = kMasked;
-#pragma unroll
-            for (int v = 0; v < kVecs; ++v) {
-                if (e / N == v) {   // (an empty vector's kMasked may equal a masked logit: no bit, no match)
-                    tops[v] = kMasked;
-#pragma unroll
-                    for (int i = 0; i < N; ++i)
-                        if (exist >> (v * N + i) & 1u) tops[v] = fmaxf(tops[v], x[v * N + i]);
-                }
-                next = fmaxf(next, tops[v]);
+            for (int i = 0; i < N; ++i) {
+                const float y = __shfl_sync(0xffffffffu, x[v * N + i], from);
+                if (y > s.least) s.insert(y, at(v, from) + i, width);
             }
-            best = exist != 0 ? rank_of(next) : 0;
+            lanes &= lanes - 1;
+            lanes &= __ballot_sync(0xffffffffu, tops[v] > s.least);
         }
     }
 }
@@ -178,21 +150,44 @@ struct Vec<__nv_bfloat16> {
     }
 };
 
+// Of n <= 32 * kPer ranks, the width-th highest (0 if there are fewer), by one warp: so many logits rank
+// at least as high, and nothing below it is among the best. Without such a floor most of a part's first
+// logits would be inserted and pushed out again.
+template <int kPer>
+__device__ __forceinline__ uint32_t floor_of(uint32_t (&r)[kPer], int width) {
+    const int lane = threadIdx.x & 31;
+    uint32_t floor = 0;
+    for (int j = 0; j < width; ++j) {
+        uint32_t top = r[0];
+#pragma unroll
+        for (int i = 1; i < kPer; ++i) top = max(top, r[i]);
+        floor = __reduce_max_sync(0xffffffffu, top);
+        if (lane == __ffs(__ballot_sync(0xffffffffu, top == floor)) - 1) {
+            bool gone = false;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (!gone && r[i] == floor) r[i] = 0, gone = true;
+        }
+    }
+    return floor;
+}
+
 // One warp reads part `chunk` of a row once, by 16-byte loads where the row allows: the unaligned
 // logits at its ends go to the first and the last part. The row's maximum and sum of exponentials
-// come from the same pass as its best logits.
+// come from the same pass as its best logits. tops: where the CTA's warps all read parts of one row, shared
+// memory for their lanes' largest logits of the first vectors, from which they take one floor.
 template <typename T>
-__device__ Seen read_part(const Args &a, int row, int chunk) {
+__device__ Seen read_part(const Args &a, int row, int chunk, uint32_t *tops) {
     constexpr int N = Vec<T>::N, kAhead = 16 / N;
     const int lane = threadIdx.x & 31;
     const T *x = static_cast<const T *>(a.logits) + row * a.row_stride;
     const int head = min((int)((16 - (reinterpret_cast<uintptr_t>(x) & 15u)) % 16 / sizeof(T)), a.vocab);
     const int vectors = (a.vocab - head) / N;                   // whole ones
     const int v0 = (int)((long long)vectors * chunk / a.chunks), v1 = (int)((long long)vectors * (chunk + 1) / a.chunks);
-    Seen s{{0, 0}, 0, kLeastRef, 0.f};
+    Seen s{-INFINITY, 0xffffffffu, -INFINITY, kLeastRef, 0.f};
     if (chunk == 0 && head > 0) {
         const float one[1] = {lane < head ? unmask((float)x[lane]) : kMasked};
-        take<1, 1>(s, one, [&](int) { return (uint32_t)lane; }, lane < head, a.width);
+        take<1, 1>(s, one, [&](int) { return lane < head; }, [&](int, int l) { return (uint32_t)l; }, a.width);
     }
     const uint4 *vec = reinterpret_cast<const uint4 *>(x + head);
     uint4 next[kAhead];
@@ -202,13 +197,12 @@ __device__ Seen read_part(const Args &a, int row, int chunk) {
             if (v + 32 * i + lane < v1) next[i] = ldg_stream(vec + v + 32 * i + lane);
     };
     request(v0);
-    for (int v = v0; v < v1; v += 32 * kAhead) {
+    for (int v = v0; v < v1 || (v == v0 && tops != nullptr); v += 32 * kAhead) {
         uint4 u[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) u[i] = next[i];
         request(v + 32 * kAhead);
         float f[kAhead * N];
-        uint32_t exist = (1ull << (kAhead * N)) - 1;
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             float g[N];
@@ -220,17 +214,38 @@ __device__ Seen read_part(const Args &a, int row, int chunk) {
 #pragma unroll
             for (int i = 0; i < kAhead; ++i)
                 if (v + 32 * i + lane >= v1) {
-                    exist &= (1u << (i * N)) - 1;
 #pragma unroll
                     for (int e = 0; e < N; ++e) f[i * N + e] = kMasked;
                 }
         }
-        take<N, kAhead>(s, f, [&](int i) { return (uint32_t)(head + (v + 32 * (i / N) + lane) * N + i % N); }, exist, a.width);
+        if (v == v0) {
+            float m = f[0];
+#pragma unroll
+            for (int i = 1; i < kAhead * N; ++i) m = fmaxf(m, f[i]);
+            const uint32_t top = v + lane < v1 ? rank_of(m) : 0;
+            uint32_t floor;
+            if (tops != nullptr) {
+                uint32_t r[kWarps];
+                tops[threadIdx.x] = top;
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < kWarps; ++i) r[i] = tops[32 * i + lane];
+                __syncthreads();
+                floor = floor_of(r, a.width);
+            } else {
+                uint32_t r[1] = {top};
+                floor = floor_of(r, a.width);
+            }
+            // the next value below it (below 0 that is not -0)
+            if (floor > 0) s.least = fmaxf(s.least, value_of(floor - (floor == 0x80000000u ? 2 : 1)));
+        }
+        take<N, kAhead>(s, f, [&](int i) { return v + 32 * i + lane < v1; },
+                        [&](int i, int l) { return (uint32_t)(head + (v + 32 * i + l) * N); }, a.width);
     }
     const int t = head + vectors * N;
     if (chunk == a.chunks - 1 && t < a.vocab) {   // fewer than a vector
         const float one[1] = {t + lane < a.vocab ? unmask((float)x[t + lane]) : kMasked};
-        take<1, 1>(s, one, [&](int) { return (uint32_t)(t + lane); }, t + lane < a.vocab, a.width);
+        take<1, 1>(s, one, [&](int) { return t + lane < a.vocab; }, [&](int, int l) { return (uint32_t)(t + l); }, a.width);
     }
     const float c = warp_max(s.c);
     s.sum = warp_sum(s.sum * ex2(s.c - c));
@@ -239,10 +254,10 @@ __device__ Seen read_part(const Args &a, int row, int chunk) {
 }
 
 // The parts of a sequence's rows joined and its continuations chosen, by one CTA of kWarps warps.
-// best, sums: [row of the sequence][part]. Where a sequence has more than a warp's lists, a warp
+// best, sums: [row of the sequence][part]; stage: room for a row's lists for each warp, or null. Where a sequence has more than a warp's lists, a warp
 // joins each row's first (into rows). Then one warp, a lane to a list, takes the best of the lists'
 // heads `width` times; candidates are compared in 64 bits, as whole numbers of the same order.
-__device__ void choose(const Args &a, int seq, const Entry *best, const float2 *sums, Entry *rows, float2 *lse) {
+__device__ void choose(const Args &a, int seq, const Entry *best, const float2 *sums, Entry *rows, float2 *lse, Entry *stage) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int lists = a.chunks;   // of a row
     for (int w = warp; w < a.width; w += kWarps) {
@@ -251,7 +266,15 @@ __device__ void choose(const Args &a, int seq, const Entry *best, const float2 *
         const float ref = warp_max(cs.x), sum = warp_sum(cs.y * ex2(cs.x - ref));
         if (lane == 0) lse[w] = make_float2(ref, sum);
         if (a.width * a.chunks <= 32) continue;
-        const Entry *list = best + ((size_t)w * a.chunks + lane) * a.width;
+        const Entry *list = best + (size_t)w * a.chunks * a.width;
+        if (stage != nullptr) {   // from global memory: all at once, not a list's entries one after another
+            Entry *mine = stage + warp * a.chunks * a.width;
+            __syncwarp();
+            for (int i = lane; i < a.chunks * a.width; i += 32) mine[i] = list[i];
+            __syncwarp();
+            list = mine;
+        }
+        list += lane * a.width;
         int at = 0;
         Entry head = part ? list[0] : Entry{0, 0};
         for (int j = 0; j < a.width; ++j) {
@@ -322,8 +345,9 @@ __device__ void choose(const Args &a, int seq, const Entry *best, const float2 *
 // the first CTA's shared memory, which joins them. No scratch, one launch.
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32) k_beam_cluster(const Args a) {
-    __shared__ Entry best[kClusterTasks * kMaxWidth], rows[kMaxWidth * kMaxWidth];
+    __shared__ Entry best[kClusterEntries], rows[kMaxWidth * kMaxWidth];
     __shared__ float2 sums[kClusterTasks], lse[kMaxWidth];
+    __shared__ uint32_t tops[kWarps * 32];
     cg::cluster_group cluster = cg::this_cluster();
     const int ctas = cluster.num_blocks(), rank = cluster.block_rank(), seq = blockIdx.x / ctas;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -331,31 +355,33 @@ __global__ void __launch_bounds__(kWarps * 32) k_beam_cluster(const Args a) {
     float2 *sums0 = cluster.map_shared_rank(sums, 0);
     cluster.sync();   // every CTA's shared memory is there
     for (int t = rank * kWarps + warp; t < a.width * a.chunks; t += ctas * kWarps) {
-        const Seen s = read_part<T>(a, seq * a.width + t / a.chunks, t % a.chunks);
-        if (lane < a.width) best0[(size_t)t * a.width + lane] = s.mine;
+        const Seen s = read_part<T>(a, seq * a.width + t / a.chunks, t % a.chunks, a.chunks % kWarps == 0 ? tops : nullptr);
+        if (lane < a.width) best0[(size_t)t * a.width + lane] = s.entry();
         if (lane == 0) sums0[t] = make_float2(s.c, s.sum);
     }
     cluster.sync();
-    if (rank == 0) choose(a, seq, best, sums, rows, lse);
+    if (rank == 0) choose(a, seq, best, sums, rows, lse, nullptr);
 }
 
 // Larger calls: a warp per part over the whole GPU, the results in scratch; then a CTA per sequence.
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32) k_beam_parts(const Args a, long long parts) {
+    __shared__ uint32_t tops[kWarps * 32];
     const int lane = threadIdx.x & 31;
     pdl_launch_dependents();
     const long long t = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (t >= parts) return;
-    const Seen s = read_part<T>(a, (int)(t / a.chunks), (int)(t % a.chunks));
-    if (lane < a.width) a.best[t * a.width + lane] = s.mine;
+    const Seen s = read_part<T>(a, (int)(t / a.chunks), (int)(t % a.chunks), a.chunks % kWarps == 0 ? tops : nullptr);
+    if (lane < a.width) a.best[t * a.width + lane] = s.entry();
     if (lane == 0) a.sums[t] = make_float2(s.c, s.sum);
 }
 __global__ void __launch_bounds__(kWarps * 32) k_beam_choose(const Args a) {
+    extern __shared__ Entry stage[];   // a row's lists for each warp
     __shared__ Entry rows[kMaxWidth * kMaxWidth];
     __shared__ float2 lse[kMaxWidth];
     pdl_wait();
     const size_t first = (size_t)blockIdx.x * a.width * a.chunks;
-    choose(a, blockIdx.x, a.best + first * a.width, a.sums + first, rows, lse);
+    choose(a, blockIdx.x, a.best + first * a.width, a.sums + first, rows, lse, stage);
 }
 
 // How a call runs. A cluster serves a sequence until its CTAs would read over kClusterLogits each;
@@ -365,7 +391,7 @@ struct Shape {
     int chunks;
 };
 constexpr int kClusterLogits = 32768, kPartLogits = 1024;
-constexpr int kTargetParts = 152 * 12;
+constexpr int kTargetParts = 152 * 20;
 
 Shape shape_of(int n_seq, int width, int vocab) {
     const long long logits = (long long)width * vocab;
@@ -377,7 +403,12 @@ Shape shape_of(int n_seq, int width, int vocab) {
         parts = (kTargetParts + n_seq - 1) / n_seq;
     }
     const long long most = std::max(1, std::min(kMaxChunks, vocab / kPartLogits));
-    p.chunks = (int)std::min(most, std::max(1ll, (parts + width - 1) / width));
+    long long chunks = std::min(most, std::max(1ll, (parts + width - 1) / width));
+    if (chunks > kWarps / 2) chunks = std::min(most, (chunks + kWarps / 2) / kWarps * kWarps);   // a CTA's warps in one row
+    chunks = std::min<long long>(chunks, kRowEntries / width);
+    if (p.ctas > 0) chunks = std::min<long long>(chunks, std::min(kClusterTasks, kClusterEntries / width) / width);
+    if (chunks >= kWarps) chunks -= chunks % kWarps;
+    p.chunks = (int)chunks;
     return p;
 }
 
@@ -438,6 +469,7 @@ talker_status talker_beam_select(const void *logits, int64_t row_stride, int dty
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.gridDim = dim3((unsigned)n_seq);
         cfg.numAttrs = 1;
+        cfg.dynamicSmemBytes = width * p.chunks > 32 ? (size_t)kWarps * p.chunks * width * sizeof(Entry) : 0;
         if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, k_beam_choose, a);
     }
     if (e == cudaSuccess) return TALKER_OK;
