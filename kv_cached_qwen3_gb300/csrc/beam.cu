@@ -443,32 +443,36 @@ talker_status talker_beam_select(const void *logits, int64_t row_stride, int dty
     if (need > 0 && (!scratch || scratch_bytes < need || (reinterpret_cast<uintptr_t>(scratch) & 15u))) return TALKER_EINVAL;
     const Shape p = shape_of(n_seq, width, vocab);
     Args a{logits, row_stride, scores, ended, width, vocab, eos_id, tokens, parents, ended_out, scores_out, p.chunks};
+    const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+    const bool f32 = dtype == TALKER_DTYPE_F32;
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kWarps * 32);
-    cfg.stream = static_cast<cudaStream_t>(cuda_stream);
     cudaLaunchAttribute attr[1];
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const bool f32 = dtype == TALKER_DTYPE_F32;
     cudaError_t e;
-    if (p.ctas > 0) {
+    if (p.ctas == 1) {
+        if (f32) k_beam_cluster<float><<<n_seq, kWarps * 32, 0, st>>>(a);
+        else k_beam_cluster<__nv_bfloat16><<<n_seq, kWarps * 32, 0, st>>>(a);
+        e = cudaGetLastError();
+    } else if (p.ctas > 1) {
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = p.ctas;
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.gridDim = dim3((unsigned)(n_seq * p.ctas));
-        cfg.numAttrs = p.ctas > 1;
         e = cudaLaunchKernelEx(&cfg, f32 ? k_beam_cluster<float> : k_beam_cluster<__nv_bfloat16>, a);
     } else {
         const long long parts = (long long)n_seq * width * p.chunks;
+        const unsigned blocks = (unsigned)((parts + kWarps - 1) / kWarps);
         a.best = static_cast<Entry *>(scratch);
         a.sums = reinterpret_cast<float2 *>(static_cast<char *>(scratch) + align16((size_t)parts * width * sizeof(Entry)));
-        cfg.gridDim = dim3((unsigned)((parts + kWarps - 1) / kWarps));
-        cfg.numAttrs = 0;
-        e = cudaLaunchKernelEx(&cfg, f32 ? k_beam_parts<float> : k_beam_parts<__nv_bfloat16>, a, parts);
+        if (f32) k_beam_parts<float><<<blocks, kWarps * 32, 0, st>>>(a, parts);
+        else k_beam_parts<__nv_bfloat16><<<blocks, kWarps * 32, 0, st>>>(a, parts);
+        e = cudaGetLastError();
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.gridDim = dim3((unsigned)n_seq);
-        cfg.numAttrs = 1;
         cfg.dynamicSmemBytes = width * p.chunks > 32 ? (size_t)kWarps * p.chunks * width * sizeof(Entry) : 0;
         if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, k_beam_choose, a);
     }

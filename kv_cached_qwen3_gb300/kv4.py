@@ -13,7 +13,10 @@ import torch
 from .talker import TalkerError, load_library
 
 PAGE = 64
-_raw_stream = torch._C._cuda_getCurrentRawStream   # torch.cuda.current_stream(device).cuda_stream, without the object
+# torch.cuda.current_stream(device).cuda_stream and torch.cuda.current_device(), without their objects and checks:
+# small calls take about as long as these (the tensors that are passed have initialised CUDA)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 _DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 
 
@@ -29,7 +32,7 @@ class _Strides(ctypes.Structure):
 
 def launch(device: int, fn, what, *args):
     """fn(*args, stream) on the current stream of a device, with that device current."""
-    if torch.cuda.current_device() == device:
+    if _current_device() == device:
         status = fn(*args, _raw_stream(device))
     else:
         with torch.cuda.device(device):
@@ -84,52 +87,50 @@ class KV4Cache:
             status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._ints("status", status, 1)
         self.status = status
-        self._lib = load_library()
+        self._lib = lib = load_library()
+        self._write, self._read = lib.talker_kv4_write, lib.talker_kv4_read
+        self._attend, self._reorder = lib.talker_kv4_attend, lib.talker_kv4_reorder
         self._c = _Cache(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), status.data_ptr(), self.n_pages,
                          self.n_streams, self.pages_per_stream, self.n_layers, self.n_kv_heads, head_dim)
         self._ref = ctypes.addressof(self._c)
         self._scratch = {}     # attend's scratch bytes by (B, n_q_heads, max_len)
 
     def _ints(self, name, t, n):
-        if t.dtype != torch.int32 or t.device != self.device or not t.is_contiguous() or \
-                (n is not None and t.numel() != n):
+        if t.dtype is not torch.int32 or t.device != self.device or (n is not None and t.numel() != n) or \
+                not t.is_contiguous():
             raise ValueError("%s must be a contiguous int32 tensor%s on %s" %
                              (name, "" if n is None else " of %d" % n, self.device))
         return t.data_ptr()
 
-    def _call(self, fn, what, *args):
-        launch(self.device.index, fn, what, *args)
-
     def _rows(self, fn, what, k, v, start, count, layer0, stream0):
-        for name, t in (("k", k), ("v", v)):
-            if t.dim() != 5 or t.dtype not in _DTYPE or t.device != self.device:
-                raise ValueError("%s: %s must be f32 or bf16 [layers, streams, rows, n_kv_heads, head_dim] on %s" %
-                                 (what, name, self.device))
-            if t.shape[3] != self.n_kv_heads or t.shape[4] != self.head_dim or (t.stride(4) != 1 and t.numel()):
-                raise ValueError("%s: %s must hold %d heads of %d contiguous dims" %
-                                 (what, name, self.n_kv_heads, self.head_dim))
-        if k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride():
-            raise ValueError("%s: k and v must have the same shape, type and strides" % what)
-        layers, streams, rows = k.shape[:3]
-        if k.numel() == 0:
+        shape, stride, dtype = k.shape, k.stride(), _DTYPE.get(k.dtype)
+        if len(shape) != 5 or dtype is None or k.device != self.device or shape[3] != self.n_kv_heads or \
+                shape[4] != self.head_dim:
+            raise ValueError("%s: k and v must be f32 or bf16 [layers, streams, rows, %d, %d] on %s" %
+                             (what, self.n_kv_heads, self.head_dim, self.device))
+        if v.shape != shape or v.stride() != stride or v.dtype is not k.dtype or v.device != self.device:
+            raise ValueError("%s: k and v must have the same shape, type, strides and device" % what)
+        layers, streams, rows = shape[:3]
+        if layers == 0 or streams == 0 or rows == 0:
             return
-        s = k.stride()
-        strides = _Strides(s[0], s[1], s[2], s[3])
-        self._call(fn, what, self._ref, layer0, layers, stream0, streams,
-                   None if start is None else self._ints("start", start, streams),
-                   None if count is None else self._ints("count", count, streams), rows, k.data_ptr(), v.data_ptr(),
-                   _DTYPE[k.dtype], ctypes.addressof(strides))
+        if stride[4] != 1:
+            raise ValueError("%s: the dims of k and v must be contiguous" % what)
+        strides = _Strides(*stride[:4])
+        launch(self.device.index, fn, what, self._ref, layer0, layers, stream0, streams,
+               None if start is None else self._ints("start", start, streams),
+               None if count is None else self._ints("count", count, streams), rows, k.data_ptr(), v.data_ptr(),
+               dtype, ctypes.addressof(strides))
 
     def write(self, k, v, start=None, count=None, layer0: int = 0, stream0: int = 0):
         """Quantize rows into the cache. k, v: [layers, streams, rows, n_kv_heads, head_dim] f32 or bf16 in any
         strides with contiguous dims, for layers layer0.. and streams stream0..; row i of stream s goes to position
         start[s] + i (start None: 0), and rows past count[s] are not written."""
-        self._rows(self._lib.talker_kv4_write, "talker_kv4_write", k, v, start, count, layer0, stream0)
+        self._rows(self._write, "talker_kv4_write", k, v, start, count, layer0, stream0)
 
     def read(self, k, v, start=None, count=None, layer0: int = 0, stream0: int = 0):
         """Read the rows that `write` with these arguments stores, into k and v, as the values they stand for. Rows
         past count[s] are left as they are. Returns (k, v)."""
-        self._rows(self._lib.talker_kv4_read, "talker_kv4_read", k, v, start, count, layer0, stream0)
+        self._rows(self._read, "talker_kv4_read", k, v, start, count, layer0, stream0)
         return k, v
 
     def attend(self, layer: int, q, lens, k_new=None, v_new=None, scale=None, max_len=None, out=None):
@@ -137,28 +138,30 @@ class KV4Cache:
         0..B-1), over the first lens[b] cached rows and, with k_new / v_new [B, n_kv_heads, head_dim], the step's own
         row as given. scale defaults to 1 / sqrt(head_dim); max_len is an estimate of the longest length (default:
         the streams' capacity) that shapes the launch. Returns [B, n_q_heads, head_dim] in q's type."""
-        if q.dim() != 3 or q.dtype not in _DTYPE or q.device != self.device or q.shape[2] != self.head_dim:
+        dtype = _DTYPE.get(q.dtype)
+        shape = q.shape
+        if len(shape) != 3 or dtype is None or q.device != self.device or shape[2] != self.head_dim:
             raise ValueError("attend: q must be f32 or bf16 [B, n_q_heads, %d] on %s" % (self.head_dim, self.device))
-        B, n_q, hd = q.shape
+        B, n_q, hd = shape
         if n_q < 1 or n_q % self.n_kv_heads or n_q // self.n_kv_heads > 8 or B > self.n_streams:
             raise ValueError("attend: needs at most %d streams and 1 to 8 query heads per KV head" % self.n_streams)
-        if not _dense_heads(q):
-            q = q.contiguous()
         if (k_new is None) != (v_new is None):
             raise ValueError("attend: k_new and v_new go together")
+        q = _dense_heads(q)
         kn = vn = None
         new_row = 0
         if k_new is not None:
             for t in (k_new, v_new):
-                if t.shape != (B, self.n_kv_heads, hd) or t.dtype != q.dtype or t.device != self.device:
+                if t.shape != (B, self.n_kv_heads, hd) or t.dtype is not q.dtype or t.device != self.device:
                     raise ValueError("attend: k_new and v_new must be [B, n_kv_heads, head_dim] in q's type")
-            if not (_dense_heads(k_new) and _dense_heads(v_new) and k_new.stride(0) == v_new.stride(0)):
+            k_new, v_new = _dense_heads(k_new), _dense_heads(v_new)
+            if k_new.stride(0) != v_new.stride(0):
                 k_new, v_new = k_new.contiguous(), v_new.contiguous()
             kn, vn, new_row = k_new.data_ptr(), v_new.data_ptr(), k_new.stride(0)
         lens_at = self._ints("lens", lens, B)
         if out is None:
-            out = torch.empty((B, n_q, hd), dtype=q.dtype, device=self.device)
-        elif out.shape != q.shape or out.dtype != q.dtype or out.device != self.device or not out.is_contiguous():
+            out = torch.empty(shape, dtype=q.dtype, device=self.device)
+        elif out.shape != shape or out.dtype is not q.dtype or out.device != self.device or not out.is_contiguous():
             raise ValueError("attend: out must be contiguous, with q's shape and type")
         if B == 0:
             return out
@@ -169,9 +172,9 @@ class KV4Cache:
         if need is None:
             need = self._scratch[(B, n_q, max_len)] = self._lib.talker_kv4_attend_scratch(self._ref, B, n_q, max_len)
         scratch = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
-        self._call(self._lib.talker_kv4_attend, "talker_kv4_attend", self._ref, layer, B, lens_at, max_len, n_q,
-                   1.0 / math.sqrt(hd) if scale is None else scale, q.data_ptr(), q.stride(0), kn, vn, new_row,
-                   _DTYPE[q.dtype], out.data_ptr(), scratch.data_ptr() if need else None, need)
+        launch(self.device.index, self._attend, "talker_kv4_attend", self._ref, layer, B, lens_at, max_len, n_q,
+               1.0 / math.sqrt(hd) if scale is None else scale, q.data_ptr(), q.stride(0), kn, vn, new_row,
+               dtype, out.data_ptr(), scratch.data_ptr() if need else None, need)
         return out
 
     def reorder(self, parents, lens, table_out=None, lens_out=None):
@@ -183,14 +186,20 @@ class KV4Cache:
         lens_at = self._ints("lens", lens, self.n_streams)
         if table_out is None:
             table_out = torch.empty_like(self.page_table)
+            table_at = table_out.data_ptr()
+        elif table_out.shape != self.page_table.shape:
+            raise ValueError("reorder: table_out must be [n_streams, pages_per_stream]")
+        else:
+            table_at = self._ints("table_out", table_out, None)
         if lens_out is None:
             lens_out = torch.empty_like(lens)
+            out_at = lens_out.data_ptr()
+        else:
+            out_at = self._ints("lens_out", lens_out, self.n_streams)
         if self.n_streams * self.pages_per_stream > self.n_pages:
             raise ValueError("reorder: needs pages_per_stream pages of the pool for every stream")
-        self._call(self._lib.talker_kv4_reorder, "talker_kv4_reorder", self._ref, at, R, lens_at,
-                   self._ints("table_out", table_out, self.page_table.numel()),
-                   self._ints("lens_out", lens_out, self.n_streams))
-        return self._with_table(table_out.view(self.page_table.shape)), lens_out
+        launch(self.device.index, self._reorder, "talker_kv4_reorder", self._ref, at, R, lens_at, table_at, out_at)
+        return self._with_table(table_out), lens_out
 
     def _with_table(self, page_table) -> "KV4Cache":
         """This cache under another page table of the same shape."""
@@ -211,5 +220,6 @@ class KV4Cache:
 
 
 def _dense_heads(t):
-    """Whether each row's heads follow one another."""
-    return t.numel() == 0 or (t.stride(2) == 1 and (t.stride(1) == t.shape[2] or t.shape[1] == 1))
+    """t with each row's heads behind one another, itself where they are."""
+    stride = t.stride()
+    return t if stride[2] == 1 and (stride[1] == t.shape[2] or t.shape[1] == 1) else t.contiguous()
