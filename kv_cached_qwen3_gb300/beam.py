@@ -31,8 +31,9 @@ def beam_select(logits, scores, ended=None, eos_id: int = -1):
     row = stride[1] if width > 1 else stride[0]
     if stride[2] != 1 or row < vocab or (n_seq > 1 and stride[0] != width * row):
         logits, row = logits.contiguous(), vocab
-    tokens, parents, done, best = torch.empty((4, n_seq, width), dtype=torch.int32, device=device).unbind(0)
-    best = best.view(torch.float32)
+    out = (n_seq, width)
+    tokens, parents, done = (torch.empty(out, dtype=torch.int32, device=device) for _ in range(3))
+    best = torch.empty(out, dtype=torch.float32, device=device)
     if n_seq == 0:
         return tokens, parents, best, done
     lib = load_library()
