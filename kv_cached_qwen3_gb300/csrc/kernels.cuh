@@ -258,8 +258,7 @@ cudaError_t launch_rmsnorm_bf16(float *x, int ld, const float *w, float eps, int
                                 cudaStream_t st, const CodeGather *gather = nullptr, int *status = nullptr,
                                 float *zero = nullptr, size_t zero_n = 0);
 // dense_kv (Q8_0 and Q4_0 storage only, else null): the rows' k / v also go to bf16 [2][rows][n_kv][hd].
-// Q4_0 storage: they go to f32 [2][rows][n_kv][hd] at rows_f32 (dense_kv may then be null), from where
-// they are quantized by another launch.
+// With rows_f32 (Q4_0 storage) they also go to f32 of the same layout.
 cudaError_t launch_qkv_post(const float *raw, int rows, int n_q, int n_kv, int hd, const float *q_norm,
                             const float *k_norm, const float2 *rope, float eps, float *q_out, const CacheView &cache,
                             int layer, const RowMap &rm, int *status, cudaStream_t st,

@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kRowThreads) k_kv4_rows(const Kv4Rows r, const
     float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (!READ && on) load8<T>(dense, vec, x);
     RowPlace p{nullptr, 0};
-    if (on) p = place_of(r, Tile::kBytes, s, l, h, is_v, (r.start != nullptr ? (long long)r.start[s] : 0) + r.start0 + i, sub == 0);
+    if (on) p = place_of(r, Tile::kBytes, s, l, h, is_v, (r.start != nullptr ? (long long)r.start[s] : 0) + i, sub == 0);
     if (READ) {
         values_of(load_codes<HD>(p.tile, p.prow, is_v, b, c), is_v, b, x);
         if (p.tile != nullptr) store8(dense, vec, x);
@@ -142,7 +142,7 @@ struct PageRows {
     int lo, hi;
 };
 __device__ __forceinline__ PageRows page_rows(const Kv4Rows &r, int s, int slot, long long &pos) {
-    const long long start = (r.start != nullptr ? (long long)r.start[s] : 0) + r.start0;
+    const long long start = r.start != nullptr ? (long long)r.start[s] : 0;
     const int n = r.count != nullptr ? min(r.count[s], r.T) : r.T;
     pos = (start >= 0 ? start / kPage : -((kPage - 1 - start) / kPage)) * kPage + (long long)slot * kPage;
     return {pos - start, (int)max(0ll, start - pos), (int)min((long long)kPage, start + n - pos)};
@@ -434,7 +434,7 @@ talker_status rows_call(const talker_kv4 *c, int layer0, int n_layers, int strea
     if (dtype != TALKER_DTYPE_F32 && dtype != TALKER_DTYPE_BF16) return TALKER_EINVAL;
     if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) % (dtype == TALKER_DTYPE_F32 ? 4 : 2))
         return TALKER_EINVAL;
-    const Kv4Rows r{*c, layer0, n_layers, stream0, n_streams, start, count, T, k, v, *st, 0};
+    const Kv4Rows r{*c, layer0, n_layers, stream0, n_streams, start, count, T, k, v, *st};
     return status_of(launch_kv4_rows(r, dtype, read, static_cast<cudaStream_t>(cuda_stream)));
 }
 

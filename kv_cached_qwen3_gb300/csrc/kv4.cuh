@@ -19,6 +19,7 @@ struct Kv4Tile {
     static constexpr int kBytes = kScales + talker_dev::kPage * NB * 2;
 };
 constexpr int kv4_tile_bytes(int hd) { return hd * 36; }
+constexpr int kPage4 = talker_dev::kPage;
 
 // Two f32 values in one 64-bit register, each instruction computing both.
 struct F2 {
@@ -97,6 +98,34 @@ __device__ __forceinline__ uint32_t q4_codes8(const float (&x)[8], unsigned shor
     return w;
 }
 
+// The code of x in a block with M = |m| > 0, s = -16 sign(m), both times 2^60 if m is tiny, id = 0.5 / M.
+__device__ __forceinline__ int q4_code(float x, float M, float s, float id) {
+    constexpr float kRound = 12582912.f;
+    const float z = x * s, k = (fmaf(z, id, 8.5f) + kRound) - kRound;
+    return min((int)k - (fmaf(fmaf(-2.f, k, 17.f), M, z) < 0.f ? 1 : 0), 15);
+}
+
+// Quantizes and stores block b of row `row` of a tile, held one dim per lane of a warp.
+__device__ __forceinline__ void q4_store_block(unsigned char *tile, int hd, int row, bool is_v, int b, float x, int lane) {
+    const int nb = hd / 32;
+    const uint32_t bits = __float_as_uint(x) & 0x7fffffffu, top = __reduce_max_sync(0xffffffffu, bits);
+    const bool bad = top >= 0x7f800000u;
+    float m = __shfl_sync(0xffffffffu, x, __ffs(__ballot_sync(0xffffffffu, bits == top)) - 1);
+    m = fminf(fmaxf(m, -524032.f), 524032.f);
+    int n = 8;
+    if (!bad && m != 0.f) {
+        const float up = fabsf(m) < 1e-30f ? 1152921504606846976.f : 1.f, M = fabsf(m) * up;   // 2^60
+        n = q4_code(fminf(fmaxf(x, -524032.f), 524032.f), M, m > 0.f ? -16.f * up : 16.f * up, 0.5f / M);
+    }
+    const int pair = n | __shfl_down_sync(0xffffffffu, n, 1) << 4;
+    if (lane % 2 == 0)   // dims lane and lane + 1 of the block
+        tile[row * (hd / 2) + (is_v ? lane / 4 * 2 * nb + 2 * b + lane % 4 / 2 : lane / 8 * 4 * nb + 4 * b + lane % 8 / 2)] =
+            (unsigned char)pair;
+    if (lane == 0)
+        *reinterpret_cast<unsigned short *>(tile + kPage4 * (hd / 2) + (row * nb + b) * 2) =
+            bad ? 0x7e00 : __half_as_ushort(__float2half_rn(m * -0.125f));
+}
+
 // The 32-bit word of a row that lane (b, c), four lanes to a block, writes or reads. K: its own
 // eight codes. V: the codes of two neighbouring blocks for group g = 2 c + b % 2, which lanes b and
 // b ^ 1 (lane ^ 4) exchange: v_word turns a lane's codes into its word, and back.
@@ -123,7 +152,6 @@ struct Kv4Rows {
     int T;
     void *k, *v;
     talker_kv4_strides st;
-    int start0;   // added to start
 };
 bool kv4_cache_ok(const talker_kv4 *c);   // the host-side checks of a caller-owned cache
 cudaError_t launch_kv4_rows(const Kv4Rows &r, int dtype, bool read, cudaStream_t s);

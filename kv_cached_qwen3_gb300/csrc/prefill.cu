@@ -19,6 +19,7 @@
 
 #include "common.cuh"
 #include "kernels.cuh"
+#include "kv4.cuh"
 
 using namespace talker_dev;
 
@@ -192,20 +193,27 @@ __global__ void k_qkv_post(const float *raw, int rows, int n_q, int n_kv, int hd
     }
     const int kvh = is_k ? h - n_q : h - n_q - n_kv;
     const size_t dense = ((size_t)(is_k ? 0 : rows) * n_kv + (size_t)r * n_kv + kvh) * hd;
+    const int page = cache.page_table[(size_t)stream * cache.pages_per_stream + pos / kPage];
     if (cache.kv_q4) {
+        unsigned char *t = static_cast<unsigned char *>(is_k ? cache.k : cache.v) + (size_t)page * cache.page_elems +
+                           (size_t)(layer * n_kv + kvh) * kv4_tile_bytes(hd);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
+            if (32 * j >= half) continue;   // each register of the warp is one block of 32 dims
+            q4_store_block(t, hd, pos % kPage, !is_k, j, a[j], lane);
+            q4_store_block(t, hd, pos % kPage, !is_k, j + half / 32, b[j], lane);
             const int i = lane + 32 * j;
-            if (i >= half) continue;
-            rows_f32[dense + i] = a[j];
-            rows_f32[dense + i + half] = b[j];
-            if (dense_kv == nullptr) continue;
-            dense_kv[dense + i] = __float2bfloat16_rn(a[j]);
-            dense_kv[dense + i + half] = __float2bfloat16_rn(b[j]);
+            if (rows_f32 != nullptr) {
+                rows_f32[dense + i] = a[j];
+                rows_f32[dense + i + half] = b[j];
+            }
+            if (dense_kv != nullptr) {
+                dense_kv[dense + i] = __float2bfloat16_rn(a[j]);
+                dense_kv[dense + i + half] = __float2bfloat16_rn(b[j]);
+            }
         }
         return;
     }
-    const int page = cache.page_table[(size_t)stream * cache.pages_per_stream + pos / kPage];
     if (cache.kv_q8) {
         // Q8_0 tile of (page, layer, head): [64][hd] codes, then [64][hd/32] fp16 scales; each valid
         // register of the warp holds one block of 32 dims (lane = dim % 32, hd is 64 or 128)
@@ -345,7 +353,7 @@ cudaError_t launch_qkv_post(const float *raw, int rows, int n_q, int n_kv, int h
                             const float *k_norm, const float2 *rope, float eps, float *q_out, const CacheView &cache,
                             int layer, const RowMap &rm, int *status, cudaStream_t st, __nv_bfloat16 *dense_kv,
                             float *rows_f32) {
-    if ((cache.kv_q8 && dense_kv == nullptr) || (cache.kv_q4 && rows_f32 == nullptr)) return cudaErrorInvalidValue;
+    if ((cache.kv_q8 && dense_kv == nullptr) || (cache.kv_q4 && dense_kv == nullptr && rows_f32 == nullptr)) return cudaErrorInvalidValue;
     const long long items = (long long)rows * (n_q + 2 * n_kv);
     const int per_block = 8;
     if (!cache.kv_q8 && !cache.kv_q4 && hd == 128)

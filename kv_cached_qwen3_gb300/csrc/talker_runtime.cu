@@ -94,7 +94,7 @@ struct talker {
     int *d_reorder = nullptr;            // the page table and lengths that a reordering writes
     bool pages_shared = false;           // streams may share full pages (talker_kv_reorder)
     float *q4_ws = nullptr;              // Q4_0 storage: parts of rows that several CTAs attend
-    float *kv_rows = nullptr;            // Q4_0 storage: a call's own k / v rows, f32 [2][rows][n_kv][hd]
+    float *kv_rows = nullptr;            // Q4_0 storage: a step's own k / v rows, f32 [2][rows][n_kv][hd]
     float2 *d_rope = nullptr;
     std::vector<int> len;
     // activations, sized for cap_rows rows
@@ -158,7 +158,7 @@ void free_ptr(void *p) {
 
 void free_workspaces(talker *t) {
     float **fl[] = {&t->x, &t->raw, &t->q, &t->attn, &t->act, &t->attn_ws, &t->head_val, &t->frame_logits,
-                    &t->x2, &t->kv_rows};
+                    &t->x2};
     for (auto pp : fl) {
         free_ptr(*pp);
         *pp = nullptr;
@@ -193,9 +193,10 @@ void free_cache(talker *t) {
     free_ptr(t->d_rope);
     free_ptr(t->d_reorder);
     free_ptr(t->q4_ws);
+    free_ptr(t->kv_rows);
     t->kpool = t->vpool = nullptr;
     t->d_pt = t->d_len = t->d_reorder = nullptr;
-    t->q4_ws = nullptr;
+    t->q4_ws = t->kv_rows = nullptr;
     t->pages_shared = false;
     t->d_rope = nullptr;
     t->kv_maps_ok = false;
@@ -268,11 +269,6 @@ talker_status ensure_capacity(talker *t, int rows, int splits) {
         const int cap = std::max(rows, 16);
         float **fl[] = {&t->x, &t->raw, &t->q, &t->attn, &t->act, &t->x2};
         const int widths[] = {t->H, t->qkv_n, t->qd, t->qd, t->I, t->H};
-        if (t->kv_q4) {
-            free_ptr(t->kv_rows);
-            t->kv_rows = nullptr;
-            TRY_CUDA(cudaMalloc(&t->kv_rows, (size_t)2 * cap * t->kvd * sizeof(float)));
-        }
         for (int i = 0; i < 6; ++i) {
             free_ptr(*fl[i]);
             *fl[i] = nullptr;
@@ -447,21 +443,8 @@ talker_kv4 kv4_view(const talker *t) {
     return {t->kpool, t->vpool, t->d_pt, t->d_status, t->n_streams * t->pps, t->n_streams, t->pps, t->c.n_layers, t->nkv, t->hd};
 }
 
-// Q4_0 storage: the call's rows (kv_rows, of n_streams streams of T rows) quantized into the cache at
-// start[s] + start0.
-talker_status enqueue_q4_write(talker *t, cudaStream_t st, int layer, int stream0, int n_streams, int T, const int *start,
-                               int start0, int *nk) {
-    const size_t rows = (size_t)n_streams * T;
-    const talker_kv4_strides strides{0, (int64_t)T * t->kvd, t->kvd, t->hd};
-    const Kv4Rows r{kv4_view(t), layer, 1, stream0, n_streams, start, nullptr, T, t->kv_rows, t->kv_rows + rows * t->kvd,
-                    strides, start0};
-    TRY_CUDA(launch_kv4_rows(r, TALKER_DTYPE_F32, false, st));
-    ++*nk;
-    return TALKER_OK;
-}
-
-// Q4_0 storage, decode: the heads finished from the raw projections, attention over the cached rows and
-// the step's own (exact, from kv_rows), which is then quantized into the cache.
+// Q4_0 storage, decode: the heads finished from the raw projections and the step's row quantized into the
+// cache; attention over the cached rows before it and the step's own (exact, from kv_rows).
 talker_status enqueue_q4_decode(talker *t, cudaStream_t st, int B, int layer, const LayerDev &d, const RowMap &rm, int grid,
                                 void *out, bool out_bf16, int *nk) {
     TRY_CUDA(launch_qkv_post(t->raw, B, t->nq, t->nkv, t->hd, d.q_norm, d.k_norm, t->d_rope, t->c.rms_eps, t->q, cache_view(t),
@@ -470,7 +453,7 @@ talker_status enqueue_q4_decode(talker *t, cudaStream_t st, int B, int layer, co
                       out, 1.0f / sqrtf((float)t->hd), grid, t->attn_cluster, t->q4_ws};
     TRY_CUDA(launch_kv4_attend(a, 0, out_bf16, st));
     *nk += t->attn_cluster ? 2 : 3;
-    return enqueue_q4_write(t, st, layer, 0, B, 1, t->d_len, 0, nk);
+    return TALKER_OK;
 }
 
 // Enqueue the whole forward for `rows` rows on the GEMV kernels: per layer QKV (+QK-norm,
@@ -706,12 +689,8 @@ talker_status enqueue_tc(talker *t, cudaStream_t st, int T, const RowMap &rm, co
         TRY(tc_gemm(t, st, t->hb, T, t->H, d.qkv, t->qkv_n, t->raw, t->qkv_n, false, &nk));
         if (rm.mode != 0) {   // prefill rows; decode rows are finished inside the attention kernel
             TRY_CUDA(launch_qkv_post(t->raw, T, t->nq, t->nkv, t->hd, d.q_norm, d.k_norm, t->d_rope, t->c.rms_eps,
-                                     t->q, cv, l, rm, t->d_status, st, t->kv_quant ? t->kv_dense : nullptr, t->kv_rows));
+                                     t->q, cv, l, rm, t->d_status, st, t->kv_quant ? t->kv_dense : nullptr));
             ++nk;
-            if (t->kv_q4) {
-                const int per = rm.rows_per_stream > 0 ? rm.rows_per_stream : T;
-                TRY(enqueue_q4_write(t, st, l, rm.stream0, T / per, per, nullptr, rm.pos0, &nk));
-            }
         }
         AttnParams a{};
         a.q = t->q;
@@ -1030,7 +1009,10 @@ talker_status talker_kv_init_batched(talker_t *t, int n_streams, int max_seq_len
     TRY_CUDA(cudaMalloc(&t->d_pt, n_pages * sizeof(int)));
     TRY_CUDA(cudaMemcpy(t->d_pt, pt.data(), n_pages * sizeof(int), cudaMemcpyHostToDevice));
     TRY_CUDA(cudaMalloc(&t->d_reorder, (n_pages + n_streams) * sizeof(int)));
-    if (t->kv_q4) TRY_CUDA(cudaMalloc(&t->q4_ws, kv4_attend_scratch({kv4_attend_full_grid(t->n_sm), 0}, t->hd)));
+    if (t->kv_q4) {
+        TRY_CUDA(cudaMalloc(&t->q4_ws, kv4_attend_scratch({kv4_attend_full_grid(t->n_sm), 0}, t->hd)));
+        TRY_CUDA(cudaMalloc(&t->kv_rows, (size_t)2 * n_streams * t->kvd * sizeof(float)));
+    }
     TRY_CUDA(cudaMalloc(&t->d_len, n_streams * sizeof(int)));
     TRY_CUDA(cudaMemsetAsync(t->d_len, 0, n_streams * sizeof(int), t->st));
     // RoPE table: angle p * theta^(-2i/hd) evaluated in double on the host, stored as f32 (cos, sin)
@@ -1196,7 +1178,7 @@ talker_status talker_decode(talker_t *t, const float *emb, int B, float *logits,
 static talker_status kv_copy(const talker *t, int stream, void *k, void *v, int len, bool to_cache) {
     if (!t->kv_q4 || len == 0) return from_cuda(launch_kv_copy(cache_view(t), stream, k, v, len, to_cache, t->st));
     const talker_kv4_strides strides{(int64_t)t->nkv * len * t->hd, 0, t->hd, (int64_t)len * t->hd};
-    const Kv4Rows r{kv4_view(t), 0, t->c.n_layers, stream, 1, nullptr, nullptr, len, k, v, strides, 0};
+    const Kv4Rows r{kv4_view(t), 0, t->c.n_layers, stream, 1, nullptr, nullptr, len, k, v, strides};
     return from_cuda(launch_kv4_rows(r, TALKER_DTYPE_F32, !to_cache, t->st));
 }
 
