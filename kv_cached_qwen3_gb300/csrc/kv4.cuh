@@ -177,7 +177,9 @@ int kv4_attend_full_grid(int n_sm);   // the largest such grid
 size_t kv4_attend_scratch(const Kv4AttendShape &p, int head_dim);
 cudaError_t prepare_kv4_attend();   // shared-memory limits, on the current device
 int kv4_multiprocessors();          // of the current device, prepared as above (0: an error)
-cudaError_t launch_kv4_attend(const Kv4Attend &a, int in_bf16, int out_bf16, cudaStream_t s);
+// pdl: starts while the kernel before it drains, which must not write lengths, page numbers or rows below
+// the lengths.
+cudaError_t launch_kv4_attend(const Kv4Attend &a, int in_bf16, int out_bf16, bool pdl, cudaStream_t s);
 
 // Streams reordered by sharing pages (talker_kv4_reorder), for any page layout of n_tiles tiles a
 // pool page, each of 64 code rows of row_bytes and, behind them, 64 rows of scale_bytes.

@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
     __shared__ float wm[kWarps + 1][kMaxG], wl[kWarps + 1][kMaxG];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     const int G = a.n_q / a.c.n_kv_heads;
-    pdl_launch_dependents();
+    if (!a.one_unit) pdl_launch_dependents();   // (the joining kernel; another would only take room)
     unsigned char *ring = ring_all + warp * kSlots * Tile::kBytes;
     if (lane == 0) {
         for (int i = 0; i < kSlots; ++i) mbar_init(&bars[warp][i], 1);
@@ -295,6 +295,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
         if (lane == 0 && n_it > 1) issue(after(after(slot)), a.c.k, page1, g);
     };
     open(b0, (int)((x_begin - before) / nu0), len0, nu0, (int)((x_begin - before) % nu0), x_end - x_begin);
+    pdl_wait();   // before it: lengths, page numbers and cached rows, which the kernel before does not write
 
     for (bool begins = true;; begins = false) {
         if (at.len < 0 && threadIdx.x == 0 && a.c.status != nullptr) atomicOr(a.c.status, ST_BAD_POSITION);
@@ -697,30 +698,39 @@ __global__ void __launch_bounds__(kThreads) k_kv4_combine(const Kv4Attend a, con
 }
 
 template <int HD, typename TI, typename TO>
-cudaError_t launch_t(const Kv4Attend &a, cudaStream_t s) {
+cudaError_t launch_t(const Kv4Attend &a, bool pdl, cudaStream_t s) {
     const bool wide = a.n_q / a.c.n_kv_heads > 4 && sizeof(TO) == 4;
     void (*kernel)(Kv4Attend) = k_kv4_attend<HD, false, TI, TO>;
     if constexpr (sizeof(TO) == 4) kernel = wide ? k_kv4_attend<HD, true, TI, TO> : kernel;
-    kernel<<<a.grid, kWarps * 32, attend_smem(HD), s>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || a.one_unit) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.n_q, a.B);
-    const bool many = a.grid >= 8ll * a.B * a.c.n_kv_heads;   // parts per row
-    cfg.blockDim = dim3(many ? kManyThreads : kFewThreads);
-    cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    cudaError_t e;
+    if (pdl) {
+        cfg.gridDim = dim3(a.grid);
+        cfg.blockDim = dim3(kWarps * 32);
+        cfg.dynamicSmemBytes = attend_smem(HD);
+        e = cudaLaunchKernelEx(&cfg, kernel, a);
+        cfg.dynamicSmemBytes = 0;
+    } else {
+        kernel<<<a.grid, kWarps * 32, attend_smem(HD), s>>>(a);
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess || a.one_unit) return e;
+    cfg.gridDim = dim3(a.n_q, a.B);
+    const bool many = a.grid >= 8ll * a.B * a.c.n_kv_heads;   // parts per row
+    cfg.blockDim = dim3(many ? kManyThreads : kFewThreads);
     return cudaLaunchKernelEx(&cfg, many ? k_kv4_combine<HD, TO, kManyThreads> : k_kv4_combine<HD, TO, kFewThreads>, a, a.grid);
 }
 
 template <int HD>
-cudaError_t launch_hd(const Kv4Attend &a, int in_bf16, int out_bf16, cudaStream_t s) {
-    if (in_bf16) return out_bf16 ? launch_t<HD, __nv_bfloat16, __nv_bfloat16>(a, s) : cudaErrorInvalidValue;
-    return out_bf16 ? launch_t<HD, float, __nv_bfloat16>(a, s) : launch_t<HD, float, float>(a, s);
+cudaError_t launch_hd(const Kv4Attend &a, int in_bf16, int out_bf16, bool pdl, cudaStream_t s) {
+    if (in_bf16) return out_bf16 ? launch_t<HD, __nv_bfloat16, __nv_bfloat16>(a, pdl, s) : cudaErrorInvalidValue;
+    return out_bf16 ? launch_t<HD, float, __nv_bfloat16>(a, pdl, s) : launch_t<HD, float, float>(a, pdl, s);
 }
 
 }  // namespace
@@ -779,9 +789,9 @@ int kv4_multiprocessors() {
     return n;
 }
 
-cudaError_t launch_kv4_attend(const Kv4Attend &a, int in_bf16, int out_bf16, cudaStream_t s) {
+cudaError_t launch_kv4_attend(const Kv4Attend &a, int in_bf16, int out_bf16, bool pdl, cudaStream_t s) {
     if (a.B == 0) return cudaSuccess;
-    return a.c.head_dim == 128 ? launch_hd<128>(a, in_bf16, out_bf16, s) : launch_hd<64>(a, in_bf16, out_bf16, s);
+    return a.c.head_dim == 128 ? launch_hd<128>(a, in_bf16, out_bf16, pdl, s) : launch_hd<64>(a, in_bf16, out_bf16, pdl, s);
 }
 
 }  // namespace talker_k
@@ -826,7 +836,7 @@ talker_status talker_kv4_attend(const talker_kv4 *c, int layer, int B, const int
     const Kv4Attend a{*c, layer, B, n_q_heads, lens, q, k_new, v_new, q_row, new_row, out, scale, shape.grid, shape.one_unit,
                       static_cast<float *>(scratch)};
     const int bf16 = dtype == TALKER_DTYPE_BF16;
-    if (launch_kv4_attend(a, bf16, bf16, static_cast<cudaStream_t>(cuda_stream)) != cudaSuccess) {
+    if (launch_kv4_attend(a, bf16, bf16, false, static_cast<cudaStream_t>(cuda_stream)) != cudaSuccess) {
         cudaGetLastError();
         return TALKER_ECUDA;
     }

@@ -451,7 +451,7 @@ talker_status enqueue_q4_decode(talker *t, cudaStream_t st, int B, int layer, co
                              layer, rm, t->d_status, st, nullptr, t->kv_rows));
     const Kv4Attend a{kv4_view(t), layer, B, t->nq, t->d_len, t->q, t->kv_rows, t->kv_rows + (size_t)B * t->kvd, t->qd, t->kvd,
                       out, 1.0f / sqrtf((float)t->hd), grid, t->attn_cluster, t->q4_ws};
-    TRY_CUDA(launch_kv4_attend(a, 0, out_bf16, st));
+    TRY_CUDA(launch_kv4_attend(a, 0, out_bf16, true, st));
     *nk += t->attn_cluster ? 2 : 3;
     return TALKER_OK;
 }
