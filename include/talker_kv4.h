@@ -88,9 +88,11 @@ talker_status talker_kv4_read(const talker_kv4 *c, int layer0, int n_layers, int
  * one more row that is attended as given (the step's own row, before or without
  * being written). q [B][n_q_heads][head_dim] and k_new, v_new [B][n_kv_heads]
  * [head_dim] are dense per head, with row strides q_row and new_row in
- * elements; out is contiguous; all are dtype (F32 or BF16). The arithmetic is
- * f32 throughout: the codes are exact in fp16 and q and the probabilities enter
- * the tensor cores as two fp16 parts, so the result is rounded only once.
+ * elements; out is contiguous; all are dtype (F32 or BF16). Scores, maxima and
+ * sums are f32, and codes are exact. With F32, q and the probabilities enter the
+ * tensor cores as two fp16 parts (22 bits). With BF16 as one: q exactly (values
+ * below 2^-27 of a head's largest lose bits), probabilities rounded to 2^-12 and
+ * again times their value's scale, before the result's own 2^-9.
  * A stream without rows gives zeros. A length outside the stream's pages sets
  * status 1 << 0 and gives zeros; keys of a page whose number is out of range
  * are not attended (status 1 << 3).
@@ -138,7 +140,7 @@ talker_status talker_kv4_reorder(const talker_kv4 *c, const int32_t *parents, in
  * [n_seq][width]: tokens, parents (the row seq * width + w that is continued),
  * scores_out, and ended_out (may be NULL): the parent had ended, or the token is
  * eos_id. Outputs must not overlap the inputs. width <= 32, width <= vocab,
- * n_seq * width < 2^26.
+ * vocab <= 2^30, n_seq * width < 2^26.
  * scratch: talker_beam_scratch bytes, 16-byte aligned (may be NULL when that is 0).
  * Errors: EINVAL, ECUDA. */
 size_t talker_beam_scratch(int n_seq, int width, int vocab);

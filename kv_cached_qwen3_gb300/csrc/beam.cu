@@ -415,7 +415,7 @@ Shape shape_of(int n_seq, int width, int vocab) {
 size_t align16(size_t n) { return (n + 15) / 16 * 16; }
 
 bool sizes_ok(int n_seq, int width, int vocab) {
-    return n_seq >= 0 && width >= 1 && width <= kMaxWidth && vocab >= width && (long long)n_seq * width <= 0x7fffffffll / kMaxChunks;
+    return n_seq >= 0 && width >= 1 && width <= kMaxWidth && vocab >= width && vocab <= 1 << 30 && (long long)n_seq * width <= 0x7fffffffll / kMaxChunks;
 }
 
 }  // namespace

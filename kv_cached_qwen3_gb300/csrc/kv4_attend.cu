@@ -36,6 +36,12 @@ __device__ __forceinline__ void mma16816_new(float (&d)[4], const uint32_t (&a)[
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
+// The same over 8 instead of 16.
+__device__ __forceinline__ void mma1688_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(b), "f"(0.f));
+}
 // (lo, hi) as an fp16 pair, rounded towards zero
 __device__ __forceinline__ uint32_t pack_rz(float lo, float hi) {
     uint32_t r;
@@ -305,7 +311,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
         const bool q_vec = (reinterpret_cast<uintptr_t>(a.q) & 15u) == 0 && a.q_row * sizeof(TI) % 16 == 0;
         const float cs = a.scale * kLog2e;
         uint32_t qf[NB][2][2], ql[NB][2][2];       // (ql: WIDE only)
-        uint32_t qc[2];                            // -8 sum(q) of the blocks, in two parts, times 2^kCorrBits
+        uint32_t qc;                               // -8 sum(q) of two blocks, times 2^kCorrBits: lanes c < H have a
+                                                   // first part, lanes c - H its rest
         F2 fs;                                     // from these units to scores in base 2, of this lane's columns 2 c, 2 c + 1
         {
             float x[NB][8], top = 0.f;
@@ -352,14 +359,14 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
                 corr[nb] = sum * (-8.f / 16777216.f * (1 << kCorrBits));
             }
-            qc[0] = qc[1] = 0;
+            qc = 0;
 #pragma unroll
-            for (int i = 0; i < NB / 2; ++i)
-                if (c == i) {
-                    const __half h0 = __float2half_rn(corr[2 * i]), h1 = __float2half_rn(corr[2 * i + 1]);
-                    qc[0] = pack_half(h0, h1);
-                    qc[1] = pack_half(__float2half_rn(corr[2 * i] - __half2float(h0)), __float2half_rn(corr[2 * i + 1] - __half2float(h1)));
-                }
+            for (int i = 0; i < NB / 2; ++i) {
+                const __half h0 = __float2half_rn(corr[2 * i]), h1 = __float2half_rn(corr[2 * i + 1]);
+                if (c == i) qc = pack_half(h0, h1);
+                if (c == i + NB / 2)
+                    qc = pack_half(__float2half_rn(corr[2 * i] - __half2float(h0)), __float2half_rn(corr[2 * i + 1] - __half2float(h1)));
+            }
         }
 
         float m0 = -INFINITY, m1 = -INFINITY;     // references of the exponents of this lane's columns
@@ -398,12 +405,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
                     d1.load(kt + Tile::kScales + (16 * i + 8 + key_r) * NB * 2);
                     F2 s0, s1;
                     {
-                        uint32_t e[4];   // scales of blocks 2 c and 2 c + 1 (columns past the blocks meet zeros)
-                        e[0] = lds_u1(kt + Tile::kScales + (16 * i + key_r) * NB * 2 + 4 * (c & (H - 1)));
-                        e[1] = lds_u1(kt + Tile::kScales + (16 * i + 8 + key_r) * NB * 2 + 4 * (c & (H - 1)));
-                        e[2] = e[0], e[3] = e[1];
+                        // scales of blocks 2 (c % H) and the next (columns past the parts meet zeros)
                         float acc[4];
-                        mma16816_new(acc, e, qc[0], qc[1]);
+                        mma1688_new(acc, lds_u1(kt + Tile::kScales + (16 * i + key_r) * NB * 2 + 4 * (c & (H - 1))),
+                                    lds_u1(kt + Tile::kScales + (16 * i + 8 + key_r) * NB * 2 + 4 * (c & (H - 1))), qc);
                         const F2 down = f2(1.f / (1 << kCorrBits), 1.f / (1 << kCorrBits));
                         s0 = f2(acc[0], acc[1]) * down, s1 = f2(acc[2], acc[3]) * down;
                     }

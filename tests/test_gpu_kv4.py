@@ -283,6 +283,35 @@ def test_attend_bad_lengths_and_pages(kv4):
     assert np.abs(host(out)[2] - want).max() < 1e-4
 
 
+def test_attend_where_streams_share_pages(kv4):
+    """One page named by several streams and twice by one, as after reordering or for a common prompt."""
+    c, K, V = filled(kv4, 3, 128, 2, 128, 15, shuffle=False)
+    c.page_table.copy_(torch.tensor([[0, 1], [0, 3], [4, 4]], dtype=torch.int32))
+    K = np.stack([K[0], np.concatenate([K[0, :64], K[1, 64:]]), np.concatenate([K[2, :64], K[2, :64]])])
+    V = np.stack([V[0], np.concatenate([V[0, :64], V[1, 64:]]), np.concatenate([V[2, :64], V[2, :64]])])
+    check_attend(kv4, c, K, V, [128, 100, 127], 2, 2, 128, torch.float32, True)
+    assert c.sync_status() == 0
+
+
+def test_attend_strided_queries_and_given_output(kv4):
+    c, K, V = filled(kv4, 2, 90, 2, 64, 16)
+    lens = torch.tensor([90, 33], dtype=torch.int32).cuda()
+    wide = rnd(3, 2, 6, 2, 64)
+    base = c.attend(0, wide[:, :, 0].contiguous(), lens)
+    out = torch.full((2, 6, 64), 5.0, device="cuda")
+    assert c.attend(0, wide[:, :, 0], lens, out=out) is out and torch.equal(out, base)
+    off = torch.empty(2 * 6 * 64 + 1, device="cuda")[1:].view(2, 6, 64)     # off 16-byte boundaries
+    off.copy_(wide[:, :, 0])
+    assert torch.equal(c.attend(0, off, lens), base)
+    assert c.attend(0, wide[:0, :, 0], lens[:0]).shape == (0, 6, 64)
+    neg = c.attend(0, wide[:, :, 0], lens, scale=-0.3)                       # a negative scale is a scale
+    for b in range(2):
+        n = int(lens[b])
+        want = ref.attend(host(wide[:, :, 0])[b], K[b, :n], V[b, :n], -0.3)
+        tol = attend_tolerance(host(wide[:, :, 0])[b], K[b, :n], V[b, :n], 0.3, torch.float32, want)
+        assert (np.abs(host(neg)[b] - want) <= tol).all()
+
+
 # ------------------------------------------------------------------ selection
 
 def check_select(logits, scores, ended=None, eos=-1):
@@ -400,6 +429,27 @@ def test_reorder(kv4, n, lens, R):
         assert same(contents(c, at), before)
         at = at + room
     assert c.sync_status() == 0
+
+
+@pytest.mark.parametrize("cut", [[150, 70, 64, 10], [0, 0, 0, 0], [130, 130, 130, 5]])
+def test_reorder_after_streams_were_cut(kv4, cut):
+    """Streams that share pages and are cut inside them get pages of their own again, all at once."""
+    c = kv4.KV4Cache(4, 192, 2, 2, 64)
+    k, v = rnd(1, 2, 4, 160, 2, 64), rnd(2, 2, 4, 160, 2, 64)
+    c.write(k, v)
+    at = torch.full((4,), 160, dtype=torch.int32).cuda()
+    c, at = c.reorder(torch.tensor([2, 2, 2, 1], dtype=torch.int32).cuda(), at)
+    old = contents(c, at)
+    at = torch.minimum(at, torch.tensor(cut, dtype=torch.int32).cuda())
+    want = [tuple(x[:, :n] for x in old[i]) for i, n in enumerate(cut)]
+    d, new = c.reorder(torch.zeros(0, dtype=torch.int32).cuda(), at)      # R = 0: every stream stays
+    assert new.tolist() == cut
+    writable_pages_are_owned(d, new)
+    assert same(contents(d, new), want)
+    row = [rnd(20 + s, 2, 4, 30, 2, 64) for s in (0, 1)]
+    d.write(*row, start=new)
+    assert same(contents(d, new), want)
+    assert d.sync_status() == 0
 
 
 def test_reorder_reports_bad_values(kv4):

@@ -100,7 +100,7 @@ def test_beam_refusals(lib):
                dict(V=200000, n=need - 1), dict(x=4098)):
         assert call(**kw) == 1, kw
     assert call(S=0) == 0
-    for bad in ((-1, 4, 100), (1, 0, 100), (1, 33, 100), (1, 4, 3), (1 << 30, 4, 100)):
+    for bad in ((-1, 4, 100), (1, 0, 100), (1, 33, 100), (1, 4, 3), (1 << 30, 4, 100), (1, 4, (1 << 30) + 1)):
         assert lib.talker_beam_scratch(*bad) == 0
 
 
