@@ -215,18 +215,18 @@ __device__ __forceinline__ int stream_of(const Kv4Attend &a, long long x, long l
 // scratch: a CTA has at most two such parts, one that begins its range and one that ends it.
 //
 // A lane is (r = lane / 4, c = lane % 4). Scores of 16 keys, S[keys x 8] = K Q^T by m16n8k16 per
-// block of 32 dims. K codes enter as they are (nibbles and bytes, below), q is scaled by a power of
-// two so that its largest value lies in [2^13, 2^14). The results times the key's scales are added
-// in f32; the codes' offset, -8 sum(q) of each block times its scale, is one more MMA, over blocks.
+// block of 32 dims; q is scaled by a power of two so that its largest value lies in [2^13, 2^14). The
+// results times the key's scales are added in f32.
 // Values, O^T[dims x 8] += V^T P^T, P being the probabilities times the value's scale of each block,
 // transposed between lanes as fp16. The exponents' reference m keeps P in fp16's range: it follows
 // the largest score plus log2 of the largest value scale, and O and l are rescaled when P would
 // pass 2^14, to below 2^9. An accumulator's columns are its lane's heads throughout.
-// f32 results (PREC): q and P in two fp16 parts (22 bits), for up to 4 query heads in columns h and
-// h + 4 of one MMA, above that (WIDE) by two MMAs; V codes centred in fp16. bf16 results: one part
-// of q (exact where q is bf16), of p and of P, each 2^-12 of a term at most, an eighth of half a
-// step of the result; V codes as they are, and one more MMA (A = -8 everywhere) takes off what they
-// are too large by, 16 keys at a time: a sum over all keys would cancel too much in f32.
+// f32 results (PREC): codes centred in fp16, q and P in two fp16 parts (22 bits), for up to 4 query
+// heads in columns h and h + 4 of one MMA, above that (WIDE) by two MMAs. bf16 results: one part of
+// q (exact where q is bf16), of p and of P, each 2^-12 of a term at most, an eighth of half a step of
+// the result. Codes as they are, times 2^-24; the scores' offset, -8 sum(q) of each block times its
+// scale, is one more MMA over blocks, and one more (A = -8 everywhere) takes off what P V is too large
+// by, 16 keys at a time. (f32 results would lose bits to either: 2e-6 instead of 5e-7 of the result.)
 template <int HD, bool WIDE, typename TI, typename TO>
 __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Attend a) {
     using Tile = Kv4Tile<HD>;
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
             const int e = min((int)(__float_as_uint(top) >> 23), 254);        // biased exponent of the largest
             const int up = min(13 + 127 - e, 120);                            // 2^up brings it to [2^13, 2^14)
             const float qs = __uint_as_float((uint32_t)(up + 127) << 23);
-            const float unit = cs * exp2f((float)(24 - up));
+            const float unit = cs * exp2f((float)((PREC ? 0 : 24) - up));
             fs = f2(__shfl_sync(0xffffffffu, unit, 8 * c), __shfl_sync(0xffffffffu, unit, 8 * c + 4));
             float corr[NB];
 #pragma unroll
@@ -404,7 +404,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
                     d0.load(kt + Tile::kScales + (16 * i + key_r) * NB * 2);
                     d1.load(kt + Tile::kScales + (16 * i + 8 + key_r) * NB * 2);
                     F2 s0, s1;
-                    {
+                    if (PREC) {
+                        s0 = s1 = f2(0.f, 0.f);
+                    } else {
                         // scales of blocks 2 (c % H) and the next (columns past the parts meet zeros)
                         float acc[4];
                         mma1688_new(acc, lds_u1(kt + Tile::kScales + (16 * i + key_r) * NB * 2 + 4 * (c & (H - 1))),
@@ -418,7 +420,11 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
                             const uint32_t w0 = t ? bytes13(k0.w[nb]) : bytes02(k0.w[nb]), w1 = t ? bytes13(k1.w[nb]) : bytes02(k1.w[nb]);
-                            const uint32_t codes[4] = {nibbles(w0), nibbles(w1), w0, w1};
+                            uint32_t codes[4] = {nibbles(w0), nibbles(w1), w0, w1};
+                            if (PREC) {
+                                codes[0] = centred(codes[0], kMidNibble), codes[1] = centred(codes[1], kMidNibble);
+                                codes[2] = centred(w0, kMidByte), codes[3] = centred(w1, kMidByte);
+                            }
                             if (t == 0) mma16816_new(acc, codes, qf[nb][0][0], qf[nb][0][1]);
                             else mma16816(acc, codes, qf[nb][1][0], qf[nb][1][1]);
                             if (WIDE) mma16816(acc, codes, ql[nb][t][0], ql[nb][t][1]);
