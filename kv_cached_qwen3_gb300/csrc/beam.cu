@@ -5,10 +5,12 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "kv4.cuh"
 #include "talker_kv4.h"
 
 namespace cg = cooperative_groups;
 using namespace talker_dev;
+using namespace talker_k;
 
 namespace {
 
@@ -17,7 +19,7 @@ constexpr int kMaxWidth = 32;
 constexpr int kMaxChunks = 32;      // parts of a row: the lists that one warp joins, a lane each
 constexpr int kCluster = 8;
 constexpr int kRowEntries = 600;    // best logits of a row's parts, at most (k_beam_choose holds a row's for each warp)
-constexpr int kClusterTasks = 128, kClusterEntries = 3072;   // parts of a sequence and their best logits, in a cluster
+constexpr int kClusterTasks = 128, kClusterEntries = 3200;   // parts of a sequence and their best logits, in a cluster
 constexpr float kMasked = -1e30f;   // at or below: counts as -inf
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLeastRef = -1.4426e30f;   // reference of a row's exponents without a logit: over kLog2e kMasked
@@ -41,12 +43,18 @@ __device__ __forceinline__ float ex2(float x) {   // relative error about 2^-22,
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {   // NaN only if all are
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
 // log2(x) for a normal x, to about 1e-10: x = 2^k f with f in [0.7, 1.5), log f = 2 atanh(z) by its
-// series in z = (f - 1) / (f + 1), |z| < 0.2. (Sums of exponentials meet here; scores next to one
+// series in z = (f - 1) / (f + 1), |z| < 0.2, a quotient in f32 and its remainder. (Sums of exponentials meet here; scores next to one
 // another are told apart in 64 bits, in which the general logarithm would take most of a small call.)
 __device__ __forceinline__ double log2_near(float x) {
     const int bits = __float_as_int(x), k = (bits - 0x3f333333) >> 23;
-    const double f = (double)__int_as_float(bits - (k << 23)), z = (f - 1.0) / (f + 1.0), q = z * z;
+    const float f = __int_as_float(bits - (k << 23)), r = __frcp_rn(f + 1.f), near = (f - 1.f) * r;
+    const double z = fma(fma(-(double)near, (double)f + 1.0, (double)f - 1.0), (double)r, (double)near), q = z * z;
     double t = 1.0 / 15.0;
     t = fma(t, q, 1.0 / 13.0);
     t = fma(t, q, 1.0 / 11.0);
@@ -94,26 +102,11 @@ struct Seen {
     }
 };
 
-// kVecs vectors of N logits per lane, of which vector v exists if on(v); at(v, l): the index of lane l's
-// first. They are taken in the order of their indexes, so a later equal one never replaces another.
-template <int N, int kVecs, typename On, typename At>
-__device__ __forceinline__ void take(Seen &s, const float (&x)[N * kVecs], On on, At at, int width) {
-    float tops[kVecs], top = kMasked;   // the largest value of each vector, and of all
-#pragma unroll
-    for (int v = 0; v < kVecs; ++v) {
-        tops[v] = x[v * N];
-#pragma unroll
-        for (int i = 1; i < N; ++i) tops[v] = fmaxf(tops[v], x[v * N + i]);
-        top = fmaxf(top, tops[v]);
-        if (!on(v)) tops[v] = -INFINITY;
-    }
-    const float c = top * kLog2e;
-    if (c > s.c) {
-        s.sum *= ex2(s.c - c);
-        s.c = c;
-    }
-#pragma unroll
-    for (int i = 0; i < N * kVecs; ++i) s.sum += ex2(fmaf(x[i], kLog2e, -s.c));
+// kVecs vectors of N logits per lane; tops: each one's largest, on(v): it exists; at(v, l): the index
+// of lane l's first. Those above `least` are inserted, in the order of their indexes, so a later equal
+// one never replaces another.
+template <int N, int kVecs, typename At>
+__device__ __forceinline__ void insert_all(Seen &s, const float (&x)[N * kVecs], const float (&tops)[kVecs], At at, int width) {
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
         uint32_t lanes = __ballot_sync(0xffffffffu, tops[v] > s.least);
@@ -129,6 +122,65 @@ __device__ __forceinline__ void take(Seen &s, const float (&x)[N * kVecs], On on
         }
     }
 }
+__device__ __forceinline__ void refer(Seen &s, float top) {   // the lane's reference to at least kLog2e top
+    const float c = top * kLog2e;
+    if (c > s.c) {
+        s.sum *= ex2(s.c - c);
+        s.c = c;
+    }
+}
+// Any logits: masked values count as kMasked, and are inserted while there are too few others.
+template <int N, int kVecs, typename On, typename At>
+__device__ __forceinline__ void take(Seen &s, const float (&raw)[N * kVecs], On on, At at, int width) {
+    float x[N * kVecs], tops[kVecs], top = kMasked;
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+        tops[v] = kMasked;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            x[v * N + i] = unmask(raw[v * N + i]);
+            tops[v] = fmaxf(tops[v], x[v * N + i]);
+        }
+        top = fmaxf(top, tops[v]);
+        if (!on(v)) tops[v] = -INFINITY;
+    }
+    refer(s, top);
+#pragma unroll
+    for (int i = 0; i < N * kVecs; ++i) s.sum += ex2(fmaf(x[i], kLog2e, -s.c));
+    insert_all<N, kVecs>(s, x, tops, at, width);
+}
+// The same where `least` is at least kMasked (and vectors that do not exist hold masked values): those
+// are not inserted any more, and add nothing to the sum as they are, but for NaN.
+template <int N, int kVecs, typename At>
+__device__ __forceinline__ void take_above(Seen &s, const float (&x)[N * kVecs], At at, int width) {
+    float tops[kVecs];
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+        tops[v] = max3(x[v * N], x[v * N + 1], x[v * N + 2]);
+#pragma unroll
+        for (int i = 3; i + 1 < N; i += 2) tops[v] = max3(tops[v], x[v * N + i], x[v * N + i + 1]);
+        tops[v] = fmaxf(tops[v], x[v * N + N - 1]);
+    }
+    float top = fmaxf(tops[0], tops[1]);
+#pragma unroll
+    for (int v = 2; v < kVecs; ++v) top = fmaxf(top, tops[v]);
+    refer(s, top);
+    const F2 log2e = f2(kLog2e, kLog2e), c = f2(-s.c, -s.c);
+    F2 sum = f2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < N * kVecs; i += 2) {
+        const F2 y = fma2(f2(x[i], x[i + 1]), log2e, c);
+        sum = sum + f2(ex2(f2_lo(y)), ex2(f2_hi(y)));
+    }
+    float both = f2_lo(sum) + f2_hi(sum);
+    if (both != both) {
+        both = 0.f;
+#pragma unroll
+        for (int i = 0; i < N * kVecs; ++i) both += ex2(fmaf(unmask(x[i]), kLog2e, -s.c));
+    }
+    s.sum += both;
+    if (__any_sync(0xffffffffu, top > s.least)) insert_all<N, kVecs>(s, x, tops, at, width);
+}
 
 template <typename T>
 struct Vec;   // 16 bytes of logits
@@ -136,8 +188,8 @@ template <>
 struct Vec<float> {
     static constexpr int N = 4;
     __device__ static __forceinline__ void get(const uint4 &u, float (&x)[4]) {
-        x[0] = unmask(__uint_as_float(u.x)), x[1] = unmask(__uint_as_float(u.y));
-        x[2] = unmask(__uint_as_float(u.z)), x[3] = unmask(__uint_as_float(u.w));
+        x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y);
+        x[2] = __uint_as_float(u.z), x[3] = __uint_as_float(u.w);
     }
 };
 template <>
@@ -146,7 +198,7 @@ struct Vec<__nv_bfloat16> {
     __device__ static __forceinline__ void get(const uint4 &u, float (&x)[8]) {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[2 * i] = unmask(bf16lo(w[i])), x[2 * i + 1] = unmask(bf16hi(w[i]));
+        for (int i = 0; i < 4; ++i) x[2 * i] = bf16lo(w[i]), x[2 * i + 1] = bf16hi(w[i]);
     }
 };
 
@@ -186,7 +238,7 @@ __device__ Seen read_part(const Args &a, int row, int chunk, uint32_t *tops) {
     const int v0 = (int)((long long)vectors * chunk / a.chunks), v1 = (int)((long long)vectors * (chunk + 1) / a.chunks);
     Seen s{-INFINITY, 0xffffffffu, -INFINITY, kLeastRef, 0.f};
     if (chunk == 0 && head > 0) {
-        const float one[1] = {lane < head ? unmask((float)x[lane]) : kMasked};
+        const float one[1] = {lane < head ? (float)x[lane] : kMasked};
         take<1, 1>(s, one, [&](int) { return lane < head; }, [&](int, int l) { return (uint32_t)l; }, a.width);
     }
     const uint4 *vec = reinterpret_cast<const uint4 *>(x + head);
@@ -197,6 +249,7 @@ __device__ Seen read_part(const Args &a, int row, int chunk, uint32_t *tops) {
             if (v + 32 * i + lane < v1) next[i] = ldg_stream(vec + v + 32 * i + lane);
     };
     request(v0);
+#pragma unroll 1
     for (int v = v0; v < v1 || (v == v0 && tops != nullptr); v += 32 * kAhead) {
         uint4 u[kAhead];
 #pragma unroll
@@ -219,9 +272,9 @@ __device__ Seen read_part(const Args &a, int row, int chunk, uint32_t *tops) {
                 }
         }
         if (v == v0) {
-            float m = f[0];
+            float m = kMasked;
 #pragma unroll
-            for (int i = 1; i < kAhead * N; ++i) m = fmaxf(m, f[i]);
+            for (int i = 0; i < kAhead * N; ++i) m = fmaxf(m, f[i]);
             const uint32_t top = v + lane < v1 ? rank_of(m) : 0;
             uint32_t floor;
             if (tops != nullptr) {
@@ -239,12 +292,13 @@ __device__ Seen read_part(const Args &a, int row, int chunk, uint32_t *tops) {
             // the next value below it (below 0 that is not -0)
             if (floor > 0) s.least = fmaxf(s.least, value_of(floor - (floor == 0x80000000u ? 2 : 1)));
         }
-        take<N, kAhead>(s, f, [&](int i) { return v + 32 * i + lane < v1; },
-                        [&](int i, int l) { return (uint32_t)(head + (v + 32 * i + l) * N); }, a.width);
+        const auto at = [&](int i, int l) { return (uint32_t)(head + (v + 32 * i + l) * N); };
+        if (s.least >= kMasked) take_above<N, kAhead>(s, f, at, a.width);
+        else take<N, kAhead>(s, f, [&](int i) { return v + 32 * i + lane < v1; }, at, a.width);
     }
     const int t = head + vectors * N;
     if (chunk == a.chunks - 1 && t < a.vocab) {   // fewer than a vector
-        const float one[1] = {t + lane < a.vocab ? unmask((float)x[t + lane]) : kMasked};
+        const float one[1] = {t + lane < a.vocab ? (float)x[t + lane] : kMasked};
         take<1, 1>(s, one, [&](int) { return t + lane < a.vocab; }, [&](int, int l) { return (uint32_t)(t + l); }, a.width);
     }
     const float c = warp_max(s.c);
@@ -253,90 +307,110 @@ __device__ Seen read_part(const Args &a, int row, int chunk, uint32_t *tops) {
     return s;
 }
 
-// The parts of a sequence's rows joined and its continuations chosen, by one CTA of kWarps warps.
-// best, sums: [row of the sequence][part]; stage: room for a row's lists for each warp, or null. Where a sequence has more than a warp's lists, a warp
-// joins each row's first (into rows). Then one warp, a lane to a list, takes the best of the lists'
-// heads `width` times; candidates are compared in 64 bits, as whole numbers of the same order.
-__device__ void choose(const Args &a, int seq, const Entry *best, const float2 *sums, Entry *rows, float2 *lse, Entry *stage) {
+// A row's beam, as its candidates see it. They score their logit plus `offset`, the beam's score less
+// the logarithm of the row's sum; an ended beam goes on with the end token alone, at its own score
+// (which is the offset then); all of a dead one's are at -inf.
+struct Beam {
+    double offset;
+    bool dead, ended;
+};
+struct Choice {   // shared memory of choose()
+    Beam beams[kMaxWidth];
+    Entry rows[kMaxWidth * kMaxWidth];
+    unsigned long long ranks[kMaxWidth * kMaxWidth];
+};
+
+// The scores and end marks of the rows that a warp joins: lane i has those of row warp + kWarps i.
+struct Given {
+    float score = 0.f;
+    int ended = 0;
+};
+__device__ __forceinline__ Given given(const Args &a, int seq) {
+    Given g;
+    const int w = (threadIdx.x >> 5) + kWarps * (threadIdx.x & 31);
+    if (w < a.width) {
+        g.score = a.scores[seq * a.width + w];
+        if (a.ended != nullptr) g.ended = a.ended[seq * a.width + w];
+    }
+    return g;
+}
+
+// The parts of a sequence's rows joined and its continuations chosen, by one CTA of kWarps warps. best,
+// sums: [row of the sequence][part]; stage: room for a row's lists for each warp, or null. Where a
+// sequence has more than a warp's lists, a warp joins each row's first (into c.rows). All candidates'
+// scores are then made at once, in 64 bits, as whole numbers of the same order; and one warp, a lane to
+// a list, takes the best of the lists' heads `width` times.
+__device__ void choose(const Args &a, int seq, const Given &g, const Entry *best, const float2 *sums, Choice &c, Entry *stage) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int lists = a.chunks;   // of a row
+    const bool join = a.width * a.chunks > 32;
+    const int lists = join ? 1 : a.chunks;   // of a row
     for (int w = warp; w < a.width; w += kWarps) {
         const bool part = lane < a.chunks;
-        const float2 cs = part ? sums[w * a.chunks + lane] : make_float2(kLeastRef, 0.f);
-        const float ref = warp_max(cs.x), sum = warp_sum(cs.y * ex2(cs.x - ref));
-        if (lane == 0) lse[w] = make_float2(ref, sum);
-        if (a.width * a.chunks <= 32) continue;
         const Entry *list = best + (size_t)w * a.chunks * a.width;
-        if (stage != nullptr) {   // from global memory: all at once, not a list's entries one after another
+        const float2 cs = part ? sums[w * a.chunks + lane] : make_float2(kLeastRef, 0.f);
+        if (join && stage != nullptr) {   // from global memory: all at once, not a list's entries one after another
             Entry *mine = stage + warp * a.chunks * a.width;
             __syncwarp();
             for (int i = lane; i < a.chunks * a.width; i += 32) mine[i] = list[i];
             __syncwarp();
             list = mine;
         }
+        const float ref = warp_max(cs.x), sum = warp_sum(cs.y * ex2(cs.x - ref));
+        const float score = __shfl_sync(0xffffffffu, g.score, w / kWarps);
+        const int ended = __shfl_sync(0xffffffffu, g.ended, w / kWarps);
+        if (lane == 0) {
+            // no candidate above -inf: a masked score, or a row of masked logits or with an infinite one
+            const bool dead = !(score > kMasked && score < INFINITY) || (!ended && !(ref > kLeastRef && ref < INFINITY));
+            const double lse = dead || ended ? 0.0 : ((double)ref + log2_near(sum)) * (1.0 / (double)kLog2e);
+            c.beams[w] = {(double)score - lse, dead, ended != 0};
+        }
+        if (!join) continue;
         list += lane * a.width;
         int at = 0;
         Entry head = part ? list[0] : Entry{0, 0};
         for (int j = 0; j < a.width; ++j) {
             const uint32_t rank = __reduce_max_sync(0xffffffffu, head.rank);
             const uint32_t index = __reduce_min_sync(0xffffffffu, head.rank == rank ? head.index : 0xffffffffu);
-            if (lane == 0) rows[w * a.width + j] = {rank, index};
+            if (lane == 0) c.rows[w * a.width + j] = {rank, index};
             if (head.rank == rank && head.index == index && rank != 0) head = ++at < a.width ? list[at] : Entry{0, 0};
         }
     }
-    if (a.width * a.chunks > 32) best = rows, lists = 1;
+    __syncthreads();
+    const int n = a.width * lists;   // lists, in the order of rows and indexes
+    for (int i = threadIdx.x; i < n * a.width; i += kWarps * 32) {
+        const int l = i / a.width, at = i - l * a.width;
+        const Beam b = c.beams[l / lists];
+        Entry e = join ? c.rows[i] : best[i];
+        double score = -INFINITY;
+        bool there = e.rank != 0;
+        if (!b.dead && !b.ended) {
+            const float x = value_of(e.rank);
+            if (x > kMasked) score = (double)x + b.offset;
+        } else {   // one list, in order of tokens after the end token
+            there = l % lists == 0;
+            e.index = b.dead ? at : at == 0 ? a.eos : at - 1 + (at - 1 >= a.eos);
+            if (!b.dead && at == 0) score = b.offset;
+        }
+        const unsigned long long u = (unsigned long long)__double_as_longlong(score + 0.0);
+        c.ranks[i] = !there ? 0 : u >> 63 ? ~u : u | 1ull << 63;   // 0: none
+        c.rows[i].index = e.index;
+    }
     __syncthreads();
     if (warp != 0) return;
-    const int w = lane / lists, row = seq * a.width + w;   // lists in the order of rows and indexes
-    const bool on = w < a.width;
-    float score = 0.f;
-    bool old = false, dead = true;
-    double base = 0.0;
-    if (on) {
-        score = a.scores[row];
-        old = a.ended != nullptr && a.ended[row] != 0;
-        const float2 cs = lse[w];
-        // no candidate above -inf: a masked score, or a row of masked logits or with an infinite one
-        dead = !(score > kMasked && score < INFINITY) || (!old && !(cs.x > kLeastRef && cs.x < INFINITY));
-        if (!dead && !old) base = ((double)cs.x + log2_near(cs.y)) / (double)kLog2e;
-    }
-    const Entry *list = best + (size_t)lane * a.width;
-    // The candidate `at` of this lane's list: its token and its score's rank (0: none left). Beams that
-    // are dead or have ended have one list, in order of tokens.
-    int at = 0, token = 0;
-    double c = 0.0;
-    unsigned long long rank = 0;
-    auto next = [&]() {
-        rank = 0;
-        if (!on || at >= a.width) return;
-        c = -INFINITY;
-        if (dead || old) {
-            if (lane % lists != 0) return;
-            token = dead ? at : at == 0 ? a.eos : at - 1 + (at - 1 >= a.eos);
-            if (!dead && at == 0) c = score;
-        } else {
-            const Entry e = list[at];
-            if (e.rank == 0) return;
-            token = (int)e.index;
-            const float x = value_of(e.rank);
-            if (x > kMasked) c = (double)x - base + (double)score;
-        }
-        const unsigned long long u = (unsigned long long)__double_as_longlong(c + 0.0);
-        rank = u >> 63 ? ~u : u | 1ull << 63;
-    };
-    next();
+    int at = lane * a.width;
+    const int end = at + (lane < n ? a.width : 0);
+    unsigned long long rank = at < end ? c.ranks[at] : 0;
     for (int j = 0; j < a.width; ++j) {
         const uint32_t hi = (uint32_t)(rank >> 32), top = __reduce_max_sync(0xffffffffu, hi);
         const uint32_t lo = hi == top ? (uint32_t)rank : 0, low = __reduce_max_sync(0xffffffffu, lo);
-        const int from = __ffs(__ballot_sync(0xffffffffu, hi == top && lo == low)) - 1;
-        if (lane == from) {
-            const int out = seq * a.width + j;
+        if (lane == __ffs(__ballot_sync(0xffffffffu, hi == top && lo == low)) - 1) {
+            const int out = seq * a.width + j, w = lane / lists, token = c.rows[at].index;
+            const unsigned long long u = rank >> 63 ? rank & ~(1ull << 63) : ~rank;
             a.tokens[out] = token;
-            a.parents[out] = row;
-            a.scores_out[out] = (float)c;
-            if (a.ended_out != nullptr) a.ended_out[out] = old || token == a.eos;
-            ++at;
-            next();
+            a.parents[out] = seq * a.width + w;
+            a.scores_out[out] = (float)__longlong_as_double((long long)u);
+            if (a.ended_out != nullptr) a.ended_out[out] = c.beams[w].ended || token == a.eos;
+            rank = ++at < end ? c.ranks[at] : 0;
         }
     }
 }
@@ -345,14 +419,17 @@ __device__ void choose(const Args &a, int seq, const Entry *best, const float2 *
 // the first CTA's shared memory, which joins them. No scratch, one launch.
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32) k_beam_cluster(const Args a) {
-    __shared__ Entry best[kClusterEntries], rows[kMaxWidth * kMaxWidth];
-    __shared__ float2 sums[kClusterTasks], lse[kMaxWidth];
+    __shared__ Entry best[kClusterEntries];
+    __shared__ Choice choice;
+    __shared__ float2 sums[kClusterTasks];
     __shared__ uint32_t tops[kWarps * 32];
     cg::cluster_group cluster = cg::this_cluster();
     const int ctas = cluster.num_blocks(), rank = cluster.block_rank(), seq = blockIdx.x / ctas;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     Entry *best0 = cluster.map_shared_rank(best, 0);
     float2 *sums0 = cluster.map_shared_rank(sums, 0);
+    Given g;
+    if (rank == 0) g = given(a, seq);
     cluster.sync();   // every CTA's shared memory is there
     for (int t = rank * kWarps + warp; t < a.width * a.chunks; t += ctas * kWarps) {
         const Seen s = read_part<T>(a, seq * a.width + t / a.chunks, t % a.chunks, a.chunks % kWarps == 0 ? tops : nullptr);
@@ -360,7 +437,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_beam_cluster(const Args a) {
         if (lane == 0) sums0[t] = make_float2(s.c, s.sum);
     }
     cluster.sync();
-    if (rank == 0) choose(a, seq, best, sums, rows, lse, nullptr);
+    if (rank == 0) choose(a, seq, g, best, sums, choice, nullptr);
 }
 
 // Larger calls: a warp per part over the whole GPU, the results in scratch; then a CTA per sequence.
@@ -368,20 +445,20 @@ template <typename T>
 __global__ void __launch_bounds__(kWarps * 32) k_beam_parts(const Args a, long long parts) {
     __shared__ uint32_t tops[kWarps * 32];
     const int lane = threadIdx.x & 31;
-    pdl_launch_dependents();
     const long long t = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (t >= parts) return;
     const Seen s = read_part<T>(a, (int)(t / a.chunks), (int)(t % a.chunks), a.chunks % kWarps == 0 ? tops : nullptr);
     if (lane < a.width) a.best[t * a.width + lane] = s.entry();
     if (lane == 0) a.sums[t] = make_float2(s.c, s.sum);
+    pdl_launch_dependents();   // (at the start 36 us instead of 25 for 24 x 8 rows of 100003: its CTAs take the parts' room)
 }
 __global__ void __launch_bounds__(kWarps * 32) k_beam_choose(const Args a) {
     extern __shared__ Entry stage[];   // a row's lists for each warp
-    __shared__ Entry rows[kMaxWidth * kMaxWidth];
-    __shared__ float2 lse[kMaxWidth];
+    __shared__ Choice choice;
+    const Given g = given(a, blockIdx.x);   // (written before the parts began)
     pdl_wait();
     const size_t first = (size_t)blockIdx.x * a.width * a.chunks;
-    choose(a, blockIdx.x, a.best + first * a.width, a.sums + first, rows, lse, stage);
+    choose(a, blockIdx.x, g, a.best + first * a.width, a.sums + first, choice, stage);
 }
 
 // How a call runs. A cluster serves a sequence until its CTAs would read over kClusterLogits each;
@@ -391,7 +468,7 @@ struct Shape {
     int chunks;
 };
 constexpr int kClusterLogits = 32768, kPartLogits = 1024;
-constexpr int kTargetParts = 152 * 20;
+constexpr int kTargetParts = 152 * 20;   // 24 x 8 rows of 100003: 24.8 us; 152 * 24: 25.0, 152 * 32 on 4 CTAs an SM 25.6
 
 Shape shape_of(int n_seq, int width, int vocab) {
     const long long logits = (long long)width * vocab;

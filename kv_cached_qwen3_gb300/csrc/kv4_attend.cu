@@ -311,8 +311,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
         const bool q_vec = (reinterpret_cast<uintptr_t>(a.q) & 15u) == 0 && a.q_row * sizeof(TI) % 16 == 0;
         const float cs = a.scale * kLog2e;
         uint32_t qf[NB][2][2], ql[NB][2][2];       // (ql: WIDE only)
-        uint32_t qc;                               // -8 sum(q) of two blocks, times 2^kCorrBits: lanes c < H have a
-                                                   // first part, lanes c - H its rest
+        uint32_t qc = 0;                           // (unless PREC) -8 sum(q) of two blocks, times 2^kCorrBits: lanes
+                                                   // c < H have a first part, lanes c - H its rest
         F2 fs;                                     // from these units to scores in base 2, of this lane's columns 2 c, 2 c + 1
         {
             float x[NB][8], top = 0.f;
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
                     hi[i] = __float2half_rn(y);
                     lo[i] = __float2half_rn(y - __half2float(hi[i]));
                     if (kParts == 2 && r >= 4) hi[i] = lo[i];
-                    sum = fmaf(__half2float(hi[i]) + (WIDE ? __half2float(lo[i]) : 0.f), i & 1 ? 17.f : 1.f, sum);
+                    if (!PREC) sum = fmaf(__half2float(hi[i]), i & 1 ? 17.f : 1.f, sum);
                 }
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
@@ -355,13 +355,13 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
                         qf[nb][t][i] = pack_half(hi[2 * t + i], hi[2 * t + 4 + i]);
                         ql[nb][t][i] = pack_half(lo[2 * t + i], lo[2 * t + 4 + i]);
                     }
+                if (PREC) continue;
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
                 corr[nb] = sum * (-8.f / 16777216.f * (1 << kCorrBits));
             }
-            qc = 0;
 #pragma unroll
-            for (int i = 0; i < NB / 2; ++i) {
+            for (int i = 0; i < NB / 2 && !PREC; ++i) {
                 const __half h0 = __float2half_rn(corr[2 * i]), h1 = __float2half_rn(corr[2 * i + 1]);
                 if (c == i) qc = pack_half(h0, h1);
                 if (c == i + NB / 2)
