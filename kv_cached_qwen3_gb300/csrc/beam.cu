@@ -18,7 +18,7 @@ constexpr int kWarps = 8;
 constexpr int kMaxWidth = 32;
 constexpr int kMaxChunks = 32;      // parts of a row: the lists that one warp joins, a lane each
 constexpr int kCluster = 8;
-constexpr int kRowEntries = 600;    // best logits of a row's parts, at most (k_beam_choose holds a row's for each warp)
+constexpr int kRowEntries = 544;    // best logits of a row's parts, at most (k_beam_choose holds a row's for each warp)
 constexpr int kClusterTasks = 128, kClusterEntries = 3200;   // parts of a sequence and their best logits, in a cluster
 constexpr float kMasked = -1e30f;   // at or below: counts as -inf
 constexpr float kLog2e = 1.4426950408889634f;
@@ -316,8 +316,8 @@ struct Beam {
 };
 struct Choice {   // shared memory of choose()
     Beam beams[kMaxWidth];
-    Entry rows[kMaxWidth * kMaxWidth];
-    unsigned long long ranks[kMaxWidth * kMaxWidth];
+    unsigned long long ranks[kMaxWidth * kMaxWidth];   // of the candidates; before, the joined lists: rank << 32 | index
+    int tokens[kMaxWidth * kMaxWidth];
 };
 
 // The scores and end marks of the rows that a warp joins: lane i has those of row warp + kWarps i.
@@ -337,7 +337,7 @@ __device__ __forceinline__ Given given(const Args &a, int seq) {
 
 // The parts of a sequence's rows joined and its continuations chosen, by one CTA of kWarps warps. best,
 // sums: [row of the sequence][part]; stage: room for a row's lists for each warp, or null. Where a
-// sequence has more than a warp's lists, a warp joins each row's first (into c.rows). All candidates'
+// sequence has more than a warp's lists, a warp joins each row's first (into c.ranks). All candidates'
 // scores are then made at once, in 64 bits, as whole numbers of the same order; and one warp, a lane to
 // a list, takes the best of the lists' heads `width` times.
 __device__ void choose(const Args &a, int seq, const Given &g, const Entry *best, const float2 *sums, Choice &c, Entry *stage) {
@@ -371,7 +371,7 @@ __device__ void choose(const Args &a, int seq, const Given &g, const Entry *best
         for (int j = 0; j < a.width; ++j) {
             const uint32_t rank = __reduce_max_sync(0xffffffffu, head.rank);
             const uint32_t index = __reduce_min_sync(0xffffffffu, head.rank == rank ? head.index : 0xffffffffu);
-            if (lane == 0) c.rows[w * a.width + j] = {rank, index};
+            if (lane == 0) c.ranks[w * a.width + j] = (unsigned long long)rank << 32 | index;
             if (head.rank == rank && head.index == index && rank != 0) head = ++at < a.width ? list[at] : Entry{0, 0};
         }
     }
@@ -380,7 +380,7 @@ __device__ void choose(const Args &a, int seq, const Given &g, const Entry *best
     for (int i = threadIdx.x; i < n * a.width; i += kWarps * 32) {
         const int l = i / a.width, at = i - l * a.width;
         const Beam b = c.beams[l / lists];
-        Entry e = join ? c.rows[i] : best[i];
+        Entry e = join ? Entry{(uint32_t)(c.ranks[i] >> 32), (uint32_t)c.ranks[i]} : best[i];
         double score = -INFINITY;
         bool there = e.rank != 0;
         if (!b.dead && !b.ended) {
@@ -393,7 +393,7 @@ __device__ void choose(const Args &a, int seq, const Given &g, const Entry *best
         }
         const unsigned long long u = (unsigned long long)__double_as_longlong(score + 0.0);
         c.ranks[i] = !there ? 0 : u >> 63 ? ~u : u | 1ull << 63;   // 0: none
-        c.rows[i].index = e.index;
+        c.tokens[i] = (int)e.index;
     }
     __syncthreads();
     if (warp != 0) return;
@@ -404,7 +404,7 @@ __device__ void choose(const Args &a, int seq, const Given &g, const Entry *best
         const uint32_t hi = (uint32_t)(rank >> 32), top = __reduce_max_sync(0xffffffffu, hi);
         const uint32_t lo = hi == top ? (uint32_t)rank : 0, low = __reduce_max_sync(0xffffffffu, lo);
         if (lane == __ffs(__ballot_sync(0xffffffffu, hi == top && lo == low)) - 1) {
-            const int out = seq * a.width + j, w = lane / lists, token = c.rows[at].index;
+            const int out = seq * a.width + j, w = lane / lists, token = c.tokens[at];
             const unsigned long long u = rank >> 63 ? rank & ~(1ull << 63) : ~rank;
             a.tokens[out] = token;
             a.parents[out] = seq * a.width + w;
@@ -467,7 +467,7 @@ struct Shape {
     int ctas;     // of the cluster, or 0: two launches
     int chunks;
 };
-constexpr int kClusterLogits = 32768, kPartLogits = 1024;
+constexpr int kClusterLogits = 16384, kPartLogits = 256;
 constexpr int kTargetParts = 152 * 20;   // 24 x 8 rows of 100003: 24.8 us; 152 * 24: 25.0, 152 * 32 on 4 CTAs an SM 25.6
 
 Shape shape_of(int n_seq, int width, int vocab) {
@@ -550,6 +550,7 @@ talker_status talker_beam_select(const void *logits, int64_t row_stride, int dty
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.gridDim = dim3((unsigned)n_seq);
+        static_assert(sizeof(Choice) + kWarps * kRowEntries * sizeof(Entry) <= 48 * 1024, "k_beam_choose's shared memory");
         cfg.dynamicSmemBytes = width * p.chunks > 32 ? (size_t)kWarps * p.chunks * width * sizeof(Entry) : 0;
         if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, k_beam_choose, a);
     }

@@ -149,7 +149,9 @@ __device__ __forceinline__ PageRows page_rows(const Kv4Rows &r, int s, int slot,
 }
 
 // Many rows: a CTA per (page, head), kRowThreads / (4 * NB) rows at a time: one look-up of the page, and
-// all its loads in flight. Bound by the dense rows' traffic (f32: 128 of 146 bytes a block).
+// all its loads in flight. 28 layers x 4096 rows of 8 heads of 128 dims: f32 written in 199 us (5.4 TB/s of
+// dense rows and codes, 79% of the measured copy), read in 164 (96%); bf16 written in 193 (46%; bound by the
+// quantization's instructions, the same for half the bytes), read in 96 (92%).
 // Grid (pages * heads, streams, layers * 2) to write and (pages * heads, streams, layers) to read, where a
 // CTA takes K and V, whose loads are small.
 template <int HD, typename T>
@@ -167,8 +169,8 @@ __global__ void __launch_bounds__(kRowThreads) k_kv4_write_pages(const Kv4Rows r
     float x[kPasses][8];
 #pragma unroll
     for (int u = 0; u < kPasses; ++u) {
-        const int row = u * RP + threadIdx.x / TPR;
-        if (row >= at.lo && row < at.hi) {
+        const int row = at.lo + u * RP + threadIdx.x / TPR;
+        if (row < at.hi) {
             load8<T>(dense + (at.first + row) * r.st.row, vec, x[u]);
         } else {
 #pragma unroll
@@ -179,8 +181,8 @@ __global__ void __launch_bounds__(kRowThreads) k_kv4_write_pages(const Kv4Rows r
     if (p.tile == nullptr) return;
 #pragma unroll
     for (int u = 0; u < kPasses; ++u) {
-        const int row = u * RP + threadIdx.x / TPR;
-        store_codes<HD>(row >= at.lo && row < at.hi ? p.tile : nullptr, row, is_v, b, c, x[u]);
+        const int row = at.lo + u * RP + threadIdx.x / TPR;
+        if (at.lo + u * RP < at.hi) store_codes<HD>(row < at.hi ? p.tile : nullptr, row, is_v, b, c, x[u]);
     }
 }
 template <int HD, typename T>
@@ -201,27 +203,31 @@ __global__ void __launch_bounds__(kRowThreads) k_kv4_read_pages(const Kv4Rows r,
     for (int v = 0; v < 2; ++v)
 #pragma unroll
         for (int u = 0; u < kPasses; ++u) {
-            const int row = u * RP + threadIdx.x / TPR;
-            k[v][u] = load_codes<HD>(row >= at.lo && row < at.hi ? tiles[v] : nullptr, row, v, b, c);
+            const int row = at.lo + u * RP + threadIdx.x / TPR;
+            k[v][u] = load_codes<HD>(row < at.hi ? tiles[v] : nullptr, row, v, b, c);
         }
     const int64_t off = l * r.st.layer + s * r.st.stream + h * r.st.head + b * 32 + c * 8;
 #pragma unroll
     for (int v = 0; v < 2; ++v)
 #pragma unroll
         for (int u = 0; u < kPasses; ++u) {
-            const int row = u * RP + threadIdx.x / TPR;
+            const int row = at.lo + u * RP + threadIdx.x / TPR;
+            if (at.lo + u * RP >= at.hi) continue;
             float x[8];
             values_of(k[v][u], v, b, x);
-            if (row >= at.lo && row < at.hi) store8(static_cast<T *>(v ? r.v : r.k) + off + (at.first + row) * r.st.row, vec, x);
+            if (row < at.hi) store8(static_cast<T *>(v ? r.v : r.k) + off + (at.first + row) * r.st.row, vec, x);
         }
 }
 
-// From this many rows a stream on, a CTA per page is faster.
-constexpr int kPageRowsMin = 16;
+// From this many rows a stream on, a CTA per page is faster: a page's loads are in flight at once, but a
+// small part of a page leaves most of its CTA without work. 32 streams, 5 layers, 8 heads of 128 in f32,
+// us by rows / by pages: written, 32 rows 13.1 / 19.1, 64 25.0 / 26.3, 128 47.9 / 45.3, 256 92.9 / 80.0;
+// read, 16 rows 6.1 / 6.9, 32 9.8 / 9.6, 64 19.8 / 15.0, 256 71.8 / 61.0. (bf16 alike.)
+constexpr int kWritePageRows = 96, kReadPageRows = 32;
 
 template <int HD, typename T, bool READ>
 cudaError_t launch_rows_t(const Kv4Rows &r, bool vec, cudaStream_t s) {
-    if (r.T >= kPageRowsMin) {
+    if (r.T >= (READ ? kReadPageRows : kWritePageRows)) {
         const long long slots = ((long long)r.T + kPage - 2) / kPage + 1;   // pages that T rows can touch
         const dim3 grid((unsigned)(slots * r.c.n_kv_heads), r.n_streams, READ ? r.n_layers : 2 * r.n_layers);
         if (READ) k_kv4_read_pages<HD, T><<<grid, kRowThreads, 0, s>>>(r, vec);

@@ -60,7 +60,8 @@ def edge_rows(x):
 @pytest.mark.parametrize("L,B,T,H,D,dt,order", [
     (1, 1, 1, 1, 64, "f32", "rows"), (1, 1, 1, 8, 128, "bf16", "rows"), (2, 3, 65, 3, 128, "f32", "rows"),
     (2, 3, 70, 2, 64, "bf16", "rows"), (3, 1, 130, 5, 128, "f32", "heads"), (1, 2, 9, 4, 128, "bf16", "packed"),
-    (1, 2, 9, 4, 64, "f32", "odd")])
+    (1, 2, 9, 4, 64, "f32", "odd"), (2, 3, 100, 3, 64, "bf16", "odd"), (1, 2, 131, 2, 64, "f32", "rows"),
+    (1, 4, 200, 3, 128, "bf16", "packed"), (1, 2, 95, 2, 128, "f32", "rows"), (1, 2, 33, 2, 128, "bf16", "heads")])
 def test_write_read(kv4, L, B, T, H, D, dt, order):
     dtype = dtype_of(dt)
     if order == "rows":
@@ -157,6 +158,25 @@ def test_rows_outside_the_cache_are_skipped_and_reported(kv4):
     c.write(t, t)
     assert torch.equal(c.k, before)
     assert c.sync_status() == 8
+
+
+def test_pages_outside_the_cache_are_skipped_and_reported(kv4):
+    """The same for enough rows that a page is written and read at once."""
+    c = kv4.KV4Cache(3, 192, 1, 2, 128)
+    t = rnd(1, 1, 3, 150, 2, 128)
+    start = torch.tensor([100, -70, 10], dtype=torch.int32).cuda()
+    c.page_table[2, 1] = 9      # n_pages
+    before = c.k.clone()
+    c.write(t, t, start=start)
+    out = torch.full_like(t, 9.0)
+    c.read(out, out.clone(), start=start)
+    want = ref.q4_roundtrip(host(t))
+    inside = np.zeros((3, 150), bool)
+    inside[0, :92] = inside[1, 70:] = inside[2, :54] = inside[2, 118:] = True
+    np.testing.assert_array_equal(host(out)[0][inside], want[0][inside])
+    assert (host(out)[0][~inside] == 9).all()
+    assert c.sync_status() == 9 and c.sync_status() == 0
+    assert torch.equal(c.k[7], before[7])       # the page that stream 2 would have at its place
 
 
 # ------------------------------------------------------------------ attention
@@ -333,7 +353,8 @@ def check_select(logits, scores, ended=None, eos=-1):
 
 @pytest.mark.parametrize("S,W,V,dt", [(1, 1, 1, "f32"), (1, 1, 5, "bf16"), (2, 4, 4, "f32"), (3, 5, 257, "bf16"),
                                       (1, 32, 33, "f32"), (2, 32, 4099, "f32"), (5, 3, 50021, "bf16"),
-                                      (1, 8, 151669, "f32"), (40, 2, 1000, "f32")])
+                                      (1, 8, 151669, "f32"), (40, 2, 1000, "f32"), (1, 32, 32003, "f32"),
+                                      (3, 17, 20000, "bf16"), (2, 32, 9001, "f32"), (1, 31, 600, "bf16")])
 def test_select(kv4, S, W, V, dt):
     x = (rnd(1, S, W, V) * 2).to(dtype_of(dt))
     scores = -10 * rnd(2, S, W).abs()
