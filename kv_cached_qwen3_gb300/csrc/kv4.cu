@@ -99,11 +99,11 @@ __device__ __forceinline__ void values_of(const Codes &k, bool is_v, int b, floa
     q4_values8(is_v ? v_word(k.w, b) : k.w, __half2float(__ushort_as_half(k.d)), x);
 }
 // A lane's eight dims quantized into the tile; every lane of the warp takes part.
-template <int HD>
+template <int HD, typename T>
 __device__ __forceinline__ void store_codes(unsigned char *tile, int prow, bool is_v, int b, int c, const float (&x)[8]) {
     using Tile = Kv4Tile<HD>;
     unsigned short d;
-    uint32_t w = q4_codes8(x, d);
+    uint32_t w = q4_codes8<sizeof(T) == 2>(x, d);
     if (is_v) w = v_word(w, b);
     if (tile == nullptr) return;
     *reinterpret_cast<uint32_t *>(tile + prow * Tile::kRow + q4_word_at<Tile::NB>(is_v, b, c)) = w;
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kRowThreads) k_kv4_rows(const Kv4Rows r, const
         values_of(load_codes<HD>(p.tile, p.prow, is_v, b, c), is_v, b, x);
         if (p.tile != nullptr) store8(dense, vec, x);
     } else {
-        store_codes<HD>(p.tile, p.prow, is_v, b, c, x);
+        store_codes<HD, T>(p.tile, p.prow, is_v, b, c, x);
     }
 }
 
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kRowThreads) k_kv4_write_pages(const Kv4Rows r
 #pragma unroll
     for (int u = 0; u < kPasses; ++u) {
         const int row = at.lo + u * RP + threadIdx.x / TPR;
-        if (at.lo + u * RP < at.hi) store_codes<HD>(row < at.hi ? p.tile : nullptr, row, is_v, b, c, x[u]);
+        if (at.lo + u * RP < at.hi) store_codes<HD, T>(row < at.hi ? p.tile : nullptr, row, is_v, b, c, x[u]);
     }
 }
 template <int HD, typename T>

@@ -48,54 +48,93 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
     return r;
 }
 
+// The largest and the smallest of three, NaN if one is NaN.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+__device__ __forceinline__ float min3_nan(float a, float b, float c) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
 // Quantizes one block of 32 values. The four lanes of an aligned group hold dims 8 c .. 8 c + 7
 // of the block, c = lane & 3; every lane of the warp has to take part. Returns the lane's eight
 // codes (dim i in bits 4 i ..) and the block's scale bits.
 //
 // code = clamp(floor(8.5 - 8 x / m), 0, 15) has to be exact (a neighbouring code is off by a
 // whole step, and values exactly between two codes are common in bf16). The whole number k nearest to
-// 8.5 - 8 x / m comes from fp32, off by less than 2e-6; the code is k, or k - 1 where
+// 8.5 - 8 x / m comes from fp32, off by less than 4e-6; the code is k, or k - 1 where
 // (17 - 2 k) |m| < 16 x sign(m): the sign of one fma, which rounds that difference only once. Blocks
 // with tiny |m| are scaled by 2^60 first (exact), so that neither 8 / m nor the sign can be lost.
+//
+// BF16: the values are bf16 numbers. A difference 16 x - (17 - 2 k) m other than 0 is then at least
+// half the last place of m where it matters (|x| >= |m| / 32), or 2^8 where m is clamped: 8.5 - 8 x / m is
+// a whole number or more than 2^-12 away from one, and fp32 plus 2^-13 decides, without that fma.
+template <bool BF16>
 __device__ __forceinline__ uint32_t q4_codes8(const float (&x)[8], unsigned short &d_bits) {
-    float m = x[0];
-    F2 zero = f2(0.f, 0.f);   // NaN if a value is not finite
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (i % 2 == 0) zero = fma2(f2(x[i], x[i + 1]), f2(0.f, 0.f), zero);
-        if (fabsf(x[i]) > fabsf(m)) m = x[i];
-    }
     const int lane = threadIdx.x & 31;
+    float hi = max3_nan(x[0], x[1], x[2]), lo = min3_nan(x[0], x[1], x[2]);
+    hi = max3_nan(hi, x[3], x[4]), lo = min3_nan(lo, x[3], x[4]);
+    hi = max3_nan(hi, x[5], x[6]), lo = min3_nan(lo, x[5], x[6]);
+    hi = max3_nan(hi, x[7], __shfl_xor_sync(0xffffffffu, max3_nan(hi, x[7], x[7]), 1));
+    lo = min3_nan(lo, x[7], __shfl_xor_sync(0xffffffffu, min3_nan(lo, x[7], x[7]), 1));
+    const float hi2 = __shfl_xor_sync(0xffffffffu, hi, 2), lo2 = __shfl_xor_sync(0xffffffffu, lo, 2);
+    hi = max3_nan(hi, hi2, hi2), lo = min3_nan(lo, lo2, lo2);
+    const bool bad = !(hi < INFINITY && lo > -INFINITY);
+    float m = hi > -lo ? hi : lo;
+    if (__any_sync(0xffffffffu, hi == -lo && hi > 0.f)) {   // both signs: the first one's
+        float first = 0.f;
 #pragma unroll
-    for (int o = 1; o <= 2; o <<= 1) {
-        const float other = __shfl_xor_sync(0xffffffffu, m, o);
-        if (fabsf(other) > fabsf(m) || (fabsf(other) == fabsf(m) && (lane & o))) m = other;
+        for (int i = 7; i >= 0; --i)
+            if (fabsf(x[i]) == hi) first = x[i];
+#pragma unroll
+        for (int o = 1; o <= 2; o <<= 1) {
+            const float other = __shfl_xor_sync(0xffffffffu, first, o), a = lane & o ? other : first, b = lane & o ? first : other;
+            first = a != 0.f ? a : b;
+        }
+        if (hi == -lo) m = first;
     }
-    // the warp's bits of "not finite", of this group of four
-    const bool bad = (__ballot_sync(0xffffffffu, !(f2_lo(zero) + f2_hi(zero) == 0.f)) >> (lane & ~3) & 15u) != 0;
-    float y[8];
+    float y[8], up = 1.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = x[i];
-    if (fabsf(m) > 524032.f) {
+    if (fabsf(m) > 524032.f || fabsf(m) < 1e-30f) {
         m = fminf(fmaxf(m, -524032.f), 524032.f);
+        up = fabsf(m) < 1.f ? 1152921504606846976.f : 1.f;   // 2^60
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = fminf(fmaxf(y[i], -524032.f), 524032.f);
+        for (int i = 0; i < 8; ++i) y[i] = fminf(fmaxf(y[i], -524032.f), 524032.f) * up;
     }
+    const bool none = bad || m == 0.f;
     d_bits = bad ? 0x7e00 : __half_as_ushort(__float2half_rn(m * -0.125f));
-    if (bad || m == 0.f) return 0x88888888u;
-    const float up = fabsf(m) < 1e-30f ? 1152921504606846976.f : 1.f;   // 2^60
-    const float M = fabsf(m) * up, s = m > 0.f ? -16.f * up : 16.f * up, id = 0.5f / M;
+    m *= up;
+    float inv;   // 1 / |m|, to 2^-23
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(fabsf(m)));
     constexpr float kRound = 12582912.f;   // 1.5 2^23: x + kRound holds the nearest whole number to x
-    uint32_t w = 0;
+    uint32_t w = 0;                        // modulo 2^32 the eight bit patterns of kRound add up to a constant
+    if (BF16) {   // 8 - 8 x / m + 2^-13 in units of kTop, which rounds to 15
+        constexpr float kTop = 15.4375f;
+        const float s = copysignf(inv * (8.f / kTop), -m);
 #pragma unroll
-    for (int i = 6; i >= 0; i -= 2) {
-        const F2 z = f2(y[i], y[i + 1]) * f2(s, s), r = fma2(z, f2(id, id), f2(8.5f, 8.5f)) + f2(kRound, kRound);
-        const F2 side = fma2(fma2(f2(-2.f, -2.f), r + f2(-kRound, -kRound), f2(17.f, 17.f)), f2(M, M), z);
-        const int n1 = __float_as_int(f2_hi(r)) - __float_as_int(kRound) + (__float_as_int(f2_hi(side)) >> 31);
-        const int n0 = __float_as_int(f2_lo(r)) - __float_as_int(kRound) + (__float_as_int(f2_lo(side)) >> 31);
-        w = w * 256 + (uint32_t)(min(n1, 15) * 16 + min(n0, 15));
+        for (int i = 6; i >= 0; i -= 2) {
+            const F2 u = f2(__saturatef(fmaf(y[i], s, (8.f + 0x1p-13f) / kTop)), __saturatef(fmaf(y[i + 1], s, (8.f + 0x1p-13f) / kTop)));
+            const F2 r = fma2(u, f2(kTop, kTop), f2(kRound, kRound));
+            w = w * 256 + (__float_as_uint(f2_hi(r)) * 16 + __float_as_uint(f2_lo(r)));
+        }
+    } else {
+        const float M = fabsf(m), s = copysignf(16.f, -m), id = 0.5f * inv;
+        const int top = __float_as_int(kRound) + 15;
+#pragma unroll
+        for (int i = 6; i >= 0; i -= 2) {
+            const F2 z = f2(y[i], y[i + 1]) * f2(s, s), r = fma2(z, f2(id, id), f2(8.5f, 8.5f)) + f2(kRound, kRound);
+            const F2 side = fma2(fma2(f2(-2.f, -2.f), r + f2(-kRound, -kRound), f2(17.f, 17.f)), f2(M, M), z);
+            const int n1 = __float_as_int(f2_hi(r)) + (__float_as_int(f2_hi(side)) >> 31);
+            const int n0 = __float_as_int(f2_lo(r)) + (__float_as_int(f2_lo(side)) >> 31);
+            w = w * 256 + ((uint32_t)min(n1, top) * 16 + (uint32_t)min(n0, top));
+        }
     }
-    return w;
+    return none ? 0x88888888u : w - 0x4b400000u * 0x11111111u;
 }
 
 // The code of x in a block with M = |m| > 0, s = -16 sign(m), both times 2^60 if m is tiny, id = 0.5 / M.

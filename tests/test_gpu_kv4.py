@@ -124,6 +124,29 @@ def test_codes_on_borders_are_exact(kv4):
     np.testing.assert_array_equal(host(o), ref.q4_roundtrip(host(t)))
 
 
+@pytest.mark.parametrize("exponent", [0, -127, 90, 19])
+def test_bf16_codes_are_exact(kv4, exponent):
+    """Every pair of bf16 mantissas of a value and of its block's maximum, at exponents down to 2^-5 of it (near
+    2^-127 some are subnormal, near 2^19 some maxima are clamped): many lie on a border between two codes."""
+    mant = np.arange(128, 256) / 128.0
+    x = np.stack(np.meshgrid(mant, mant, 2.0 ** np.arange(0, -6, -1), [1, -1], indexing="ij"), -1).reshape(128, -1, 4)
+    x = x[..., 1] * x[..., 2] * x[..., 3]       # 1536 values for each maximum
+    x = np.concatenate([x, x[:, :14]], 1).reshape(128, 50, 31)
+    m = np.broadcast_to(mant[:, None, None] * np.where(np.arange(50) % 2, 1, -1)[None, :, None], (128, 50, 1))
+    x = np.clip(x, -np.abs(m), np.abs(m))
+    blocks = np.concatenate([m, x], -1).reshape(-1, 32) * 2.0 ** exponent
+    t = torch.from_numpy(blocks.reshape(1, 1, -1, 1, 128)).to(torch.bfloat16).cuda()
+    c = kv4.KV4Cache(1, t.shape[2], 1, 1, 128)
+    c.write(t, t)
+    codes, d = ref.q4_quantize(host(t)[0, 0, :, 0])
+    for page in range(c.pages_per_stream):
+        n = min(PAGE, t.shape[2] - page * PAGE)
+        cc, dd = np.zeros((PAGE, 128), np.uint8), np.zeros((PAGE, 4), np.float16)
+        cc[:n], dd[:n] = codes[page * PAGE:page * PAGE + n], d[page * PAGE:page * PAGE + n]
+        np.testing.assert_array_equal(c.k[page, 0, 0].cpu().numpy(), ref.tile_bytes(cc, dd, False))
+        np.testing.assert_array_equal(c.v[page, 0, 0].cpu().numpy(), ref.tile_bytes(cc, dd, True))
+
+
 def test_blocks_with_nan_or_inf_read_back_as_nan(kv4):
     t = rnd(1, 1, 1, 3, 2, 128)
     t[0, 0, 0, 0, 5] = float("nan")
