@@ -252,30 +252,33 @@ __device__ __forceinline__ int parent_of(const KvReorder &r, int i) {
 }
 __device__ __forceinline__ int length_of(const KvReorder &r, int p) { return min(max(r.lens[p], 0), r.pps * kPage); }
 
-// One warp finds column j of the new table. Row i keeps its parent's page where that is full
+// What row i's parent holds of column j: its page's r, plus kFull if the page is full (else it is the
+// tail), or -1. Rows first, first + step, ...
+constexpr int kFull = 0x4000;
+__device__ __forceinline__ void column_entries(const KvReorder &r, int j, int first, int step, bool report, short *entries) {
+#pragma unroll 4
+    for (int i = first; i < r.n_streams; i += step) {
+        const int p = parent_of(r, i), tail = length_of(r, p) / kPage, entry = r.table[(size_t)p * r.pps + j], er = entry / r.pps;
+        const bool ok = entry >= 0 && entry - er * r.pps == j && er < r.n_streams;
+        if (report && !ok && j <= tail && r.status != nullptr) atomicOr(r.status, ST_BAD_ARG);
+        entries[i] = (short)(ok && j <= tail ? er | (j < tail ? kFull : 0) : -1);
+    }
+}
+
+// One warp finds column j of the new table from its entries. Row i keeps its parent's page where that is full
 // (shared), and takes it over at the parent's tail page, unless a row before it did (another child) or a
 // stream shares the page (as one may after this one was cut shorter); every other row needs a page of
 // its own, and gets the pages of the column's set {r * pps + j} that no kept entry uses, in order. A row
 // refers to one page of a column, so there are always enough. Writes the column when `store`; returns
 // row `ask`'s entry.
-__device__ int reorder_column(const KvReorder &r, int j, int ask, bool store, bool report, ReorderScratch &w) {
+__device__ int reorder_column(const KvReorder &r, int j, int ask, bool store, const short *entries, ReorderScratch &w) {
     const int lane = threadIdx.x & 31;
     w.used[lane] = w.need[lane] = 0;
     __syncwarp();
-    // the page of the column that row i's parent holds (its r), and whether it is full (1) or the tail (0)
-    auto entry_of = [&](int i, int &p, int &full) {
-        p = parent_of(r, i);
-        const int tail = length_of(r, p) / kPage, entry = r.table[(size_t)p * r.pps + j], er = entry / r.pps;
-        const bool ok = entry >= 0 && entry - er * r.pps == j && er < r.n_streams;
-        if (report && !ok && j <= tail && r.status != nullptr) atomicOr(r.status, ST_BAD_ARG);
-        full = j < tail;
-        return ok && j <= tail ? er : -1;
-    };
     int answer = -1;
     for (int i = lane; i < r.n_streams; i += 32) {
-        int p, full;
-        const int er = entry_of(i, p, full);
-        if (er < 0 || !full) continue;
+        const int e = entries[i], er = e & ~kFull;
+        if (e < 0 || !(e & kFull)) continue;
         atomicOr(&w.used[er >> 5], 1u << (er & 31));
         if (store) r.table_out[(size_t)i * r.pps + j] = er * r.pps + j;
         if (i == ask) answer = er * r.pps + j;
@@ -284,9 +287,8 @@ __device__ int reorder_column(const KvReorder &r, int j, int ask, bool store, bo
     for (int base = 0; base < r.n_streams; base += 32) {
         const int i = base + lane;
         const bool in = i < r.n_streams;
-        int p = 0, full = 0;
-        const int er = in ? entry_of(i, p, full) : -1;
-        const bool tail = er >= 0 && !full;
+        const int e = in ? entries[i] : -1, er = e;
+        const bool full = e >= 0 && (e & kFull), tail = e >= 0 && !full;
         const uint32_t same = __match_any_sync(0xffffffffu, tail ? er : -1 - lane);
         const bool takes = tail && (same & ((1u << lane) - 1)) == 0 && !(w.used[er >> 5] >> (er & 31) & 1u);
         __syncwarp();
@@ -295,7 +297,7 @@ __device__ int reorder_column(const KvReorder &r, int j, int ask, bool store, bo
             if (store) r.table_out[(size_t)i * r.pps + j] = er * r.pps + j;
             if (i == ask) answer = er * r.pps + j;
         }
-        const uint32_t wants = __ballot_sync(0xffffffffu, in && !takes && !(er >= 0 && full));
+        const uint32_t wants = __ballot_sync(0xffffffffu, in && !takes && !full);
         if (lane == 0) w.need[base >> 5] = wants;
         __syncwarp();
     }
@@ -310,8 +312,9 @@ __device__ int reorder_column(const KvReorder &r, int j, int ask, bool store, bo
         if (lane >= o) before += t;
     }
     before -= __popc(fw);
-    int taken = 0;
-    for (int base = 0; base < r.n_streams; base += 32) {
+    const int first = store ? 0 : ask & ~31, last = store ? r.n_streams : first + 1;   // (just the row that is asked for)
+    int taken = __reduce_add_sync(0xffffffffu, 32 * lane < first ? __popc(w.need[lane]) : 0);
+    for (int base = first; base < last; base += 32) {
         const uint32_t wants = w.need[base >> 5];
         int k = taken + __popc(wants & ((1u << lane) - 1));
         taken += __popc(wants);
@@ -338,6 +341,7 @@ __device__ int reorder_column(const KvReorder &r, int j, int ask, bool store, bo
 // in use refers to, so copies need no order.
 __global__ void __launch_bounds__(256) k_reorder(const KvReorder r, int table_blocks, int copy_blocks) {
     __shared__ ReorderScratch scratch[8];
+    __shared__ short entries[8][kReorderMaxStreams];
     __shared__ int to_s;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (blockIdx.x < table_blocks) {
@@ -349,7 +353,10 @@ __global__ void __launch_bounds__(256) k_reorder(const KvReorder r, int table_bl
                 if (r.status != nullptr && asked != p) atomicOr(r.status, ST_BAD_ARG);
                 if (r.status != nullptr && r.lens[p] != length_of(r, p)) atomicOr(r.status, ST_BAD_POSITION);
             }
-        if (j < r.pps) reorder_column(r, j, 0, true, true, scratch[warp]);
+        if (j >= r.pps) return;
+        column_entries(r, j, lane, 32, true, entries[warp]);
+        __syncwarp();
+        reorder_column(r, j, 0, true, entries[warp], scratch[warp]);
         return;
     }
     const int i = (blockIdx.x - table_blocks) / copy_blocks, part = (blockIdx.x - table_blocks) % copy_blocks;
@@ -364,8 +371,10 @@ __global__ void __launch_bounds__(256) k_reorder(const KvReorder r, int table_bl
         other |= (tail > col || (tail == col && k < i)) && r.table[(size_t)pk * r.pps + col] == src;
     }
     if (!__syncthreads_or(other)) return;
+    column_entries(r, col, threadIdx.x, 256, false, entries[0]);
+    __syncthreads();
     if (warp == 0) {
-        const int dst = reorder_column(r, col, i, false, false, scratch[0]);
+        const int dst = reorder_column(r, col, i, false, entries[0], scratch[0]);
         if (lane == 0) to_s = dst;
     }
     __syncthreads();
