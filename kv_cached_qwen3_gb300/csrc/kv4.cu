@@ -111,7 +111,7 @@ __device__ __forceinline__ void store_codes(unsigned char *tile, int prow, bool 
 }
 
 // Few rows: grid (items, streams, layers * 2), a head row per 4 * NB threads, rows of a head behind
-// one another.
+// one another. A row of 32 streams in 5 layers: 2.3 us, most of it a launch's own time.
 template <int HD, typename T, bool READ>
 __global__ void __launch_bounds__(kRowThreads) k_kv4_rows(const Kv4Rows r, const bool vec) {
     using Tile = Kv4Tile<HD>;
@@ -149,9 +149,9 @@ __device__ __forceinline__ PageRows page_rows(const Kv4Rows &r, int s, int slot,
 }
 
 // Many rows: a CTA per (page, head), kRowThreads / (4 * NB) rows at a time: one look-up of the page, and
-// all its loads in flight. 28 layers x 4096 rows of 8 heads of 128 dims: f32 written in 199 us (5.4 TB/s of
-// dense rows and codes, 79% of the measured copy), read in 164 (96%); bf16 written in 193 (46%; bound by the
-// quantization's instructions, the same for half the bytes), read in 96 (92%).
+// all its loads in flight. 28 layers x 4096 rows of 8 heads of 128 dims: f32 written in 172 us (6.2 TB/s of
+// dense rows and codes, 92% of the measured copy rate), read in 165 (96%); bf16 written in 141 (63%; bound by
+// the quantization's instructions, nearly the same for half the bytes), read in 96 (92%).
 // Grid (pages * heads, streams, layers * 2) to write and (pages * heads, streams, layers) to read, where a
 // CTA takes K and V, whose loads are small.
 template <int HD, typename T>
@@ -221,8 +221,8 @@ __global__ void __launch_bounds__(kRowThreads) k_kv4_read_pages(const Kv4Rows r,
 
 // From this many rows a stream on, a CTA per page is faster: a page's loads are in flight at once, but a
 // small part of a page leaves most of its CTA without work. 32 streams, 5 layers, 8 heads of 128 in f32,
-// us by rows / by pages: written, 32 rows 13.1 / 19.1, 64 25.0 / 26.3, 128 47.9 / 45.3, 256 92.9 / 80.0;
-// read, 16 rows 6.1 / 6.9, 32 9.8 / 9.6, 64 19.8 / 15.0, 256 71.8 / 61.0. (bf16 alike.)
+// us by rows / by pages: written, 32 rows 11.9 / 17.9, 64 22.8 / 23.8, 128 43.6 / 40.4, 256 84.1 / 70.2;
+// read, 16 rows 6.0 / 6.9, 32 9.8 / 9.5, 64 19.9 / 15.1, 256 72.4 / 61.7. (bf16: 128 rows written 42.3 / 35.0.)
 constexpr int kWritePageRows = 96, kReadPageRows = 32;
 
 template <int HD, typename T, bool READ>
@@ -338,7 +338,9 @@ __device__ int reorder_column(const KvReorder &r, int j, int ask, bool store, co
 // the rows of a tail page that its stream did not take over from its parent: copy_blocks CTAs per
 // stream, a warp per tile. Each finds its destination itself (the column is a few hundred bytes), so
 // that one launch does it all. Sources are pages that stay in use, destinations pages that nothing
-// in use refers to, so copies need no order.
+// in use refers to, so copies need no order. 32 streams of 700 rows in 5 layers 6.6 us, of 8192 rows in
+// 28 layers (tails at a page's end: nothing to copy) 3.2, 512 streams of 1000 rows in 5 layers 37: bound by
+// the chain parents -> lengths -> table -> column of a copying CTA, not by the copies.
 __global__ void __launch_bounds__(256) k_reorder(const KvReorder r, int table_blocks, int copy_blocks) {
     __shared__ ReorderScratch scratch[8];
     __shared__ short entries[8][kReorderMaxStreams];

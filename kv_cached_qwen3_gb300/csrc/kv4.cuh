@@ -85,7 +85,7 @@ __device__ __forceinline__ uint32_t q4_codes8(const float (&x)[8], unsigned shor
     hi = max3_nan(hi, hi2, hi2), lo = min3_nan(lo, lo2, lo2);
     const bool bad = !(hi < INFINITY && lo > -INFINITY);
     float m = hi > -lo ? hi : lo;
-    if (__any_sync(0xffffffffu, hi == -lo && hi > 0.f)) {   // both signs: the first one's
+    if (__any_sync(0xffffffffu, hi == -lo)) {   // both signs: the first one's
         float first = 0.f;
 #pragma unroll
         for (int i = 7; i >= 0; --i)
@@ -95,7 +95,8 @@ __device__ __forceinline__ uint32_t q4_codes8(const float (&x)[8], unsigned shor
             const float other = __shfl_xor_sync(0xffffffffu, first, o), a = lane & o ? other : first, b = lane & o ? first : other;
             first = a != 0.f ? a : b;
         }
-        if (hi == -lo) m = first;
+        const float x0 = __shfl_sync(0xffffffffu, x[0], lane & ~3);   // (of zeros)
+        if (hi == -lo) m = hi > 0.f ? first : x0;
     }
     float y[8], up = 1.f;
 #pragma unroll

@@ -226,7 +226,15 @@ __device__ __forceinline__ int stream_of(const Kv4Attend &a, long long x, long l
 // q (exact where q is bf16), of p and of P, each 2^-12 of a term at most, an eighth of half a step of
 // the result. Codes as they are, times 2^-24; the scores' offset, -8 sum(q) of each block times its
 // scale, is one more MMA over blocks, and one more (A = -8 everywhere) takes off what P V is too large
-// by, 16 keys at a time. (f32 results would lose bits to either: 2e-6 instead of 5e-7 of the result.)
+// by, 16 keys at a time. (f32 results would lose bits to either: an error of 2e-6 of the result instead of
+// 3e-7 for 128 dims and G = 2, for 135 instead of 150 us below.)
+//
+// 64 streams x 8192 rows x 8 KV heads of 128 dims (604 MB of tiles, 89 us at the measured copy rate):
+// bf16, G = 8 128 us; f32, G = 2 150, G = 8 (WIDE) 182; bf16 with 64 dims, G = 8 86 (floor 44.5). About 3% less
+// with all pages in L2, so not DRAM: 1060 instructions a page and warp in bf16 at 2.2 per cycle and
+// multiprocessor (ALU pipe 50%, tensor pipe 33% busy); twelve warps are what 168 registers allow, and with 128
+// registers it spills (178 us). One wave of CTAs over balanced ranges instead of a CTA per split of a
+// row: 144 instead of 164 us.
 template <int HD, bool WIDE, typename TI, typename TO>
 __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Attend a) {
     using Tile = Kv4Tile<HD>;
@@ -239,7 +247,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
     __shared__ float wm[kWarps + 1][kMaxG], wl[kWarps + 1][kMaxG];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     const int G = a.n_q / a.c.n_kv_heads;
-    if (!a.one_unit) pdl_launch_dependents();   // (the joining kernel; another would only take room)
+    if (!a.one_unit) pdl_launch_dependents();   // (the joining kernel, 20.5 -> 22.2 us for 32768 rows if at the end;
+                                                // another would only take room)
     unsigned char *ring = ring_all + warp * kSlots * Tile::kBytes;
     if (lane == 0) {
         for (int i = 0; i < kSlots; ++i) mbar_init(&bars[warp][i], 1);
@@ -653,7 +662,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
 
 // Grid (n_q, B): the parts of rows that several CTAs shared, joined. The maxima and sums of all parts
 // are read at once, then each group of HD threads adds up every kGroups-th part, several in flight.
-// A few rows have many parts each (512 threads: their reads in few steps); many rows have about two.
+// A few rows have many parts each (512 threads: their reads in few steps); many rows have about two. With
+// 128 / 512 threads: 1 stream of 32768 rows x 8 heads 23.0 / 18.8 us, 64 streams of 8192 126 / 151.
 constexpr int kFewThreads = 128, kManyThreads = 512;
 template <int HD, typename TO, int kThreads>
 __global__ void __launch_bounds__(kThreads) k_kv4_combine(const Kv4Attend a, const int grid) {
@@ -747,7 +757,9 @@ cudaError_t launch_hd(const Kv4Attend &a, int in_bf16, int out_bf16, bool pdl, c
 }  // namespace
 
 // CTAs of a launch and whether rows are left whole: with at most kWholePages pages (one or two per
-// warp) the second launch costs more than splitting wins.
+// warp) the second launch costs more than splitting wins. A Talker step over one stream of 300 / 480 / 700 /
+// 1000 rows with 4: 658 / 688 / 681 / 693 us, 8: 625 / 679 / 679 / 693, 12: 625 / 677 / 690 / 694, 16: 626 / 678 /
+// 690 / 818.
 constexpr int kWholePages = 8;
 
 Kv4AttendShape kv4_attend_shape(int B, int n_kv, int max_len, int n_sm) {

@@ -147,6 +147,28 @@ def test_bf16_codes_are_exact(kv4, exponent):
         np.testing.assert_array_equal(c.v[page, 0, 0].cpu().numpy(), ref.tile_bytes(cc, dd, True))
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_blocks_of_zeros_and_of_both_signs(kv4, dt):
+    """The largest magnitude with both signs, and zeros of both signs: the first one gives the scale its sign."""
+    t = torch.zeros(1, 1, 8, 1, 128)
+    t.view(8, 4, 32)[1::2, :, 0] = -0.0
+    t.view(8, 4, 32)[2, :, 1:] = -0.0
+    for i in range(4):
+        t.view(8, 4, 32)[4 + i] = rnd(i, 4, 32).cpu().clamp(-1, 1)
+        t.view(8, 4, 32)[4 + i, 0, [5, 20]] = torch.tensor([2.0, -2.0])
+        t.view(8, 4, 32)[4 + i, 1, [7, 3]] = torch.tensor([2.0, -2.0])
+        t.view(8, 4, 32)[4 + i, 2, [31, 8, 15]] = torch.tensor([2.0, -2.0, 2.0])
+    t = t.to(dtype_of(dt)).cuda()
+    for rows in (t, t.repeat(1, 1, 16, 1, 1)):       # by rows and by pages
+        c = kv4.KV4Cache(1, rows.shape[2], 1, 1, 128)
+        c.write(rows, rows)
+        codes, d = ref.q4_quantize(host(rows)[0, 0, :PAGE, 0])
+        n = len(codes)
+        cc, dd = np.zeros((PAGE, 128), np.uint8), np.zeros((PAGE, 4), np.float16)
+        cc[:n], dd[:n] = codes, d
+        np.testing.assert_array_equal(c.k[0, 0, 0].cpu().numpy(), ref.tile_bytes(cc, dd, False))
+
+
 def test_blocks_with_nan_or_inf_read_back_as_nan(kv4):
     t = rnd(1, 1, 1, 3, 2, 128)
     t[0, 0, 0, 0, 5] = float("nan")
