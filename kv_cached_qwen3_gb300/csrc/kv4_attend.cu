@@ -227,10 +227,10 @@ __device__ __forceinline__ int stream_of(const Kv4Attend &a, long long x, long l
 // the result. Codes as they are, times 2^-24; the scores' offset, -8 sum(q) of each block times its
 // scale, is one more MMA over blocks, and one more (A = -8 everywhere) takes off what P V is too large
 // by, 16 keys at a time. (f32 results would lose bits to either: an error of 2e-6 of the result instead of
-// 3e-7 for 128 dims and G = 2, for 135 instead of 150 us below.)
+// 3e-7 for 128 dims and G = 2, for 15 us less below.)
 //
 // 64 streams x 8192 rows x 8 KV heads of 128 dims (604 MB of tiles, 89 us at the measured copy rate):
-// bf16, G = 8 128 us; f32, G = 2 150, G = 8 (WIDE) 182; bf16 with 64 dims, G = 8 86 (floor 44.5). About 3% less
+// bf16, G = 8 123 us; f32, G = 2 148, G = 8 (WIDE) 178; bf16 with 64 dims, G = 8 80 (floor 44.5). About 3% less
 // with all pages in L2, so not DRAM: 1060 instructions a page and warp in bf16 at 2.2 per cycle and
 // multiprocessor (ALU pipe 50%, tensor pipe 33% busy); twelve warps are what 168 registers allow, and with 128
 // registers it spills (178 us). One wave of CTAs over balanced ranges instead of a CTA per split of a
@@ -660,26 +660,75 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
     }
 }
 
-// Grid (n_q, B): the parts of rows that several CTAs shared, joined. The maxima and sums of all parts
-// are read at once, then each group of HD threads adds up every kGroups-th part, several in flight.
-// A few rows have many parts each (512 threads: their reads in few steps); many rows have about two. With
-// 128 / 512 threads: 1 stream of 32768 rows x 8 heads 23.0 / 18.8 us, 64 streams of 8192 126 / 151.
-constexpr int kFewThreads = 128, kManyThreads = 512;
-template <int HD, typename TO, int kThreads>
-__global__ void __launch_bounds__(kThreads) k_kv4_combine(const Kv4Attend a, const int grid) {
-    constexpr int kGroups = kThreads / HD, kAhead = 8, kWarpsHere = kThreads / 32;
-    __shared__ float weight[kMaxGrid], red[2][kWarpsHere], sums[kGroups][HD];
-    const int b = blockIdx.y, G = a.n_q / a.c.n_kv_heads, g = blockIdx.x / G, h = blockIdx.x % G;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = threadIdx.x % HD, group = threadIdx.x / HD;
-    long long before;   // (lengths were there before the kernel that this one follows)
+// The parts of a row that several CTAs shared: CTAs [first, last] have one each (first == last: none).
+struct Parts {
+    int first, last, tail;   // tail: the first CTA's range began with another row
+};
+__device__ __forceinline__ Parts parts_of(const Kv4Attend &a, int grid, int b, int g) {
+    long long before;
     const long long U = count_units(a, b, before) * a.c.n_kv_heads;
     const int nu = units_of(a, checked_len(a, b));
     const long long n = min(U, (long long)grid), x0 = before * a.c.n_kv_heads + (long long)g * nu;
-    const int first = (int)(((x0 + 1) * n - 1) / U), last = (int)(((x0 + nu) * n - 1) / U);   // CTAs of the row's ends
+    Parts p{(int)(((x0 + 1) * n - 1) / U), (int)(((x0 + nu) * n - 1) / U), 0};   // CTAs of the row's ends
+    p.tail = p.first * U / n != x0;
+    return p;
+}
+template <int HD>
+__device__ __forceinline__ const float *part_at(const Kv4Attend &a, const Parts &p, int i, int h) {
+    return a.scratch + (((size_t)i * 2 + (i == p.first ? p.tail : 0)) * kMaxG + h) * (HD + 4);
+}
+
+// Many rows have about two parts each. Grid (KV heads, B), HD x kJoinHeads threads: a thread has one dim of
+// every kJoinHeads-th head of the group, and reads all it needs at once.
+constexpr int kJoinHeads = 4, kJoinAhead = 4;
+template <int HD, typename TO>
+__global__ void __launch_bounds__(HD * kJoinHeads) k_kv4_join(const Kv4Attend a, const int grid) {
+    const int b = blockIdx.y, g = blockIdx.x, G = a.n_q / a.c.n_kv_heads, d = threadIdx.x % HD;
+    const Parts p = parts_of(a, grid, b, g);   // (lengths were there before the kernel that this one follows)
+    pdl_wait();
+    if (p.first == p.last) return;
+    for (int h = threadIdx.x / HD; h < G; h += kJoinHeads) {
+        float m = -INFINITY, L = 0.f, O = 0.f;
+        for (int i0 = p.first; i0 <= p.last; i0 += kJoinAhead) {
+            float2 ml[kJoinAhead];
+            float o[kJoinAhead];
+#pragma unroll
+            for (int i = 0; i < kJoinAhead; ++i)
+                if (i0 + i <= p.last) {
+                    const float *part = part_at<HD>(a, p, i0 + i, h);
+                    ml[i] = *reinterpret_cast<const float2 *>(part), o[i] = part[4 + d];
+                } else {
+                    ml[i] = make_float2(-INFINITY, 0.f), o[i] = 0.f;
+                }
+            float top = m;
+#pragma unroll
+            for (int i = 0; i < kJoinAhead; ++i) top = fmaxf(top, ml[i].x);
+            const float old = m == -INFINITY ? 0.f : ex2(m - top);
+            L *= old, O *= old, m = top;
+#pragma unroll
+            for (int i = 0; i < kJoinAhead; ++i) {
+                const float e = ml[i].x == -INFINITY ? 0.f : ex2(ml[i].x - top);
+                L = fmaf(ml[i].y, e, L), O = fmaf(o[i], e, O);
+            }
+        }
+        static_cast<TO *>(a.out)[((size_t)b * a.n_q + g * G + h) * HD + d] = (TO)(L == 0.f ? 0.f : O / L);
+    }
+}
+
+// A few rows have many parts each. Grid (n_q, B): the maxima and sums of all parts are read at once, then each
+// group of HD threads adds up every kGroups-th part, several in flight.
+constexpr int kCombineThreads = 512;
+template <int HD, typename TO>
+__global__ void __launch_bounds__(kCombineThreads) k_kv4_combine(const Kv4Attend a, const int grid) {
+    constexpr int kThreads = kCombineThreads, kGroups = kThreads / HD, kAhead = 8, kWarpsHere = kThreads / 32;
+    __shared__ float weight[kMaxGrid], red[2][kWarpsHere], sums[kGroups][HD];
+    const int b = blockIdx.y, G = a.n_q / a.c.n_kv_heads, g = blockIdx.x / G, h = blockIdx.x % G;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = threadIdx.x % HD, group = threadIdx.x / HD;
+    const Parts p = parts_of(a, grid, b, g);
+    const int first = p.first, last = p.last;
     pdl_wait();
     if (first == last) return;
-    const int tail = first * U / n != x0;   // the first CTA begins with another row
-    auto part = [&](int i) { return a.scratch + (((size_t)i * 2 + (i == first ? tail : 0)) * kMaxG + h) * (HD + 4); };
+    auto part = [&](int i) { return part_at<HD>(a, p, i, h); };
     float m = -INFINITY;
     for (int i = first + threadIdx.x; i <= last; i += kThreads) m = fmaxf(m, part(i)[0]);
     m = warp_max(m);
@@ -718,6 +767,10 @@ __global__ void __launch_bounds__(kThreads) k_kv4_combine(const Kv4Attend a, con
     static_cast<TO *>(a.out)[((size_t)b * a.n_q + blockIdx.x) * HD + d] = (TO)(L == 0.f ? 0.f : O / L);
 }
 
+// Parts of a row, if all are alike, from which on it is k_kv4_combine (a CTA per query head) that joins them. With
+// k_kv4_join / with it: 64 streams of 8192 rows x 8 heads (2 parts) 122 / 126 us, 16 streams of up to 2048 (4) 16.5 /
+// 17.7, 7 streams of up to 5001 x 5 heads (13) 13.1 / 11.0, 1 stream of 32768 x 8 heads (57) 24 / 20.
+constexpr int kManyParts = 8;
 template <int HD, typename TI, typename TO>
 cudaError_t launch_t(const Kv4Attend &a, bool pdl, cudaStream_t s) {
     const bool wide = a.n_q / a.c.n_kv_heads > 4 && sizeof(TO) == 4;
@@ -742,10 +795,10 @@ cudaError_t launch_t(const Kv4Attend &a, bool pdl, cudaStream_t s) {
         e = cudaGetLastError();
     }
     if (e != cudaSuccess || a.one_unit) return e;
-    cfg.gridDim = dim3(a.n_q, a.B);
-    const bool many = a.grid >= 8ll * a.B * a.c.n_kv_heads;   // parts per row
-    cfg.blockDim = dim3(many ? kManyThreads : kFewThreads);
-    return cudaLaunchKernelEx(&cfg, many ? k_kv4_combine<HD, TO, kManyThreads> : k_kv4_combine<HD, TO, kFewThreads>, a, a.grid);
+    const bool many = a.grid >= (long long)kManyParts * a.B * a.c.n_kv_heads;
+    cfg.gridDim = dim3(many ? a.n_q : a.c.n_kv_heads, a.B);
+    cfg.blockDim = dim3(many ? kCombineThreads : HD * kJoinHeads);
+    return cudaLaunchKernelEx(&cfg, many ? k_kv4_combine<HD, TO> : k_kv4_join<HD, TO>, a, a.grid);
 }
 
 template <int HD>
