@@ -92,7 +92,8 @@ talker_status talker_kv4_read(const talker_kv4 *c, int layer0, int n_layers, int
  * sums are f32, and codes are exact. With F32, q and the probabilities enter the
  * tensor cores as two fp16 parts (22 bits). With BF16 as one: q exactly (values
  * below 2^-27 of a head's largest lose bits), probabilities rounded to 2^-12 and
- * again times their value's scale, before the result's own 2^-9.
+ * again times their value's scale, before the result's own 2^-9. Values of q are to
+ * lie below 2^116, those of k_new and v_new where products and sums stay finite.
  * A stream without rows gives zeros. A length outside the stream's pages sets
  * status 1 << 0 and gives zeros; keys of a page whose number is out of range
  * are not attended (status 1 << 3).

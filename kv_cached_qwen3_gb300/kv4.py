@@ -170,7 +170,8 @@ class KV4Cache:
         max_len = min(-(-max_len // PAGE), self.pages_per_stream) * PAGE      # whole pages: few different calls
         need = self._scratch.get((B, n_q, max_len))
         if need is None:
-            need = self._scratch[(B, n_q, max_len)] = self._lib.talker_kv4_attend_scratch(self._ref, B, n_q, max_len)
+            with torch.cuda.device(self.device):      # (by its multiprocessors)
+                need = self._scratch[(B, n_q, max_len)] = self._lib.talker_kv4_attend_scratch(self._ref, B, n_q, max_len)
         scratch = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
         launch(self.device.index, self._attend, "talker_kv4_attend", self._ref, layer, B, lens_at, max_len, n_q,
                1.0 / math.sqrt(hd) if scale is None else scale, q.data_ptr(), q.stride(0), kn, vn, new_row,

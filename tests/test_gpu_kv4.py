@@ -432,6 +432,50 @@ def test_select_ties_masks_and_specials(kv4):
     check_select(x, first, torch.tensor([[0, 1, 0, 1]], dtype=torch.int32).cuda(), 299)
 
 
+@pytest.mark.parametrize("V,dt", [(20000, "f32"), (20000, "bf16"), (40003, "f32"), (40003, "bf16")])
+def test_select_long_masked_rows(kv4, V, dt):
+    """Masked values (NaN, -inf, the type's lowest) between, before and after a row's logits, and rows of nothing else;
+    40003: by parts over the whole GPU."""
+    dtype = dtype_of(dt)
+    low = torch.finfo(dtype).min
+    x = (rnd(1, 3, 5, V) * 2).to(dtype)
+    some = rnd(2, V) > 1
+    x[0, 0, some] = float("nan")
+    x[0, 1, : V - 700] = -float("inf")
+    x[0, 2, 900:] = low
+    x[0, 3, :] = float("nan")
+    x[0, 4, some] = low
+    x[1, :, : V // 2] = low
+    x[1, 1] = low
+    x[1, 2, some] = -float("inf")
+    x[2] = -float("inf")            # fewer than five candidates in all
+    x[2, 1, V - 2] = 3.0
+    x[2, 4, 11] = 1.0
+    check_select(x, -10 * rnd(3, 3, 5).abs())
+
+
+def test_rows_past_four_gigabytes(kv4):
+    """Pages whose bytes lie more than 2^32 from the pool's first."""
+    L, H, D = 28, 8, 128
+    n = 4300
+    k = torch.empty(n, L, H, 36 * D, dtype=torch.uint8, device="cuda")
+    assert k.numel() > 2 ** 32
+    c = kv4.KV4Cache.over(k, torch.empty_like(k), torch.tensor([[n - 1, 3], [n - 2, n - 3]], dtype=torch.int32).cuda(), D)
+    for T in (5, 128):
+        kv = [rnd(s, 2, 2, T, H, D) for s in (1, 2)]
+        c.write(kv[0], kv[1], layer0=L - 2)
+        out = [torch.empty_like(t) for t in kv]
+        c.read(*out, layer0=L - 2)
+        for t, o in zip(kv, out):
+            np.testing.assert_array_equal(host(o), ref.q4_roundtrip(host(t)))
+    q = rnd(3, 2, 2 * H, D)
+    got = host(c.attend(L - 1, q, torch.full((2,), 128, dtype=torch.int32).cuda()))
+    K, V = (ref.q4_roundtrip(host(t))[1] for t in kv)
+    for b in range(2):
+        want = ref.attend(host(q)[b], K[b], V[b], D ** -0.5)
+        assert (np.abs(got[b] - want) <= attend_tolerance(host(q)[b], K[b], V[b], D ** -0.5, torch.float32, want)).all()
+
+
 def test_select_strided_rows(kv4):
     x = rnd(1, 2, 3, 515)
     check_select(x[..., 1:500], -rnd(2, 2, 3).abs())
