@@ -66,13 +66,17 @@ __device__ __forceinline__ float half_hi(uint32_t u) { return __half2float(__ush
 __device__ __forceinline__ uint32_t bytes02(uint32_t w) { return w & 0x00ff00ffu; }
 __device__ __forceinline__ uint32_t bytes13(uint32_t w) { return __byte_perm(w, 0, 0x4341); }
 __device__ __forceinline__ uint32_t nibbles(uint32_t bytes) { return bytes & 0x000f000fu; }
-// x - 8 of nibbles or x - 136 of bytes (8 + 16 8) as fp16 values: they go under the exponent of 1024.
+// Centred: bytes 0 and 2, or 1 and 3, are raised under the fp16 exponent of 1024, and 1024 + 8 is taken off
+// their low nibbles, 1024 + 136 (8 + 16 8) off the bytes.
+__device__ __forceinline__ uint32_t raised02(uint32_t w) { return __byte_perm(w, 0x64646464u, 0x4240); }
+__device__ __forceinline__ uint32_t raised13(uint32_t w) { return __byte_perm(w, 0x64646464u, 0x4341); }
 __device__ __forceinline__ uint32_t centred(uint32_t x, uint32_t mid) {
     uint32_t r;
-    asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x | 0x64006400u), "r"(mid));
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(mid));
     return r;
 }
-constexpr uint32_t kMidNibble = 0x64086408u, kMidByte = 0x64886488u;   // 1032, 1160
+__device__ __forceinline__ uint32_t centred_nibbles(uint32_t raised) { return centred(raised & 0xff0fff0fu, 0x64086408u); }
+__device__ __forceinline__ uint32_t centred_bytes(uint32_t raised) { return centred(raised, 0x64886488u); }
 
 // What is left of x after its first 11 bits (the fp16 part that pack_rz keeps), or x where mask is 0.
 __device__ __forceinline__ F2 rest11(F2 x, uint32_t mask) {
@@ -85,9 +89,11 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
-__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+// a times half `hi` of b, twice
+__device__ __forceinline__ uint32_t mul_half2_by(uint32_t a, uint32_t b, bool hi) {
     uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("{.reg .b16 h0, h1; .reg .b32 t; mov.b32 {h0, h1}, %2; mov.b32 t, {h0, h0}; mul.rn.f16x2 %0, %1, t;}"
+        : "=r"(r) : "r"(a), "r"(hi ? b >> 16 : b));
     return r;
 }
 // Half i of the words of a key's scales.
@@ -221,20 +227,20 @@ __device__ __forceinline__ int stream_of(const Kv4Attend &a, long long x, long l
 // transposed between lanes as fp16. The exponents' reference m keeps P in fp16's range: it follows
 // the largest score plus log2 of the largest value scale, and O and l are rescaled when P would
 // pass 2^14, to below 2^9. An accumulator's columns are its lane's heads throughout.
-// f32 results (PREC): codes centred in fp16, q and P in two fp16 parts (22 bits), for up to 4 query
-// heads in columns h and h + 4 of one MMA, above that (WIDE) by two MMAs. bf16 results: one part of
-// q (exact where q is bf16), of p and of P, each 2^-12 of a term at most, an eighth of half a step of
-// the result. Codes as they are, times 2^-24; the scores' offset, -8 sum(q) of each block times its
-// scale, is one more MMA over blocks, and one more (A = -8 everywhere) takes off what P V is too large
-// by, 16 keys at a time. (f32 results would lose bits to either: an error of 2e-6 of the result instead of
-// 3e-7 for 128 dims and G = 2, for 15 us less below.)
+// V codes are centred in fp16 before the MMA (with codes as they are, another MMA that takes off 8 times
+// P costs 123 instead of 117 us below). f32 results (PREC): K codes too, q and P in two fp16 parts (22 bits),
+// for up to 4 query heads in columns h and h + 4 of one MMA, above that (WIDE) by two MMAs. bf16 results:
+// one part of q (exact where q is bf16), of p and of P, each 2^-12 of a term at most, an eighth of half a
+// step of the result; K codes as they are, times 2^-24, and the scores' offset, -8 sum(q) of each block
+// times its scale, by one more MMA over blocks. (f32 results would lose bits to that: an error of 2e-6
+// of the result instead of 3e-7 for 128 dims and G = 2.)
 //
 // 64 streams x 8192 rows x 8 KV heads of 128 dims (604 MB of tiles, 89 us at the measured copy rate):
-// bf16, G = 8 123 us; f32, G = 2 148, G = 8 (WIDE) 178; bf16 with 64 dims, G = 8 80 (floor 44.5). About 3% less
-// with all pages in L2, so not DRAM: 1060 instructions a page and warp in bf16 at 2.2 per cycle and
-// multiprocessor (ALU pipe 50%, tensor pipe 33% busy); twelve warps are what 168 registers allow, and with 128
-// registers it spills (178 us). One wave of CTAs over balanced ranges instead of a CTA per split of a
-// row: 144 instead of 164 us.
+// bf16, G = 8 115 us; f32, G = 2 130, G = 8 (WIDE) 162; bf16 with 64 dims, G = 8 76 (floor 44.5). About 3% less
+// with all pages in L2, so not DRAM: 1110 instructions a page and warp in bf16 at 2.2 per cycle and
+// multiprocessor, 340 of them on the ALU pipe (masks and byte permutations of codes), which takes one in two
+// cycles; twelve warps are what 168 registers allow, and with 128 registers it spills (178 instead of 144
+// us). One wave of CTAs over balanced ranges instead of a CTA per split of a row: 144 instead of 164 us.
 template <int HD, bool WIDE, typename TI, typename TO>
 __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Attend a) {
     using Tile = Kv4Tile<HD>;
@@ -247,7 +253,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
     __shared__ float wm[kWarps + 1][kMaxG], wl[kWarps + 1][kMaxG];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     const int G = a.n_q / a.c.n_kv_heads;
-    if (!a.one_unit) pdl_launch_dependents();   // (the joining kernel, 20.5 -> 22.2 us for 32768 rows if at the end;
+    if (!a.one_unit) pdl_launch_dependents();   // (the joining kernel; at the end 2 us more for 32768 rows;
                                                 // another would only take room)
     unsigned char *ring = ring_all + warp * kSlots * Tile::kBytes;
     if (lane == 0) {
@@ -263,7 +269,6 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
     const int b0 = stream_of(a, x_begin, before), len0 = checked_len(a, b0), nu0 = units_of(a, len0);
     int slot = 0, phase = 0;   // where the next K tile goes, and the parity that each slot's next wait has
     const uint32_t lo_mask = kParts == 1 || c >= 2 ? 0xffffe000u : 0u;
-    const uint32_t eight[4] = {0x80088008u, 0x80888088u, 0x80088008u, 0x80888088u};   // -8 2^-24 (nibbles), -136 2^-24 (bytes)
     // Of 8 keys, row 2 c of the scores (and so slot 2 c of P) is key c and row 2 c + 1 key c2: the
     // two rows of codes that eight lanes load together lie in other banks.
     const int c2 = 4 + (c ^ 1), key_r = r & 1 ? 4 + ((r >> 1) ^ 1) : r >> 1;
@@ -380,8 +385,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
 
         float m0 = -INFINITY, m1 = -INFINITY;     // references of the exponents of this lane's columns
         F2 l2 = f2(0.f, 0.f);                     // its keys' parts of their sums
-        // dim 32 (t / 2) + 4 r + 2 (t % 2), and it plus 16 times the next one (e >= 2), of heads 2 c, 2 c + 1;
-        // with V codes as they are, times 2^-24
+        // dim 32 (t / 2) + 4 r + 2 (t % 2), and it plus 16 times the next one (e >= 2), of heads 2 c, 2 c + 1
         float o[2 * NB][4];
 #pragma unroll
         for (int t = 0; t < 2 * NB; ++t)
@@ -431,8 +435,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
                             const uint32_t w0 = t ? bytes13(k0.w[nb]) : bytes02(k0.w[nb]), w1 = t ? bytes13(k1.w[nb]) : bytes02(k1.w[nb]);
                             uint32_t codes[4] = {nibbles(w0), nibbles(w1), w0, w1};
                             if (PREC) {
-                                codes[0] = centred(codes[0], kMidNibble), codes[1] = centred(codes[1], kMidNibble);
-                                codes[2] = centred(w0, kMidByte), codes[3] = centred(w1, kMidByte);
+                                const uint32_t x0 = t ? raised13(k0.w[nb]) : raised02(k0.w[nb]);
+                                const uint32_t x1 = t ? raised13(k1.w[nb]) : raised02(k1.w[nb]);
+                                codes[0] = centred_nibbles(x0), codes[1] = centred_nibbles(x1);
+                                codes[2] = centred_bytes(x0), codes[3] = centred_bytes(x1);
                             }
                             if (t == 0) mma16816_new(acc, codes, qf[nb][0][0], qf[nb][0][1]);
                             else mma16816(acc, codes, qf[nb][1][0], qf[nb][1][1]);
@@ -520,18 +526,17 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
                         p[i] = f2(ex2(f2_lo(x)), ex2(f2_hi(x)));
                         l2 = l2 + p[i];
                     }
-                    Words<H> v[4], d[4];   // of slots 2 c, 2 c + 1 and 8 further
+                    Words<H> v[4], d[2];   // codes of slots 2 c, 2 c + 1 and 8 further, scales of p's keys
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int key = 16 * ks + 8 * (i >> 1) + (i & 1 ? c2 : c);
                         v[i].load(vt + key * Tile::kRow + r * 2 * NB);
-                        if (!PREC) d[i].load(vt + Tile::kScales + key * NB * 2);
                     }
-                    uint32_t pt[2];
+                    uint32_t pp[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        if (PREC) d[i].load(vt + Tile::kScales + (16 * ks + 8 * i + key_r) * NB * 2);   // of p's keys
-                        else pt[i] = transpose8(pack_rn(f2_lo(p[i]), f2_hi(p[i])));
+                        d[i].load(vt + Tile::kScales + (16 * ks + 8 * i + key_r) * NB * 2);
+                        if (!PREC) pp[i] = pack_rn(f2_lo(p[i]), f2_hi(p[i]));
                     }
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb) {
@@ -540,7 +545,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             if (!PREC) {
-                                ph[i] = mul_half2(pt[i], __byte_perm(d[2 * i].w[nb / 2], d[2 * i + 1].w[nb / 2], sel));
+                                ph[i] = transpose8(mul_half2_by(pp[i], d[i].w[nb / 2], nb & 1));
                             } else {
                                 const float e = scale_at(d[i].w, nb);
                                 const F2 y = f2(f2_lo(p[i]) * e, f2_hi(p[i]) * e), z = rest11(y, lo_mask);
@@ -553,17 +558,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             float(&acc)[4] = o[2 * nb + e];
-                            const uint32_t x0 = e ? bytes13(u0) : bytes02(u0), x1 = e ? bytes13(u1) : bytes02(u1);
-                            if (PREC) {
-                                const uint32_t codes[4] = {centred(nibbles(x0), kMidNibble), centred(x0, kMidByte),
-                                                           centred(nibbles(x1), kMidNibble), centred(x1, kMidByte)};
-                                if (WIDE) mma16816(acc, codes, ph[0], ph[1]);
-                                mma16816(acc, codes, pl[0], pl[1]);
-                            } else {
-                                const uint32_t codes[4] = {nibbles(x0), x0, nibbles(x1), x1};
-                                mma16816(acc, eight, ph[0], ph[1]);
-                                mma16816(acc, codes, ph[0], ph[1]);
-                            }
+                            const uint32_t x0 = e ? raised13(u0) : raised02(u0), x1 = e ? raised13(u1) : raised02(u1);
+                            const uint32_t codes[4] = {centred_nibbles(x0), centred_bytes(x0), centred_nibbles(x1), centred_bytes(x1)};
+                            if (!PREC || WIDE) mma16816(acc, codes, ph[0], ph[1]);
+                            if (PREC) mma16816(acc, codes, pl[0], pl[1]);
                         }
                     }
                 }
@@ -612,7 +610,6 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 float y = e < 2 ? o[t][e] : (o[t][e] - o[t][e - 2]) * 0.0625f;
-                if (!PREC) y *= 16777216.f;
                 if (kParts == 2) y += __shfl_xor_sync(0xffffffffu, y, 2);   // the parts of head h: columns h and h + 4
                 const int h = 2 * c + (e & 1), dim = 32 * (t >> 1) + 4 * r + 2 * (t & 1) + (e >> 1);
                 if (kParts == 1 || c < 2) wo[(warp * kMaxG + h) * HD + dim] = y;
