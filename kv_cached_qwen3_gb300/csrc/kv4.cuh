@@ -205,16 +205,18 @@ struct Kv4Attend {
     int64_t q_row, new_row;
     void *out;
     float scale;
-    int grid, one_unit;   // Kv4AttendShape
+    int grid, one_unit, ctas;   // Kv4AttendShape
     float *scratch;
 };
 // CTAs of a launch, and whether each (stream, KV head) row is one CTA's work (no scratch then).
 struct Kv4AttendShape {
     int grid, one_unit;
+    int ctas;        // CTAs that a multiprocessor holds
+    int full_grid;   // the grid of any more work than this
 };
 Kv4AttendShape kv4_attend_shape(int B, int n_kv, int max_len, int n_sm);
-int kv4_attend_full_grid(int n_sm);   // the largest such grid
 size_t kv4_attend_scratch(const Kv4AttendShape &p, int head_dim);
+size_t kv4_attend_scratch(int grid, int head_dim);
 cudaError_t prepare_kv4_attend();   // shared-memory limits, on the current device
 int kv4_multiprocessors();          // of the current device, prepared as above (0: an error)
 // pdl: starts while the kernel before it drains, which must not write lengths, page numbers or rows below

@@ -12,8 +12,9 @@ namespace talker_k {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kCtas = 3;                  // CTAs a multiprocessor holds: 12 warps, 168 registers
-constexpr int kSlots = 3;                 // tiles (a page's K, its V, the next page's K ...) a warp has in shared memory
+constexpr int kFewCtas = 3, kManyCtas = 4;   // CTAs a multiprocessor holds, by units (kv4_attend_shape)
+// Tiles that a warp has in shared memory. 3: a page's K, its V, the next page's K ...; 2: K and V, each refilled once used.
+constexpr int slots_of(int hd, int ctas) { return hd == 128 && ctas == kManyCtas ? 2 : 3; }
 constexpr int kMaxG = 8;
 constexpr int kMaxGrid = 1024;            // CTAs of a launch
 constexpr float kLog2e = 1.4426950408889634f;
@@ -137,8 +138,8 @@ __device__ __forceinline__ bool bounded_wait(uint64_t *bar, uint32_t parity) {
     return true;
 }
 
-constexpr size_t attend_smem(int hd) {
-    return (size_t)kWarps * kSlots * kv4_tile_bytes(hd) + (size_t)kWarps * kMaxG * hd * 4;
+constexpr size_t attend_smem(int hd, int ctas) {
+    return (size_t)kWarps * slots_of(hd, ctas) * kv4_tile_bytes(hd) + (size_t)kWarps * kMaxG * hd * 4;
 }
 
 // Eight dims of a query head; vec: rows lie on 16-byte boundaries.
@@ -241,11 +242,11 @@ __device__ __forceinline__ int stream_of(const Kv4Attend &a, long long x, long l
 // multiprocessor, 340 of them on the ALU pipe (masks and byte permutations of codes), which takes one in two
 // cycles; twelve warps are what 168 registers allow, and with 128 registers it spills (178 instead of 144
 // us). One wave of CTAs over balanced ranges instead of a CTA per split of a row: 144 instead of 164 us.
-template <int HD, bool WIDE, typename TI, typename TO>
-__global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Attend a) {
+template <int HD, bool WIDE, typename TI, typename TO, int CTAS>
+__global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Attend a) {
     using Tile = Kv4Tile<HD>;
     constexpr bool PREC = sizeof(TO) == 4;
-    constexpr int NB = Tile::NB;
+    constexpr int NB = Tile::NB, kSlots = slots_of(HD, CTAS);
     constexpr int kParts = PREC && !WIDE ? 2 : 1;       // columns of P per query head
     constexpr int kCorrBits = 10;
     extern __shared__ __align__(128) unsigned char ring_all[];
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
         page = __shfl_sync(0xffffffffu, pages, 0);
         page1 = __shfl_sync(0xffffffffu, pages, 1);
         if (lane == 0 && n_it > 0) issue(slot, a.c.k, page, g), issue(after(slot), a.c.v, page, g);
-        if (lane == 0 && n_it > 1) issue(after(after(slot)), a.c.k, page1, g);
+        if (kSlots == 3 && lane == 0 && n_it > 1) issue(after(after(slot)), a.c.k, page1, g);
     };
     open(b0, (int)((x_begin - before) / nu0), len0, nu0, (int)((x_begin - before) % nu0), x_end - x_begin);
     pdl_wait();   // before it: lengths, page numbers and cached rows, which the kernel before does not write
@@ -466,9 +467,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
                 }
             }
             __syncwarp();
-            if (lane == 0 && it + 1 < n_it) {   // the next page's V over this K
+            if (lane == 0 && it + 1 < n_it) {   // the next page's V (of two slots: K) over this K
                 fence_proxy_async();
-                issue(slot, a.c.v, page1, at.g);
+                issue(slot, kSlots == 3 ? a.c.v : a.c.k, page1, at.g);
             }
             failed = !wait(vslot);
             if (failed) break;
@@ -567,9 +568,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) k_kv4_attend(const Kv4Atte
                 }
             }
             __syncwarp();
-            if (lane == 0 && it + 2 < n_it) {   // the K after the next over this V
+            if (lane == 0 && it + (kSlots == 3 ? 2 : 1) < n_it) {   // the K after the next (V of the next) over this V
                 fence_proxy_async();
-                issue(vslot, a.c.k, page2, at.g);
+                issue(vslot, kSlots == 3 ? a.c.k : a.c.v, kSlots == 3 ? page2 : page1, at.g);
             }
             slot = after(vslot);
             page = page1;
@@ -769,10 +770,16 @@ __global__ void __launch_bounds__(kCombineThreads) k_kv4_combine(const Kv4Attend
 // 17.7, 7 streams of up to 5001 x 5 heads (13) 13.1 / 11.0, 1 stream of 32768 x 8 heads (57) 24 / 20.
 constexpr int kManyParts = 8;
 template <int HD, typename TI, typename TO>
-cudaError_t launch_t(const Kv4Attend &a, bool pdl, cudaStream_t s) {
+cudaError_t launch_t(Kv4Attend a, bool pdl, cudaStream_t s) {
     const bool wide = a.n_q / a.c.n_kv_heads > 4 && sizeof(TO) == 4;
-    void (*kernel)(Kv4Attend) = k_kv4_attend<HD, false, TI, TO>;
-    if constexpr (sizeof(TO) == 4) kernel = wide ? k_kv4_attend<HD, true, TI, TO> : kernel;
+    void (*kernel)(Kv4Attend) = a.ctas == kManyCtas ? k_kv4_attend<HD, false, TI, TO, kManyCtas> : k_kv4_attend<HD, false, TI, TO, kFewCtas>;
+    if constexpr (sizeof(TO) == 4)
+        if (wide) {   // (162 us above instead of 164, which spills)
+            if (a.ctas == kManyCtas) a.grid = std::max(1, a.grid * kFewCtas / kManyCtas);
+            a.ctas = kFewCtas;
+            kernel = k_kv4_attend<HD, true, TI, TO, kFewCtas>;
+        }
+    const size_t smem = attend_smem(HD, a.ctas);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -784,11 +791,11 @@ cudaError_t launch_t(const Kv4Attend &a, bool pdl, cudaStream_t s) {
     if (pdl) {
         cfg.gridDim = dim3(a.grid);
         cfg.blockDim = dim3(kWarps * 32);
-        cfg.dynamicSmemBytes = attend_smem(HD);
+        cfg.dynamicSmemBytes = smem;
         e = cudaLaunchKernelEx(&cfg, kernel, a);
         cfg.dynamicSmemBytes = 0;
     } else {
-        kernel<<<a.grid, kWarps * 32, attend_smem(HD), s>>>(a);
+        kernel<<<a.grid, kWarps * 32, smem, s>>>(a);
         e = cudaGetLastError();
     }
     if (e != cudaSuccess || a.one_unit) return e;
@@ -817,31 +824,38 @@ Kv4AttendShape kv4_attend_shape(int B, int n_kv, int max_len, int n_sm) {
     Kv4AttendShape p;
     p.one_unit = pages <= kWholePages;
     const long long units = p.one_unit ? rows : rows * ((pages + kWarps - 1) / kWarps);
-    p.grid = (int)std::max<long long>(1, std::min<long long>(units, kv4_attend_full_grid(n_sm)));
+    p.ctas = units <= (long long)kFewCtas * n_sm ? kFewCtas : kManyCtas;
+    p.full_grid = std::min(p.ctas * n_sm, kMaxGrid);
+    p.grid = (int)std::max<long long>(1, std::min<long long>(units, p.full_grid));
     return p;
 }
 
-int kv4_attend_full_grid(int n_sm) { return std::min(kCtas * n_sm, kMaxGrid); }
-
 size_t kv4_attend_scratch(const Kv4AttendShape &p, int head_dim) {
-    return p.one_unit ? 0 : (size_t)p.grid * 2 * kMaxG * (head_dim + 4) * sizeof(float);
+    return p.one_unit ? 0 : kv4_attend_scratch(p.grid, head_dim);
+}
+size_t kv4_attend_scratch(int grid, int head_dim) {
+    return (size_t)grid * 2 * kMaxG * (head_dim + 4) * sizeof(float);
 }
 
-template <int HD, bool WIDE, typename TI, typename TO>
+template <int HD, bool WIDE, typename TI, typename TO, int CTAS>
 cudaError_t raise_one() {
-    return cudaFuncSetAttribute(k_kv4_attend<HD, WIDE, TI, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attend_smem(HD));
+    return cudaFuncSetAttribute(k_kv4_attend<HD, WIDE, TI, TO, CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)attend_smem(HD, CTAS));
 }
-template <int HD>
+template <int HD, int CTAS>
 cudaError_t raise_hd() {
-    cudaError_t e = raise_one<HD, false, float, float>();
-    e = e ? e : raise_one<HD, true, float, float>();
-    e = e ? e : raise_one<HD, false, float, __nv_bfloat16>();
-    return e ? e : raise_one<HD, false, __nv_bfloat16, __nv_bfloat16>();
+    cudaError_t e = raise_one<HD, false, float, float, CTAS>();
+    e = e ? e : raise_one<HD, false, float, __nv_bfloat16, CTAS>();
+    return e ? e : raise_one<HD, false, __nv_bfloat16, __nv_bfloat16, CTAS>();
 }
 
 cudaError_t prepare_kv4_attend() {
-    cudaError_t e = raise_hd<128>();
-    return e ? e : raise_hd<64>();
+    cudaError_t e = raise_hd<128, kFewCtas>();
+    e = e ? e : raise_hd<128, kManyCtas>();
+    e = e ? e : raise_hd<64, kFewCtas>();
+    e = e ? e : raise_hd<64, kManyCtas>();
+    e = e ? e : raise_one<128, true, float, float, kFewCtas>();
+    return e ? e : raise_one<64, true, float, float, kFewCtas>();
 }
 
 int kv4_multiprocessors() {
@@ -906,7 +920,7 @@ talker_status talker_kv4_attend(const talker_kv4 *c, int layer, int B, const int
     const Kv4AttendShape shape = shape_here(c, B, max_len);
     const size_t need = kv4_attend_scratch(shape, c->head_dim);
     if (need > 0 && (!scratch || scratch_bytes < need || (reinterpret_cast<uintptr_t>(scratch) & 15u))) return TALKER_EINVAL;
-    const Kv4Attend a{*c, layer, B, n_q_heads, lens, q, k_new, v_new, q_row, new_row, out, scale, shape.grid, shape.one_unit,
+    const Kv4Attend a{*c, layer, B, n_q_heads, lens, q, k_new, v_new, q_row, new_row, out, scale, shape.grid, shape.one_unit, shape.ctas,
                       static_cast<float *>(scratch)};
     const int bf16 = dtype == TALKER_DTYPE_BF16;
     if (launch_kv4_attend(a, bf16, bf16, false, static_cast<cudaStream_t>(cuda_stream)) != cudaSuccess) {

@@ -232,9 +232,9 @@ constexpr int kAttnMmMinPages = 3;
 void attn_config(const talker *t, int B, int max_len, int *splits, int *cluster, int *mm) {
     if (t->kv_q4) {   // its own attention: a CTA per (row, KV group), or balanced ranges of pages over the GPU
         const Kv4AttendShape shape = kv4_attend_shape(B, t->nkv, max_len, t->n_sm);
-        *splits = shape.one_unit ? shape.grid : kv4_attend_full_grid(t->n_sm);
+        *splits = shape.one_unit ? shape.grid : shape.full_grid;
         *cluster = shape.one_unit;
-        *mm = 0;
+        *mm = shape.ctas;   // (which of its kernels)
         return;
     }
     const int pages_max = (max_len + 1 + kPageRows - 1) / kPageRows;
@@ -450,7 +450,7 @@ talker_status enqueue_q4_decode(talker *t, cudaStream_t st, int B, int layer, co
     TRY_CUDA(launch_qkv_post(t->raw, B, t->nq, t->nkv, t->hd, d.q_norm, d.k_norm, t->d_rope, t->c.rms_eps, t->q, cache_view(t),
                              layer, rm, t->d_status, st, nullptr, t->kv_rows));
     const Kv4Attend a{kv4_view(t), layer, B, t->nq, t->d_len, t->q, t->kv_rows, t->kv_rows + (size_t)B * t->kvd, t->qd, t->kvd,
-                      out, 1.0f / sqrtf((float)t->hd), grid, t->attn_cluster, t->q4_ws};
+                      out, 1.0f / sqrtf((float)t->hd), grid, t->attn_cluster, t->attn_mm, t->q4_ws};
     TRY_CUDA(launch_kv4_attend(a, 0, out_bf16, true, st));
     *nk += t->attn_cluster ? 2 : 3;
     return TALKER_OK;
@@ -1010,7 +1010,7 @@ talker_status talker_kv_init_batched(talker_t *t, int n_streams, int max_seq_len
     TRY_CUDA(cudaMemcpy(t->d_pt, pt.data(), n_pages * sizeof(int), cudaMemcpyHostToDevice));
     TRY_CUDA(cudaMalloc(&t->d_reorder, (n_pages + n_streams) * sizeof(int)));
     if (t->kv_q4) {
-        TRY_CUDA(cudaMalloc(&t->q4_ws, kv4_attend_scratch({kv4_attend_full_grid(t->n_sm), 0}, t->hd)));
+        TRY_CUDA(cudaMalloc(&t->q4_ws, kv4_attend_scratch(kv4_attend_shape(n_streams, t->nkv, pps * kPageRows, t->n_sm).full_grid, t->hd)));
         TRY_CUDA(cudaMalloc(&t->kv_rows, (size_t)2 * n_streams * t->kvd * sizeof(float)));
     }
     TRY_CUDA(cudaMalloc(&t->d_len, n_streams * sizeof(int)));
