@@ -214,7 +214,7 @@ struct Kv4AttendShape {
     int ctas;        // CTAs that a multiprocessor holds
     int full_grid;   // the grid of any more work than this
 };
-Kv4AttendShape kv4_attend_shape(int B, int n_kv, int max_len, int n_sm);
+Kv4AttendShape kv4_attend_shape(int B, int n_kv, int hd, int max_len, int n_sm);
 size_t kv4_attend_scratch(const Kv4AttendShape &p, int head_dim);
 size_t kv4_attend_scratch(int grid, int head_dim);
 cudaError_t prepare_kv4_attend();   // shared-memory limits, on the current device

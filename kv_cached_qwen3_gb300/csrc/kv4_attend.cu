@@ -14,7 +14,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kFewCtas = 3, kManyCtas = 4;   // CTAs a multiprocessor holds, by units (kv4_attend_shape)
 // Tiles that a warp has in shared memory. 3: a page's K, its V, the next page's K ...; 2: K and V, each refilled once used.
-constexpr int slots_of(int hd, int ctas) { return hd == 128 && ctas == kManyCtas ? 2 : 3; }
+constexpr int slots_of(int ctas) { return ctas == kManyCtas ? 2 : 3; }
 constexpr int kMaxG = 8;
 constexpr int kMaxGrid = 1024;            // CTAs of a launch
 constexpr float kLog2e = 1.4426950408889634f;
@@ -139,7 +139,7 @@ __device__ __forceinline__ bool bounded_wait(uint64_t *bar, uint32_t parity) {
 }
 
 constexpr size_t attend_smem(int hd, int ctas) {
-    return (size_t)kWarps * slots_of(hd, ctas) * kv4_tile_bytes(hd) + (size_t)kWarps * kMaxG * hd * 4;
+    return (size_t)kWarps * slots_of(ctas) * kv4_tile_bytes(hd) + (size_t)kWarps * kMaxG * hd * 4;
 }
 
 // Eight dims of a query head; vec: rows lie on 16-byte boundaries.
@@ -237,16 +237,16 @@ __device__ __forceinline__ int stream_of(const Kv4Attend &a, long long x, long l
 // of the result instead of 3e-7 for 128 dims and G = 2.)
 //
 // 64 streams x 8192 rows x 8 KV heads of 128 dims (604 MB of tiles, 89 us at the measured copy rate):
-// bf16, G = 8 115 us; f32, G = 2 130, G = 8 (WIDE) 162; bf16 with 64 dims, G = 8 76 (floor 44.5). About 3% less
-// with all pages in L2, so not DRAM: 1110 instructions a page and warp in bf16 at 2.2 per cycle and
+// bf16, G = 8 111 us; f32, G = 2 126, G = 8 (WIDE) 162; bf16 with 64 dims, G = 8 76 (floor 44.5). About 3% less
+// with all pages in L2, so not DRAM: 1120 instructions a page and warp in bf16 at 2.4 per cycle and
 // multiprocessor, 340 of them on the ALU pipe (masks and byte permutations of codes), which takes one in two
-// cycles; twelve warps are what 168 registers allow, and with 128 registers it spills (178 instead of 144
-// us). One wave of CTAs over balanced ranges instead of a CTA per split of a row: 144 instead of 164 us.
+// cycles; the rest is the latency that its 12 or 16 warps do not hide (kv4_attend_shape). One wave of CTAs over
+// balanced ranges instead of a CTA per split of a row: 144 instead of 164 us.
 template <int HD, bool WIDE, typename TI, typename TO, int CTAS>
 __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Attend a) {
     using Tile = Kv4Tile<HD>;
     constexpr bool PREC = sizeof(TO) == 4;
-    constexpr int NB = Tile::NB, kSlots = slots_of(HD, CTAS);
+    constexpr int NB = Tile::NB, kSlots = slots_of(CTAS);
     constexpr int kParts = PREC && !WIDE ? 2 : 1;       // columns of P per query head
     constexpr int kCorrBits = 10;
     extern __shared__ __align__(128) unsigned char ring_all[];
@@ -772,9 +772,11 @@ constexpr int kManyParts = 8;
 template <int HD, typename TI, typename TO>
 cudaError_t launch_t(Kv4Attend a, bool pdl, cudaStream_t s) {
     const bool wide = a.n_q / a.c.n_kv_heads > 4 && sizeof(TO) == 4;
-    void (*kernel)(Kv4Attend) = a.ctas == kManyCtas ? k_kv4_attend<HD, false, TI, TO, kManyCtas> : k_kv4_attend<HD, false, TI, TO, kFewCtas>;
+    void (*kernel)(Kv4Attend) = k_kv4_attend<HD, false, TI, TO, kFewCtas>;
+    if constexpr (HD == 128)
+        if (a.ctas == kManyCtas) kernel = k_kv4_attend<HD, false, TI, TO, kManyCtas>;
     if constexpr (sizeof(TO) == 4)
-        if (wide) {   // (162 us above instead of 164, which spills)
+        if (wide) {   // (162 us above; with 128 registers, which spills, 164)
             if (a.ctas == kManyCtas) a.grid = std::max(1, a.grid * kFewCtas / kManyCtas);
             a.ctas = kFewCtas;
             kernel = k_kv4_attend<HD, true, TI, TO, kFewCtas>;
@@ -819,12 +821,18 @@ cudaError_t launch_hd(const Kv4Attend &a, int in_bf16, int out_bf16, bool pdl, c
 // 690 / 818.
 constexpr int kWholePages = 8;
 
-Kv4AttendShape kv4_attend_shape(int B, int n_kv, int max_len, int n_sm) {
+// Three or four CTAs a multiprocessor: four hide more latency and finish more units at once, but have two tiles
+// in flight per warp instead of three. us with 3 / 4, 8 KV heads of 128 dims, G = 2, bf16 unless said: 64 streams
+// of 8192 rows, G = 8 115 / 111; 32 of up to 4096 35.3 / 33.6 (all of 4096: 37.9 / 38.3); 16 of up to 2048 15.2 / 12.4
+// (all of 2048: 17.5 / 18.9); 2 of 16384 18.2 / 16.8; 1 of 32768 16.6 / 17.2, of 131072 35.9 / 37.3; with a row to a
+// CTA, 100 streams of 500 20.1 / 23.4; with 64 dims, 7 of up to 5001, G = 7 13.6 / 15.3.
+Kv4AttendShape kv4_attend_shape(int B, int n_kv, int hd, int max_len, int n_sm) {
     const long long rows = (long long)B * n_kv, pages = ((long long)max_len + kPage - 1) / kPage;
     Kv4AttendShape p;
     p.one_unit = pages <= kWholePages;
     const long long units = p.one_unit ? rows : rows * ((pages + kWarps - 1) / kWarps);
-    p.ctas = units <= (long long)kFewCtas * n_sm ? kFewCtas : kManyCtas;
+    const bool many = hd == 128 && B > 1 && !p.one_unit && units > (long long)kFewCtas * n_sm;
+    p.ctas = many ? kManyCtas : kFewCtas;
     p.full_grid = std::min(p.ctas * n_sm, kMaxGrid);
     p.grid = (int)std::max<long long>(1, std::min<long long>(units, p.full_grid));
     return p;
@@ -853,7 +861,6 @@ cudaError_t prepare_kv4_attend() {
     cudaError_t e = raise_hd<128, kFewCtas>();
     e = e ? e : raise_hd<128, kManyCtas>();
     e = e ? e : raise_hd<64, kFewCtas>();
-    e = e ? e : raise_hd<64, kManyCtas>();
     e = e ? e : raise_one<128, true, float, float, kFewCtas>();
     return e ? e : raise_one<64, true, float, float, kFewCtas>();
 }
@@ -894,7 +901,7 @@ bool attend_sizes_ok(const talker_kv4 *c, int B, int n_q, int max_len) {
 
 Kv4AttendShape shape_here(const talker_kv4 *c, int B, int max_len) {
     const int n_sm = std::max(kv4_multiprocessors(), 1);
-    return kv4_attend_shape(B, c->n_kv_heads, std::min(max_len, c->pages_per_stream * kPage), n_sm);
+    return kv4_attend_shape(B, c->n_kv_heads, c->head_dim, std::min(max_len, c->pages_per_stream * kPage), n_sm);
 }
 
 }  // namespace

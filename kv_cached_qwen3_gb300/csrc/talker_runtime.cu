@@ -231,7 +231,7 @@ constexpr int kAttnMmMinPages = 3;
 
 void attn_config(const talker *t, int B, int max_len, int *splits, int *cluster, int *mm) {
     if (t->kv_q4) {   // its own attention: a CTA per (row, KV group), or balanced ranges of pages over the GPU
-        const Kv4AttendShape shape = kv4_attend_shape(B, t->nkv, max_len, t->n_sm);
+        const Kv4AttendShape shape = kv4_attend_shape(B, t->nkv, t->hd, max_len, t->n_sm);
         *splits = shape.one_unit ? shape.grid : shape.full_grid;
         *cluster = shape.one_unit;
         *mm = shape.ctas;   // (which of its kernels)
@@ -1010,7 +1010,8 @@ talker_status talker_kv_init_batched(talker_t *t, int n_streams, int max_seq_len
     TRY_CUDA(cudaMemcpy(t->d_pt, pt.data(), n_pages * sizeof(int), cudaMemcpyHostToDevice));
     TRY_CUDA(cudaMalloc(&t->d_reorder, (n_pages + n_streams) * sizeof(int)));
     if (t->kv_q4) {
-        TRY_CUDA(cudaMalloc(&t->q4_ws, kv4_attend_scratch(kv4_attend_shape(n_streams, t->nkv, pps * kPageRows, t->n_sm).full_grid, t->hd)));
+        const int grid = kv4_attend_shape(n_streams, t->nkv, t->hd, pps * kPageRows, t->n_sm).full_grid;   // the largest
+        TRY_CUDA(cudaMalloc(&t->q4_ws, kv4_attend_scratch(grid, t->hd)));
         TRY_CUDA(cudaMalloc(&t->kv_rows, (size_t)2 * n_streams * t->kvd * sizeof(float)));
     }
     TRY_CUDA(cudaMalloc(&t->d_len, n_streams * sizeof(int)));
