@@ -297,6 +297,33 @@ def test_attend_long(kv4, n, B, H, G, D):
     assert torch.equal(outs[2], again)
 
 
+@pytest.mark.parametrize("G,dt,fresh", [(1, "bf16", True), (2, "f32", False), (4, "f32", True), (8, "bf16", False),
+                                        (8, "f32", True)])
+def test_attend_many_streams(kv4, G, dt, fresh):
+    """More work than a wave of CTAs, of very different lengths: ranges that hold many rows, and parts of rows."""
+    B, n, H, D = 40, 1000, 8, 128
+    c, K, V = filled(kv4, B, n, H, D, 14)
+    rng = np.random.default_rng(G)
+    lens = [int(x) for x in rng.integers(0, n + 1, B)]
+    lens[:6] = [0, 1, 64, n, 0, 63]
+    lens[-1] = 0
+    outs = [check_attend(kv4, c, K, V, lens, H, G, D, dtype_of(dt), fresh) for _ in range(2)]
+    assert torch.equal(outs[0], outs[1])
+    check_attend(kv4, c, K, V, [n] * B, H, G, D, dtype_of(dt), fresh)
+    assert c.sync_status() == 0
+    # a page that is not there, and a length past the pages: those streams alone are told apart
+    c.page_table[3, 2] = c.n_pages
+    lens[7] = 16 * PAGE + 1
+    q = rnd(60, B, H * G, D, dtype=dtype_of(dt))
+    got = host(c.attend(0, q, torch.tensor(lens, dtype=torch.int32).cuda()))
+    for b in (2, 3, 7, 8):
+        keep = np.r_[0:128, 192:n] if b == 3 else np.arange(0 if b == 7 else lens[b])
+        want = ref.attend(host(q)[b], K[b, keep], V[b, keep], D ** -0.5)
+        tol = attend_tolerance(host(q)[b], K[b, keep], V[b, keep], D ** -0.5, dtype_of(dt), want)
+        assert (np.abs(got[b] - want) <= tol).all(), b
+    assert c.sync_status() == 9
+
+
 def test_attend_packed_rows_and_scales(kv4):
     c, K, V = filled(kv4, 3, 100, 2, 128, 13)
     check_attend(kv4, c, K, V, [100, 64, 5], 2, 3, 128, torch.bfloat16, True, packed=True)
