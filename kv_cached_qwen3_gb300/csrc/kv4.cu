@@ -252,20 +252,17 @@ __device__ __forceinline__ int parent_of(const KvReorder &r, int i) {
 }
 __device__ __forceinline__ int length_of(const KvReorder &r, int p) { return min(max(r.lens[p], 0), r.pps * kPage); }
 
-// What row i's parent holds of column j: its page's r, plus kFull if the page is full (else it is the
-// tail), or -1. Rows first, first + step, ...
+// What stream p, whose tail page is in column `tail`, holds of column j: its page's r, plus kFull if the page
+// is full (else it is the tail), or -1.
 constexpr int kFull = 0x4000;
-__device__ __forceinline__ void column_entries(const KvReorder &r, int j, int first, int step, bool report, short *entries) {
-#pragma unroll 4
-    for (int i = first; i < r.n_streams; i += step) {
-        const int p = parent_of(r, i), tail = length_of(r, p) / kPage, entry = r.table[(size_t)p * r.pps + j], er = entry / r.pps;
-        const bool ok = entry >= 0 && entry - er * r.pps == j && er < r.n_streams;
-        if (report && !ok && j <= tail && r.status != nullptr) atomicOr(r.status, ST_BAD_ARG);
-        entries[i] = (short)(ok && j <= tail ? er | (j < tail ? kFull : 0) : -1);
-    }
+__device__ __forceinline__ int entry_of(const KvReorder &r, int j, int p, int tail, bool report) {
+    const int entry = r.table[(size_t)p * r.pps + j], er = entry / r.pps;
+    const bool ok = entry >= 0 && entry - er * r.pps == j && er < r.n_streams;
+    if (report && !ok && j <= tail && r.status != nullptr) atomicOr(r.status, ST_BAD_ARG);
+    return ok && j <= tail ? er | (j < tail ? kFull : 0) : -1;
 }
 
-// One warp finds column j of the new table from its entries. Row i keeps its parent's page where that is full
+// One warp finds column j of the new table from the entries of its rows' parents. Row i keeps its parent's page where that is full
 // (shared), and takes it over at the parent's tail page, unless a row before it did (another child) or a
 // stream shares the page (as one may after this one was cut shorter); every other row needs a page of
 // its own, and gets the pages of the column's set {r * pps + j} that no kept entry uses, in order. A row
@@ -338,8 +335,8 @@ __device__ int reorder_column(const KvReorder &r, int j, int ask, bool store, co
 // the rows of a tail page that its stream did not take over from its parent: copy_blocks CTAs per
 // stream, a warp per tile. Each finds its destination itself (the column is a few hundred bytes), so
 // that one launch does it all. Sources are pages that stay in use, destinations pages that nothing
-// in use refers to, so copies need no order. 32 streams of 700 rows in 5 layers 6.6 us, of 8192 rows in
-// 28 layers (tails at a page's end: nothing to copy) 3.2, 512 streams of 1000 rows in 5 layers 37: bound by
+// in use refers to, so copies need no order. 32 streams of 700 rows in 5 layers 6.2 us, of 8192 rows in
+// 28 layers (tails at a page's end: nothing to copy) 3.2, 512 streams of 1000 rows in 5 layers 36: bound by
 // the chain parents -> lengths -> table -> column of a copying CTA, not by the copies.
 __global__ void __launch_bounds__(256) k_reorder(const KvReorder r, int table_blocks, int copy_blocks) {
     __shared__ ReorderScratch scratch[8];
@@ -356,31 +353,35 @@ __global__ void __launch_bounds__(256) k_reorder(const KvReorder r, int table_bl
                 if (r.status != nullptr && r.lens[p] != length_of(r, p)) atomicOr(r.status, ST_BAD_POSITION);
             }
         if (j >= r.pps) return;
-        column_entries(r, j, lane, 32, true, entries[warp]);
+#pragma unroll 4
+        for (int k = lane; k < r.n_streams; k += 32) {
+            const int pk = parent_of(r, k);
+            entries[warp][k] = (short)entry_of(r, j, pk, length_of(r, pk) / kPage, true);
+        }
         __syncwarp();
         reorder_column(r, j, 0, true, entries[warp], scratch[warp]);
         return;
     }
     const int i = (blockIdx.x - table_blocks) / copy_blocks, part = (blockIdx.x - table_blocks) % copy_blocks;
     const int p = parent_of(r, i), len = length_of(r, p);
+    int k = threadIdx.x, pk = k < r.n_streams ? parent_of(r, k) : 0, tail = length_of(r, pk) / kPage;
     const int col = len / kPage, rows = len % kPage;
     if (rows == 0) return;
-    const int src = r.table[(size_t)p * r.pps + col], sr = src / r.pps;
-    if (src < 0 || src - sr * r.pps != col || sr >= r.n_streams) return;
+    const int sr = entry_of(r, col, p, col, false);
     int other = 0;   // whether a row before i takes the page over, or a stream shares it
-    for (int k = threadIdx.x; k < r.n_streams; k += 256) {
-        const int pk = parent_of(r, k), tail = length_of(r, pk) / kPage;
-        other |= (tail > col || (tail == col && k < i)) && r.table[(size_t)pk * r.pps + col] == src;
+    while (k < r.n_streams) {
+        const int e = entry_of(r, col, pk, tail, false);
+        entries[0][k] = (short)e;
+        other |= e >= 0 && (e & ~kFull) == sr && ((e & kFull) || k < i);
+        if ((k += 256) < r.n_streams) pk = parent_of(r, k), tail = length_of(r, pk) / kPage;
     }
-    if (!__syncthreads_or(other)) return;
-    column_entries(r, col, threadIdx.x, 256, false, entries[0]);
-    __syncthreads();
+    if (!__syncthreads_or(other) || sr < 0) return;
     if (warp == 0) {
         const int dst = reorder_column(r, col, i, false, entries[0], scratch[0]);
         if (lane == 0) to_s = dst;
     }
     __syncthreads();
-    const int dst = to_s, t = part * 8 + warp;
+    const int src = sr * r.pps + col, dst = to_s, t = part * 8 + warp;
     if (t >= 2 * r.n_tiles) return;
     unsigned char *pool = t < r.n_tiles ? r.k : r.v;
     const size_t off = (size_t)(t < r.n_tiles ? t : t - r.n_tiles) * r.tile_bytes;
