@@ -49,12 +49,6 @@ __device__ __forceinline__ uint32_t pack_rz(float lo, float hi) {
     asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// ... and to nearest
-__device__ __forceinline__ uint32_t pack_rn(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 __device__ __forceinline__ uint32_t pack_half(__half lo, __half hi) {
     return (uint32_t)__half_as_ushort(lo) | ((uint32_t)__half_as_ushort(hi) << 16);
 }
@@ -88,13 +82,6 @@ __device__ __forceinline__ F2 rest11(F2 x, uint32_t mask) {
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t r;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-    return r;
-}
-// a times half `hi` of b, twice
-__device__ __forceinline__ uint32_t mul_half2_by(uint32_t a, uint32_t b, bool hi) {
-    uint32_t r;
-    asm("{.reg .b16 h0, h1; .reg .b32 t; mov.b32 {h0, h1}, %2; mov.b32 t, {h0, h0}; mul.rn.f16x2 %0, %1, t;}"
-        : "=r"(r) : "r"(a), "r"(hi ? b >> 16 : b));
     return r;
 }
 // Half i of the words of a key's scales.
@@ -228,13 +215,11 @@ __device__ __forceinline__ int stream_of(const Kv4Attend &a, long long x, long l
 // transposed between lanes as fp16. The exponents' reference m keeps P in fp16's range: it follows
 // the largest score plus log2 of the largest value scale, and O and l are rescaled when P would
 // pass 2^14, to below 2^9. An accumulator's columns are its lane's heads throughout.
-// V codes are centred in fp16 before the MMA (with codes as they are, another MMA that takes off 8 times
-// P costs 123 instead of 117 us below). f32 results (PREC): K codes too, q and P in two fp16 parts (22 bits),
-// for up to 4 query heads in columns h and h + 4 of one MMA, above that (WIDE) by two MMAs. bf16 results:
-// one part of q (exact where q is bf16), of p and of P, each 2^-12 of a term at most, an eighth of half a
-// step of the result; K codes as they are, times 2^-24, and the scores' offset, -8 sum(q) of each block
-// times its scale, by one more MMA over blocks. (f32 results would lose bits to that: an error of 2e-6
-// of the result instead of 3e-7 for 128 dims and G = 2.)
+// V codes are centred in fp16 before the MMA. P is held in two fp16 parts (22 bits): for up to 4 query heads in
+// columns h and h + 4 of one MMA, above that (WIDE) by two MMAs. f32 results (PREC): K codes centred too, and q in
+// two parts likewise. bf16 results: q in one part; K codes as they are, times 2^-24, and the scores'
+// offset, -8 sum(q) of each block times its scale, by one more MMA over blocks. (f32 results would lose bits to
+// that: an error of 2e-6 of the result instead of 3e-7 for 128 dims and G = 2.)
 //
 // 64 streams x 8192 rows x 8 KV heads of 128 dims (604 MB of tiles, 89 us at the measured copy rate):
 // bf16, G = 8 111 us; f32, G = 2 126, G = 8 (WIDE) 162; bf16 with 64 dims, G = 8 76 (floor 44.5). About 3% less
@@ -247,7 +232,8 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
     using Tile = Kv4Tile<HD>;
     constexpr bool PREC = sizeof(TO) == 4;
     constexpr int NB = Tile::NB, kSlots = slots_of(CTAS);
-    constexpr int kParts = PREC && !WIDE ? 2 : 1;       // columns of P per query head
+    constexpr int kParts = WIDE ? 1 : 2;                // columns of P per query head
+    constexpr int kQParts = PREC ? kParts : 1;          // ... that hold parts of q (else both hold q)
     constexpr int kCorrBits = 10;
     extern __shared__ __align__(128) unsigned char ring_all[];
     __shared__ __align__(8) uint64_t bars[kWarps][kSlots];
@@ -360,7 +346,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
                     const float y = i & 1 ? x[nb][i] * qs * 0.0625f : fmaf(x[nb][i + 1], qs * -0.0625f, x[nb][i] * qs);
                     hi[i] = __float2half_rn(y);
                     lo[i] = __float2half_rn(y - __half2float(hi[i]));
-                    if (kParts == 2 && r >= 4) hi[i] = lo[i];
+                    if (kQParts == 2 && r >= 4) hi[i] = lo[i];
                     if (!PREC) sum = fmaf(__half2float(hi[i]), i & 1 ? 17.f : 1.f, sum);
                 }
 #pragma unroll
@@ -443,7 +429,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
                             }
                             if (t == 0) mma16816_new(acc, codes, qf[nb][0][0], qf[nb][0][1]);
                             else mma16816(acc, codes, qf[nb][1][0], qf[nb][1][1]);
-                            if (WIDE) mma16816(acc, codes, ql[nb][t][0], ql[nb][t][1]);
+                            if (WIDE && PREC) mma16816(acc, codes, ql[nb][t][0], ql[nb][t][1]);
                         }
                         const float e0 = scale_at(d0.w, nb), e1 = scale_at(d1.w, nb);
                         s0 = f2(fmaf(e0, acc[0], f2_lo(s0)), fmaf(e0, acc[1], f2_hi(s0)));
@@ -456,7 +442,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         F2 &x = sc[i][u];
-                        if (kParts == 2)   // the parts of head h: columns h and h + 4
+                        if (kQParts == 2)   // the parts of head h: columns h and h + 4
                             x = x + f2(__shfl_xor_sync(0xffffffffu, f2_lo(x), 2), __shfl_xor_sync(0xffffffffu, f2_hi(x), 2));
                         x = x * fs;
                     }
@@ -479,8 +465,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
                     for (int i = valid * NB + lane; i < kPage * NB; i += 32) reinterpret_cast<unsigned short *>(d)[i] = 0;
                     __syncwarp();
                 }
-                // exponent of the largest value scale (a NaN is no size), at least that of the smallest fp16, or 0
-                // where p itself is held in fp16
+                // exponent of the largest value scale (a NaN is no size), at least that of the smallest fp16
                 int de;
                 {
                     __half2 top = __float2half2_rn(0.f);
@@ -493,7 +478,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
                             top = __hmax2(top, __habs2(*reinterpret_cast<__half2 *>(&d.w[i])));
                     }
                     const uint32_t dmax = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(__low2float(top), __high2float(top))));
-                    de = max((int)(dmax >> 23) - 126, PREC ? -24 : 0);
+                    de = max((int)(dmax >> 23) - 126, -24);
                 }
                 F2 mx = f2(-INFINITY, -INFINITY);
 #pragma unroll
@@ -533,26 +518,18 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
                         const int key = 16 * ks + 8 * (i >> 1) + (i & 1 ? c2 : c);
                         v[i].load(vt + key * Tile::kRow + r * 2 * NB);
                     }
-                    uint32_t pp[2];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        d[i].load(vt + Tile::kScales + (16 * ks + 8 * i + key_r) * NB * 2);
-                        if (!PREC) pp[i] = pack_rn(f2_lo(p[i]), f2_hi(p[i]));
-                    }
+                    for (int i = 0; i < 2; ++i) d[i].load(vt + Tile::kScales + (16 * ks + 8 * i + key_r) * NB * 2);
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb) {
                         const uint32_t sel = nb & 1 ? 0x7632 : 0x5410;   // halves nb % 2 of two keys' words
                         uint32_t ph[2], pl[2];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            if (!PREC) {
-                                ph[i] = transpose8(mul_half2_by(pp[i], d[i].w[nb / 2], nb & 1));
-                            } else {
-                                const float e = scale_at(d[i].w, nb);
-                                const F2 y = f2(f2_lo(p[i]) * e, f2_hi(p[i]) * e), z = rest11(y, lo_mask);
-                                if (WIDE) ph[i] = transpose8(pack_rz(f2_lo(y), f2_hi(y)));
-                                pl[i] = transpose8(pack_rz(f2_lo(z), f2_hi(z)));
-                            }
+                            const float e = scale_at(d[i].w, nb);
+                            const F2 y = f2(f2_lo(p[i]) * e, f2_hi(p[i]) * e), z = rest11(y, lo_mask);
+                            if (WIDE) ph[i] = transpose8(pack_rz(f2_lo(y), f2_hi(y)));
+                            pl[i] = transpose8(pack_rz(f2_lo(z), f2_hi(z)));
                         }
                         const uint32_t u0 = __byte_perm(v[0].w[nb / 2], v[1].w[nb / 2], sel);
                         const uint32_t u1 = __byte_perm(v[2].w[nb / 2], v[3].w[nb / 2], sel);
@@ -561,8 +538,8 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
                             float(&acc)[4] = o[2 * nb + e];
                             const uint32_t x0 = e ? raised13(u0) : raised02(u0), x1 = e ? raised13(u1) : raised02(u1);
                             const uint32_t codes[4] = {centred_nibbles(x0), centred_bytes(x0), centred_nibbles(x1), centred_bytes(x1)};
-                            if (!PREC || WIDE) mma16816(acc, codes, ph[0], ph[1]);
-                            if (PREC) mma16816(acc, codes, pl[0], pl[1]);
+                            if (WIDE) mma16816(acc, codes, ph[0], ph[1]);
+                            mma16816(acc, codes, pl[0], pl[1]);
                         }
                     }
                 }
@@ -771,16 +748,15 @@ __global__ void __launch_bounds__(kCombineThreads) k_kv4_combine(const Kv4Attend
 constexpr int kManyParts = 8;
 template <int HD, typename TI, typename TO>
 cudaError_t launch_t(Kv4Attend a, bool pdl, cudaStream_t s) {
-    const bool wide = a.n_q / a.c.n_kv_heads > 4 && sizeof(TO) == 4;
+    const bool wide = a.n_q / a.c.n_kv_heads > 4;
     void (*kernel)(Kv4Attend) = k_kv4_attend<HD, false, TI, TO, kFewCtas>;
     if constexpr (HD == 128)
         if (a.ctas == kManyCtas) kernel = k_kv4_attend<HD, false, TI, TO, kManyCtas>;
-    if constexpr (sizeof(TO) == 4)
-        if (wide) {   // (162 us above; with 128 registers, which spills, 164)
-            if (a.ctas == kManyCtas) a.grid = std::max(1, a.grid * kFewCtas / kManyCtas);
-            a.ctas = kFewCtas;
-            kernel = k_kv4_attend<HD, true, TI, TO, kFewCtas>;
-        }
+    if (wide) {   // (162 us above; with 128 registers, which spills, 164)
+        if (a.ctas == kManyCtas) a.grid = std::max(1, a.grid * kFewCtas / kManyCtas);
+        a.ctas = kFewCtas;
+        kernel = k_kv4_attend<HD, true, TI, TO, kFewCtas>;
+    }
     const size_t smem = attend_smem(HD, a.ctas);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -850,19 +826,19 @@ cudaError_t raise_one() {
     return cudaFuncSetAttribute(k_kv4_attend<HD, WIDE, TI, TO, CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)attend_smem(HD, CTAS));
 }
-template <int HD, int CTAS>
-cudaError_t raise_hd() {
-    cudaError_t e = raise_one<HD, false, float, float, CTAS>();
-    e = e ? e : raise_one<HD, false, float, __nv_bfloat16, CTAS>();
-    return e ? e : raise_one<HD, false, __nv_bfloat16, __nv_bfloat16, CTAS>();
+template <int HD, bool WIDE, int CTAS>
+cudaError_t raise_types() {
+    cudaError_t e = raise_one<HD, WIDE, float, float, CTAS>();
+    e = e ? e : raise_one<HD, WIDE, float, __nv_bfloat16, CTAS>();
+    return e ? e : raise_one<HD, WIDE, __nv_bfloat16, __nv_bfloat16, CTAS>();
 }
 
 cudaError_t prepare_kv4_attend() {
-    cudaError_t e = raise_hd<128, kFewCtas>();
-    e = e ? e : raise_hd<128, kManyCtas>();
-    e = e ? e : raise_hd<64, kFewCtas>();
-    e = e ? e : raise_one<128, true, float, float, kFewCtas>();
-    return e ? e : raise_one<64, true, float, float, kFewCtas>();
+    cudaError_t e = raise_types<128, false, kFewCtas>();
+    e = e ? e : raise_types<128, false, kManyCtas>();
+    e = e ? e : raise_types<64, false, kFewCtas>();
+    e = e ? e : raise_types<128, true, kFewCtas>();
+    return e ? e : raise_types<64, true, kFewCtas>();
 }
 
 int kv4_multiprocessors() {
