@@ -55,14 +55,14 @@ __device__ __forceinline__ uint32_t pack_half(__half lo, __half hi) {
 __device__ __forceinline__ float half_lo(uint32_t u) { return __half2float(__ushort_as_half((unsigned short)u)); }
 __device__ __forceinline__ float half_hi(uint32_t u) { return __half2float(__ushort_as_half((unsigned short)(u >> 16))); }
 
-// Two codes share a byte, and both operands made of it are the byte's low part: the low nibble n0 by
-// one AND, and the whole byte n0 + 16 n1, whose product takes n0's part along (the other operand, or
-// the result, takes it off again). As fp16 subnormals both are exact, times 2^-24.
-__device__ __forceinline__ uint32_t bytes02(uint32_t w) { return w & 0x00ff00ffu; }
+// Two codes share a byte. As they are: its nibbles n0 and 16 n1 by an AND each, exact as fp16 subnormals
+// (times 2^-24).
 __device__ __forceinline__ uint32_t bytes13(uint32_t w) { return __byte_perm(w, 0, 0x4341); }
-__device__ __forceinline__ uint32_t nibbles(uint32_t bytes) { return bytes & 0x000f000fu; }
+__device__ __forceinline__ uint32_t low_nibbles(uint32_t bytes) { return bytes & 0x000f000fu; }
+__device__ __forceinline__ uint32_t high_nibbles(uint32_t bytes) { return bytes & 0x00f000f0u; }
 // Centred: bytes 0 and 2, or 1 and 3, are raised under the fp16 exponent of 1024, and 1024 + 8 is taken off
-// their low nibbles, 1024 + 136 (8 + 16 8) off the bytes.
+// their low nibbles, 1024 + 136 (8 + 16 8) off the bytes n0 + 16 n1, whose product takes n0's part along (the
+// other operand, or the result, takes it off again).
 __device__ __forceinline__ uint32_t raised02(uint32_t w) { return __byte_perm(w, 0x64646464u, 0x4240); }
 __device__ __forceinline__ uint32_t raised13(uint32_t w) { return __byte_perm(w, 0x64646464u, 0x4341); }
 __device__ __forceinline__ uint32_t centred(uint32_t x, uint32_t mid) {
@@ -216,8 +216,8 @@ __device__ __forceinline__ int stream_of(const Kv4Attend &a, long long x, long l
 // the largest score plus log2 of the largest value scale, and O and l are rescaled when P would
 // pass 2^14, to below 2^9. An accumulator's columns are its lane's heads throughout.
 // V codes are centred in fp16 before the MMA. P is held in two fp16 parts (22 bits): for up to 4 query heads in
-// columns h and h + 4 of one MMA, above that (WIDE) by two MMAs. f32 results (PREC): K codes centred too, and q in
-// two parts likewise. bf16 results: q in one part; K codes as they are, times 2^-24, and the scores'
+// columns h and h + 4 of one MMA, above that (WIDE) by two MMAs. So is q where it is f32 (QTWO); a bf16 q is exact
+// in one part. f32 results (PREC): K codes centred too. bf16 results: K codes as they are, times 2^-24, and the scores'
 // offset, -8 sum(q) of each block times its scale, by one more MMA over blocks. (f32 results would lose bits to
 // that: an error of 2e-6 of the result instead of 3e-7 for 128 dims and G = 2.)
 //
@@ -233,7 +233,8 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
     constexpr bool PREC = sizeof(TO) == 4;
     constexpr int NB = Tile::NB, kSlots = slots_of(CTAS);
     constexpr int kParts = WIDE ? 1 : 2;                // columns of P per query head
-    constexpr int kQParts = PREC ? kParts : 1;          // ... that hold parts of q (else both hold q)
+    constexpr bool QTWO = sizeof(TI) == 4;              // q has two parts, in WIDE's second MMA or in columns of their own
+    constexpr int kQParts = QTWO ? kParts : 1;
     constexpr int kCorrBits = 10;
     extern __shared__ __align__(128) unsigned char ring_all[];
     __shared__ __align__(8) uint64_t bars[kWarps][kSlots];
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
         const int hq = kParts == 2 ? r & 3 : r;
         const bool q_vec = (reinterpret_cast<uintptr_t>(a.q) & 15u) == 0 && a.q_row * sizeof(TI) % 16 == 0;
         const float cs = a.scale * kLog2e;
-        uint32_t qf[NB][2][2], ql[NB][2][2];       // (ql: WIDE only)
+        uint32_t qf[NB][2][2], ql[NB][2][2];       // (ql: WIDE and QTWO)
         uint32_t qc = 0;                           // (unless PREC) -8 sum(q) of two blocks, times 2^kCorrBits: lanes
                                                    // c < H have a first part, lanes c - H its rest
         F2 fs;                                     // from these units to scores in base 2, of this lane's columns 2 c, 2 c + 1
@@ -342,12 +343,13 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
                 __half hi[8], lo[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    // of the byte that holds dims i and i + 1: the part of n0 alone, and that of n0 + 16 n1
-                    const float y = i & 1 ? x[nb][i] * qs * 0.0625f : fmaf(x[nb][i + 1], qs * -0.0625f, x[nb][i] * qs);
+                    // of the byte that holds dims i and i + 1: n0's part, and that of 16 n1 (PREC: of n0 + 16 n1)
+                    const float y = i & 1 ? x[nb][i] * qs * 0.0625f
+                                          : PREC ? fmaf(x[nb][i + 1], qs * -0.0625f, x[nb][i] * qs) : x[nb][i] * qs;
                     hi[i] = __float2half_rn(y);
                     lo[i] = __float2half_rn(y - __half2float(hi[i]));
                     if (kQParts == 2 && r >= 4) hi[i] = lo[i];
-                    if (!PREC) sum = fmaf(__half2float(hi[i]), i & 1 ? 17.f : 1.f, sum);
+                    if (!PREC) sum = fmaf(__half2float(hi[i]) + (WIDE && QTWO ? __half2float(lo[i]) : 0.f), i & 1 ? 16.f : 1.f, sum);
                 }
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
@@ -419,9 +421,12 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
                         float acc[4];
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
-                            const uint32_t w0 = t ? bytes13(k0.w[nb]) : bytes02(k0.w[nb]), w1 = t ? bytes13(k1.w[nb]) : bytes02(k1.w[nb]);
-                            uint32_t codes[4] = {nibbles(w0), nibbles(w1), w0, w1};
-                            if (PREC) {
+                            uint32_t codes[4];
+                            if (!PREC) {
+                                const uint32_t w0 = t ? bytes13(k0.w[nb]) : k0.w[nb], w1 = t ? bytes13(k1.w[nb]) : k1.w[nb];
+                                codes[0] = low_nibbles(w0), codes[1] = low_nibbles(w1);
+                                codes[2] = high_nibbles(w0), codes[3] = high_nibbles(w1);
+                            } else {
                                 const uint32_t x0 = t ? raised13(k0.w[nb]) : raised02(k0.w[nb]);
                                 const uint32_t x1 = t ? raised13(k1.w[nb]) : raised02(k1.w[nb]);
                                 codes[0] = centred_nibbles(x0), codes[1] = centred_nibbles(x1);
@@ -429,7 +434,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
                             }
                             if (t == 0) mma16816_new(acc, codes, qf[nb][0][0], qf[nb][0][1]);
                             else mma16816(acc, codes, qf[nb][1][0], qf[nb][1][1]);
-                            if (WIDE && PREC) mma16816(acc, codes, ql[nb][t][0], ql[nb][t][1]);
+                            if (WIDE && QTWO) mma16816(acc, codes, ql[nb][t][0], ql[nb][t][1]);
                         }
                         const float e0 = scale_at(d0.w, nb), e1 = scale_at(d1.w, nb);
                         s0 = f2(fmaf(e0, acc[0], f2_lo(s0)), fmaf(e0, acc[1], f2_hi(s0)));

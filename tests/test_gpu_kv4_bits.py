@@ -107,7 +107,7 @@ DT = {"f32": torch.float32, "bf16": torch.bfloat16}
 
 @pytest.mark.parametrize("H,G,D", [(2, 1, 64), (2, 2, 128), (1, 4, 128), (2, 5, 64), (3, 8, 128), (1, 7, 128)])
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
-@pytest.mark.parametrize("s", [0.05])
+@pytest.mark.parametrize("s", [0.05, 1.0, 4.0])
 def test_random_rows(kv4, H, G, D, dt, s):
     lens = [1, 2, 3, 5, 64, 200]
     k, v = rnd(1, 6, 200, H, D), rnd(2, 6, 200, H, D)
@@ -129,3 +129,18 @@ def test_one_key_above_many(kv4, G, dt, bits, mag):
     v = (1 + torch.rand(1, n, 1, D, generator=torch.Generator().manual_seed(1))) * mag
     v[0, 7] *= 2.0 ** -8
     run(kv4, k.cuda(), v.cuda(), q.to(DT[dt]).cuda(), [n], bits * math.log(2) / D)
+
+
+@pytest.mark.parametrize("G,D", [(1, 64), (4, 128), (5, 128), (8, 64)])
+def test_bf16_queries_are_exact(kv4, G, D):
+    """Two keys whose exact scores are equal, one on even dims and one on odd ones, at a score of 100: values of
+    opposite sign cancel. q has numbers whose sixteenths need all of bf16's bits beside them."""
+    k = torch.zeros(1, 2, 1, D)
+    k[0, 0, 0, ::2] = 1.0
+    k[0, 1, 0, 1::2] = 1.0
+    v = rnd(2, 1, 2, 1, D)
+    v[0, 1] = -v[0, 0]
+    v[0, :, :, ::32] = torch.tensor([4.0, -4.0]).view(2, 1, 1).cuda()
+    for a in (255, 253, 251, 193, 129):
+        q = torch.full((1, G, D), a / 128, dtype=torch.bfloat16)
+        run(kv4, k.cuda(), v, q.cuda(), [2], 100 / (D / 2 * a / 128))
