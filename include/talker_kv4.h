@@ -90,9 +90,11 @@ talker_status talker_kv4_read(const talker_kv4 *c, int layer0, int n_layers, int
  * [head_dim] are dense per head, with row strides q_row and new_row in
  * elements; out is contiguous; all are dtype (F32 or BF16). Scores, maxima and
  * sums are f32, and codes are exact. Probabilities, times their value's scale, enter
- * the tensor cores as two fp16 parts (22 bits); so does q with F32, and with BF16
- * exactly (values below 2^-26 of a head's largest lose bits). Values of q are to lie
- * below 2^116, those of k_new and v_new where products and sums stay finite.
+ * the tensor cores as two fp16 parts (22 bits, down to 2^-31 of the largest
+ * probability times the largest scale of the block of dims, for scales from 2^-13);
+ * so does q with F32, and with BF16 exactly (values below 2^-26 of a head's largest
+ * lose bits). Values of q are to lie below 2^116, those of k_new and v_new where
+ * products and sums stay finite.
  * A stream without rows gives zeros. A length outside the stream's pages sets
  * status 1 << 0 and gives zeros; keys of a page whose number is out of range
  * are not attended (status 1 << 3).

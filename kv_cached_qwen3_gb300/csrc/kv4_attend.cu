@@ -18,8 +18,10 @@ constexpr int slots_of(int ctas) { return ctas == kManyCtas ? 2 : 3; }
 constexpr int kMaxG = 8;
 constexpr int kMaxGrid = 1024;            // CTAs of a launch
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kTopBits = 14;              // probabilities times value scales stay below 2^14 (fp16) ...
-constexpr int kNewBits = 9;               // ... and are brought below 2^9 when they would pass it
+constexpr int kTopBits = 11;              // probabilities stay below 2^11 ...
+constexpr int kNewBits = 6;               // ... and the largest is brought to 2^6 when one would pass it
+constexpr int kTopScale = 4;              // value scales stay below 2^4, times their block's power of two ...
+constexpr int kNewScale = 2;              // ... which brings the largest to [2^2, 2^3) when one would pass it
 
 __device__ __forceinline__ float ex2(float x) {   // relative error about 2^-22, 0 at -inf
     float y;
@@ -43,10 +45,10 @@ __device__ __forceinline__ void mma1688_new(float (&d)[4], uint32_t a0, uint32_t
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(b), "f"(0.f));
 }
-// (lo, hi) as an fp16 pair, rounded towards zero
-__device__ __forceinline__ uint32_t pack_rz(float lo, float hi) {
+// (lo, hi) as an fp16 pair, rounded to nearest
+__device__ __forceinline__ uint32_t pack_rn(float lo, float hi) {
     uint32_t r;
-    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
 __device__ __forceinline__ uint32_t pack_half(__half lo, __half hi) {
@@ -73,15 +75,31 @@ __device__ __forceinline__ uint32_t centred(uint32_t x, uint32_t mid) {
 __device__ __forceinline__ uint32_t centred_nibbles(uint32_t raised) { return centred(raised & 0xff0fff0fu, 0x64086408u); }
 __device__ __forceinline__ uint32_t centred_bytes(uint32_t raised) { return centred(raised, 0x64886488u); }
 
-// What is left of x after its first 11 bits (the fp16 part that pack_rz keeps), or x where mask is 0.
-__device__ __forceinline__ F2 rest11(F2 x, uint32_t mask) {
-    const F2 first = f2(__uint_as_float((uint32_t)x.v & mask), __uint_as_float((uint32_t)(x.v >> 32) & mask));
-    return fma2(first, f2(-1.f, -1.f), x);
-}
 // Transposes an 8 x 8 matrix of fp16 pairs: from row r, columns 2 c and 2 c + 1 to rows 2 c and 2 c + 1, column r.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t r;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// Two numbers p = ph + pl times half `hi` of d, as two fp16 parts again: x = ph d rounded, y the rest.
+struct HalfParts {
+    uint32_t x, y;
+};
+__device__ __forceinline__ HalfParts mul_parts(uint32_t ph, uint32_t pl, uint32_t d, bool hi) {
+    HalfParts r;
+    asm("{.reg .b16 h0, h1; .reg .b32 t, u;\n\t"
+        "mov.b32 {h0, h1}, %4;\n\t"
+        "mov.b32 t, {h0, h0};\n\t"
+        "mul.rn.f16x2 %0, %2, t;\n\t"
+        "neg.f16x2 u, %0;\n\t"
+        "fma.rn.f16x2 u, %2, t, u;\n\t"
+        "fma.rn.f16x2 %1, %3, t, u;}"
+        : "=&r"(r.x), "=r"(r.y) : "r"(ph), "r"(pl), "r"(hi ? d >> 16 : d));
     return r;
 }
 // Half i of the words of a key's scales.
@@ -211,10 +229,13 @@ __device__ __forceinline__ int stream_of(const Kv4Attend &a, long long x, long l
 // A lane is (r = lane / 4, c = lane % 4). Scores of 16 keys, S[keys x 8] = K Q^T by m16n8k16 per
 // block of 32 dims; q is scaled by a power of two so that its largest value lies in [2^13, 2^14). The
 // results times the key's scales are added in f32.
-// Values, O^T[dims x 8] += V^T P^T, P being the probabilities times the value's scale of each block,
-// transposed between lanes as fp16. The exponents' reference m keeps P in fp16's range: it follows
-// the largest score plus log2 of the largest value scale, and O and l are rescaled when P would
-// pass 2^14, to below 2^9. An accumulator's columns are its lane's heads throughout.
+// Values, O^T[dims x 8] += V^T P^T, P being the probabilities p times the value's scale of each block,
+// transposed between lanes as fp16. p = ph + pl, and P = ph d rounded, plus what that leaves and pl d: three fp16
+// instructions. Two things keep P in fp16's range and bits. The exponents' reference m follows the largest
+// score: where a p would pass 2^11, O and l are rescaled so that the largest is 2^6. And each block of 32 dims
+// has a power of two, up to 2^15, that brings its largest value scale so far to [2^2, 2^3) and under which its
+// O is summed; where a scale would pass 2^4, that block's O is rescaled. So the parts hold a
+// P to 2^-31 of the largest of its own block. An accumulator's columns are its lane's heads throughout.
 // V codes are centred in fp16 before the MMA. P is held in two fp16 parts (22 bits): for up to 4 query heads in
 // columns h and h + 4 of one MMA, above that (WIDE) by two MMAs. So is q where it is f32 (QTWO); a bf16 q is exact
 // in one part. f32 results (PREC): K codes centred too. bf16 results: K codes as they are, times 2^-24, and the scores'
@@ -256,7 +277,6 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
     const long long x_begin = blockIdx.x * U / n, x_end = (blockIdx.x + 1) * U / n;
     const int b0 = stream_of(a, x_begin, before), len0 = checked_len(a, b0), nu0 = units_of(a, len0);
     int slot = 0, phase = 0;   // where the next K tile goes, and the parity that each slot's next wait has
-    const uint32_t lo_mask = kParts == 1 || c >= 2 ? 0xffffe000u : 0u;
     // Of 8 keys, row 2 c of the scores (and so slot 2 c of P) is key c and row 2 c + 1 key c2: the
     // two rows of codes that eight lanes load together lie in other banks.
     const int c2 = 4 + (c ^ 1), key_r = r & 1 ? 4 + ((r >> 1) ^ 1) : r >> 1;
@@ -372,6 +392,10 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
             }
         }
 
+        constexpr int H = NB / 2;
+        uint32_t up[H];                           // the powers of two of blocks 2 i, 2 i + 1 (fp16), and
+#pragma unroll
+        for (int i = 0; i < H; ++i) up[i] = 0x78007800u;   // ... 2^15 at first, the largest
         float m0 = -INFINITY, m1 = -INFINITY;     // references of the exponents of this lane's columns
         F2 l2 = f2(0.f, 0.f);                     // its keys' parts of their sums
         // dim 32 (t / 2) + 4 r + 2 (t % 2), and it plus 16 times the next one (e >= 2), of heads 2 c, 2 c + 1
@@ -389,7 +413,6 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
             }
             const int page2 = __shfl_sync(0xffffffffu, pages, (it + 2) % 32), vslot = after(slot);
             const int valid = min(kPage, rows - it * kWarps * kPage);
-            constexpr int H = NB / 2;
             const uint32_t kt = smem_u32(ring) + slot * Tile::kBytes, vt = smem_u32(ring) + vslot * Tile::kBytes;
             failed = !wait(slot);
             if (failed) break;
@@ -470,20 +493,39 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
                     for (int i = valid * NB + lane; i < kPage * NB; i += 32) reinterpret_cast<unsigned short *>(d)[i] = 0;
                     __syncwarp();
                 }
-                // exponent of the largest value scale (a NaN is no size), at least that of the smallest fp16
-                int de;
+                // the page's value scales under their blocks' powers of two (a NaN is no size)
                 {
-                    __half2 top = __float2half2_rn(0.f);
+                    __half2 top[H];
+                    bool past = false;
+#pragma unroll
+                    for (int i = 0; i < H; ++i) top[i] = __float2half2_rn(0.f);
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         Words<H> d;
                         d.load(vt + Tile::kScales + (2 * lane + u) * NB * 2);
 #pragma unroll
                         for (int i = 0; i < H; ++i)
-                            top = __hmax2(top, __habs2(*reinterpret_cast<__half2 *>(&d.w[i])));
+                            top[i] = __hmax2(top[i], __habs2(*reinterpret_cast<__half2 *>(&d.w[i])));
                     }
-                    const uint32_t dmax = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(__low2float(top), __high2float(top))));
-                    de = max((int)(dmax >> 23) - 126, -24);
+                    const __half2 most = __float2half2_rn((float)(1 << kTopScale));
+#pragma unroll
+                    for (int i = 0; i < H; ++i)
+                        past |= !__hble2(__hmul2(top[i], *reinterpret_cast<const __half2 *>(&up[i])), most);
+                    if (__any_sync(0xffffffffu, past)) {
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) {
+                            const uint32_t bits = *reinterpret_cast<const uint32_t *>(&top[nb / 2]), at = 16 * (nb & 1);
+                            const uint32_t e = __reduce_max_sync(0xffffffffu, bits >> at & 0xffffu) >> 10;   // biased by 15
+                            const uint32_t old = up[nb / 2] >> (at + 10) & 31u;
+                            const uint32_t now = min(old, min(30u, kNewScale + 30u - max(e, 1u)));
+                            const float by = __uint_as_float((127u + now - old) << 23);
+                            up[nb / 2] += (now - old) << (at + 10);
+#pragma unroll
+                            for (int t = 2 * nb; t < 2 * nb + 2; ++t)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) o[t][i] *= by;
+                        }
+                    }
                 }
                 F2 mx = f2(-INFINITY, -INFINITY);
 #pragma unroll
@@ -494,8 +536,8 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
                 for (int j = 4; j < 32; j <<= 1)
                     mx = f2(fmaxf(f2_lo(mx), __shfl_xor_sync(0xffffffffu, f2_lo(mx), j)),
                             fmaxf(f2_hi(mx), __shfl_xor_sync(0xffffffffu, f2_hi(mx), j)));
-                if (__any_sync(0xffffffffu, f2_lo(mx) + de > m0 + kTopBits || f2_hi(mx) + de > m1 + kTopBits)) {
-                    const float n0 = fmaxf(m0, f2_lo(mx) + (de - kNewBits)), n1 = fmaxf(m1, f2_hi(mx) + (de - kNewBits));
+                if (__any_sync(0xffffffffu, f2_lo(mx) > m0 + kTopBits || f2_hi(mx) > m1 + kTopBits)) {
+                    const float n0 = fmaxf(m0, f2_lo(mx) - kNewBits), n1 = fmaxf(m1, f2_hi(mx) - kNewBits);
                     const F2 al = f2(m0 == n0 ? 1.f : ex2(m0 - n0), m1 == n1 ? 1.f : ex2(m1 - n1));
                     m0 = n0;
                     m1 = n1;
@@ -517,6 +559,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
                         p[i] = f2(ex2(f2_lo(x)), ex2(f2_hi(x)));
                         l2 = l2 + p[i];
                     }
+                    uint32_t ph[2], pl[2];
                     Words<H> v[4], d[2];   // codes of slots 2 c, 2 c + 1 and 8 further, scales of p's keys
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -524,17 +567,23 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
                         v[i].load(vt + key * Tile::kRow + r * 2 * NB);
                     }
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) d[i].load(vt + Tile::kScales + (16 * ks + 8 * i + key_r) * NB * 2);
+                    for (int i = 0; i < 2; ++i) {
+                        d[i].load(vt + Tile::kScales + (16 * ks + 8 * i + key_r) * NB * 2);
+#pragma unroll
+                        for (int u = 0; u < H; ++u) d[i].w[u] = mul_half2(d[i].w[u], up[u]);
+                        ph[i] = pack_rn(f2_lo(p[i]), f2_hi(p[i]));
+                        const F2 rest = fma2(f2(half_lo(ph[i]), half_hi(ph[i])), f2(-1.f, -1.f), p[i]);
+                        pl[i] = pack_rn(f2_lo(rest), f2_hi(rest));
+                    }
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb) {
                         const uint32_t sel = nb & 1 ? 0x7632 : 0x5410;   // halves nb % 2 of two keys' words
-                        uint32_t ph[2], pl[2];
+                        uint32_t bh[2], bl[2];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const float e = scale_at(d[i].w, nb);
-                            const F2 y = f2(f2_lo(p[i]) * e, f2_hi(p[i]) * e), z = rest11(y, lo_mask);
-                            if (WIDE) ph[i] = transpose8(pack_rz(f2_lo(y), f2_hi(y)));
-                            pl[i] = transpose8(pack_rz(f2_lo(z), f2_hi(z)));
+                            const HalfParts y = mul_parts(ph[i], pl[i], d[i].w[nb / 2], nb & 1);
+                            bh[i] = transpose8(WIDE || c < 2 ? y.x : y.y);   // (else columns h and h + 4 have head h's parts)
+                            if (WIDE) bl[i] = transpose8(y.y);
                         }
                         const uint32_t u0 = __byte_perm(v[0].w[nb / 2], v[1].w[nb / 2], sel);
                         const uint32_t u1 = __byte_perm(v[2].w[nb / 2], v[3].w[nb / 2], sel);
@@ -543,8 +592,8 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
                             float(&acc)[4] = o[2 * nb + e];
                             const uint32_t x0 = e ? raised13(u0) : raised02(u0), x1 = e ? raised13(u1) : raised02(u1);
                             const uint32_t codes[4] = {centred_nibbles(x0), centred_bytes(x0), centred_nibbles(x1), centred_bytes(x1)};
-                            if (WIDE) mma16816(acc, codes, ph[0], ph[1]);
-                            mma16816(acc, codes, pl[0], pl[1]);
+                            mma16816(acc, codes, bh[0], bh[1]);
+                            if (WIDE) mma16816(acc, codes, bl[0], bl[1]);
                         }
                     }
                 }
@@ -593,6 +642,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 float y = e < 2 ? o[t][e] : (o[t][e] - o[t][e - 2]) * 0.0625f;
+                y *= __uint_as_float((127u + 15u - (up[t / 4] >> (t & 2 ? 26 : 10) & 31u)) << 23);   // (less its block's power of two)
                 if (kParts == 2) y += __shfl_xor_sync(0xffffffffu, y, 2);   // the parts of head h: columns h and h + 4
                 const int h = 2 * c + (e & 1), dim = 32 * (t >> 1) + 4 * r + 2 * (t & 1) + (e >> 1);
                 if (kParts == 1 || c < 2) wo[(warp * kMaxG + h) * HD + dim] = y;

@@ -131,6 +131,19 @@ def test_one_key_above_many(kv4, G, dt, bits, mag):
     run(kv4, k.cuda(), v.cuda(), q.to(DT[dt]).cuda(), [n], bits * math.log(2) / D)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("G", [1, 6])
+@pytest.mark.parametrize("D", [64, 128])
+def test_blocks_of_values_of_very_different_size(kv4, dt, G, D):
+    """Each block of dims keeps its bits, whatever the others hold."""
+    n = 150
+    k, v = rnd(1, 2, n, 2, D), rnd(2, 2, n, 2, D)
+    v[..., 32:64] *= 2.0 ** -13
+    v[:, :, :, :32] *= 2.0 ** 12
+    v[:, 100:, :, 32:64] *= 8      # larger ones come later
+    run(kv4, k, v, rnd(3, 2, 2 * G, D, dtype=DT[dt]), [n, 101], 2 / math.sqrt(D))
+
+
 @pytest.mark.parametrize("G,D", [(1, 64), (4, 128), (5, 128), (8, 64)])
 def test_bf16_queries_are_exact(kv4, G, D):
     """Two keys whose exact scores are equal, one on even dims and one on odd ones, at a score of 100: values of
