@@ -132,7 +132,7 @@ talker_status talker_kv4_reorder(const talker_kv4 *c, const int32_t *parents, in
  * of which the best `width` are chosen, in descending order, equal ones by the
  * lowest w * vocab + v. Masked values: a NaN, or a value at or below -1e30 (the
  * lowest value of a type), counts as -inf, in logits and scores; a score of +inf
- * too, and every candidate of a row with a logit above 2e38. Where fewer than
+ * too, and every candidate of a row with a logit of +inf. Where fewer than
  * width candidates are above -inf, those at -inf follow in the same order. With
  * `ended`, a beam whose flag is not 0 has one candidate, eos_id, at its
  * unchanged score (all others -inf).

@@ -22,7 +22,8 @@ constexpr int kRowEntries = 544;    // best logits of a row's parts, at most (k_
 constexpr int kClusterTasks = 128, kClusterEntries = 3200;   // parts of a sequence and their best logits, in a cluster
 constexpr float kMasked = -1e30f;   // at or below: counts as -inf
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLeastRef = -1.4426e30f;   // reference of a row's exponents without a logit: over kLog2e kMasked
+constexpr float kLeastRef = -9.9999994e29f;   // reference of a row's exponents without a logit: the next value above kMasked
+static_assert(kLeastRef > kMasked && kLeastRef - kMasked < 1e23f, "next to one another");
 
 // Masked values (and NaN) as kMasked, the lowest value that is told apart.
 __device__ __forceinline__ float unmask(float x) { return fmaxf(x, kMasked); }
@@ -76,14 +77,14 @@ struct Args {
     float *scores_out;
     int chunks;       // parts of a row
     Entry *best;      // scratch: [row][chunk][width], best first
-    float2 *sums;     // scratch: [row][chunk] (reference c, sum of 2^(kLog2e x - c))
+    float2 *sums;     // scratch: [row][chunk] (reference c, sum of e^(x - c))
 };
 
 // What a warp has seen of a row: lane i < width holds the i-th best logit (-inf: none yet); every lane
-// has its part of the sum of 2^(kLog2e x - c) and its reference c, kLog2e times its largest logit (at
-// least kLeastRef, below which masked values, and lanes that have none, add nothing). With one multiply-
-// add per exponent: the same rounded factor in every term, and in the end. A logit that is not above
-// `least` is not among the best any more.
+// has its part of the sum of e^(x - c) and its reference c, its largest logit (at least kLeastRef, below
+// which masked values, and lanes that have none, add nothing). The difference comes before the factor log2 e:
+// for logits of any size it is exact or of its own size's bits, while kLog2e x - c in one multiply-add would leave
+// half a step of kLog2e x, 2^16 where x is 1e12. A logit that is not above `least` is not among the best any more.
 struct Seen {
     float value;
     uint32_t index;
@@ -122,11 +123,10 @@ __device__ __forceinline__ void insert_all(Seen &s, const float (&x)[N * kVecs],
         }
     }
 }
-__device__ __forceinline__ void refer(Seen &s, float top) {   // the lane's reference to at least kLog2e top
-    const float c = top * kLog2e;
-    if (c > s.c) {
-        s.sum *= ex2(s.c - c);
-        s.c = c;
+__device__ __forceinline__ void refer(Seen &s, float top) {   // the lane's reference to at least top
+    if (top > s.c) {
+        s.sum *= ex2((s.c - top) * kLog2e);
+        s.c = top;
     }
 }
 // Any logits: masked values count as kMasked, and are inserted while there are too few others.
@@ -146,7 +146,7 @@ __device__ __forceinline__ void take(Seen &s, const float (&raw)[N * kVecs], On 
     }
     refer(s, top);
 #pragma unroll
-    for (int i = 0; i < N * kVecs; ++i) s.sum += ex2(fmaf(x[i], kLog2e, -s.c));
+    for (int i = 0; i < N * kVecs; ++i) s.sum += ex2((x[i] - s.c) * kLog2e);
     insert_all<N, kVecs>(s, x, tops, at, width);
 }
 // The same where `least` is at least kMasked (and vectors that do not exist hold masked values): those
@@ -169,14 +169,14 @@ __device__ __forceinline__ void take_above(Seen &s, const float (&x)[N * kVecs],
     F2 sum = f2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < N * kVecs; i += 2) {
-        const F2 y = fma2(f2(x[i], x[i + 1]), log2e, c);
+        const F2 y = (f2(x[i], x[i + 1]) + c) * log2e;
         sum = sum + f2(ex2(f2_lo(y)), ex2(f2_hi(y)));
     }
     float both = f2_lo(sum) + f2_hi(sum);
     if (both != both) {
         both = 0.f;
 #pragma unroll
-        for (int i = 0; i < N * kVecs; ++i) both += ex2(fmaf(unmask(x[i]), kLog2e, -s.c));
+        for (int i = 0; i < N * kVecs; ++i) both += ex2((unmask(x[i]) - s.c) * kLog2e);
     }
     s.sum += both;
     if (__any_sync(0xffffffffu, top > s.least)) insert_all<N, kVecs>(s, x, tops, at, width);
@@ -302,16 +302,18 @@ __device__ Seen read_part(const Args &a, int row, int chunk, uint32_t *tops) {
         take<1, 1>(s, one, [&](int) { return t + lane < a.vocab; }, [&](int, int l) { return (uint32_t)(t + l); }, a.width);
     }
     const float c = warp_max(s.c);
-    s.sum = warp_sum(s.sum * ex2(s.c - c));
+    s.sum = warp_sum(s.sum * ex2((s.c - c) * kLog2e));
     s.c = c;
     return s;
 }
 
-// A row's beam, as its candidates see it. They score their logit plus `offset`, the beam's score less
-// the logarithm of the row's sum; an ended beam goes on with the end token alone, at its own score
-// (which is the offset then); all of a dead one's are at -inf.
+// A row's beam, as its candidates see it. They score their logit less `ref`, the row's largest (exactly, so that
+// a score is not lost beside large logits), plus `offset`, the beam's score less the logarithm of the row's sum; an
+// ended beam goes on with the end token alone, at its own score (which is the offset then); all of a dead
+// one's are at -inf.
 struct Beam {
     double offset;
+    float ref;
     bool dead, ended;
 };
 struct Choice {   // shared memory of choose()
@@ -355,14 +357,14 @@ __device__ void choose(const Args &a, int seq, const Given &g, const Entry *best
             __syncwarp();
             list = mine;
         }
-        const float ref = warp_max(cs.x), sum = warp_sum(cs.y * ex2(cs.x - ref));
+        const float ref = warp_max(cs.x), sum = warp_sum(cs.y * ex2((cs.x - ref) * kLog2e));
         const float score = __shfl_sync(0xffffffffu, g.score, w / kWarps);
         const int ended = __shfl_sync(0xffffffffu, g.ended, w / kWarps);
         if (lane == 0) {
-            // no candidate above -inf: a masked score, or a row of masked logits or with an infinite one
-            const bool dead = !(score > kMasked && score < INFINITY) || (!ended && !(ref > kLeastRef && ref < INFINITY));
-            const double lse = dead || ended ? 0.0 : ((double)ref + log2_near(sum)) * (1.0 / (double)kLog2e);
-            c.beams[w] = {(double)score - lse, dead, ended != 0};
+            // no candidate above -inf: a masked score, or a row of masked logits (whose sum is 0) or with an infinite one
+            const bool dead = !(score > kMasked && score < INFINITY) || (!ended && !(sum > 0.f && ref < INFINITY));
+            const double ls = dead || ended ? 0.0 : log2_near(sum) * 0.69314718055994530942;
+            c.beams[w] = {(double)score - ls, ref, dead, ended != 0};
         }
         if (!join) continue;
         list += lane * a.width;
@@ -385,7 +387,7 @@ __device__ void choose(const Args &a, int seq, const Given &g, const Entry *best
         bool there = e.rank != 0;
         if (!b.dead && !b.ended) {
             const float x = value_of(e.rank);
-            if (x > kMasked) score = (double)x + b.offset;
+            if (x > kMasked) score = ((double)x - (double)b.ref) + b.offset;
         } else {   // one list, in order of tokens after the end token
             there = l % lists == 0;
             e.index = b.dead ? at : at == 0 ? a.eos : at - 1 + (at - 1 >= a.eos);
