@@ -183,13 +183,21 @@ __device__ __forceinline__ void take_above(Seen &s, const float (&x)[N * kVecs],
 }
 
 template <typename T>
-struct Vec;   // 16 bytes of logits
+struct Vec;   // 16 bytes of logits; pieces(p): those at p where p is a multiple of 4 but not of 16
 template <>
 struct Vec<float> {
     static constexpr int N = 4;
     __device__ static __forceinline__ void get(const uint4 &u, float (&x)[4]) {
         x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y);
         x[2] = __uint_as_float(u.z), x[3] = __uint_as_float(u.w);
+    }
+    __device__ static __forceinline__ uint4 pieces(const float *p) {
+        if (reinterpret_cast<uintptr_t>(p) % 8 == 0) {   // (the same in all lanes)
+            const uint2 a = __ldg(reinterpret_cast<const uint2 *>(p)), b = __ldg(reinterpret_cast<const uint2 *>(p) + 1);
+            return make_uint4(a.x, a.y, b.x, b.y);
+        }
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(p);
+        return make_uint4(__ldg(w), __ldg(w + 1), __ldg(w + 2), __ldg(w + 3));
     }
 };
 template <>
@@ -200,7 +208,21 @@ struct Vec<__nv_bfloat16> {
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[2 * i] = bf16lo(w[i]), x[2 * i + 1] = bf16hi(w[i]);
     }
+    __device__ static __forceinline__ uint4 pieces(const __nv_bfloat16 *p) {
+        return Vec<float>::pieces(reinterpret_cast<const float *>(p));
+    }
 };
+// Eight bf16 logits at an odd place: the three words between the first and the last one, and the last; the first.
+__device__ __forceinline__ uint4 odd_pieces(const void *p, uint32_t &first) {
+    const unsigned short *h = static_cast<const unsigned short *>(p);
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(h + 1);
+    first = __ldg(h);
+    return make_uint4(__ldg(w), __ldg(w + 1), __ldg(w + 2), __ldg(h + 7));
+}
+__device__ __forceinline__ uint4 odd_joined(const uint4 &u, uint32_t first) {
+    return make_uint4(__byte_perm(first, u.x, 0x5410), __byte_perm(u.x, u.y, 0x5432), __byte_perm(u.y, u.z, 0x5432),
+                      __byte_perm(u.z, u.w, 0x5432));
+}
 
 // Of n <= 32 * kPer ranks, the width-th highest (0 if there are fewer), by one warp: so many logits rank
 // at least as high, and nothing below it is among the best. Without such a floor most of a part's first
@@ -224,36 +246,44 @@ __device__ __forceinline__ uint32_t floor_of(uint32_t (&r)[kPer], int width) {
     return floor;
 }
 
-// One warp reads part `chunk` of a row once, by 16-byte loads where the row allows: the unaligned
-// logits at its ends go to the first and the last part. The row's maximum and sum of exponentials
-// come from the same pass as its best logits. tops: where the CTA's warps all read parts of one row, shared
-// memory for their lanes' largest logits of the first vectors, from which they take one floor.
+// One warp reads part `chunk` of a row once, by 16-byte loads where the row lies on 16 bytes. The row's
+// maximum and sum of exponentials come from the same pass as its best logits. Parts, vectors and lanes are
+// counted from the row's first logit wherever it lies, so that the sum's rounding depends on the row's values alone: equal
+// beams have equal scores. (Parts of aligned vectors, with the logits before the first one for themselves, gave
+// equal rows sums that differed in their last bits.) tops: where the CTA's warps all read parts of one row,
+// shared memory for their lanes' largest logits of the first vectors, from which they take one floor.
 template <typename T>
 __device__ Seen read_part(const Args &a, int row, int chunk, uint32_t *tops) {
     constexpr int N = Vec<T>::N, kAhead = 16 / N;
     const int lane = threadIdx.x & 31;
     const T *x = static_cast<const T *>(a.logits) + row * a.row_stride;
-    const int head = min((int)((16 - (reinterpret_cast<uintptr_t>(x) & 15u)) % 16 / sizeof(T)), a.vocab);
-    const int vectors = (a.vocab - head) / N;                   // whole ones
+    const bool aligned = reinterpret_cast<uintptr_t>(x) % 16 == 0, odd = sizeof(T) == 2 && reinterpret_cast<uintptr_t>(x) % 4 != 0;
+    const int vectors = a.vocab / N;                            // whole ones
     const int v0 = (int)((long long)vectors * chunk / a.chunks), v1 = (int)((long long)vectors * (chunk + 1) / a.chunks);
     Seen s{-INFINITY, 0xffffffffu, -INFINITY, kLeastRef, 0.f};
-    if (chunk == 0 && head > 0) {
-        const float one[1] = {lane < head ? (float)x[lane] : kMasked};
-        take<1, 1>(s, one, [&](int) { return lane < head; }, [&](int, int l) { return (uint32_t)l; }, a.width);
-    }
-    const uint4 *vec = reinterpret_cast<const uint4 *>(x + head);
     uint4 next[kAhead];
+    uint32_t first[kAhead];   // (odd rows)
     auto request = [&](int v) {
+        if (aligned) {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (v + 32 * i + lane < v1) next[i] = ldg_stream(vec + v + 32 * i + lane);
+            for (int i = 0; i < kAhead; ++i)
+                if (v + 32 * i + lane < v1) next[i] = ldg_stream(x + (size_t)(v + 32 * i + lane) * N);
+        } else if (odd) {
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (v + 32 * i + lane < v1) next[i] = odd_pieces(x + (size_t)(v + 32 * i + lane) * N, first[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (v + 32 * i + lane < v1) next[i] = Vec<T>::pieces(x + (size_t)(v + 32 * i + lane) * N);
+        }
     };
     request(v0);
 #pragma unroll 1
     for (int v = v0; v < v1 || (v == v0 && tops != nullptr); v += 32 * kAhead) {
         uint4 u[kAhead];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) u[i] = next[i];
+        for (int i = 0; i < kAhead; ++i) u[i] = odd ? odd_joined(next[i], first[i]) : next[i];
         request(v + 32 * kAhead);
         float f[kAhead * N];
 #pragma unroll
@@ -292,11 +322,11 @@ __device__ Seen read_part(const Args &a, int row, int chunk, uint32_t *tops) {
             // the next value below it (below 0 that is not -0)
             if (floor > 0) s.least = fmaxf(s.least, value_of(floor - (floor == 0x80000000u ? 2 : 1)));
         }
-        const auto at = [&](int i, int l) { return (uint32_t)(head + (v + 32 * i + l) * N); };
+        const auto at = [&](int i, int l) { return (uint32_t)((v + 32 * i + l) * N); };
         if (s.least >= kMasked) take_above<N, kAhead>(s, f, at, a.width);
         else take<N, kAhead>(s, f, [&](int i) { return v + 32 * i + lane < v1; }, at, a.width);
     }
-    const int t = head + vectors * N;
+    const int t = vectors * N;
     if (chunk == a.chunks - 1 && t < a.vocab) {   // fewer than a vector
         const float one[1] = {t + lane < a.vocab ? (float)x[t + lane] : kMasked};
         take<1, 1>(s, one, [&](int) { return t + lane < a.vocab; }, [&](int, int l) { return (uint32_t)(t + l); }, a.width);

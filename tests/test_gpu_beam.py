@@ -75,3 +75,39 @@ def test_a_masked_row_scores_no_better_than_its_beam(select):
     x[0, 0] = -1e10
     best = select(x.cuda(), torch.zeros(1, 2).cuda())[2]
     assert float(best.max()) < 0
+
+
+@pytest.mark.parametrize("V,dt", [(32001, "f32"), (50257, "f32"), (2049, "f32"), (2047, "bf16"), (50257, "bf16"), (12345, "bf16"),
+                                  (151669, "f32"), (7, "f32")])
+@pytest.mark.parametrize("W", [4, 7])
+def test_equal_rows_are_taken_in_order(select, V, dt, W):
+    """The same logits and score in every beam, in rows that lie on every place of 16 bytes: the best token of each
+    beam is chosen, beam after beam, with one score."""
+    for seed in range(3):
+        x = (rnd(seed, V) * 2).to(DT[dt])
+        x[V // 2] += 4
+        rows = x.expand(2, W, V).contiguous().cuda()
+        tok, par, best, _ = select(rows, torch.full((2, W), -1.5).cuda())
+        want = torch.arange(2 * W).view(2, W)
+        assert torch.equal(par.cpu().long(), want)
+        assert (tok.cpu() == int(x.float().argmax())).all()
+        assert (best == best[0, 0]).all()
+        # some of the beams: those that are equal stay in order, between others
+        rows[:, ::2] = (rnd(100 + seed, V) * 2).to(DT[dt]).cuda()
+        check(select, rows, torch.full((2, W), -1.5).cuda())
+
+
+def test_equal_rows_at_any_place(select):
+    """Rows with a stride, in a tensor that starts anywhere: the same bits."""
+    V, W = 5001, 5
+    for dt in DT.values():
+        x = (rnd(7, V) * 2).to(dt).cuda()
+        got = []
+        for off in range(9):
+            for stride in (V, V + 3, V + 7):
+                buf = torch.zeros(W * stride + off, dtype=dt, device="cuda")
+                rows = buf[off:].view(1, W, stride)[..., :V]
+                rows.copy_(x.expand(1, W, V))
+                got.append([t.cpu() for t in select(rows, torch.zeros(1, W).cuda())])
+        for g in got:
+            assert all(torch.equal(a, b) for a, b in zip(g, got[0]))
