@@ -108,6 +108,12 @@ talker_status talker_kv4_attend(const talker_kv4 *c, int layer, int B, const int
                                 int64_t new_row, int dtype, void *out, void *scratch, size_t scratch_bytes,
                                 void *cuda_stream);
 
+/* Test support: the form that a Talker's steps on the tensor cores run, f32 q
+ * [B][n_q_heads][head_dim] with bf16 results, over layer 0. Scratch and errors as above. */
+talker_status talker_test_kv4_attend_mixed(const talker_kv4 *c, int B, const int32_t *lens, int max_len, int n_q_heads,
+                                           float scale, const float *q, void *out_bf16, void *scratch,
+                                           size_t scratch_bytes, void *cuda_stream);
+
 /* Reorder the streams (beam search): afterwards, under table_out and lens_out,
  * stream i < R holds what stream parents[i] holds under c->page_table and lens
  * (streams i >= R hold their own). Full pages are shared, by page number; the

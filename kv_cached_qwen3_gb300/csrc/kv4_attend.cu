@@ -935,6 +935,29 @@ Kv4AttendShape shape_here(const talker_kv4 *c, int B, int max_len) {
     return kv4_attend_shape(B, c->n_kv_heads, c->head_dim, std::min(max_len, c->pages_per_stream * kPage), n_sm);
 }
 
+talker_status attend_call(const talker_kv4 *c, int layer, int B, const int32_t *lens, int max_len, int n_q_heads, float scale,
+                          const void *q, int64_t q_row, const void *k_new, const void *v_new, int64_t new_row, int in_dtype,
+                          int out_dtype, void *out, void *scratch, size_t scratch_bytes, void *cuda_stream) {
+    if (!attend_sizes_ok(c, B, n_q_heads, max_len) || layer < 0 || layer >= c->n_layers) return TALKER_EINVAL;
+    if (!lens || !q || !out || (k_new == nullptr) != (v_new == nullptr)) return TALKER_EINVAL;
+    if (in_dtype != TALKER_DTYPE_F32 && in_dtype != TALKER_DTYPE_BF16) return TALKER_EINVAL;
+    const uintptr_t size = in_dtype == TALKER_DTYPE_F32 ? 4 : 2, out_size = out_dtype == TALKER_DTYPE_F32 ? 4 : 2;
+    if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new)) % size ||
+        reinterpret_cast<uintptr_t>(out) % out_size)
+        return TALKER_EINVAL;
+    const Kv4AttendShape shape = shape_here(c, B, max_len);
+    const size_t need = kv4_attend_scratch(shape, c->head_dim);
+    if (need > 0 && (!scratch || scratch_bytes < need || (reinterpret_cast<uintptr_t>(scratch) & 15u))) return TALKER_EINVAL;
+    const Kv4Attend a{*c, layer, B, n_q_heads, lens, q, k_new, v_new, q_row, new_row, out, scale, shape.grid, shape.one_unit, shape.ctas,
+                      static_cast<float *>(scratch)};
+    if (launch_kv4_attend(a, in_dtype == TALKER_DTYPE_BF16, out_dtype == TALKER_DTYPE_BF16, false,
+                          static_cast<cudaStream_t>(cuda_stream)) != cudaSuccess) {
+        cudaGetLastError();
+        return TALKER_ECUDA;
+    }
+    return TALKER_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -948,24 +971,16 @@ talker_status talker_kv4_attend(const talker_kv4 *c, int layer, int B, const int
                                 float scale, const void *q, int64_t q_row, const void *k_new, const void *v_new,
                                 int64_t new_row, int dtype, void *out, void *scratch, size_t scratch_bytes,
                                 void *cuda_stream) {
-    if (!attend_sizes_ok(c, B, n_q_heads, max_len) || layer < 0 || layer >= c->n_layers) return TALKER_EINVAL;
-    if (!lens || !q || !out || (k_new == nullptr) != (v_new == nullptr)) return TALKER_EINVAL;
-    if (dtype != TALKER_DTYPE_F32 && dtype != TALKER_DTYPE_BF16) return TALKER_EINVAL;
-    const uintptr_t size = dtype == TALKER_DTYPE_F32 ? 4 : 2;
-    if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(k_new) |
-         reinterpret_cast<uintptr_t>(v_new)) % size)
-        return TALKER_EINVAL;
-    const Kv4AttendShape shape = shape_here(c, B, max_len);
-    const size_t need = kv4_attend_scratch(shape, c->head_dim);
-    if (need > 0 && (!scratch || scratch_bytes < need || (reinterpret_cast<uintptr_t>(scratch) & 15u))) return TALKER_EINVAL;
-    const Kv4Attend a{*c, layer, B, n_q_heads, lens, q, k_new, v_new, q_row, new_row, out, scale, shape.grid, shape.one_unit, shape.ctas,
-                      static_cast<float *>(scratch)};
-    const int bf16 = dtype == TALKER_DTYPE_BF16;
-    if (launch_kv4_attend(a, bf16, bf16, false, static_cast<cudaStream_t>(cuda_stream)) != cudaSuccess) {
-        cudaGetLastError();
-        return TALKER_ECUDA;
-    }
-    return TALKER_OK;
+    return attend_call(c, layer, B, lens, max_len, n_q_heads, scale, q, q_row, k_new, v_new, new_row, dtype, dtype, out, scratch,
+                       scratch_bytes, cuda_stream);
+}
+
+talker_status talker_test_kv4_attend_mixed(const talker_kv4 *c, int B, const int32_t *lens, int max_len, int n_q_heads,
+                                           float scale, const float *q, void *out_bf16, void *scratch, size_t scratch_bytes,
+                                           void *cuda_stream) {
+    if (!c) return TALKER_EINVAL;
+    return attend_call(c, 0, B, lens, max_len, n_q_heads, scale, q, (int64_t)n_q_heads * c->head_dim, nullptr, nullptr, 0,
+                       TALKER_DTYPE_F32, TALKER_DTYPE_BF16, out_bf16, scratch, scratch_bytes, cuda_stream);
 }
 
 }  // extern "C"

@@ -98,6 +98,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "talker_kv4_attend_scratch": (ctypes.c_size_t, [vp] + [ctypes.c_int] * 3),
         "talker_kv4_attend": (st, [vp, ctypes.c_int, ctypes.c_int, vp, ctypes.c_int, ctypes.c_int, ctypes.c_float, vp,
                                    i64, vp, vp, i64, ctypes.c_int, vp, vp, ctypes.c_size_t, vp]),
+        "talker_test_kv4_attend_mixed": (st, [vp, ctypes.c_int, vp, ctypes.c_int, ctypes.c_int, ctypes.c_float, vp, vp, vp,
+                                              ctypes.c_size_t, vp]),
         "talker_kv4_reorder": (st, [vp, vp, ctypes.c_int, vp, vp, vp, vp]),
         "talker_beam_scratch": (ctypes.c_size_t, [ctypes.c_int] * 3),
         "talker_beam_select": (st, [vp, i64, ctypes.c_int, vp, vp] + [ctypes.c_int] * 4 + [vp] * 5 +

@@ -157,3 +157,25 @@ def test_bf16_queries_are_exact(kv4, G, D):
     for a in (255, 253, 251, 193, 129):
         q = torch.full((1, G, D), a / 128, dtype=torch.bfloat16)
         run(kv4, k.cuda(), v, q.cuda(), [2], 100 / (D / 2 * a / 128))
+
+
+@pytest.mark.parametrize("H,G,D", [(2, 2, 128), (1, 3, 64), (2, 8, 128), (1, 5, 64)])
+def test_f32_queries_with_bf16_results(kv4, H, G, D):
+    """The form of a Talker's steps on the tensor cores: q keeps 22 bits. Each q is 1 + 2^-12 times one of bf16, which
+    its first eleven bits would lose, at scores of up to 100 of two keys that nearly cancel."""
+    k = torch.zeros(1, 2, H, D)
+    k[0, 0, :, ::2] = 1.0
+    k[0, 1, :, 1::2] = 1.0
+    v = rnd(2, 1, 2, H, D)
+    v[0, 1] = -v[0, 0]
+    v[0, :, :, ::32] = torch.tensor([4.0, -4.0]).view(2, 1, 1).cuda()
+    c = kv4.KV4Cache(1, 2, 1, H, D)
+    c.write(k.cuda()[None], v[None])
+    q = torch.full((1, H * G, D), 1.0)
+    q[..., 1::2] = 1 + 2.0 ** -12
+    q, lens = q.cuda(), torch.tensor([2], dtype=torch.int32).cuda()
+    out = torch.empty(1, H * G, D, dtype=torch.bfloat16, device="cuda")
+    scale = 100 / (D / 2)
+    kv4.launch(c.device.index, c._lib.talker_test_kv4_attend_mixed, "talker_test_kv4_attend_mixed", c._ref, 1, lens.data_ptr(),
+               2, H * G, scale, q.data_ptr(), out.data_ptr(), None, 0)
+    check(host(out)[0], host(q)[0], ref.q4_roundtrip(host(k))[0], ref.q4_roundtrip(host(v))[0], scale, torch.bfloat16)
