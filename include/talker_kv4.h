@@ -27,8 +27,8 @@
  * (lengths, page numbers, parents) is checked there: what is out of range is
  * skipped as described and sets a bit of *status (when status is not NULL):
  * 1 << 0 a position or length outside the stream's pages, 1 << 1 a copy that did
- * not arrive within a second (the row is NaN), 1 << 3 a page number
- * or parent out of range. Nothing is allocated; every call may be captured into
+ * not arrive within a second (its row is NaN, and so are those that its CTA had yet
+ * to attend), 1 << 3 a page number or parent out of range. Nothing is allocated; every call may be captured into
  * a CUDA graph; scratch need not hold anything on entry, and calls that may run
  * at the same time need scratch of their own.
  */

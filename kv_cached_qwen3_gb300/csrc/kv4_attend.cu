@@ -4,6 +4,7 @@
 #include <math.h>
 
 #include "kv4.cuh"
+#include "kv4_ring.cuh"
 
 using namespace talker_dev;
 
@@ -276,7 +277,8 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
     if (blockIdx.x >= n) return;
     const long long x_begin = blockIdx.x * U / n, x_end = (blockIdx.x + 1) * U / n;
     const int b0 = stream_of(a, x_begin, before), len0 = checked_len(a, b0), nu0 = units_of(a, len0);
-    int slot = 0, phase = 0;   // where the next K tile goes, and the parity that each slot's next wait has
+    int slot = 0;   // where the next K tile goes
+    Kv4Ring state;
     // Of 8 keys, row 2 c of the scores (and so slot 2 c of P) is key c and row 2 c + 1 key c2: the
     // two rows of codes that eight lanes load together lie in other banks.
     const int c2 = 4 + (c ^ 1), key_r = r & 1 ? 4 + ((r >> 1) ^ 1) : r >> 1;
@@ -290,17 +292,20 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
     __shared__ Range ranges[kWarps];
     Range &at = ranges[warp];
     auto good = [&](int page) { return page >= 0 && page < a.c.n_pages; };
-    // a tile to a slot, by one lane; a bad page number copies page 0, which is not used
+    // a tile to a slot, by one lane, behind what the warp read there; a bad page number copies page 0, which is not used
     auto issue = [&](int to, const void *pool, int page, int g) {
+        state.issued(to);
+        if (lane != 0) return;
+        fence_proxy_async();
         const size_t tile = ((size_t)(good(page) ? page : 0) * a.c.n_layers + a.layer) * a.c.n_kv_heads + g;
         mbar_arrive_expect_tx(&bars[warp][to], Tile::kBytes);
         bulk_g2s(ring + to * Tile::kBytes, static_cast<const unsigned char *>(pool) + tile * Tile::kBytes, Tile::kBytes,
                  &bars[warp][to]);
     };
     auto wait = [&](int at) {
-        const bool ok = bounded_wait(&bars[warp][at], phase >> at & 1);
-        phase ^= 1 << at;
-        return !__any_sync(0xffffffffu, !ok);
+        const bool ok = !__any_sync(0xffffffffu, !bounded_wait(&bars[warp][at], state.parity(at)));
+        if (ok) state.landed(at);
+        return ok;
     };
     auto after = [](int at) { return at == kSlots - 1 ? 0 : at + 1; };
     // of the warp's pages: how many, the numbers of 32 j + lane, of this one and of the next
@@ -311,7 +316,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
     };
     auto open = [&](int b, int g, int len, int nu, int u0, long long left) {   // ... and its first copies
         const int u1 = (int)min((long long)nu, u0 + left), pb = u0 * kWarps + warp, pe = u1 == nu ? pages_of(len) : u1 * kWarps;
-        n_it = pb < pe ? (pe - pb + kWarps - 1) / kWarps : 0;
+        n_it = pb < pe && !state.lost() ? (pe - pb + kWarps - 1) / kWarps : 0;
         rows = len - pb * kPage;
         if (lane == 0) at = {b, g, len, nu, u0, u1, left - (u1 - u0)};
         __syncwarp();
@@ -319,8 +324,8 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
         ahead = page_of(32 + lane);
         page = __shfl_sync(0xffffffffu, pages, 0);
         page1 = __shfl_sync(0xffffffffu, pages, 1);
-        if (lane == 0 && n_it > 0) issue(slot, a.c.k, page, g), issue(after(slot), a.c.v, page, g);
-        if (kSlots == 3 && lane == 0 && n_it > 1) issue(after(after(slot)), a.c.k, page1, g);
+        if (n_it > 0) issue(slot, a.c.k, page, g), issue(after(slot), a.c.v, page, g);
+        if (kSlots == 3 && n_it > 1) issue(after(after(slot)), a.c.k, page1, g);
     };
     open(b0, (int)((x_begin - before) / nu0), len0, nu0, (int)((x_begin - before) % nu0), x_end - x_begin);
     pdl_wait();   // before it: lengths, page numbers and cached rows, which the kernel before does not write
@@ -405,7 +410,6 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
 
-        bool failed = false;
         for (int it = 0; it < n_it; ++it) {
             if ((it + 2) % 32 == 0) {
                 pages = ahead;
@@ -414,8 +418,10 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
             const int page2 = __shfl_sync(0xffffffffu, pages, (it + 2) % 32), vslot = after(slot);
             const int valid = min(kPage, rows - it * kWarps * kPage);
             const uint32_t kt = smem_u32(ring) + slot * Tile::kBytes, vt = smem_u32(ring) + vslot * Tile::kBytes;
-            failed = !wait(slot);
-            if (failed) break;
+            if (!wait(slot)) {
+                state.lose();
+                break;
+            }
             F2 sc[4][2];   // scores in base 2: of keys 16 i + key_r and 16 i + 8 + key_r
             if (!good(page)) {
                 if (lane == 0 && a.c.status != nullptr) atomicOr(a.c.status, ST_BAD_ARG);
@@ -481,12 +487,11 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
                 }
             }
             __syncwarp();
-            if (lane == 0 && it + 1 < n_it) {   // the next page's V (of two slots: K) over this K
-                fence_proxy_async();
-                issue(slot, kSlots == 3 ? a.c.v : a.c.k, page1, at.g);
+            if (it + 1 < n_it) issue(slot, kSlots == 3 ? a.c.v : a.c.k, page1, at.g);   // the next page's V (of two slots: K) over this K
+            if (!wait(vslot)) {
+                state.lose();
+                break;
             }
-            failed = !wait(vslot);
-            if (failed) break;
             if (good(page)) {
                 if (valid < kPage) {   // value scales past the length: zero (a row's last page: never refilled)
                     unsigned char *d = ring + vslot * Tile::kBytes + Tile::kScales;
@@ -599,17 +604,16 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
                 }
             }
             __syncwarp();
-            if (lane == 0 && it + (kSlots == 3 ? 2 : 1) < n_it) {   // the K after the next (V of the next) over this V
-                fence_proxy_async();
+            if (it + (kSlots == 3 ? 2 : 1) < n_it)   // the K after the next (V of the next) over this V
                 issue(vslot, kSlots == 3 ? a.c.k : a.c.v, kSlots == 3 ? page2 : page1, at.g);
-            }
             slot = after(vslot);
             page = page1;
             page1 = page2;
         }
-        if (failed) {   // report, and give the copies in flight their chance to land
+        if (n_it > 0 && state.lost()) {   // report, and give the copies in flight their chance to land; no more follow
             if (lane == 0 && a.c.status != nullptr) atomicOr(a.c.status, ST_WAIT_TIMEOUT);
-            for (int i = 0; i < kSlots; ++i) bounded_wait(&bars[warp][i], phase >> i & 1);
+            for (int i = 0; i < kSlots; ++i)
+                if (state.in_flight(i)) wait(i);
         }
 
         // The next range's first copies go out now. (This warp's reads and writes of its ring lie behind it.)
@@ -627,7 +631,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
 #pragma unroll
         for (int j = 4; j < 32; j <<= 1)
             l2 = l2 + f2(__shfl_xor_sync(0xffffffffu, f2_lo(l2), j), __shfl_xor_sync(0xffffffffu, f2_hi(l2), j));
-        if (failed) {
+        if (state.lost()) {   // this row and the rest of the CTA's
             m0 = m1 = __int_as_float(0x7fc00000);
             l2 = f2(m0, m0);
         }
