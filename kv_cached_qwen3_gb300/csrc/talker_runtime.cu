@@ -806,9 +806,10 @@ talker_status check_stream(const talker *t, int stream) {
 
 // Run `enqueue(stream, &n_kernels)` as a CUDA graph captured once per key and replayed
 // afterwards (the host then issues one launch instead of a few hundred, and the tensor maps
-// of the GEMMs are encoded once, at capture). Keeps the last kMaxGraphs prefill graphs.
-template <typename F>
-talker_status run_graph(talker *t, const std::vector<long long> &key, F enqueue) {
+// of the GEMMs are encoded once, at capture). Keeps the last kMaxGraphs prefill graphs. `ready()` runs
+// just before the launch: what it does to a stream is not done where the graph cannot be made.
+template <typename F, typename R>
+talker_status run_graph(talker *t, const std::vector<long long> &key, R ready, F enqueue) {
     PrefillGraph *pg = nullptr;
     for (auto &g : t->pgraphs)
         if (g.key == key) pg = &g;
@@ -834,6 +835,7 @@ talker_status run_graph(talker *t, const std::vector<long long> &key, F enqueue)
         t->pgraphs.push_back(PrefillGraph{key, exec, nk});
         pg = &t->pgraphs.back();
     }
+    TRY(ready());
     TRY_CUDA(cudaGraphLaunch(pg->exec, t->st));
     t->launches += pg->n_kernels;
     return TALKER_OK;
@@ -871,10 +873,13 @@ talker_status reorder_pages(talker *t, const int32_t *parents, int R, int group)
 // its own again.
 talker_status own_pages(talker *t) { return t->pages_shared ? reorder_pages(t, nullptr, 0, 0) : TALKER_OK; }
 
-// The same before a call that writes streams [s0, s0 + n) from position 0.
+// The same before a call that writes streams [s0, s0 + n) from position 0. They are empty then, for the host too.
 talker_status own_pages_from_0(talker *t, int s0, int n) {
     if (!t->pages_shared) return TALKER_OK;
-    for (int s = s0; s < s0 + n; ++s) TRY_CUDA(launch_set_len(t->d_len, s, 0, t->st));
+    for (int s = s0; s < s0 + n; ++s) {
+        TRY_CUDA(launch_set_len(t->d_len, s, 0, t->st));
+        t->len[s] = 0;
+    }
     t->launches += n;
     return reorder_pages(t, nullptr, 0, 0);
 }
@@ -895,11 +900,11 @@ talker_status prefill_impl(talker *t, int stream, const float *emb, int T, float
     if (t->kv_quant && !tc_usable(t)) return TALKER_EINVAL;
     const bool tc = t->kv_quant || (T >= kTcMinRows && t->prefill_mode != 2 && tc_usable(t));   // quantized rows: always tc
     if (tc) TRY(ensure_tc(t, T));
-    if (!append) TRY(own_pages_from_0(t, stream, 1));
     const std::vector<long long> key = {0, tc, T, stream, pos0, all_rows, t->prefill_mode,
                                         (long long)(uintptr_t)emb, (long long)(uintptr_t)hidden,
                                         (long long)(uintptr_t)logits, (long long)(uintptr_t)out.argmax};
-    TRY(run_graph(t, key, [&](cudaStream_t st, int *nk) -> talker_status {
+    const auto ready = [&] { return append ? TALKER_OK : own_pages_from_0(t, stream, 1); };
+    TRY(run_graph(t, key, ready, [&](cudaStream_t st, int *nk) -> talker_status {
         if (tc) TRY(enqueue_tc(t, st, T, rm, emb, 1, out, nk));
         else TRY(enqueue_forward(t, st, T, rm, emb, 1, out, nk));
         TRY_CUDA(launch_set_len(t->d_len, stream, pos0 + T, st));
@@ -1098,13 +1103,12 @@ talker_status talker_prefill_batched(talker_t *t, int B, const float *emb, int T
     const int rows = B * T;
     TRY(ensure_capacity(t, rows, 1));
     TRY(ensure_tc(t, rows));
-    TRY(own_pages_from_0(t, 0, B));
     RowMap rm{1, 0, 0, t->d_len, T};
     ForwardOut out{logits_last, hidden_last, argmax_last, false, 0, T};
     const std::vector<long long> key = {1, B, T, t->prefill_mode, (long long)(uintptr_t)emb,
                                         (long long)(uintptr_t)hidden_last, (long long)(uintptr_t)logits_last,
                                         (long long)(uintptr_t)argmax_last};
-    TRY(run_graph(t, key, [&](cudaStream_t st, int *nk) -> talker_status {
+    TRY(run_graph(t, key, [&] { return own_pages_from_0(t, 0, B); }, [&](cudaStream_t st, int *nk) -> talker_status {
         TRY(enqueue_tc(t, st, rows, rm, emb, 1, out, nk));
         for (int s = 0; s < B; ++s) TRY_CUDA(launch_set_len(t->d_len, s, T, st));
         *nk += B;
