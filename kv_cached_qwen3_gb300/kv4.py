@@ -108,8 +108,12 @@ class KV4Cache:
                 shape[4] != self.head_dim:
             raise ValueError("%s: k and v must be f32 or bf16 [layers, streams, rows, %d, %d] on %s" %
                              (what, self.n_kv_heads, self.head_dim, self.device))
-        if v.shape != shape or v.stride() != stride or v.dtype is not k.dtype or v.device != self.device:
+        if v.shape != shape or v.dtype is not k.dtype or v.device != self.device:
             raise ValueError("%s: k and v must have the same shape, type, strides and device" % what)
+        if v.stride() != stride:      # (a dimension of one element has no stride)
+            stride = tuple(a if n > 1 else 0 for n, a in zip(shape, stride))
+            if stride != tuple(a if n > 1 else 0 for n, a in zip(shape, v.stride())):
+                raise ValueError("%s: k and v must have the same shape, type, strides and device" % what)
         layers, streams, rows = shape[:3]
         if layers == 0 or streams == 0 or rows == 0:
             return
