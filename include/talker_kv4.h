@@ -124,7 +124,9 @@ talker_status talker_test_kv4_attend_mixed(const talker_kv4 *c, int B, const int
  * pages_per_stream (the table r * pages_per_stream + j follows it). Streams that
  * nobody has as a parent are given up: the old table must not be used any more
  * once rows are written through the new one, but reordering again from the old
- * table with the same parents gives the same result.
+ * table with the same parents gives the same result. A program that cuts streams
+ * which share pages (writes fewer into lens) calls it with R = 0 before it writes to
+ * them: every stream keeps its rows, and the page that its next row goes to is its own.
  * table_out [n_streams][pages_per_stream] and lens_out [n_streams] must not
  * overlap the inputs. Lens in [0, 64 * pages_per_stream]; parents in
  * [0, n_streams). A bad parent (status 1 << 3) counts as the stream itself, a bad
@@ -140,8 +142,10 @@ talker_status talker_kv4_reorder(const talker_kv4 *c, const int32_t *parents, in
  * lowest value of a type), counts as -inf, in logits and scores; a score of +inf
  * too, and every candidate of a row with a logit of +inf. Where fewer than
  * width candidates are above -inf, those at -inf follow in the same order. With
- * `ended`, a beam whose flag is not 0 has one candidate, eos_id, at its
- * unchanged score (all others -inf).
+ * `ended`, a beam whose flag is not 0 has one candidate, eos_id, at its unchanged
+ * score (all others -inf). A row's sum of exponentials is made in f32 (off by about
+ * 2^-22 of itself), in an order that the row's values set and not its address: equal
+ * rows have equal sums. From there on candidates are compared in 64 bits.
  * logits: [n_seq * width] rows of vocab elements, row_stride elements apart,
  * dtype F32 or BF16; scores f32 [n_seq][width]; ended int32 [n_seq][width] or
  * NULL (eos_id may then be negative: no token ends a beam). Outputs

@@ -185,7 +185,8 @@ class KV4Cache:
     def reorder(self, parents, lens, table_out=None, lens_out=None):
         """Beam reordering: returns (cache, lens) in which stream i holds what stream parents[i] holds here under
         lens. Pools are shared: full pages are named by several streams, and only rows of a page that is still being
-        filled are copied. This cache must not be used after rows are written through the new one."""
+        filled are copied. This cache must not be used after rows are written through the new one. Streams that share
+        pages and are cut (a smaller lens) get pages of their own to write to by a call without parents (a tensor of 0)."""
         R = parents.numel()
         at = self._ints("parents", parents, R)
         lens_at = self._ints("lens", lens, self.n_streams)
