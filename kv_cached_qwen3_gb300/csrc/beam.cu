@@ -449,7 +449,7 @@ __device__ void choose(const Args &a, int seq, const Given &g, const Entry *best
 
 // One cluster per sequence (gridDim.x / n_seq CTAs): its warps share the parts, whose results go to
 // the first CTA's shared memory, which joins them. No scratch, one launch. Bound by latencies: 4 rows of 2048
-// take 7.1 us, of which a launch is 2.
+// take 7.0 us, of which a launch is 2.
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32) k_beam_cluster(const Args a) {
     __shared__ Entry best[kClusterEntries];
@@ -474,8 +474,9 @@ __global__ void __launch_bounds__(kWarps * 32) k_beam_cluster(const Args a) {
 }
 
 // Larger calls: a warp per part over the whole GPU, the results in scratch; then a CTA per sequence. 24 x 8
-// rows of 100003 f32 logits (77 MB, 11.3 us at the measured copy rate) take 25: about 17 for the parts, whose
-// warps spend two thirds of their 3200 instructions finding and inserting the best logits, 6 for the joining CTAs.
+// rows of 100003 f32 logits (77 MB, 11.3 us at the measured copy rate) take 28: about 20 for the parts, whose
+// warps spend over half of their 3700 instructions finding and inserting the best logits, 6 for the joining CTAs. Rows
+// off 16 bytes, three of four here, cost 2 of them (of 100000 logits: 26); in bf16 29.5 (28).
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32) k_beam_parts(const Args a, long long parts) {
     __shared__ uint32_t tops[kWarps * 32];
@@ -485,7 +486,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_beam_parts(const Args a, long l
     const Seen s = read_part<T>(a, (int)(t / a.chunks), (int)(t % a.chunks), a.chunks % kWarps == 0 ? tops : nullptr);
     if (lane < a.width) a.best[t * a.width + lane] = s.entry();
     if (lane == 0) a.sums[t] = make_float2(s.c, s.sum);
-    pdl_launch_dependents();   // (at the start 36 us instead of 25 for 24 x 8 rows of 100003: its CTAs take the parts' room)
+    pdl_launch_dependents();   // (at the start 11 us more for 24 x 8 rows of 100003: its CTAs take the parts' room)
 }
 __global__ void __launch_bounds__(kWarps * 32) k_beam_choose(const Args a) {
     extern __shared__ Entry stage[];   // a row's lists for each warp
@@ -498,16 +499,16 @@ __global__ void __launch_bounds__(kWarps * 32) k_beam_choose(const Args a) {
 
 // How a call runs. A cluster serves a sequence until its CTAs would read over kClusterLogits each;
 // then the parts are spread over the GPU, at least kPartLogits each. us by a cluster / over the GPU, of
-// (sequences, beams, vocabulary) in f32: (1, 4, 2048) 6.9 / 7.4, (24, 8, 8000) 14.0 / 12.9, (1, 4, 32000) 9.5 / 8.7 (and
-// a second launch for the host, about 3 us), (1, 4, 65000) 11.7 / 9.8, (64, 4, 50257) 22.0 / 18.8,
-// (1, 8, 100003) 23.8 / 16.2, (1, 32, 32000) 94 / 47. Parts of 256 / 1024 / 4096 logits: (1, 4, 2048) 7.3 / 8.3 / 9.9,
-// (4, 8, 4099) 10.9 / 14.0 / 18.7, (24, 8, 8000) 13.9 / 17.3 / 24.7.
+// (sequences, beams, vocabulary) in f32: (1, 4, 2048) 7.4 / 7.5, (24, 8, 8000) 14.0 / 13.4, (1, 4, 32000) 9.9 / 9.2 (and
+// a second launch for the host, about 3 us), (1, 4, 65000) 12.2 / 10.5, (64, 4, 50257) 26.2 / 23.7,
+// (1, 8, 100003) 27.3 / 17.0, (1, 32, 32000) 95 / 47. Parts of 256 / 1024 / 4096 logits: (1, 4, 2048) 7.3 / 8.8 / 9.8,
+// (4, 8, 4099) 10.9 / 14.3 / 20.6, (24, 8, 8000) 14.0 / 17.5 / 25.9.
 struct Shape {
     int ctas;     // of the cluster, or 0: two launches
     int chunks;
 };
 constexpr int kClusterLogits = 16384, kPartLogits = 256;
-constexpr int kTargetParts = 152 * 20;   // 24 x 8 rows of 100003: 24.8 us; 152 * 24: 25.0, 152 * 32 on 4 CTAs an SM 25.6
+constexpr int kTargetParts = 152 * 20;   // 24 x 8 rows of 100003: 28.2 us; 152 * 16: 28.2, 152 * 24: 28.5, 152 * 32: 34.1
 
 Shape shape_of(int n_seq, int width, int vocab) {
     const long long logits = (long long)width * vocab;

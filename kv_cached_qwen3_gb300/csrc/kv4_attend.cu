@@ -244,11 +244,12 @@ __device__ __forceinline__ int stream_of(const Kv4Attend &a, long long x, long l
 // that: an error of 2e-6 of the result instead of 3e-7 for 128 dims and G = 2.)
 //
 // 64 streams x 8192 rows x 8 KV heads of 128 dims (604 MB of tiles, 89 us at the measured copy rate):
-// bf16, G = 8 111 us; f32, G = 2 126, G = 8 (WIDE) 162; bf16 with 64 dims, G = 8 76 (floor 44.5). About 3% less
-// with all pages in L2, so not DRAM: 1120 instructions a page and warp in bf16 at 2.4 per cycle and
-// multiprocessor, 340 of them on the ALU pipe (masks and byte permutations of codes), which takes one in two
-// cycles; the rest is the latency that its 12 or 16 warps do not hide (kv4_attend_shape). One wave of CTAs over
-// balanced ranges instead of a CTA per split of a row: 144 instead of 164 us.
+// bf16, G = 8 139 us, G = 2 122; f32, G = 2 128, G = 8 (WIDE) 161; bf16 with 64 dims, G = 8 90 (floor 44.5).
+// (P in one fp16 part: 111 us in bf16 with G = 8, terms off by up to 2^-10.) Not DRAM, but
+// instructions: 1340 a page and warp in bf16 with G = 8 at 2.3 per cycle and multiprocessor, over a quarter on
+// the ALU pipe (masks and byte permutations of codes), which takes one in two cycles; the rest is the latency that
+// its 12 or 16 warps do not hide (kv4_attend_shape). One wave of CTAs over balanced ranges instead of a CTA per
+// split of a row: 144 instead of 164 us, at that time.
 template <int HD, bool WIDE, typename TI, typename TO, int CTAS>
 __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Attend a) {
     using Tile = Kv4Tile<HD>;
@@ -802,8 +803,8 @@ __global__ void __launch_bounds__(kCombineThreads) k_kv4_combine(const Kv4Attend
 }
 
 // Parts of a row, if all are alike, from which on it is k_kv4_combine (a CTA per query head) that joins them. With
-// k_kv4_join / with it: 64 streams of 8192 rows x 8 heads (2 parts) 122 / 126 us, 16 streams of up to 2048 (4) 16.5 /
-// 17.7, 7 streams of up to 5001 x 5 heads (13) 13.1 / 11.0, 1 stream of 32768 x 8 heads (57) 24 / 20.
+// k_kv4_join / with it: 64 streams of 8192 rows x 8 heads (2 parts) 128 / 136 us, 16 streams of up to 2048 (5) 13.0 /
+// 14.4, 7 streams of up to 5001 x 5 heads (13) 13.4 / 11.1, 1 stream of 32768 x 8 heads (57) 22.6 / 18.4.
 constexpr int kManyParts = 8;
 template <int HD, typename TI, typename TO>
 cudaError_t launch_t(Kv4Attend a, bool pdl, cudaStream_t s) {
@@ -811,7 +812,9 @@ cudaError_t launch_t(Kv4Attend a, bool pdl, cudaStream_t s) {
     void (*kernel)(Kv4Attend) = k_kv4_attend<HD, false, TI, TO, kFewCtas>;
     if constexpr (HD == 128)
         if (a.ctas == kManyCtas) kernel = k_kv4_attend<HD, false, TI, TO, kManyCtas>;
-    if (wide) {   // (162 us above; with 128 registers, which spills, 164)
+    // With three / four CTAs (128 registers, which spill), G = 8 in bf16: 64 x 8192 rows 139 / 139 us, 32 x 4096 49 / 52,
+    // 16 x 2048 23.2 / 27.5, 16 of up to 2048 22.8 / 18.5, 32 of up to 4096 36.1 / 36.5; f32 161 / 161 and 53.5 / 57.3.
+    if (wide) {
         if (a.ctas == kManyCtas) a.grid = std::max(1, a.grid * kFewCtas / kManyCtas);
         a.ctas = kFewCtas;
         kernel = k_kv4_attend<HD, true, TI, TO, kFewCtas>;
@@ -856,11 +859,11 @@ cudaError_t launch_hd(const Kv4Attend &a, int in_bf16, int out_bf16, bool pdl, c
 // 690 / 818.
 constexpr int kWholePages = 8;
 
-// Three or four CTAs a multiprocessor: four hide more latency and finish more units at once, but have two tiles
-// in flight per warp instead of three. us with 3 / 4, 8 KV heads of 128 dims, G = 2, bf16 unless said: 64 streams
-// of 8192 rows, G = 8 115 / 111; 32 of up to 4096 35.3 / 33.6 (all of 4096: 37.9 / 38.3); 16 of up to 2048 15.2 / 12.4
-// (all of 2048: 17.5 / 18.9); 2 of 16384 18.2 / 16.8; 1 of 32768 16.6 / 17.2, of 131072 35.9 / 37.3; with a row to a
-// CTA, 100 streams of 500 20.1 / 23.4; with 64 dims, 7 of up to 5001, G = 7 13.6 / 15.3.
+// Three or four CTAs a multiprocessor, up to 4 query heads a KV head: four hide more latency and finish more units
+// at once, but have two tiles in flight per warp instead of three. us with 3 / 4, 8 KV heads of 128 dims, G = 2, bf16:
+// 64 streams of 8192 rows 127 / 122; 32 of up to 4096 30.8 / 29.6 (all of 4096: 43.7 / 43.9); 16 of up to 2048 17.7 /
+// 13.2 (all of 2048: 19.5 / 20.5); 2 of 16384 20.1 / 18.3; 1 of 32768 18.3 / 19.1, of 131072 41.0 / 41.3; with a row to
+// a CTA, 100 streams of 500 22.0 / 26.1. (With 64 dims four were slower too: 13.6 / 15.3 for 7 of up to 5001.)
 Kv4AttendShape kv4_attend_shape(int B, int n_kv, int hd, int max_len, int n_sm) {
     const long long rows = (long long)B * n_kv, pages = ((long long)max_len + kPage - 1) / kPage;
     Kv4AttendShape p;
