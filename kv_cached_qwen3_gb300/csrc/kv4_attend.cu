@@ -242,9 +242,13 @@ __device__ __forceinline__ int stream_of(const Kv4Attend &a, long long x, long l
 // in one part. f32 results (PREC): K codes centred too. bf16 results: K codes as they are, times 2^-24, and the scores'
 // offset, -8 sum(q) of each block times its scale, by one more MMA over blocks. (f32 results would lose bits to
 // that: an error of 2e-6 of the result instead of 3e-7 for 128 dims and G = 2.)
+// The MMA cuts its sums off instead of rounding them, so a long chain of them shrinks: over 8192 rows a CTA
+// f32 results were 1e-6 off, with WIDE 3e-6 (2e-5 for 20000 values of one sign). So theirs start from zero every 16
+// keys, and 2 to 3e-7 is left at any length (G = 2 135 instead of 129 us below, G = 8 172 instead of 161). bf16
+// results, whose step is 2^-8, keep the chain.
 //
 // 64 streams x 8192 rows x 8 KV heads of 128 dims (604 MB of tiles, 89 us at the measured copy rate):
-// bf16, G = 8 139 us, G = 2 122; f32, G = 2 128, G = 8 (WIDE) 161; bf16 with 64 dims, G = 8 90 (floor 44.5).
+// bf16, G = 8 139 us, G = 2 122; f32, G = 2 135, G = 8 (WIDE) 172; bf16 with 64 dims, G = 8 90 (floor 44.5).
 // (P in one fp16 part: 111 us in bf16 with G = 8, terms off by up to 2^-10.) Not DRAM, but
 // instructions: 1340 a page and warp in bf16 with G = 8 at 2.3 per cycle and multiprocessor, over a quarter on
 // the ALU pipe (masks and byte permutations of codes), which takes one in two cycles; the rest is the latency that
@@ -598,8 +602,19 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) k_kv4_attend(const Kv4Atten
                             float(&acc)[4] = o[2 * nb + e];
                             const uint32_t x0 = e ? raised13(u0) : raised02(u0), x1 = e ? raised13(u1) : raised02(u1);
                             const uint32_t codes[4] = {centred_nibbles(x0), centred_bytes(x0), centred_nibbles(x1), centred_bytes(x1)};
-                            mma16816(acc, codes, bh[0], bh[1]);
-                            if (WIDE) mma16816(acc, codes, bl[0], bl[1]);
+                            if (PREC) {   // the 16 keys' sums on their own, then to the others' by rounded additions
+                                float part[4];
+                                mma16816_new(part, codes, WIDE ? bl[0] : bh[0], WIDE ? bl[1] : bh[1]);
+                                if (WIDE) mma16816(part, codes, bh[0], bh[1]);
+#pragma unroll
+                                for (int i = 0; i < 4; i += 2) {
+                                    const F2 x = f2(acc[i], acc[i + 1]) + f2(part[i], part[i + 1]);
+                                    acc[i] = f2_lo(x), acc[i + 1] = f2_hi(x);
+                                }
+                            } else {
+                                mma16816(acc, codes, bh[0], bh[1]);
+                                if (WIDE) mma16816(acc, codes, bl[0], bl[1]);
+                            }
                         }
                     }
                 }
@@ -803,8 +818,8 @@ __global__ void __launch_bounds__(kCombineThreads) k_kv4_combine(const Kv4Attend
 }
 
 // Parts of a row, if all are alike, from which on it is k_kv4_combine (a CTA per query head) that joins them. With
-// k_kv4_join / with it: 64 streams of 8192 rows x 8 heads (2 parts) 128 / 136 us, 16 streams of up to 2048 (5) 13.0 /
-// 14.4, 7 streams of up to 5001 x 5 heads (13) 13.4 / 11.1, 1 stream of 32768 x 8 heads (57) 22.6 / 18.4.
+// k_kv4_join / with it, bf16: 64 streams of 8192 rows x 8 heads (2 parts) 122 / 130 us, 16 streams of up to 2048 (5) 13.2 /
+// 14.6, 7 streams of up to 5001 x 5 heads (13) 13.4 / 11.1, 1 stream of 32768 x 8 heads (57) 22.4 / 18.3.
 constexpr int kManyParts = 8;
 template <int HD, typename TI, typename TO>
 cudaError_t launch_t(Kv4Attend a, bool pdl, cudaStream_t s) {

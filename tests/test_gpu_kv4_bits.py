@@ -179,3 +179,19 @@ def test_f32_queries_with_bf16_results(kv4, H, G, D):
     kv4.launch(c.device.index, c._lib.talker_test_kv4_attend_mixed, "talker_test_kv4_attend_mixed", c._ref, 1, lens.data_ptr(),
                2, H * G, scale, q.data_ptr(), out.data_ptr(), None, 0)
     check(host(out)[0], host(q)[0], ref.q4_roundtrip(host(k))[0], ref.q4_roundtrip(host(v))[0], scale, torch.bfloat16)
+
+
+@pytest.mark.parametrize("G,D", [(2, 128), (8, 128), (3, 64), (6, 64)])
+def test_long_rows_do_not_shrink(kv4, G, D):
+    """Values of one sign over a row that one CTA attends (max_len says it is short): rounded sums leave errors of either
+    sign, so their mean over all dims stays at what the chains of two MMAs cut off, 2^-24 each, and the parts' own last
+    bits. Sums cut off from start to end would be 313 * 2^-25 low and more."""
+    n = 20000
+    c = kv4.KV4Cache(1, n, 1, 1, D)
+    k, v = rnd(1, 1, 1, n, 1, D), 1 + torch.rand(1, 1, n, 1, D, generator=torch.Generator().manual_seed(2)).cuda()
+    c.write(k, v)
+    q = rnd(3, 1, G, D)
+    got = host(c.attend(0, q, torch.tensor([n], dtype=torch.int32).cuda(), max_len=1))[0]
+    want = ref.attend(host(q)[0], ref.q4_roundtrip(host(k))[0, 0], ref.q4_roundtrip(host(v))[0, 0], D ** -0.5)
+    e = (got - want) / want
+    assert abs(e.mean()) <= 2.0 ** -21 and np.abs(e).max() <= 2.0 ** -18, (e.mean(), np.abs(e).max())
