@@ -828,7 +828,7 @@ cudaError_t launch_t(Kv4Attend a, bool pdl, cudaStream_t s) {
     if constexpr (HD == 128)
         if (a.ctas == kManyCtas) kernel = k_kv4_attend<HD, false, TI, TO, kManyCtas>;
     // With three / four CTAs (128 registers, which spill), G = 8 in bf16: 64 x 8192 rows 139 / 139 us, 32 x 4096 49 / 52,
-    // 16 x 2048 23.2 / 27.5, 16 of up to 2048 22.8 / 18.5, 32 of up to 4096 36.1 / 36.5; f32 161 / 161 and 53.5 / 57.3.
+    // 16 x 2048 23.2 / 27.5, 16 of up to 2048 22.8 / 18.5, 32 of up to 4096 36.6 / 36.5; f32 172 / 172 and 56.8 / 60.7.
     if (wide) {
         if (a.ctas == kManyCtas) a.grid = std::max(1, a.grid * kFewCtas / kManyCtas);
         a.ctas = kFewCtas;
