@@ -59,7 +59,13 @@ typedef enum {
  * head_dim 128 (EINVAL otherwise).
  * TALKER_DTYPE_Q4_0 likewise, with blocks of 32 4-bit codes and an fp16 scale as
  * talker_kv4.h defines them: 4.5 bits an element. */
-typedef enum { TALKER_DTYPE_F32 = 0, TALKER_DTYPE_BF16 = 1, TALKER_DTYPE_Q8_0 = 2, TALKER_DTYPE_Q4_0 = 3 } talker_dtype;
+typedef enum {
+    TALKER_DTYPE_F32 = 0,
+    TALKER_DTYPE_BF16 = 1,
+    TALKER_DTYPE_Q8_0 = 2,
+    TALKER_DTYPE_Q4_0 = 3,
+    TALKER_DTYPE_E4M3 = 4 /* rows of talker_layer.h only: 8-bit floats with scales beside them */
+} talker_dtype;
 
 /* Geometry and storage formats (names as in the rightkit-qts TtsTransformerConfig).
  * Supported: head_dim in {32, 64, 128}; n_q_heads a multiple of n_kv_heads with

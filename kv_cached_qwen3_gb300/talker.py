@@ -101,6 +101,20 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "talker_test_kv4_attend_mixed": (st, [vp, ctypes.c_int, vp, ctypes.c_int, ctypes.c_int, ctypes.c_float, vp, vp, vp,
                                               ctypes.c_size_t, vp]),
         "talker_kv4_reorder": (st, [vp, vp, ctypes.c_int, vp, vp, vp, vp]),
+        "talker_rms_norm": (st, [vp, ctypes.c_int, vp, vp, ctypes.c_int, vp, vp, ctypes.c_float] + [ctypes.c_int] * 3 +
+                            [vp, vp, vp, ctypes.c_int, vp, ctypes.c_int, vp, vp]),
+        "talker_rope_turns": (st, [vp, vp, ctypes.POINTER(ctypes.c_float)]),
+        "talker_rotate": (st, [vp, ctypes.c_float] + [ctypes.c_int] * 3 + [vp, ctypes.c_int, ctypes.c_int, vp, ctypes.c_int,
+                                                                           ctypes.c_int, vp]),
+        "talker_draft_scratch": (ctypes.c_size_t, [ctypes.c_int] * 3),
+        "talker_draft_verify": (st, [vp, i64, i64, vp, i64, i64, ctypes.c_int] + [vp] * 4 + [ctypes.c_int] * 3 + [vp] * 4 +
+                                [ctypes.c_size_t, vp]),
+        "talker_w4_bytes": (ctypes.c_size_t, [vp]),
+        "talker_w4_pack": (st, [vp] * 8),
+        "talker_w4_quantize": (st, [vp, ctypes.c_int, i64] + [ctypes.c_int] * 3 + [vp] * 3),
+        "talker_w4_scratch": (ctypes.c_size_t, [vp, ctypes.c_int, ctypes.c_int]),
+        "talker_w4_matmul": (st, [vp, vp, ctypes.c_int, i64, vp, ctypes.c_int, ctypes.c_int, vp, i64, vp, ctypes.c_int, i64, vp,
+                                  ctypes.c_size_t, vp]),
         "talker_beam_scratch": (ctypes.c_size_t, [ctypes.c_int] * 3),
         "talker_beam_select": (st, [vp, i64, ctypes.c_int, vp, vp] + [ctypes.c_int] * 4 + [vp] * 5 +
                                [ctypes.c_size_t, vp]),
