@@ -25,7 +25,7 @@ extern "C" {
  *   the next token t is the first with sum_{v <= t} w(v) > u_n_draft sum_v w(v),
  *   w = max(p_n - q_n, 0) where x_n was refused (p_n if that is 0 everywhere, which
  *   only rounding can bring about), w = p_n if all count were taken.
- * T not above 1e-20 (0, negative or NaN) is greedy: p_i is all on the first of the row's
+ * T above 1e18 counts as 1e18. T not above 1e-20 (0, negative or NaN) is greedy: p_i is all on the first of the row's
  * largest logits, x_i is taken if it is that token, and draft logits are not read.
  *
  * tokens_out [n_seq][n_draft + 1]: the taken tokens, the next token, then -1;
@@ -48,7 +48,7 @@ extern "C" {
  * contiguous values; draft likewise (NULL: none), n_draft rows. dtype F32 or BF16 for
  * both. tokens int32 [n_seq][n_draft], counts int32 [n_seq] or NULL, uniforms f32
  * [n_seq][n_draft + 1], temperatures f32 [n_seq] or NULL (1). Outputs must not overlap
- * inputs. n_draft <= 64, vocab <= 2^26, n_seq <= 65536.
+ * inputs. n_draft <= 64, vocab <= 2^26, n_seq <= 65535.
  * scratch: talker_draft_scratch bytes, 16-byte aligned (may be NULL when that is 0); it need not
  * hold anything on entry, and calls that may run at the same time need their own.
  * Errors: EINVAL, ECUDA. */

@@ -12,13 +12,17 @@ using namespace talker_dev;
 
 namespace {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kWarps = 16, kThreads = kWarps * 32;   // of the CTAs that choose
+constexpr int kRowWarps = 8;            // of those that read rows for them
 constexpr int kCluster = 8;
-constexpr int kMaxDraft = 64;
-constexpr int kMaxParts = 16;           // of a row
+constexpr int kMaxDraft = 64, kMaxRows = 2 * kMaxDraft + 1;
+constexpr int kMaxParts = 32;           // of a row: a lane each where they are joined
+constexpr int kOwnParts = kMaxRows + kCluster * kWarps;   // of a sequence, where its cluster reads its rows itself
 constexpr float kMasked = -1e30f;       // at or below: counts as -inf
+constexpr float kLeastRef = -9.9999994e29f;   // reference of a row's exponents without a logit: the next value above kMasked
 constexpr float kGreedy = 1e-20f;       // a temperature not above it
-constexpr float kNear = 1e-5f;          // of f32 sums: decisions nearer to their border are made again, exactly
+constexpr float kHottest = 1e18f;       // a temperature above it counts as this one (masked logits still add nothing)
+constexpr float kNear = 1e-4f;          // of f32 sums: decisions nearer to their border are made again, exactly
 constexpr double kLog2e = 1.4426950408889634074;
 
 struct Args {
@@ -30,55 +34,140 @@ struct Args {
     int32_t *tokens_out, *accepted;
     float *logprobs;
     int parts;              // of a row
+    struct Seen *seen;      // scratch: [sequence][row][part]
 };
 
 template <typename T>
 __device__ __forceinline__ float load_logit(const T *p, int i) { return Elem<T>::load(p, i); }
 __device__ __forceinline__ bool masked(float x) { return !(x > kMasked); }
 
-// A row's largest logit, the first place that has it, and the sum of e^((x - most) / T). Without a logit that is not masked:
-// -inf, and a sum of 0.
+// What is read of a sequence: target rows 0 .. count, then draft rows 0 .. count - 1, unless it is greedy.
+struct Sequence {
+    int count;
+    float temperature;
+    bool greedy, drafted;
+    __device__ __forceinline__ int targets() const { return count + 1; }
+    __device__ __forceinline__ int rows() const { return targets() + (drafted ? count : 0); }
+};
+__device__ __forceinline__ Sequence sequence(const Args &a, int seq) {
+    Sequence s;
+    s.count = a.counts ? min(max(a.counts[seq], 0), a.n_draft) : a.n_draft;
+    s.temperature = a.temperatures ? fminf(a.temperatures[seq], kHottest) : 1.f;
+    if (a.temperatures && isnan(a.temperatures[seq])) s.temperature = 0.f;
+    s.greedy = !(s.temperature > kGreedy);
+    s.drafted = a.draft != nullptr && !s.greedy;
+    return s;
+}
+template <typename T>
+__device__ __forceinline__ const T *row_at(const Args &a, const Sequence &s, int seq, int r) {
+    return r < s.targets() ? static_cast<const T *>(a.target) + seq * a.target_seq + r * a.target_row
+                           : static_cast<const T *>(a.draft) + seq * a.draft_seq + (r - s.targets()) * a.draft_row;
+}
+
+// A row's largest logit (at least kLeastRef, below which masked ones add nothing), the first place that has it (of greedy
+// sequences), and the sum of e^((x - most) / T) (of others).
 struct Seen {
     float most, sum;
     int first;
+    __device__ __forceinline__ bool alive() const { return most > kLeastRef && most < INFINITY; }
 };
 __device__ __forceinline__ float ex2(float x) {   // relative error about 2^-22, 0 at -inf
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ Seen join(const Seen &a, const Seen &b, float c) {
-    Seen r;
-    r.most = fmaxf(a.most, b.most);
-    r.first = a.most == r.most ? (b.most == r.most ? min(a.first, b.first) : a.first) : b.first;
-    // (a difference of -inf from itself is not made)
-    r.sum = (a.sum > 0.f ? a.sum * ex2((a.most - r.most) * c) : 0.f) + (b.sum > 0.f ? b.sum * ex2((b.most - r.most) * c) : 0.f);
-    return r;
+__device__ __forceinline__ Seen warp_join(Seen s, float c) {
+    const float most = warp_max(s.most);
+    s.sum = warp_sum(s.sum * ex2((s.most - most) * c));
+    s.first = (int)__reduce_min_sync(0xffffffffu, s.most == most ? (uint32_t)s.first : 0x7fffffffu);
+    s.most = most;
+    return s;
 }
 
-// Part `part` of `parts` of a row, by one warp; c = log2 e / T.
+template <typename T> struct Vec;
+template <> struct Vec<float> {
+    static constexpr int N = 4;
+    __device__ static __forceinline__ void unpack(const uint4 u, float *x) {
+        x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y), x[2] = __uint_as_float(u.z), x[3] = __uint_as_float(u.w);
+    }
+};
+template <> struct Vec<__nv_bfloat16> {
+    static constexpr int N = 8;
+    __device__ static __forceinline__ void unpack(const uint4 u, float *x) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[2 * i] = bf16lo(w[i]), x[2 * i + 1] = bf16hi(w[i]);
+    }
+};
+
+// n values, the first of them logit `at` of its row.
+template <int N>
+__device__ __forceinline__ void take(Seen &s, float (&x)[N], int at, float c, bool greedy) {
+    float top = kLeastRef;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        x[i] = fmaxf(x[i], kMasked);   // NaN too
+        top = fmaxf(top, x[i]);
+    }
+    if (greedy) {
+        if (top > s.most) {
+            s.most = top;
+            int first = 0;
+#pragma unroll
+            for (int i = N - 1; i >= 0; --i)
+                if (x[i] == top) first = i;
+            s.first = at + first;
+        }
+        return;
+    }
+    if (top > s.most) {
+        s.sum *= ex2((s.most - top) * c);
+        s.most = top;
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum += ex2((x[i] - s.most) * c);
+    s.sum += sum;
+}
+
+// Part `part` of `parts` of a row, by one warp; c = log2 e / T. A part is so many of the row's vectors of 16 bytes; logits
+// before the first and after the last are the first and the last part's.
 template <typename T>
-__device__ Seen see_part(const T *row, int vocab, int part, int parts, float c) {
+__device__ Seen see_part(const T *row, int vocab, int part, int parts, float c, bool greedy) {
+    constexpr int N = Vec<T>::N, kAhead = 4;
     const int lane = threadIdx.x & 31;
-    const int from = (int)((long long)vocab * part / parts), to = (int)((long long)vocab * (part + 1) / parts);
-    Seen s{-INFINITY, 0.f, 0x7fffffff};
-    for (int i = from + lane; i < to; i += 32) {
-        const float x = load_logit(row, i);
-        if (masked(x)) continue;
-        if (x > s.most) {
-            s.sum = (s.sum > 0.f ? s.sum * ex2((s.most - x) * c) : 0.f) + 1.f;
-            s.most = x;
-            s.first = i;
-        } else {
-            s.sum += ex2((x - s.most) * c);
+    const int lead = min(vocab, (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) % 16 / sizeof(T)));
+    const int vecs = (vocab - lead) / N;
+    const int from = (int)((long long)vecs * part / parts), to = (int)((long long)vecs * (part + 1) / parts);
+    Seen s{kLeastRef, 0.f, 0x7fffffff};
+    if (part == 0 && lane < lead) {
+        float x[1] = {load_logit(row, lane)};
+        take(s, x, lane, c, greedy);
+    }
+    const uint4 *v = reinterpret_cast<const uint4 *>(row + lead);
+    int i = from + lane;
+    for (; i + (kAhead - 1) * 32 < to; i += kAhead * 32) {
+        uint4 u[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) u[j] = ldg_stream(v + i + j * 32);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            float x[N];
+            Vec<T>::unpack(u[j], x);
+            take(s, x, lead + (i + j * 32) * N, c, greedy);
         }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const Seen b{__shfl_xor_sync(0xffffffffu, s.most, o), __shfl_xor_sync(0xffffffffu, s.sum, o), __shfl_xor_sync(0xffffffffu, s.first, o)};
-        s = join(s, b, c);
+    for (; i < to; i += 32) {
+        float x[N];
+        Vec<T>::unpack(ldg_stream(v + i), x);
+        take(s, x, lead + i * N, c, greedy);
     }
-    return s;
+    const int tail = lead + vecs * N + lane;
+    if (part == parts - 1 && tail < vocab) {
+        float x[1] = {load_logit(row, tail)};
+        take(s, x, tail, c, greedy);
+    }
+    return warp_join(s, c);
 }
 
 // e^((x - most) / T) = m 2^(-31 - shift), m in [2^31, 2^32), for x <= most, to about 2^-31 of itself. With
@@ -112,87 +201,100 @@ __device__ __forceinline__ Exact exact_exp(float x, float most, const Scale c, c
     return {r + (uint32_t)(((long long)r * rise) >> 32), -(k >> 5)};
 }
 
-// Sums of whole numbers over the CTA, in every thread.
 __device__ __forceinline__ unsigned long long warp_sum64(unsigned long long v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
+// The rows' parts, a warp each, for calls that a sequence's cluster would read too slowly.
+template <typename T>
+__global__ void __launch_bounds__(kRowWarps * 32) k_draft_rows(const Args a) {
+    const int seq = blockIdx.y, t = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+    const Sequence q = sequence(a, seq);
+    if (t < q.rows() * a.parts) {
+        const int r = t / a.parts;
+        const Seen s = see_part(row_at<T>(a, q, seq, r), a.vocab, t - r * a.parts, a.parts, (float)kLog2e / q.temperature, q.greedy);
+        if ((threadIdx.x & 31) == 0) a.seen[(size_t)seq * (2 * a.n_draft + 1) * a.parts + t] = s;
+    }
+    pdl_launch_dependents();
+}
+
 enum Verdict : int { kTake = 0, kRefuse = 1, kUnsure = 2 };
 
 struct Shared {
     uint32_t roots[32];                        // 2^(31 + j / 32)
-    Seen parts[(2 * kMaxDraft + 1) * kMaxParts];   // of CTA 0: the rows' parts
-    Seen rows[2 * kMaxDraft + 1];              // joined; target rows, then draft rows
+    Seen parts[kOwnParts];                     // of CTA 0
+    Seen rows[kMaxRows];                       // joined
     int verdict[kMaxDraft];
     unsigned long long warp[kWarps][2];
     unsigned long long cta[kCluster][2];       // every CTA's sums
-    float most[kCluster][2];
-    int row;                                   // the row that is looked at, decided: drawn from
-    int found;
+    int row;                                   // the row that is looked at; decided: drawn from
 };
 
-// Everything a draw needs to know of a row of probabilities: p = m scale >> (down + shift), in units of 2^-62.
+// A row of probabilities: p = m factor >> (down + shift), in units of 2^-62, of an Exact.
 struct Row {
     float most;
-    Scale c;
     uint32_t factor;   // 0: no distribution
     int down;
     double z;          // the sum of e^((x - most) / T)
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_draft_verify(const Args a) {
-    extern __shared__ unsigned char raw[];
-    Shared &s = *reinterpret_cast<Shared *>(raw);
+// A cluster per sequence. Its first CTA decides by f32 sums which drafts are surely taken and which first one is
+// not; that one's rows, and those that the next token is drawn from, are gone over by all CTAs, each a range of the vocabulary, with
+// exponentials of 31 bits and sums in whole numbers: which token a uniform number meets is a question of sums of
+// 10^5 terms next to one another, where f32 would err once in some hundred draws.
+template <typename T, bool OWN>
+__global__ void __launch_bounds__(kThreads, 1) k_draft_choose(const Args a) {
+    __shared__ Shared s;
     cg::cluster_group cluster = cg::this_cluster();
     const int ctas = cluster.num_blocks(), rank = cluster.block_rank(), seq = blockIdx.x / ctas;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int K = a.n_draft, V = a.vocab;
-    const int count = a.counts ? min(max(a.counts[seq], 0), K) : K;
-    const float temperature = a.temperatures ? a.temperatures[seq] : 1.f;
-    const bool greedy = !(temperature > kGreedy), drafted = a.draft != nullptr && !greedy;
-    const Scale c = greedy ? Scale{1.f, 0.f} : scale_of(temperature);
-    const T *target = static_cast<const T *>(a.target) + seq * a.target_seq;
-    const T *draft = static_cast<const T *>(a.draft) + seq * a.draft_seq;
+    const Sequence sq = sequence(a, seq);
+    const int count = sq.count, n_rows = sq.rows();
+    const bool greedy = sq.greedy, drafted = sq.drafted;
+    const double temperature = sq.temperature;
+    const Scale c = greedy ? Scale{1.f, 0.f} : scale_of(sq.temperature);
     const float *u = a.uniforms + (size_t)seq * (K + 1);
     const int32_t *tokens = a.tokens + (size_t)seq * K;
     Shared *lead = cluster.map_shared_rank(&s, 0);
     if (tid < 32) s.roots[tid] = (uint32_t)llrint(exp2(31.0 + tid / 32.0));
     cluster.sync();   // every CTA's shared memory is there
 
-    // the rows' sums: target rows before the last draft (of greedy sequences the one after too), and draft rows
-    const int n_target = count + (greedy ? 1 : 0), n_rows = n_target + (drafted ? count : 0);
-    for (int t = rank * kWarps + warp; t < n_rows * a.parts; t += ctas * kWarps) {
-        const int r = t / a.parts;
-        const T *row = r < n_target ? target + r * a.target_row : draft + (r - n_target) * a.draft_row;
-        const Seen seen = see_part(row, V, t - r * a.parts, a.parts, c.hi);
-        if (lane == 0) lead->parts[t] = seen;
+    if (OWN) {
+        for (int t = rank * kWarps + warp; t < n_rows * a.parts; t += ctas * kWarps) {
+            const int r = t / a.parts;
+            const Seen seen = see_part(row_at<T>(a, sq, seq, r), V, t - r * a.parts, a.parts, c.hi, greedy);
+            if (lane == 0) lead->parts[t] = seen;
+        }
+        cluster.sync();
+    } else {
+        pdl_wait();
     }
-    cluster.sync();
     if (rank == 0) {
-        for (int r = tid; r < n_rows; r += kThreads) {
-            Seen seen = s.parts[r * a.parts];
-            for (int i = 1; i < a.parts; ++i) seen = join(seen, s.parts[r * a.parts + i], c.hi);
-            s.rows[r] = seen;
+        const Seen *parts = OWN ? s.parts : a.seen + (size_t)seq * (2 * K + 1) * a.parts;
+        for (int r = warp; r < n_rows; r += kWarps) {
+            const Seen one = lane < a.parts ? parts[r * a.parts + lane] : Seen{kLeastRef, 0.f, 0x7fffffff};
+            const Seen seen = warp_join(one, c.hi);
+            if (lane == 0) s.rows[r] = seen;
         }
         __syncthreads();
         for (int i = tid; i < count; i += kThreads) {
             const int x = tokens[i];
             int v = kRefuse;
-            if (x >= 0 && x < V) {
-                const Seen p = s.rows[i];
-                const float logit = load_logit(target + i * a.target_row, x);
+            const Seen p = s.rows[i];
+            if (x >= 0 && x < V && p.alive()) {
+                const float logit = load_logit(row_at<T>(a, sq, seq, i), x);
                 if (greedy) {
-                    v = p.most < INFINITY && x == p.first ? kTake : kRefuse;
-                } else if (!masked(logit) && p.most < INFINITY) {
+                    v = x == p.first ? kTake : kRefuse;
+                } else if (!masked(logit)) {
                     const float px = ex2((logit - p.most) * c.hi) / p.sum;
                     float qx = 1.f;
                     if (drafted) {
-                        const Seen q = s.rows[n_target + i];
-                        const float other = load_logit(draft + i * a.draft_row, x);
-                        qx = masked(other) || !(q.most < INFINITY) ? 0.f : ex2((other - q.most) * c.hi) / q.sum;
+                        const Seen q = s.rows[sq.targets() + i];
+                        const float other = load_logit(row_at<T>(a, sq, seq, sq.targets() + i), x);
+                        qx = masked(other) || !q.alive() ? 0.f : ex2((other - q.most) * c.hi) / q.sum;
                     }
                     const float need = fminf(fmaxf(u[i], 0.f), 1.f) * qx;
                     // (an exponential that f32 cannot tell from 0 decides nothing)
@@ -204,11 +306,30 @@ __global__ void __launch_bounds__(kThreads) k_draft_verify(const Args a) {
         __syncthreads();
     }
 
-    // the first draft that is not surely taken, exactly; then the draw
     int n = 0;
     Row p{}, q{};
-    const int bits = 32 - __clz(V - 1 > 0 ? V - 1 : 1), lift = 32 - bits;   // a sum of V numbers below 2^(32 + lift) fits
+    const int bits = 32 - __clz(max(V - 1, 1)), lift = 32 - bits;   // a sum of V numbers below 2^(32 + lift) fits 64 bits
+    // this CTA's range, and its warps'
     const int from = (int)((long long)V * rank / ctas), to = (int)((long long)V * (rank + 1) / ctas);
+    const int each = (to - from + kWarps - 1) / kWarps;
+    const int w0 = min(from + warp * each, to), w1 = min(w0 + each, to);
+    const T *rp = nullptr, *rq = nullptr;
+    // a value from each CTA's sums over its warps to all CTAs
+    auto spread = [&](unsigned long long v0, unsigned long long v1) {
+        v0 = warp_sum64(v0), v1 = warp_sum64(v1);
+        if (lane == 0) s.warp[warp][0] = v0, s.warp[warp][1] = v1;
+        __syncthreads();
+        if (tid < 2 * ctas) {
+            unsigned long long v = 0;
+            for (int w = 0; w < kWarps; ++w) v += s.warp[w][tid & 1];
+            cluster.map_shared_rank(&s, tid >> 1)->cta[rank][tid & 1] = v;
+        }
+        cluster.sync();
+    };
+    auto whole = [&](float x, float most) -> unsigned long long {   // e^((x - most) / T) in units of 2^-(31 + lift)
+        const Exact e = exact_exp(x, most, c, s.roots);
+        return e.shift < 64 ? (((unsigned long long)e.m << lift) + (1ull << e.shift >> 1)) >> e.shift : 0;
+    };
     while (true) {
         if (rank == 0 && tid == 0) {
             while (n < count && s.verdict[n] == kTake) ++n;
@@ -218,137 +339,90 @@ __global__ void __launch_bounds__(kThreads) k_draft_verify(const Args a) {
         n = lead->row;
         const int verdict = n < count ? lead->verdict[n] : kRefuse;   // (read before CTA 0 may change it below)
         if (greedy) break;
-        // the largest logits
-        const T *rows[2] = {target + n * a.target_row, draft + n * a.draft_row};
-        const int both = drafted && n < count ? 2 : 1;
-        if (n < count) {
-            p.most = lead->rows[n].most;
-            if (both == 2) q.most = lead->rows[n_target + n].most;
-        } else {
-            float m = -INFINITY;
-            for (int i = from + tid; i < to; i += kThreads) {
-                const float x = load_logit(rows[0], i);
-                if (!masked(x)) m = fmaxf(m, x);
-            }
-            m = warp_max(m);
-            if (lane == 0) s.warp[warp][0] = __float_as_uint(m);
-            __syncthreads();
-            if (tid < ctas) {
-                m = -INFINITY;
-                for (int w = 0; w < kWarps; ++w) m = fmaxf(m, __uint_as_float((uint32_t)s.warp[w][0]));
-                cluster.map_shared_rank(&s, tid)->most[rank][0] = m;
-            }
-            cluster.sync();
-            p.most = -INFINITY;
-            for (int i = 0; i < ctas; ++i) p.most = fmaxf(p.most, s.most[i][0]);
-        }
-        // their sums
+        const Seen ps = lead->rows[n], qs = drafted && n < count ? lead->rows[sq.targets() + n] : Seen{kLeastRef, 0.f, 0};
+        p.most = ps.most, q.most = qs.most;
+        rp = row_at<T>(a, sq, seq, n);
+        rq = drafted && n < count ? row_at<T>(a, sq, seq, sq.targets() + n) : nullptr;
+        p.factor = q.factor = 0;
+        p.z = 0.0;
+        if (rq == nullptr && verdict == kRefuse) break;   // (drawn from p alone: its sum is the draw's)
         unsigned long long sums[2] = {0, 0};
-        for (int w = 0; w < both; ++w) {
-            const float most = w ? q.most : p.most;
-            if (!(most > kMasked && most < INFINITY)) continue;
-            for (int i = from + tid; i < to; i += kThreads) {
-                const Exact e = exact_exp(load_logit(rows[w], i), most, c, s.roots);
-                if (e.shift < 64) sums[w] += (((unsigned long long)e.m << lift) + (1ull << e.shift >> 1)) >> e.shift;
+        if (ps.alive() && qs.alive()) {
+#pragma unroll 4
+            for (int i = w0 + lane; i < w1; i += 32) {
+                const float x = load_logit(rp, i), y = load_logit(rq, i);
+                sums[0] += whole(x, p.most);
+                sums[1] += whole(y, q.most);
             }
+        } else if (ps.alive()) {
+#pragma unroll 4
+            for (int i = w0 + lane; i < w1; i += 32) sums[0] += whole(load_logit(rp, i), p.most);
         }
-        for (int w = 0; w < 2; ++w) {
-            sums[w] = warp_sum64(sums[w]);
-            if (lane == 0) s.warp[warp][w] = sums[w];
-        }
-        __syncthreads();
-        if (tid < 2 * ctas) {
-            unsigned long long v = 0;
-            for (int w = 0; w < kWarps; ++w) v += s.warp[w][tid & 1];
-            cluster.map_shared_rank(&s, tid >> 1)->cta[rank][tid & 1] = v;
-        }
-        cluster.sync();
+        spread(sums[0], sums[1]);
         for (int w = 0; w < 2; ++w) {
             unsigned long long z = 0;
             for (int i = 0; i < ctas; ++i) z += s.cta[i][w];
-            Row &r = w ? q : p;
-            r.c = c;
-            r.factor = 0;
             if (z == 0) continue;
-            const int lead_zeros = __clzll(z);
-            // 2^95 / (z 2^lead_zeros), in (2^31, 2^32]
-            r.factor = (uint32_t)fmin(0x1p95 / (double)(z << lead_zeros), 4294967295.0);
-            r.down = 33 - lift - lead_zeros;
+            Row &r = w ? q : p;
+            const int zeros = __clzll(z);
+            // 2^95 / (z 2^zeros), in (2^31, 2^32]
+            r.factor = (uint32_t)fmin(0x1p95 / (double)(z << zeros), 4294967295.0);
+            r.down = 33 - lift - zeros;
             r.z = (double)z * exp2(-(double)(31 + lift));
         }
         if (verdict == kRefuse) break;
-        // an unsure draft
-        if (rank == 0 && tid == 0) {
+        if (rank == 0 && tid == 0) {   // an unsure draft
             const int x = tokens[n];
             auto of = [&](const T *row, const Row &r) {   // (of values that the draw takes for 0 too)
                 const float logit = load_logit(row, x);
-                return r.factor && !masked(logit) ? exp(((double)logit - (double)r.most) / (double)temperature) / r.z : 0.0;
+                return r.factor && !masked(logit) ? exp(((double)logit - (double)r.most) / temperature) / r.z : 0.0;
             };
-            const double px = of(rows[0], p), qx = both == 2 ? of(rows[1], q) : 1.0;
+            const double px = of(rp, p), qx = rq != nullptr ? of(rq, q) : 1.0;
             s.verdict[n] = (double)fminf(fmaxf(u[n], 0.f), 1.f) * qx < px ? kTake : kRefuse;
         }
         cluster.sync();
         if (lead->verdict[n] == kRefuse) break;
     }
 
+    const size_t out = (size_t)seq * (K + 1);
     if (rank == 0) {   // the drafts that are taken
         for (int i = tid; i <= K; i += kThreads) {
-            a.tokens_out[(size_t)seq * (K + 1) + i] = i < n ? tokens[i] : -1;
+            int token = i < n ? tokens[i] : -1;
+            if (greedy && i == n && s.rows[n].alive()) token = s.rows[n].first;
+            a.tokens_out[out + i] = token;
             if (a.logprobs) {
                 float lp = 0.f;
                 if (i < n && !greedy)
-                    lp = (float)(((double)load_logit(target + i * a.target_row, tokens[i]) - (double)s.rows[i].most) / (double)temperature -
-                                 log((double)s.rows[i].sum));
-                a.logprobs[(size_t)seq * (K + 1) + i] = lp;
+                    lp = (float)(((double)load_logit(row_at<T>(a, sq, seq, i), token) - (double)s.rows[i].most) / temperature - log((double)s.rows[i].sum));
+                a.logprobs[out + i] = lp;
             }
         }
         if (tid == 0) a.accepted[seq] = n;
-        __syncthreads();
-    }
-    if (greedy) {
-        if (rank == 0 && tid == 0) {
-            const Seen r = s.rows[n];
-            a.tokens_out[(size_t)seq * (K + 1) + n] = r.most > kMasked && r.most < INFINITY ? r.first : -1;
-        }
-        cluster.sync();   // (CTA 0's shared memory is read until here)
-        return;
     }
     // the draw
-    const T *rp = target + n * a.target_row, *rq = draft + n * a.draft_row;
-    const bool minus_q = n < count && drafted;
-    const int gone = n < count && a.draft == nullptr ? tokens[n] : -1;   // (without draft logits: all of q is on the draft)
-    auto weight = [&](int i, bool plain) -> unsigned long long {
-        if (p.factor == 0) return 0;
-        const Exact e = exact_exp(load_logit(rp, i), p.most, c, s.roots);
-        const int sh = p.down + e.shift;
-        unsigned long long w = e.shift < 64 && sh < 64 ? (unsigned long long)e.m * p.factor >> sh : 0;
-        if (plain) return w;
-        if (i == gone) return 0;
-        if (minus_q && q.factor) {
-            const Exact g = exact_exp(load_logit(rq, i), q.most, c, s.roots);
-            const int gs = q.down + g.shift;
-            const unsigned long long v = g.shift < 64 && gs < 64 ? (unsigned long long)g.m * q.factor >> gs : 0;
-            w = w > v ? w - v : 0;
-        }
-        return w;
+    const bool minus_q = rq != nullptr && q.factor != 0;
+    const int gone = n < count && a.draft == nullptr ? tokens[n] : -1;   // (without draft logits all of q is on the draft)
+    auto weight = [&](float x, float y, int i, bool plain) -> unsigned long long {
+        if (!minus_q) return i == gone && !plain ? 0 : whole(x, p.most);
+        const Exact e = exact_exp(x, p.most, c, s.roots), g = exact_exp(y, q.most, c, s.roots);
+        const int es = p.down + e.shift, gs = q.down + g.shift;
+        const unsigned long long w = e.shift < 64 && es < 64 ? (unsigned long long)e.m * p.factor >> es : 0;
+        const unsigned long long v = g.shift < 64 && gs < 64 && !plain ? (unsigned long long)g.m * q.factor >> gs : 0;
+        return w > v ? w - v : 0;
     };
-    const int each = (to - from + kWarps - 1) / kWarps;   // of a warp
-    const int w0 = min(from + warp * each, to), w1 = min(w0 + each, to);
     bool plain = n == count;
     unsigned long long total = 0, before = 0;
-    while (true) {
+    while (!greedy && lead->rows[n].alive()) {
         cluster.sync();   // (s.cta is free again)
         unsigned long long sum = 0;
-        for (int i = w0 + lane; i < w1; i += 32) sum += weight(i, plain);
-        sum = warp_sum64(sum);
-        if (lane == 0) s.warp[warp][0] = sum;
-        __syncthreads();
-        if (tid < ctas) {
-            unsigned long long v = 0;
-            for (int w = 0; w < kWarps; ++w) v += s.warp[w][0];
-            cluster.map_shared_rank(&s, tid)->cta[rank][0] = v;
+        if (minus_q) {
+#pragma unroll 4
+            for (int i = w0 + lane; i < w1; i += 32) sum += weight(load_logit(rp, i), load_logit(rq, i), i, plain);
+        } else {
+#pragma unroll 4
+            for (int i = w0 + lane; i < w1; i += 32) sum += weight(load_logit(rp, i), 0.f, i, plain);
         }
-        cluster.sync();
+        spread(sum, 0);
         total = before = 0;
         for (int i = 0; i < ctas; ++i) {
             if (i < rank) before += s.cta[i][0];
@@ -357,52 +431,75 @@ __global__ void __launch_bounds__(kThreads) k_draft_verify(const Args a) {
         if (total != 0 || plain) break;
         plain = true;
     }
-    if (total == 0) {
-        cluster.sync();
-        return;   // no distribution: -1 is there already
-    }
-    const float un = fminf(fmaxf(u[K], 0.f), 1.f);
-    const unsigned long long un64 = un >= 1.f ? ~0ull : (unsigned long long)(un * 0x1p64f);
-    const unsigned long long border = __umul64hi(un64, total);   // the first token whose sum is above it
-    if (border >= before && border < before + s.cta[rank][0]) {
-        // its warp's tokens, then a thread's, then itself
-        int w = 0;
-        while (border - before >= s.warp[w][0]) before += s.warp[w++][0];
-        const int b0 = min(from + w * each, to), b1 = min(b0 + each, to), own = (b1 - b0 + kThreads - 1) / kThreads;
-        const int i0 = min(b0 + tid * own, b1), i1 = min(i0 + own, b1);
-        unsigned long long sum = 0;
-        for (int i = i0; i < i1; ++i) sum += weight(i, plain);
-        unsigned long long up = sum;
+    if (total != 0) {
+        const float un = fminf(fmaxf(u[K], 0.f), 1.f);
+        const unsigned long long un64 = un >= 1.f ? ~0ull : (unsigned long long)(un * 0x1p64f);
+        const unsigned long long border = __umul64hi(un64, total);   // the first token whose sum is above it
+        if (border >= before && border - before < s.cta[rank][0]) {
+            // its warp's tokens, then a thread's, then itself
+            int w = 0;
+            while (border - before >= s.warp[w][0]) before += s.warp[w++][0];
+            const int b0 = min(from + w * each, to), b1 = min(b0 + each, to), own = (b1 - b0 + kThreads - 1) / kThreads;
+            const int i0 = min(b0 + tid * own, b1), i1 = min(i0 + own, b1);
+            auto at_token = [&](int i) { return weight(load_logit(rp, i), minus_q ? load_logit(rq, i) : 0.f, i, plain); };
+            unsigned long long sum = 0;
+            for (int i = i0; i < i1; ++i) sum += at_token(i);
+            unsigned long long up = sum;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const unsigned long long v = __shfl_up_sync(0xffffffffu, up, o);
-            if (lane >= o) up += v;
-        }
-        if (lane == 31) s.warp[warp][1] = up;
-        __syncthreads();
-        unsigned long long at = before + up - sum;
-        for (int i = 0; i < warp; ++i) at += s.warp[i][1];
-        if (border >= at && border - at < sum) {
-            int i = i0;
-            for (unsigned long long v; border - at >= (v = weight(i, plain)); ++i) at += v;
-            a.tokens_out[(size_t)seq * (K + 1) + n] = i;
-            if (a.logprobs)
-                a.logprobs[(size_t)seq * (K + 1) + n] =
-                    (float)(((double)load_logit(rp, i) - (double)p.most) / (double)temperature - log(p.z));
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned long long v = __shfl_up_sync(0xffffffffu, up, o);
+                if (lane >= o) up += v;
+            }
+            if (lane == 31) s.warp[warp][1] = up;
+            __syncthreads();
+            unsigned long long at = before + up - sum;
+            for (int i = 0; i < warp; ++i) at += s.warp[i][1];
+            if (border >= at && border - at < sum) {
+                int i = i0;
+                for (unsigned long long v; border - at >= (v = at_token(i)); ++i) at += v;
+                a.tokens_out[out + n] = i;
+                if (a.logprobs) {
+                    double z = p.z;
+                    if (z == 0.0) {   // (no sum of p alone was made: it is the draw's, and the token's that was left out)
+                        const unsigned long long left = gone >= 0 && gone < V && !plain ? whole(load_logit(rp, gone), p.most) : 0;
+                        z = (double)(total + left) * exp2(-(double)(31 + lift));
+                    }
+                    a.logprobs[out + n] = (float)(((double)load_logit(rp, i) - (double)p.most) / temperature - log(z));
+                }
+            }
         }
     }
     cluster.sync();   // (nobody leaves while others read its shared memory)
 }
 
 bool sizes_ok(int n_seq, int n_draft, int vocab) {
-    return n_seq >= 0 && n_seq <= 65536 && n_draft >= 0 && n_draft <= kMaxDraft && vocab >= 1 && vocab <= 1 << 26;
+    return n_seq >= 0 && n_seq <= 65535 && n_draft >= 0 && n_draft <= kMaxDraft && vocab >= 1 && vocab <= 1 << 26;
+}
+
+// A sequence's own cluster reads its rows while they are few logits; else the whole GPU does, in a launch before.
+constexpr int kOwnLogits = 65536;
+struct Shape {
+    bool own;
+    int parts;
+};
+Shape shape_of(int n_seq, int n_draft, int vocab) {
+    const int rows = 2 * n_draft + 1;
+    Shape p;
+    p.own = (long long)rows * vocab <= kOwnLogits;
+    const long long warps = p.own ? kCluster * kWarps : std::max(1ll, 152ll * 32 / std::max(1, n_seq));   // for a sequence
+    p.parts = (int)std::max(1ll, std::min<long long>(std::min(kMaxParts, vocab / 256), warps / rows));
+    return p;
 }
 
 }  // namespace
 
 extern "C" {
 
-size_t talker_draft_scratch(int, int, int) { return 0; }
+size_t talker_draft_scratch(int n_seq, int n_draft, int vocab) {
+    if (!sizes_ok(n_seq, n_draft, vocab)) return 0;
+    const Shape p = shape_of(n_seq, n_draft, vocab);
+    return p.own ? 0 : (size_t)n_seq * (2 * n_draft + 1) * p.parts * sizeof(Seen);
+}
 
 talker_status talker_draft_verify(const void *target, int64_t target_seq, int64_t target_row, const void *draft,
                                   int64_t draft_seq, int64_t draft_row, int dtype, const int32_t *tokens,
@@ -414,24 +511,34 @@ talker_status talker_draft_verify(const void *target, int64_t target_seq, int64_
     if (dtype != TALKER_DTYPE_F32 && dtype != TALKER_DTYPE_BF16) return TALKER_EINVAL;
     if ((reinterpret_cast<uintptr_t>(target) | reinterpret_cast<uintptr_t>(draft)) % (dtype == TALKER_DTYPE_F32 ? 4 : 2)) return TALKER_EINVAL;
     if (n_seq == 0) return TALKER_OK;
-    const int rows = 2 * n_draft + 1;
-    Args a{target, draft, target_seq, target_row, draft_seq, draft_row, tokens, counts, uniforms, temperatures, n_draft, vocab,
-           tokens_out, accepted, logprobs, 1};
-    a.parts = std::max(1, std::min(kMaxParts, kCluster * kWarps / rows));
+    const size_t need = talker_draft_scratch(n_seq, n_draft, vocab);
+    if (need > 0 && (!scratch || scratch_bytes < need || reinterpret_cast<uintptr_t>(scratch) % 16)) return TALKER_EINVAL;
+    const Shape p = shape_of(n_seq, n_draft, vocab);
+    const Args a{target, draft, target_seq, target_row, draft_seq, draft_row, tokens, counts, uniforms, temperatures, n_draft, vocab,
+                 tokens_out, accepted, logprobs, p.parts, static_cast<Seen *>(scratch)};
+    const bool f32 = dtype == TALKER_DTYPE_F32;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     cfg.blockDim = dim3(kThreads);
     cfg.gridDim = dim3((unsigned)(n_seq * kCluster));
-    cfg.dynamicSmemBytes = sizeof(Shared);
-    static_assert(sizeof(Shared) <= 48 * 1024, "without a raised limit");
     cfg.stream = static_cast<cudaStream_t>(cuda_stream);
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = kCluster;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e =
-        cudaLaunchKernelEx(&cfg, dtype == TALKER_DTYPE_F32 ? k_draft_verify<float> : k_draft_verify<__nv_bfloat16>, a);
+    cfg.numAttrs = p.own ? 1 : 2;
+    cudaError_t e = cudaSuccess;
+    if (!p.own) {
+        const dim3 grid((unsigned)(((2 * n_draft + 1) * p.parts + kRowWarps - 1) / kRowWarps), (unsigned)n_seq);
+        if (f32) k_draft_rows<float><<<grid, kRowWarps * 32, 0, cfg.stream>>>(a);
+        else k_draft_rows<__nv_bfloat16><<<grid, kRowWarps * 32, 0, cfg.stream>>>(a);
+        e = cudaGetLastError();
+        if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, f32 ? k_draft_choose<float, false> : k_draft_choose<__nv_bfloat16, false>, a);
+    } else {
+        e = cudaLaunchKernelEx(&cfg, f32 ? k_draft_choose<float, true> : k_draft_choose<__nv_bfloat16, true>, a);
+    }
     if (e == cudaSuccess) return TALKER_OK;
     cudaGetLastError();
     return TALKER_ECUDA;

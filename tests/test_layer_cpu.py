@@ -117,7 +117,7 @@ def test_draft_refusals(lib):
     def call(t=64, ts=30, tr=10, d=128, ds=20, dr=10, dtype=0, tok=256, cnt=None, u=320, temp=None, S=1, K=2, V=10, out=384, acc=448, lp=512, scratch=1024, need=1 << 30):
         return lib.talker_draft_verify(t, ts, tr, d, ds, dr, dtype, tok, cnt, u, temp, S, K, V, out, acc, lp, scratch, need, None)
     assert call(S=0) == 0
-    for kw in (dict(t=None), dict(t=66), dict(d=130), dict(t=65, dtype=1), dict(dtype=2), dict(dtype=4), dict(tok=None), dict(u=None), dict(S=-1), dict(S=65537), dict(K=-1), dict(K=65),
+    for kw in (dict(t=None), dict(t=66), dict(d=130), dict(t=65, dtype=1), dict(dtype=2), dict(dtype=4), dict(tok=None), dict(u=None), dict(S=-1), dict(S=65536), dict(K=-1), dict(K=65),
                dict(V=0), dict(V=(1 << 26) + 1), dict(out=None), dict(acc=None)):
         assert call(**kw) == 1, kw
 
