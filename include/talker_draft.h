@@ -39,7 +39,7 @@ extern "C" {
  * are taken to [0, n_draft] and uniform numbers to [0, 1] (NaN: 0).
  *
  * Probabilities that decide (p and q of a draft near its border, all of the row that is
- * drawn from) are made to about 2^-31 of themselves and summed as whole numbers (in the
+ * drawn from) are made to about 2^-30 of themselves and summed as whole numbers (in the
  * sums and the draw those below 2^-70 of the row's largest count as 0), so
  * neither a row's address nor the launch's shape changes a token; the sums of taken drafts'
  * logprobs are f32.

@@ -3,18 +3,21 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
+#include <utility>
 
 #include "common.cuh"
+#include "kv4.cuh"
 #include "talker_draft.h"
 
 namespace cg = cooperative_groups;
 using namespace talker_dev;
+using namespace talker_k;
 
 namespace {
 
-constexpr int kWarps = 16, kThreads = kWarps * 32;   // of the CTAs that choose
-constexpr int kRowWarps = 8;            // of those that read rows for them
-constexpr int kCluster = 8;
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kCluster = 16;            // CTAs of a sequence, at most
 constexpr int kMaxDraft = 64, kMaxRows = 2 * kMaxDraft + 1;
 constexpr int kMaxParts = 32;           // of a row: a lane each where they are joined
 constexpr int kOwnParts = kMaxRows + kCluster * kWarps;   // of a sequence, where its cluster reads its rows itself
@@ -23,7 +26,6 @@ constexpr float kLeastRef = -9.9999994e29f;   // reference of a row's exponents 
 constexpr float kGreedy = 1e-20f;       // a temperature not above it
 constexpr float kHottest = 1e18f;       // a temperature above it counts as this one (masked logits still add nothing)
 constexpr float kNear = 1e-4f;          // of f32 sums: decisions nearer to their border are made again, exactly
-constexpr double kLog2e = 1.4426950408889634074;
 
 struct Args {
     const void *target, *draft;
@@ -34,6 +36,7 @@ struct Args {
     int32_t *tokens_out, *accepted;
     float *logprobs;
     int parts;              // of a row
+    int ctas;               // of a sequence's cluster
     struct Seen *seen;      // scratch: [sequence][row][part]
 };
 
@@ -138,7 +141,7 @@ __device__ Seen see_part(const T *row, int vocab, int part, int parts, float c, 
     const int lane = threadIdx.x & 31;
     const int lead = min(vocab, (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) % 16 / sizeof(T)));
     const int vecs = (vocab - lead) / N;
-    const int from = (int)((long long)vecs * part / parts), to = (int)((long long)vecs * (part + 1) / parts);
+    const int from = (unsigned)vecs * part / parts, to = (unsigned)vecs * (part + 1) / parts;   // (2^24 times 32 at most)
     Seen s{kLeastRef, 0.f, 0x7fffffff};
     if (part == 0 && lane < lead) {
         float x[1] = {load_logit(row, lane)};
@@ -170,35 +173,66 @@ __device__ Seen see_part(const T *row, int vocab, int part, int parts, float c, 
     return warp_join(s, c);
 }
 
-// e^((x - most) / T) = m 2^(-31 - shift), m in [2^31, 2^32), for x <= most, to about 2^-31 of itself. With
+// e^((x - most) / T) = m 2^(-31 - shift), m in [2^31, 2^32), for x <= most, to about 2^-30 of itself. With
 // t = (x - most) log2 e / T in two floats, t = k / 32 + f, |f| <= 1/64: m = 2^31 2^(k % 32 / 32) e^y, y = f log 2, by the
-// series of e^y - 1, whose terms after y^4 / 24 are below 2^-39.
+// series of e^y - 1, whose terms after y^4 / 24 are below 2^-39. Below 2^-70, and of masked logits: 0, by a shift that
+// leaves nothing.
 struct Exact {
     uint32_t m;
-    int shift;   // 64: 0
+    int shift;
 };
+// v 2^32 >> s for any s (shifts of 32 or more give 0): five instructions, a 64-bit shift takes nine.
+__device__ __forceinline__ unsigned long long place(uint32_t v, int s) {
+    uint32_t hi, up, down;
+    asm("shr.u32 %0, %1, %2;" : "=r"(hi) : "r"(v), "r"(s));
+    asm("shl.b32 %0, %1, %2;" : "=r"(up) : "r"(v), "r"(32 - s));
+    asm("shr.u32 %0, %1, %2;" : "=r"(down) : "r"(v), "r"(s - 32));
+    return (unsigned long long)hi << 32 | (up | down);
+}
 struct Scale {   // log2 e / T in two floats
     float hi, lo;
 };
 __device__ __forceinline__ Scale scale_of(float temperature) {
-    const double c = kLog2e / (double)temperature;
-    const float hi = (float)c;
-    return {hi, (float)(c - (double)hi)};
+    constexpr float kHi = 1.44269502162933349609375f, kLo = 1.92596299112661746887e-08f;   // log2 e
+    const float hi = kHi / temperature;
+    return {hi, (fmaf(-hi, temperature, kHi) + kLo) / temperature};
 }
-__device__ __forceinline__ Exact exact_exp(float x, float most, const Scale c, const uint32_t *roots) {
-    const float d = x - most, b = d - x, dl = (x - (d - b)) - (most + b);   // x - most = d + dl, exactly
-    const float t = d * c.hi;
-    if (masked(x) || !(t > -70.f)) return {0u, 64};
-    const float tl = fmaf(d, c.hi, -t) + fmaf(d, c.lo, dl * c.hi);
-    const float kf = rintf(t * 32.f);
-    const int k = (int)kf;
-    const float f = fmaf(kf, -1.f / 32.f, t);
+__constant__ uint32_t kRoots[32] = {   // 2^(31 + j / 32), to the nearest
+    2147483648u, 2194507417u, 2242560872u, 2291666561u, 2341847524u, 2393127307u, 2445529972u, 2499080105u,
+    2553802834u, 2609723834u, 2666869345u, 2725266179u, 2784941738u, 2845924021u, 2908241642u, 2971923842u,
+    3037000500u, 3103502151u, 3171459999u, 3240905930u, 3311872529u, 3384393094u, 3458501653u, 3534232978u,
+    3611622603u, 3690706840u, 3771522796u, 3854108391u, 3938502376u, 4024744348u, 4112874773u, 4202935003u};
+// Two of them at once, in packed f32 arithmetic (half the instructions), with -most of each. Whole numbers come from f32
+// sums with 1.5 2^23, whose last place is 1: conversions are a quarter as fast. Where the result is 0 what is made on the
+// way means nothing. ROUNDED: a difference of logits may not fit f32 (of bf16 ones it does wherever it counts: exponents less
+// than 2^15 apart), so what is left of it is carried along.
+template <bool ROUNDED>
+__device__ __forceinline__ void exact_exp2(float x0, float x1, F2 less, const Scale c, const uint32_t *roots, Exact &e0, Exact &e1) {
+    constexpr float kWhole = 12582912.f;
+    constexpr int kWholeBits = 0x4b400000;
     constexpr float kLn2 = 0.693147182464599609375f, kLn2Lo = -1.904654299957768e-09f;   // log 2 in two floats
-    const float y = f * kLn2, yl = fmaf(f, kLn2, -y) + fmaf(f, kLn2Lo, tl * kLn2);
-    const float q = y * y * fmaf(y, fmaf(y, 1.f / 24.f, 1.f / 6.f), 0.5f) + yl;
-    const int rise = __float2int_rn(y * 0x1p32f) + __float2int_rn(q * 0x1p32f);   // (e^y - 1) 2^32
-    const uint32_t r = roots[k & 31];
-    return {r + (uint32_t)(((long long)r * rise) >> 32), -(k >> 5)};
+    const F2 minus = f2(-1.f, -1.f), hi = f2(c.hi, c.hi), ln2 = f2(kLn2, kLn2), whole = f2(kWhole, kWhole), up = f2(65536.f, 65536.f);
+    const F2 x = f2(x0, x1), d = x + less, t = d * hi;
+    F2 tl = fma2(d, f2(c.lo, c.lo), fma2(d, hi, t * minus));
+    if (ROUNDED) {
+        const F2 b = fma2(x, minus, d), dl = (x + fma2(d, minus, b)) + fma2(b, minus, less);   // x - most = d + dl, exactly
+        tl = fma2(dl, hi, tl);
+    }
+    const F2 k = fma2(t, f2(32.f, 32.f), whole), f0 = fma2(fma2(whole, minus, k), f2(-1.f / 32.f, -1.f / 32.f), t);
+    const F2 f = f0 + tl, fl = fma2(fma2(f0, minus, f), minus, tl);
+    const F2 y = f * ln2, yl = fma2(f, f2(kLn2Lo, kLn2Lo), fma2(fl, ln2, fma2(f, ln2, y * minus)));
+    const F2 q = fma2(y * y, fma2(y, fma2(y, f2(1.f / 24.f, 1.f / 24.f), f2(1.f / 6.f, 1.f / 6.f)), f2(0.5f, 0.5f)), yl);
+    // (e^y - 1) 2^32 = (y + q) 2^32: y 2^16 as a whole number and what is left of it
+    const F2 y16 = fma2(y, up, whole), left = fma2(y, up, fma2(y16, minus, whole));
+    const F2 rest = fma2(q, f2(0x1p32f, 0x1p32f), fma2(left, up, whole));
+    auto make = [&](float t, float k, float y16, float rest) -> Exact {
+        const int kk = __float_as_int(k) - kWholeBits;
+        const int rise = (__float_as_int(y16) - kWholeBits) * 65536 + (__float_as_int(rest) - kWholeBits);
+        const uint32_t r = roots[kk & 31];
+        return {r + (uint32_t)__mulhi((int)(r >> 1), rise) * 2u, t > -70.f ? -(kk >> 5) : 256};
+    };
+    e0 = make(f2_lo(t), f2_lo(k), f2_lo(y16), f2_lo(rest));
+    e1 = make(f2_hi(t), f2_hi(k), f2_hi(y16), f2_hi(rest));
 }
 
 __device__ __forceinline__ unsigned long long warp_sum64(unsigned long long v) {
@@ -209,12 +243,12 @@ __device__ __forceinline__ unsigned long long warp_sum64(unsigned long long v) {
 
 // The rows' parts, a warp each, for calls that a sequence's cluster would read too slowly.
 template <typename T>
-__global__ void __launch_bounds__(kRowWarps * 32) k_draft_rows(const Args a) {
-    const int seq = blockIdx.y, t = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(kWarps * 32) k_draft_rows(const Args a) {
+    const int seq = blockIdx.y, t = blockIdx.x * kWarps + (threadIdx.x >> 5);
     const Sequence q = sequence(a, seq);
     if (t < q.rows() * a.parts) {
         const int r = t / a.parts;
-        const Seen s = see_part(row_at<T>(a, q, seq, r), a.vocab, t - r * a.parts, a.parts, (float)kLog2e / q.temperature, q.greedy);
+        const Seen s = see_part(row_at<T>(a, q, seq, r), a.vocab, t - r * a.parts, a.parts, scale_of(q.temperature).hi, q.greedy);
         if ((threadIdx.x & 31) == 0) a.seen[(size_t)seq * (2 * a.n_draft + 1) * a.parts + t] = s;
     }
     pdl_launch_dependents();
@@ -222,6 +256,10 @@ __global__ void __launch_bounds__(kRowWarps * 32) k_draft_rows(const Args a) {
 
 enum Verdict : int { kTake = 0, kRefuse = 1, kUnsure = 2 };
 
+struct Plan {            // of the row that is looked at: the first draft that is not surely taken, or the row after them
+    int n, verdict;
+    float p_most, q_most;   // the largest logits; kLeastRef: no distribution
+};
 struct Shared {
     uint32_t roots[32];                        // 2^(31 + j / 32)
     Seen parts[kOwnParts];                     // of CTA 0
@@ -229,40 +267,65 @@ struct Shared {
     int verdict[kMaxDraft];
     unsigned long long warp[kWarps][2];
     unsigned long long cta[kCluster][2];       // every CTA's sums
-    int row;                                   // the row that is looked at; decided: drawn from
+    Plan plan;
 };
 
-// A row of probabilities: p = m factor >> (down + shift), in units of 2^-62, of an Exact.
+// A row of probabilities: p = (m factor >> 32) 2^32 >> (down + shift), in units of 2^-62, of an Exact.
 struct Row {
     float most;
-    uint32_t factor;   // 0: no distribution
+    uint32_t factor;        // 0: no distribution
     int down;
-    double z;          // the sum of e^((x - most) / T)
+    unsigned long long z;   // the sum of e^((x - most) / T), in units of 2^-(31 + lift); 0: not made
+    __device__ __forceinline__ bool alive() const { return most > kLeastRef; }
 };
+// 2^95 / z for z in [2^63, 2^64), in [2^31, 2^32), to about 2^-31 of itself: an f32 reciprocal and one step of Newton's
+// method on the upper 32 bits. (f64 divisions by all threads of a CTA would take 3 us.)
+__device__ __forceinline__ uint32_t reciprocal(unsigned long long z) {
+    const uint32_t top = (uint32_t)(z >> 32);
+    const uint32_t r = (uint32_t)fminf(0x1p63f / (float)top, 4294967040.f);
+    const long long left = (long long)((1ull << 63) - (unsigned long long)r * top);   // 2^63 times what is missing of r, relative
+    const long long better = (long long)r + (((long long)r * (left >> 31)) >> 32);
+    return (uint32_t)min(better, 0xffffffffll);
+}
 
 // A cluster per sequence. Its first CTA decides by f32 sums which drafts are surely taken and which first one is
 // not; that one's rows, and those that the next token is drawn from, are gone over by all CTAs, each a range of the vocabulary, with
-// exponentials of 31 bits and sums in whole numbers: which token a uniform number meets is a question of sums of
+// exponentials of 30 bits and sums in whole numbers: which token a uniform number meets is a question of sums of
 // 10^5 terms next to one another, where f32 would err once in some hundred draws.
 template <typename T, bool OWN>
-__global__ void __launch_bounds__(kThreads, 1) k_draft_choose(const Args a) {
+__global__ void __launch_bounds__(kThreads, 3) k_draft_choose(const Args a) {
     __shared__ Shared s;
     cg::cluster_group cluster = cg::this_cluster();
-    const int ctas = cluster.num_blocks(), rank = cluster.block_rank(), seq = blockIdx.x / ctas;
+    const int ctas = a.ctas, rank = cluster.block_rank(), seq = blockIdx.x / ctas;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int K = a.n_draft, V = a.vocab;
+    auto arrived = cluster.barrier_arrive();
     const Sequence sq = sequence(a, seq);
     const int count = sq.count, n_rows = sq.rows();
     const bool greedy = sq.greedy, drafted = sq.drafted;
-    const double temperature = sq.temperature;
+    const float temperature = sq.temperature;
     const Scale c = greedy ? Scale{1.f, 0.f} : scale_of(sq.temperature);
     const float *u = a.uniforms + (size_t)seq * (K + 1);
     const int32_t *tokens = a.tokens + (size_t)seq * K;
-    Shared *lead = cluster.map_shared_rank(&s, 0);
-    if (tid < 32) s.roots[tid] = (uint32_t)llrint(exp2(31.0 + tid / 32.0));
-    cluster.sync();   // every CTA's shared memory is there
+    if (tid < 32) s.roots[tid] = kRoots[tid];
+    // CTA 0: a thread per draft
+    int x = -1;
+    float x_target = -INFINITY, x_draft = -INFINITY, x_u = 0.f;
+    if (rank == 0 && tid < count) {
+        x = tokens[tid];
+        x_u = fminf(fmaxf(u[tid], 0.f), 1.f);
+        if (x >= 0 && x < V) {
+            x_target = load_logit(row_at<T>(a, sq, seq, tid), x);
+            if (drafted) x_draft = load_logit(row_at<T>(a, sq, seq, sq.targets() + tid), x);
+        } else {
+            x = -1;
+        }
+    }
+    const float u_draw = fminf(fmaxf(u[K], 0.f), 1.f);
+    cluster.barrier_wait(std::move(arrived));   // every CTA's shared memory is there
 
     if (OWN) {
+        Shared *lead = cluster.map_shared_rank(&s, 0);
         for (int t = rank * kWarps + warp; t < n_rows * a.parts; t += ctas * kWarps) {
             const int r = t / a.parts;
             const Seen seen = see_part(row_at<T>(a, sq, seq, r), V, t - r * a.parts, a.parts, c.hi, greedy);
@@ -280,150 +343,161 @@ __global__ void __launch_bounds__(kThreads, 1) k_draft_choose(const Args a) {
             if (lane == 0) s.rows[r] = seen;
         }
         __syncthreads();
-        for (int i = tid; i < count; i += kThreads) {
-            const int x = tokens[i];
+        if (tid < count) {
+            const Seen p = s.rows[tid];
             int v = kRefuse;
-            const Seen p = s.rows[i];
-            if (x >= 0 && x < V && p.alive()) {
-                const float logit = load_logit(row_at<T>(a, sq, seq, i), x);
-                if (greedy) {
-                    v = x == p.first ? kTake : kRefuse;
-                } else if (!masked(logit)) {
-                    const float px = ex2((logit - p.most) * c.hi) / p.sum;
-                    float qx = 1.f;
-                    if (drafted) {
-                        const Seen q = s.rows[sq.targets() + i];
-                        const float other = load_logit(row_at<T>(a, sq, seq, sq.targets() + i), x);
-                        qx = masked(other) || !q.alive() ? 0.f : ex2((other - q.most) * c.hi) / q.sum;
-                    }
-                    const float need = fminf(fmaxf(u[i], 0.f), 1.f) * qx;
-                    // (an exponential that f32 cannot tell from 0 decides nothing)
-                    v = px > 1e-30f && need < px * (1.f - kNear) ? kTake : need > px * (1.f + kNear) && need > 1e-30f ? kRefuse : kUnsure;
+            if (greedy) {
+                v = p.alive() && x == p.first ? kTake : kRefuse;
+            } else if (p.alive() && !masked(x_target)) {
+                const float px = ex2((x_target - p.most) * c.hi) / p.sum;
+                float qx = 1.f;
+                if (drafted) {
+                    const Seen q = s.rows[sq.targets() + tid];
+                    qx = masked(x_draft) || !q.alive() ? 0.f : ex2((x_draft - q.most) * c.hi) / q.sum;
                 }
+                const float need = x_u * qx;
+                // (an exponential that f32 cannot tell from 0 decides nothing)
+                v = px > 1e-30f && need < px * (1.f - kNear) ? kTake : need > px * (1.f + kNear) && need > 1e-30f ? kRefuse : kUnsure;
             }
-            s.verdict[i] = v;
+            s.verdict[tid] = v;
         }
         __syncthreads();
     }
 
-    int n = 0;
+    int n = 0, verdict;
+    bool spent = false;   // s.cta may still be read
     Row p{}, q{};
     const int bits = 32 - __clz(max(V - 1, 1)), lift = 32 - bits;   // a sum of V numbers below 2^(32 + lift) fits 64 bits
     // this CTA's range, and its warps'
-    const int from = (int)((long long)V * rank / ctas), to = (int)((long long)V * (rank + 1) / ctas);
-    const int each = (to - from + kWarps - 1) / kWarps;
+    const int slice = (V + ctas - 1) / ctas, from = min(rank * slice, V), to = min(from + slice, V);
+    const int each = (slice + kWarps - 1) / kWarps;
     const int w0 = min(from + warp * each, to), w1 = min(w0 + each, to);
     const T *rp = nullptr, *rq = nullptr;
-    // a value from each CTA's sums over its warps to all CTAs
+    // CTA 0's first warp: the first draft from n on that is not surely taken, to all CTAs
+    auto tell = [&]() {
+        if (rank != 0 || warp != 0) return;
+        int first = n;
+        while (first < count) {
+            const uint32_t other = __ballot_sync(0xffffffffu, first + lane >= count || s.verdict[first + lane] != kTake);
+            if (other != 0) {
+                first += __ffs(other) - 1;
+                break;
+            }
+            first += 32;
+        }
+        first = min(first, count);
+        const bool has_q = drafted && first < count;
+        Plan plan{first, first < count ? s.verdict[first] : kRefuse, kLeastRef, kLeastRef};
+        if (s.rows[first].alive()) plan.p_most = s.rows[first].most;
+        if (has_q && s.rows[sq.targets() + first].alive()) plan.q_most = s.rows[sq.targets() + first].most;
+        if (lane < ctas) cluster.map_shared_rank(&s, lane)->plan = plan;
+    };
+    // a value or two of each thread, summed over every CTA, to all CTAs
     auto spread = [&](unsigned long long v0, unsigned long long v1) {
         v0 = warp_sum64(v0), v1 = warp_sum64(v1);
         if (lane == 0) s.warp[warp][0] = v0, s.warp[warp][1] = v1;
         __syncthreads();
         if (tid < 2 * ctas) {
             unsigned long long v = 0;
+#pragma unroll
             for (int w = 0; w < kWarps; ++w) v += s.warp[w][tid & 1];
             cluster.map_shared_rank(&s, tid >> 1)->cta[rank][tid & 1] = v;
         }
         cluster.sync();
     };
-    auto whole = [&](float x, float most) -> unsigned long long {   // e^((x - most) / T) in units of 2^-(31 + lift)
-        const Exact e = exact_exp(x, most, c, s.roots);
-        return e.shift < 64 ? (((unsigned long long)e.m << lift) + (1ull << e.shift >> 1)) >> e.shift : 0;
+    constexpr bool kRounded = sizeof(T) == 4;
+    // f(exponential of token i of p, i), or f(p's, q's), for the warp's range: loads ahead of what is made of them
+    auto over_one = [&](auto f) {
+        const F2 less = f2(-p.most, -p.most);
+        for (int i = w0 + lane; i < w1; i += 32 * 8) {
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = i + 32 * j < w1 ? load_logit(rp, i + 32 * j) : -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                Exact e, g;
+                exact_exp2<kRounded>(x[j], x[j + 1], less, c, s.roots, e, g);
+                f(e, i + 32 * j);
+                f(g, i + 32 * j + 32);
+            }
+        }
+    };
+    auto over_both = [&](auto f) {
+        const F2 less = f2(-p.most, -q.most);
+        for (int i = w0 + lane; i < w1; i += 32 * 4) {
+            float x[4], y[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[j] = i + 32 * j < w1 ? load_logit(rp, i + 32 * j) : -INFINITY;
+                y[j] = i + 32 * j < w1 ? load_logit(rq, i + 32 * j) : -INFINITY;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                Exact e, g;
+                exact_exp2<kRounded>(x[j], y[j], less, c, s.roots, e, g);
+                f(e, g);
+            }
+        }
     };
     while (true) {
-        if (rank == 0 && tid == 0) {
-            while (n < count && s.verdict[n] == kTake) ++n;
-            s.row = n;
-        }
+        tell();
         cluster.sync();
-        n = lead->row;
-        const int verdict = n < count ? lead->verdict[n] : kRefuse;   // (read before CTA 0 may change it below)
+        const Plan plan = s.plan;
+        n = plan.n, verdict = plan.verdict;
         if (greedy) break;
-        const Seen ps = lead->rows[n], qs = drafted && n < count ? lead->rows[sq.targets() + n] : Seen{kLeastRef, 0.f, 0};
-        p.most = ps.most, q.most = qs.most;
+        p = Row{plan.p_most, 0, 0, 0}, q = Row{plan.q_most, 0, 0, 0};
         rp = row_at<T>(a, sq, seq, n);
         rq = drafted && n < count ? row_at<T>(a, sq, seq, sq.targets() + n) : nullptr;
-        p.factor = q.factor = 0;
-        p.z = 0.0;
         if (rq == nullptr && verdict == kRefuse) break;   // (drawn from p alone: its sum is the draw's)
         unsigned long long sums[2] = {0, 0};
-        if (ps.alive() && qs.alive()) {
-#pragma unroll 4
-            for (int i = w0 + lane; i < w1; i += 32) {
-                const float x = load_logit(rp, i), y = load_logit(rq, i);
-                sums[0] += whole(x, p.most);
-                sums[1] += whole(y, q.most);
-            }
-        } else if (ps.alive()) {
-#pragma unroll 4
-            for (int i = w0 + lane; i < w1; i += 32) sums[0] += whole(load_logit(rp, i), p.most);
-        }
+        if (p.alive() && q.alive())
+            over_both([&](Exact e, Exact g) { sums[0] += place(e.m, bits + e.shift), sums[1] += place(g.m, bits + g.shift); });
+        else if (p.alive())
+            over_one([&](Exact e, int) { sums[0] += place(e.m, bits + e.shift); });
         spread(sums[0], sums[1]);
+        spent = true;
         for (int w = 0; w < 2; ++w) {
             unsigned long long z = 0;
             for (int i = 0; i < ctas; ++i) z += s.cta[i][w];
             if (z == 0) continue;
             Row &r = w ? q : p;
             const int zeros = __clzll(z);
-            // 2^95 / (z 2^zeros), in (2^31, 2^32]
-            r.factor = (uint32_t)fmin(0x1p95 / (double)(z << zeros), 4294967295.0);
+            r.factor = reciprocal(z << zeros);
             r.down = 33 - lift - zeros;
-            r.z = (double)z * exp2(-(double)(31 + lift));
+            r.z = z;
         }
         if (verdict == kRefuse) break;
-        if (rank == 0 && tid == 0) {   // an unsure draft
-            const int x = tokens[n];
-            auto of = [&](const T *row, const Row &r) {   // (of values that the draw takes for 0 too)
-                const float logit = load_logit(row, x);
-                return r.factor && !masked(logit) ? exp(((double)logit - (double)r.most) / temperature) / r.z : 0.0;
+        if (rank == 0 && tid == n) {   // an unsure draft
+            auto of = [&](float logit, const Row &r) {   // (of values that the draw takes for 0 too)
+                return r.factor && !masked(logit) ? exp(((double)logit - (double)r.most) / (double)temperature) / ((double)r.z * exp2(-31.0 - lift)) : 0.0;
             };
-            const double px = of(rp, p), qx = rq != nullptr ? of(rq, q) : 1.0;
-            s.verdict[n] = (double)fminf(fmaxf(u[n], 0.f), 1.f) * qx < px ? kTake : kRefuse;
+            s.verdict[n] = (double)x_u * (rq != nullptr ? of(x_draft, q) : 1.0) < of(x_target, p) ? kTake : kRefuse;
         }
-        cluster.sync();
-        if (lead->verdict[n] == kRefuse) break;
+        cluster.sync();   // (s.cta and s.plan are free again)
+        spent = false;
+        // a draft that is refused after all: its rows' sums are made once more by the next turn
     }
 
-    const size_t out = (size_t)seq * (K + 1);
-    if (rank == 0) {   // the drafts that are taken
-        for (int i = tid; i <= K; i += kThreads) {
-            int token = i < n ? tokens[i] : -1;
-            if (greedy && i == n && s.rows[n].alive()) token = s.rows[n].first;
-            a.tokens_out[out + i] = token;
-            if (a.logprobs) {
-                float lp = 0.f;
-                if (i < n && !greedy)
-                    lp = (float)(((double)load_logit(row_at<T>(a, sq, seq, i), token) - (double)s.rows[i].most) / temperature - log((double)s.rows[i].sum));
-                a.logprobs[out + i] = lp;
-            }
-        }
-        if (tid == 0) a.accepted[seq] = n;
-    }
     // the draw
+    const size_t out = (size_t)seq * (K + 1);
     const bool minus_q = rq != nullptr && q.factor != 0;
     const int gone = n < count && a.draft == nullptr ? tokens[n] : -1;   // (without draft logits all of q is on the draft)
-    auto weight = [&](float x, float y, int i, bool plain) -> unsigned long long {
-        if (!minus_q) return i == gone && !plain ? 0 : whole(x, p.most);
-        const Exact e = exact_exp(x, p.most, c, s.roots), g = exact_exp(y, q.most, c, s.roots);
-        const int es = p.down + e.shift, gs = q.down + g.shift;
-        const unsigned long long w = e.shift < 64 && es < 64 ? (unsigned long long)e.m * p.factor >> es : 0;
-        const unsigned long long v = g.shift < 64 && gs < 64 && !plain ? (unsigned long long)g.m * q.factor >> gs : 0;
+    auto weight = [&](Exact e, int i, bool plain) { return i == gone && !plain ? 0 : place(e.m, bits + e.shift); };
+    auto left = [&](Exact e, Exact g, bool plain) {   // of p without q, in units of 2^-62
+        const unsigned long long w = place(__umulhi(e.m, p.factor), p.down + e.shift);
+        const unsigned long long v = plain ? 0 : place(__umulhi(g.m, q.factor), q.down + g.shift);
         return w > v ? w - v : 0;
     };
     bool plain = n == count;
     unsigned long long total = 0, before = 0;
-    while (!greedy && lead->rows[n].alive()) {
-        cluster.sync();   // (s.cta is free again)
+    while (!greedy && p.alive()) {
+        if (spent) cluster.sync();   // (s.cta is free again)
+        spent = true;
         unsigned long long sum = 0;
-        if (minus_q) {
-#pragma unroll 4
-            for (int i = w0 + lane; i < w1; i += 32) sum += weight(load_logit(rp, i), load_logit(rq, i), i, plain);
-        } else {
-#pragma unroll 4
-            for (int i = w0 + lane; i < w1; i += 32) sum += weight(load_logit(rp, i), 0.f, i, plain);
-        }
+        if (minus_q) over_both([&](Exact e, Exact g) { sum += left(e, g, plain); });
+        else over_one([&](Exact e, int i) { sum += weight(e, i, plain); });
         spread(sum, 0);
-        total = before = 0;
+        before = 0;
         for (int i = 0; i < ctas; ++i) {
             if (i < rank) before += s.cta[i][0];
             total += s.cta[i][0];
@@ -432,8 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_draft_choose(const Args a) {
         plain = true;
     }
     if (total != 0) {
-        const float un = fminf(fmaxf(u[K], 0.f), 1.f);
-        const unsigned long long un64 = un >= 1.f ? ~0ull : (unsigned long long)(un * 0x1p64f);
+        const unsigned long long un64 = u_draw >= 1.f ? ~0ull : (unsigned long long)(u_draw * 0x1p64f);
         const unsigned long long border = __umul64hi(un64, total);   // the first token whose sum is above it
         if (border >= before && border - before < s.cta[rank][0]) {
             // its warp's tokens, then a thread's, then itself
@@ -441,7 +514,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_draft_choose(const Args a) {
             while (border - before >= s.warp[w][0]) before += s.warp[w++][0];
             const int b0 = min(from + w * each, to), b1 = min(b0 + each, to), own = (b1 - b0 + kThreads - 1) / kThreads;
             const int i0 = min(b0 + tid * own, b1), i1 = min(i0 + own, b1);
-            auto at_token = [&](int i) { return weight(load_logit(rp, i), minus_q ? load_logit(rq, i) : 0.f, i, plain); };
+            auto at_token = [&](int i) {
+                Exact e, g;
+                exact_exp2<kRounded>(load_logit(rp, i), minus_q ? load_logit(rq, i) : 0.f, f2(-p.most, -q.most), c, s.roots, e, g);
+                return minus_q ? left(e, g, plain) : weight(e, i, plain);
+            };
             unsigned long long sum = 0;
             for (int i = i0; i < i1; ++i) sum += at_token(i);
             unsigned long long up = sum;
@@ -459,36 +536,76 @@ __global__ void __launch_bounds__(kThreads, 1) k_draft_choose(const Args a) {
                 for (unsigned long long v; border - at >= (v = at_token(i)); ++i) at += v;
                 a.tokens_out[out + n] = i;
                 if (a.logprobs) {
-                    double z = p.z;
-                    if (z == 0.0) {   // (no sum of p alone was made: it is the draw's, and the token's that was left out)
-                        const unsigned long long left = gone >= 0 && gone < V && !plain ? whole(load_logit(rp, gone), p.most) : 0;
-                        z = (double)(total + left) * exp2(-(double)(31 + lift));
+                    unsigned long long z = p.z;
+                    if (z == 0) {   // (no sum of p alone was made: it is the draw's, and the token's that was left out)
+                        z = total;
+                        if (gone >= 0 && gone < V && !plain) {
+                            Exact e, g;
+                            exact_exp2<kRounded>(load_logit(rp, gone), 0.f, f2(-p.most, 0.f), c, s.roots, e, g);
+                            z += place(e.m, bits + e.shift);
+                        }
                     }
-                    a.logprobs[out + n] = (float)(((double)load_logit(rp, i) - (double)p.most) / temperature - log(z));
+                    a.logprobs[out + n] = (load_logit(rp, i) - p.most) / temperature - logf((float)z * exp2f(-(float)(31 + lift)));
                 }
             }
         }
     }
-    cluster.sync();   // (nobody leaves while others read its shared memory)
+    if (rank != 0) return;
+    // the rest of the results
+    for (int i = tid; i <= K; i += kThreads) {
+        int token = -1;
+        if (i < n) token = tokens[i];
+        else if (i == n && greedy && s.rows[n].alive()) token = s.rows[n].first;
+        else if (i == n && total != 0) continue;
+        a.tokens_out[out + i] = token;
+        if (a.logprobs) {
+            float lp = 0.f;
+            if (i < n && !greedy) lp = (load_logit(row_at<T>(a, sq, seq, i), token) - s.rows[i].most) / temperature - logf(s.rows[i].sum);
+            a.logprobs[out + i] = lp;
+        }
+    }
+    if (tid == 0) a.accepted[seq] = n;
 }
 
 bool sizes_ok(int n_seq, int n_draft, int vocab) {
     return n_seq >= 0 && n_seq <= 65535 && n_draft >= 0 && n_draft <= kMaxDraft && vocab >= 1 && vocab <= 1 << 26;
 }
 
-// A sequence's own cluster reads its rows while they are few logits; else the whole GPU does, in a launch before.
+
+// How a call runs. A sequence's own cluster reads its rows while they are few logits; else the whole GPU does, in a launch before.
 constexpr int kOwnLogits = 65536;
 struct Shape {
     bool own;
-    int parts;
+    int parts, ctas;
 };
 Shape shape_of(int n_seq, int n_draft, int vocab) {
     const int rows = 2 * n_draft + 1;
     Shape p;
     p.own = (long long)rows * vocab <= kOwnLogits;
-    const long long warps = p.own ? kCluster * kWarps : std::max(1ll, 152ll * 32 / std::max(1, n_seq));   // for a sequence
+    p.ctas = 1;
+    const int most = (long long)n_seq * kCluster <= 152 * 3 ? kCluster : kCluster / 2;
+    while (p.ctas < most && (p.own ? (long long)rows * vocab : vocab) > p.ctas * 1024ll) p.ctas *= 2;
+    const long long warps = p.own ? p.ctas * kWarps : std::max(1ll, 152ll * 32 / std::max(1, n_seq));   // for a sequence
     p.parts = (int)std::max(1ll, std::min<long long>(std::min(kMaxParts, vocab / 256), warps / rows));
     return p;
+}
+
+// Clusters of 16 are allowed once for each device.
+template <typename T, bool OWN>
+cudaError_t allow() {
+    return cudaFuncSetAttribute(k_draft_choose<T, OWN>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+}
+cudaError_t allow_clusters() {
+    static std::atomic<unsigned long long> done{0};
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    const unsigned long long bit = device < 64 ? 1ull << device : 0;
+    if (e != cudaSuccess || (done.load() & bit)) return e;
+    if ((e = allow<float, true>()) != cudaSuccess || (e = allow<float, false>()) != cudaSuccess ||
+        (e = allow<__nv_bfloat16, true>()) != cudaSuccess || (e = allow<__nv_bfloat16, false>()) != cudaSuccess)
+        return e;
+    done |= bit;
+    return cudaSuccess;
 }
 
 }  // namespace
@@ -515,25 +632,29 @@ talker_status talker_draft_verify(const void *target, int64_t target_seq, int64_
     if (need > 0 && (!scratch || scratch_bytes < need || reinterpret_cast<uintptr_t>(scratch) % 16)) return TALKER_EINVAL;
     const Shape p = shape_of(n_seq, n_draft, vocab);
     const Args a{target, draft, target_seq, target_row, draft_seq, draft_row, tokens, counts, uniforms, temperatures, n_draft, vocab,
-                 tokens_out, accepted, logprobs, p.parts, static_cast<Seen *>(scratch)};
+                 tokens_out, accepted, logprobs, p.parts, p.ctas, static_cast<Seen *>(scratch)};
     const bool f32 = dtype == TALKER_DTYPE_F32;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     cfg.blockDim = dim3(kThreads);
-    cfg.gridDim = dim3((unsigned)(n_seq * kCluster));
+    cfg.gridDim = dim3((unsigned)(n_seq * p.ctas));
     cfg.stream = static_cast<cudaStream_t>(cuda_stream);
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kCluster;
+    attr[0].val.clusterDim.x = p.ctas;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.own ? 1 : 2;
-    cudaError_t e = cudaSuccess;
+    cudaError_t e = allow_clusters();
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return TALKER_ECUDA;
+    }
     if (!p.own) {
-        const dim3 grid((unsigned)(((2 * n_draft + 1) * p.parts + kRowWarps - 1) / kRowWarps), (unsigned)n_seq);
-        if (f32) k_draft_rows<float><<<grid, kRowWarps * 32, 0, cfg.stream>>>(a);
-        else k_draft_rows<__nv_bfloat16><<<grid, kRowWarps * 32, 0, cfg.stream>>>(a);
+        const dim3 grid((unsigned)(((2 * n_draft + 1) * p.parts + kWarps - 1) / kWarps), (unsigned)n_seq);
+        if (f32) k_draft_rows<float><<<grid, kWarps * 32, 0, cfg.stream>>>(a);
+        else k_draft_rows<__nv_bfloat16><<<grid, kWarps * 32, 0, cfg.stream>>>(a);
         e = cudaGetLastError();
         if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, f32 ? k_draft_choose<float, false> : k_draft_choose<__nv_bfloat16, false>, a);
     } else {
