@@ -37,6 +37,7 @@ struct Args {
     float *logprobs;
     int parts;              // of a row
     int ctas;               // of a sequence's cluster
+    int staged;             // bytes of shared memory for a range of one row, 0: ranges are read where they are
     struct Seen *seen;      // scratch: [sequence][row][part]
 };
 
@@ -173,8 +174,8 @@ __device__ Seen see_part(const T *row, int vocab, int part, int parts, float c, 
     return warp_join(s, c);
 }
 
-// e^((x - most) / T) = m 2^(-31 - shift), m in [2^31, 2^32), for x <= most, to about 2^-30 of itself. With
-// t = (x - most) log2 e / T in two floats, t = k / 32 + f, |f| <= 1/64: m = 2^31 2^(k % 32 / 32) e^y, y = f log 2, by the
+// e^((x - most) / T) = m 2^(-30 - shift), m in [2^30, 2^31), for x <= most, to about 2^-30 of itself. With
+// t = (x - most) log2 e / T in two floats, t = k / 32 + f, |f| <= 1/64: m = 2^30 2^(k % 32 / 32) e^y, y = f log 2, by the
 // series of e^y - 1, whose terms after y^4 / 24 are below 2^-39. Below 2^-70, and of masked logits: 0, by a shift that
 // leaves nothing.
 struct Exact {
@@ -209,30 +210,31 @@ __constant__ uint32_t kRoots[32] = {   // 2^(31 + j / 32), to the nearest
 template <bool ROUNDED>
 __device__ __forceinline__ void exact_exp2(float x0, float x1, F2 less, const Scale c, const uint32_t *roots, Exact &e0, Exact &e1) {
     constexpr float kWhole = 12582912.f;
-    constexpr int kWholeBits = 0x4b400000;
+    constexpr uint32_t kWholeBits = 0x4b400000u;
     constexpr float kLn2 = 0.693147182464599609375f, kLn2Lo = -1.904654299957768e-09f;   // log 2 in two floats
-    const F2 minus = f2(-1.f, -1.f), hi = f2(c.hi, c.hi), ln2 = f2(kLn2, kLn2), whole = f2(kWhole, kWhole), up = f2(65536.f, 65536.f);
+    // (what is named n... is the negative, so that no sign has to be changed)
+    const F2 minus = f2(-1.f, -1.f), hi = f2(c.hi, c.hi), nhi = f2(-c.hi, -c.hi), nlo = f2(-c.lo, -c.lo);
+    const F2 ln2 = f2(kLn2, kLn2), nln2 = f2(-kLn2, -kLn2), whole = f2(kWhole, kWhole), nwhole = f2(-kWhole, -kWhole);
     const F2 x = f2(x0, x1), d = x + less, t = d * hi;
-    F2 tl = fma2(d, f2(c.lo, c.lo), fma2(d, hi, t * minus));
+    F2 nt = fma2(d, nlo, fma2(d, nhi, t));
     if (ROUNDED) {
-        const F2 b = fma2(x, minus, d), dl = (x + fma2(d, minus, b)) + fma2(b, minus, less);   // x - most = d + dl, exactly
-        tl = fma2(dl, hi, tl);
+        const F2 b = fma2(d, minus, x), dl = fma2(d + b, minus, x) + (b + less);   // x - most = d + dl, exactly
+        nt = fma2(dl, nhi, nt);
     }
-    const F2 k = fma2(t, f2(32.f, 32.f), whole), f0 = fma2(fma2(whole, minus, k), f2(-1.f / 32.f, -1.f / 32.f), t);
-    const F2 f = f0 + tl, fl = fma2(fma2(f0, minus, f), minus, tl);
-    const F2 y = f * ln2, yl = fma2(f, f2(kLn2Lo, kLn2Lo), fma2(fl, ln2, fma2(f, ln2, y * minus)));
-    const F2 q = fma2(y * y, fma2(y, fma2(y, f2(1.f / 24.f, 1.f / 24.f), f2(1.f / 6.f, 1.f / 6.f)), f2(0.5f, 0.5f)), yl);
-    // (e^y - 1) 2^32 = (y + q) 2^32: y 2^16 as a whole number and what is left of it
-    const F2 y16 = fma2(y, up, whole), left = fma2(y, up, fma2(y16, minus, whole));
-    const F2 rest = fma2(q, f2(0x1p32f, 0x1p32f), fma2(left, up, whole));
-    auto make = [&](float t, float k, float y16, float rest) -> Exact {
-        const int kk = __float_as_int(k) - kWholeBits;
-        const int rise = (__float_as_int(y16) - kWholeBits) * 65536 + (__float_as_int(rest) - kWholeBits);
-        const uint32_t r = roots[kk & 31];
-        return {r + (uint32_t)__mulhi((int)(r >> 1), rise) * 2u, t > -70.f ? -(kk >> 5) : 256};
+    const F2 k = fma2(t, f2(32.f, 32.f), whole), f0 = fma2(k + nwhole, f2(-1.f / 32.f, -1.f / 32.f), t);
+    const F2 f = fma2(nt, minus, f0), nf = nt + fma2(f0, minus, f);
+    const F2 y = f * ln2, ny = fma2(f, f2(-kLn2Lo, -kLn2Lo), fma2(nf, ln2, fma2(f, nln2, y)));
+    const F2 q = (y * y) * fma2(y, fma2(y, f2(1.f / 24.f, 1.f / 24.f), f2(1.f / 6.f, 1.f / 6.f)), f2(0.5f, 0.5f));
+    // (e^y - 1) 2^31 = (y + q - ny) 2^31: y 2^15 as a whole number, what is left of it, and the rest
+    const F2 y15 = fma2(y, f2(32768.f, 32768.f), whole), over = fma2(y, f2(-32768.f, -32768.f), y15 + nwhole);
+    const F2 rest = fma2(ny, f2(-0x1p31f, -0x1p31f), fma2(q, f2(0x1p31f, 0x1p31f), fma2(over, f2(-65536.f, -65536.f), whole)));
+    auto make = [&](float t, float k, float y15, float rest) -> Exact {
+        constexpr uint32_t kOne = 0x80000000u - kWholeBits * 65536u - kWholeBits;   // 2^31 less the two sums' own bits
+        const uint32_t e = __float_as_uint(y15) * 65536u + __float_as_uint(rest) + kOne, bits = __float_as_uint(k);   // 2^31 e^y
+        return {__umulhi(roots[bits & 31], e), t > -70.f ? (int)((kWholeBits >> 5) - (bits >> 5)) : 256};
     };
-    e0 = make(f2_lo(t), f2_lo(k), f2_lo(y16), f2_lo(rest));
-    e1 = make(f2_hi(t), f2_hi(k), f2_hi(y16), f2_hi(rest));
+    e0 = make(f2_lo(t), f2_lo(k), f2_lo(y15), f2_lo(rest));
+    e1 = make(f2_hi(t), f2_hi(k), f2_hi(y15), f2_hi(rest));
 }
 
 __device__ __forceinline__ unsigned long long warp_sum64(unsigned long long v) {
@@ -256,18 +258,13 @@ __global__ void __launch_bounds__(kWarps * 32) k_draft_rows(const Args a) {
 
 enum Verdict : int { kTake = 0, kRefuse = 1, kUnsure = 2 };
 
-struct Plan {            // of the row that is looked at: the first draft that is not surely taken, or the row after them
-    int n, verdict;
-    float p_most, q_most;   // the largest logits; kLeastRef: no distribution
-};
 struct Shared {
     uint32_t roots[32];                        // 2^(31 + j / 32)
-    Seen parts[kOwnParts];                     // of CTA 0
+    Seen parts[kOwnParts];
     Seen rows[kMaxRows];                       // joined
     int verdict[kMaxDraft];
     unsigned long long warp[kWarps][2];
     unsigned long long cta[kCluster][2];       // every CTA's sums
-    Plan plan;
 };
 
 // A row of probabilities: p = (m factor >> 32) 2^32 >> (down + shift), in units of 2^-62, of an Exact.
@@ -288,12 +285,12 @@ __device__ __forceinline__ uint32_t reciprocal(unsigned long long z) {
     return (uint32_t)min(better, 0xffffffffll);
 }
 
-// A cluster per sequence. Its first CTA decides by f32 sums which drafts are surely taken and which first one is
+// A cluster per sequence. f32 sums decide which drafts are surely taken and which first one is
 // not; that one's rows, and those that the next token is drawn from, are gone over by all CTAs, each a range of the vocabulary, with
 // exponentials of 30 bits and sums in whole numbers: which token a uniform number meets is a question of sums of
 // 10^5 terms next to one another, where f32 would err once in some hundred draws.
 template <typename T, bool OWN>
-__global__ void __launch_bounds__(kThreads, 3) k_draft_choose(const Args a) {
+__global__ void __launch_bounds__(kThreads, 4) k_draft_choose(const Args a) {
     __shared__ Shared s;
     cg::cluster_group cluster = cg::this_cluster();
     const int ctas = a.ctas, rank = cluster.block_rank(), seq = blockIdx.x / ctas;
@@ -308,10 +305,10 @@ __global__ void __launch_bounds__(kThreads, 3) k_draft_choose(const Args a) {
     const float *u = a.uniforms + (size_t)seq * (K + 1);
     const int32_t *tokens = a.tokens + (size_t)seq * K;
     if (tid < 32) s.roots[tid] = kRoots[tid];
-    // CTA 0: a thread per draft
+    // a thread per draft
     int x = -1;
     float x_target = -INFINITY, x_draft = -INFINITY, x_u = 0.f;
-    if (rank == 0 && tid < count) {
+    if (tid < count) {
         x = tokens[tid];
         x_u = fminf(fmaxf(u[tid], 0.f), 1.f);
         if (x >= 0 && x < V) {
@@ -325,17 +322,18 @@ __global__ void __launch_bounds__(kThreads, 3) k_draft_choose(const Args a) {
     cluster.barrier_wait(std::move(arrived));   // every CTA's shared memory is there
 
     if (OWN) {
-        Shared *lead = cluster.map_shared_rank(&s, 0);
+        Shared *other = cluster.map_shared_rank(&s, lane < ctas ? lane : 0);
         for (int t = rank * kWarps + warp; t < n_rows * a.parts; t += ctas * kWarps) {
             const int r = t / a.parts;
             const Seen seen = see_part(row_at<T>(a, sq, seq, r), V, t - r * a.parts, a.parts, c.hi, greedy);
-            if (lane == 0) lead->parts[t] = seen;
+            if (lane < ctas) other->parts[t] = seen;
         }
         cluster.sync();
     } else {
         pdl_wait();
     }
-    if (rank == 0) {
+    // every CTA makes the same decisions: a wait for one that tells them to the others takes 2 to 4 us
+    {
         const Seen *parts = OWN ? s.parts : a.seen + (size_t)seq * (2 * K + 1) * a.parts;
         for (int r = warp; r < n_rows; r += kWarps) {
             const Seen one = lane < a.parts ? parts[r * a.parts + lane] : Seen{kLeastRef, 0.f, 0x7fffffff};
@@ -367,31 +365,13 @@ __global__ void __launch_bounds__(kThreads, 3) k_draft_choose(const Args a) {
     int n = 0, verdict;
     bool spent = false;   // s.cta may still be read
     Row p{}, q{};
-    const int bits = 32 - __clz(max(V - 1, 1)), lift = 32 - bits;   // a sum of V numbers below 2^(32 + lift) fits 64 bits
+    const int bits = 31 - __clz(max(V - 1, 1)), lift = 31 - bits;   // a sum of V numbers m 2^32 >> bits, below 2^(32 + lift), fits 64 bits
     // this CTA's range, and its warps'
     const int slice = (V + ctas - 1) / ctas, from = min(rank * slice, V), to = min(from + slice, V);
     const int each = (slice + kWarps - 1) / kWarps;
     const int w0 = min(from + warp * each, to), w1 = min(w0 + each, to);
-    const T *rp = nullptr, *rq = nullptr;
-    // CTA 0's first warp: the first draft from n on that is not surely taken, to all CTAs
-    auto tell = [&]() {
-        if (rank != 0 || warp != 0) return;
-        int first = n;
-        while (first < count) {
-            const uint32_t other = __ballot_sync(0xffffffffu, first + lane >= count || s.verdict[first + lane] != kTake);
-            if (other != 0) {
-                first += __ffs(other) - 1;
-                break;
-            }
-            first += 32;
-        }
-        first = min(first, count);
-        const bool has_q = drafted && first < count;
-        Plan plan{first, first < count ? s.verdict[first] : kRefuse, kLeastRef, kLeastRef};
-        if (s.rows[first].alive()) plan.p_most = s.rows[first].most;
-        if (has_q && s.rows[sq.targets() + first].alive()) plan.q_most = s.rows[sq.targets() + first].most;
-        if (lane < ctas) cluster.map_shared_rank(&s, lane)->plan = plan;
-    };
+    const T *rp = nullptr, *rq = nullptr, *rp_staged = nullptr, *rq_staged = nullptr, *rp_row = nullptr;
+    int rp_n = -1;        // the row whose range is staged
     // a value or two of each thread, summed over every CTA, to all CTAs
     auto spread = [&](unsigned long long v0, unsigned long long v1) {
         v0 = warp_sum64(v0), v1 = warp_sum64(v1);
@@ -406,48 +386,59 @@ __global__ void __launch_bounds__(kThreads, 3) k_draft_choose(const Args a) {
         cluster.sync();
     };
     constexpr bool kRounded = sizeof(T) == 4;
-    // f(exponential of token i of p, i), or f(p's, q's), for the warp's range: loads ahead of what is made of them
+    // This CTA's range of a row, copied to shared memory at once where there is room: passes over it would each wait for
+    // the L2 a few times. The pointer is to be used as the row's.
+    extern __shared__ uint4 stage[];
+    auto staged = [&](const T *row, int slot) -> const T * {
+        if (a.staged == 0) return row;
+        char *to_at = reinterpret_cast<char *>(stage) + slot * a.staged;
+        const char *at = reinterpret_cast<const char *>(row + from);
+        const int off = (int)(reinterpret_cast<uintptr_t>(at) & 3), words = ((to - from) * (int)sizeof(T) + off + 3) / 4;   // (bf16: whole words)
+        const uint32_t to_u = smem_u32(to_at);
+        for (int w = tid; w < words; w += kThreads)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to_u + 4 * w), "l"(at - off + 4 * w) : "memory");
+        return reinterpret_cast<const T *>(to_at + off) - from;
+    };
+    // f(exponential of token i of p, i), or f(p's, q's), for the warp's range
     auto over_one = [&](auto f) {
         const F2 less = f2(-p.most, -p.most);
-        for (int i = w0 + lane; i < w1; i += 32 * 8) {
-            float x[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = i + 32 * j < w1 ? load_logit(rp, i + 32 * j) : -INFINITY;
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                Exact e, g;
-                exact_exp2<kRounded>(x[j], x[j + 1], less, c, s.roots, e, g);
-                f(e, i + 32 * j);
-                f(g, i + 32 * j + 32);
-            }
+#pragma unroll 2
+        for (int i = w0 + lane; i < w1; i += 64) {
+            Exact e, g;
+            exact_exp2<kRounded>(load_logit(rp, i), i + 32 < w1 ? load_logit(rp, i + 32) : -INFINITY, less, c, s.roots, e, g);
+            f(e, i);
+            f(g, i + 32);
         }
     };
     auto over_both = [&](auto f) {
         const F2 less = f2(-p.most, -q.most);
-        for (int i = w0 + lane; i < w1; i += 32 * 4) {
-            float x[4], y[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[j] = i + 32 * j < w1 ? load_logit(rp, i + 32 * j) : -INFINITY;
-                y[j] = i + 32 * j < w1 ? load_logit(rq, i + 32 * j) : -INFINITY;
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                Exact e, g;
-                exact_exp2<kRounded>(x[j], y[j], less, c, s.roots, e, g);
-                f(e, g);
-            }
+#pragma unroll 2
+        for (int i = w0 + lane; i < w1; i += 32) {
+            Exact e, g;
+            exact_exp2<kRounded>(load_logit(rp, i), load_logit(rq, i), less, c, s.roots, e, g);
+            f(e, g);
         }
     };
     while (true) {
-        tell();
-        cluster.sync();
-        const Plan plan = s.plan;
-        n = plan.n, verdict = plan.verdict;
+        while (n < count && s.verdict[n] == kTake) ++n;
         if (greedy) break;
-        p = Row{plan.p_most, 0, 0, 0}, q = Row{plan.q_most, 0, 0, 0};
+        verdict = n < count ? s.verdict[n] : kRefuse;
+        const bool has_q = drafted && n < count;
+        p = Row{kLeastRef, 0, 0, 0}, q = p;
+        if (s.rows[n].alive()) p.most = s.rows[n].most;
+        if (has_q && s.rows[sq.targets() + n].alive()) q.most = s.rows[sq.targets() + n].most;
         rp = row_at<T>(a, sq, seq, n);
-        rq = drafted && n < count ? row_at<T>(a, sq, seq, sq.targets() + n) : nullptr;
+        rq = has_q ? row_at<T>(a, sq, seq, sq.targets() + n) : nullptr;
+        if (rp_n != n) {
+            rp_row = rp;
+            if (rp_n >= 0) __syncthreads();   // (the ranges of the row before are not read any more)
+            rp_staged = staged(rp, 0);
+            rq_staged = has_q ? staged(rq, 1) : nullptr;
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncthreads();
+            rp_n = n;
+        }
+        rp = rp_staged, rq = rq_staged;
         if (rq == nullptr && verdict == kRefuse) break;   // (drawn from p alone: its sum is the draw's)
         unsigned long long sums[2] = {0, 0};
         if (p.alive() && q.alive())
@@ -463,17 +454,17 @@ __global__ void __launch_bounds__(kThreads, 3) k_draft_choose(const Args a) {
             Row &r = w ? q : p;
             const int zeros = __clzll(z);
             r.factor = reciprocal(z << zeros);
-            r.down = 33 - lift - zeros;
+            r.down = 32 - lift - zeros;
             r.z = z;
         }
         if (verdict == kRefuse) break;
-        if (rank == 0 && tid == n) {   // an unsure draft
+        if (tid == n) {   // an unsure draft: the same in every CTA
             auto of = [&](float logit, const Row &r) {   // (of values that the draw takes for 0 too)
                 return r.factor && !masked(logit) ? exp(((double)logit - (double)r.most) / (double)temperature) / ((double)r.z * exp2(-31.0 - lift)) : 0.0;
             };
             s.verdict[n] = (double)x_u * (rq != nullptr ? of(x_draft, q) : 1.0) < of(x_target, p) ? kTake : kRefuse;
         }
-        cluster.sync();   // (s.cta and s.plan are free again)
+        cluster.sync();   // (s.cta is free again)
         spent = false;
         // a draft that is refused after all: its rows' sums are made once more by the next turn
     }
@@ -541,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_draft_choose(const Args a) {
                         z = total;
                         if (gone >= 0 && gone < V && !plain) {
                             Exact e, g;
-                            exact_exp2<kRounded>(load_logit(rp, gone), 0.f, f2(-p.most, 0.f), c, s.roots, e, g);
+                            exact_exp2<kRounded>(load_logit(rp_row, gone), 0.f, f2(-p.most, 0.f), c, s.roots, e, g);
                             z += place(e.m, bits + e.shift);
                         }
                     }
@@ -576,24 +567,29 @@ bool sizes_ok(int n_seq, int n_draft, int vocab) {
 constexpr int kOwnLogits = 65536;
 struct Shape {
     bool own;
-    int parts, ctas;
+    int parts, ctas, staged;
 };
-Shape shape_of(int n_seq, int n_draft, int vocab) {
+constexpr int kMostStaged = 100 * 1024;
+Shape shape_of(int n_seq, int n_draft, int vocab, int size) {
     const int rows = 2 * n_draft + 1;
     Shape p;
     p.own = (long long)rows * vocab <= kOwnLogits;
     p.ctas = 1;
     const int most = (long long)n_seq * kCluster <= 152 * 3 ? kCluster : kCluster / 2;
     while (p.ctas < most && (p.own ? (long long)rows * vocab : vocab) > p.ctas * 1024ll) p.ctas *= 2;
-    const long long warps = p.own ? p.ctas * kWarps : std::max(1ll, 152ll * 32 / std::max(1, n_seq));   // for a sequence
+    const long long warps = p.own ? p.ctas * kWarps : std::max(1ll, 152ll * 64 / std::max(1, n_seq));   // for a sequence
+    const int slice = (vocab + p.ctas - 1) / p.ctas;
+    p.staged = (slice * size + 4 + 15) / 16 * 16;
+    if (2 * p.staged > kMostStaged) p.staged = 0;
     p.parts = (int)std::max(1ll, std::min<long long>(std::min(kMaxParts, vocab / 256), warps / rows));
     return p;
 }
 
-// Clusters of 16 are allowed once for each device.
+// Clusters of 16 and their shared memory are allowed once for each device.
 template <typename T, bool OWN>
 cudaError_t allow() {
-    return cudaFuncSetAttribute(k_draft_choose<T, OWN>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    const cudaError_t e = cudaFuncSetAttribute(k_draft_choose<T, OWN>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    return e ? e : cudaFuncSetAttribute(k_draft_choose<T, OWN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostStaged);
 }
 cudaError_t allow_clusters() {
     static std::atomic<unsigned long long> done{0};
@@ -614,7 +610,7 @@ extern "C" {
 
 size_t talker_draft_scratch(int n_seq, int n_draft, int vocab) {
     if (!sizes_ok(n_seq, n_draft, vocab)) return 0;
-    const Shape p = shape_of(n_seq, n_draft, vocab);
+    const Shape p = shape_of(n_seq, n_draft, vocab, 4);   // (the types differ in what is staged alone)
     return p.own ? 0 : (size_t)n_seq * (2 * n_draft + 1) * p.parts * sizeof(Seen);
 }
 
@@ -630,14 +626,15 @@ talker_status talker_draft_verify(const void *target, int64_t target_seq, int64_
     if (n_seq == 0) return TALKER_OK;
     const size_t need = talker_draft_scratch(n_seq, n_draft, vocab);
     if (need > 0 && (!scratch || scratch_bytes < need || reinterpret_cast<uintptr_t>(scratch) % 16)) return TALKER_EINVAL;
-    const Shape p = shape_of(n_seq, n_draft, vocab);
+    const Shape p = shape_of(n_seq, n_draft, vocab, dtype == TALKER_DTYPE_F32 ? 4 : 2);
     const Args a{target, draft, target_seq, target_row, draft_seq, draft_row, tokens, counts, uniforms, temperatures, n_draft, vocab,
-                 tokens_out, accepted, logprobs, p.parts, p.ctas, static_cast<Seen *>(scratch)};
+                 tokens_out, accepted, logprobs, p.parts, p.ctas, p.staged, static_cast<Seen *>(scratch)};
     const bool f32 = dtype == TALKER_DTYPE_F32;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     cfg.blockDim = dim3(kThreads);
     cfg.gridDim = dim3((unsigned)(n_seq * p.ctas));
+    cfg.dynamicSmemBytes = 2 * (size_t)p.staged;
     cfg.stream = static_cast<cudaStream_t>(cuda_stream);
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = p.ctas;
