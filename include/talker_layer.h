@@ -117,7 +117,8 @@ talker_status talker_rotate(const uint64_t *turns, float amplitude, int head_dim
  * four bits of byte i and input 2 i + 1 in the high ones; scales fp16 [n][ceil(k / group)]; zeros uint8
  * of the same shape, or NULL. talker_w4_pack lays them out as the kernels read them, in `tiles`:
  *   16 rows to a tile (rows past n are zeros; of a gated matrix 8 rows of W, then the same 8 of U), inputs padded
- *   to a multiple of 128. For each tile and 128 inputs one record. Twice 512 bytes for 64 inputs: 16 of lane l =
+ *   to a multiple of 128. For each tile and 128 inputs one record, in the order of spans of 32 tiles (the last may have
+ *   fewer), in a span of inputs, then of tiles. In a record twice 512 bytes for 64 inputs: 16 of lane l =
  *   4 g + t, words j = 0..3, whose 4-bit fields 0..7 are, with i = 16 j + 4 t: inputs i and i + 1 of row g in fields 0
  *   and 4, i + 2 and i + 3 in fields 1 and 5, and the same of row g + 8 in fields 2, 6, 3, 7 (the operand's registers
  *   of a tensor-core product, one mask away). Then for each group 8 pairs of scales of rows (g, g + 8), and, with
@@ -146,8 +147,8 @@ talker_status talker_w4_quantize(const void *w, int dtype, int64_t row_stride, i
  * likewise, res_row apart, in out's type; it may be out itself. Products of codes and x are
  * made by the tensor cores with f32 sums: bf16 x enters exactly (values below 2^-31 of a row's largest lose bits), others with
  * 22 bits in two parts. A row of x with a NaN or an infinity gives NaN. Made for few rows (32 columns of x,
- * one a bf16 row and two any other, in one pass over the weights; more are taken in several), at most 2^19. scratch: talker_w4_scratch bytes, 16-byte aligned
- * (may be NULL when that is 0), for the same sizes and types; it need not hold anything on entry, and calls that may run at the same
+ * one a bf16 row and two any other, in one pass over the weights; more are taken in several), at most 2^16. scratch: talker_w4_scratch bytes, 16-byte aligned,
+ * for the same sizes and types; it need not hold anything on entry, and calls that may run at the same
  * time need their own. Errors: EINVAL, ECUDA. */
 size_t talker_w4_scratch(const talker_w4 *w, int x_dtype, int rows);
 talker_status talker_w4_matmul(const talker_w4 *w, const void *x, int x_dtype, int64_t x_row, const float *x_scales,

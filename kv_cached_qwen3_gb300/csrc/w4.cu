@@ -13,7 +13,11 @@ namespace {
 
 constexpr int kUnit = 128;              // inputs: what k is padded to, and what one warp takes at a time
 constexpr int kUnitBytes = 16 * kUnit / 2;
-constexpr int kMostRows = 1 << 19;
+constexpr int kMostRows = 1 << 16;
+
+constexpr int kWarps = 16, kThreads = kWarps * 32;
+constexpr int kTiles = 2;               // of a warp
+constexpr int kSpan = kWarps * kTiles;  // row tiles of a CTA
 
 struct Sizes {
     int tiles, units, groups;   // row tiles, units of inputs, groups of a unit
@@ -28,6 +32,11 @@ __host__ __device__ inline Sizes sizes_of(int n, int k, int group, int zeros, in
     s.record = kUnitBytes + 32 * s.groups + (zeros ? (s.groups == 1 ? 32 : 16 * s.groups) : 0);   // (whole sectors of 32 bytes)
     s.bytes = (size_t)s.tiles * s.units * s.record;
     return s;
+}
+// Where a tile's unit lies: a span's records of one unit are neighbours.
+__host__ __device__ inline size_t record_at(const Sizes &s, int tile, int unit) {
+    const int span = tile / kSpan, first = span * kSpan, of_span = s.tiles - first < kSpan ? s.tiles - first : kSpan;
+    return ((size_t)first * s.units + (size_t)unit * of_span + (tile - first)) * s.record;
 }
 
 // ---- layout
@@ -63,7 +72,7 @@ __global__ void __launch_bounds__(256) k_w4_pack_codes(const PackArgs a, long lo
             w |= c << 4 * ((e & 1) * 4 + (e >> 1) + 2 * half);
         }
     }
-    reinterpret_cast<uint32_t *>(a.tiles + ((size_t)tile * a.s.units + own / 2) * a.s.record + own % 2 * 512)[i & 127] = w;
+    reinterpret_cast<uint32_t *>(a.tiles + record_at(a.s, tile, own / 2) + own % 2 * 512)[i & 127] = w;
 }
 // A thread per scale (and zero) of a tile's row.
 __global__ void __launch_bounds__(256) k_w4_pack_scales(const PackArgs a, long long scales) {
@@ -76,7 +85,7 @@ __global__ void __launch_bounds__(256) k_w4_pack_scales(const PackArgs a, long l
     const int row = row_of(a, tile, g + 8 * half, m), in_unit = group % a.s.groups;
     const bool there = row < a.n && group < groups;
     const size_t from = (size_t)row * groups + group;
-    unsigned char *record = a.tiles + ((size_t)tile * a.s.units + group / a.s.groups) * a.s.record + kUnitBytes;
+    unsigned char *record = a.tiles + record_at(a.s, tile, group / a.s.groups) + kUnitBytes;
     reinterpret_cast<__half *>(record + in_unit * 32)[r] = there ? a.scales[m][from] : __float2half_rn(0.f);
     if (a.zeros[0]) (record + 32 * a.s.groups + in_unit * 16)[r] = there ? a.zeros[m][from] & 15 : 0;
 }
@@ -222,7 +231,7 @@ __device__ __forceinline__ void prepare_rows(const XArgs &a, int first, int rows
         for (int p = 0; p < PARTS; ++p) frags[((quarter * cols + col + own * PARTS + p) * 4 + t) * 2 + s] = make_uint2(h[p][0], h[p][1]);
     }
 }
-__device__ __forceinline__ void prepare_rows(const XArgs &a, int first, int rows, uint2 *frags, int cols, int col, int units, float *back, float *red) {
+__device__ __noinline__ void prepare_rows(const XArgs &a, int first, int rows, uint2 *frags, int cols, int col, int units, float *back, float *red) {
     if (a.dtype == TALKER_DTYPE_BF16) prepare_rows<__nv_bfloat16, 1>(a, first, rows, frags, cols, col, units, back, red);
     else if (a.dtype == TALKER_DTYPE_F32) prepare_rows<float, 2>(a, first, rows, frags, cols, col, units, back, red);
     else prepare_rows<__nv_fp8_storage_t, 2>(a, first, rows, frags, cols, col, units, back, red);
@@ -262,12 +271,19 @@ struct Zero {
 __device__ __forceinline__ Zero zero_of(uint32_t z) { return {(0xe400u | z) * 0x10001u, (0xd400u | z << 4) * 0x10001u}; }
 __device__ __forceinline__ uint32_t centred(uint32_t v, Zero z) {
     uint32_t y;
-    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"((v & 0x000f000fu) | 0x64006400u), "r"(z.a));
+    asm("{.reg .b32 t;\n\t"
+        "lop3.b32 t, %1, 0x000f000f, 0x64006400, 0xea;\n\t"   // (v & ..) | ..: one instruction, two as the compiler makes it
+        "add.rn.f16x2 %0, t, %2;}"
+        : "=r"(y) : "r"(v), "r"(z.a));
     return y;
 }
 __device__ __forceinline__ uint32_t centred16(uint32_t v, Zero z) {
     uint32_t y;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"((v & 0x00f000f0u) | 0x64006400u), "r"(0x2c002c00u), "r"(z.b));
+    asm("{.reg .b32 t, s;\n\t"
+        "lop3.b32 t, %1, 0x00f000f0, 0x64006400, 0xea;\n\t"
+        "mov.b32 s, 0x2c002c00;\n\t"
+        "fma.rn.f16x2 %0, t, s, %2;}"
+        : "=r"(y) : "r"(v), "r"(z.b));
     return y;
 }
 __device__ __forceinline__ void copy16(uint32_t to, const void *from) {
@@ -290,246 +306,239 @@ __device__ __forceinline__ uint32_t read2(uint32_t at) {
     return v;
 }
 
-constexpr int kWarps = 16, kThreads = kWarps * 32;
 constexpr int kMultiprocessors = 152, kMostShared = 227 * 1024;
+constexpr int kDepth = 3, kSlots = kDepth + 1;   // steps whose copies are on their way: 100 KB a multiprocessor
+constexpr int kOwnRows = 4, kOwnValues = 16384;  // of x: up to so many the CTAs prepare themselves
+
+// A product is `steps` steps, in the order of passes, spans and units: a step is a unit of all tiles of a span for a pass's columns. CTA
+// c takes the steps from start(c) to start(c + 1), so all have the same number, give or take one. A stretch of steps of one
+// pass and span is a segment, whose sums go to the place c + pass * spans + span.
+struct Steps {
+    long long all;
+    int ctas, units;
+    __host__ __device__ long long start(int c) const { return all * c / ctas; }
+    __host__ __device__ int cta_of(long long step) const { return (int)(((step + 1) * ctas - 1) / all); }
+};
 struct MatmulArgs {
     const unsigned char *tiles;
     Sizes s;
+    Steps steps;
     XArgs x;
     const uint4 *frags;       // null: the CTAs prepare the rows themselves
-    const float *back;
-    float4 *partial;          // [pass][tile][column tile][lane]: sums of the inputs so far, where they do not fit at once
+    float *back;              // [row]: what undoes the rows' scaling
+    float4 *sums;             // [place][warp][tile][column tile][lane]
     const void *res;
     void *out;
     long long res_row, out_row;
-    int n, rows;
+    int n, spans;
     Columns c;
-    int k_parts;              // warps that share a tile
-    int units_at_once;        // of x in shared memory
-    int fixed;                // bytes of shared memory before x
+    int rows, x_bytes;        // of x in a slot, or of all of x
     bool zeros, gated, bf16;
 };
 
-// A warp's ring of records that are on their way: RT tiles' of a unit a slot, 68 KB in flight a multiprocessor.
-constexpr int ring_depth(int rt) { return rt == 1 ? 4 : 2; }
-constexpr int fixed_bytes(int nt, int rt, int record) {   // the rings, the sums of one of a warp's tiles, the rows' factors
-    return kWarps * (ring_depth(rt) + 1) * rt * record + kWarps * nt * 512 + 1024;
-}
-static_assert((kMostShared - fixed_bytes(4, 2, kUnitBytes + 4 * 48)) / (32 * 256) >= 8, "room for 8 units of x");
-
-// Persistent CTAs, one a multiprocessor, over groups of row tiles. x lies in shared memory as fragments (all of it, or so many
-// units at a time); records come through rings of asynchronous copies, a ring a warp, so that no warp waits for
-// another. In a round the warps take kWarps / k_parts tiles (RT of them at once a warp: one fragment of x then serves two
-// tiles), k_parts warps share a tile's units, and their sums meet in shared memory, always in the same order. A group's sum
-// is added to the total times its scale.
+// One CTA a multiprocessor, all with the same number of steps, in a ring of asynchronous copies: each warp's two records of the step, and the step's
+// fragments of x (where the CTAs do not prepare x themselves and keep all of it). Nothing is joined in here: a segment's sums go
+// to memory, and the kernel after adds them up. A group of inputs' sum is added to the total times its scale.
 template <int NT, int NG>
 __global__ void __launch_bounds__(kThreads, 1) k_w4_matmul(const MatmulArgs a) {
-    constexpr int RT = NT >= 3 ? 2 : 1, kDepth = ring_depth(RT), kSlots = kDepth + 1;
     extern __shared__ uint4 smem[];
+    __shared__ float red[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int units = a.s.units, record = a.s.record, pass = blockIdx.y, parts = a.c.parts;
-    const int cols = min(a.c.cols, a.rows * parts - pass * a.c.cols);
-    const int slot_bytes = RT * record;
-    float4 *sums = reinterpret_cast<float4 *>(smem) + kWarps * kSlots * slot_bytes / 16;
-    float *back = reinterpret_cast<float *>(sums + kWarps * NT * 32);   // 32 rows at most, and room for a reduction
-    uint4 *xs = smem + a.fixed / 16;
-    const int k_part = warp % a.k_parts, slot = warp / a.k_parts, per_round = kWarps / a.k_parts;
-    const int groups_of_tiles = (a.s.tiles + RT - 1) / RT;
-    const int rounds = (groups_of_tiles + gridDim.x * per_round - 1) / (gridDim.x * per_round);
-    // tile group of this warp in a round: neighbours read neighbouring memory
-    auto group_of = [&](int round) { return (round * per_round + slot) * (int)gridDim.x + (int)blockIdx.x; };
-    const uint32_t mine = smem_u32(smem) + warp * kSlots * slot_bytes;
+    const int units = a.s.units, record = a.s.record, parts = a.c.parts;
+    const bool own = a.frags == nullptr;
+    const int slot_bytes = kSpan * record + (own ? 0 : a.x_bytes);
+    const uint32_t slots = smem_u32(smem) + (own ? a.x_bytes : 0), slots_end = slots + kSlots * slot_bytes;
+    const uint32_t mine = warp * kTiles * record + lane * 16;   // in a slot
     const bool extra = lane < (record - kUnitBytes) / 16;
+    const long long first = a.steps.start(blockIdx.x);
+    const int count = (int)(a.steps.start(blockIdx.x + 1) - first);
 
-    int first = 0, last = 0, steps = 0;      // the units at hand, and a warp's steps a round
-    int at_round = 0, at_unit = 0, end_unit = 0, to_slot = 0;   // of the next copy
-    const unsigned char *src = nullptr;
-    int second = 0;                          // the other tile's record, from src
-    auto begin = [&]() {
-        const int tg = group_of(at_round);
-        at_unit = first + k_part;
-        end_unit = at_round < rounds && tg < groups_of_tiles ? last : 0;
-        src = a.tiles + ((size_t)min(tg, groups_of_tiles - 1) * RT * units + at_unit) * record + lane * 16;
-        if (RT == 2) second = tg * 2 + 1 < a.s.tiles ? units * record : 0;
+    // where a step is: place = pass * spans + span
+    struct At {
+        int place, unit, tiles, cols;     // tiles of this warp: 0 to 2
+        const unsigned char *codes;       // this lane's of the warp's first tile
+        const uint4 *x;
+        int stride;                       // to the next unit's codes
     };
-    auto copy_next = [&]() {
-        if (at_unit < end_unit) {
-            const uint32_t to = mine + to_slot * slot_bytes + lane * 16;
-#pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                const unsigned char *from = src + (i ? second : 0);
-                copy16(to + i * record, from);
-                copy16(to + i * record + 512, from + 512);
-                if (extra) copy16(to + i * record + 1024, from + 1024);
-            }
+    auto enter = [&](At &p) {   // a place, at p.unit
+        const int pass = p.place / a.spans, span = p.place - pass * a.spans, of_span = min(a.s.tiles - span * kSpan, kSpan);
+        p.tiles = min(max(of_span - warp * kTiles, 0), kTiles);
+        p.cols = min(a.c.cols, a.rows * parts - pass * a.c.cols);
+        p.stride = of_span * record;
+        p.codes = a.tiles + ((size_t)span * kSpan * units + (size_t)p.unit * of_span + warp * kTiles) * record + lane * 16;
+        p.x = a.frags + ((size_t)pass * units + p.unit) * 16 * a.c.cols;
+    };
+    auto next = [&](At &p) {
+        p.codes += p.stride;
+        p.x += 16 * a.c.cols;
+        if (++p.unit == units) {
+            p.unit = 0, ++p.place;
+            enter(p);
         }
-        src += a.k_parts * record;
-        at_unit += a.k_parts;
-        if (at_unit - k_part >= first + steps * a.k_parts) ++at_round, begin();
-        if (++to_slot == kSlots) to_slot = 0;
-        asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    At to;
+    to.place = (int)(first / units), to.unit = (int)(first - (long long)to.place * units);
+    enter(to);
+    At from = to;
+    auto copy_codes = [&](const At &p, uint32_t slot) {
+        if (p.tiles > 0) {
+            copy16(slot + mine, p.codes);
+            copy16(slot + mine + 512, p.codes + 512);
+            if (extra) copy16(slot + mine + 1024, p.codes + 1024);
+        }
+        if (p.tiles > 1) {
+            copy16(slot + mine + record, p.codes + record);
+            copy16(slot + mine + record + 512, p.codes + record + 512);
+            if (extra) copy16(slot + mine + record + 1024, p.codes + record + 1024);
+        }
+    };
+    auto copy_x = [&](const At &p, uint32_t slot) {   // (also columns past the last pass's: they are not looked at)
+        if (!own && tid < 16 * a.c.cols) copy16(slot + kSpan * record + tid * 16, p.x + tid);
+    };
+    // codes do not wait for the kernel before, x does
+    At ahead = to;
+    uint32_t slot = slots;
+    for (int i = 0; i < min(kDepth, count); ++i, next(ahead), slot += slot_bytes) copy_codes(ahead, slot);
+    if (own) {
+        prepare_rows(a.x, 0, a.rows, reinterpret_cast<uint2 *>(smem), a.c.cols, 0, units, a.back, red);   // (the same in every CTA)
+    } else {
+        pdl_wait();
+        slot = slots;
+        for (int i = 0; i < min(kDepth, count); ++i, next(to), slot += slot_bytes) copy_x(to, slot);
+    }
+    to = ahead;
+#pragma unroll
+    for (int i = 0; i < kDepth; ++i) asm volatile("cp.async.commit_group;" ::: "memory");   // (the first has them all)
+    uint32_t now = slots;
+    slot = slots + kDepth * slot_bytes;
 
-    for (first = 0; first < units; first = last) {
-        last = min(first + a.units_at_once, units);
-        steps = (last - first + a.k_parts - 1) / a.k_parts;
-        if (first > 0) {   // the copies before are done and read, and so is x
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            __syncthreads();
-        }
-        if (a.frags == nullptr) {
-            at_round = to_slot = 0;
-            begin();
-            for (int i = 0; i < kDepth; ++i) copy_next();   // (codes do not wait for x)
-            prepare_rows(a.x, 0, a.rows, reinterpret_cast<uint2 *>(xs), cols, 0, units, back, back + 64);
-        } else {
-            at_round = to_slot = 0;
-            begin();
-            for (int i = 0; i < kDepth; ++i) copy_next();
-            if (first == 0) {
-                pdl_wait();
-                if (tid < cols / parts) back[tid] = a.back[pass * a.c.cols / parts + tid];
-            }
-            const uint4 *from = a.frags + ((size_t)pass * units + first) * 4 * a.c.cols * 4;
-            const int n = (last - first) * 4 * cols * 4;
-            if (cols == a.c.cols) {
-#pragma unroll 8
-                for (int i = tid; i < n; i += kThreads) xs[i] = from[i];
-            } else {
-                for (int i = tid; i < n; i += kThreads) {
-                    const int quarter = i / (cols * 4);
-                    xs[i] = from[quarter * a.c.cols * 4 + i - quarter * cols * 4];
-                }
-            }
-        }
-        __syncthreads();
-        int from_col[NT];
+    float total[kTiles][NT][4];
+    bool fresh = true;
+    int from_col[NT];
+    for (int step = 0; step < count; ++step) {
+        if (fresh) {
+            fresh = false;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) from_col[i] = min(i * 8 + g, cols - 1) * 4 + t;   // (columns past the last are not looked at)
-        int from_slot = 0;
-        for (int round = 0; round < rounds; ++round) {
-            const int end = group_of(round) < groups_of_tiles ? last : 0;
-            float total[RT][NT][4];
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
+            for (int r = 0; r < kTiles; ++r)
 #pragma unroll
                 for (int i = 0; i < NT; ++i)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) total[r][i][j] = 0.f;
-            int unit = first + k_part;
-            const uint4 *x = xs + k_part * 16 * cols;
-            for (int step = 0; step < steps; ++step, unit += a.k_parts, x += a.k_parts * 16 * cols) {
-                asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
-                __syncwarp();   // (other lanes' copies too; and the slot before this one has been read by all)
-                copy_next();    // (into that one)
-                const uint32_t at = mine + from_slot * slot_bytes;
-                if (++from_slot == kSlots) from_slot = 0;
-                if (unit >= end) continue;
-                uint4 w[RT][2];
 #pragma unroll
-                for (int r = 0; r < RT; ++r) w[r][0] = read16(at + r * record + lane * 16), w[r][1] = read16(at + r * record + 512 + lane * 16);
-                float c[RT][NT][4];
-                Zero z0[RT], z1[RT];
+            for (int i = 0; i < NT; ++i) from_col[i] = (min(i * 8 + g, from.cols - 1) * 4 + t) * 16;   // (columns past the last are not looked at)
+        }
+        asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+        __syncthreads();   // (others' copies too; and the slot before this one has been read by all)
+        if (step + kDepth < count) {
+            copy_codes(to, slot);
+            copy_x(to, slot);
+            next(to);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        slot = slot + slot_bytes == slots_end ? slots : slot + slot_bytes;
+        if (from.tiles > 0) {
+            const uint32_t x = own ? smem_u32(smem) + from.unit * 256 * a.c.cols : now + kSpan * record;
+            const uint32_t tail = now + mine - lane * 16 + kUnitBytes;   // scales, then zeros
+            uint4 w[kTiles][2];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {   // 32 inputs
-                    if (q * NG % 4 == 0) {
+            for (int r = 0; r < kTiles; ++r) w[r][0] = read16(now + mine + r * record), w[r][1] = read16(now + mine + r * record + 512);
+            float c[kTiles][NT][4];
+            Zero z0[kTiles], z1[kTiles];
 #pragma unroll
-                        for (int r = 0; r < RT; ++r) {
-                            uint32_t z = 0x0808;
-                            if (a.zeros) z = read2(at + r * record + kUnitBytes + 32 * NG + q * NG / 4 * 16 + g * 2);
-                            z0[r] = zero_of(z & 15), z1[r] = zero_of(z >> 8);
+            for (int q = 0; q < 4; ++q) {   // 32 inputs
+                if (q * NG % 4 == 0) {
+#pragma unroll
+                    for (int r = 0; r < kTiles; ++r) {
+                        if (a.zeros) {
+                            const uint32_t z = read2(tail + r * record + 32 * NG + q * NG / 4 * 16 + g * 2);
+                            z0[r] = zero_of(z & 15), z1[r] = zero_of(z >> 8 & 15);
+                        } else {
+                            z0[r] = z1[r] = zero_of(8);
                         }
                     }
-                    uint4 b[NT];
+                }
+                uint4 b[NT];
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) b[i] = x[q * cols * 4 + from_col[i]];
+                for (int i = 0; i < NT; ++i) b[i] = read16(x + q * 64 * a.c.cols + from_col[i]);
 #pragma unroll
-                    for (int r = 0; r < RT; ++r)
+                for (int r = 0; r < kTiles; ++r)
 #pragma unroll
-                        for (int s = 0; s < 2; ++s) {
-                            const uint4 ww = w[r][q / 2];
-                            const uint32_t v = q % 2 ? (s ? ww.w : ww.z) : (s ? ww.y : ww.x), v8 = v >> 8;
-                            const uint32_t a0 = centred(v, z0[r]), a1 = centred(v8, z1[r]), a2 = centred16(v, z0[r]), a3 = centred16(v8, z1[r]);
+                    for (int s = 0; s < 2; ++s) {
+                        const uint4 ww = w[r][q / 2];
+                        const uint32_t v = q % 2 ? (s ? ww.w : ww.z) : (s ? ww.y : ww.x), v8 = v >> 8;
+                        const uint32_t a0 = centred(v, z0[r]), a1 = centred(v8, z1[r]), a2 = centred16(v, z0[r]), a3 = centred16(v8, z1[r]);
 #pragma unroll
-                            for (int i = 0; i < NT; ++i) {
-                                if (s == 0 && q * NG % 4 == 0) mma_f16_first(c[r][i], a0, a1, a2, a3, b[i].x, b[i].y);
-                                else mma_f16(c[r][i], a0, a1, a2, a3, s ? b[i].z : b[i].x, s ? b[i].w : b[i].y);
-                            }
+                        for (int i = 0; i < NT; ++i) {
+                            if (s == 0 && q * NG % 4 == 0) mma_f16_first(c[r][i], a0, a1, a2, a3, b[i].x, b[i].y);
+                            else mma_f16(c[r][i], a0, a1, a2, a3, s ? b[i].z : b[i].x, s ? b[i].w : b[i].y);
                         }
-                    if ((q + 1) * NG % 4 == 0) {
+                    }
+                if ((q + 1) * NG % 4 == 0) {
 #pragma unroll
-                        for (int r = 0; r < RT; ++r) {
-                            const uint32_t d = read4(at + r * record + kUnitBytes + q * NG / 4 * 32 + g * 4);
-                            const float d0 = __half2float(__ushort_as_half((unsigned short)d)), d1 = __half2float(__ushort_as_half((unsigned short)(d >> 16)));
+                    for (int r = 0; r < kTiles; ++r) {
+                        const uint32_t d = read4(tail + r * record + q * NG / 4 * 32 + g * 4);
+                        const float d0 = __half2float(__ushort_as_half((unsigned short)d)), d1 = __half2float(__ushort_as_half((unsigned short)(d >> 16)));
 #pragma unroll
-                            for (int i = 0; i < NT; ++i) {
-                                total[r][i][0] = fmaf(d0, c[r][i][0], total[r][i][0]), total[r][i][1] = fmaf(d0, c[r][i][1], total[r][i][1]);
-                                total[r][i][2] = fmaf(d1, c[r][i][2], total[r][i][2]), total[r][i][3] = fmaf(d1, c[r][i][3], total[r][i][3]);
-                            }
+                        for (int i = 0; i < NT; ++i) {
+                            total[r][i][0] = fmaf(d0, c[r][i][0], total[r][i][0]), total[r][i][1] = fmaf(d0, c[r][i][1], total[r][i][1]);
+                            total[r][i][2] = fmaf(d1, c[r][i][2], total[r][i][2]), total[r][i][3] = fmaf(d1, c[r][i][3], total[r][i][3]);
                         }
                     }
                 }
             }
-            // the round's sums: an item is a lane's part of a tile's result, rows g and g + 8 of two columns
+        }
+        now = now + slot_bytes == slots_end ? slots : now + slot_bytes;
+        if (step + 1 == count || from.unit + 1 == units) {   // the segment's end
+            float4 *place = a.sums + ((size_t)(blockIdx.x + from.place) * kWarps + warp) * kTiles * NT * 32 + lane;
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
+            for (int r = 0; r < kTiles; ++r)
 #pragma unroll
                 for (int i = 0; i < NT; ++i)
-                    sums[(warp * NT + i) * 32 + lane] = make_float4(total[r][i][0], total[r][i][1], total[r][i][2], total[r][i][3]);
-                __syncthreads();
-                for (int item = tid; item < per_round * NT * 32; item += kThreads) {
-                    const int l = item & 31, i = item / 32 % NT, sl = item / (NT * 32);
-                    const int tile = ((round * per_round + sl) * (int)gridDim.x + (int)blockIdx.x) * RT + r, col = i * 8 + 2 * (l & 3);
-                    if (tile >= a.s.tiles || col >= cols) continue;
-                    float v[4] = {0.f, 0.f, 0.f, 0.f};
-                    for (int k = 0; k < a.k_parts; ++k) {
-                        const float4 p = sums[((sl * a.k_parts + k) * NT + i) * 32 + l];
-                        v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
-                    }
-                    float4 *partial = a.partial + (((size_t)pass * a.s.tiles + tile) * NT + i) * 32 + l;   // (the same thread's every time)
-                    if (first > 0) {
-                        const float4 p = *partial;
-                        v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
-                    }
-                    if (last < units) {
-                        *partial = make_float4(v[0], v[1], v[2], v[3]);
-                        continue;
-                    }
-                    const int row0 = a.gated ? tile * 8 + (l >> 2) : tile * 16 + (l >> 2);
-                    if (parts == 2) v[0] += v[1], v[2] += v[3];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        if (col + e >= cols || (e == 1 && parts == 2)) continue;
-                        const int own = parts == 2 ? col / 2 : col + e, x_row = pass * a.c.cols / parts + own;
-                        const float up = back[own], y0 = v[e] * up, y1 = v[2 + e] * up;
-                        for (int half = 0; half < (a.gated ? 1 : 2); ++half) {
-                            const int row = row0 + 8 * half;
-                            if (row >= a.n) continue;
-                            float y = a.gated ? y0 / (1.f + expf(-y0)) * y1 : half ? y1 : y0;
-                            if (a.bf16) {
-                                if (a.res) y += Elem<__nv_bfloat16>::load(static_cast<const __nv_bfloat16 *>(a.res) + x_row * a.res_row, row);
-                                Elem<__nv_bfloat16>::store(static_cast<__nv_bfloat16 *>(a.out) + x_row * a.out_row, row, y);
-                            } else {
-                                if (a.res) y += static_cast<const float *>(a.res)[x_row * a.res_row + row];
-                                static_cast<float *>(a.out)[x_row * a.out_row + row] = y;
-                            }
-                        }
-                    }
-                }
-                __syncthreads();
-            }
+                    if (r < from.tiles) place[(r * NT + i) * 32] = make_float4(total[r][i][0], total[r][i][1], total[r][i][2], total[r][i][3]);
+            fresh = true;
+        }
+        next(from);
+    }
+    pdl_launch_dependents();
+}
+
+// A CTA per row tile and pass: the segments' sums in their order, and the result. A thread adds up one number of a lane's four:
+// rows g (0, 1) and g + 8 (2, 3) of two columns.
+__global__ void __launch_bounds__(128) k_w4_join(const MatmulArgs a, int nt) {
+    const int pass = blockIdx.y, tile = blockIdx.x, span = tile / kSpan, of_warp = tile % kSpan, place = pass * a.spans + span, parts = a.c.parts;
+    const int j = threadIdx.x & 3, l = threadIdx.x >> 2, cols = min(a.c.cols, a.rows * parts - pass * a.c.cols);
+    const int c0 = a.steps.cta_of((long long)place * a.steps.units), c1 = a.steps.cta_of((long long)(place + 1) * a.steps.units - 1);
+    const int row = a.gated ? tile * 8 + (l >> 2) : tile * 16 + (l >> 2) + 8 * (j >> 1);
+    pdl_wait();
+    for (int i = 0; i < nt; ++i) {
+        const int col = i * 8 + 2 * (l & 3) + (j & 1);
+        const float *from = reinterpret_cast<const float *>(a.sums + ((((size_t)(c0 + place) * kWarps + of_warp / kTiles) * kTiles + of_warp % kTiles) * nt + i) * 32) + threadIdx.x;
+        float v = 0.f;
+#pragma unroll 4
+        for (int c = c0; c <= c1; ++c, from += (size_t)kSpan * nt * 128) v += *from;
+        if (parts == 2) v += __shfl_xor_sync(0xffffffffu, v, 1);
+        const int x_row = pass * a.c.cols / parts + col / parts;
+        float y = v * (col < cols ? a.back[x_row] : 0.f);
+        const float up = __shfl_xor_sync(0xffffffffu, y, 2);   // (U's row of a gated matrix)
+        if (a.gated) y = y / (1.f + expf(-y)) * up;
+        if (row >= a.n || col >= cols || (parts == 2 && j & 1) || (a.gated && j & 2)) continue;
+        if (a.bf16) {
+            if (a.res) y += Elem<__nv_bfloat16>::load(static_cast<const __nv_bfloat16 *>(a.res) + x_row * a.res_row, row);
+            Elem<__nv_bfloat16>::store(static_cast<__nv_bfloat16 *>(a.out) + x_row * a.out_row, row, y);
+        } else {
+            if (a.res) y += static_cast<const float *>(a.res)[x_row * a.res_row + row];
+            static_cast<float *>(a.out)[x_row * a.out_row + row] = y;
         }
     }
 }
 
-constexpr int kOwnRows = 4, kOwnValues = 16384;   // of x: up to so many the CTAs prepare themselves
-
 // How a call runs.
 struct Plan {
     Columns c;
-    int nt, k_parts, ctas, units_at_once, fixed;
+    Steps steps;
+    int nt, spans, x_bytes;
     bool own;
-    size_t back_at, partial_at, bytes;   // of the scratch
+    size_t shared, back_at, sums_at, bytes;   // (the last three: of the scratch)
 };
 Plan plan_of(const Sizes &s, int k, int x_dtype, int rows) {
     Plan p{};
@@ -538,27 +547,36 @@ Plan plan_of(const Sizes &s, int k, int x_dtype, int rows) {
     p.c.passes = (int)((col_tiles + 3) / 4);
     p.nt = (int)((col_tiles + p.c.passes - 1) / p.c.passes);
     p.c.cols = (int)std::min<long long>(columns, p.nt * 8);
-    const int rt = p.nt >= 3 ? 2 : 1;
-    p.fixed = fixed_bytes(p.nt, rt, s.record);
-    const int room = (kMostShared - p.fixed) / (p.c.cols * 256);   // units of x, 8 or more
-    p.own = rows <= kOwnRows && (long long)rows * k <= kOwnValues && s.units <= room;
-    const int blocks = (s.units + room - 1) / room;
-    p.units_at_once = (s.units + blocks - 1) / blocks;
-    // the fewest steps: rounds of tiles times a warp's units, and a round's end, which takes about as long as one
-    const int groups = (s.tiles + rt - 1) / rt;
-    p.ctas = std::min(groups, std::max(1, kMultiprocessors / std::min(p.c.passes, kMultiprocessors)));
-    long long best = 1ll << 62;
-    for (int k = 1; k <= kWarps; k *= 2) {
-        const long long rounds = (groups + (long long)p.ctas * (kWarps / k) - 1) / ((long long)p.ctas * (kWarps / k));
-        const long long cost = rounds * ((p.units_at_once + k - 1) / k + 1);
-        if (cost < best) best = cost, p.k_parts = k;
-    }
+    p.own = rows <= kOwnRows && (long long)rows * k <= kOwnValues;
+    p.x_bytes = p.c.cols * 256 * (p.own ? s.units : 1);
+    p.shared = (size_t)kSlots * (kSpan * s.record + (p.own ? 0 : p.x_bytes)) + (p.own ? p.x_bytes : 0);
+    p.spans = (s.tiles + kSpan - 1) / kSpan;
+    p.steps.units = s.units;
+    p.steps.all = (long long)p.c.passes * p.spans * s.units;
+    p.steps.ctas = (int)std::min<long long>(p.steps.all, kMultiprocessors);
     p.back_at = p.own ? 0 : (size_t)p.c.passes * s.units * 16 * p.c.cols * sizeof(uint4);
-    p.partial_at = p.own ? 0 : (p.back_at + (size_t)rows * 4 + 15) / 16 * 16;
-    p.bytes = p.partial_at + (blocks > 1 ? (size_t)p.c.passes * s.tiles * p.nt * 32 * sizeof(float4) : 0);
+    p.sums_at = (p.back_at + (size_t)rows * 4 + 15) / 16 * 16;
+    p.bytes = p.sums_at + ((size_t)p.c.passes * p.spans + p.steps.ctas - 1) * kSpan * p.nt * 32 * sizeof(float4);
     return p;
 }
+// The most shared memory that a plan asks for: four column tiles of x in the slots, or all of x as two parts of f32.
+static_assert(kSlots * (kSpan * (kUnitBytes + 4 * 48) + 32 * 256) <= kMostShared - 64, "slots");
+static_assert(kSlots * kSpan * (kUnitBytes + 4 * 48) + (kOwnValues + kOwnRows * kUnit) * 4 <= kMostShared - 64, "slots and x");
 
+template <typename... A>
+cudaError_t launch_after(void (*kernel)(A...), dim3 grid, int threads, size_t shared, bool after, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = shared;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = after ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 template <int NT, int NG>
 cudaError_t launch_one(const MatmulArgs &a, const Plan &p, cudaStream_t st) {
     static std::atomic<unsigned long long> raised{0};   // devices whose limit of shared memory is raised
@@ -566,33 +584,26 @@ cudaError_t launch_one(const MatmulArgs &a, const Plan &p, cudaStream_t st) {
     cudaError_t e = cudaGetDevice(&device);
     const unsigned long long bit = device < 64 ? 1ull << device : 0;
     if (e == cudaSuccess && !(raised.load() & bit)) {
-        e = cudaFuncSetAttribute(k_w4_matmul<NT, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
+        e = cudaFuncSetAttribute(k_w4_matmul<NT, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared - 64);
         if (e == cudaSuccess) raised |= bit;
     }
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3(p.ctas, p.c.passes);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = p.fixed + (size_t)p.units_at_once * p.c.cols * 256;
-    cfg.stream = st;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = p.own ? 0 : 1;
-    return cudaLaunchKernelEx(&cfg, k_w4_matmul<NT, NG>, a);
+    return launch_after(k_w4_matmul<NT, NG>, dim3(p.steps.ctas), kThreads, p.shared, !p.own, st, a);
 }
 template <int NT>
 cudaError_t launch_tiles(const MatmulArgs &a, const Plan &p, cudaStream_t st) {
     return a.s.groups == 1 ? launch_one<NT, 1>(a, p, st) : a.s.groups == 2 ? launch_one<NT, 2>(a, p, st) : launch_one<NT, 4>(a, p, st);
 }
 cudaError_t launch_matmul(const MatmulArgs &a, const Plan &p, char *scratch, cudaStream_t st) {
+    cudaError_t e = cudaSuccess;
     if (!p.own) {
-        k_w4_rows<<<a.rows, kRowThreads, 0, st>>>(a.x, reinterpret_cast<uint2 *>(scratch), reinterpret_cast<float *>(scratch + p.back_at), a.s.units, p.c);
-        const cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
+        k_w4_rows<<<a.rows, kRowThreads, 0, st>>>(a.x, reinterpret_cast<uint2 *>(scratch), a.back, a.s.units, p.c);
+        e = cudaGetLastError();
     }
-    return p.nt == 1 ? launch_tiles<1>(a, p, st) : p.nt == 2 ? launch_tiles<2>(a, p, st) : p.nt == 3 ? launch_tiles<3>(a, p, st) : launch_tiles<4>(a, p, st);
+    if (e == cudaSuccess)
+        e = p.nt == 1 ? launch_tiles<1>(a, p, st) : p.nt == 2 ? launch_tiles<2>(a, p, st) : p.nt == 3 ? launch_tiles<3>(a, p, st) : launch_tiles<4>(a, p, st);
+    if (e == cudaSuccess) e = launch_after(k_w4_join, dim3(a.s.tiles, p.c.passes), 128, 0, true, st, a, p.nt);
+    return e;
 }
 
 bool matrix_ok(const talker_w4 *w) {
@@ -659,16 +670,15 @@ talker_status talker_w4_matmul(const talker_w4 *w, const void *x, int x_dtype, i
     if (rows == 0) return TALKER_OK;
     const Sizes s = sizes_of(w);
     const Plan p = plan_of(s, w->k, x_dtype, rows);
-    if (p.bytes > 0 && (!scratch || scratch_bytes < p.bytes || !aligned(scratch, 16))) return TALKER_EINVAL;
+    if (!scratch || scratch_bytes < p.bytes || !aligned(scratch, 16)) return TALKER_EINVAL;
     char *base = static_cast<char *>(scratch);
     MatmulArgs a{};
-    a.tiles = static_cast<const unsigned char *>(w->tiles), a.s = s;
+    a.tiles = static_cast<const unsigned char *>(w->tiles), a.s = s, a.steps = p.steps;
     a.x = {x, x_scales, x_row, x_dtype, x_block, w->k, rows, aligned(x, 4 * size_of(x_dtype)) && (rows == 1 || x_row % 4 == 0)};
-    if (!p.own) a.frags = reinterpret_cast<const uint4 *>(base), a.back = reinterpret_cast<const float *>(base + p.back_at);
-    a.partial = reinterpret_cast<float4 *>(base + p.partial_at);
+    if (!p.own) a.frags = reinterpret_cast<const uint4 *>(base);
+    a.back = reinterpret_cast<float *>(base + p.back_at), a.sums = reinterpret_cast<float4 *>(base + p.sums_at);
     a.res = residual, a.out = out, a.res_row = res_row, a.out_row = out_row;
-    a.n = w->n, a.rows = rows, a.c = p.c;
-    a.k_parts = p.k_parts, a.units_at_once = p.units_at_once, a.fixed = p.fixed;
+    a.n = w->n, a.spans = p.spans, a.c = p.c, a.rows = rows, a.x_bytes = p.x_bytes;
     a.zeros = w->zeros != 0, a.gated = w->gated != 0, a.bf16 = out_dtype == TALKER_DTYPE_BF16;
     const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
     const cudaError_t e = launch_matmul(a, p, base, st);

@@ -104,8 +104,8 @@ def test_w4_refusals(lib):
     for kw in (dict(codes2=None), dict(scales2=None), dict(scales2=321), dict(zeros2=None)):
         assert pack(matrix(gated=1), **kw) == 1, kw
     assert matmul(good, rows=0) == 0
-    for kw in (dict(x=None), dict(x=66), dict(xt=2), dict(xt=3), dict(xt=4), dict(xt=4, xs=130), dict(xt=4, xs=128, block=16), dict(rows=-1), dict(rows=(1 << 19) + 1),
-               dict(out=None), dict(out=513), dict(ot=4), dict(out_row=32), dict(res=514), dict(res=512, res_row=40), dict(rows=999, need=1), dict(rows=999, scratch=1032), dict(rows=999, scratch=None)):
+    for kw in (dict(x=None), dict(x=66), dict(xt=2), dict(xt=3), dict(xt=4), dict(xt=4, xs=130), dict(xt=4, xs=128, block=16), dict(rows=-1), dict(rows=(1 << 16) + 1),
+               dict(out=None), dict(out=513), dict(ot=4), dict(out_row=32), dict(res=514), dict(res=512, res_row=40), dict(need=1), dict(scratch=1032), dict(scratch=None)):
         assert matmul(good, **kw) == 1, kw
 
     def quantize(w=64, dtype=0, stride=130, n=4, k=130, group=32, codes=128, scales=256):
