@@ -15,8 +15,8 @@ constexpr int kUnit = 128;              // inputs: what k is padded to, and what
 constexpr int kUnitBytes = 16 * kUnit / 2;
 constexpr int kMostRows = 1 << 16;
 
-constexpr int kWarps = 16, kThreads = kWarps * 32;
-constexpr int kTiles = 2;               // of a warp
+constexpr int kWarps = 16, kThreads = (kWarps + 1) * 32;   // that multiply; one more makes the copies
+constexpr int kTiles = 2;               // of a warp: one fragment of x, and one turn of the loop, serve both
 constexpr int kSpan = kWarps * kTiles;  // row tiles of a CTA
 
 struct Sizes {
@@ -286,9 +286,6 @@ __device__ __forceinline__ uint32_t centred16(uint32_t v, Zero z) {
         : "=r"(y) : "r"(v), "r"(z.b));
     return y;
 }
-__device__ __forceinline__ void copy16(uint32_t to, const void *from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-}
 // (In their place: what they read arrives by copies that the compiler does not see.)
 __device__ __forceinline__ uint4 read16(uint32_t at) {
     uint4 v;
@@ -307,7 +304,7 @@ __device__ __forceinline__ uint32_t read2(uint32_t at) {
 }
 
 constexpr int kMultiprocessors = 152, kMostShared = 227 * 1024;
-constexpr int kDepth = 3, kSlots = kDepth + 1;   // steps whose copies are on their way: 100 KB a multiprocessor
+constexpr int kSlots = 4;                        // steps on their way or at hand: 135 KB a multiprocessor
 constexpr int kOwnRows = 4, kOwnValues = 16384;  // of x: up to so many the CTAs prepare themselves
 
 // A product is `steps` steps, in the order of passes, spans and units: a step is a unit of all tiles of a span for a pass's columns. CTA
@@ -336,108 +333,118 @@ struct MatmulArgs {
     bool zeros, gated, bf16;
 };
 
-// One CTA a multiprocessor, all with the same number of steps, in a ring of asynchronous copies: each warp's two records of the step, and the step's
-// fragments of x (where the CTAs do not prepare x themselves and keep all of it). Nothing is joined in here: a segment's sums go
-// to memory, and the kernel after adds them up. A group of inputs' sum is added to the total times its scale.
+// The phase of `parity` of a barrier, waited for up to a second: false if it did not come.
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
+    return true;
+}
+
+// One CTA a multiprocessor, all with the same number of steps. A thread of its own brings each step into a ring of slots by two
+// bulk copies: a span's records of a unit lie together, and so do its fragments of x (where the CTAs do not prepare x
+// themselves and keep all of it). Warps run on their own, up to a ring's length apart. Nothing is joined in here: a segment's
+// sums go to memory, and the kernel after adds them up. A group of inputs' sum is added to the total times its
+// scale. A copy that does not arrive within a second makes its warps' sums NaN from there on.
 template <int NT, int NG>
 __global__ void __launch_bounds__(kThreads, 1) k_w4_matmul(const MatmulArgs a) {
     extern __shared__ uint4 smem[];
-    __shared__ float red[kWarps];
+    __shared__ uint64_t full[kSlots], empty[kSlots];
+    __shared__ float red[kThreads / 32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int units = a.s.units, record = a.s.record, parts = a.c.parts;
     const bool own = a.frags == nullptr;
     const int slot_bytes = kSpan * record + (own ? 0 : a.x_bytes);
-    const uint32_t slots = smem_u32(smem) + (own ? a.x_bytes : 0), slots_end = slots + kSlots * slot_bytes;
-    const uint32_t mine = warp * kTiles * record + lane * 16;   // in a slot
-    const bool extra = lane < (record - kUnitBytes) / 16;
+    const uint32_t slots = smem_u32(smem) + (own ? a.x_bytes : 0);
     const long long first = a.steps.start(blockIdx.x);
     const int count = (int)(a.steps.start(blockIdx.x + 1) - first);
-
-    // where a step is: place = pass * spans + span
+    // where a step is: place = pass * spans + span, of the unit's tiles of_span there
     struct At {
-        int place, unit, tiles, cols;     // tiles of this warp: 0 to 2
-        const unsigned char *codes;       // this lane's of the warp's first tile
-        const uint4 *x;
-        int stride;                       // to the next unit's codes
+        int place, unit, pass, span, of_span;
     };
-    auto enter = [&](At &p) {   // a place, at p.unit
-        const int pass = p.place / a.spans, span = p.place - pass * a.spans, of_span = min(a.s.tiles - span * kSpan, kSpan);
-        p.tiles = min(max(of_span - warp * kTiles, 0), kTiles);
-        p.cols = min(a.c.cols, a.rows * parts - pass * a.c.cols);
-        p.stride = of_span * record;
-        p.codes = a.tiles + ((size_t)span * kSpan * units + (size_t)p.unit * of_span + warp * kTiles) * record + lane * 16;
-        p.x = a.frags + ((size_t)pass * units + p.unit) * 16 * a.c.cols;
+    auto enter = [&](At &p) {
+        p.pass = p.place / a.spans, p.span = p.place - p.pass * a.spans;
+        p.of_span = min(a.s.tiles - p.span * kSpan, kSpan);
     };
     auto next = [&](At &p) {
-        p.codes += p.stride;
-        p.x += 16 * a.c.cols;
-        if (++p.unit == units) {
-            p.unit = 0, ++p.place;
-            enter(p);
-        }
+        if (++p.unit < units) return;
+        p.unit = 0, ++p.place;
+        enter(p);
     };
-    At to;
-    to.place = (int)(first / units), to.unit = (int)(first - (long long)to.place * units);
-    enter(to);
-    At from = to;
-    auto copy_codes = [&](const At &p, uint32_t slot) {
-        if (p.tiles > 0) {
-            copy16(slot + mine, p.codes);
-            copy16(slot + mine + 512, p.codes + 512);
-            if (extra) copy16(slot + mine + 1024, p.codes + 1024);
-        }
-        if (p.tiles > 1) {
-            copy16(slot + mine + record, p.codes + record);
-            copy16(slot + mine + record + 512, p.codes + record + 512);
-            if (extra) copy16(slot + mine + record + 1024, p.codes + record + 1024);
-        }
+    At at;
+    at.place = (int)(first / units), at.unit = (int)(first - (long long)at.place * units);
+    enter(at);
+    auto copy_codes = [&](const At &p, int slot) {
+        const uint32_t bytes = p.of_span * record;
+        mbar_arrive_expect_tx(&full[slot], bytes + (own ? 0 : a.x_bytes));
+        bulk_g2s(reinterpret_cast<char *>(smem) + (slots - smem_u32(smem)) + slot * slot_bytes,
+                 a.tiles + ((size_t)p.span * kSpan * units + (size_t)p.unit * p.of_span) * record, bytes, &full[slot]);
     };
-    auto copy_x = [&](const At &p, uint32_t slot) {   // (also columns past the last pass's: they are not looked at)
-        if (!own && tid < 16 * a.c.cols) copy16(slot + kSpan * record + tid * 16, p.x + tid);
+    auto copy_x = [&](const At &p, int slot) {   // (also columns past the last pass's: they are not looked at)
+        if (!own)
+            bulk_g2s(reinterpret_cast<char *>(smem) + slot * slot_bytes + kSpan * record, a.frags + ((size_t)p.pass * units + p.unit) * 16 * a.c.cols,
+                     a.x_bytes, &full[slot]);
     };
-    // codes do not wait for the kernel before, x does
-    At ahead = to;
-    uint32_t slot = slots;
-    for (int i = 0; i < min(kDepth, count); ++i, next(ahead), slot += slot_bytes) copy_codes(ahead, slot);
-    if (own) {
-        prepare_rows(a.x, 0, a.rows, reinterpret_cast<uint2 *>(smem), a.c.cols, 0, units, a.back, red);   // (the same in every CTA)
-    } else {
-        pdl_wait();
-        slot = slots;
-        for (int i = 0; i < min(kDepth, count); ++i, next(to), slot += slot_bytes) copy_x(to, slot);
+    At ahead = at;
+    if (tid == kWarps * 32) {
+        for (int i = 0; i < kSlots; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], kWarps);
+        fence_barrier_init();
+        fence_proxy_async();
+        // codes do not wait for the kernel before, x does
+        for (int i = 0; i < min(kSlots, count); ++i, next(ahead)) copy_codes(ahead, i);
     }
-    to = ahead;
-#pragma unroll
-    for (int i = 0; i < kDepth; ++i) asm volatile("cp.async.commit_group;" ::: "memory");   // (the first has them all)
-    uint32_t now = slots;
-    slot = slots + kDepth * slot_bytes;
+    __syncthreads();
+    if (own) prepare_rows(a.x, 0, a.rows, reinterpret_cast<uint2 *>(smem), a.c.cols, 0, units, a.back, red);   // (the same in every CTA)
+    __syncthreads();
+    if (warp == kWarps) {
+        if (lane != 0) return;
+        if (!own) {
+            pdl_wait();
+            At x = at;
+            for (int i = 0; i < min(kSlots, count); ++i, next(x)) copy_x(x, i);
+        }
+        int i = kSlots;
+        for (; i < count; ++i, next(ahead)) {
+            if (!wait_for(&empty[i % kSlots], (i / kSlots - 1) & 1)) break;
+            copy_codes(ahead, i % kSlots);
+            copy_x(ahead, i % kSlots);
+        }
+        for (int k = max(0, min(i, count) - kSlots); k < min(i, count); ++k) wait_for(&full[k % kSlots], k / kSlots & 1);   // (nothing is on its way when the CTA ends)
+        return;
+    }
 
+    const uint32_t mine = warp * kTiles * record + lane * 16;   // in a slot
+    bool lost = false;
     float total[kTiles][NT][4];
     bool fresh = true;
     int from_col[NT];
     for (int step = 0; step < count; ++step) {
+        const int slot = step % kSlots, tiles = at.of_span - warp * kTiles;   // tiles of this warp
         if (fresh) {
             fresh = false;
+            const int cols = min(a.c.cols, a.rows * parts - at.pass * a.c.cols);
 #pragma unroll
             for (int r = 0; r < kTiles; ++r)
 #pragma unroll
                 for (int i = 0; i < NT; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) total[r][i][j] = 0.f;
+                    for (int j = 0; j < 4; ++j) total[r][i][j] = lost ? NAN : 0.f;
 #pragma unroll
-            for (int i = 0; i < NT; ++i) from_col[i] = (min(i * 8 + g, from.cols - 1) * 4 + t) * 16;   // (columns past the last are not looked at)
+            for (int i = 0; i < NT; ++i) from_col[i] = (min(i * 8 + g, cols - 1) * 4 + t) * 16;   // (columns past the last are not looked at)
         }
-        asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
-        __syncthreads();   // (others' copies too; and the slot before this one has been read by all)
-        if (step + kDepth < count) {
-            copy_codes(to, slot);
-            copy_x(to, slot);
-            next(to);
+        if (!lost && !wait_for(&full[slot], step / kSlots & 1)) {
+            lost = true;
+#pragma unroll
+            for (int r = 0; r < kTiles; ++r)
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) total[r][i][j] = NAN;
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        slot = slot + slot_bytes == slots_end ? slots : slot + slot_bytes;
-        if (from.tiles > 0) {
-            const uint32_t x = own ? smem_u32(smem) + from.unit * 256 * a.c.cols : now + kSpan * record;
+        if (tiles > 0 && !lost) {
+            const uint32_t now = slots + slot * slot_bytes;
+            const uint32_t x = own ? smem_u32(smem) + at.unit * 256 * a.c.cols : now + kSpan * record;
             const uint32_t tail = now + mine - lane * 16 + kUnitBytes;   // scales, then zeros
             uint4 w[kTiles][2];
 #pragma unroll
@@ -487,17 +494,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_matmul(const MatmulArgs a) {
                 }
             }
         }
-        now = now + slot_bytes == slots_end ? slots : now + slot_bytes;
-        if (step + 1 == count || from.unit + 1 == units) {   // the segment's end
-            float4 *place = a.sums + ((size_t)(blockIdx.x + from.place) * kWarps + warp) * kTiles * NT * 32 + lane;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[slot]);   // (all of it has been read)
+        if (step + 1 == count || at.unit + 1 == units) {   // the segment's end
+            float4 *place = a.sums + ((size_t)(blockIdx.x + at.place) * kWarps + warp) * kTiles * NT * 32 + lane;
 #pragma unroll
             for (int r = 0; r < kTiles; ++r)
 #pragma unroll
                 for (int i = 0; i < NT; ++i)
-                    if (r < from.tiles) place[(r * NT + i) * 32] = make_float4(total[r][i][0], total[r][i][1], total[r][i][2], total[r][i][3]);
+                    if (r < tiles) place[(r * NT + i) * 32] = make_float4(total[r][i][0], total[r][i][1], total[r][i][2], total[r][i][3]);
             fresh = true;
         }
-        next(from);
+        next(at);
     }
     pdl_launch_dependents();
 }
@@ -560,8 +568,8 @@ Plan plan_of(const Sizes &s, int k, int x_dtype, int rows) {
     return p;
 }
 // The most shared memory that a plan asks for: four column tiles of x in the slots, or all of x as two parts of f32.
-static_assert(kSlots * (kSpan * (kUnitBytes + 4 * 48) + 32 * 256) <= kMostShared - 64, "slots");
-static_assert(kSlots * kSpan * (kUnitBytes + 4 * 48) + (kOwnValues + kOwnRows * kUnit) * 4 <= kMostShared - 64, "slots and x");
+static_assert(kSlots * (kSpan * (kUnitBytes + 4 * 48) + 32 * 256) <= kMostShared - 256, "slots");
+static_assert(kSlots * kSpan * (kUnitBytes + 4 * 48) + (kOwnValues + kOwnRows * kUnit) * 4 <= kMostShared - 256, "slots and x");
 
 template <typename... A>
 cudaError_t launch_after(void (*kernel)(A...), dim3 grid, int threads, size_t shared, bool after, cudaStream_t st, A... args) {
@@ -584,7 +592,7 @@ cudaError_t launch_one(const MatmulArgs &a, const Plan &p, cudaStream_t st) {
     cudaError_t e = cudaGetDevice(&device);
     const unsigned long long bit = device < 64 ? 1ull << device : 0;
     if (e == cudaSuccess && !(raised.load() & bit)) {
-        e = cudaFuncSetAttribute(k_w4_matmul<NT, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared - 64);
+        e = cudaFuncSetAttribute(k_w4_matmul<NT, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared - 256);
         if (e == cudaSuccess) raised |= bit;
     }
     if (e != cudaSuccess) return e;
