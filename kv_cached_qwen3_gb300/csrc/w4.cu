@@ -176,49 +176,55 @@ __device__ __forceinline__ void load_x4<__nv_fp8_storage_t>(const XArgs &a, int 
     for (int i = 0; i < 4; ++i) v[i] = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)(u >> (8 * i)), __NV_E4M3))) * d;
 }
 
-// Rows first .. first + rows - 1 (at most as many as warps) by the CTA, each by as many warps as there are for it: their columns to frags
-// (of `cols` columns, the first row's at `col`), and what undoes the scaling to back. red: a float for each warp.
+// How the columns of all rows are taken: in `passes` over the weights, `cols` columns each (the last may have fewer).
+struct Columns {
+    int passes, cols, parts;   // parts: columns of a row
+};
+
+// A CTA per row: its columns to frags, and what undoes the scaling to back. A row's values are read once where eight quads a thread
+// hold them (k <= 16384). The product's CTAs may begin at once: they bring weights in until they need this.
+constexpr int kRowThreads = 512, kHeld = 8;
 template <typename T, int PARTS>
-__device__ __forceinline__ void prepare_rows(const XArgs &a, int first, int rows, uint2 *frags, int cols, int col, int units, float *back, float *red) {
-    const int tid = threadIdx.x, warps = blockDim.x >> 5, warp = tid >> 5;
-    int each = warps;
-    while (each * rows > warps) each >>= 1;
-    const int own = warp / each, lane = tid - own * each * 32, step = 4 * 32 * each;
-    const bool busy = own < rows;
-    const int r = first + own;
+__device__ __forceinline__ void prepare_row(const XArgs &a, int r, uint2 *frags, int cols, int col, int units, float *back) {
+    __shared__ float red[kRowThreads / 32];
+    const int tid = threadIdx.x;
+    float held[kHeld][4];
     float most = 0.f;
     bool bad = false;
-    if (busy) {
-#pragma unroll 4
-        for (int k = 4 * lane; k < a.k; k += step) {
-            float v[4];
-            load_x4<T>(a, r, k, v);
+    auto see = [&](const float (&v)[4]) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                bad |= !(fabsf(v[i]) < INFINITY);
-                most = fmaxf(most, fabsf(v[i]));
-            }
+        for (int i = 0; i < 4; ++i) {
+            bad |= !(fabsf(v[i]) < INFINITY);
+            most = fmaxf(most, fabsf(v[i]));
         }
+    };
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+        const int k = 4 * (tid + j * kRowThreads);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) held[j][i] = 0.f;
+        if (k < a.k) load_x4<T>(a, r, k, held[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) see(held[j]);
+    for (int k = 4 * (tid + kHeld * kRowThreads); k < a.k; k += 4 * kRowThreads) {
+        float v[4];
+        load_x4<T>(a, r, k, v);
+        see(v);
     }
     most = warp_max(most);
-    bad = __any_sync(0xffffffffu, bad);
-    if ((tid & 31) == 0) red[warp] = bad ? INFINITY : most;
-    __syncthreads();
-    if (!busy) return;
-    for (int i = 0; i < each; ++i) most = fmaxf(most, red[own * each + i]);
-    bad = most == INFINITY;
+    if ((tid & 31) == 0) red[tid >> 5] = most;
+    bad = __syncthreads_or(bad);
+    most = warp_max(red[tid & 15]);
     int e = most > 0.f && !bad ? ilogbf(most) : 0;     // 2^e <= most
     e = min(max(14 - e, -113), 120);
     const float up = ldexpf(1.f, e);                   // (most below 2^-106 keeps fewer bits)
-    if (lane == 0) back[own] = bad ? NAN : ldexpf(1.f, -e);
-#pragma unroll 4
-    for (int k = 4 * lane; k < units * kUnit; k += step) {
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        if (k < a.k && !bad) load_x4<T>(a, r, k, v);
+    if (tid == 0) *back = bad ? NAN : ldexpf(1.f, -e);
+    auto store = [&](int k, const float (&v)[4]) {
         uint32_t h[PARTS][2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const float v0 = v[2 * i] * up, v1 = v[2 * i + 1] * up;
+            const float v0 = bad ? 0.f : v[2 * i] * up, v1 = bad ? 0.f : v[2 * i + 1] * up;
             const __half2 near = __floats2half2_rn(v0, v1);
             h[0][i] = *reinterpret_cast<const uint32_t *>(&near);
             if (PARTS == 2) {
@@ -228,27 +234,26 @@ __device__ __forceinline__ void prepare_rows(const XArgs &a, int first, int rows
         }
         const int quarter = k / 32, s = k % 32 / 16, t = k % 16 / 4;
 #pragma unroll
-        for (int p = 0; p < PARTS; ++p) frags[((quarter * cols + col + own * PARTS + p) * 4 + t) * 2 + s] = make_uint2(h[p][0], h[p][1]);
+        for (int p = 0; p < PARTS; ++p) frags[((quarter * cols + col + p) * 4 + t) * 2 + s] = make_uint2(h[p][0], h[p][1]);
+    };
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+        const int k = 4 * (tid + j * kRowThreads);
+        if (k < units * kUnit) store(k, held[j]);
+    }
+    for (int k = 4 * (tid + kHeld * kRowThreads); k < units * kUnit; k += 4 * kRowThreads) {
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (k < a.k) load_x4<T>(a, r, k, v);
+        store(k, v);
     }
 }
-__device__ __noinline__ void prepare_rows(const XArgs &a, int first, int rows, uint2 *frags, int cols, int col, int units, float *back, float *red) {
-    if (a.dtype == TALKER_DTYPE_BF16) prepare_rows<__nv_bfloat16, 1>(a, first, rows, frags, cols, col, units, back, red);
-    else if (a.dtype == TALKER_DTYPE_F32) prepare_rows<float, 2>(a, first, rows, frags, cols, col, units, back, red);
-    else prepare_rows<__nv_fp8_storage_t, 2>(a, first, rows, frags, cols, col, units, back, red);
-}
-
-// How the columns of all rows are taken: in `passes` over the weights, `cols` columns each (the last may have fewer).
-struct Columns {
-    int passes, cols, parts;   // parts: columns of a row
-};
-
-// A CTA per row, for calls whose own CTAs would take too long over it.
-constexpr int kRowThreads = 512;
 __global__ void __launch_bounds__(kRowThreads) k_w4_rows(const XArgs a, uint2 *frags, float *back, int units, const Columns c) {
-    __shared__ float red[kRowThreads / 32];
-    const int r = blockIdx.x, pass = r * c.parts / c.cols, col = r * c.parts % c.cols;
-    prepare_rows(a, r, 1, frags + (size_t)pass * units * 4 * c.cols * 8, c.cols, col, units, back + r, red);
     pdl_launch_dependents();
+    const int r = blockIdx.x, pass = r * c.parts / c.cols, col = r * c.parts % c.cols;
+    frags += (size_t)pass * units * 4 * c.cols * 8;
+    if (a.dtype == TALKER_DTYPE_BF16) prepare_row<__nv_bfloat16, 1>(a, r, frags, c.cols, col, units, back + r);
+    else if (a.dtype == TALKER_DTYPE_F32) prepare_row<float, 2>(a, r, frags, c.cols, col, units, back + r);
+    else prepare_row<__nv_fp8_storage_t, 2>(a, r, frags, c.cols, col, units, back + r);
 }
 
 // ---- the product
@@ -305,7 +310,6 @@ __device__ __forceinline__ uint32_t read2(uint32_t at) {
 
 constexpr int kMultiprocessors = 152, kMostShared = 227 * 1024;
 constexpr int kSlots = 4;                        // steps on their way or at hand: 135 KB a multiprocessor
-constexpr int kOwnRows = 4, kOwnValues = 16384;  // of x: up to so many the CTAs prepare themselves
 
 // A product is `steps` steps, in the order of passes, spans and units: a step is a unit of all tiles of a span for a pass's columns. CTA
 // c takes the steps from start(c) to start(c + 1), so all have the same number, give or take one. A stretch of steps of one
@@ -321,15 +325,15 @@ struct MatmulArgs {
     Sizes s;
     Steps steps;
     XArgs x;
-    const uint4 *frags;       // null: the CTAs prepare the rows themselves
-    float *back;              // [row]: what undoes the rows' scaling
+    const uint4 *frags;
+    const float *back;              // [row]: what undoes the rows' scaling
     float4 *sums;             // [place][warp][tile][column tile][lane]
     const void *res;
     void *out;
     long long res_row, out_row;
     int n, spans;
     Columns c;
-    int rows, x_bytes;        // of x in a slot, or of all of x
+    int rows, x_bytes;        // of x in a slot
     bool zeros, gated, bf16;
 };
 
@@ -343,20 +347,17 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity) {
 }
 
 // One CTA a multiprocessor, all with the same number of steps. A thread of its own brings each step into a ring of slots by two
-// bulk copies: a span's records of a unit lie together, and so do its fragments of x (where the CTAs do not prepare x
-// themselves and keep all of it). Warps run on their own, up to a ring's length apart. Nothing is joined in here: a segment's
+// bulk copies: a span's records of a unit lie together, and so do its fragments of x. Warps run on their own, up to a ring's length apart. Nothing is joined in here: a segment's
 // sums go to memory, and the kernel after adds them up. A group of inputs' sum is added to the total times its
 // scale. A copy that does not arrive within a second makes its warps' sums NaN from there on.
 template <int NT, int NG>
 __global__ void __launch_bounds__(kThreads, 1) k_w4_matmul(const MatmulArgs a) {
     extern __shared__ uint4 smem[];
     __shared__ uint64_t full[kSlots], empty[kSlots];
-    __shared__ float red[kThreads / 32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int units = a.s.units, record = a.s.record, parts = a.c.parts;
-    const bool own = a.frags == nullptr;
-    const int slot_bytes = kSpan * record + (own ? 0 : a.x_bytes);
-    const uint32_t slots = smem_u32(smem) + (own ? a.x_bytes : 0);
+    const int slot_bytes = kSpan * record + a.x_bytes;
+    const uint32_t slots = smem_u32(smem);
     const long long first = a.steps.start(blockIdx.x);
     const int count = (int)(a.steps.start(blockIdx.x + 1) - first);
     // where a step is: place = pass * spans + span, of the unit's tiles of_span there
@@ -377,14 +378,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_matmul(const MatmulArgs a) {
     enter(at);
     auto copy_codes = [&](const At &p, int slot) {
         const uint32_t bytes = p.of_span * record;
-        mbar_arrive_expect_tx(&full[slot], bytes + (own ? 0 : a.x_bytes));
-        bulk_g2s(reinterpret_cast<char *>(smem) + (slots - smem_u32(smem)) + slot * slot_bytes,
-                 a.tiles + ((size_t)p.span * kSpan * units + (size_t)p.unit * p.of_span) * record, bytes, &full[slot]);
+        mbar_arrive_expect_tx(&full[slot], bytes + a.x_bytes);
+        bulk_g2s(reinterpret_cast<char *>(smem) + slot * slot_bytes, a.tiles + ((size_t)p.span * kSpan * units + (size_t)p.unit * p.of_span) * record, bytes, &full[slot]);
     };
     auto copy_x = [&](const At &p, int slot) {   // (also columns past the last pass's: they are not looked at)
-        if (!own)
-            bulk_g2s(reinterpret_cast<char *>(smem) + slot * slot_bytes + kSpan * record, a.frags + ((size_t)p.pass * units + p.unit) * 16 * a.c.cols,
-                     a.x_bytes, &full[slot]);
+        bulk_g2s(reinterpret_cast<char *>(smem) + slot * slot_bytes + kSpan * record, a.frags + ((size_t)p.pass * units + p.unit) * 16 * a.c.cols,
+                 a.x_bytes, &full[slot]);
     };
     At ahead = at;
     if (tid == kWarps * 32) {
@@ -395,15 +394,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_matmul(const MatmulArgs a) {
         for (int i = 0; i < min(kSlots, count); ++i, next(ahead)) copy_codes(ahead, i);
     }
     __syncthreads();
-    if (own) prepare_rows(a.x, 0, a.rows, reinterpret_cast<uint2 *>(smem), a.c.cols, 0, units, a.back, red);   // (the same in every CTA)
-    __syncthreads();
     if (warp == kWarps) {
         if (lane != 0) return;
-        if (!own) {
-            pdl_wait();
-            At x = at;
-            for (int i = 0; i < min(kSlots, count); ++i, next(x)) copy_x(x, i);
-        }
+        pdl_wait();
+        At x = at;
+        for (int i = 0; i < min(kSlots, count); ++i, next(x)) copy_x(x, i);
         int i = kSlots;
         for (; i < count; ++i, next(ahead)) {
             if (!wait_for(&empty[i % kSlots], (i / kSlots - 1) & 1)) break;
@@ -444,8 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_matmul(const MatmulArgs a) {
         }
         if (tiles > 0 && !lost) {
             const uint32_t now = slots + slot * slot_bytes;
-            const uint32_t x = own ? smem_u32(smem) + at.unit * 256 * a.c.cols : now + kSpan * record;
-            const uint32_t tail = now + mine - lane * 16 + kUnitBytes;   // scales, then zeros
+            const uint32_t x = now + kSpan * record, tail = now + mine - lane * 16 + kUnitBytes;   // scales, then zeros
             uint4 w[kTiles][2];
 #pragma unroll
             for (int r = 0; r < kTiles; ++r) w[r][0] = read16(now + mine + r * record), w[r][1] = read16(now + mine + r * record + 512);
@@ -511,19 +505,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_matmul(const MatmulArgs a) {
 }
 
 // A CTA per row tile and pass: the segments' sums in their order, and the result. A thread adds up one number of a lane's four:
-// rows g (0, 1) and g + 8 (2, 3) of two columns.
-__global__ void __launch_bounds__(128) k_w4_join(const MatmulArgs a, int nt) {
+// rows g (0, 1) and g + 8 (2, 3) of two columns. Where there are many segments, groups of 128 threads take a range each.
+__global__ void __launch_bounds__(1024) k_w4_join(const MatmulArgs a, int nt) {
+    __shared__ float sums[7 * 128];
     const int pass = blockIdx.y, tile = blockIdx.x, span = tile / kSpan, of_warp = tile % kSpan, place = pass * a.spans + span, parts = a.c.parts;
-    const int j = threadIdx.x & 3, l = threadIdx.x >> 2, cols = min(a.c.cols, a.rows * parts - pass * a.c.cols);
-    const int c0 = a.steps.cta_of((long long)place * a.steps.units), c1 = a.steps.cta_of((long long)(place + 1) * a.steps.units - 1);
+    const int id = threadIdx.x & 127, j = id & 3, l = id >> 2, own = threadIdx.x >> 7, ranges = blockDim.x >> 7;
+    const int cols = min(a.c.cols, a.rows * parts - pass * a.c.cols);
+    const int c0 = a.steps.cta_of((long long)place * a.steps.units), all = a.steps.cta_of((long long)(place + 1) * a.steps.units - 1) + 1 - c0;
+    const int from = all * own / ranges, to = all * (own + 1) / ranges;
     const int row = a.gated ? tile * 8 + (l >> 2) : tile * 16 + (l >> 2) + 8 * (j >> 1);
+    const size_t segment = (size_t)kSpan * nt * 128;
+    const float *at = reinterpret_cast<const float *>(a.sums) + (size_t)(c0 + place + from) * segment + (size_t)of_warp * nt * 128 + id;
     pdl_wait();
-    for (int i = 0; i < nt; ++i) {
+    for (int i = 0; i < nt; ++i, at += 128) {
         const int col = i * 8 + 2 * (l & 3) + (j & 1);
-        const float *from = reinterpret_cast<const float *>(a.sums + ((((size_t)(c0 + place) * kWarps + of_warp / kTiles) * kTiles + of_warp % kTiles) * nt + i) * 32) + threadIdx.x;
         float v = 0.f;
-#pragma unroll 4
-        for (int c = c0; c <= c1; ++c, from += (size_t)kSpan * nt * 128) v += *from;
+#pragma unroll 8
+        for (int c = 0; c < to - from; ++c) v += at[c * segment];
+        if (ranges > 1) {
+            __syncthreads();
+            if (own > 0) sums[(own - 1) * 128 + id] = v;
+            __syncthreads();
+            if (own > 0) continue;
+            for (int k = 1; k < ranges; ++k) v += sums[(k - 1) * 128 + id];
+        }
         if (parts == 2) v += __shfl_xor_sync(0xffffffffu, v, 1);
         const int x_row = pass * a.c.cols / parts + col / parts;
         float y = v * (col < cols ? a.back[x_row] : 0.f);
@@ -544,35 +549,35 @@ __global__ void __launch_bounds__(128) k_w4_join(const MatmulArgs a, int nt) {
 struct Plan {
     Columns c;
     Steps steps;
-    int nt, spans, x_bytes;
-    bool own;
+    int nt, spans, x_bytes, join_threads;
     size_t shared, back_at, sums_at, bytes;   // (the last three: of the scratch)
 };
-Plan plan_of(const Sizes &s, int k, int x_dtype, int rows) {
+Plan plan_of(const Sizes &s, int x_dtype, int rows) {
     Plan p{};
     p.c.parts = x_dtype == TALKER_DTYPE_BF16 ? 1 : 2;
     const long long columns = (long long)rows * p.c.parts, col_tiles = (columns + 7) / 8;
     p.c.passes = (int)((col_tiles + 3) / 4);
     p.nt = (int)((col_tiles + p.c.passes - 1) / p.c.passes);
     p.c.cols = (int)std::min<long long>(columns, p.nt * 8);
-    p.own = rows <= kOwnRows && (long long)rows * k <= kOwnValues;
-    p.x_bytes = p.c.cols * 256 * (p.own ? s.units : 1);
-    p.shared = (size_t)kSlots * (kSpan * s.record + (p.own ? 0 : p.x_bytes)) + (p.own ? p.x_bytes : 0);
+    p.x_bytes = p.c.cols * 256;
+    p.shared = (size_t)kSlots * (kSpan * s.record + p.x_bytes);
     p.spans = (s.tiles + kSpan - 1) / kSpan;
     p.steps.units = s.units;
     p.steps.all = (long long)p.c.passes * p.spans * s.units;
     p.steps.ctas = (int)std::min<long long>(p.steps.all, kMultiprocessors);
-    p.back_at = p.own ? 0 : (size_t)p.c.passes * s.units * 16 * p.c.cols * sizeof(uint4);
+    const long long segments = (s.units * (long long)p.steps.ctas + p.steps.all - 1) / p.steps.all;   // of a place, about
+    p.join_threads = segments <= 8 ? 128 : segments <= 16 ? 256 : segments <= 32 ? 512 : 1024;
+    p.back_at = (size_t)p.c.passes * s.units * 16 * p.c.cols * sizeof(uint4);
     p.sums_at = (p.back_at + (size_t)rows * 4 + 15) / 16 * 16;
     p.bytes = p.sums_at + ((size_t)p.c.passes * p.spans + p.steps.ctas - 1) * kSpan * p.nt * 32 * sizeof(float4);
     return p;
 }
-// The most shared memory that a plan asks for: four column tiles of x in the slots, or all of x as two parts of f32.
+// The most shared memory that a plan asks for.
 static_assert(kSlots * (kSpan * (kUnitBytes + 4 * 48) + 32 * 256) <= kMostShared - 256, "slots");
-static_assert(kSlots * kSpan * (kUnitBytes + 4 * 48) + (kOwnValues + kOwnRows * kUnit) * 4 <= kMostShared - 256, "slots and x");
 
+// After the kernel before it on the stream, of this call: it may begin earlier and waits for what it needs.
 template <typename... A>
-cudaError_t launch_after(void (*kernel)(A...), dim3 grid, int threads, size_t shared, bool after, cudaStream_t st, A... args) {
+cudaError_t launch_after(void (*kernel)(A...), dim3 grid, int threads, size_t shared, cudaStream_t st, A... args) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = grid;
@@ -582,7 +587,7 @@ cudaError_t launch_after(void (*kernel)(A...), dim3 grid, int threads, size_t sh
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = after ? 1 : 0;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 template <int NT, int NG>
@@ -596,21 +601,18 @@ cudaError_t launch_one(const MatmulArgs &a, const Plan &p, cudaStream_t st) {
         if (e == cudaSuccess) raised |= bit;
     }
     if (e != cudaSuccess) return e;
-    return launch_after(k_w4_matmul<NT, NG>, dim3(p.steps.ctas), kThreads, p.shared, !p.own, st, a);
+    return launch_after(k_w4_matmul<NT, NG>, dim3(p.steps.ctas), kThreads, p.shared, st, a);
 }
 template <int NT>
 cudaError_t launch_tiles(const MatmulArgs &a, const Plan &p, cudaStream_t st) {
     return a.s.groups == 1 ? launch_one<NT, 1>(a, p, st) : a.s.groups == 2 ? launch_one<NT, 2>(a, p, st) : launch_one<NT, 4>(a, p, st);
 }
 cudaError_t launch_matmul(const MatmulArgs &a, const Plan &p, char *scratch, cudaStream_t st) {
-    cudaError_t e = cudaSuccess;
-    if (!p.own) {
-        k_w4_rows<<<a.rows, kRowThreads, 0, st>>>(a.x, reinterpret_cast<uint2 *>(scratch), a.back, a.s.units, p.c);
-        e = cudaGetLastError();
-    }
+    k_w4_rows<<<a.rows, kRowThreads, 0, st>>>(a.x, reinterpret_cast<uint2 *>(scratch), reinterpret_cast<float *>(scratch + p.back_at), a.s.units, p.c);
+    cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess)
         e = p.nt == 1 ? launch_tiles<1>(a, p, st) : p.nt == 2 ? launch_tiles<2>(a, p, st) : p.nt == 3 ? launch_tiles<3>(a, p, st) : launch_tiles<4>(a, p, st);
-    if (e == cudaSuccess) e = launch_after(k_w4_join, dim3(a.s.tiles, p.c.passes), 128, 0, true, st, a, p.nt);
+    if (e == cudaSuccess) e = launch_after(k_w4_join, dim3(a.s.tiles, p.c.passes), p.join_threads, 0, st, a, p.nt);
     return e;
 }
 
@@ -663,7 +665,7 @@ talker_status talker_w4_quantize(const void *w, int dtype, int64_t row_stride, i
 }
 
 size_t talker_w4_scratch(const talker_w4 *w, int x_dtype, int rows) {
-    return matrix_ok(w) && rows > 0 && rows <= kMostRows ? plan_of(sizes_of(w), w->k, x_dtype, rows).bytes : 0;
+    return matrix_ok(w) && rows > 0 && rows <= kMostRows ? plan_of(sizes_of(w), x_dtype, rows).bytes : 0;
 }
 
 talker_status talker_w4_matmul(const talker_w4 *w, const void *x, int x_dtype, int64_t x_row, const float *x_scales,
@@ -677,14 +679,13 @@ talker_status talker_w4_matmul(const talker_w4 *w, const void *x, int x_dtype, i
     if (rows > 1 && (out_row < w->n || (residual == out && residual && res_row != out_row))) return TALKER_EINVAL;
     if (rows == 0) return TALKER_OK;
     const Sizes s = sizes_of(w);
-    const Plan p = plan_of(s, w->k, x_dtype, rows);
+    const Plan p = plan_of(s, x_dtype, rows);
     if (!scratch || scratch_bytes < p.bytes || !aligned(scratch, 16)) return TALKER_EINVAL;
     char *base = static_cast<char *>(scratch);
     MatmulArgs a{};
     a.tiles = static_cast<const unsigned char *>(w->tiles), a.s = s, a.steps = p.steps;
     a.x = {x, x_scales, x_row, x_dtype, x_block, w->k, rows, aligned(x, 4 * size_of(x_dtype)) && (rows == 1 || x_row % 4 == 0)};
-    if (!p.own) a.frags = reinterpret_cast<const uint4 *>(base);
-    a.back = reinterpret_cast<float *>(base + p.back_at), a.sums = reinterpret_cast<float4 *>(base + p.sums_at);
+    a.frags = reinterpret_cast<const uint4 *>(base), a.back = reinterpret_cast<const float *>(base + p.back_at), a.sums = reinterpret_cast<float4 *>(base + p.sums_at);
     a.res = residual, a.out = out, a.res_row = res_row, a.out_row = out_row;
     a.n = w->n, a.spans = p.spans, a.c = p.c, a.rows = rows, a.x_bytes = p.x_bytes;
     a.zeros = w->zeros != 0, a.gated = w->gated != 0, a.bf16 = out_dtype == TALKER_DTYPE_BF16;
