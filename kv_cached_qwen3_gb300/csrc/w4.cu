@@ -15,9 +15,7 @@ constexpr int kUnit = 128;              // inputs: what k is padded to, and what
 constexpr int kUnitBytes = 16 * kUnit / 2;
 constexpr int kMostRows = 1 << 16;
 
-constexpr int kWarps = 16, kThreads = (kWarps + 1) * 32;   // that multiply; one more makes the copies
-constexpr int kTiles = 2;               // of a warp: one fragment of x, and one turn of the loop, serve both
-constexpr int kSpan = kWarps * kTiles;  // row tiles of a CTA
+constexpr int kSpan = 32;               // row tiles whose records of a unit are neighbours
 
 struct Sizes {
     int tiles, units, groups;   // row tiles, units of inputs, groups of a unit
@@ -309,11 +307,17 @@ __device__ __forceinline__ uint32_t read2(uint32_t at) {
 }
 
 constexpr int kMultiprocessors = 152, kMostShared = 227 * 1024;
+constexpr int kTiles = 2;                        // of a warp: one fragment of x, and one turn of the loop, serve both
 constexpr int kSlots = 4;                        // steps on their way or at hand: 135 KB a multiprocessor
+// Warps that multiply (one more makes the copies). With three or four column tiles a warp needs more registers than
+// sixteen leave it, and has enough to do for the tensor cores by itself.
+constexpr int warps_of(int nt) { return nt <= 2 ? 16 : 8; }
+constexpr int tiles_of(int nt) { return warps_of(nt) * kTiles; }   // of a step: a span, or half of one
+static_assert(kSpan % tiles_of(1) == 0 && kSpan % tiles_of(4) == 0, "steps within spans");
 
-// A product is `steps` steps, in the order of passes, spans and units: a step is a unit of all tiles of a span for a pass's columns. CTA
-// c takes the steps from start(c) to start(c + 1), so all have the same number, give or take one. A stretch of steps of one
-// pass and span is a segment, whose sums go to the place c + pass * spans + span.
+// A product is `all` steps, in the order of passes, blocks of tiles_of(nt) row tiles, and units: a step is a unit of a block's tiles
+// for a pass's columns. CTA c takes the steps from start(c) to start(c + 1), so all have the same number, give or take one. A
+// stretch of steps of one pass and block is a segment, whose sums go to the place c + pass * blocks + block.
 struct Steps {
     long long all;
     int ctas, units;
@@ -331,7 +335,7 @@ struct MatmulArgs {
     const void *res;
     void *out;
     long long res_row, out_row;
-    int n, spans;
+    int n, blocks;
     Columns c;
     int rows, x_bytes;        // of x in a slot
     bool zeros, gated, bf16;
@@ -351,22 +355,23 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity) {
 // sums go to memory, and the kernel after adds them up. A group of inputs' sum is added to the total times its
 // scale. A copy that does not arrive within a second makes its warps' sums NaN from there on.
 template <int NT, int NG>
-__global__ void __launch_bounds__(kThreads, 1) k_w4_matmul(const MatmulArgs a) {
+__global__ void __launch_bounds__((warps_of(NT) + 1) * 32, 1) k_w4_matmul(const MatmulArgs a) {
+    constexpr int kWarps = warps_of(NT), kBlock = tiles_of(NT);
     extern __shared__ uint4 smem[];
     __shared__ uint64_t full[kSlots], empty[kSlots];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int units = a.s.units, record = a.s.record, parts = a.c.parts;
-    const int slot_bytes = kSpan * record + a.x_bytes;
+    const int slot_bytes = kBlock * record + a.x_bytes;
     const uint32_t slots = smem_u32(smem);
     const long long first = a.steps.start(blockIdx.x);
     const int count = (int)(a.steps.start(blockIdx.x + 1) - first);
-    // where a step is: place = pass * spans + span, of the unit's tiles of_span there
+    // where a step is: place = pass * blocks + block, the block's tiles and the first of them
     struct At {
-        int place, unit, pass, span, of_span;
+        int place, unit, pass, first, tiles;
     };
     auto enter = [&](At &p) {
-        p.pass = p.place / a.spans, p.span = p.place - p.pass * a.spans;
-        p.of_span = min(a.s.tiles - p.span * kSpan, kSpan);
+        p.pass = p.place / a.blocks, p.first = (p.place - p.pass * a.blocks) * kBlock;
+        p.tiles = min(a.s.tiles - p.first, kBlock);
     };
     auto next = [&](At &p) {
         if (++p.unit < units) return;
@@ -377,12 +382,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_matmul(const MatmulArgs a) {
     at.place = (int)(first / units), at.unit = (int)(first - (long long)at.place * units);
     enter(at);
     auto copy_codes = [&](const At &p, int slot) {
-        const uint32_t bytes = p.of_span * record;
+        const uint32_t bytes = p.tiles * record;
         mbar_arrive_expect_tx(&full[slot], bytes + a.x_bytes);
-        bulk_g2s(reinterpret_cast<char *>(smem) + slot * slot_bytes, a.tiles + ((size_t)p.span * kSpan * units + (size_t)p.unit * p.of_span) * record, bytes, &full[slot]);
+        bulk_g2s(reinterpret_cast<char *>(smem) + slot * slot_bytes, a.tiles + record_at(a.s, p.first, p.unit), bytes, &full[slot]);
     };
     auto copy_x = [&](const At &p, int slot) {   // (also columns past the last pass's: they are not looked at)
-        bulk_g2s(reinterpret_cast<char *>(smem) + slot * slot_bytes + kSpan * record, a.frags + ((size_t)p.pass * units + p.unit) * 16 * a.c.cols,
+        bulk_g2s(reinterpret_cast<char *>(smem) + slot * slot_bytes + kBlock * record, a.frags + ((size_t)p.pass * units + p.unit) * 16 * a.c.cols,
                  a.x_bytes, &full[slot]);
     };
     At ahead = at;
@@ -415,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_matmul(const MatmulArgs a) {
     bool fresh = true;
     int from_col[NT];
     for (int step = 0; step < count; ++step) {
-        const int slot = step % kSlots, tiles = at.of_span - warp * kTiles;   // tiles of this warp
+        const int slot = step % kSlots, tiles = at.tiles - warp * kTiles;   // tiles of this warp
         if (fresh) {
             fresh = false;
             const int cols = min(a.c.cols, a.rows * parts - at.pass * a.c.cols);
@@ -439,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_matmul(const MatmulArgs a) {
         }
         if (tiles > 0 && !lost) {
             const uint32_t now = slots + slot * slot_bytes;
-            const uint32_t x = now + kSpan * record, tail = now + mine - lane * 16 + kUnitBytes;   // scales, then zeros
+            const uint32_t x = now + kBlock * record, tail = now + mine - lane * 16 + kUnitBytes;   // scales, then zeros
             uint4 w[kTiles][2];
 #pragma unroll
             for (int r = 0; r < kTiles; ++r) w[r][0] = read16(now + mine + r * record), w[r][1] = read16(now + mine + r * record + 512);
@@ -508,14 +513,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_matmul(const MatmulArgs a) {
 // rows g (0, 1) and g + 8 (2, 3) of two columns. Where there are many segments, groups of 128 threads take a range each.
 __global__ void __launch_bounds__(1024) k_w4_join(const MatmulArgs a, int nt) {
     __shared__ float sums[7 * 128];
-    const int pass = blockIdx.y, tile = blockIdx.x, span = tile / kSpan, of_warp = tile % kSpan, place = pass * a.spans + span, parts = a.c.parts;
+    const int per = tiles_of(nt), pass = blockIdx.y, tile = blockIdx.x, place = pass * a.blocks + tile / per, parts = a.c.parts;
     const int id = threadIdx.x & 127, j = id & 3, l = id >> 2, own = threadIdx.x >> 7, ranges = blockDim.x >> 7;
     const int cols = min(a.c.cols, a.rows * parts - pass * a.c.cols);
     const int c0 = a.steps.cta_of((long long)place * a.steps.units), all = a.steps.cta_of((long long)(place + 1) * a.steps.units - 1) + 1 - c0;
     const int from = all * own / ranges, to = all * (own + 1) / ranges;
     const int row = a.gated ? tile * 8 + (l >> 2) : tile * 16 + (l >> 2) + 8 * (j >> 1);
-    const size_t segment = (size_t)kSpan * nt * 128;
-    const float *at = reinterpret_cast<const float *>(a.sums) + (size_t)(c0 + place + from) * segment + (size_t)of_warp * nt * 128 + id;
+    const size_t segment = (size_t)per * nt * 128;
+    const float *at = reinterpret_cast<const float *>(a.sums) + (size_t)(c0 + place + from) * segment + (size_t)(tile % per) * nt * 128 + id;
     pdl_wait();
     for (int i = 0; i < nt; ++i, at += 128) {
         const int col = i * 8 + 2 * (l & 3) + (j & 1);
@@ -549,7 +554,7 @@ __global__ void __launch_bounds__(1024) k_w4_join(const MatmulArgs a, int nt) {
 struct Plan {
     Columns c;
     Steps steps;
-    int nt, spans, x_bytes, join_threads;
+    int nt, blocks, x_bytes, join_threads;
     size_t shared, back_at, sums_at, bytes;   // (the last three: of the scratch)
 };
 Plan plan_of(const Sizes &s, int x_dtype, int rows) {
@@ -560,20 +565,21 @@ Plan plan_of(const Sizes &s, int x_dtype, int rows) {
     p.nt = (int)((col_tiles + p.c.passes - 1) / p.c.passes);
     p.c.cols = (int)std::min<long long>(columns, p.nt * 8);
     p.x_bytes = p.c.cols * 256;
-    p.shared = (size_t)kSlots * (kSpan * s.record + p.x_bytes);
-    p.spans = (s.tiles + kSpan - 1) / kSpan;
+    p.shared = (size_t)kSlots * (tiles_of(p.nt) * s.record + p.x_bytes);
+    p.blocks = (s.tiles + tiles_of(p.nt) - 1) / tiles_of(p.nt);
     p.steps.units = s.units;
-    p.steps.all = (long long)p.c.passes * p.spans * s.units;
+    p.steps.all = (long long)p.c.passes * p.blocks * s.units;
     p.steps.ctas = (int)std::min<long long>(p.steps.all, kMultiprocessors);
     const long long segments = (s.units * (long long)p.steps.ctas + p.steps.all - 1) / p.steps.all;   // of a place, about
     p.join_threads = segments <= 8 ? 128 : segments <= 16 ? 256 : segments <= 32 ? 512 : 1024;
     p.back_at = (size_t)p.c.passes * s.units * 16 * p.c.cols * sizeof(uint4);
     p.sums_at = (p.back_at + (size_t)rows * 4 + 15) / 16 * 16;
-    p.bytes = p.sums_at + ((size_t)p.c.passes * p.spans + p.steps.ctas - 1) * kSpan * p.nt * 32 * sizeof(float4);
+    p.bytes = p.sums_at + ((size_t)p.c.passes * p.blocks + p.steps.ctas - 1) * tiles_of(p.nt) * p.nt * 32 * sizeof(float4);
     return p;
 }
 // The most shared memory that a plan asks for.
-static_assert(kSlots * (kSpan * (kUnitBytes + 4 * 48) + 32 * 256) <= kMostShared - 256, "slots");
+static_assert(kSlots * (tiles_of(2) * (kUnitBytes + 4 * 48) + 16 * 256) <= kMostShared - 256, "slots");
+static_assert(kSlots * (tiles_of(4) * (kUnitBytes + 4 * 48) + 32 * 256) <= kMostShared - 256, "slots");
 
 // After the kernel before it on the stream, of this call: it may begin earlier and waits for what it needs.
 template <typename... A>
@@ -601,7 +607,7 @@ cudaError_t launch_one(const MatmulArgs &a, const Plan &p, cudaStream_t st) {
         if (e == cudaSuccess) raised |= bit;
     }
     if (e != cudaSuccess) return e;
-    return launch_after(k_w4_matmul<NT, NG>, dim3(p.steps.ctas), kThreads, p.shared, st, a);
+    return launch_after(k_w4_matmul<NT, NG>, dim3(p.steps.ctas), (warps_of(NT) + 1) * 32, p.shared, st, a);
 }
 template <int NT>
 cudaError_t launch_tiles(const MatmulArgs &a, const Plan &p, cudaStream_t st) {
@@ -687,7 +693,7 @@ talker_status talker_w4_matmul(const talker_w4 *w, const void *x, int x_dtype, i
     a.x = {x, x_scales, x_row, x_dtype, x_block, w->k, rows, aligned(x, 4 * size_of(x_dtype)) && (rows == 1 || x_row % 4 == 0)};
     a.frags = reinterpret_cast<const uint4 *>(base), a.back = reinterpret_cast<const float *>(base + p.back_at), a.sums = reinterpret_cast<float4 *>(base + p.sums_at);
     a.res = residual, a.out = out, a.res_row = res_row, a.out_row = out_row;
-    a.n = w->n, a.spans = p.spans, a.c = p.c, a.rows = rows, a.x_bytes = p.x_bytes;
+    a.n = w->n, a.blocks = p.blocks, a.c = p.c, a.rows = rows, a.x_bytes = p.x_bytes;
     a.zeros = w->zeros != 0, a.gated = w->gated != 0, a.bf16 = out_dtype == TALKER_DTYPE_BF16;
     const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
     const cudaError_t e = launch_matmul(a, p, base, st);
