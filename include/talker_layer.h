@@ -35,8 +35,8 @@ extern "C" {
  *   scales[r][b] = max|y| / 448 over block b; code = e4m3(y * (448 / max|y|)), to
  *   the nearest, ties to even; y stands for code * scale.
  * scales is f32 [rows][ceil(width / block)], contiguous. Blocks with max|y| below
- * 2^-100 store zeros; one with a NaN or an infinity reads back as NaN. A NaN in s makes
- * its row NaN; the sum of a row's squares is to stay in f32's range.
+ * 2^-100 (or max|s * gain| below it) store zeros; one with an infinity reads back as NaN.
+ * A NaN in s makes its row NaN; the sum of a row's squares is to stay in f32's range.
  * sum_out may be residual or x, and y may be x or residual, with the same strides
  * and type; other overlaps are not allowed.
  * Errors: EINVAL (null x, gain or y; types; width not in 1..2^24; rows not in 0..2^30;
@@ -102,8 +102,8 @@ typedef struct {
 } talker_heads;
 /* Rotate the heads of n_sets (1 or 2, for example q and k; HOST array) sets of heads of
  * the same rows. positions: int32 [streams][rows], any value (negative ones rotate back). turns: device table.
- * dtype F32 or BF16 for all. Errors: EINVAL (null pointers, sizes below 0, head_dim not in 2..1024,
- * rotary_dim odd or above head_dim, more than 65536 heads), ECUDA. */
+ * dtype F32 or BF16 for all. Errors: EINVAL (null pointers, sizes below 0, head_dim not in 2..512,
+ * rotary_dim odd or above head_dim, more than 16384 heads in a set, streams * rows above 2^30), ECUDA. */
 talker_status talker_rotate(const uint64_t *turns, float amplitude, int head_dim, int rotary_dim, int interleaved,
                             const int32_t *positions, int streams, int rows, const talker_heads *sets, int n_sets,
                             int dtype, void *cuda_stream);

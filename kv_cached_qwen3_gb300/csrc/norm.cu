@@ -21,11 +21,15 @@ struct NormArgs {
     float *scales;
     Place x_at, res_at, sum_at, y_at;
     float eps;
-    int rows, inner, width, block;   // block: in values, 0: a row
+    int rows, inner, width;
+    int block, block_shift, blocks;   // in values (0: a row), its log2, blocks of a row
+    float inv_width;
     bool gain_vec;
 };
 
-__device__ __forceinline__ long long at(const Place &p, int outer, int inner) { return outer * p.outer + inner * p.inner; }
+__device__ __forceinline__ long long at(const Place &p, int outer, int inner) {
+    return inner < 0 ? outer * p.outer : outer * p.outer + inner * p.inner;
+}
 
 template <typename T>
 __device__ __forceinline__ void load_row8(const T *p, int i, int width, bool vec, float (&v)[8]) {
@@ -50,15 +54,10 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) |
            (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3) << 16;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float y;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-    return y;
-}
 __device__ __forceinline__ float max_abs8(const float (&v)[8]) {
     float m = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max_nan(m, fabsf(v[j]));
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));   // (a NaN shows in the norm's factor)
     return m;
 }
 
@@ -67,7 +66,7 @@ template <bool MAX>
 __device__ __forceinline__ float row_all(float v, float *red) {
     if (MAX) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+        for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
     } else {
         v = warp_sum(v);
     }
@@ -79,100 +78,171 @@ __device__ __forceinline__ float row_all(float v, float *red) {
     float w = lane < warps ? red[lane] : 0.f;
     if (MAX) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) w = max_nan(w, __shfl_xor_sync(0xffffffffu, w, o));
+        for (int o = 16; o > 0; o >>= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, o));
         return w;
     }
     return warp_sum(w);
 }
 
-// blockDim.x threads a row, blockDim.y rows a CTA; a thread has eight consecutive values of every chunk of 8 *
-// blockDim.x. C chunks stay in registers between the sum and the result; with C = 0 (rows of more) they are read again.
+// 1 / sqrt(x): the hardware's (2^-23 off) and a step of Newton's method; of 0 and infinity as it is.
+__device__ __forceinline__ float root(float x) {
+    float r;
+    asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    const float better = fmaf(r * 0.5f, fmaf(-x * r, r, 1.f), r);
+    return r > 0.f && r < INFINITY ? better : r;
+}
+
+// Eight values of a row as they lie in memory, so that nothing waits for them until they are used.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<float> {
+    float v[8];
+    __device__ __forceinline__ void load(const float *p, int i, int width, bool vec) { load_row8(p, i, width, vec, v); }
+    __device__ __forceinline__ float at(int j) const { return v[j]; }
+};
+template <>
+struct Raw<__nv_bfloat16> {
+    uint32_t w[4];
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p, int i, int width, bool vec) {
+        if (vec && i + 8 <= width) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(p + i);
+            w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+        } else {
+            const unsigned short *q = reinterpret_cast<const unsigned short *>(p);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[j] = (i + 2 * j < width ? q[i + 2 * j] : 0u) | (i + 2 * j + 1 < width ? (uint32_t)q[i + 2 * j + 1] : 0u) << 16;
+        }
+    }
+    __device__ __forceinline__ float at(int j) const { return j & 1 ? bf16hi(w[j / 2]) : bf16lo(w[j / 2]); }
+};
+
+// blockDim.x threads a row, blockDim.y rows at a time; a thread has eight consecutive values of every chunk of 8 *
+// blockDim.x. C chunks stay in registers between the sum and the result, and the next rows' are on their way meanwhile; with
+// C = 0 (rows of more than 16384 values) they are read again. For E4M3 the norm's factor cancels: a code is that of s gain
+// over the largest of its block.
+// Bound by HBM: 4096 x 5120, bf16 and f32 to f32 and e4m3.
+constexpr int kNarrow = 672;   // threads of a row at most, with one chunk: two CTAs of them at 48 registers
 template <typename TX, typename TR, typename TY, int C>
-__global__ void __launch_bounds__(1024) k_rms_norm(const NormArgs a) {
+__global__ void __launch_bounds__(C == 1 ? kNarrow : 1024, C == 1 ? 2 : 1) k_rms_norm(const NormArgs a) {
     constexpr bool kRes = !std::is_same<TR, void>::value, k8 = std::is_same<TY, __nv_fp8_storage_t>::value;
+    constexpr int H = C > 0 ? C : 1;   // chunks in registers
+    constexpr bool kAhead = C == 1;    // (two chunks of the next row too would not fit in 64 registers)
     using R = typename std::conditional<kRes, TR, float>::type;
     using Y = typename std::conditional<k8, float, TY>::type;
-    __shared__ float sums[32], tops[32];   // of a row's warps
-    const int row = blockIdx.x * blockDim.y + threadIdx.y;
-    const bool live = row < a.rows;
-    const int outer = live ? row / a.inner : 0, inner = live ? row - outer * a.inner : 0;
-    const TX *x = static_cast<const TX *>(a.x) + at(a.x_at, outer, inner);
-    const R *res = kRes ? static_cast<const R *>(a.res) + at(a.res_at, outer, inner) : nullptr;
-    const int width = live ? a.width : 0, step = 8 * blockDim.x, first = 8 * threadIdx.x;
-    const int chunks = C > 0 ? C : (a.width + step - 1) / step;
-    float *const red = sums + threadIdx.y * (blockDim.x >> 5), *const top = tops + threadIdx.y * (blockDim.x >> 5);
-
-    auto take = [&](int c, float (&v)[8]) {
+    __shared__ float sums[2][32], tops[2][32];   // of a row's warps; of every other turn, so that one wait a turn is enough
+    const int step = 8 * blockDim.x, first = 8 * threadIdx.x, per = blockDim.y * gridDim.x;
+    const int chunks = C > 0 ? C : (a.width + step - 1) / step, warps = blockDim.x >> 5;
+    struct Row {
+        int outer, inner, width;   // inner -1: rows at one stride; width 0: none
+    };
+    auto row_of = [&](int row) -> Row {
+        if (row >= a.rows) return {0, -1, 0};
+        if (a.inner == 1) return {row, -1, a.width};
+        const int outer = (unsigned)row / (unsigned)a.inner;
+        return {outer, row - outer * a.inner, a.width};
+    };
+    Raw<TX> x[H];
+    Raw<R> r[H];
+    auto fetch = [&](const Row &w, int c, Raw<TX> &x, Raw<R> &r) {
         const int i = c * step + first;
-        load_row8(x, i, width, a.x_at.vec, v);
-        if (kRes) {
-            float r[8];
-            load_row8(res, i, width, a.res_at.vec, r);
+        x.load(static_cast<const TX *>(a.x) + at(a.x_at, w.outer, w.inner), i, w.width, a.x_at.vec);
+        if (kRes) r.load(static_cast<const R *>(a.res) + at(a.res_at, w.outer, w.inner), i, w.width, a.res_at.vec);
+    };
+    auto sum_of = [&](const Raw<TX> &x, const Raw<R> &r, float (&v)[8]) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] += r[j];
+        for (int j = 0; j < 8; ++j) v[j] = kRes ? x.at(j) + r.at(j) : x.at(j);
+    };
+    int row = blockIdx.x * blockDim.y + threadIdx.y;
+    Row now = row_of(row);
+    if (kAhead) fetch(now, 0, x[0], r[0]);
+    for (int turn = 0; row - (int)threadIdx.y < a.rows; row += per, turn ^= 1) {   // (all of a CTA's threads together)
+        float *const red = sums[turn] + threadIdx.y * warps, *const top = tops[turn] + threadIdx.y * warps;
+        float held[H][8];
+        float sum = 0.f;
+        auto add = [&](const float (&v)[8]) {
+            float t = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) t = fmaf(v[j], v[j], t);
+            sum += t;
+        };
+        const Row next = row_of(row + per < a.rows ? row + per : a.rows);
+        if (C > 0) {
+            if (!kAhead) {
+#pragma unroll
+                for (int c = 0; c < H; ++c) fetch(now, c, x[c], r[c]);
+            }
+#pragma unroll
+            for (int c = 0; c < H; ++c) sum_of(x[c], r[c], held[c]);
+            if (kAhead) fetch(next, 0, x[0], r[0]);
+#pragma unroll
+            for (int c = 0; c < H; ++c) add(held[c]);
+        } else {
+            for (int c = 0; c < chunks; ++c) {
+                fetch(now, c, x[0], r[0]);
+                sum_of(x[0], r[0], held[0]);
+                add(held[0]);
+            }
         }
-    };
-    float held[C > 0 ? C : 1][8];
-    float sum = 0.f;
+        const float scale = root(fmaf(row_all<false>(sum, red), a.inv_width, a.eps));
+        auto take = [&](int c, float (&v)[8], float (&g)[8]) {   // s and s gain
+            if (C == 0) {
+                fetch(now, c, x[0], r[0]);
+                sum_of(x[0], r[0], v);
+            }
+            load_row8(a.gain, c * step + first, a.width, a.gain_vec, g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) g[j] *= v[j];
+        };
+        float most = 0.f;   // of the row
+        if (k8 && a.block == 0) {
 #pragma unroll(C > 0 ? C : 1)
-    for (int c = 0; c < chunks; ++c) {
-        float(&v)[8] = held[C > 0 ? c : 0];
-        take(c, v);
-        float t = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) t = fmaf(v[j], v[j], t);
-        sum += t;
-    }
-    const float scale = 1.0f / sqrtf(row_all<false>(sum, red) / (float)a.width + a.eps);
-    auto result = [&](int c, float (&v)[8], float (&y)[8]) {
-        if (C == 0) take(c, v);
-        const int i = c * step + first;
-        float g[8];
-        load_row8(a.gain, i, width, a.gain_vec, g);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = v[j] * scale * g[j];
-    };
-    float most = 0.f;   // of the row
-    if (k8 && a.block == 0) {
+            for (int c = 0; c < chunks; ++c) {
+                float g[8];
+                take(c, held[C > 0 ? c : 0], g);
+                most = fmaxf(most, max_abs8(g));
+            }
+            most = row_all<true>(most, top);
+        }
 #pragma unroll(C > 0 ? C : 1)
         for (int c = 0; c < chunks; ++c) {
-            float y[8];
-            result(c, held[C > 0 ? c : 0], y);
-            most = max_nan(most, max_abs8(y));
-        }
-        most = row_all<true>(most, top);
-    }
-#pragma unroll(C > 0 ? C : 1)
-    for (int c = 0; c < chunks; ++c) {
-        float(&v)[8] = held[C > 0 ? c : 0];
-        float y[8];
-        result(c, v, y);
-        const int i = c * step + first;
-        if (kRes && a.sum != nullptr) store_row8(static_cast<R *>(a.sum) + at(a.sum_at, outer, inner), i, width, a.sum_at.vec, v);
-        if (k8) {
-            float m = most;
-            if (a.block != 0) {   // its threads are neighbours in a warp
-                m = max_abs8(y);
-                for (int o = a.block / 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-            }
-            const bool none = m < 0x1p-100f;
-            const float inv = none ? 0.f : 448.f / m;
-            const int blocks = a.block == 0 ? 1 : (a.width + a.block - 1) / a.block;
-            if (a.block == 0 ? i == 0 : i % a.block == 0 && i < width)
-                if (live) a.scales[(size_t)row * blocks + (a.block == 0 ? 0 : i / a.block)] = none ? 0.f : m / 448.f;
-            uint8_t *out = static_cast<uint8_t *>(a.y) + at(a.y_at, outer, inner);
-            const uint2 w = make_uint2(e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
-                                       e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
-            if (a.y_at.vec && i + 8 <= width) {
-                *reinterpret_cast<uint2 *>(out + i) = w;
-            } else {
+            float(&v)[8] = held[C > 0 ? c : 0];
+            float g[8];
+            take(c, v, g);
+            const int i = c * step + first;
+            if (kRes && a.sum != nullptr) store_row8(static_cast<R *>(a.sum) + at(a.sum_at, now.outer, now.inner), i, now.width, a.sum_at.vec, v);
+            if (k8) {
+                float m = most;
+                if (a.block != 0) {   // its threads are neighbours in a warp
+                    m = max_abs8(g);
+                    for (int o = a.block / 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                }
+                const float d = m * scale;   // max|y|
+                const bool none = d < 0x1p-100f || m < 0x1p-100f;
+                float inv;
+                asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(m));
+                inv = none ? 0.f : d < INFINITY ? 448.f * inv : NAN;
+                if ((a.block == 0 ? i == 0 : (i & (a.block - 1)) == 0) && i < now.width)
+                    a.scales[(size_t)row * a.blocks + (a.block == 0 ? 0 : i >> a.block_shift)] = none ? 0.f : d * (1.f / 448.f);
+                uint8_t *out = static_cast<uint8_t *>(a.y) + at(a.y_at, now.outer, now.inner);
+                const uint2 w = make_uint2(e4m3x4(g[0] * inv, g[1] * inv, g[2] * inv, g[3] * inv),
+                                           e4m3x4(g[4] * inv, g[5] * inv, g[6] * inv, g[7] * inv));
+                if (a.y_at.vec && i + 8 <= now.width) {
+                    *reinterpret_cast<uint2 *>(out + i) = w;
+                } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (i + j < width) out[i + j] = (uint8_t)((j < 4 ? w.x : w.y) >> (8 * (j % 4)));
+                    for (int j = 0; j < 8; ++j)
+                        if (i + j < now.width) out[i + j] = (uint8_t)((j < 4 ? w.x : w.y) >> (8 * (j % 4)));
+                }
+            } else {
+                float y[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[j] = g[j] * scale;
+                store_row8(static_cast<Y *>(a.y) + at(a.y_at, now.outer, now.inner), i, now.width, a.y_at.vec, y);
             }
-        } else {
-            store_row8(static_cast<Y *>(a.y) + at(a.y_at, outer, inner), i, width, a.y_at.vec, y);
         }
+        now = next;
     }
 }
 
@@ -221,18 +291,22 @@ extern "C" talker_status talker_rms_norm(const void *x, int x_dtype, const talke
     NormArgs a{};
     a.x = x, a.res = residual, a.gain = gain, a.sum = sum_out, a.y = y, a.scales = scales;
     a.eps = eps, a.rows = rows, a.inner = inner, a.width = width, a.block = y_dtype == TALKER_DTYPE_E4M3 ? block : 0;
+    a.block_shift = a.block == 32 ? 5 : a.block == 64 ? 6 : 7, a.blocks = a.block == 0 ? 1 : (width + a.block - 1) / a.block;
+    a.inv_width = (float)(1.0 / width);
     a.x_at = place(x, x_dtype, x_at, rows, inner);
     if (residual) a.res_at = place(residual, res_dtype, res_at, rows, inner);
     if (sum_out) a.sum_at = place(sum_out, res_dtype, sum_at, rows, inner);
     a.y_at = place(y, y_dtype, y_at, rows, inner);
     a.gain_vec = aligned(gain, 32);
-    const int c = width <= 8192 ? 1 : width <= 16384 ? 2 : 0;
+    const int c = width <= 8 * kNarrow ? 1 : width <= 16384 ? 2 : 0;
     const int threads = c == 0 ? 1024 : (width + 256 * c - 1) / (256 * c) * 32;
     const int per = std::max(1, 128 / threads);
     const dim3 block_dim(threads, per);
     const Kernel k = x_dtype == TALKER_DTYPE_F32 ? by_res<float>(residual != nullptr, res_dtype, y_dtype, c)
                                                  : by_res<__nv_bfloat16>(residual != nullptr, res_dtype, y_dtype, c);
-    k<<<(rows + per - 1) / per, block_dim, 0, static_cast<cudaStream_t>(cuda_stream)>>>(a);
+    // as many CTAs as the multiprocessors hold, each with several rows where there are more
+    const int most = 152 * std::max(1, 65536 / (c == 1 ? 48 : 64) / (threads * per));
+    k<<<std::min((rows + per - 1) / per, most), block_dim, 0, static_cast<cudaStream_t>(cuda_stream)>>>(a);
     if (cudaGetLastError() != cudaSuccess) return TALKER_ECUDA;
     return TALKER_OK;
 }

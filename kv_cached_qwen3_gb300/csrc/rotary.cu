@@ -9,18 +9,19 @@ using namespace talker_dev;
 
 namespace {
 
+constexpr int kMostThreads = 512;   // groups of a head at most: of one dim and another, or of two neighbours
+
 struct RotateArgs {
     const unsigned long long *turns;
     const int32_t *positions;
     talker_heads set[2];
-    long long units;    // threads with work: rows * slices * groups
     float amplitude;
-    int rows;           // of a stream
+    int all, rows;      // rows of all streams, of a stream
     int heads;          // of both sets
-    int slices;         // a row's heads h, h + slices, ... are one thread's
-    int half;           // rotary_dim / 2
-    int pair_groups;    // groups of VP pairs of a head
-    int groups;         // and of 2 VP dims that stay, where they are copied
+    int per, subs;      // a CTA's rows, and threads for each group of a row: every subs * gridDim.y th head each
+    int rotary;         // rotary_dim
+    int pair_groups;    // groups of dims of a head that are turned
+    int groups;         // and of dims that stay, where they are copied
     int head_dim;
 };
 
@@ -35,74 +36,109 @@ __device__ __forceinline__ float2 turn(int p, unsigned long long step, float amp
     return make_float2((quarter + 1) & 2 ? -a * amplitude : a * amplitude, quarter & 2 ? -b * amplitude : b * amplitude);
 }
 
-// VP values by one access.
-template <typename T, int VP>
-struct alignas(sizeof(T) * VP) Vec {
-    T v[VP];
+// A values by one access; two bf16 values make a word.
+template <typename T, int A>
+struct alignas(sizeof(T) * A) Vec {
+    T v[A];
+};
+template <typename T, int A, int N>
+struct Group {   // N values by accesses of A, the first `left` of them
+    Vec<T, A> v[N / A];
+    __device__ __forceinline__ void load(const T *p, int left) {
+#pragma unroll
+        for (int i = 0; i < N / A; ++i)
+            if (i * A < left) v[i] = *reinterpret_cast<const Vec<T, A> *>(p + i * A);
+    }
+    __device__ __forceinline__ void store(T *p, int left) const {
+#pragma unroll
+        for (int i = 0; i < N / A; ++i)
+            if (i * A < left) *reinterpret_cast<Vec<T, A> *>(p + i * A) = v[i];
+    }
+    __device__ __forceinline__ void get(float (&x)[N]) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = Elem<T>::load(v[i / A].v, i % A);
+    }
+    __device__ __forceinline__ void set(const float (&x)[N]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (sizeof(T) == 2 && A % 2 == 0) {
+                if (i % 2 == 0) *reinterpret_cast<__nv_bfloat162 *>(&v[i / A].v[i % A]) = __floats2bfloat162_rn(x[i], x[i + 1]);
+            } else {
+                Elem<T>::store(v[i / A].v, i % A, x[i]);
+            }
+        }
+    }
 };
 
-// A thread has one group of VP pairs of a row, makes their cosines and sines once, and turns the group in every
-// `slices`th head of the row: two vectors of VP values read and written.
-template <typename T, int VP, bool INTERLEAVED>
-__global__ void __launch_bounds__(256) k_rotate(const RotateArgs a) {
-    using V = Vec<T, VP>;
-    const long long u = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (u >= a.units) return;
-    const int group = (int)(u % a.groups);
-    const long long rest = u / a.groups;
-    const int slice = (int)(rest % a.slices);
-    const long long row = rest / a.slices;
-    const long long stream = row / a.rows;
-    const int t = (int)(row - stream * a.rows);
+// A CTA has `per` rows. A thread has one group of a head's dims of a row: A dims and those half a rotary_dim further, or N
+// neighbours (with neighbours as pairs, and of dims that stay). It makes their cosines and sines once and turns the group in
+// its heads. Bound by HBM where there are many rows: index arithmetic is kept out of the loop over heads (64-bit divisions a
+// thread, and places made anew a head, took 59 and 97 us for 3 x 5001 rows of 40 heads).
+template <typename T, int A, bool INTERLEAVED>
+__global__ void __launch_bounds__(kMostThreads) k_rotate(const RotateArgs a) {
+    constexpr int N = INTERLEAVED && A == 1 ? 2 : A, kPairs = INTERLEAVED ? N / 2 : A, kBatch = 4;
+    const int id = threadIdx.x / (unsigned)a.groups, group = threadIdx.x - id * a.groups;
+    const int in_cta = id / (unsigned)a.subs, row = blockIdx.x * a.per + in_cta;
+    if (in_cta >= a.per || row >= a.all) return;
+    const int stream = (unsigned)row / (unsigned)a.rows, t = row - stream * a.rows;
+    const int stride = a.subs * gridDim.y;
     const bool turned = group < a.pair_groups;
-    int lo, hi;   // the first dims of the two vectors
-    if (turned) {
-        lo = INTERLEAVED ? 2 * group * VP : group * VP;
-        hi = INTERLEAVED ? lo + VP : lo + a.half;
-    } else {
-        lo = 2 * a.half + (group - a.pair_groups) * 2 * VP;
-        hi = lo + VP;
-    }
-    const bool two = hi < a.head_dim;
-    float2 cs[VP];
-    if (turned) {
-        const int p = a.positions[row];
+    const int lo = turned ? group * N : a.rotary + (group - a.pair_groups) * N, left = a.head_dim - lo;
+    float2 cs[kPairs];
+    bool made = false;
+    auto run = [&](const talker_heads &s, int h) {   // heads h, h + stride, ...
+        const T *in = static_cast<const T *>(s.in) + stream * s.in_stream + t * s.in_row + h * s.in_head + lo;
+        T *out = static_cast<T *>(s.out) + stream * s.out_stream + t * s.out_row + h * s.out_head + lo;
+        const long long in_step = stride * s.in_head, out_step = stride * s.out_head;
+        // in batches: all of a batch is on its way before the first is turned (what is written may be what is read)
+        for (; h < s.heads; h += kBatch * stride) {
+            Group<T, A, N> x[kBatch], y[kBatch];
 #pragma unroll
-        for (int i = 0; i < VP; ++i) cs[i] = turn(p, a.turns[group * VP + i], a.amplitude);
-    }
-#pragma unroll 4
-    for (int h = slice; h < a.heads; h += a.slices) {
-        const int k = h >= a.set[0].heads;
-        const talker_heads &s = a.set[k];
-        const int head = k ? h - a.set[0].heads : h;
-        const T *in = static_cast<const T *>(s.in) + stream * s.in_stream + t * s.in_row + head * s.in_head;
-        T *out = static_cast<T *>(s.out) + stream * s.out_stream + t * s.out_row + head * s.out_head;
-        V x = *reinterpret_cast<const V *>(in + lo), y{};
-        if (two) y = *reinterpret_cast<const V *>(in + hi);
-        if (turned) {
-            float e[2 * VP];
+            for (int b = 0; b < kBatch; ++b, in += in_step)
+                if (h + b * stride < s.heads) {
+                    x[b].load(in, left);
+                    if (!INTERLEAVED && turned) y[b].load(in + a.rotary / 2, left);
+                }
+            if (turned && !made) {   // (while the first are on their way)
+                const int p = a.positions[row];
 #pragma unroll
-            for (int i = 0; i < VP; ++i) e[i] = Elem<T>::load(x.v, i), e[VP + i] = Elem<T>::load(y.v, i);
-#pragma unroll
-            for (int i = 0; i < VP; ++i) {
-                float &p = e[INTERLEAVED ? 2 * i : i], &q = e[INTERLEAVED ? 2 * i + 1 : VP + i];
-                const float c = cs[i].x, n = cs[i].y, p0 = p;
-                p = p0 * c - q * n;
-                q = p0 * n + q * c;
+                for (int i = 0; i < kPairs; ++i) cs[i] = turn(p, a.turns[group * kPairs + i], a.amplitude);
+                made = true;
             }
 #pragma unroll
-            for (int i = 0; i < VP; ++i) Elem<T>::store(x.v, i, e[i]), Elem<T>::store(y.v, i, e[VP + i]);
+            for (int b = 0; b < kBatch; ++b, out += out_step) {
+                if (h + b * stride >= s.heads) break;
+                if (turned) {
+                    float u[N], v[N];
+                    x[b].get(u);
+                    if (!INTERLEAVED) y[b].get(v);
+#pragma unroll
+                    for (int i = 0; i < kPairs; ++i) {
+                        float &p = u[INTERLEAVED ? 2 * i : i], &q = INTERLEAVED ? u[2 * i + 1] : v[i];
+                        const float p0 = p;
+                        p = p0 * cs[i].x - q * cs[i].y;
+                        q = p0 * cs[i].y + q * cs[i].x;
+                    }
+                    x[b].set(u);
+                    if (!INTERLEAVED) y[b].set(v);
+                }
+                x[b].store(out, left);
+                if (!INTERLEAVED && turned) y[b].store(out + a.rotary / 2, left);
+            }
         }
-        *reinterpret_cast<V *>(out + lo) = x;
-        if (two) *reinterpret_cast<V *>(out + hi) = y;
-    }
+    };
+    const int first = blockIdx.y * a.subs + id - in_cta * a.subs;
+    run(a.set[0], first);
+    const int skip = a.set[0].heads % (unsigned)stride;   // (as if the sets were one)
+    run(a.set[1], first < skip ? first - skip + stride : first - skip);
 }
 
-template <typename T, int VP>
-void launch(const RotateArgs &a, bool interleaved, cudaStream_t st) {
-    const unsigned blocks = (unsigned)((a.units + 255) / 256);
-    if (interleaved) k_rotate<T, VP, true><<<blocks, 256, 0, st>>>(a);
-    else k_rotate<T, VP, false><<<blocks, 256, 0, st>>>(a);
+template <typename T, int A>
+void launch(const RotateArgs &a, int slices, bool interleaved, cudaStream_t st) {
+    const dim3 grid((unsigned)((a.all + a.per - 1) / a.per), slices);
+    const int threads = (a.per * a.subs * a.groups + 31) / 32 * 32;
+    if (interleaved) k_rotate<T, A, true><<<grid, threads, 0, st>>>(a);
+    else k_rotate<T, A, false><<<grid, threads, 0, st>>>(a);
 }
 
 }  // namespace
@@ -145,7 +181,7 @@ talker_status talker_rotate(const uint64_t *turns, float amplitude, int head_dim
                             const int32_t *positions, int streams, int rows, const talker_heads *sets, int n_sets,
                             int dtype, void *cuda_stream) {
     if (!turns || !positions || !sets || n_sets < 1 || n_sets > 2 || streams < 0 || rows < 0) return TALKER_EINVAL;
-    if (head_dim < 2 || head_dim > 1024 || rotary_dim < 2 || rotary_dim % 2 || rotary_dim > head_dim) return TALKER_EINVAL;
+    if (head_dim < 2 || head_dim > 512 || rotary_dim < 2 || rotary_dim % 2 || rotary_dim > head_dim) return TALKER_EINVAL;
     if (dtype != TALKER_DTYPE_F32 && dtype != TALKER_DTYPE_BF16) return TALKER_EINVAL;
     const int size = dtype == TALKER_DTYPE_F32 ? 4 : 2;
     if (reinterpret_cast<uintptr_t>(turns) % 8 || reinterpret_cast<uintptr_t>(positions) % 4) return TALKER_EINVAL;
@@ -153,7 +189,7 @@ talker_status talker_rotate(const uint64_t *turns, float amplitude, int head_dim
     bool copy = false;
     for (int i = 0; i < n_sets; ++i) {
         const talker_heads &s = sets[i];
-        if (!s.in || !s.out || s.heads < 0 || s.heads > 65536) return TALKER_EINVAL;
+        if (!s.in || !s.out || s.heads < 0 || s.heads > 16384) return TALKER_EINVAL;
         if (reinterpret_cast<uintptr_t>(s.in) % size || reinterpret_cast<uintptr_t>(s.out) % size) return TALKER_EINVAL;
         a.set[i] = s;
         a.heads += s.heads;
@@ -163,7 +199,7 @@ talker_status talker_rotate(const uint64_t *turns, float amplitude, int head_dim
     // the largest vector that fits the dims and every tensor's place and strides
     int vp = 16 / size;
     auto fits = [&](int n) {
-        long long bits = rotary_dim / 2 | (head_dim - rotary_dim);
+        long long bits = (interleaved ? rotary_dim : rotary_dim / 2) | (head_dim - rotary_dim);
         uintptr_t at = 0;
         for (int i = 0; i < n_sets; ++i) {
             const talker_heads &s = sets[i];
@@ -179,24 +215,30 @@ talker_status talker_rotate(const uint64_t *turns, float amplitude, int head_dim
     a.positions = positions;
     a.amplitude = amplitude;
     a.rows = rows;
-    a.half = rotary_dim / 2;
+    a.rotary = rotary_dim;
     a.head_dim = head_dim;
-    a.pair_groups = a.half / vp;
-    a.groups = a.pair_groups + (copy ? (head_dim - rotary_dim + 2 * vp - 1) / (2 * vp) : 0);
-    const long long n = (long long)streams * rows;
-    a.slices = (int)std::min<long long>(a.heads, std::max<long long>(1, 152ll * 2048 / (n * a.groups)));
-    a.units = n * a.slices * a.groups;
-    if ((a.units + 255) / 256 > 0x7fffffffll) return TALKER_EINVAL;
+    const int dims = interleaved ? std::max(vp, 2) : vp;   // of a group: also of dims that stay
+    a.pair_groups = (interleaved ? rotary_dim : rotary_dim / 2) / dims;
+    a.groups = a.pair_groups + (copy ? (head_dim - rotary_dim + dims - 1) / dims : 0);
+    if ((long long)streams * rows > 1 << 30) return TALKER_EINVAL;
+    a.all = streams * rows;
+    // about ten heads a thread, so that cosines are shared; with few rows fewer, down to one
+    const int room = std::max(1, 256 / a.groups);   // threads for a group, of a CTA
+    const long long want = (152ll * 2048 + (long long)a.all * a.groups - 1) / ((long long)a.all * a.groups);   // for a row, to fill the GPU
+    const int threads = (int)std::min<long long>(a.heads, std::max<long long>(want, (a.heads + 9) / 10));
+    a.subs = std::min(room, threads);
+    a.per = room / a.subs;
+    const int slices = (threads + a.subs - 1) / a.subs;
     const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
     if (dtype == TALKER_DTYPE_F32) {
-        if (vp == 4) launch<float, 4>(a, interleaved, st);
-        else if (vp == 2) launch<float, 2>(a, interleaved, st);
-        else launch<float, 1>(a, interleaved, st);
+        if (vp == 4) launch<float, 4>(a, slices, interleaved, st);
+        else if (vp == 2) launch<float, 2>(a, slices, interleaved, st);
+        else launch<float, 1>(a, slices, interleaved, st);
     } else {
-        if (vp == 8) launch<__nv_bfloat16, 8>(a, interleaved, st);
-        else if (vp == 4) launch<__nv_bfloat16, 4>(a, interleaved, st);
-        else if (vp == 2) launch<__nv_bfloat16, 2>(a, interleaved, st);
-        else launch<__nv_bfloat16, 1>(a, interleaved, st);
+        if (vp == 8) launch<__nv_bfloat16, 8>(a, slices, interleaved, st);
+        else if (vp == 4) launch<__nv_bfloat16, 4>(a, slices, interleaved, st);
+        else if (vp == 2) launch<__nv_bfloat16, 2>(a, slices, interleaved, st);
+        else launch<__nv_bfloat16, 1>(a, slices, interleaved, st);
     }
     return cudaGetLastError() == cudaSuccess ? TALKER_OK : TALKER_ECUDA;
 }

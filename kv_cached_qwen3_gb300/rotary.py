@@ -34,8 +34,8 @@ class Rotary:
     def __init__(self, head_dim: int, rotary_dim: int | None = None, theta: float = 1e6, interleaved: bool = False,
                  scaling: dict | None = None, device="cuda"):
         rotary_dim = head_dim if rotary_dim is None else rotary_dim
-        if not 2 <= head_dim <= 1024 or rotary_dim < 2 or rotary_dim % 2 or rotary_dim > head_dim:
-            raise ValueError("Rotary: needs head_dim 2 to 1024 and an even rotary_dim of at most head_dim")
+        if not 2 <= head_dim <= 512 or rotary_dim < 2 or rotary_dim % 2 or rotary_dim > head_dim:
+            raise ValueError("Rotary: needs head_dim 2 to 512 and an even rotary_dim of at most head_dim")
         given = dict(scaling or {"type": "none"})
         kind = given.pop("type", None)
         names = {"none": (), "linear": ("factor",), "ntk": ("factor",), "smooth": ("factor", "original", "low", "high"),

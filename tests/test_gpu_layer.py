@@ -213,7 +213,7 @@ def test_rotate_no_rows_and_no_heads():
 
 def test_rotate_refusals():
     from kv_cached_qwen3_gb300.rotary import Rotary
-    for kw in (dict(head_dim=0), dict(head_dim=1025), dict(head_dim=64, rotary_dim=63), dict(head_dim=64, rotary_dim=66), dict(head_dim=64, scaling=dict(type="x")),
+    for kw in (dict(head_dim=0), dict(head_dim=513), dict(head_dim=64, rotary_dim=63), dict(head_dim=64, rotary_dim=66), dict(head_dim=64, scaling=dict(type="x")),
                dict(head_dim=64, scaling=dict(type="linear")), dict(head_dim=64, scaling=dict(type="linear", factor=2.0, low=1.0))):
         with pytest.raises(ValueError):
             Rotary(**kw)

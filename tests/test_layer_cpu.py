@@ -66,8 +66,8 @@ def test_rotate_refusals(lib):
         return lib.talker_rotate(turns, 1.0, hd, rd, 0, pos, streams, rows, None if null else ctypes.addressof(sets), n, dtype, None)
     for kw in (dict(rows=0), dict(streams=0), dict(heads=0)):
         assert call(**kw) == 0, kw
-    for kw in (dict(turns=None), dict(turns=260), dict(pos=None), dict(pos=513), dict(hd=1), dict(hd=1025), dict(rd=0), dict(rd=63), dict(rd=66), dict(streams=-1), dict(rows=-1),
-               dict(n=0), dict(n=3), dict(dtype=2), dict(at=None), dict(out=None), dict(heads=-1), dict(heads=65537), dict(at=1026), dict(out=1025, dtype=1),
+    for kw in (dict(turns=None), dict(turns=260), dict(pos=None), dict(pos=513), dict(hd=1), dict(hd=513), dict(rd=0), dict(rd=63), dict(rd=66), dict(streams=-1), dict(rows=-1),
+               dict(n=0), dict(n=3), dict(dtype=2), dict(at=None), dict(out=None), dict(heads=-1), dict(heads=16385), dict(streams=1 << 16, rows=1 << 15), dict(at=1026), dict(out=1025, dtype=1),
                dict(null=True), dict(n=2)):
         assert call(**kw) == 1, kw
 
