@@ -122,13 +122,15 @@ struct Raw<__nv_bfloat16> {
 // blockDim.x. C chunks stay in registers between the sum and the result, and the next rows' are on their way meanwhile; with
 // C = 0 (rows of more than 16384 values) they are read again. For E4M3 the norm's factor cancels: a code is that of s gain
 // over the largest of its block.
-// Bound by HBM: 4096 x 5120, bf16 and f32 to f32 and e4m3.
-constexpr int kNarrow = 672;   // threads of a row at most, with one chunk: two CTAs of them at 48 registers
+// Threads of a CTA at most. Few threads with several chunks each: what a thread does for a row once is shared by more
+// values, and more CTAs are out of step with one another (4096 x 5120: one chunk of 640 threads 57 us, two of 320 54, four of
+// 160 42).
+constexpr int most_threads(int c) { return c == 0 ? 1024 : c == 4 ? 512 : 128; }
 template <typename TX, typename TR, typename TY, int C>
-__global__ void __launch_bounds__(C == 1 ? kNarrow : 1024, C == 1 ? 2 : 1) k_rms_norm(const NormArgs a) {
+__global__ void __launch_bounds__(most_threads(C), 1) k_rms_norm(const NormArgs a) {
     constexpr bool kRes = !std::is_same<TR, void>::value, k8 = std::is_same<TY, __nv_fp8_storage_t>::value;
     constexpr int H = C > 0 ? C : 1;   // chunks in registers
-    constexpr bool kAhead = C == 1;    // (two chunks of the next row too would not fit in 64 registers)
+    constexpr bool kAhead = C > 0;
     using R = typename std::conditional<kRes, TR, float>::type;
     using Y = typename std::conditional<k8, float, TY>::type;
     __shared__ float sums[2][32], tops[2][32];   // of a row's warps; of every other turn, so that one wait a turn is enough
@@ -156,7 +158,10 @@ __global__ void __launch_bounds__(C == 1 ? kNarrow : 1024, C == 1 ? 2 : 1) k_rms
     };
     int row = blockIdx.x * blockDim.y + threadIdx.y;
     Row now = row_of(row);
-    if (kAhead) fetch(now, 0, x[0], r[0]);
+    if (kAhead) {
+#pragma unroll
+        for (int c = 0; c < H; ++c) fetch(now, c, x[c], r[c]);
+    }
     for (int turn = 0; row - (int)threadIdx.y < a.rows; row += per, turn ^= 1) {   // (all of a CTA's threads together)
         float *const red = sums[turn] + threadIdx.y * warps, *const top = tops[turn] + threadIdx.y * warps;
         float held[H][8];
@@ -169,13 +174,10 @@ __global__ void __launch_bounds__(C == 1 ? kNarrow : 1024, C == 1 ? 2 : 1) k_rms
         };
         const Row next = row_of(row + per < a.rows ? row + per : a.rows);
         if (C > 0) {
-            if (!kAhead) {
-#pragma unroll
-                for (int c = 0; c < H; ++c) fetch(now, c, x[c], r[c]);
-            }
 #pragma unroll
             for (int c = 0; c < H; ++c) sum_of(x[c], r[c], held[c]);
-            if (kAhead) fetch(next, 0, x[0], r[0]);
+#pragma unroll
+            for (int c = 0; c < H; ++c) fetch(next, c, x[c], r[c]);
 #pragma unroll
             for (int c = 0; c < H; ++c) add(held[c]);
         } else {
@@ -249,7 +251,7 @@ __global__ void __launch_bounds__(C == 1 ? kNarrow : 1024, C == 1 ? 2 : 1) k_rms
 using Kernel = void (*)(NormArgs);
 template <typename TX, typename TR, typename TY>
 Kernel by_chunks(int c) {
-    return c == 1 ? k_rms_norm<TX, TR, TY, 1> : c == 2 ? k_rms_norm<TX, TR, TY, 2> : k_rms_norm<TX, TR, TY, 0>;
+    return c == 1 ? k_rms_norm<TX, TR, TY, 1> : c == 4 ? k_rms_norm<TX, TR, TY, 4> : k_rms_norm<TX, TR, TY, 0>;
 }
 template <typename TX, typename TR>
 Kernel by_y(int y, int c) {
@@ -298,14 +300,14 @@ extern "C" talker_status talker_rms_norm(const void *x, int x_dtype, const talke
     if (sum_out) a.sum_at = place(sum_out, res_dtype, sum_at, rows, inner);
     a.y_at = place(y, y_dtype, y_at, rows, inner);
     a.gain_vec = aligned(gain, 32);
-    const int c = width <= 8 * kNarrow ? 1 : width <= 16384 ? 2 : 0;
+    const int c = width <= 256 ? 1 : width <= 4 * 8 * most_threads(4) ? 4 : 0;
     const int threads = c == 0 ? 1024 : (width + 256 * c - 1) / (256 * c) * 32;
     const int per = std::max(1, 128 / threads);
     const dim3 block_dim(threads, per);
     const Kernel k = x_dtype == TALKER_DTYPE_F32 ? by_res<float>(residual != nullptr, res_dtype, y_dtype, c)
                                                  : by_res<__nv_bfloat16>(residual != nullptr, res_dtype, y_dtype, c);
     // as many CTAs as the multiprocessors hold, each with several rows where there are more
-    const int most = 152 * std::max(1, 65536 / (c == 1 ? 48 : 64) / (threads * per));
+    const int registers = c == 4 ? 128 : 64, most = 152 * std::max(1, std::min(32, 65536 / registers / (threads * per)));
     k<<<std::min((rows + per - 1) / per, most), block_dim, 0, static_cast<cudaStream_t>(cuda_stream)>>>(a);
     if (cudaGetLastError() != cudaSuccess) return TALKER_ECUDA;
     return TALKER_OK;
