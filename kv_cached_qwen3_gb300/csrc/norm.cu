@@ -12,7 +12,6 @@ namespace {
 
 struct Place {
     long long outer, inner;
-    bool vec;   // eight values of a row by one access
 };
 struct NormArgs {
     const void *x, *res;
@@ -24,30 +23,34 @@ struct NormArgs {
     int rows, inner, width;
     int block, block_shift, blocks;   // in values (0: a row), its log2, blocks of a row
     float inv_width;
-    bool gain_vec;
+    bool vec;   // eight neighbouring values by one access, in all tensors
 };
 
 __device__ __forceinline__ long long at(const Place &p, int outer, int inner) {
     return inner < 0 ? outer * p.outer : outer * p.outer + inner * p.inner;
 }
 
+// A thread's eight values of a chunk: neighbours from `at` on, or, where rows do not lie on whole accesses, every 32nd (a
+// warp has the same 256 either way, and reads them in whole sectors).
 template <typename T>
-__device__ __forceinline__ void load_row8(const T *p, int i, int width, bool vec, float (&v)[8]) {
-    if (i + 8 <= width) {
-        load8(p + i, vec, v);
+__device__ __forceinline__ void load_row8(const T *p, int at, int width, bool vec, float (&v)[8]) {
+    if (vec && at + 8 <= width) {
+        load8(p + at, true, v);
     } else {
+        const int step = vec ? 1 : 32;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = i + j < width ? Elem<T>::load(p, i + j) : 0.f;
+        for (int j = 0; j < 8; ++j) v[j] = at + j * step < width ? Elem<T>::load(p, at + j * step) : 0.f;
     }
 }
 template <typename T>
-__device__ __forceinline__ void store_row8(T *p, int i, int width, bool vec, const float (&v)[8]) {
-    if (i + 8 <= width) {
-        store8(p + i, vec, v);
+__device__ __forceinline__ void store_row8(T *p, int at, int width, bool vec, const float (&v)[8]) {
+    if (vec && at + 8 <= width) {
+        store8(p + at, true, v);
     } else {
+        const int step = vec ? 1 : 32;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (i + j < width) Elem<T>::store(p, i + j, v[j]);
+            if (at + j * step < width) Elem<T>::store(p, at + j * step, v[j]);
     }
 }
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
@@ -110,9 +113,11 @@ struct Raw<__nv_bfloat16> {
             w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
         } else {
             const unsigned short *q = reinterpret_cast<const unsigned short *>(p);
+            const int step = vec ? 1 : 32;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                w[j] = (i + 2 * j < width ? q[i + 2 * j] : 0u) | (i + 2 * j + 1 < width ? (uint32_t)q[i + 2 * j + 1] : 0u) << 16;
+                w[j] = (i + 2 * j * step < width ? q[i + 2 * j * step] : 0u) |
+                       (i + (2 * j + 1) * step < width ? (uint32_t)q[i + (2 * j + 1) * step] : 0u) << 16;
         }
     }
     __device__ __forceinline__ float at(int j) const { return j & 1 ? bf16hi(w[j / 2]) : bf16lo(w[j / 2]); }
@@ -130,11 +135,12 @@ template <typename TX, typename TR, typename TY, int C>
 __global__ void __launch_bounds__(most_threads(C), 1) k_rms_norm(const NormArgs a) {
     constexpr bool kRes = !std::is_same<TR, void>::value, k8 = std::is_same<TY, __nv_fp8_storage_t>::value;
     constexpr int H = C > 0 ? C : 1;   // chunks in registers
-    constexpr bool kAhead = C > 0;
+    constexpr bool kAhead = C == 4;    // (65536 rows of 128: 29 us without, 39 with)
     using R = typename std::conditional<kRes, TR, float>::type;
     using Y = typename std::conditional<k8, float, TY>::type;
     __shared__ float sums[2][32], tops[2][32];   // of a row's warps; of every other turn, so that one wait a turn is enough
-    const int step = 8 * blockDim.x, first = 8 * threadIdx.x, per = blockDim.y * gridDim.x;
+    const int lane = threadIdx.x & 31, step = 8 * blockDim.x, per = blockDim.y * gridDim.x;
+    const int first = a.vec ? 8 * threadIdx.x : 8 * (threadIdx.x - lane) + lane;
     const int chunks = C > 0 ? C : (a.width + step - 1) / step, warps = blockDim.x >> 5;
     struct Row {
         int outer, inner, width;   // inner -1: rows at one stride; width 0: none
@@ -149,8 +155,8 @@ __global__ void __launch_bounds__(most_threads(C), 1) k_rms_norm(const NormArgs 
     Raw<R> r[H];
     auto fetch = [&](const Row &w, int c, Raw<TX> &x, Raw<R> &r) {
         const int i = c * step + first;
-        x.load(static_cast<const TX *>(a.x) + at(a.x_at, w.outer, w.inner), i, w.width, a.x_at.vec);
-        if (kRes) r.load(static_cast<const R *>(a.res) + at(a.res_at, w.outer, w.inner), i, w.width, a.res_at.vec);
+        x.load(static_cast<const TX *>(a.x) + at(a.x_at, w.outer, w.inner), i, w.width, a.vec);
+        if (kRes) r.load(static_cast<const R *>(a.res) + at(a.res_at, w.outer, w.inner), i, w.width, a.vec);
     };
     auto sum_of = [&](const Raw<TX> &x, const Raw<R> &r, float (&v)[8]) {
 #pragma unroll
@@ -174,10 +180,13 @@ __global__ void __launch_bounds__(most_threads(C), 1) k_rms_norm(const NormArgs 
         };
         const Row next = row_of(row + per < a.rows ? row + per : a.rows);
         if (C > 0) {
+            if (!kAhead) fetch(now, 0, x[0], r[0]);
 #pragma unroll
             for (int c = 0; c < H; ++c) sum_of(x[c], r[c], held[c]);
+            if (kAhead) {
 #pragma unroll
-            for (int c = 0; c < H; ++c) fetch(next, c, x[c], r[c]);
+                for (int c = 0; c < H; ++c) fetch(next, c, x[c], r[c]);
+            }
 #pragma unroll
             for (int c = 0; c < H; ++c) add(held[c]);
         } else {
@@ -193,7 +202,7 @@ __global__ void __launch_bounds__(most_threads(C), 1) k_rms_norm(const NormArgs 
                 fetch(now, c, x[0], r[0]);
                 sum_of(x[0], r[0], v);
             }
-            load_row8(a.gain, c * step + first, a.width, a.gain_vec, g);
+            load_row8(a.gain, c * step + first, a.width, a.vec, g);
 #pragma unroll
             for (int j = 0; j < 8; ++j) g[j] *= v[j];
         };
@@ -213,35 +222,59 @@ __global__ void __launch_bounds__(most_threads(C), 1) k_rms_norm(const NormArgs 
             float g[8];
             take(c, v, g);
             const int i = c * step + first;
-            if (kRes && a.sum != nullptr) store_row8(static_cast<R *>(a.sum) + at(a.sum_at, now.outer, now.inner), i, now.width, a.sum_at.vec, v);
+            if (kRes && a.sum != nullptr) store_row8(static_cast<R *>(a.sum) + at(a.sum_at, now.outer, now.inner), i, now.width, a.vec, v);
             if (k8) {
-                float m = most;
-                if (a.block != 0) {   // its threads are neighbours in a warp
-                    m = max_abs8(g);
-                    for (int o = a.block / 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                }
-                const float d = m * scale;   // max|y|
-                const bool none = d < 0x1p-100f || m < 0x1p-100f;
-                float inv;
-                asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(m));
-                inv = none ? 0.f : d < INFINITY ? 448.f * inv : NAN;
-                if ((a.block == 0 ? i == 0 : (i & (a.block - 1)) == 0) && i < now.width)
-                    a.scales[(size_t)row * a.blocks + (a.block == 0 ? 0 : i >> a.block_shift)] = none ? 0.f : d * (1.f / 448.f);
                 uint8_t *out = static_cast<uint8_t *>(a.y) + at(a.y_at, now.outer, now.inner);
-                const uint2 w = make_uint2(e4m3x4(g[0] * inv, g[1] * inv, g[2] * inv, g[3] * inv),
-                                           e4m3x4(g[4] * inv, g[5] * inv, g[6] * inv, g[7] * inv));
-                if (a.y_at.vec && i + 8 <= now.width) {
-                    *reinterpret_cast<uint2 *>(out + i) = w;
-                } else {
+                // the factor of codes in a block with max|s gain| m, whose scale the thread that is told to writes
+                auto factor = [&](float m, bool writes, int i) -> float {
+                    const float d = m * scale;   // max|y|
+                    const bool none = d < 0x1p-100f || m < 0x1p-100f;
+                    float inv;
+                    asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(m));
+                    if (writes && i < now.width) a.scales[(size_t)row * a.blocks + (a.block == 0 ? 0 : i >> a.block_shift)] = none ? 0.f : d * (1.f / 448.f);
+                    return none ? 0.f : d < INFINITY ? 448.f * inv : NAN;
+                };
+                if (a.vec) {
+                    float m = most;
+                    if (a.block != 0) {   // its threads are neighbours in a warp
+                        m = max_abs8(g);
+                        for (int o = a.block / 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    }
+                    const float inv = factor(m, a.block == 0 ? i == 0 : (i & (a.block - 1)) == 0, i);
+                    const uint2 w = make_uint2(e4m3x4(g[0] * inv, g[1] * inv, g[2] * inv, g[3] * inv),
+                                               e4m3x4(g[4] * inv, g[5] * inv, g[6] * inv, g[7] * inv));
+                    if (i + 8 <= now.width) {
+                        *reinterpret_cast<uint2 *>(out + i) = w;
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (i + j < now.width) out[i + j] = (uint8_t)((j < 4 ? w.x : w.y) >> (8 * (j % 4)));
+                        for (int j = 0; j < 8; ++j)
+                            if (i + j < now.width) out[i + j] = (uint8_t)((j < 4 ? w.x : w.y) >> (8 * (j % 4)));
+                    }
+                } else {   // a block is the whole warp's, of one to four of a thread's values
+                    float m[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) m[j] = fabsf(g[j]);
+                    if (a.block >= 64) {
+#pragma unroll
+                        for (int j = 0; j < 8; j += 2) m[j] = m[j + 1] = fmaxf(m[j], m[j + 1]);
+                    }
+                    if (a.block == 128) {
+#pragma unroll
+                        for (int j = 0; j < 8; j += 4) m[j] = m[j + 1] = m[j + 2] = m[j + 3] = fmaxf(m[j], m[j + 2]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int at = i + 32 * j;
+                        const float t = a.block == 0 ? most : warp_max(m[j]);
+                        const float inv = factor(t, a.block == 0 ? at == 0 : (at & (a.block - 1)) == 0, at);
+                        if (at < now.width) out[at] = (uint8_t)e4m3x4(g[j] * inv, 0.f, 0.f, 0.f);
+                    }
                 }
             } else {
                 float y[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) y[j] = g[j] * scale;
-                store_row8(static_cast<Y *>(a.y) + at(a.y_at, now.outer, now.inner), i, now.width, a.y_at.vec, y);
+                store_row8(static_cast<Y *>(a.y) + at(a.y_at, now.outer, now.inner), i, now.width, a.vec, y);
             }
         }
         now = next;
@@ -268,9 +301,9 @@ int size_of(int t) { return t == TALKER_DTYPE_F32 ? 4 : t == TALKER_DTYPE_BF16 ?
 bool aligned(const void *p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 // Strides of dimensions of one element do not count.
-Place place(const void *p, int dtype, const talker_row_strides *s, int rows, int inner) {
-    Place r{rows > inner ? s->outer : 0, inner > 1 ? s->inner : 0, false};
-    r.vec = aligned(p, 8 * size_of(dtype)) && r.outer % 8 == 0 && r.inner % 8 == 0;
+Place place(const void *p, int dtype, const talker_row_strides *s, int rows, int inner, bool &vec) {
+    const Place r{rows > inner ? s->outer : 0, inner > 1 ? s->inner : 0};
+    vec = vec && aligned(p, 8 * size_of(dtype)) && r.outer % 8 == 0 && r.inner % 8 == 0;
     return r;
 }
 
@@ -295,11 +328,11 @@ extern "C" talker_status talker_rms_norm(const void *x, int x_dtype, const talke
     a.eps = eps, a.rows = rows, a.inner = inner, a.width = width, a.block = y_dtype == TALKER_DTYPE_E4M3 ? block : 0;
     a.block_shift = a.block == 32 ? 5 : a.block == 64 ? 6 : 7, a.blocks = a.block == 0 ? 1 : (width + a.block - 1) / a.block;
     a.inv_width = (float)(1.0 / width);
-    a.x_at = place(x, x_dtype, x_at, rows, inner);
-    if (residual) a.res_at = place(residual, res_dtype, res_at, rows, inner);
-    if (sum_out) a.sum_at = place(sum_out, res_dtype, sum_at, rows, inner);
-    a.y_at = place(y, y_dtype, y_at, rows, inner);
-    a.gain_vec = aligned(gain, 32);
+    a.vec = aligned(gain, 32);
+    a.x_at = place(x, x_dtype, x_at, rows, inner, a.vec);
+    if (residual) a.res_at = place(residual, res_dtype, res_at, rows, inner, a.vec);
+    if (sum_out) a.sum_at = place(sum_out, res_dtype, sum_at, rows, inner, a.vec);
+    a.y_at = place(y, y_dtype, y_at, rows, inner, a.vec);
     const int c = width <= 256 ? 1 : width <= 4 * 8 * most_threads(4) ? 4 : 0;
     const int threads = c == 0 ? 1024 : (width + 256 * c - 1) / (256 * c) * 32;
     const int per = std::max(1, 128 / threads);
@@ -307,8 +340,8 @@ extern "C" talker_status talker_rms_norm(const void *x, int x_dtype, const talke
     const Kernel k = x_dtype == TALKER_DTYPE_F32 ? by_res<float>(residual != nullptr, res_dtype, y_dtype, c)
                                                  : by_res<__nv_bfloat16>(residual != nullptr, res_dtype, y_dtype, c);
     // as many CTAs as the multiprocessors hold, each with several rows where there are more
-    const int registers = c == 4 ? 128 : 64, most = 152 * std::max(1, std::min(32, 65536 / registers / (threads * per)));
-    k<<<std::min((rows + per - 1) / per, most), block_dim, 0, static_cast<cudaStream_t>(cuda_stream)>>>(a);
+    const int all = (rows + per - 1) / per, most = 152 * std::max(1, 65536 / (c == 4 ? 128 : 64) / (threads * per));
+    k<<<std::min(all, most), block_dim, 0, static_cast<cudaStream_t>(cuda_stream)>>>(a);
     if (cudaGetLastError() != cudaSuccess) return TALKER_ECUDA;
     return TALKER_OK;
 }
