@@ -79,7 +79,7 @@ typedef enum {
     TALKER_ROPE_YARN = 4
 } talker_rope_scaling;
 typedef struct {
-    int32_t rotary_dim;  /* even, at least 2 (NTK: at least 4) */
+    int32_t rotary_dim;  /* even, 2 to 512 (NTK: at least 4) */
     int32_t scaling;     /* talker_rope_scaling */
     double theta;        /* above 1 */
     double factor;       /* at least 1 */
@@ -90,6 +90,12 @@ typedef struct {
 /* The table (HOST array of rotary_dim / 2) and amplitude (HOST) of a rope. A host function:
  * the caller copies the table to the device. Errors: EINVAL. */
 talker_status talker_rope_turns(const talker_rope *rope, uint64_t *turns, float *amplitude);
+
+/* A Talker with a scaled rope (talker.h): its positions turn with these frequencies and amplitude, in
+ * prefills, decodes and frames. Before talker_kv_init_batched (ESTATE after it: cached rows
+ * are turned already). rotary_dim must be the handle's head_dim, theta its rope_theta (pairs
+ * are halves). rope is a HOST struct. Errors: EINVAL, ESTATE. */
+talker_status talker_set_rope_scaling(talker_t *t, const talker_rope *rope);
 
 /* Heads of rows: head h of row t of stream s lies at s * stream + t * row + h * head
  * elements; its dims are contiguous. */
@@ -109,47 +115,57 @@ talker_status talker_rotate(const uint64_t *turns, float amplitude, int head_dim
                             int dtype, void *cuda_stream);
 
 /* Products with 4-bit weights. A matrix W of n outputs and k inputs is cut into groups of
- * `group` consecutive inputs (32, 64 or 128; the last one shorter where k is no multiple), each with a
- * scale d (fp16) and, with zeros, a whole number z in 0..15 (8 without): the code c in 0..15
- * stands for (c - z) d. A gated matrix is two of the same sizes, W and U, for silu(W x) * (U x).
+ * `group` consecutive inputs (32, 64 or 128; the last one shorter where k is no multiple),
+ * each with a scale d (fp16) and, with zeros, a whole number z in 0..15 (8 without): the code
+ * c in 0..15 stands for (c - z) d. A gated matrix is two of the same sizes, W and U, for
+ * silu(W x) * (U x).
  *
  * Exchange format (what quantizers write): codes uint8 [n][ceil(k / 2)], input 2 i in the low
- * four bits of byte i and input 2 i + 1 in the high ones; scales fp16 [n][ceil(k / group)]; zeros uint8
- * of the same shape, or NULL. talker_w4_pack lays them out as the kernels read them, in `tiles`:
- *   16 rows to a tile (rows past n are zeros; of a gated matrix 8 rows of W, then the same 8 of U), inputs padded
- *   to a multiple of 128. For each tile and 128 inputs one record, in the order of spans of 32 tiles (the last may have
- *   fewer), in a span of inputs, then of tiles. In a record twice 512 bytes for 64 inputs: 16 of lane l =
- *   4 g + t, words j = 0..3, whose 4-bit fields 0..7 are, with i = 16 j + 4 t: inputs i and i + 1 of row g in fields 0
- *   and 4, i + 2 and i + 3 in fields 1 and 5, and the same of row g + 8 in fields 2, 6, 3, 7 (the operand's registers
- *   of a tensor-core product, one mask away). Then for each group 8 pairs of scales of rows (g, g + 8), and, with
- *   zeros, for each group 8 pairs of bytes; a record is padded to 32 bytes. */
+ * four bits of byte i and input 2 i + 1 in the high ones; scales fp16 [n][ceil(k / group)];
+ * zeros uint8 of the same shape, or NULL. talker_w4_pack lays them out as the kernels read
+ * them, in `tiles`: 16 rows to a tile (rows past n are zeros; of a gated matrix 8 rows of W,
+ * then the same 8 of U), inputs padded to a multiple of 128. For each tile and 128 inputs one
+ * record, in the order of spans of 32 tiles (the last may have fewer), in a span of inputs,
+ * then of tiles. In a record twice 512 bytes for 64 inputs: 16 of lane l = 4 g + t, words
+ * j = 0..3, whose 4-bit fields 0..7 are, with i = 16 j + 4 t: inputs i and i + 1 of row g in
+ * fields 0 and 4, i + 2 and i + 3 in fields 1 and 5, and the same of row g + 8 in fields 2, 6,
+ * 3, 7 (the operand's registers of a tensor-core product, one mask away). Then for each group
+ * 8 pairs of scales of rows (g, g + 8), and, with zeros, for each group 8 pairs of bytes; a
+ * record is padded to 32 bytes. */
 typedef struct {
     void *tiles; /* talker_w4_bytes bytes, 16-byte aligned */
     int32_t n, k, group;
     int32_t zeros, gated; /* 0 or 1 */
 } talker_w4;
-/* Bytes of the tiles (`tiles` is not looked at); 0 for sizes that are not supported: n in 1..2^27, k in 1..2^20. */
+/* Bytes of the tiles (`tiles` is not looked at); 0 for sizes that are not supported: n in
+ * 1..2^27, k in 1..2^20. */
 size_t talker_w4_bytes(const talker_w4 *w);
-/* Lay out a matrix; codes2, scales2 and zeros2 are U's of a gated one (else not looked at). Bits of zeros above
- * the low four are not looked at. Errors: EINVAL, ECUDA. */
+/* Lay out a matrix; codes2, scales2 and zeros2 are U's of a gated one (else not looked at).
+ * Bits of zeros above the low four are not looked at. Errors: EINVAL, ECUDA. */
 talker_status talker_w4_pack(const talker_w4 *w, const uint8_t *codes, const void *scales, const uint8_t *zeros,
                              const uint8_t *codes2, const void *scales2, const uint8_t *zeros2, void *cuda_stream);
-/* Quantize a dense matrix [n] rows of k values (F32 or BF16, row_stride elements apart) to the exchange format
- * without zeros, by the rule of the 4-bit cache (talker_kv4.h) over groups: m the group's value of largest magnitude
- * (the first on ties), clamped to +-524032; d = fp16(-m / 8); code = clamp(floor(8.5 - 8 x / m), 0, 15), decided
- * exactly, 8 where m = 0. A group with a NaN or an infinity gets codes 8 and d = NaN. Errors: EINVAL, ECUDA. */
+/* Quantize a dense matrix, n rows of k values (F32 or BF16, row_stride elements apart), to the
+ * exchange format without zeros, by the rule of the 4-bit cache (talker_kv4.h) over groups: m
+ * the group's value of largest magnitude (the first on ties), clamped to +-524032; d =
+ * fp16(-m / 8); code = clamp(floor(8.5 - 8 x / m), 0, 15), decided exactly, 8 where m = 0. A
+ * group with a NaN or an infinity gets codes 8 and d = NaN. Errors: EINVAL, ECUDA. */
 talker_status talker_w4_quantize(const void *w, int dtype, int64_t row_stride, int n, int k, int group, uint8_t *codes,
                                  void *scales, void *cuda_stream);
-/* out[r] = W x[r] for r < rows, or silu(W x[r]) * (U x[r]) of a gated matrix, plus residual[r] where it is given;
- * silu(g) = g / (1 + exp(-g)).
- * x: rows of k values, x_row elements apart, F32, BF16, or E4M3 with x_scales f32 [rows][ceil(k / x_block)] (x_block 32, 64 or
- * 128; 0: a scale a row), as talker_rms_norm writes them. out: rows of n values, out_row apart, F32 or BF16; residual
- * likewise, res_row apart, in out's type; it may be out itself. Products of codes and x are
- * made by the tensor cores with f32 sums: bf16 x enters exactly (values below 2^-31 of a row's largest lose bits), others with
- * 22 bits in two parts. A row of x with a NaN or an infinity gives NaN. Made for few rows (32 columns of x,
- * one a bf16 row and two any other, in one pass over the weights; more are taken in several), at most 2^16. scratch: talker_w4_scratch bytes, 16-byte aligned,
- * for the same sizes and types; it need not hold anything on entry, and calls that may run at the same
- * time need their own. Errors: EINVAL, ECUDA. */
+/* out[r] = W x[r] for r < rows, or silu(W x[r]) * (U x[r]) of a gated matrix, plus residual[r]
+ * where it is given; silu(g) = g / (1 + exp(-g)).
+ * x: rows of k values, x_row elements apart, F32, BF16, or E4M3 with x_scales f32
+ * [rows][ceil(k / x_block)] (x_block 32, 64 or 128; 0: a scale a row), as talker_rms_norm
+ * writes them. out: rows of n values, out_row apart, F32 or BF16; residual likewise, res_row
+ * apart, in out's type; it may be out itself (same stride). Other overlaps are not allowed.
+ * Products of codes and x are made by the tensor cores with f32 sums: bf16 x enters exactly
+ * (values below 2^-31 of a row's largest lose bits), others with 22 bits in two parts. The order
+ * of a sum depends on n, k, rows and types alone. A row of x with a NaN or an infinity gives
+ * NaN. (So would a copy of weights that does not arrive within a second, from there on.)
+ * Made for few rows: 32 columns of x, one a bf16 row and two any other, in one pass over the
+ * weights; more are taken in several, at most 2^16 rows.
+ * scratch: talker_w4_scratch bytes, 16-byte aligned, for the same sizes and types; it need not
+ * hold anything on entry, and calls that may run at the same time need their own.
+ * Errors: EINVAL, ECUDA. */
 size_t talker_w4_scratch(const talker_w4 *w, int x_dtype, int rows);
 talker_status talker_w4_matmul(const talker_w4 *w, const void *x, int x_dtype, int64_t x_row, const float *x_scales,
                                int x_block, int rows, const void *residual, int64_t res_row, void *out, int out_dtype,

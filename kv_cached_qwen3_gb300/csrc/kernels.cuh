@@ -8,6 +8,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "talker_layer.h"
+
 namespace talker_k {
 
 enum Epilogue : int {
@@ -266,5 +268,8 @@ cudaError_t launch_qkv_post(const float *raw, int rows, int n_q, int n_kv, int h
 // silu(gate) * up of a split-K [gate; up] sum; gu is zeroed behind the read (its split-K
 // accumulation always starts from zeros).
 cudaError_t launch_swiglu_bf16(float *gu, int rows, int I, void *out, cudaStream_t st);
+
+// Frequencies (radians a position, rotary_dim / 2 of them) and amplitude of a rope (rotary.cu); false: EINVAL.
+bool rope_frequencies(const talker_rope &r, double *freq, double *amplitude);
 
 }  // namespace talker_k

@@ -2,6 +2,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "kernels.cuh"
 #include "rows.cuh"
 #include "talker_layer.h"
 
@@ -9,6 +10,8 @@ using namespace talker_dev;
 
 namespace {
 
+constexpr double kPi = 3.14159265358979323846;
+constexpr int kMostDims = 512;      // of a head
 constexpr int kMostThreads = 512;   // groups of a head at most: of one dim and another, or of two neighbours
 
 struct RotateArgs {
@@ -143,37 +146,46 @@ void launch(const RotateArgs &a, int slices, bool interleaved, cudaStream_t st) 
 
 }  // namespace
 
+namespace talker_k {
+
+bool rope_frequencies(const talker_rope &r, double *freq, double *amplitude) {
+    if (r.rotary_dim < 2 || r.rotary_dim % 2 || r.scaling < TALKER_ROPE_NONE || r.scaling > TALKER_ROPE_YARN) return false;
+    const bool ranged = r.scaling == TALKER_ROPE_SMOOTH || r.scaling == TALKER_ROPE_YARN;
+    if (!(r.theta > 1.0) || !std::isfinite(r.theta)) return false;
+    if (r.scaling != TALKER_ROPE_NONE && (!(r.factor >= 1.0) || !std::isfinite(r.factor))) return false;
+    if (r.scaling == TALKER_ROPE_NTK && r.rotary_dim < 4) return false;
+    if (ranged && (!(r.original > 0.0) || !std::isfinite(r.original) || !(r.low > 0.0) || !(r.high > r.low) || !std::isfinite(r.high))) return false;
+    if (r.scaling == TALKER_ROPE_YARN && (!(r.amplitude >= 0.0) || !std::isfinite(r.amplitude))) return false;
+    const double d = r.rotary_dim;
+    double lo = 0.0, hi = 0.0, theta = r.theta;
+    *amplitude = 1.0;
+    if (r.scaling == TALKER_ROPE_NTK) theta *= std::pow(r.factor, d / (d - 2.0));
+    if (r.scaling == TALKER_ROPE_YARN) {
+        auto pair = [&](double beta) { return d * std::log(r.original / (2.0 * kPi * beta)) / (2.0 * std::log(r.theta)); };
+        lo = std::max(0.0, std::floor(pair(r.high)));
+        hi = std::min(d - 1.0, std::ceil(pair(r.low)));
+        *amplitude = r.amplitude > 0.0 ? r.amplitude : 0.1 * std::log(r.factor) + 1.0;
+    }
+    for (int i = 0; i < r.rotary_dim / 2; ++i) {
+        double f = std::pow(theta, -2.0 * i / d), keep = 1.0;
+        if (r.scaling == TALKER_ROPE_LINEAR) keep = 0.0;
+        if (r.scaling == TALKER_ROPE_SMOOTH) keep = std::min(1.0, std::max(0.0, (r.original * f / (2.0 * kPi) - r.low) / (r.high - r.low)));
+        if (r.scaling == TALKER_ROPE_YARN) keep = 1.0 - std::min(1.0, std::max(0.0, (i - lo) / std::max(hi - lo, 0.001)));
+        freq[i] = keep < 1.0 ? f * keep + f / r.factor * (1.0 - keep) : f;
+    }
+    return true;
+}
+
+}  // namespace talker_k
+
 extern "C" {
 
 talker_status talker_rope_turns(const talker_rope *r, uint64_t *turns, float *amplitude) {
-    if (!r || !turns || !amplitude || r->rotary_dim < 2 || r->rotary_dim % 2 || r->rotary_dim > 1 << 20) return TALKER_EINVAL;
-    if (!(r->theta > 1.0) || !std::isfinite(r->theta)) return TALKER_EINVAL;
-    const double pi = 3.14159265358979323846, d = r->rotary_dim;
-    const bool ranged = r->scaling == TALKER_ROPE_SMOOTH || r->scaling == TALKER_ROPE_YARN;
-    if (r->scaling < TALKER_ROPE_NONE || r->scaling > TALKER_ROPE_YARN) return TALKER_EINVAL;
-    if (r->scaling != TALKER_ROPE_NONE && (!(r->factor >= 1.0) || !std::isfinite(r->factor))) return TALKER_EINVAL;
-    if (r->scaling == TALKER_ROPE_NTK && r->rotary_dim < 4) return TALKER_EINVAL;
-    if (ranged && (!(r->original > 0.0) || !std::isfinite(r->original) || !(r->low > 0.0) || !(r->high > r->low) || !std::isfinite(r->high)))
-        return TALKER_EINVAL;
-    *amplitude = 1.0f;
-    double lo = 0.0, hi = 0.0, theta = r->theta;
-    if (r->scaling == TALKER_ROPE_NTK) theta *= std::pow(r->factor, d / (d - 2.0));
-    if (r->scaling == TALKER_ROPE_YARN) {
-        if (!(r->amplitude >= 0.0) || !std::isfinite(r->amplitude)) return TALKER_EINVAL;
-        auto pair = [&](double beta) { return d * std::log(r->original / (2.0 * pi * beta)) / (2.0 * std::log(r->theta)); };
-        lo = std::max(0.0, std::floor(pair(r->high)));
-        hi = std::min(d - 1.0, std::ceil(pair(r->low)));
-        *amplitude = (float)(r->amplitude > 0.0 ? r->amplitude : 0.1 * std::log(r->factor) + 1.0);
-    }
-    for (int i = 0; i < r->rotary_dim / 2; ++i) {
-        double f = std::pow(theta, -2.0 * i / d), keep = 1.0;
-        if (r->scaling == TALKER_ROPE_LINEAR) keep = 0.0;
-        if (r->scaling == TALKER_ROPE_SMOOTH)
-            keep = std::min(1.0, std::max(0.0, (r->original * f / (2.0 * pi) - r->low) / (r->high - r->low)));
-        if (r->scaling == TALKER_ROPE_YARN) keep = 1.0 - std::min(1.0, std::max(0.0, (i - lo) / std::max(hi - lo, 0.001)));
-        if (keep < 1.0) f = f * keep + f / r->factor * (1.0 - keep);
-        turns[i] = (uint64_t)std::llround(std::ldexp(f / (2.0 * pi), 64));   // (f is at most 1 radian)
-    }
+    if (!r || !turns || !amplitude || r->rotary_dim < 2 || r->rotary_dim > kMostDims) return TALKER_EINVAL;
+    double freq[kMostDims / 2], amp;
+    if (!talker_k::rope_frequencies(*r, freq, &amp)) return TALKER_EINVAL;
+    for (int i = 0; i < r->rotary_dim / 2; ++i) turns[i] = (uint64_t)std::llround(std::ldexp(freq[i] / (2.0 * kPi), 64));   // (at most 1 radian)
+    *amplitude = (float)amp;
     return TALKER_OK;
 }
 
@@ -181,7 +193,7 @@ talker_status talker_rotate(const uint64_t *turns, float amplitude, int head_dim
                             const int32_t *positions, int streams, int rows, const talker_heads *sets, int n_sets,
                             int dtype, void *cuda_stream) {
     if (!turns || !positions || !sets || n_sets < 1 || n_sets > 2 || streams < 0 || rows < 0) return TALKER_EINVAL;
-    if (head_dim < 2 || head_dim > 512 || rotary_dim < 2 || rotary_dim % 2 || rotary_dim > head_dim) return TALKER_EINVAL;
+    if (head_dim < 2 || head_dim > kMostDims || rotary_dim < 2 || rotary_dim % 2 || rotary_dim > head_dim) return TALKER_EINVAL;
     if (dtype != TALKER_DTYPE_F32 && dtype != TALKER_DTYPE_BF16) return TALKER_EINVAL;
     const int size = dtype == TALKER_DTYPE_F32 ? 4 : 2;
     if (reinterpret_cast<uintptr_t>(turns) % 8 || reinterpret_cast<uintptr_t>(positions) % 4) return TALKER_EINVAL;

@@ -96,6 +96,8 @@ struct talker {
     float *q4_ws = nullptr;              // Q4_0 storage: parts of rows that several CTAs attend
     float *kv_rows = nullptr;            // Q4_0 storage: a step's own k / v rows, f32 [2][rows][n_kv][hd]
     float2 *d_rope = nullptr;
+    double rope_freq[64] = {};   // radians a position (head_dim is at most 128)
+    double rope_amplitude = 1.0;
     std::vector<int> len;
     // activations, sized for cap_rows rows
     int cap_rows = 0;
@@ -955,6 +957,7 @@ talker_status talker_create(const talker_config *cfg, const talker_weight_ptrs *
     t->kv_bf16 = cfg->kv_dtype == TALKER_DTYPE_BF16;
     t->kv_q8 = cfg->kv_dtype == TALKER_DTYPE_Q8_0;
     t->kv_q4 = cfg->kv_dtype == TALKER_DTYPE_Q4_0;
+    for (int i = 0; i < cfg->head_dim / 2; ++i) t->rope_freq[i] = std::pow((double)cfg->rope_theta, -2.0 * i / cfg->head_dim);
     t->kv_quant = t->kv_q8 || t->kv_q4;
     t->kv_kind = t->kv_q4 ? 3 : t->kv_q8 ? 2 : (t->kv_bf16 ? 1 : 0);
     t->wsz = t->w_bf16 ? 2 : 4;
@@ -1021,14 +1024,14 @@ talker_status talker_kv_init_batched(talker_t *t, int n_streams, int max_seq_len
     }
     TRY_CUDA(cudaMalloc(&t->d_len, n_streams * sizeof(int)));
     TRY_CUDA(cudaMemsetAsync(t->d_len, 0, n_streams * sizeof(int), t->st));
-    // RoPE table: angle p * theta^(-2i/hd) evaluated in double on the host, stored as f32 (cos, sin)
+    // RoPE table: angles p f_i evaluated in double on the host, stored as f32 (cos, sin); f_i = theta^(-2i/hd), or as
+    // talker_set_rope_scaling changes them
     const int half = t->hd / 2;
     std::vector<float2> rope((size_t)max_seq_len * half);
     for (int i = 0; i < half; ++i) {
-        const double inv = std::pow((double)t->c.rope_theta, -2.0 * i / t->hd);
         for (int pos = 0; pos < max_seq_len; ++pos) {
-            const double ang = pos * inv;
-            rope[(size_t)pos * half + i] = make_float2((float)std::cos(ang), (float)std::sin(ang));
+            const double ang = pos * t->rope_freq[i], amp = t->rope_amplitude;
+            rope[(size_t)pos * half + i] = make_float2((float)(amp * std::cos(ang)), (float)(amp * std::sin(ang)));
         }
     }
     TRY_CUDA(cudaMalloc(&t->d_rope, rope.size() * sizeof(float2)));
@@ -1290,6 +1293,16 @@ talker_status talker_test_gemm_swiglu_bf16(const void *A, int M, int K, const vo
     }
     TRY_CUDA(cudaMemcpy(&h, d_status, sizeof(int), cudaMemcpyDeviceToHost));
     return h ? TALKER_EDEVICE : TALKER_OK;
+}
+
+talker_status talker_set_rope_scaling(talker_t *t, const talker_rope *rope) {
+    if (!t || !rope || rope->rotary_dim != t->hd || rope->theta != (double)t->c.rope_theta) return TALKER_EINVAL;
+    double freq[64], amplitude = 1.0;
+    if (!talker_k::rope_frequencies(*rope, freq, &amplitude)) return TALKER_EINVAL;
+    if (t->d_rope) return TALKER_ESTATE;   // (rows are cached as they were turned)
+    std::copy(freq, freq + t->hd / 2, t->rope_freq);
+    t->rope_amplitude = amplitude;
+    return TALKER_OK;
 }
 
 talker_status talker_set_logit_suppression(talker_t *t, int vocab_tail, int eos_id) {

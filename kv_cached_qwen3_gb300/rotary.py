@@ -22,6 +22,18 @@ class _Heads(ctypes.Structure):
         (n, ctypes.c_int64) for n in ("in_stream", "in_row", "in_head", "out_stream", "out_row", "out_head")]
 
 
+def make_rope(rotary_dim: int, theta: float, scaling: dict | None) -> _Rope:
+    """The C struct of a rope with a scaling as Rotary describes it."""
+    given = dict(scaling or {"type": "none"})
+    kind = given.pop("type", None)
+    names = {"none": (), "linear": ("factor",), "ntk": ("factor",), "smooth": ("factor", "original", "low", "high"),
+             "yarn": ("factor", "original", "beta_slow", "beta_fast")}.get(kind)
+    if names is None or not set(names) <= set(given) or set(given) - set(names) - ({"amplitude"} if kind == "yarn" else set()):
+        raise ValueError("rotary positions: scaling %r" % (scaling,))
+    v = [float(given[n]) for n in names]
+    return _Rope(rotary_dim, SCALINGS[kind], theta, *(v + [0.0] * (4 - len(v))), float(given.get("amplitude", 0.0)))
+
+
 class Rotary:
     """The plan of a rope: its table of frequencies on a device.
 
@@ -36,14 +48,7 @@ class Rotary:
         rotary_dim = head_dim if rotary_dim is None else rotary_dim
         if not 2 <= head_dim <= 512 or rotary_dim < 2 or rotary_dim % 2 or rotary_dim > head_dim:
             raise ValueError("Rotary: needs head_dim 2 to 512 and an even rotary_dim of at most head_dim")
-        given = dict(scaling or {"type": "none"})
-        kind = given.pop("type", None)
-        names = {"none": (), "linear": ("factor",), "ntk": ("factor",), "smooth": ("factor", "original", "low", "high"),
-                 "yarn": ("factor", "original", "beta_slow", "beta_fast")}.get(kind)
-        if names is None or not set(names) <= set(given) or set(given) - set(names) - ({"amplitude"} if kind == "yarn" else set()):
-            raise ValueError("Rotary: scaling %r" % (scaling,))
-        v = [float(given[n]) for n in names]
-        rope = _Rope(rotary_dim, SCALINGS[kind], theta, *(v + [0.0] * (4 - len(v))), float(given.get("amplitude", 0.0)))
+        rope = make_rope(rotary_dim, theta, scaling)
         table = np.empty(rotary_dim // 2, np.uint64)
         amplitude = ctypes.c_float()
         lib = load_library()

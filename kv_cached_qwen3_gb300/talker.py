@@ -104,6 +104,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "talker_rms_norm": (st, [vp, ctypes.c_int, vp, vp, ctypes.c_int, vp, vp, ctypes.c_float] + [ctypes.c_int] * 3 +
                             [vp, vp, vp, ctypes.c_int, vp, ctypes.c_int, vp, vp]),
         "talker_rope_turns": (st, [vp, vp, ctypes.POINTER(ctypes.c_float)]),
+        "talker_set_rope_scaling": (st, [vp, vp]),
         "talker_rotate": (st, [vp, ctypes.c_float] + [ctypes.c_int] * 3 + [vp, ctypes.c_int, ctypes.c_int, vp, ctypes.c_int,
                                                                            ctypes.c_int, vp]),
         "talker_draft_scratch": (ctypes.c_size_t, [ctypes.c_int] * 3),
@@ -263,6 +264,12 @@ class Talker:
 
     def set_logit_suppression(self, vocab_tail: int, eos_id: int):
         self._check(self.lib.talker_set_logit_suppression(self.h, vocab_tail, eos_id), "talker_set_logit_suppression")
+
+    def set_rope_scaling(self, scaling: dict):
+        """Scaled rotary positions (see rotary.Rotary for the dict), before kv_init_batched."""
+        from .rotary import make_rope
+        rope = make_rope(self.g.head_dim, ctypes.c_float(self.g.rope_theta).value, scaling)
+        self._check(self.lib.talker_set_rope_scaling(self.h, ctypes.byref(rope)), "talker_set_rope_scaling")
 
     def set_code_tables(self, tables, dtype_bf16: bool):
         """tables: list of cuda tensors [V_g, H] (kept referenced by this object while registered)."""

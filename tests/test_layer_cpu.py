@@ -135,3 +135,7 @@ def test_draft_reference_on_hand_cases():
     assert ref.verify(t, [2], [0.2, 0.31])[:2] == ([2, 2], 1)
     assert ref.verify(t, [1], [0.0, 0.5], temp=0.0)[:2] == ([0, -1], 0)
     assert ref.verify(t, [0], [0.0, 0.5], temp=0.0)[:2] == ([0, 2], 1)
+
+
+def test_rope_scaling_of_a_talker_refusals(lib):
+    assert lib.talker_set_rope_scaling(None, None) == 1
