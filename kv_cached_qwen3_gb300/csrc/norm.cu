@@ -2,6 +2,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "rows.cuh"
 #include "talker_layer.h"
@@ -23,34 +24,40 @@ struct NormArgs {
     int rows, inner, width;
     int block, block_shift, blocks;   // in values (0: a row), its log2, blocks of a row
     float inv_width;
-    bool vec;   // eight neighbouring values by one access, in all tensors
 };
 
 __device__ __forceinline__ long long at(const Place &p, int outer, int inner) {
     return inner < 0 ? outer * p.outer : outer * p.outer + inner * p.inner;
 }
 
-// A thread's eight values of a chunk: neighbours from `at` on, or, where rows do not lie on whole accesses, every 32nd (a
-// warp has the same 256 either way, and reads them in whole sectors).
+struct Row {
+    int outer, inner, width;   // inner -1: rows at one stride; width 0: none
+};
+__device__ __forceinline__ Row place_of(const NormArgs &a, int row) {
+    if (row >= a.rows) return {0, -1, 0};
+    if (a.inner == 1) return {row, -1, a.width};
+    const int outer = (unsigned)row / (unsigned)a.inner;
+    return {outer, row - outer * a.inner, a.width};
+}
+
+// Eight neighbouring values of a row, at its end those that it has.
 template <typename T>
-__device__ __forceinline__ void load_row8(const T *p, int at, int width, bool vec, float (&v)[8]) {
-    if (vec && at + 8 <= width) {
+__device__ __forceinline__ void load_row8(const T *p, int at, int width, float (&v)[8]) {
+    if (at + 8 <= width) {
         load8(p + at, true, v);
     } else {
-        const int step = vec ? 1 : 32;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = at + j * step < width ? Elem<T>::load(p, at + j * step) : 0.f;
+        for (int j = 0; j < 8; ++j) v[j] = at + j < width ? Elem<T>::load(p, at + j) : 0.f;
     }
 }
 template <typename T>
-__device__ __forceinline__ void store_row8(T *p, int at, int width, bool vec, const float (&v)[8]) {
-    if (vec && at + 8 <= width) {
+__device__ __forceinline__ void store_row8(T *p, int at, int width, const float (&v)[8]) {
+    if (at + 8 <= width) {
         store8(p + at, true, v);
     } else {
-        const int step = vec ? 1 : 32;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (at + j * step < width) Elem<T>::store(p, at + j * step, v[j]);
+            if (at + j < width) Elem<T>::store(p, at + j, v[j]);
     }
 }
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
@@ -95,29 +102,40 @@ __device__ __forceinline__ float root(float x) {
     return r > 0.f && r < INFINITY ? better : r;
 }
 
+// Of a block with max|s gain| m, in a row whose norm's factor is `norm`: its scale, and what s gain is multiplied by for codes.
+struct Scale {
+    float scale, codes;
+    __device__ __forceinline__ Scale(float m, float norm) {
+        const float d = m * norm;   // max|y|
+        const bool none = d < 0x1p-100f || m < 0x1p-100f;
+        float inv;
+        asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(m));
+        scale = none ? 0.f : d * (1.f / 448.f);
+        codes = none ? 0.f : d < INFINITY ? 448.f * inv : NAN;
+    }
+};
+
 // Eight values of a row as they lie in memory, so that nothing waits for them until they are used.
 template <typename T>
 struct Raw;
 template <>
 struct Raw<float> {
     float v[8];
-    __device__ __forceinline__ void load(const float *p, int i, int width, bool vec) { load_row8(p, i, width, vec, v); }
+    __device__ __forceinline__ void load(const float *p, int i, int width) { load_row8(p, i, width, v); }
     __device__ __forceinline__ float at(int j) const { return v[j]; }
 };
 template <>
 struct Raw<__nv_bfloat16> {
     uint32_t w[4];
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p, int i, int width, bool vec) {
-        if (vec && i + 8 <= width) {
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p, int i, int width) {
+        if (i + 8 <= width) {
             const uint4 u = *reinterpret_cast<const uint4 *>(p + i);
             w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
         } else {
             const unsigned short *q = reinterpret_cast<const unsigned short *>(p);
-            const int step = vec ? 1 : 32;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                w[j] = (i + 2 * j * step < width ? q[i + 2 * j * step] : 0u) |
-                       (i + (2 * j + 1) * step < width ? (uint32_t)q[i + (2 * j + 1) * step] : 0u) << 16;
+                w[j] = (i + 2 * j < width ? q[i + 2 * j] : 0u) | (i + 2 * j + 1 < width ? (uint32_t)q[i + 2 * j + 1] : 0u) << 16;
         }
     }
     __device__ __forceinline__ float at(int j) const { return j & 1 ? bf16hi(w[j / 2]) : bf16lo(w[j / 2]); }
@@ -130,33 +148,25 @@ struct Raw<__nv_bfloat16> {
 // Threads of a CTA at most. Few threads with several chunks each: what a thread does for a row once is shared by more
 // values, and more CTAs are out of step with one another (4096 x 5120: one chunk of 640 threads 57 us, two of 320 54, four of
 // 160 42).
-constexpr int most_threads(int c) { return c == 0 ? 1024 : c == 4 ? 512 : 128; }
+constexpr int most_threads(int c) { return c == 0 ? 1024 : 512; }
 template <typename TX, typename TR, typename TY, int C>
 __global__ void __launch_bounds__(most_threads(C), 1) k_rms_norm(const NormArgs a) {
     constexpr bool kRes = !std::is_same<TR, void>::value, k8 = std::is_same<TY, __nv_fp8_storage_t>::value;
     constexpr int H = C > 0 ? C : 1;   // chunks in registers
-    constexpr bool kAhead = C == 4;    // (65536 rows of 128: 29 us without, 39 with)
+    constexpr bool kAhead = C > 0;
     using R = typename std::conditional<kRes, TR, float>::type;
     using Y = typename std::conditional<k8, float, TY>::type;
     __shared__ float sums[2][32], tops[2][32];   // of a row's warps; of every other turn, so that one wait a turn is enough
-    const int lane = threadIdx.x & 31, step = 8 * blockDim.x, per = blockDim.y * gridDim.x;
-    const int first = a.vec ? 8 * threadIdx.x : 8 * (threadIdx.x - lane) + lane;
+    const int step = 8 * blockDim.x, per = blockDim.y * gridDim.x;
+    const int first = 8 * threadIdx.x;
     const int chunks = C > 0 ? C : (a.width + step - 1) / step, warps = blockDim.x >> 5;
-    struct Row {
-        int outer, inner, width;   // inner -1: rows at one stride; width 0: none
-    };
-    auto row_of = [&](int row) -> Row {
-        if (row >= a.rows) return {0, -1, 0};
-        if (a.inner == 1) return {row, -1, a.width};
-        const int outer = (unsigned)row / (unsigned)a.inner;
-        return {outer, row - outer * a.inner, a.width};
-    };
+    auto row_of = [&](int row) { return place_of(a, row); };
     Raw<TX> x[H];
     Raw<R> r[H];
     auto fetch = [&](const Row &w, int c, Raw<TX> &x, Raw<R> &r) {
         const int i = c * step + first;
-        x.load(static_cast<const TX *>(a.x) + at(a.x_at, w.outer, w.inner), i, w.width, a.vec);
-        if (kRes) r.load(static_cast<const R *>(a.res) + at(a.res_at, w.outer, w.inner), i, w.width, a.vec);
+        x.load(static_cast<const TX *>(a.x) + at(a.x_at, w.outer, w.inner), i, w.width);
+        if (kRes) r.load(static_cast<const R *>(a.res) + at(a.res_at, w.outer, w.inner), i, w.width);
     };
     auto sum_of = [&](const Raw<TX> &x, const Raw<R> &r, float (&v)[8]) {
 #pragma unroll
@@ -202,7 +212,7 @@ __global__ void __launch_bounds__(most_threads(C), 1) k_rms_norm(const NormArgs 
                 fetch(now, c, x[0], r[0]);
                 sum_of(x[0], r[0], v);
             }
-            load_row8(a.gain, c * step + first, a.width, a.vec, g);
+            load_row8(a.gain, c * step + first, a.width, g);
 #pragma unroll
             for (int j = 0; j < 8; ++j) g[j] *= v[j];
         };
@@ -222,78 +232,222 @@ __global__ void __launch_bounds__(most_threads(C), 1) k_rms_norm(const NormArgs 
             float g[8];
             take(c, v, g);
             const int i = c * step + first;
-            if (kRes && a.sum != nullptr) store_row8(static_cast<R *>(a.sum) + at(a.sum_at, now.outer, now.inner), i, now.width, a.vec, v);
+            if (kRes && a.sum != nullptr) store_row8(static_cast<R *>(a.sum) + at(a.sum_at, now.outer, now.inner), i, now.width, v);
             if (k8) {
                 uint8_t *out = static_cast<uint8_t *>(a.y) + at(a.y_at, now.outer, now.inner);
-                // the factor of codes in a block with max|s gain| m, whose scale the thread that is told to writes
-                auto factor = [&](float m, bool writes, int i) -> float {
-                    const float d = m * scale;   // max|y|
-                    const bool none = d < 0x1p-100f || m < 0x1p-100f;
-                    float inv;
-                    asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(m));
-                    if (writes && i < now.width) a.scales[(size_t)row * a.blocks + (a.block == 0 ? 0 : i >> a.block_shift)] = none ? 0.f : d * (1.f / 448.f);
-                    return none ? 0.f : d < INFINITY ? 448.f * inv : NAN;
-                };
-                if (a.vec) {
-                    float m = most;
-                    if (a.block != 0) {   // its threads are neighbours in a warp
-                        m = max_abs8(g);
-                        for (int o = a.block / 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                    }
-                    const float inv = factor(m, a.block == 0 ? i == 0 : (i & (a.block - 1)) == 0, i);
-                    const uint2 w = make_uint2(e4m3x4(g[0] * inv, g[1] * inv, g[2] * inv, g[3] * inv),
-                                               e4m3x4(g[4] * inv, g[5] * inv, g[6] * inv, g[7] * inv));
-                    if (i + 8 <= now.width) {
-                        *reinterpret_cast<uint2 *>(out + i) = w;
-                    } else {
+                float m = most;
+                if (a.block != 0) {   // its threads are neighbours in a warp
+                    m = max_abs8(g);
+                    for (int o = a.block / 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                }
+                const Scale f(m, scale);
+                if (i < now.width && (a.block == 0 ? i == 0 : (i & (a.block - 1)) == 0)) a.scales[(size_t)row * a.blocks + (a.block == 0 ? 0 : i >> a.block_shift)] = f.scale;
+                const uint2 w = make_uint2(e4m3x4(g[0] * f.codes, g[1] * f.codes, g[2] * f.codes, g[3] * f.codes),
+                                           e4m3x4(g[4] * f.codes, g[5] * f.codes, g[6] * f.codes, g[7] * f.codes));
+                if (i + 8 <= now.width) {
+                    *reinterpret_cast<uint2 *>(out + i) = w;
+                } else {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (i + j < now.width) out[i + j] = (uint8_t)((j < 4 ? w.x : w.y) >> (8 * (j % 4)));
-                    }
-                } else {   // a block is the whole warp's, of one to four of a thread's values
-                    float m[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) m[j] = fabsf(g[j]);
-                    if (a.block >= 64) {
-#pragma unroll
-                        for (int j = 0; j < 8; j += 2) m[j] = m[j + 1] = fmaxf(m[j], m[j + 1]);
-                    }
-                    if (a.block == 128) {
-#pragma unroll
-                        for (int j = 0; j < 8; j += 4) m[j] = m[j + 1] = m[j + 2] = m[j + 3] = fmaxf(m[j], m[j + 2]);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int at = i + 32 * j;
-                        const float t = a.block == 0 ? most : warp_max(m[j]);
-                        const float inv = factor(t, a.block == 0 ? at == 0 : (at & (a.block - 1)) == 0, at);
-                        if (at < now.width) out[at] = (uint8_t)e4m3x4(g[j] * inv, 0.f, 0.f, 0.f);
-                    }
+                    for (int j = 0; j < 8; ++j)
+                        if (i + j < now.width) out[i + j] = (uint8_t)((j < 4 ? w.x : w.y) >> (8 * (j % 4)));
                 }
             } else {
                 float y[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) y[j] = g[j] * scale;
-                store_row8(static_cast<Y *>(a.y) + at(a.y_at, now.outer, now.inner), i, now.width, a.vec, y);
+                store_row8(static_cast<Y *>(a.y) + at(a.y_at, now.outer, now.inner), i, now.width, y);
             }
         }
         now = next;
     }
 }
 
-using Kernel = void (*)(NormArgs);
-template <typename TX, typename TR, typename TY>
-Kernel by_chunks(int c) {
-    return c == 1 ? k_rms_norm<TX, TR, TY, 1> : c == 4 ? k_rms_norm<TX, TR, TY, 4> : k_rms_norm<TX, TR, TY, 0>;
+// Rows that no vector access fits (odd widths, strides or starts), and narrow ones. blockDim.x threads share a row: a warp reads
+// 32 neighbouring values of it at a time. STAGED: rows pass through shared memory, where the next ones arrive while these
+// are worked on, in whole 16 bytes but for their ends; otherwise (rows that do not fit there) they are read twice.
+constexpr int kOddThreads = 512, kTileRows = 8;
+constexpr int kMostStaged = 220 * 1024;
+__host__ __device__ constexpr int slot_bytes(int width, int size) { return (width * size + 31) & ~15; }   // at any offset in 16 bytes
+
+__device__ __forceinline__ void copy_async(uint32_t to, const char *from, bool sixteen) {
+    if (sixteen)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
 }
+// One value of two bytes at a row's odd end: loaded when the row's copies begin, stored when they are waited for.
+struct End {
+    unsigned short value;
+    int to = -1;   // in shared memory
+};
+// A row of n bytes to a slot, by `threads` threads; those with t / 2 == turn take its odd ends.
+__device__ __forceinline__ void stage_row(char *smem, int slot, const char *p, int n, int t, int threads, bool ends, End &end) {
+    const int off = (int)(reinterpret_cast<uintptr_t>(p) & 15);
+    const int low = min((16 - off) & 15, n), high = max(low, ((off + n) & ~15) - off);   // whole 16 bytes
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(smem + slot + off);
+    for (int u = low + 16 * t; u < high; u += 16 * threads) copy_async(to + u, p + u, true);
+    // words before and after
+    if (t < 8) {
+        const int u = t < 4 ? ((4 - off) & 3) + 4 * t : high + (t - 4) * 4;
+        const int first = (4 - off) & 3;
+        if (t < 4 ? u + 4 <= low : u + 4 <= n && u >= first) copy_async(to + u, p + u, false);
+    }
+    if (ends) {
+        const int u = t & 1 ? n - 2 : 0;
+        if ((off + (t & 1 ? n : 0)) & 2) end.value = *reinterpret_cast<const unsigned short *>(p + u), end.to = slot + off + u;
+    }
+}
+
+template <typename TX, typename TR, typename TY, bool STAGED>
+__global__ void __launch_bounds__(kOddThreads, 2) k_rms_norm_odd(const NormArgs a, const int tile) {
+    constexpr bool kRes = !std::is_same<TR, void>::value, k8 = std::is_same<TY, __nv_fp8_storage_t>::value;
+    using R = typename std::conditional<kRes, TR, float>::type;
+    using Y = typename std::conditional<k8, float, TY>::type;
+    extern __shared__ __align__(16) char smem[];
+    __shared__ float sums[2][32], tops[2][32];
+    const int t = threadIdx.x, threads = blockDim.x, lane = t & 31, warps = threads >> 5, width = a.width;
+    const int x_slot = slot_bytes(width, sizeof(TX)), slot = x_slot + (kRes ? slot_bytes(width, sizeof(R)) : 0);
+    const int per = blockDim.y * tile * gridDim.x;
+    End x_end, r_end;
+    auto x_of = [&](const Row &w) { return static_cast<const TX *>(a.x) + at(a.x_at, w.outer, w.inner); };
+    auto r_of = [&](const Row &w) { return static_cast<const R *>(a.res) + at(a.res_at, w.outer, w.inner); };
+    auto slot_of = [&](int turn, int k) { return (((turn & 1) * (int)blockDim.y + (int)threadIdx.y) * tile + k) * slot; };
+    auto issue = [&](int first, int turn) {
+        for (int k = 0; k < tile && first + k < a.rows; ++k) {
+            const Row w = place_of(a, first + k);
+            const bool ends = t >> 1 == k;
+            stage_row(smem, slot_of(turn, k), reinterpret_cast<const char *>(x_of(w)), width * (int)sizeof(TX), t, threads, sizeof(TX) == 2 && ends, x_end);
+            if (kRes) stage_row(smem, slot_of(turn, k) + x_slot, reinterpret_cast<const char *>(r_of(w)), width * (int)sizeof(R), t, threads, sizeof(R) == 2 && ends, r_end);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int first = (blockIdx.x * blockDim.y + threadIdx.y) * tile;
+    if (STAGED) issue(first, 0);
+    for (int turn = 0; first - (int)threadIdx.y * tile < a.rows; first += per, ++turn) {   // (all of a CTA's threads together)
+        if (STAGED) {
+            if (x_end.to >= 0) *reinterpret_cast<unsigned short *>(smem + x_end.to) = x_end.value;
+            if (kRes && r_end.to >= 0) *reinterpret_cast<unsigned short *>(smem + r_end.to) = r_end.value;
+            x_end.to = r_end.to = -1;
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            if (warps == 1) __syncwarp();
+            else __syncthreads();
+            issue(first + per, turn + 1);   // to the slots that the last turn is done with
+        }
+        for (int k = 0; k < tile; ++k) {
+            const Row now = place_of(a, first + k);
+            if (warps == 1 && now.width == 0) break;
+            const TX *x = x_of(now);
+            const R *r = kRes ? r_of(now) : nullptr;
+            if (STAGED) {   // (a place of 16 bytes in global memory is one in shared memory)
+                r = reinterpret_cast<const R *>(smem + slot_of(turn, k) + x_slot + (reinterpret_cast<uintptr_t>(r) & 15));
+                x = reinterpret_cast<const TX *>(smem + slot_of(turn, k) + (reinterpret_cast<uintptr_t>(x) & 15));
+            }
+            auto value = [&](int i) { return Elem<TX>::load(x, i) + (kRes ? Elem<R>::load(r, i) : 0.f); };
+            float sum = 0.f, most = 0.f;
+            for (int i = t; i < now.width; i += 8 * threads) {
+                float s8 = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const bool in = i + j * threads < now.width;
+                    const float v = in ? value(i + j * threads) : 0.f;
+                    s8 = fmaf(v, v, s8);
+                    if (k8 && a.block == 0) most = fmaxf(most, in ? fabsf(v * a.gain[i + j * threads]) : 0.f);
+                }
+                sum += s8;
+            }
+            float *const red = sums[turn & 1] + threadIdx.y * warps, *const top = tops[turn & 1] + threadIdx.y * warps;
+            const float scale = root(fmaf(row_all<false>(sum, red), a.inv_width, a.eps));
+            R *const s_out = !kRes || a.sum == nullptr ? nullptr : static_cast<R *>(a.sum) + at(a.sum_at, now.outer, now.inner);
+            // four of a thread's values, `apart` from one another: s to its place, s gain to g (0 behind the row)
+            auto four = [&](int i, int apart, float (&g)[4]) {
+                float v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const bool in = i + apart * j < now.width;
+                    v[j] = in ? value(i + apart * j) : 0.f;
+                    g[j] = in ? a.gain[i + apart * j] : 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (kRes && s_out != nullptr && i + apart * j < now.width) Elem<R>::store(s_out, i + apart * j, v[j]);
+                    g[j] *= v[j];
+                }
+            };
+            uint8_t *const codes = static_cast<uint8_t *>(a.y) + (k8 ? at(a.y_at, now.outer, now.inner) : 0);
+            float *const scales = a.scales + (size_t)(first + k) * a.blocks;
+            if (!k8 || a.block == 0) {
+                Y *const y = static_cast<Y *>(a.y) + at(a.y_at, now.outer, now.inner);
+                const Scale f(k8 ? row_all<true>(most, top) : 0.f, scale);
+                if (k8 && t == 0 && now.width > 0) *scales = f.scale;
+                for (int i = t; i < now.width; i += 4 * threads) {
+                    float g[4];
+                    four(i, threads, g);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int p = i + j * threads;
+                        if (p >= now.width) continue;
+                        if (k8) codes[p] = __nv_cvt_float_to_fp8(g[j] * f.codes, __NV_SATFINITE, __NV_E4M3);
+                        else Elem<Y>::store(y, p, g[j] * scale);
+                    }
+                }
+            } else {
+                for (int i = (t - lane) * 4 + lane; i - lane < now.width; i += 4 * threads) {   // a warp: four times 32 values, one to four blocks
+                    float g[4], m[4];
+                    four(i, 32, g);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) m[j] = fabsf(g[j]);
+                    if (a.block >= 64) m[0] = m[1] = fmaxf(m[0], m[1]), m[2] = m[3] = fmaxf(m[2], m[3]);
+                    if (a.block == 128) m[0] = fmaxf(m[0], m[2]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (a.block == 32 || (a.block == 64 && j % 2 == 0) || j == 0)   // (of values that are not negative, as whole numbers)
+                            m[j] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m[j])));
+                        else
+                            m[j] = m[a.block == 64 ? j - 1 : 0];
+                        const Scale f(m[j], scale);
+                        const int p = i + 32 * j;
+                        if (p < now.width) {
+                            if ((p & (a.block - 1)) == 0) scales[p >> a.block_shift] = f.scale;
+                            codes[p] = __nv_cvt_float_to_fp8(g[j] * f.codes, __NV_SATFINITE, __NV_E4M3);
+                        }
+                    }
+                }
+            }
+        }
+    }
+}
+
+// Kernels by what they do: -1 and -2 rows without vector accesses, staged and read twice; else chunks in registers.
+template <typename TX, typename TR, typename TY>
+cudaError_t launch(const NormArgs &a, int kind, dim3 grid, dim3 block, int tile, int shared, cudaStream_t st) {
+    if (kind == 4) {
+        k_rms_norm<TX, TR, TY, 4><<<grid, block, 0, st>>>(a);
+    } else if (kind == 0) {
+        k_rms_norm<TX, TR, TY, 0><<<grid, block, 0, st>>>(a);
+    } else if (kind == -2) {
+        k_rms_norm_odd<TX, TR, TY, false><<<grid, block, 0, st>>>(a, 1);
+    } else {
+        static std::atomic<unsigned long long> raised{0};   // devices whose limit of shared memory is raised
+        int device = 0;
+        cudaError_t e = cudaGetDevice(&device);
+        const unsigned long long bit = device < 64 ? 1ull << device : 0;
+        if (e == cudaSuccess && !(raised.load() & bit)) {
+            e = cudaFuncSetAttribute(k_rms_norm_odd<TX, TR, TY, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostStaged);
+            if (e == cudaSuccess) raised |= bit;
+        }
+        if (e != cudaSuccess) return e;
+        k_rms_norm_odd<TX, TR, TY, true><<<grid, block, shared, st>>>(a, tile);
+    }
+    return cudaGetLastError();
+}
+using Launch = cudaError_t (*)(const NormArgs &, int, dim3, dim3, int, int, cudaStream_t);
 template <typename TX, typename TR>
-Kernel by_y(int y, int c) {
-    return y == TALKER_DTYPE_F32 ? by_chunks<TX, TR, float>(c)
-                                 : y == TALKER_DTYPE_BF16 ? by_chunks<TX, TR, __nv_bfloat16>(c) : by_chunks<TX, TR, __nv_fp8_storage_t>(c);
+Launch by_y(int y) {
+    return y == TALKER_DTYPE_F32 ? launch<TX, TR, float> : y == TALKER_DTYPE_BF16 ? launch<TX, TR, __nv_bfloat16> : launch<TX, TR, __nv_fp8_storage_t>;
 }
 template <typename TX>
-Kernel by_res(bool res, int r, int y, int c) {
-    return !res ? by_y<TX, void>(y, c) : r == TALKER_DTYPE_F32 ? by_y<TX, float>(y, c) : by_y<TX, __nv_bfloat16>(y, c);
+Launch by_res(bool res, int r, int y) {
+    return !res ? by_y<TX, void>(y) : r == TALKER_DTYPE_F32 ? by_y<TX, float>(y) : by_y<TX, __nv_bfloat16>(y);
 }
 
 bool dense_type(int t) { return t == TALKER_DTYPE_F32 || t == TALKER_DTYPE_BF16; }
@@ -328,20 +482,28 @@ extern "C" talker_status talker_rms_norm(const void *x, int x_dtype, const talke
     a.eps = eps, a.rows = rows, a.inner = inner, a.width = width, a.block = y_dtype == TALKER_DTYPE_E4M3 ? block : 0;
     a.block_shift = a.block == 32 ? 5 : a.block == 64 ? 6 : 7, a.blocks = a.block == 0 ? 1 : (width + a.block - 1) / a.block;
     a.inv_width = (float)(1.0 / width);
-    a.vec = aligned(gain, 32);
-    a.x_at = place(x, x_dtype, x_at, rows, inner, a.vec);
-    if (residual) a.res_at = place(residual, res_dtype, res_at, rows, inner, a.vec);
-    if (sum_out) a.sum_at = place(sum_out, res_dtype, sum_at, rows, inner, a.vec);
-    a.y_at = place(y, y_dtype, y_at, rows, inner, a.vec);
-    const int c = width <= 256 ? 1 : width <= 4 * 8 * most_threads(4) ? 4 : 0;
-    const int threads = c == 0 ? 1024 : (width + 256 * c - 1) / (256 * c) * 32;
+    bool vec = aligned(gain, 32);
+    a.x_at = place(x, x_dtype, x_at, rows, inner, vec);
+    if (residual) a.res_at = place(residual, res_dtype, res_at, rows, inner, vec);
+    if (sum_out) a.sum_at = place(sum_out, res_dtype, sum_at, rows, inner, vec);
+    a.y_at = place(y, y_dtype, y_at, rows, inner, vec);
+    const int row_bytes = slot_bytes(width, size_of(x_dtype)) + (residual ? slot_bytes(width, size_of(res_dtype)) : 0);
+    const int kind = !vec || width <= 256 ? 2 * row_bytes <= kMostStaged ? -1 : -2 : width <= 4 * 8 * most_threads(4) ? 4 : 0;
+    int threads = kind == 0 ? 1024 : (width + 1023) / 1024 * 32, tile = 1, ctas = 0, shared = 0;
+    if (kind < 0) threads = std::min(kOddThreads, (width + 511) / 512 * 32);
     const int per = std::max(1, 128 / threads);
-    const dim3 block_dim(threads, per);
-    const Kernel k = x_dtype == TALKER_DTYPE_F32 ? by_res<float>(residual != nullptr, res_dtype, y_dtype, c)
-                                                 : by_res<__nv_bfloat16>(residual != nullptr, res_dtype, y_dtype, c);
+    if (kind == -1) {
+        if (threads == 32) tile = std::max(1, std::min({kTileRows, 2048 / row_bytes, rows / (152 * 32)}));
+        shared = 2 * per * tile * row_bytes;
+        ctas = std::max(1, std::min(1024 / (threads * per), 227 * 1024 / (shared + 1536)));
+    } else {
+        ctas = std::max(1, (kind == -2 ? 1024 : 512) / (threads * per));
+    }
     // as many CTAs as the multiprocessors hold, each with several rows where there are more
-    const int all = (rows + per - 1) / per, most = 152 * std::max(1, 65536 / (c == 4 ? 128 : 64) / (threads * per));
-    k<<<std::min(all, most), block_dim, 0, static_cast<cudaStream_t>(cuda_stream)>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return TALKER_ECUDA;
-    return TALKER_OK;
+    const long long all = ((long long)rows + per * tile - 1) / (per * tile);
+    const Launch go = x_dtype == TALKER_DTYPE_F32 ? by_res<float>(residual != nullptr, res_dtype, y_dtype)
+                                                  : by_res<__nv_bfloat16>(residual != nullptr, res_dtype, y_dtype);
+    const cudaError_t e = go(a, kind, dim3((unsigned)std::min<long long>(all, 152 * ctas)), dim3(threads, per), tile, shared,
+                             static_cast<cudaStream_t>(cuda_stream));
+    return e == cudaSuccess ? TALKER_OK : TALKER_ECUDA;
 }
