@@ -71,27 +71,27 @@ __device__ __forceinline__ float max_abs8(const float (&v)[8]) {
     return m;
 }
 
-// A row's sum or maximum over its blockDim.x threads, in every one of them. All threads of the CTA take part.
+// A row's sum or maximum over its blockDim.x threads (4, 8, 16 or whole warps), in every one of them. All threads of the CTA
+// take part.
+template <bool MAX>
+__device__ __forceinline__ float lanes_all(float v, int lanes) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        if (o >= lanes) continue;
+        const float w = __shfl_xor_sync(0xffffffffu, v, o);
+        v = MAX ? fmaxf(v, w) : v + w;
+    }
+    return v;
+}
 template <bool MAX>
 __device__ __forceinline__ float row_all(float v, float *red) {
-    if (MAX) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    } else {
-        v = warp_sum(v);
-    }
+    v = lanes_all<MAX>(v, blockDim.x);
     const int warps = blockDim.x >> 5;
-    if (warps == 1) return v;
+    if (warps <= 1) return v;
     const int lane = threadIdx.x & 31;
     if (lane == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
-    float w = lane < warps ? red[lane] : 0.f;
-    if (MAX) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, o));
-        return w;
-    }
-    return warp_sum(w);
+    return lanes_all<MAX>(lane < warps ? red[lane] : 0.f, 32);
 }
 
 // 1 / sqrt(x): the hardware's (2^-23 off) and a step of Newton's method; of 0 and infinity as it is.
@@ -141,13 +141,15 @@ struct Raw<__nv_bfloat16> {
     __device__ __forceinline__ float at(int j) const { return j & 1 ? bf16hi(w[j / 2]) : bf16lo(w[j / 2]); }
 };
 
-// blockDim.x threads a row, blockDim.y rows at a time; a thread has eight consecutive values of every chunk of 8 *
-// blockDim.x. C chunks stay in registers between the sum and the result, and the next rows' are on their way meanwhile; with
-// C = 0 (rows of more than 16384 values) they are read again. For E4M3 the norm's factor cancels: a code is that of s gain
-// over the largest of its block.
-// Threads of a CTA at most. Few threads with several chunks each: what a thread does for a row once is shared by more
-// values, and more CTAs are out of step with one another (4096 x 5120: one chunk of 640 threads 57 us, two of 320 54, four of
-// 160 42).
+// Rows that lie on whole accesses. What bounds them is memory: a value is read once and written once. blockDim.x threads a
+// row, blockDim.y rows at a time; a thread has eight consecutive values of every chunk of 8 * blockDim.x. C chunks stay in
+// registers between the sum and the result, and the next rows' are on their way meanwhile (4096 x 5120 bf16 + f32 to e4m3:
+// 62 us without); with C = 0 (rows of more than 16384 values) they are read again. For e4m3 the norm's factor cancels: a
+// code is that of s gain over the largest of its block.
+// Few threads with several chunks each: what a thread does for a row once is shared by more values, and more CTAs are out
+// of step with one another (4096 x 5120: one chunk of 640 threads 57 us, two of 320 54, four of 160 40, which is 86% of the
+// copy rate). Narrow rows take a quarter, half or whole warp's share of lanes (65536 x 128 bf16: a warp each 31 us, four
+// threads each 12). A lone row of 1024: 3 us, all of it latency.
 constexpr int most_threads(int c) { return c == 0 ? 1024 : 512; }
 template <typename TX, typename TR, typename TY, int C>
 __global__ void __launch_bounds__(most_threads(C), 1) k_rms_norm(const NormArgs a) {
@@ -262,10 +264,14 @@ __global__ void __launch_bounds__(most_threads(C), 1) k_rms_norm(const NormArgs 
     }
 }
 
-// Rows that no vector access fits (odd widths, strides or starts), and narrow ones. blockDim.x threads share a row: a warp reads
-// 32 neighbouring values of it at a time. STAGED: rows pass through shared memory, where the next ones arrive while these
-// are worked on, in whole 16 bytes but for their ends; otherwise (rows that do not fit there) they are read twice.
-constexpr int kOddThreads = 512, kTileRows = 8;
+// Rows that no vector access fits (odd widths, strides or starts). blockDim.x threads share a row: a warp reads 32
+// neighbouring values of it at a time, so that loads and stores touch whole sectors. STAGED: rows pass through shared
+// memory, where the next ones arrive while these are worked on, in whole 16 bytes but for their ends; otherwise (two rows
+// of more than 220 KB) they are read twice. What bounds it are the instructions, a value at a time: 4001 x 5003 bf16 + f32
+// to e4m3 in blocks 74 us (148 from registers, without shared memory), 2000 x 10001 bf16 + bf16 to f32 55 (207). A
+// thread for 16 values (of 8: 84 us, of 32: 82); of narrow rows 8 or 16 threads (100000 x 47: a warp each 57 us, eight
+// threads each 25), unless a warp's lanes have to be blocks.
+constexpr int kOddThreads = 512;
 constexpr int kMostStaged = 220 * 1024;
 __host__ __device__ constexpr int slot_bytes(int width, int size) { return (width * size + 31) & ~15; }   // at any offset in 16 bytes
 
@@ -280,7 +286,7 @@ struct End {
     unsigned short value;
     int to = -1;   // in shared memory
 };
-// A row of n bytes to a slot, by `threads` threads; those with t / 2 == turn take its odd ends.
+// A row of n bytes to a slot, by `threads` threads; two of them take its odd ends.
 __device__ __forceinline__ void stage_row(char *smem, int slot, const char *p, int n, int t, int threads, bool ends, End &end) {
     const int off = (int)(reinterpret_cast<uintptr_t>(p) & 15);
     const int low = min((16 - off) & 15, n), high = max(low, ((off + n) & ~15) - off);   // whole 16 bytes
@@ -329,13 +335,12 @@ __global__ void __launch_bounds__(kOddThreads, 2) k_rms_norm_odd(const NormArgs 
             if (kRes && r_end.to >= 0) *reinterpret_cast<unsigned short *>(smem + r_end.to) = r_end.value;
             x_end.to = r_end.to = -1;
             asm volatile("cp.async.wait_group 0;" ::: "memory");
-            if (warps == 1) __syncwarp();
+            if (warps <= 1) __syncwarp();
             else __syncthreads();
             issue(first + per, turn + 1);   // to the slots that the last turn is done with
         }
         for (int k = 0; k < tile; ++k) {
             const Row now = place_of(a, first + k);
-            if (warps == 1 && now.width == 0) break;
             const TX *x = x_of(now);
             const R *r = kRes ? r_of(now) : nullptr;
             if (STAGED) {   // (a place of 16 bytes in global memory is one in shared memory)
@@ -487,13 +492,16 @@ extern "C" talker_status talker_rms_norm(const void *x, int x_dtype, const talke
     if (residual) a.res_at = place(residual, res_dtype, res_at, rows, inner, vec);
     if (sum_out) a.sum_at = place(sum_out, res_dtype, sum_at, rows, inner, vec);
     a.y_at = place(y, y_dtype, y_at, rows, inner, vec);
+    // (both kernels' sides are beside them)
     const int row_bytes = slot_bytes(width, size_of(x_dtype)) + (residual ? slot_bytes(width, size_of(res_dtype)) : 0);
-    const int kind = !vec || width <= 256 ? 2 * row_bytes <= kMostStaged ? -1 : -2 : width <= 4 * 8 * most_threads(4) ? 4 : 0;
+    const int kind = !vec ? 2 * row_bytes <= kMostStaged ? -1 : -2 : width <= 4 * 8 * most_threads(4) ? 4 : 0;
     int threads = kind == 0 ? 1024 : (width + 1023) / 1024 * 32, tile = 1, ctas = 0, shared = 0;
-    if (kind < 0) threads = std::min(kOddThreads, (width + 511) / 512 * 32);
+    if (kind == 4 && width <= 512)   // several rows a warp; a block's threads are neighbours
+        for (threads = std::max(4, a.block / 8); threads * 32 < width;) threads *= 2;
+    if (kind < 0) threads = a.block == 0 && width <= 128 ? width <= 64 ? 8 : 16 : std::min(kOddThreads, (width + 511) / 512 * 32);
     const int per = std::max(1, 128 / threads);
     if (kind == -1) {
-        if (threads == 32) tile = std::max(1, std::min({kTileRows, 2048 / row_bytes, rows / (152 * 32)}));
+        if (threads <= 32) tile = std::max(1, std::min({threads / 2, 8, 8192 / (per * row_bytes), rows / (152 * 8 * per)}));
         shared = 2 * per * tile * row_bytes;
         ctas = std::max(1, std::min(1024 / (threads * per), 227 * 1024 / (shared + 1536)));
     } else {

@@ -63,6 +63,36 @@ def test_norm(x, res, out, block, rows, width):
     check_norm(xs, (1 + 0.1 * ref.rnd(3, width)).cuda(), r, out, block)
 
 
+@pytest.mark.parametrize("x,res,out,block,rows,width", [
+    ("f32", "f32", "bf16", 0, 80003, 13), ("bf16", "bf16", "bf16", 0, 80003, 47), ("bf16", "f32", "e4m3", 0, 40009, 65), ("f32", "bf16", "f32", 0, 40009, 127),
+    ("bf16", None, "e4m3", 32, 20011, 131), ("bf16", "bf16", "e4m3", 128, 3001, 301), ("f32", None, "e4m3", 64, 20011, 33), ("bf16", "f32", "e4m3", 0, 701, 5003),
+    ("bf16", None, "bf16", 0, 80003, 32), ("bf16", "f32", "e4m3", 32, 40009, 64), ("f32", "f32", "e4m3", 128, 20011, 136), ("bf16", "bf16", "f32", 0, 9001, 512)])
+def test_norm_of_many_rows(x, res, out, block, rows, width):
+    """Narrow and odd rows, several turns of every CTA."""
+    xs = (ref.rnd(1, rows, width) * 2).to(DT[x]).cuda()
+    r = None if res is None else (ref.rnd(2, rows, width) * 5).to(DT[res]).cuda()
+    check_norm(xs, (1 + 0.1 * ref.rnd(3, width)).cuda(), r, out, block)
+
+
+@pytest.mark.parametrize("width", [1, 5, 17, 40, 200])
+@pytest.mark.parametrize("x,res", [("bf16", "bf16"), ("f32", "bf16"), ("bf16", "f32")])
+def test_norm_at_every_start(x, res, width):
+    """x, residual and sum each at an offset of its own, as views of larger buffers that keep what is around them."""
+    from kv_cached_qwen3_gb300.norm import rms_norm
+    gain = (1 + 0.1 * ref.rnd(3, width)).cuda()
+    for start in range(9):
+        xb, rb = (ref.rnd(1, 4 * width + 9) * 2).to(DT[x]).cuda(), (ref.rnd(2, 4 * width + 9) * 5).to(DT[res]).cuda()
+        xs = xb[start:start + 3 * width].view(3, width)
+        rs = rb[(start * 5) % 9:][:3 * width].view(3, width)
+        check_norm(xs, gain, rs, "bf16")
+        want_y, want, _ = rms_norm(xs, gain, residual=rs)
+        before = rb.clone()
+        y, s, _ = rms_norm(xs, gain, residual=rs, sum_out=rs)   # in place
+        assert s is rs and torch.equal(rs, want) and torch.equal(y, want_y)
+        rs.copy_(before[(start * 5) % 9:][:3 * width].view(3, width))
+        assert torch.equal(rb, before)
+
+
 @pytest.mark.parametrize("out", ["f32", "e4m3"])
 def test_norm_of_heads_in_strides(out):
     """Heads of a fused projection (rows and heads at strides of their own), written in strides, odd starts."""
