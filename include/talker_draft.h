@@ -6,7 +6,7 @@
  * No handle: the caller owns every buffer; the call enqueues its kernels on
  * cuda_stream (NULL = legacy stream) of the current device and returns. Nothing is
  * allocated and the call may be captured into a CUDA graph. All pointers are
- * device pointers.
+ * device pointers, aligned to their elements.
  */
 #ifndef TALKER_DRAFT_H
 #define TALKER_DRAFT_H
@@ -39,7 +39,7 @@ extern "C" {
  * are taken to [0, n_draft] and uniform numbers to [0, 1] (NaN: 0).
  *
  * Probabilities that decide (p and q of a draft near its border, all of the row that is
- * drawn from) are made to about 2^-30 of themselves and summed as whole numbers (in the
+ * drawn from) are made to about 2^-29 of themselves and summed as whole numbers (in the
  * sums and the draw those below 2^-70 of the row's largest count as 0), so
  * neither a row's address nor the launch's shape changes a token; the sums of taken drafts'
  * logprobs are f32.

@@ -37,7 +37,6 @@ struct Args {
     float *logprobs;
     int parts;              // of a row
     int ctas;               // of a sequence's cluster
-    int staged;             // bytes of shared memory for a range of one row, 0: ranges are read where they are
     struct Seen *seen;      // scratch: [sequence][row][part]
 };
 
@@ -174,7 +173,7 @@ __device__ Seen see_part(const T *row, int vocab, int part, int parts, float c, 
     return warp_join(s, c);
 }
 
-// e^((x - most) / T) = m 2^(-30 - shift), m in [2^30, 2^31), for x <= most, to about 2^-30 of itself. With
+// e^((x - most) / T) = m 2^(-30 - shift), m in [2^30, 2^31), for x <= most, to about 2^-29 of itself. With
 // t = (x - most) log2 e / T in two floats, t = k / 32 + f, |f| <= 1/64: m = 2^30 2^(k % 32 / 32) e^y, y = f log 2, by the
 // series of e^y - 1, whose terms after y^4 / 24 are below 2^-39. Below 2^-70, and of masked logits: 0, by a shift that
 // leaves nothing.
@@ -287,7 +286,7 @@ __device__ __forceinline__ uint32_t reciprocal(unsigned long long z) {
 
 // A cluster per sequence. f32 sums decide which drafts are surely taken and which first one is
 // not; that one's rows, and those that the next token is drawn from, are gone over by all CTAs, each a range of the vocabulary, with
-// exponentials of 30 bits and sums in whole numbers: which token a uniform number meets is a question of sums of
+// exponentials of 29 bits and sums in whole numbers: which token a uniform number meets is a question of sums of
 // 10^5 terms next to one another, where f32 would err once in some hundred draws.
 template <typename T, bool OWN>
 __global__ void __launch_bounds__(kThreads, 4) k_draft_choose(const Args a) {
@@ -370,8 +369,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_draft_choose(const Args a) {
     const int slice = (V + ctas - 1) / ctas, from = min(rank * slice, V), to = min(from + slice, V);
     const int each = (slice + kWarps - 1) / kWarps;
     const int w0 = min(from + warp * each, to), w1 = min(w0 + each, to);
-    const T *rp = nullptr, *rq = nullptr, *rp_staged = nullptr, *rq_staged = nullptr, *rp_row = nullptr;
-    int rp_n = -1;        // the row whose range is staged
+    const T *rp = nullptr, *rq = nullptr;
     // a value or two of each thread, summed over every CTA, to all CTAs
     auto spread = [&](unsigned long long v0, unsigned long long v1) {
         v0 = warp_sum64(v0), v1 = warp_sum64(v1);
@@ -386,19 +384,6 @@ __global__ void __launch_bounds__(kThreads, 4) k_draft_choose(const Args a) {
         cluster.sync();
     };
     constexpr bool kRounded = sizeof(T) == 4;
-    // This CTA's range of a row, copied to shared memory at once where there is room: passes over it would each wait for
-    // the L2 a few times. The pointer is to be used as the row's.
-    extern __shared__ uint4 stage[];
-    auto staged = [&](const T *row, int slot) -> const T * {
-        if (a.staged == 0) return row;
-        char *to_at = reinterpret_cast<char *>(stage) + slot * a.staged;
-        const char *at = reinterpret_cast<const char *>(row + from);
-        const int off = (int)(reinterpret_cast<uintptr_t>(at) & 3), words = ((to - from) * (int)sizeof(T) + off + 3) / 4;   // (bf16: whole words)
-        const uint32_t to_u = smem_u32(to_at);
-        for (int w = tid; w < words; w += kThreads)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to_u + 4 * w), "l"(at - off + 4 * w) : "memory");
-        return reinterpret_cast<const T *>(to_at + off) - from;
-    };
     // f(exponential of token i of p, i), or f(p's, q's), for the warp's range
     auto over_one = [&](auto f) {
         const F2 less = f2(-p.most, -p.most);
@@ -429,16 +414,6 @@ __global__ void __launch_bounds__(kThreads, 4) k_draft_choose(const Args a) {
         if (has_q && s.rows[sq.targets() + n].alive()) q.most = s.rows[sq.targets() + n].most;
         rp = row_at<T>(a, sq, seq, n);
         rq = has_q ? row_at<T>(a, sq, seq, sq.targets() + n) : nullptr;
-        if (rp_n != n) {
-            rp_row = rp;
-            if (rp_n >= 0) __syncthreads();   // (the ranges of the row before are not read any more)
-            rp_staged = staged(rp, 0);
-            rq_staged = has_q ? staged(rq, 1) : nullptr;
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            __syncthreads();
-            rp_n = n;
-        }
-        rp = rp_staged, rq = rq_staged;
         if (rq == nullptr && verdict == kRefuse) break;   // (drawn from p alone: its sum is the draw's)
         unsigned long long sums[2] = {0, 0};
         if (p.alive() && q.alive())
@@ -532,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_draft_choose(const Args a) {
                         z = total;
                         if (gone >= 0 && gone < V && !plain) {
                             Exact e, g;
-                            exact_exp2<kRounded>(load_logit(rp_row, gone), 0.f, f2(-p.most, 0.f), c, s.roots, e, g);
+                            exact_exp2<kRounded>(load_logit(rp, gone), 0.f, f2(-p.most, 0.f), c, s.roots, e, g);
                             z += place(e.m, bits + e.shift);
                         }
                     }
@@ -562,34 +537,34 @@ bool sizes_ok(int n_seq, int n_draft, int vocab) {
     return n_seq >= 0 && n_seq <= 65535 && n_draft >= 0 && n_draft <= kMaxDraft && vocab >= 1 && vocab <= 1 << 26;
 }
 
-
-// How a call runs. A sequence's own cluster reads its rows while they are few logits; else the whole GPU does, in a launch before.
-constexpr int kOwnLogits = 65536;
+// How a call runs. A sequence's own cluster reads its rows while they are few logits; else the whole GPU does, in a launch
+// before (bf16, 4 drafts: 8192 tokens 9.9 against 11.2 us, 32768 tokens 14.5 against 12.9). CTAs of a cluster: each has
+// something to do, and all clusters are soon there, which take longer to begin the more CTAs they have (4 drafts of 2048
+// tokens: one sequence 8.8 us with eight, 9.9 with four; 28 sequences 13.1 and 11.6; 64 17.5 and 13.5; 8 sequences of 8
+// drafts of 100003 tokens: 37.6 with eight, 32.6 with sixteen).
+constexpr int kOwnLogits = 1 << 17;
 struct Shape {
     bool own;
-    int parts, ctas, staged;
+    int parts, ctas;
 };
-constexpr int kMostStaged = 100 * 1024;
-Shape shape_of(int n_seq, int n_draft, int vocab, int size) {
+Shape shape_of(int n_seq, int n_draft, int vocab) {
     const int rows = 2 * n_draft + 1;
+    const long long logits = (long long)rows * vocab;
     Shape p;
-    p.own = (long long)rows * vocab <= kOwnLogits;
+    p.own = logits <= kOwnLogits;
     p.ctas = 1;
-    const int most = (long long)n_seq * kCluster <= 152 * 3 ? kCluster : kCluster / 2;
-    while (p.ctas < most && (p.own ? (long long)rows * vocab : vocab) > p.ctas * 1024ll) p.ctas *= 2;
+    while (p.ctas < kCluster && (long long)n_seq * p.ctas * 2 <= (p.own ? 256 : 512) &&
+           (p.own ? logits > (p.ctas < 8 ? 4096ll : 12288ll) * p.ctas : vocab > p.ctas * 1024ll))
+        p.ctas *= 2;
     const long long warps = p.own ? p.ctas * kWarps : std::max(1ll, 152ll * 64 / std::max(1, n_seq));   // for a sequence
-    const int slice = (vocab + p.ctas - 1) / p.ctas;
-    p.staged = (slice * size + 4 + 15) / 16 * 16;
-    if (2 * p.staged > kMostStaged) p.staged = 0;
     p.parts = (int)std::max(1ll, std::min<long long>(std::min(kMaxParts, vocab / 256), warps / rows));
     return p;
 }
 
-// Clusters of 16 and their shared memory are allowed once for each device.
+// Clusters of 16 are allowed once for each device.
 template <typename T, bool OWN>
 cudaError_t allow() {
-    const cudaError_t e = cudaFuncSetAttribute(k_draft_choose<T, OWN>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    return e ? e : cudaFuncSetAttribute(k_draft_choose<T, OWN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostStaged);
+    return cudaFuncSetAttribute(k_draft_choose<T, OWN>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
 }
 cudaError_t allow_clusters() {
     static std::atomic<unsigned long long> done{0};
@@ -610,7 +585,7 @@ extern "C" {
 
 size_t talker_draft_scratch(int n_seq, int n_draft, int vocab) {
     if (!sizes_ok(n_seq, n_draft, vocab)) return 0;
-    const Shape p = shape_of(n_seq, n_draft, vocab, 4);   // (the types differ in what is staged alone)
+    const Shape p = shape_of(n_seq, n_draft, vocab);
     return p.own ? 0 : (size_t)n_seq * (2 * n_draft + 1) * p.parts * sizeof(Seen);
 }
 
@@ -623,18 +598,20 @@ talker_status talker_draft_verify(const void *target, int64_t target_seq, int64_
     if (n_draft > 0 && !tokens) return TALKER_EINVAL;
     if (dtype != TALKER_DTYPE_F32 && dtype != TALKER_DTYPE_BF16) return TALKER_EINVAL;
     if ((reinterpret_cast<uintptr_t>(target) | reinterpret_cast<uintptr_t>(draft)) % (dtype == TALKER_DTYPE_F32 ? 4 : 2)) return TALKER_EINVAL;
+    for (const void *p : {static_cast<const void *>(tokens), static_cast<const void *>(counts), static_cast<const void *>(uniforms), static_cast<const void *>(temperatures),
+                          static_cast<const void *>(tokens_out), static_cast<const void *>(accepted), static_cast<const void *>(logprobs)})
+        if (reinterpret_cast<uintptr_t>(p) % 4) return TALKER_EINVAL;
     if (n_seq == 0) return TALKER_OK;
     const size_t need = talker_draft_scratch(n_seq, n_draft, vocab);
     if (need > 0 && (!scratch || scratch_bytes < need || reinterpret_cast<uintptr_t>(scratch) % 16)) return TALKER_EINVAL;
-    const Shape p = shape_of(n_seq, n_draft, vocab, dtype == TALKER_DTYPE_F32 ? 4 : 2);
+    const Shape p = shape_of(n_seq, n_draft, vocab);
     const Args a{target, draft, target_seq, target_row, draft_seq, draft_row, tokens, counts, uniforms, temperatures, n_draft, vocab,
-                 tokens_out, accepted, logprobs, p.parts, p.ctas, p.staged, static_cast<Seen *>(scratch)};
+                 tokens_out, accepted, logprobs, p.parts, p.ctas, static_cast<Seen *>(scratch)};
     const bool f32 = dtype == TALKER_DTYPE_F32;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     cfg.blockDim = dim3(kThreads);
     cfg.gridDim = dim3((unsigned)(n_seq * p.ctas));
-    cfg.dynamicSmemBytes = 2 * (size_t)p.staged;
     cfg.stream = static_cast<cudaStream_t>(cuda_stream);
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = p.ctas;

@@ -119,7 +119,8 @@ def test_draft_refusals(lib):
         return lib.talker_draft_verify(t, ts, tr, d, ds, dr, dtype, tok, cnt, u, temp, S, K, V, out, acc, lp, scratch, need, None)
     assert call(S=0) == 0
     for kw in (dict(t=None), dict(t=66), dict(d=130), dict(t=65, dtype=1), dict(dtype=2), dict(dtype=4), dict(tok=None), dict(u=None), dict(S=-1), dict(S=65536), dict(K=-1), dict(K=65),
-               dict(V=0), dict(V=(1 << 26) + 1), dict(out=None), dict(acc=None)):
+               dict(V=0), dict(V=(1 << 26) + 1), dict(out=None), dict(acc=None), dict(tok=257), dict(cnt=66), dict(u=322), dict(temp=513), dict(out=386),
+               dict(acc=449), dict(lp=514)):
         assert call(**kw) == 1, kw
 
 
