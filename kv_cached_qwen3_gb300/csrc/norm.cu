@@ -3,6 +3,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "rows.cuh"
 #include "talker_layer.h"
@@ -110,8 +111,9 @@ struct Scale {
         const bool none = d < 0x1p-100f || m < 0x1p-100f;
         float inv;
         asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(m));
+        const float near = 448.f * inv, better = fmaf(fmaf(-m, near, 448.f), inv, near);   // (an error here is all of a block's)
         scale = none ? 0.f : d * (1.f / 448.f);
-        codes = none ? 0.f : d < INFINITY ? 448.f * inv : NAN;
+        codes = none ? 0.f : d < INFINITY ? better : NAN;
     }
 };
 
@@ -267,10 +269,11 @@ __global__ void __launch_bounds__(most_threads(C), 1) k_rms_norm(const NormArgs 
 // Rows that no vector access fits (odd widths, strides or starts). blockDim.x threads share a row: a warp reads 32
 // neighbouring values of it at a time, so that loads and stores touch whole sectors. STAGED: rows pass through shared
 // memory, where the next ones arrive while these are worked on, in whole 16 bytes but for their ends; otherwise (two rows
-// of more than 220 KB) they are read twice. What bounds it are the instructions, a value at a time: 4001 x 5003 bf16 + f32
-// to e4m3 in blocks 74 us (148 from registers, without shared memory), 2000 x 10001 bf16 + bf16 to f32 55 (207). A
-// thread for 16 values (of 8: 84 us, of 32: 82); of narrow rows 8 or 16 threads (100000 x 47: a warp each 57 us, eight
-// threads each 25), unless a warp's lanes have to be blocks.
+// of more than 220 KB) they are read twice. What bounds it are the instructions, a value at a time (24 or so): 4001 x 5003
+// bf16 + f32 to e4m3 in blocks 53 us, 61% of the copy rate (148 from registers, without shared memory; 74 with a thread's
+// values as far apart as a row has threads, whose addresses take instructions), 2000 x 10001 bf16 + bf16 to f32 49 (207). A
+// thread for 16 values (74 us then; for 8: 84, for 32: 82); of narrow rows 8 or 16 threads (100000 x 47: a warp each 57 us,
+// eight threads each 22), unless a warp's lanes have to be blocks.
 constexpr int kOddThreads = 512;
 constexpr int kMostStaged = 220 * 1024;
 __host__ __device__ constexpr int slot_bytes(int width, int size) { return (width * size + 31) & ~15; }   // at any offset in 16 bytes
@@ -311,7 +314,7 @@ __global__ void __launch_bounds__(kOddThreads, 2) k_rms_norm_odd(const NormArgs 
     using Y = typename std::conditional<k8, float, TY>::type;
     extern __shared__ __align__(16) char smem[];
     __shared__ float sums[2][32], tops[2][32];
-    const int t = threadIdx.x, threads = blockDim.x, lane = t & 31, warps = threads >> 5, width = a.width;
+    const int t = threadIdx.x, threads = blockDim.x, warps = threads >> 5, width = a.width;
     const int x_slot = slot_bytes(width, sizeof(TX)), slot = x_slot + (kRes ? slot_bytes(width, sizeof(R)) : 0);
     const int per = blockDim.y * tile * gridDim.x;
     End x_end, r_end;
@@ -349,75 +352,84 @@ __global__ void __launch_bounds__(kOddThreads, 2) k_rms_norm_odd(const NormArgs 
             }
             auto value = [&](int i) { return Elem<TX>::load(x, i) + (kRes ? Elem<R>::load(r, i) : 0.f); };
             float sum = 0.f, most = 0.f;
-            for (int i = t; i < now.width; i += 8 * threads) {
-                float s8 = 0.f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const bool in = i + j * threads < now.width;
-                    const float v = in ? value(i + j * threads) : 0.f;
-                    s8 = fmaf(v, v, s8);
-                    if (k8 && a.block == 0) most = fmaxf(most, in ? fabsf(v * a.gain[i + j * threads]) : 0.f);
-                }
-                sum += s8;
-            }
             float *const red = sums[turn & 1] + threadIdx.y * warps, *const top = tops[turn & 1] + threadIdx.y * warps;
-            const float scale = root(fmaf(row_all<false>(sum, red), a.inv_width, a.eps));
             R *const s_out = !kRes || a.sum == nullptr ? nullptr : static_cast<R *>(a.sum) + at(a.sum_at, now.outer, now.inner);
-            // four of a thread's values, `apart` from one another: s to its place, s gain to g (0 behind the row)
-            auto four = [&](int i, int apart, float (&g)[4]) {
-                float v[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const bool in = i + apart * j < now.width;
-                    v[j] = in ? value(i + apart * j) : 0.f;
-                    g[j] = in ? a.gain[i + apart * j] : 0.f;
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (kRes && s_out != nullptr && i + apart * j < now.width) Elem<R>::store(s_out, i + apart * j, v[j]);
-                    g[j] *= v[j];
-                }
-            };
+            Y *const y = static_cast<Y *>(a.y) + (k8 ? 0 : at(a.y_at, now.outer, now.inner));
             uint8_t *const codes = static_cast<uint8_t *>(a.y) + (k8 ? at(a.y_at, now.outer, now.inner) : 0);
             float *const scales = a.scales + (size_t)(first + k) * a.blocks;
-            if (!k8 || a.block == 0) {
-                Y *const y = static_cast<Y *>(a.y) + at(a.y_at, now.outer, now.inner);
-                const Scale f(k8 ? row_all<true>(most, top) : 0.f, scale);
-                if (k8 && t == 0 && now.width > 0) *scales = f.scale;
-                for (int i = t; i < now.width; i += 4 * threads) {
-                    float g[4];
-                    four(i, threads, g);
+            auto spread = [&](auto apart_) {   // a thread's values are `apart` from one another, at offsets that instructions hold
+                constexpr int apart = decltype(apart_)::value;
+                const int own = t % apart, from = t - own;
+                for (int i = 8 * from + own; i < now.width; i += 8 * threads) {
+                    float s8 = 0.f;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int p = i + j * threads;
-                        if (p >= now.width) continue;
-                        if (k8) codes[p] = __nv_cvt_float_to_fp8(g[j] * f.codes, __NV_SATFINITE, __NV_E4M3);
-                        else Elem<Y>::store(y, p, g[j] * scale);
+                    for (int j = 0; j < 8; ++j) {
+                        const bool in = i + j * apart < now.width;
+                        const float v = in ? value(i + j * apart) : 0.f;
+                        s8 = fmaf(v, v, s8);
+                        if (k8 && a.block == 0) most = fmaxf(most, in ? fabsf(v * a.gain[i + j * apart]) : 0.f);
                     }
+                    sum += s8;
                 }
-            } else {
-                for (int i = (t - lane) * 4 + lane; i - lane < now.width; i += 4 * threads) {   // a warp: four times 32 values, one to four blocks
-                    float g[4], m[4];
-                    four(i, 32, g);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) m[j] = fabsf(g[j]);
-                    if (a.block >= 64) m[0] = m[1] = fmaxf(m[0], m[1]), m[2] = m[3] = fmaxf(m[2], m[3]);
-                    if (a.block == 128) m[0] = fmaxf(m[0], m[2]);
+                const float scale = root(fmaf(row_all<false>(sum, red), a.inv_width, a.eps));
+                // four values: s to its place, s gain to g (0 behind the row)
+                auto four = [&](int i, float (&g)[4]) {
+                    float v[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        if (a.block == 32 || (a.block == 64 && j % 2 == 0) || j == 0)   // (of values that are not negative, as whole numbers)
-                            m[j] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m[j])));
-                        else
-                            m[j] = m[a.block == 64 ? j - 1 : 0];
-                        const Scale f(m[j], scale);
-                        const int p = i + 32 * j;
-                        if (p < now.width) {
-                            if ((p & (a.block - 1)) == 0) scales[p >> a.block_shift] = f.scale;
-                            codes[p] = __nv_cvt_float_to_fp8(g[j] * f.codes, __NV_SATFINITE, __NV_E4M3);
+                        const bool in = i + apart * j < now.width;
+                        v[j] = in ? value(i + apart * j) : 0.f;
+                        g[j] = in ? a.gain[i + apart * j] : 0.f;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (kRes && s_out != nullptr && i + apart * j < now.width) Elem<R>::store(s_out, i + apart * j, v[j]);
+                        g[j] *= v[j];
+                    }
+                };
+                if (!k8 || a.block == 0) {
+                    const Scale f(k8 ? row_all<true>(most, top) : 0.f, scale);
+                    if (k8 && t == 0 && now.width > 0) *scales = f.scale;
+                    for (int i = 4 * from + own; i < now.width; i += 4 * threads) {
+                        float g[4];
+                        four(i, g);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int p = i + j * apart;
+                            if (p >= now.width) continue;
+                            if (k8) codes[p] = __nv_cvt_float_to_fp8(g[j] * f.codes, __NV_SATFINITE, __NV_E4M3);
+                            else Elem<Y>::store(y, p, g[j] * scale);
                         }
                     }
+                    return;
                 }
-            }
+                if constexpr (apart == 32) {   // (rows in blocks have whole warps)
+                    auto blocks = [&](auto values) {   // of so many values: a warp has four, two or one
+                        constexpr int B = decltype(values)::value, per = B / 32;
+                        for (int i = 4 * from + own; i - own < now.width; i += 4 * threads) {
+                            float g[4];
+                            four(i, g);
+#pragma unroll
+                            for (int j = 0; j < 4; j += per) {
+                                float m = 0.f;
+#pragma unroll
+                                for (int l = 0; l < per; ++l) m = fmaxf(m, fabsf(g[j + l]));
+                                const Scale f(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m))), scale);   // (not negative: ordered as whole numbers)
+                                if (own == 0 && i + 32 * j < now.width) scales[(i + 32 * j) / B] = f.scale;
+#pragma unroll
+                                for (int l = j; l < j + per; ++l)
+                                    if (i + 32 * l < now.width) codes[i + 32 * l] = __nv_cvt_float_to_fp8(g[l] * f.codes, __NV_SATFINITE, __NV_E4M3);
+                            }
+                        }
+                    };
+                    if (a.block == 32) blocks(std::integral_constant<int, 32>());
+                    else if (a.block == 64) blocks(std::integral_constant<int, 64>());
+                    else blocks(std::integral_constant<int, 128>());
+                }
+            };
+            if (threads >= 32) spread(std::integral_constant<int, 32>());
+            else if (threads == 16) spread(std::integral_constant<int, 16>());
+            else spread(std::integral_constant<int, 8>());
         }
     }
 }

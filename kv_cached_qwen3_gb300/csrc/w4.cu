@@ -179,8 +179,9 @@ struct Columns {
     int passes, cols, parts;   // parts: columns of a row
 };
 
-// A CTA per row: its columns to frags, and what undoes the scaling to back. A row's values are read once where eight quads a thread
-// hold them (k <= 16384). The product's CTAs may begin at once: they bring weights in until they need this.
+// A CTA per row: its columns to frags, and what undoes the scaling to back. A row's values are read once where eight quads
+// a thread hold them (k <= 16384). Bound by latency (6.8 us by itself for one row of 8192, of which the product's CTAs, which
+// may begin at once and bring weights in until they need this, hide all but 3).
 constexpr int kRowThreads = 512, kHeld = 8;
 template <typename T, int PARTS>
 __device__ __forceinline__ void prepare_row(const XArgs &a, int r, uint2 *frags, int cols, int col, int units, float *back) {
@@ -350,10 +351,17 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity) {
     return true;
 }
 
-// One CTA a multiprocessor, all with the same number of steps. A thread of its own brings each step into a ring of slots by two
-// bulk copies: a span's records of a unit lie together, and so do its fragments of x. Warps run on their own, up to a ring's length apart. Nothing is joined in here: a segment's
-// sums go to memory, and the kernel after adds them up. A group of inputs' sum is added to the total times its
-// scale. A copy that does not arrive within a second makes its warps' sums NaN from there on.
+// One CTA a multiprocessor, all with the same number of steps. A thread of its own brings each step into a ring of slots by
+// two bulk copies: a span's records of a unit lie together, and so do its fragments of x. Warps run on their own, up to a
+// ring's length apart. Nothing is joined in here: a segment's sums go to memory, and the kernel after adds them up. A group
+// of inputs' sum is added to the total times its scale. A copy that does not arrive within a second makes its warps' sums NaN
+// from there on.
+// Few rows are bound by the instructions that make codes operands, nine for the four registers of an MMA. 24576 x 8192,
+// groups of 128, one row: 26 us for 104 MB (59% of the copy rate, 59% of the issue slots, a quarter of the tensor cores'
+// cycles), 30 with the kernels around it; 8 bf16 rows 29, 16 37, 32 56 (MMAs and their operands), 64 in two passes 100. Equal
+// steps: with whole tiles to a CTA the last ones run alone (49 us); a ring and warps of their own
+// instead of a barrier a step: 36; codes as whole numbers under a scale a group instead of scaled ones: 31. Codes that keep
+// their offset of 8, taken off the sum: an instruction less for two, but errors of 1e-6 instead of 9e-8.
 template <int NT, int NG>
 __global__ void __launch_bounds__((warps_of(NT) + 1) * 32, 1) k_w4_matmul(const MatmulArgs a) {
     constexpr int kWarps = warps_of(NT), kBlock = tiles_of(NT);
@@ -509,8 +517,10 @@ __global__ void __launch_bounds__((warps_of(NT) + 1) * 32, 1) k_w4_matmul(const 
     pdl_launch_dependents();
 }
 
-// A CTA per row tile and pass: the segments' sums in their order, and the result. A thread adds up one number of a lane's four:
-// rows g (0, 1) and g + 8 (2, 3) of two columns. Where there are many segments, groups of 128 threads take a range each.
+// A CTA per row tile and pass: the segments' sums in their order, and the result. A thread adds up one number of a lane's
+// four: rows g (0, 1) and g + 8 (2, 3) of two columns. Where there are many segments, groups of 128 threads take a range each.
+// Bound by latency: 3 to 4 us after the product. (Adding in the product, by whoever is last, needs counters that are zero
+// on entry, and its chain at the end is as long.)
 __global__ void __launch_bounds__(1024) k_w4_join(const MatmulArgs a, int nt) {
     __shared__ float sums[7 * 128];
     const int per = tiles_of(nt), pass = blockIdx.y, tile = blockIdx.x, place = pass * a.blocks + tile / per, parts = a.c.parts;
