@@ -150,7 +150,7 @@ struct Raw<__nv_bfloat16> {
 // code is that of s gain over the largest of its block.
 // Few threads with several chunks each: what a thread does for a row once is shared by more values, and more CTAs are out
 // of step with one another (4096 x 5120: one chunk of 640 threads 57 us, two of 320 54, four of 160 40, which is 86% of the
-// copy rate). Narrow rows take a quarter, half or whole warp's share of lanes (65536 x 128 bf16: a warp each 31 us, four
+// copy rate). Narrow rows take 4 to 16 threads, so that a warp has several (65536 x 128 bf16: a warp each 31 us, four
 // threads each 12). A lone row of 1024: 3 us, all of it latency.
 constexpr int most_threads(int c) { return c == 0 ? 1024 : 512; }
 template <typename TX, typename TR, typename TY, int C>
@@ -269,11 +269,11 @@ __global__ void __launch_bounds__(most_threads(C), 1) k_rms_norm(const NormArgs 
 // Rows that no vector access fits (odd widths, strides or starts). blockDim.x threads share a row: a warp reads 32
 // neighbouring values of it at a time, so that loads and stores touch whole sectors. STAGED: rows pass through shared
 // memory, where the next ones arrive while these are worked on, in whole 16 bytes but for their ends; otherwise (two rows
-// of more than 220 KB) they are read twice. What bounds it are the instructions, a value at a time (60; 69% of the issue slots): 4001
-// x 5003 bf16 + f32 to e4m3 in blocks 53 us, 61% of the copy rate (148 from registers, without shared memory; 74 with a thread's
-// values as far apart as a row has threads, whose addresses take instructions), 2000 x 10001 bf16 + bf16 to f32 49 (207). A
-// thread for 16 values (74 us then; for 8: 84, for 32: 82); of narrow rows 8 or 16 threads (100000 x 47: a warp each 57 us,
-// eight threads each 22), unless a warp's lanes have to be blocks.
+// of more than 220 KB) they are read twice. What bounds it are the instructions, a value at a time (60 each; 69% of the
+// issue slots): 4001 x 5003 bf16 + f32 to e4m3 in blocks 53 us, 61% of the copy rate (148 from registers, without shared
+// memory; 74 with a thread's values as far apart as a row has threads, whose addresses take instructions), 2000 x 10001
+// bf16 + bf16 to f32 49 (207). A thread for 16 values (74 us then; for 8: 84, for 32: 82); of narrow rows 8 or 16 threads
+// (100000 x 47: a warp each 57 us, eight threads each 22), unless a warp's lanes have to be blocks.
 constexpr int kOddThreads = 512;
 constexpr int kMostStaged = 220 * 1024;
 __host__ __device__ constexpr int slot_bytes(int width, int size) { return (width * size + 31) & ~15; }   // at any offset in 16 bytes
