@@ -19,7 +19,8 @@ _strides = {}     # structs by their values: calls of a program have few
 
 
 def _at(t, dims):
-    """The address of a _RowStrides for rows of t (2 or 3 dims, or more that are contiguous)."""
+    """(address, struct) of a _RowStrides for rows of t (2 or 3 dims, or more that are contiguous). The pair is what keeps the
+    struct: whoever hands the address on holds it until the library has returned, for the table may have let go of it."""
     s = t.stride()
     key = (s[0], 0) if dims == 2 else (s[0], s[1]) if dims == 3 else (t.shape[-1], 0)
     found = _strides.get(key)
@@ -28,7 +29,7 @@ def _at(t, dims):
             _strides.clear()
         struct = _RowStrides(*key)
         found = _strides[key] = (ctypes.addressof(struct), struct)
-    return found[0]
+    return found
 
 
 def rms_norm(x, gain, eps: float = 1e-6, residual=None, out_dtype=None, block: int = 0, out=None, sum_out=None):
@@ -79,9 +80,11 @@ def rms_norm(x, gain, eps: float = 1e-6, residual=None, out_dtype=None, block: i
         scales = torch.empty(shape[:-1] + (-(-width // block) if block else 1,), dtype=torch.float32, device=device)
     if rows == 0:
         return y, s, scales
-    launch(device.index, load_library().talker_rms_norm, "talker_rms_norm", x.data_ptr(), xt, _at(x, dims),
-           None if residual is None else residual.data_ptr(), rt, None if residual is None else _at(residual, dims),
-           gain.data_ptr(), eps, rows, shape[1] if dims == 3 else 1, width, None if s is None else s.data_ptr(),
-           None if s is None else _at(s, dims), y.data_ptr(), yt, _at(y, dims), block,
-           None if scales is None else scales.data_ptr())
+    none = (None, None)
+    x_at, y_at = _at(x, dims), _at(y, dims)
+    r_at, s_at = (none, none) if residual is None else (_at(residual, dims), _at(s, dims))
+    launch(device.index, load_library().talker_rms_norm, "talker_rms_norm", x.data_ptr(), xt, x_at[0],
+           None if residual is None else residual.data_ptr(), rt, r_at[0], gain.data_ptr(), eps, rows,
+           shape[1] if dims == 3 else 1, width, None if s is None else s.data_ptr(), s_at[0], y.data_ptr(), yt, y_at[0],
+           block, None if scales is None else scales.data_ptr())
     return y, s, scales
