@@ -6,8 +6,10 @@
 
 #include "rows.cuh"
 #include "talker_layer.h"
+#include "w4_ring.cuh"
 
 using namespace talker_dev;
+using namespace talker_k;
 
 namespace {
 
@@ -309,7 +311,7 @@ __device__ __forceinline__ uint32_t read2(uint32_t at) {
 
 constexpr int kMultiprocessors = 152, kMostShared = 227 * 1024;
 constexpr int kTiles = 2;                        // of a warp: one fragment of x, and one turn of the loop, serve both
-constexpr int kSlots = 4;                        // steps on their way or at hand: 135 KB a multiprocessor
+constexpr int kSlots = kW4Slots;                 // 135 KB a multiprocessor
 // Warps that multiply (one more makes the copies). With three or four column tiles a warp needs more registers than
 // sixteen leave it, and has enough to do for the tensor cores by itself.
 constexpr int warps_of(int nt) { return nt <= 2 ? 16 : 8; }
@@ -414,21 +416,21 @@ __global__ void __launch_bounds__((warps_of(NT) + 1) * 32, 1) k_w4_matmul(const 
         for (int i = 0; i < min(kSlots, count); ++i, next(x)) copy_x(x, i);
         int i = kSlots;
         for (; i < count; ++i, next(ahead)) {
-            if (!wait_for(&empty[i % kSlots], (i / kSlots - 1) & 1)) break;
-            copy_codes(ahead, i % kSlots);
-            copy_x(ahead, i % kSlots);
+            if (!wait_for(&empty[w4_slot(i)], w4_empty_parity(i))) break;
+            copy_codes(ahead, w4_slot(i));
+            copy_x(ahead, w4_slot(i));
         }
-        for (int k = max(0, min(i, count) - kSlots); k < min(i, count); ++k) wait_for(&full[k % kSlots], k / kSlots & 1);   // (nothing is on its way when the CTA ends)
+        for (int k = max(0, min(i, count) - kSlots); k < min(i, count); ++k) wait_for(&full[w4_slot(k)], w4_full_parity(k));   // (nothing is on its way when the CTA ends)
         return;
     }
 
     const uint32_t mine = warp * kTiles * record + lane * 16;   // in a slot
-    bool lost = false;
+    W4Ring ring;
     float total[kTiles][NT][4];
     bool fresh = true;
     int from_col[NT];
     for (int step = 0; step < count; ++step) {
-        const int slot = step % kSlots, tiles = at.tiles - warp * kTiles;   // tiles of this warp
+        const int slot = w4_slot(step), tiles = at.tiles - warp * kTiles;   // tiles of this warp
         if (fresh) {
             fresh = false;
             const int cols = min(a.c.cols, a.rows * parts - at.pass * a.c.cols);
@@ -437,20 +439,22 @@ __global__ void __launch_bounds__((warps_of(NT) + 1) * 32, 1) k_w4_matmul(const 
 #pragma unroll
                 for (int i = 0; i < NT; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) total[r][i][j] = lost ? NAN : 0.f;
+                    for (int j = 0; j < 4; ++j) total[r][i][j] = ring.lost ? NAN : 0.f;
 #pragma unroll
             for (int i = 0; i < NT; ++i) from_col[i] = (min(i * 8 + g, cols - 1) * 4 + t) * 16;   // (columns past the last are not looked at)
         }
-        if (!lost && !wait_for(&full[slot], step / kSlots & 1)) {
-            lost = true;
+        if (ring.waits()) {
+            ring.waited(__all_sync(0xffffffffu, wait_for(&full[slot], w4_full_parity(step))));   // (a warp's lanes agree)
+            if (ring.lost) {
 #pragma unroll
-            for (int r = 0; r < kTiles; ++r)
+                for (int r = 0; r < kTiles; ++r)
 #pragma unroll
-                for (int i = 0; i < NT; ++i)
+                    for (int i = 0; i < NT; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) total[r][i][j] = NAN;
+                        for (int j = 0; j < 4; ++j) total[r][i][j] = NAN;
+            }
         }
-        if (tiles > 0 && !lost) {
+        if (tiles > 0 && ring.reads()) {
             const uint32_t now = slots + slot * slot_bytes;
             const uint32_t x = now + kBlock * record, tail = now + mine - lane * 16 + kUnitBytes;   // scales, then zeros
             uint4 w[kTiles][2];
@@ -502,7 +506,7 @@ __global__ void __launch_bounds__((warps_of(NT) + 1) * 32, 1) k_w4_matmul(const 
             }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[slot]);   // (all of it has been read)
+        if (lane == 0 && ring.releases()) mbar_arrive(&empty[slot]);   // (all of it has been read)
         if (step + 1 == count || at.unit + 1 == units) {   // the segment's end
             float4 *place = a.sums + ((size_t)(blockIdx.x + at.place) * kWarps + warp) * kTiles * NT * 32 + lane;
 #pragma unroll
