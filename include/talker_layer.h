@@ -36,7 +36,7 @@ extern "C" {
  *   the nearest, ties to even; y stands for code * scale.
  * scales is f32 [rows][ceil(width / block)], contiguous. Blocks with max|y| below
  * 2^-100 (or max|s * gain| below it) store zeros; one with an infinity reads back as NaN.
- * A NaN in s makes its row NaN; the sum of a row's squares is to stay in f32's range.
+ * A NaN in s makes its row NaN, blocks of zeros too; the sum of a row's squares is to stay in f32's range.
  * sum_out may be residual or x, and y may be x or residual, with the same strides
  * and type; other overlaps are not allowed.
  * Errors: EINVAL (null x, gain or y; types; width not in 1..2^24; rows not in 0..2^30;
