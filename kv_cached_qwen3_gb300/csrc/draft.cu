@@ -25,7 +25,11 @@ constexpr float kMasked = -1e30f;       // at or below: counts as -inf
 constexpr float kLeastRef = -9.9999994e29f;   // reference of a row's exponents without a logit: the next value above kMasked
 constexpr float kGreedy = 1e-20f;       // a temperature not above it
 constexpr float kHottest = 1e18f;       // a temperature above it counts as this one (masked logits still add nothing)
-constexpr float kNear = 1e-4f;          // of f32 sums: decisions nearer to their border are made again, exactly
+// Of f32 sums: decisions nearer to their border are made again, exactly. A p above 1e-30 has an exponent of at most 100, whose
+// three roundings are 1.3e-5 of it; the terms of a sum that count have 46 at most (6e-6), and their additions add 1e-6 however
+// long the row is (Lane). With ex2's own 2^-22, p and q are off by 2.5e-5 each at most.
+constexpr float kNear = 1e-4f;
+constexpr float kAbove = 16.f;          // a lane's reference is moved by terms of more than 2^16
 
 struct Args {
     const void *target, *draft;
@@ -79,9 +83,10 @@ __device__ __forceinline__ float ex2(float x) {   // relative error about 2^-22,
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ Seen warp_join(Seen s, float c) {
+// s.sum is of e^((x - ref) / T).
+__device__ __forceinline__ Seen warp_join(Seen s, float ref, float c) {
     const float most = warp_max(s.most);
-    s.sum = warp_sum(s.sum * ex2((s.most - most) * c));
+    s.sum = warp_sum(s.sum * ex2((ref - most) * c));
     s.first = (int)__reduce_min_sync(0xffffffffu, s.most == most ? (uint32_t)s.first : 0x7fffffffu);
     s.most = most;
     return s;
@@ -103,9 +108,18 @@ template <> struct Vec<__nv_bfloat16> {
     }
 };
 
+// What a lane has seen, with sums whose error does not grow with the row: `lost` is what their roundings took off (Kahan), and
+// `ref`, from which exponents count, is moved only by a term of more than 2^16, next to which an earlier sum's errors, the
+// factor's own among them, are below 2^-16 of what they were. (One f32 sum, scaled anew whenever a larger logit came, was off by
+// up to 2^-22 for each of a row's 2^14 vectors.)
+struct Lane {
+    Seen seen{kLeastRef, 0.f, 0x7fffffff};
+    float ref = kLeastRef, lost = 0.f;
+};
 // n values, the first of them logit `at` of its row.
 template <int N>
-__device__ __forceinline__ void take(Seen &s, float (&x)[N], int at, float c, bool greedy) {
+__device__ __forceinline__ void take(Lane &l, float (&x)[N], int at, float c, bool greedy) {
+    Seen &s = l.seen;
     float top = kLeastRef;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -123,14 +137,18 @@ __device__ __forceinline__ void take(Seen &s, float (&x)[N], int at, float c, bo
         }
         return;
     }
-    if (top > s.most) {
-        s.sum *= ex2((s.most - top) * c);
-        s.most = top;
+    s.most = fmaxf(s.most, top);
+    if ((top - l.ref) * c > kAbove) {
+        const float less = ex2((l.ref - top) * c);
+        s.sum *= less, l.lost *= less;
+        l.ref = top;
     }
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) sum += ex2((x[i] - s.most) * c);
-    s.sum += sum;
+    for (int i = 0; i < N; ++i) sum += ex2((x[i] - l.ref) * c);
+    const float part = sum - l.lost, all = s.sum + part;
+    l.lost = (all - s.sum) - part;
+    s.sum = all;
 }
 
 // Part `part` of `parts` of a row, by one warp; c = log2 e / T. A part is so many of the row's vectors of 16 bytes; logits
@@ -142,7 +160,7 @@ __device__ Seen see_part(const T *row, int vocab, int part, int parts, float c, 
     const int lead = min(vocab, (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) % 16 / sizeof(T)));
     const int vecs = (vocab - lead) / N;
     const int from = (unsigned)vecs * part / parts, to = (unsigned)vecs * (part + 1) / parts;   // (2^24 times 32 at most)
-    Seen s{kLeastRef, 0.f, 0x7fffffff};
+    Lane s;
     if (part == 0 && lane < lead) {
         float x[1] = {load_logit(row, lane)};
         take(s, x, lane, c, greedy);
@@ -170,7 +188,7 @@ __device__ Seen see_part(const T *row, int vocab, int part, int parts, float c, 
         float x[1] = {load_logit(row, tail)};
         take(s, x, tail, c, greedy);
     }
-    return warp_join(s, c);
+    return warp_join(s.seen, s.ref, c);
 }
 
 // e^((x - most) / T) = m 2^(-30 - shift), m in [2^30, 2^31), for x <= most, to about 2^-29 of itself. With
@@ -342,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_draft_choose(const Args a) {
         const Seen *parts = OWN ? s.parts : a.seen + (size_t)seq * (2 * K + 1) * a.parts;
         for (int r = warp; r < n_rows; r += kWarps) {
             const Seen one = lane < a.parts ? parts[r * a.parts + lane] : Seen{kLeastRef, 0.f, 0x7fffffff};
-            const Seen seen = warp_join(one, c.hi);
+            const Seen seen = warp_join(one, one.most, c.hi);
             if (lane == 0) s.rows[r] = seen;
         }
         __syncthreads();

@@ -1,0 +1,83 @@
+"""GPU: the verification of drafts over very long vocabularies, and over rows whose logits are the least that count."""
+import math
+
+import numpy as np
+import pytest
+
+import layer_ref as ref
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module")
+def verify():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from kv_cached_qwen3_gb300.draft import draft_verify
+    return draft_verify
+
+
+def row(kind, vocab, dt):
+    i = torch.arange(vocab, device="cuda", dtype=torch.float32) / vocab
+    if kind == "equal":
+        x = torch.full((vocab,), -0.1, device="cuda")
+        x[5] = 0.0
+    elif kind == "rising":
+        x = 3 * i - 2
+    elif kind == "falling":
+        x = -3 * i
+    elif kind == "steep":
+        x = 40 * i
+    else:
+        x = torch.randn(vocab, device="cuda", generator=torch.Generator(device="cuda").manual_seed(3))
+    return x.to(DT[dt])
+
+
+def logs64(x):
+    """log p of every token, in 64 bits."""
+    x = x.double()
+    return x - torch.logsumexp(x, 0)
+
+
+# u q / p of a taken draft, and of a refused one: a decision is exact, or made by f32 sums with 1e-4 of room on both sides
+NEAR = (1 - 2e-4, 1 + 2e-4, 1 - 2e-6, 1 + 2e-6)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["equal", "rising", "falling", "steep", "random"])
+@pytest.mark.parametrize("n_seq,vocab", [(4, 1 << 26), (3300, 1 << 20), (4, 999983)])
+def test_long_rows(verify, dt, kind, n_seq, vocab):
+    """Rows of 2^26 logits, and of 2^20 with so many sequences that a warp goes over a row by itself; the same row for all.
+    log p of a taken draft: a sum whose error does not grow with the row, of exponentials within 2^-22 whose arguments
+    (58 at most, three roundings) add 58 * 3 * 2^-24 = 1e-5, and the result's own rounding."""
+    x = row(kind, vocab, dt)
+    token = vocab - 77
+    lp = float(logs64(x)[token])
+    target = x.expand(n_seq, 2, vocab)
+    tokens = torch.full((n_seq, 1), token, dtype=torch.int32, device="cuda")
+    near = torch.tensor(NEAR, dtype=torch.float64).repeat(n_seq // 4 + 1)[:n_seq]
+    u = torch.full((n_seq, 2), 0.25, dtype=torch.float32)
+    u[:, 0] = (math.exp(lp) * near).float()       # (rounded by 2^-24 at most)
+    out, n, lps = verify(target, tokens, u.cuda())
+    want = (near < 1).to(torch.int32)
+    assert torch.equal(n.cpu(), want), (kind, (n.cpu() != want).nonzero().flatten().tolist()[:8])
+    taken = want.bool()
+    assert (out.cpu()[taken, 0] == token).all()
+    assert ((lps.cpu()[taken, 0].double() - lp).abs() <= 1e-5 + abs(lp) * 2.0 ** -23).all(), (kind, lps.cpu()[taken, 0], lp)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_long_rows_of_both_models(verify, dt):
+    vocab = 1 << 24
+    p, q = row("equal", vocab, dt), row("rising", vocab, dt)
+    token = vocab - 77
+    ratio = math.exp(float(logs64(p)[token]) - float(logs64(q)[token]))
+    assert ratio < 1
+    u = torch.full((4, 2), 0.5, dtype=torch.float32)
+    u[:, 0] = (ratio * torch.tensor(NEAR, dtype=torch.float64)).float()
+    tokens = torch.full((4, 1), token, dtype=torch.int32, device="cuda")
+    _, n, _ = verify(p.expand(4, 2, vocab), tokens, u.cuda(), draft_logits=q.expand(4, 1, vocab))
+    assert n.tolist() == [1, 0, 1, 0]
