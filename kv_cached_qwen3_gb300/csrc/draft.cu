@@ -22,7 +22,7 @@ constexpr int kMaxDraft = 64, kMaxRows = 2 * kMaxDraft + 1;
 constexpr int kMaxParts = 32;           // of a row: a lane each where they are joined
 constexpr int kOwnParts = kMaxRows + kCluster * kWarps;   // of a sequence, where its cluster reads its rows itself
 constexpr float kMasked = -1e30f;       // at or below: counts as -inf
-constexpr float kLeastRef = -9.9999994e29f;   // reference of a row's exponents without a logit: the next value above kMasked
+constexpr float kLeastRef = -9.9999994e29f;   // the next value above kMasked: the least reference of exponents, below which masked ones add nothing
 constexpr float kGreedy = 1e-20f;       // a temperature not above it
 constexpr float kHottest = 1e18f;       // a temperature above it counts as this one (masked logits still add nothing)
 // Of f32 sums: decisions nearer to their border are made again, exactly. A p above 1e-30 has an exponent of at most 100, whose
@@ -71,25 +71,26 @@ __device__ __forceinline__ const T *row_at(const Args &a, const Sequence &s, int
                            : static_cast<const T *>(a.draft) + seq * a.draft_seq + (r - s.targets()) * a.draft_row;
 }
 
-// A row's largest logit (at least kLeastRef, below which masked ones add nothing), the first place that has it (of greedy
-// sequences), and the sum of e^((x - most) / T) (of others).
+// A row's largest logit (kMasked where none counts), the first place that has it (of greedy sequences), and the sum of
+// e^((x - ref) / T) (of others).
 struct Seen {
     float most, sum;
     int first;
-    __device__ __forceinline__ bool alive() const { return most > kLeastRef && most < INFINITY; }
+    __device__ __forceinline__ float ref() const { return fmaxf(most, kLeastRef); }
+    __device__ __forceinline__ bool alive() const { return most > kMasked && most < INFINITY; }
 };
 __device__ __forceinline__ float ex2(float x) {   // relative error about 2^-22, 0 at -inf
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// s.sum is of e^((x - ref) / T).
+// s.sum counts from `ref`.
 __device__ __forceinline__ Seen warp_join(Seen s, float ref, float c) {
-    const float most = warp_max(s.most);
-    s.sum = warp_sum(s.sum * ex2((ref - most) * c));
-    s.first = (int)__reduce_min_sync(0xffffffffu, s.most == most ? (uint32_t)s.first : 0x7fffffffu);
-    s.most = most;
-    return s;
+    Seen all;
+    all.most = warp_max(s.most);
+    all.sum = warp_sum(s.sum * ex2((ref - all.ref()) * c));
+    all.first = (int)__reduce_min_sync(0xffffffffu, s.most == all.most ? (uint32_t)s.first : 0x7fffffffu);
+    return all;
 }
 
 template <typename T> struct Vec;
@@ -113,14 +114,14 @@ template <> struct Vec<__nv_bfloat16> {
 // factor's own among them, are below 2^-16 of what they were. (One f32 sum, scaled anew whenever a larger logit came, was off by
 // up to 2^-22 for each of a row's 2^14 vectors.)
 struct Lane {
-    Seen seen{kLeastRef, 0.f, 0x7fffffff};
+    Seen seen{kMasked, 0.f, 0x7fffffff};
     float ref = kLeastRef, lost = 0.f;
 };
 // n values, the first of them logit `at` of its row.
 template <int N>
 __device__ __forceinline__ void take(Lane &l, float (&x)[N], int at, float c, bool greedy) {
     Seen &s = l.seen;
-    float top = kLeastRef;
+    float top = kMasked;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         x[i] = fmaxf(x[i], kMasked);   // NaN too
@@ -292,7 +293,7 @@ struct Row {
     uint32_t factor;        // 0: no distribution
     int down;
     unsigned long long z;   // the sum of e^((x - most) / T), in units of 2^-(31 + lift); 0: not made
-    __device__ __forceinline__ bool alive() const { return most > kLeastRef; }
+    __device__ __forceinline__ bool alive() const { return most > kMasked; }
 };
 // 2^95 / z for z in [2^63, 2^64), in [2^31, 2^32), to about 2^-31 of itself: an f32 reciprocal and one step of Newton's
 // method on the upper 32 bits. (f64 divisions by all threads of a CTA would take 3 us.)
@@ -359,8 +360,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_draft_choose(const Args a) {
     {
         const Seen *parts = OWN ? s.parts : a.seen + (size_t)seq * (2 * K + 1) * a.parts;
         for (int r = warp; r < n_rows; r += kWarps) {
-            const Seen one = lane < a.parts ? parts[r * a.parts + lane] : Seen{kLeastRef, 0.f, 0x7fffffff};
-            const Seen seen = warp_join(one, one.most, c.hi);
+            const Seen one = lane < a.parts ? parts[r * a.parts + lane] : Seen{kMasked, 0.f, 0x7fffffff};
+            const Seen seen = warp_join(one, one.ref(), c.hi);
             if (lane == 0) s.rows[r] = seen;
         }
         __syncthreads();
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_draft_choose(const Args a) {
         if (greedy) break;
         verdict = n < count ? s.verdict[n] : kRefuse;
         const bool has_q = drafted && n < count;
-        p = Row{kLeastRef, 0, 0, 0}, q = p;
+        p = Row{kMasked, 0, 0, 0}, q = p;
         if (s.rows[n].alive()) p.most = s.rows[n].most;
         if (has_q && s.rows[sq.targets() + n].alive()) q.most = s.rows[sq.targets() + n].most;
         rp = row_at<T>(a, sq, seq, n);

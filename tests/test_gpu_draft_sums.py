@@ -81,3 +81,34 @@ def test_long_rows_of_both_models(verify, dt):
     tokens = torch.full((4, 1), token, dtype=torch.int32, device="cuda")
     _, n, _ = verify(p.expand(4, 2, vocab), tokens, u.cuda(), draft_logits=q.expand(4, 1, vocab))
     assert n.tolist() == [1, 0, 1, 0]
+
+
+LEAST = float(np.nextafter(np.float32(-1e30), np.float32(0)))    # the least logit that counts
+
+
+@pytest.mark.parametrize("temp", [0.0, 1e-19, 1.0, 1e18, math.inf])
+@pytest.mark.parametrize("vocab", [1, 3, 700, 50001])
+def test_least_logits(verify, temp, vocab):
+    """Rows whose only logits that count are the least that do: one, two, and beside masked values and NaNs."""
+    S = 6
+    t = torch.full((S, 2, vocab), -1e30)
+    at = vocab // 2
+    t[0, :, at] = LEAST
+    t[1, :, 0] = t[1, :, at] = LEAST
+    t[2] = LEAST
+    t[3, :, at] = float(np.nextafter(np.float32(LEAST), np.float32(0)))
+    t[4, :, 0], t[4, :, at] = math.nan, LEAST
+    # (row 5: none)
+    tokens = torch.full((S, 1), at, dtype=torch.int32)
+    u = torch.tensor([[0.4, 0.6]]).repeat(S, 1)
+    d = torch.full((S, 1, vocab), -math.inf)
+    d[:, 0, at] = LEAST
+    temps = torch.full((S,), temp)
+    for draft in (None, d):
+        out, n, lp = (x.cpu() for x in verify(t.cuda(), tokens.cuda(), u.cuda(), draft_logits=None if draft is None else draft.cuda(), temperatures=temps.cuda()))
+        for s in range(S):
+            # (temperatures above 1e18 count as it; so do they to the reference, whose rows hold equal logits or masked ones)
+            want = ref.verify(t[s].double().numpy(), tokens[s].numpy(), u[s].double().numpy(), None if draft is None else draft[s].double().numpy(),
+                              temp=min(temp, 1e18))
+            assert out[s].tolist() == want[0] and int(n[s]) == want[1], (s, out[s], want)
+            assert (lp[s].double() - torch.tensor(want[2])).abs().max() <= 2e-5
