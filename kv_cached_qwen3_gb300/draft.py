@@ -3,7 +3,7 @@ from __future__ import annotations
 
 import torch
 
-from .kv4 import _DTYPE, launch
+from .kv4 import _DTYPE, contiguous_rows, launch
 from .talker import load_library
 
 _scratch = {}     # scratch bytes by (n_seq, n_draft, vocab)
@@ -20,7 +20,7 @@ def draft_verify(target_logits, tokens, uniforms, draft_logits=None, counts=None
     Logits lie in any strides with contiguous vocabularies. Returns tokens int32 [n_seq, n_draft + 1] (those taken, the next one, then -1), the
     number taken int32 [n_seq], and the log-probabilities of the tokens f32 [n_seq, n_draft + 1] (0 for those of -1)."""
     shape, dtype, device = target_logits.shape, _DTYPE.get(target_logits.dtype), target_logits.device
-    if len(shape) != 3 or dtype is None or device.type != "cuda" or target_logits.stride(2) != 1:
+    if len(shape) != 3 or dtype is None or device.type != "cuda" or not contiguous_rows(target_logits):
         raise ValueError("draft_verify: target_logits must be an f32 or bf16 CUDA tensor [n_seq, n_draft + 1, vocab] with "
                          "contiguous vocabularies")
     n_seq, n_draft, vocab = shape[0], shape[1] - 1, shape[2]
@@ -34,7 +34,7 @@ def draft_verify(target_logits, tokens, uniforms, draft_logits=None, counts=None
     d_at, d_seq, d_row = None, 0, 0
     if draft_logits is not None and n_draft > 0:
         if draft_logits.shape != (n_seq, n_draft, vocab) or draft_logits.dtype is not target_logits.dtype or \
-                draft_logits.device != device or draft_logits.stride(2) != 1:
+                draft_logits.device != device or not contiguous_rows(draft_logits):
             raise ValueError("draft_verify: draft_logits must be [n_seq, n_draft, vocab] in target_logits' type with "
                              "contiguous vocabularies")
         d_at, (d_seq, d_row, _) = draft_logits.data_ptr(), draft_logits.stride()

@@ -41,6 +41,11 @@ def launch(device: int, fn, what, *args):
         raise TalkerError(status, what)
 
 
+def contiguous_rows(t) -> bool:
+    """The values of t's last dimension are neighbours (a dimension of one element has no stride)."""
+    return t.stride(-1) == 1 or t.shape[-1] == 1
+
+
 class KV4Cache:
     """Pools of 4-bit pages and the page table that names each stream's pages.
 

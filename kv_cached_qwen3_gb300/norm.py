@@ -5,7 +5,7 @@ import ctypes
 
 import torch
 
-from .kv4 import launch
+from .kv4 import contiguous_rows, launch
 from .talker import load_library
 
 ROW_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float8_e4m3fn: 4}
@@ -44,7 +44,7 @@ def rms_norm(x, gain, eps: float = 1e-6, residual=None, out_dtype=None, block: i
     shape, device = x.shape, x.device
     dims = len(shape)
     xt = ROW_TYPES.get(x.dtype, 4)
-    if dims < 2 or xt == 4 or device.type != "cuda" or x.stride(-1) != 1 or shape[-1] < 1:
+    if dims < 2 or xt == 4 or device.type != "cuda" or not contiguous_rows(x) or shape[-1] < 1:
         raise ValueError("rms_norm: x must be an f32 or bf16 CUDA tensor [..., width] with contiguous values")
     width = shape[-1]
     rows = x.numel() // width
@@ -62,16 +62,16 @@ def rms_norm(x, gain, eps: float = 1e-6, residual=None, out_dtype=None, block: i
         rt, s = 0, None
     else:
         rt = ROW_TYPES.get(residual.dtype, 4)
-        if residual.shape != shape or rt == 4 or residual.device != device or residual.stride(-1) != 1:
+        if residual.shape != shape or rt == 4 or residual.device != device or not contiguous_rows(residual):
             raise ValueError("rms_norm: residual must be f32 or bf16 of x's shape and device with contiguous values")
         s = torch.empty(shape, dtype=residual.dtype, device=device) if sum_out is None else sum_out
-        if sum_out is not None and (s.shape != shape or s.dtype is not residual.dtype or s.device != device or s.stride(-1) != 1):
+        if sum_out is not None and (s.shape != shape or s.dtype is not residual.dtype or s.device != device or not contiguous_rows(s)):
             raise ValueError("rms_norm: sum_out must have residual's shape and type and contiguous values")
     if out is None:
         y = torch.empty(shape, dtype=out_dtype, device=device)
     else:
         y = out
-        if y.shape != shape or y.dtype is not out_dtype or y.device != device or y.stride(-1) != 1:
+        if y.shape != shape or y.dtype is not out_dtype or y.device != device or not contiguous_rows(y):
             raise ValueError("rms_norm: out must have x's shape, out_dtype and contiguous values")
     if dims > 3 and not all(t is None or t.is_contiguous() for t in (x, residual, s, y)):
         raise ValueError("rms_norm: tensors of more than 3 dims must be contiguous")

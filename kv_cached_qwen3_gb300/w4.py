@@ -5,7 +5,7 @@ import ctypes
 
 import torch
 
-from .kv4 import _DTYPE, launch
+from .kv4 import _DTYPE, contiguous_rows, launch
 from .norm import ROW_TYPES
 from .talker import load_library
 
@@ -19,7 +19,7 @@ def quantize(w, group: int = 32):
     (the even input in the low four bits), and fp16 [n, ceil(k / group)], by the rule of the 4-bit cache over groups of 32,
     64 or 128 inputs: a code c stands for (c - 8) scale."""
     dtype = _DTYPE.get(w.dtype)
-    if w.dim() != 2 or dtype is None or not w.is_cuda or w.stride(1) != 1 or 0 in w.shape:
+    if w.dim() != 2 or dtype is None or not w.is_cuda or not contiguous_rows(w) or 0 in w.shape:
         raise ValueError("quantize: w must be an f32 or bf16 CUDA tensor [n, k] with contiguous rows")
     if group not in (32, 64, 128):
         raise ValueError("quantize: group must be 32, 64 or 128")
@@ -81,7 +81,7 @@ class W4Matrix:
         gated matrix silu(W x) * (U x). residual [rows, n] in the result's type is added. Returns [rows, n] f32 or bf16
         (out_dtype; default x's type, of 8-bit rows f32); out names a tensor to write to, which may be residual."""
         xt, shape = ROW_TYPES.get(x.dtype), x.shape
-        if len(shape) != 2 or xt is None or shape[1] != self.k or x.device != self.device or x.stride(1) != 1:
+        if len(shape) != 2 or xt is None or shape[1] != self.k or x.device != self.device or not contiguous_rows(x):
             raise ValueError("matmul: x must be f32, bf16 or float8_e4m3fn [rows, %d] on %s with contiguous rows" % (self.k, self.device))
         rows, block = shape[0], 0
         if xt == 4:
@@ -99,10 +99,10 @@ class W4Matrix:
             raise ValueError("matmul: out_dtype must be float32 or bfloat16")
         if out is None:
             out = torch.empty((rows, self.n), dtype=out_dtype, device=self.device)
-        elif out.shape != (rows, self.n) or out.dtype is not out_dtype or out.device != self.device or out.stride(1) != 1:
+        elif out.shape != (rows, self.n) or out.dtype is not out_dtype or out.device != self.device or not contiguous_rows(out):
             raise ValueError("matmul: out must be [rows, %d] with contiguous rows" % self.n)
         if residual is not None and (residual.shape != out.shape or residual.dtype is not out_dtype or
-                                     residual.device != self.device or residual.stride(1) != 1):
+                                     residual.device != self.device or not contiguous_rows(residual)):
             raise ValueError("matmul: residual must be [rows, %d] in the result's type with contiguous rows" % self.n)
         if rows == 0:
             return out
