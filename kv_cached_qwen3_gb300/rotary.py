@@ -48,6 +48,8 @@ class Rotary:
         rotary_dim = head_dim if rotary_dim is None else rotary_dim
         if not 2 <= head_dim <= 512 or rotary_dim < 2 or rotary_dim % 2 or rotary_dim > head_dim:
             raise ValueError("Rotary: needs head_dim 2 to 512 and an even rotary_dim of at most head_dim")
+        if torch.device(device).type != "cuda":
+            raise ValueError("Rotary: needs a CUDA device")
         rope = make_rope(rotary_dim, theta, scaling)
         table = np.empty(rotary_dim // 2, np.uint64)
         amplitude = ctypes.c_float()
