@@ -84,7 +84,7 @@ typedef struct {
     double theta;        /* above 1 */
     double factor;       /* at least 1 */
     double original;     /* SMOOTH, YARN: positions of the original context */
-    double low, high;    /* SMOOTH, YARN (its beta_slow and beta_fast): turns, low < high */
+    double low, high;    /* SMOOTH, YARN (its beta_slow and beta_fast, above 0): turns, low < high */
     double amplitude;    /* YARN: 0 for the rule above */
 } talker_rope;
 /* The table (HOST array of rotary_dim / 2) and amplitude (HOST) of a rope. A host function:

@@ -154,8 +154,8 @@ bool rope_frequencies(const talker_rope &r, double *freq, double *amplitude) {
     if (!(r.theta > 1.0) || !std::isfinite(r.theta)) return false;
     if (r.scaling != TALKER_ROPE_NONE && (!(r.factor >= 1.0) || !std::isfinite(r.factor))) return false;
     if (r.scaling == TALKER_ROPE_NTK && r.rotary_dim < 4) return false;
-    if (ranged && (!(r.original > 0.0) || !std::isfinite(r.original) || !(r.low > 0.0) || !(r.high > r.low) || !std::isfinite(r.high))) return false;
-    if (r.scaling == TALKER_ROPE_YARN && (!(r.amplitude >= 0.0) || !std::isfinite(r.amplitude))) return false;
+    if (ranged && (!(r.original > 0.0) || !std::isfinite(r.original) || !std::isfinite(r.low) || !(r.high > r.low) || !std::isfinite(r.high))) return false;
+    if (r.scaling == TALKER_ROPE_YARN && (!(r.low > 0.0) || !(r.amplitude >= 0.0) || !std::isfinite(r.amplitude))) return false;
     const double d = r.rotary_dim;
     double lo = 0.0, hi = 0.0, theta = r.theta;
     *amplitude = 1.0;
