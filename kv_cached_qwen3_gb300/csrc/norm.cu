@@ -109,11 +109,8 @@ struct Scale {
     __device__ __forceinline__ Scale(float m, float norm) {
         const float d = m * norm;   // max|y|
         const bool none = d < 0x1p-100f || (m < 0x1p-100f && norm == norm);   // (a NaN in the row: in all its blocks, of zeros too)
-        float inv;
-        asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(m));
-        const float near = 448.f * inv, better = fmaf(fmaf(-m, near, 448.f), inv, near);   // (an error here is all of a block's)
         scale = none ? 0.f : d * (1.f / 448.f);
-        codes = none ? 0.f : d < INFINITY ? better : NAN;
+        codes = none ? 0.f : d < INFINITY ? __fdiv_rn(448.f, m) : NAN;   // (to the last place: an error here is all of a block's)
     }
 };
 
