@@ -154,7 +154,6 @@ template <typename TX, typename TR, typename TY, int C>
 __global__ void __launch_bounds__(most_threads(C), 1) k_rms_norm(const NormArgs a) {
     constexpr bool kRes = !std::is_same<TR, void>::value, k8 = std::is_same<TY, __nv_fp8_storage_t>::value;
     constexpr int H = C > 0 ? C : 1;   // chunks in registers
-    constexpr bool kAhead = C > 0;
     using R = typename std::conditional<kRes, TR, float>::type;
     using Y = typename std::conditional<k8, float, TY>::type;
     __shared__ float sums[2][32], tops[2][32];   // of a row's warps; of every other turn, so that one wait a turn is enough
@@ -175,7 +174,7 @@ __global__ void __launch_bounds__(most_threads(C), 1) k_rms_norm(const NormArgs 
     };
     int row = blockIdx.x * blockDim.y + threadIdx.y;
     Row now = row_of(row);
-    if (kAhead) {
+    if (C > 0) {
 #pragma unroll
         for (int c = 0; c < H; ++c) fetch(now, c, x[c], r[c]);
     }
@@ -191,13 +190,10 @@ __global__ void __launch_bounds__(most_threads(C), 1) k_rms_norm(const NormArgs 
         };
         const Row next = row_of(row + per < a.rows ? row + per : a.rows);
         if (C > 0) {
-            if (!kAhead) fetch(now, 0, x[0], r[0]);
 #pragma unroll
             for (int c = 0; c < H; ++c) sum_of(x[c], r[c], held[c]);
-            if (kAhead) {
 #pragma unroll
-                for (int c = 0; c < H; ++c) fetch(next, c, x[c], r[c]);
-            }
+            for (int c = 0; c < H; ++c) fetch(next, c, x[c], r[c]);
 #pragma unroll
             for (int c = 0; c < H; ++c) add(held[c]);
         } else {
