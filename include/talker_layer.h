@@ -38,10 +38,10 @@ extern "C" {
  * 2^-100 (or max|s * gain| below it) store zeros; one with an infinity reads back as NaN.
  * A NaN in s makes its row NaN, blocks of zeros too; the sum of a row's squares is to stay in f32's range.
  * sum_out may be residual or x, and y may be x or residual, with the same strides
- * and type; other overlaps are not allowed.
+ * and type; other overlaps are not allowed, nor are rows of sum_out or y at a stride of 0.
  * Errors: EINVAL (null x, gain or y; types; width not in 1..2^24; rows not in 0..2^30;
  * inner < 1; eps not at least 0; a block that is not offered; scales missing with
- * E4M3), ECUDA. */
+ * E4M3; results at a stride of 0), ECUDA. */
 typedef struct {
     int64_t outer, inner; /* strides in elements */
 } talker_row_strides;
@@ -109,7 +109,7 @@ typedef struct {
 /* Rotate the heads of n_sets (1 or 2, for example q and k; HOST array) sets of heads of
  * the same rows. positions: int32 [streams][rows], any value (negative ones rotate back). turns: device table.
  * dtype F32 or BF16 for all. Errors: EINVAL (null pointers, sizes below 0, head_dim not in 2..512,
- * rotary_dim odd or above head_dim, more than 16384 heads in a set, streams * rows above 2^30), ECUDA. */
+ * rotary_dim odd or above head_dim, more than 16384 heads in a set, streams * rows above 2^30, several heads written at a stride of 0), ECUDA. */
 talker_status talker_rotate(const uint64_t *turns, float amplitude, int head_dim, int rotary_dim, int interleaved,
                             const int32_t *positions, int streams, int rows, const talker_heads *sets, int n_sets,
                             int dtype, void *cuda_stream);

@@ -470,6 +470,8 @@ Place place(const void *p, int dtype, const talker_row_strides *s, int rows, int
     vec = vec && aligned(p, 8 * size_of(dtype)) && r.outer % 8 == 0 && r.inner % 8 == 0;
     return r;
 }
+// Rows of a result lie in places of their own.
+bool apart(const Place &p, int rows, int inner) { return (rows <= inner || p.outer != 0) && (std::min(rows, inner) <= 1 || p.inner != 0); }
 
 }  // namespace
 
@@ -497,6 +499,7 @@ extern "C" talker_status talker_rms_norm(const void *x, int x_dtype, const talke
     if (residual) a.res_at = place(residual, res_dtype, res_at, rows, inner, vec);
     if (sum_out) a.sum_at = place(sum_out, res_dtype, sum_at, rows, inner, vec);
     a.y_at = place(y, y_dtype, y_at, rows, inner, vec);
+    if (!apart(a.y_at, rows, inner) || (sum_out && !apart(a.sum_at, rows, inner))) return TALKER_EINVAL;
     // (both kernels' sides are beside them)
     const int row_bytes = slot_bytes(width, size_of(x_dtype)) + (residual ? slot_bytes(width, size_of(res_dtype)) : 0);
     const int kind = !vec ? 2 * row_bytes <= kMostStaged ? -1 : -2 : width <= 4 * 8 * most_threads(4) ? 4 : 0;

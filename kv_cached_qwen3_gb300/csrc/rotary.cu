@@ -208,6 +208,10 @@ talker_status talker_rotate(const uint64_t *turns, float amplitude, int head_dim
         copy |= s.in != s.out;
     }
     if (streams == 0 || rows == 0 || a.heads == 0) return TALKER_OK;
+    for (int i = 0; i < n_sets; ++i) {   // heads of a result lie in places of their own
+        const talker_heads &s = sets[i];
+        if (s.heads > 0 && ((streams > 1 && s.out_stream == 0) || (rows > 1 && s.out_row == 0) || (s.heads > 1 && s.out_head == 0))) return TALKER_EINVAL;
+    }
     // the largest vector that fits the dims and every tensor's place and strides
     int vp = 16 / size;
     auto fits = [&](int n) {

@@ -52,3 +52,33 @@ def test_drafts_over_one_token():
     tokens, u = torch.zeros(3, 2, dtype=torch.int32).cuda(), ref.uni(3, 3, 3).cuda()
     for a, b in zip(draft_verify(odd(t), tokens, u, draft_logits=odd(d)), draft_verify(t, tokens, u, draft_logits=d)):
         assert torch.equal(a, b)
+
+
+def test_rows_that_all_read_one_place():
+    """Inputs that rows share, and results that they would: the first are taken, the second refused."""
+    from kv_cached_qwen3_gb300.norm import rms_norm
+    from kv_cached_qwen3_gb300.rotary import Rotary
+    from kv_cached_qwen3_gb300.talker import TalkerError
+    for width in (64, 47):
+        x, r, gain = ref.rnd(1, 5, width).cuda(), ref.rnd(2, 1, width).cuda(), torch.ones(width).cuda()
+        y, s, _ = rms_norm(x, gain, residual=r.expand(5, width))
+        y2, s2, _ = rms_norm(x, gain, residual=r.expand(5, width).contiguous())
+        assert torch.equal(y, y2) and torch.equal(s, s2)
+        with pytest.raises(TalkerError):
+            rms_norm(x, gain, residual=r.expand(5, width), sum_out=r.expand(5, width))
+        with pytest.raises(TalkerError):
+            rms_norm(x, gain, out=torch.zeros(1, width).cuda().expand(5, width))
+        h = ref.rnd(3, 4, 1, width).cuda()
+        z = rms_norm(h.expand(4, 3, width), gain)[0]
+        assert torch.equal(z, rms_norm(h, gain)[0].expand(4, 3, width))
+        with pytest.raises(TalkerError):
+            rms_norm(h.expand(4, 3, width), gain, out=h.expand(4, 3, width))
+    rope, pos = Rotary(64), torch.arange(4, dtype=torch.int32).cuda()
+    q = ref.rnd(4, 4, 1, 64).cuda()
+    turned = rope.rotate(q, None, pos)[0]
+    assert torch.equal(rope.rotate(q.expand(4, 3, 64), None, pos)[0], turned.expand(4, 3, 64))
+    before = q.clone()
+    with pytest.raises(TalkerError):
+        rope.rotate(q.expand(4, 3, 64), None, pos, out=(q.expand(4, 3, 64),))
+    assert torch.equal(q, before)
+    assert torch.equal(rope.rotate(q, None, pos, out=(q,))[0], turned)
