@@ -223,9 +223,8 @@ __constant__ uint32_t kRoots[32] = {   // 2^(31 + j / 32), to the nearest
     3611622603u, 3690706840u, 3771522796u, 3854108391u, 3938502376u, 4024744348u, 4112874773u, 4202935003u};
 // Two of them at once, in packed f32 arithmetic (half the instructions), with -most of each. Whole numbers come from f32
 // sums with 1.5 2^23, whose last place is 1: conversions are a quarter as fast. Where the result is 0 what is made on the
-// way means nothing. ROUNDED: a difference of logits may not fit f32 (of bf16 ones it does wherever it counts: exponents less
-// than 2^15 apart), so what is left of it is carried along.
-template <bool ROUNDED>
+// way means nothing. A difference of logits may not fit f32 (of bf16 ones neither: 16 and -2^-20), so what is left of it is
+// carried along.
 __device__ __forceinline__ void exact_exp2(float x0, float x1, F2 less, const Scale c, const uint32_t *roots, Exact &e0, Exact &e1) {
     constexpr float kWhole = 12582912.f;
     constexpr uint32_t kWholeBits = 0x4b400000u;
@@ -234,11 +233,8 @@ __device__ __forceinline__ void exact_exp2(float x0, float x1, F2 less, const Sc
     const F2 minus = f2(-1.f, -1.f), hi = f2(c.hi, c.hi), nhi = f2(-c.hi, -c.hi), nlo = f2(-c.lo, -c.lo);
     const F2 ln2 = f2(kLn2, kLn2), nln2 = f2(-kLn2, -kLn2), whole = f2(kWhole, kWhole), nwhole = f2(-kWhole, -kWhole);
     const F2 x = f2(x0, x1), d = x + less, t = d * hi;
-    F2 nt = fma2(d, nlo, fma2(d, nhi, t));
-    if (ROUNDED) {
-        const F2 b = fma2(d, minus, x), dl = fma2(d + b, minus, x) + (b + less);   // x - most = d + dl, exactly
-        nt = fma2(dl, nhi, nt);
-    }
+    const F2 b = fma2(d, minus, x), dl = fma2(d + b, minus, x) + (b + less);   // x - most = d + dl, exactly
+    const F2 nt = fma2(dl, nhi, fma2(d, nlo, fma2(d, nhi, t)));
     const F2 k = fma2(t, f2(32.f, 32.f), whole), f0 = fma2(k + nwhole, f2(-1.f / 32.f, -1.f / 32.f), t);
     const F2 f = fma2(nt, minus, f0), nf = nt + fma2(f0, minus, f);
     const F2 y = f * ln2, ny = fma2(f, f2(-kLn2Lo, -kLn2Lo), fma2(nf, ln2, fma2(f, nln2, y)));
@@ -408,14 +404,13 @@ __global__ void __launch_bounds__(kThreads, 4) k_draft_choose(const Args a) {
         }
         cluster.sync();
     };
-    constexpr bool kRounded = sizeof(T) == 4;
     // f(exponential of token i of p, i), or f(p's, q's), for the warp's range
     auto over_one = [&](auto f) {
         const F2 less = f2(-p.most, -p.most);
 #pragma unroll 2
         for (int i = w0 + lane; i < w1; i += 64) {
             Exact e, g;
-            exact_exp2<kRounded>(load_logit(rp, i), i + 32 < w1 ? load_logit(rp, i + 32) : -INFINITY, less, c, s.roots, e, g);
+            exact_exp2(load_logit(rp, i), i + 32 < w1 ? load_logit(rp, i + 32) : -INFINITY, less, c, s.roots, e, g);
             f(e, i);
             f(g, i + 32);
         }
@@ -425,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_draft_choose(const Args a) {
 #pragma unroll 2
         for (int i = w0 + lane; i < w1; i += 32) {
             Exact e, g;
-            exact_exp2<kRounded>(load_logit(rp, i), load_logit(rq, i), less, c, s.roots, e, g);
+            exact_exp2(load_logit(rp, i), load_logit(rq, i), less, c, s.roots, e, g);
             f(e, g);
         }
     };
@@ -507,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_draft_choose(const Args a) {
             const int i0 = min(b0 + tid * own, b1), i1 = min(i0 + own, b1);
             auto at_token = [&](int i) {
                 Exact e, g;
-                exact_exp2<kRounded>(load_logit(rp, i), minus_q ? load_logit(rq, i) : 0.f, f2(-p.most, -q.most), c, s.roots, e, g);
+                exact_exp2(load_logit(rp, i), minus_q ? load_logit(rq, i) : 0.f, f2(-p.most, -q.most), c, s.roots, e, g);
                 return minus_q ? left(e, g, plain) : weight(e, i, plain);
             };
             unsigned long long sum = 0;
@@ -532,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_draft_choose(const Args a) {
                         z = total;
                         if (gone >= 0 && gone < V && !plain) {
                             Exact e, g;
-                            exact_exp2<kRounded>(load_logit(rp, gone), 0.f, f2(-p.most, 0.f), c, s.roots, e, g);
+                            exact_exp2(load_logit(rp, gone), 0.f, f2(-p.most, 0.f), c, s.roots, e, g);
                             z += place(e.m, bits + e.shift);
                         }
                     }

@@ -112,3 +112,21 @@ def test_least_logits(verify, temp, vocab):
                               temp=min(temp, 1e18))
             assert out[s].tolist() == want[0] and int(n[s]) == want[1], (s, out[s], want)
             assert (lp[s].double() - torch.tensor(want[2])).abs().max() <= 2e-5
+
+
+@pytest.mark.parametrize("top,rest", [(9.0, -0.9921875 * 2.0 ** -21), (12.0, -0.9921875 * 2.0 ** -21), (9.0, 0.4921875 * 2.0 ** -20), (5.0, -0.9921875 * 2.0 ** -22)])
+def test_bf16_logits_far_apart_in_size(verify, top, rest):
+    """Logits next to 0 under a larger one, whose differences have more bits than f32: a draw is that of the same logits in f32.
+    (Half of them are 0 and lose nothing; without what the difference rounds off of the others, 2^-22 or 2^-21, draws
+    among 2^24 are a token or more away.)"""
+    S, vocab = 64, 1 << 24
+    x = torch.zeros(vocab, dtype=torch.bfloat16, device="cuda")
+    x[1:vocab // 2] = rest
+    x[0] = top
+    assert float(x[1]) == rest
+    u = (0.2 + 0.6 * torch.arange(S, dtype=torch.float32) / S)[:, None].cuda()
+    none = torch.zeros(S, 0, dtype=torch.int32, device="cuda")
+    out, _, lp = verify(x.expand(S, 1, vocab), none, u)
+    same, _, lp32 = verify(x.float().expand(S, 1, vocab), none, u)
+    assert torch.equal(out, same)
+    assert (lp - lp32).abs().max() <= 1e-6
