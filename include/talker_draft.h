@@ -39,8 +39,9 @@ extern "C" {
  * are taken to [0, n_draft] and uniform numbers to [0, 1] (NaN: 0).
  *
  * Probabilities that decide (p and q of a draft near its border, all of the row that is
- * drawn from) are made to about 2^-29 of themselves and summed as whole numbers (in the
- * sums and the draw those below 2^-70 of the row's largest count as 0), so
+ * drawn from) are made to about 2^-29 of themselves and summed as whole numbers, in units
+ * that cut off less than 2^-28 of a sum (those below 2^-70 of the row's largest count as 0,
+ * and where q is taken off, those below 2^-62), so
  * neither a row's address nor the launch's shape changes a token; the sums of taken drafts'
  * logprobs are f32.
  *

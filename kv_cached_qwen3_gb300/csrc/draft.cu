@@ -283,13 +283,16 @@ struct Shared {
     unsigned long long cta[kCluster][2];       // every CTA's sums
 };
 
-// A row of probabilities: p = (m factor >> 32) 2^32 >> (down + shift), in units of 2^-62, of an Exact.
+// A row of probabilities: p = (m factor >> 32) 2^32 >> (down + shift), in units of 2^-62, of an Exact. (A row's largest has 2^(62 - bits) units
+// of z: no shift to the left.)
 struct Row {
     float most;
     uint32_t factor;        // 0: no distribution
     int down;
-    unsigned long long z;   // the sum of e^((x - most) / T), in units of 2^-(31 + lift); 0: not made
+    unsigned long long z;   // the sum of e^((x - most) / T), in units of 2^(bits - 62); 0: not made
+    int bits;
     __device__ __forceinline__ bool alive() const { return most > kMasked; }
+    __device__ __forceinline__ void has(unsigned long long sum);
 };
 // 2^95 / z for z in [2^63, 2^64), in [2^31, 2^32), to about 2^-31 of itself: an f32 reciprocal and one step of Newton's
 // method on the upper 32 bits. (f64 divisions by all threads of a CTA would take 3 us.)
@@ -299,6 +302,12 @@ __device__ __forceinline__ uint32_t reciprocal(unsigned long long z) {
     const long long left = (long long)((1ull << 63) - (unsigned long long)r * top);   // 2^63 times what is missing of r, relative
     const long long better = (long long)r + (((long long)r * (left >> 31)) >> 32);
     return (uint32_t)min(better, 0xffffffffll);
+}
+
+__device__ __forceinline__ void Row::has(unsigned long long sum) {
+    if (sum == 0) return;
+    const int zeros = __clzll(sum);
+    z = sum, factor = reciprocal(sum << zeros), down = 1 + bits - zeros;
 }
 
 // A cluster per sequence. f32 sums decide which drafts are surely taken and which first one is not; that one's rows, and
@@ -385,7 +394,14 @@ __global__ void __launch_bounds__(kThreads, 4) k_draft_choose(const Args a) {
     int n = 0, verdict;
     bool spent = false;   // s.cta may still be read
     Row p{}, q{};
-    const int bits = 31 - __clz(max(V - 1, 1)), lift = 31 - bits;   // a sum of V numbers m 2^32 >> bits, below 2^(32 + lift), fits 64 bits
+    // Sums are of exponentials in units of 2^(bits - 62), m 2^32 >> bits + shift of an Exact, with what is left cut off. V of them fit
+    // 64 bits with `whole`. Where what was cut off may be more than 2^-28 of a sum z (few tokens have most of a long row, or
+    // the one that does is left out), the sum is made again in units that it needs; a whole number, it is the same
+    // whatever the launch's shape, and so are the units.
+    const int whole = 31 - __clz(max(V - 1, 1));
+    auto finer = [&](unsigned long long z, int bits) {   // (z + V units are more than the sum)
+        return z >> 28 >= (unsigned)V || bits <= -70 ? bits : max(-70, bits + 2 - __clzll(z + V));
+    };
     // this CTA's range, and its warps'
     const int slice = (V + ctas - 1) / ctas, from = min(rank * slice, V), to = min(from + slice, V);
     const int each = (slice + kWarps - 1) / kWarps;
@@ -429,33 +445,34 @@ __global__ void __launch_bounds__(kThreads, 4) k_draft_choose(const Args a) {
         if (greedy) break;
         verdict = n < count ? s.verdict[n] : kRefuse;
         const bool has_q = drafted && n < count;
-        p = Row{kMasked, 0, 0, 0}, q = p;
+        p = Row{kMasked, 0, 0, 0, whole}, q = p;
         if (s.rows[n].alive()) p.most = s.rows[n].most;
         if (has_q && s.rows[sq.targets() + n].alive()) q.most = s.rows[sq.targets() + n].most;
         rp = row_at<T>(a, sq, seq, n);
         rq = has_q ? row_at<T>(a, sq, seq, sq.targets() + n) : nullptr;
         if (rq == nullptr && verdict == kRefuse) break;   // (drawn from p alone: its sum is the draw's)
-        unsigned long long sums[2] = {0, 0};
-        if (p.alive() && q.alive())
-            over_both([&](Exact e, Exact g) { sums[0] += place(e.m, bits + e.shift), sums[1] += place(g.m, bits + g.shift); });
-        else if (p.alive())
-            over_one([&](Exact e, int) { sums[0] += place(e.m, bits + e.shift); });
-        spread(sums[0], sums[1]);
-        spent = true;
-        for (int w = 0; w < 2; ++w) {
-            unsigned long long z = 0;
-            for (int i = 0; i < ctas; ++i) z += s.cta[i][w];
-            if (z == 0) continue;
-            Row &r = w ? q : p;
-            const int zeros = __clzll(z);
-            r.factor = reciprocal(z << zeros);
-            r.down = 32 - lift - zeros;
-            r.z = z;
+        while (true) {
+            unsigned long long sums[2] = {0, 0};
+            if (p.alive() && q.alive())
+                over_both([&](Exact e, Exact g) { sums[0] += place(e.m, p.bits + e.shift), sums[1] += place(g.m, q.bits + g.shift); });
+            else if (p.alive())
+                over_one([&](Exact e, int) { sums[0] += place(e.m, p.bits + e.shift); });
+            if (spent) cluster.sync();   // (s.cta is free again)
+            spread(sums[0], sums[1]);
+            spent = true;
+            unsigned long long z0 = 0, z1 = 0;
+            for (int i = 0; i < ctas; ++i) z0 += s.cta[i][0], z1 += s.cta[i][1];
+            const int bits0 = z0 ? finer(z0, p.bits) : p.bits, bits1 = z1 ? finer(z1, q.bits) : q.bits;
+            if (bits0 == p.bits && bits1 == q.bits) {
+                p.has(z0), q.has(z1);
+                break;
+            }
+            p.bits = bits0, q.bits = bits1;
         }
         if (verdict == kRefuse) break;
         if (tid == n) {   // an unsure draft: the same in every CTA
             auto of = [&](float logit, const Row &r) {   // (of values that the draw takes for 0 too)
-                return r.factor && !masked(logit) ? exp(((double)logit - (double)r.most) / (double)temperature) / ((double)r.z * exp2(-31.0 - lift)) : 0.0;
+                return r.factor && !masked(logit) ? exp(((double)logit - (double)r.most) / (double)temperature) / ((double)r.z * exp2(r.bits - 62.0)) : 0.0;
             };
             s.verdict[n] = (double)x_u * (rq != nullptr ? of(x_draft, q) : 1.0) < of(x_target, p) ? kTake : kRefuse;
         }
@@ -468,7 +485,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_draft_choose(const Args a) {
     const size_t out = (size_t)seq * (K + 1);
     const bool minus_q = rq != nullptr && q.factor != 0;
     const int gone = n < count && a.draft == nullptr ? tokens[n] : -1;   // (without draft logits all of q is on the draft)
-    auto weight = [&](Exact e, int i, bool plain) { return i == gone && !plain ? 0 : place(e.m, bits + e.shift); };
+    int units = p.z ? p.bits : whole;   // of the sum of p, where q is not taken off
+    auto weight = [&](Exact e, int i, bool plain) { return i == gone && !plain ? 0 : place(e.m, units + e.shift); };
     auto left = [&](Exact e, Exact g, bool plain) {   // of p without q, in units of 2^-62
         const unsigned long long w = place(__umulhi(e.m, p.factor), p.down + e.shift);
         const unsigned long long v = plain ? 0 : place(__umulhi(g.m, q.factor), q.down + g.shift);
@@ -483,13 +501,19 @@ __global__ void __launch_bounds__(kThreads, 4) k_draft_choose(const Args a) {
         if (minus_q) over_both([&](Exact e, Exact g) { sum += left(e, g, plain); });
         else over_one([&](Exact e, int i) { sum += weight(e, i, plain); });
         spread(sum, 0);
-        before = 0;
+        total = before = 0;
         for (int i = 0; i < ctas; ++i) {
             if (i < rank) before += s.cta[i][0];
             total += s.cta[i][0];
         }
+        const int bits = minus_q ? units : finer(total, units);
+        if (bits != units) {
+            units = bits;
+            continue;
+        }
         if (total != 0 || plain) break;
         plain = true;
+        units = p.z ? p.bits : whole;
     }
     if (total != 0) {
         const unsigned long long un64 = u_draw >= 1.f ? ~0ull : (unsigned long long)(u_draw * 0x1p64f);
@@ -522,16 +546,16 @@ __global__ void __launch_bounds__(kThreads, 4) k_draft_choose(const Args a) {
                 for (unsigned long long v; border - at >= (v = at_token(i)); ++i) at += v;
                 a.tokens_out[out + n] = i;
                 if (a.logprobs) {
-                    unsigned long long z = p.z;
-                    if (z == 0) {   // (no sum of p alone was made: it is the draw's, and the token's that was left out)
-                        z = total;
+                    float z = (float)p.z * exp2f((float)(p.bits - 62));
+                    if (p.z == 0) {   // (no sum of p alone was made: it is the draw's, and the token's that was left out)
+                        z = (float)total * exp2f((float)(units - 62));
                         if (gone >= 0 && gone < V && !plain) {
                             Exact e, g;
                             exact_exp2(load_logit(rp, gone), 0.f, f2(-p.most, 0.f), c, s.roots, e, g);
-                            z += place(e.m, bits + e.shift);
+                            z += (float)e.m * exp2f((float)(-30 - e.shift));
                         }
                     }
-                    a.logprobs[out + n] = (load_logit(rp, i) - p.most) / temperature - logf((float)z * exp2f(-(float)(31 + lift)));
+                    a.logprobs[out + n] = (load_logit(rp, i) - p.most) / temperature - logf(z);
                 }
             }
         }

@@ -130,3 +130,81 @@ def test_bf16_logits_far_apart_in_size(verify, top, rest):
     same, _, lp32 = verify(x.float().expand(S, 1, vocab), none, u)
     assert torch.equal(out, same)
     assert (lp - lp32).abs().max() <= 1e-6
+
+
+def behind(u, first, parts):
+    """Which token a draw meets, as a real number of tokens behind the first: `first` is the first token's weight, parts the
+    (tokens, weight of each) that follow. Also how many of its tokens the whole sum is."""
+    total = first + sum(n * w for n, w in parts)
+    left, at = u * total - first, 0.0
+    if left < 0:
+        return -1.0, 1.0
+    for n, w in parts:
+        if left < n * w:
+            return at + left / w, total / w
+        left, at = left - n * w, at + n
+    return at, total / parts[-1][1]
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("top,vocab", [(16.0, 1 << 24), (16.0, 1 << 26), (12.0, 1 << 26), (20.0, 1 << 26), (10.0, 151936), (30.0, 262144)])
+def test_a_large_logit_before_many_small_ones(verify, dt, top, vocab):
+    """One token with most of a long row, which the others have the rest of: draws against 64 bits. An exponential is off by 2^-29 of itself,
+    a sum by what its units cut off, 2^-28: 2^-27 of the sum, in tokens."""
+    x = torch.full((vocab,), -0.5, dtype=DT[dt], device="cuda")
+    x[vocab // 2:] = 0
+    x[0] = top
+    S = 64
+    total = 1 + math.exp(-top) * (vocab // 2) + math.exp(-top - 0.5) * (vocab // 2 - 1)
+    u = ((1 / total) + (1 - 1 / total) * (0.02 + 0.96 * torch.arange(S, dtype=torch.float64) / S)).float()[:, None]
+    out, _, lp = verify(x.expand(S, 1, vocab), torch.zeros(S, 0, dtype=torch.int32, device="cuda"), u.cuda())
+    for s in range(S):
+        at, tokens = behind(float(u[s, 0]), 1.0, [(vocab // 2 - 1, math.exp(-top - 0.5)), (vocab // 2, math.exp(-top))])
+        near, got = tokens * 2.0 ** -27, int(out[s, 0])
+        assert math.floor(at - near) <= got - 1 <= math.floor(at + near), (s, got, at, near)
+        if got > 0:
+            assert abs(float(lp[s, 0]) - (float(x[got]) - top - math.log(total))) <= 1e-5
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("gone,small,vocab", [(0, 40.0, 100003), (77, 40.0, 1000), (100002, 25.0, 100003), (5, 47.0, 2048), (5, 47.0, 151936), (0, 30.0, 1 << 24)])
+def test_what_is_left_of_a_refused_token(verify, dt, gone, small, vocab):
+    """A certain draft that has nearly all of p, refused by u = 1: the next token is one of the others, in their proportions, not the draft."""
+    x = torch.full((vocab,), -small, dtype=DT[dt], device="cuda")
+    x[vocab // 2:] = -small + 1
+    x[gone] = 0
+    S = 32
+    u = torch.ones(S, 2)
+    u[:, 1] = 0.01 + 0.98 * torch.arange(S) / S
+    tokens = torch.full((S, 1), gone, dtype=torch.int32)
+    out, n, lp = (t.cpu() for t in verify(x.expand(S, 2, vocab), tokens.cuda(), u.cuda()))
+    assert (n == 0).all() and (out[:, 1] == -1).all()
+    half = vocab // 2
+    parts = [(half - (gone < half), math.exp(-1.0)), (vocab - half - (gone >= half), 1.0)]
+    for s in range(S):
+        at, of = behind(float(u[s, 1]), 0.0, parts)
+        near = of * 2.0 ** -27
+        got = int(out[s, 0])
+        assert got != gone
+        assert math.floor(at - near) <= got - (got > gone) <= math.floor(at + near), (s, got, at, near)
+        total = 1 + sum(n * w for n, w in parts) * math.exp(1 - small)
+        assert abs(float(lp[s, 0]) - (float(x[got]) - math.log(total))) <= 1e-5
+
+
+def test_a_draft_near_its_border_beside_a_large_logit(verify):
+    """u q next to p, both rows with most on one token and 2^24 small ones: decided by sums of both rows as 64 bits decide."""
+    vocab, top = 1 << 24, 17.0
+    p = torch.zeros(vocab, device="cuda")
+    p[0] = top
+    q = torch.full((vocab,), 1.0, device="cuda")
+    q[1] = top + 0.5
+    token = 12345
+    lp, lq = float(logs64(p)[token]), float(logs64(q)[token])
+    ratio = math.exp(lp - lq)
+    assert ratio < 1
+    near = torch.tensor([1 - 2e-7, 1 + 2e-7, 1 - 1e-6, 1 + 1e-6], dtype=torch.float64)
+    u = torch.full((4, 2), 0.5)
+    u[:, 0] = (ratio * near).float()
+    tokens = torch.full((4, 1), token, dtype=torch.int32, device="cuda")
+    _, n, _ = verify(p.expand(4, 2, vocab), tokens, u.cuda(), draft_logits=q.expand(4, 1, vocab))
+    assert n.tolist() == [int(float(u[i, 0]) < ratio) for i in range(4)] == [1, 0, 1, 0]
