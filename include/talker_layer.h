@@ -158,7 +158,8 @@ talker_status talker_w4_quantize(const void *w, int dtype, int64_t row_stride, i
  * writes them. out: rows of n values, out_row apart, F32 or BF16; residual likewise, res_row
  * apart, in out's type; it may be out itself (same stride). Other overlaps are not allowed.
  * Products of codes and x are made by the tensor cores with f32 sums: bf16 x enters exactly
- * (values below 2^-31 of a row's largest lose bits), others with 22 bits in two parts. The order
+ * (values below 2^-31 of a row's largest lose bits), others with 22 bits in two parts (values
+ * below 2^-16 of a row's largest with fewer, down to 2^-39 of it). The order
  * of a sum depends on n, k, rows and types alone. A row of x with a NaN or an infinity gives
  * NaN. (So would a copy of weights that does not arrive within a second, from there on.)
  * Made for few rows: 32 columns of x, one a bf16 row and two any other, in one pass over the

@@ -258,8 +258,8 @@ __device__ __forceinline__ unsigned long long warp_sum64(unsigned long long v) {
 }
 
 // The rows' parts, a warp each, for calls that a sequence's cluster would read too slowly. One pass: the running largest
-// and the sum of exponentials. 24 sequences of up to 5 drafts of 100003 tokens, f32, both models' logits (58 MB): 13 us,
-// 65% of the copy rate; a multiply-add, an exponential and two maxima a value.
+// and the sum of exponentials. 24 sequences of up to 5 drafts of 100003 tokens, f32, both models' logits (58 MB): 14 us,
+// 61% of the copy rate; a multiply-add, an exponential and two maxima a value, and a few additions a vector that keep the sum.
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32) k_draft_rows(const Args a) {
     const int seq = blockIdx.y, t = blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -315,9 +315,11 @@ __device__ __forceinline__ void Row::has(unsigned long long sum) {
 // 29 bits and sums in whole numbers: which token a uniform number meets is a question of sums of 10^5 terms next to one
 // another, where f32 would err once in some hundred draws.
 // Small calls are a chain of latencies: a cluster's start, two or three of its barriers (a microsecond or two each), a
-// draw (one sequence of 4 drafts of 2048 tokens: 9 us). Large ones are bound by instructions: two exponentials of some 25
-// a token, once for the sums and once for the draw (the batch above: 30 us of 46 with its rows). With f64, and the rows
-// read by the cluster: 376 us; rows by the whole GPU 79; exponentials in packed f32 and sixteen CTAs 52; every CTA deciding by itself 46.
+// draw (one sequence of 4 drafts of 2048 tokens: 9 us). Large ones make an exponential of some 25 instructions twice a token, once
+// for the sums and once for the draw (the batch above: 30 us of 43 with its rows), but are bound by waits, not by their issue:
+// with 28% of a multiprocessor's warps there (64 registers, clusters of unequal work) instructions are issued in 38% of the
+// cycles, and most stalls are on loads and barriers. With f64, and the rows read by the cluster: 376 us; rows by the whole
+// GPU 79; exponentials in packed f32 and sixteen CTAs 52; every CTA deciding by itself 46.
 template <typename T, bool OWN>
 __global__ void __launch_bounds__(kThreads, 4) k_draft_choose(const Args a) {
     __shared__ Shared s;
@@ -582,10 +584,10 @@ bool sizes_ok(int n_seq, int n_draft, int vocab) {
 }
 
 // How a call runs. A sequence's own cluster reads its rows while they are few logits; else the whole GPU does, in a launch
-// before (bf16, 4 drafts: 8192 tokens 9.9 against 11.2 us, 32768 tokens 14.5 against 12.9). CTAs of a cluster: each has
-// something to do, and all clusters are soon there, which take longer to begin the more CTAs they have (4 drafts of 2048
-// tokens: one sequence 8.8 us with eight, 9.9 with four; 28 sequences 13.1 and 11.6; 64 17.5 and 13.5; 8 sequences of 8
-// drafts of 100003 tokens: 37.6 with eight, 32.6 with sixteen).
+// before (bf16, 4 drafts, one sequence: 8192 tokens 9.2 against 10.9 us, 32768 tokens 13.7 against 12). CTAs of a cluster: each
+// has something to do, and all clusters are soon there, which take longer to begin the more CTAs they have (4 drafts of 2048
+// tokens: one sequence 9.0 us with eight, 9.6 with four; 64 sequences 13.1 with eight, 11.2 with two; 8 sequences of 8
+// drafts of 100003 tokens: 40 with eight, 33.7 with sixteen).
 constexpr int kOwnLogits = 1 << 17;
 struct Shape {
     bool own;

@@ -146,9 +146,11 @@ struct Raw<__nv_bfloat16> {
 // 62 us without); with C = 0 (rows of more than 16384 values) they are read again. For e4m3 the norm's factor cancels: a
 // code is that of s gain over the largest of its block.
 // Few threads with several chunks each: what a thread does for a row once is shared by more values, and more CTAs are out
-// of step with one another (4096 x 5120: one chunk of 640 threads 57 us, two of 320 54, four of 160 40, which is 86% of the
-// copy rate). Narrow rows take 4 to 16 threads, so that a warp has several (65536 x 128 bf16: a warp each 31 us, four
-// threads each 12). A lone row of 1024: 3 us, all of it latency.
+// of step with one another (4096 x 5120: one chunk of 640 threads 57 us, two of 320 54, four of 160 41, which is 83% of the
+// copy rate; 65536 x 1024 bf16 to bf16 47.5, 83%, 89% with a residual). Narrow rows take 4 to 16 threads, so that a warp has
+// several (65536 x 128 bf16, a call by itself: a warp each 31 us, four threads each 12; one of many 7.6). In blocks of 128
+// they take sixteen, and three of their four chunks are empty: 131072 x 128 to e4m3 93 us, 29%. A lone row of 1024: 3 us, all of
+// it latency.
 constexpr int most_threads(int c) { return c == 0 ? 1024 : 512; }
 template <typename TX, typename TR, typename TY, int C>
 __global__ void __launch_bounds__(most_threads(C), 1) k_rms_norm(const NormArgs a) {
@@ -263,7 +265,7 @@ __global__ void __launch_bounds__(most_threads(C), 1) k_rms_norm(const NormArgs 
 // neighbouring values of it at a time, so that loads and stores touch whole sectors. STAGED: rows pass through shared
 // memory, where the next ones arrive while these are worked on, in whole 16 bytes but for their ends; otherwise (two rows
 // of more than 220 KB) they are read twice. What bounds it are the instructions, a value at a time (60 each; 69% of the
-// issue slots): 4001 x 5003 bf16 + f32 to e4m3 in blocks 53 us, 61% of the copy rate (148 from registers, without shared
+// issue slots): 4001 x 5003 bf16 + f32 to e4m3 in blocks 51 us, 64% of the copy rate (as calls by themselves, 2 to 7 us more: 53; 148 from registers, without shared
 // memory; 74 with a thread's values as far apart as a row has threads, whose addresses take instructions), 2000 x 10001
 // bf16 + bf16 to f32 49 (207). A thread for 16 values (74 us then; for 8: 84, for 32: 82); of narrow rows 8 or 16 threads
 // (100000 x 47: a warp each 57 us, eight threads each 22), unless a warp's lanes have to be blocks.

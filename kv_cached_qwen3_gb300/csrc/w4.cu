@@ -269,7 +269,7 @@ __device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-// Codes of one word as the operand's registers: fields 0 and 4 of v (or of v >> 8) under 1024, whose last place is 1, are
+// Codes of one word as the operand's registers, by a widely published method (an integer under an fp16 power of two): fields 0 and 4 of v (or of v >> 8) under 1024, whose last place is 1, are
 // 1024 + c; fields 1 and 5 are 1024 + 16 c. Taking off 1024 + z, or 64 + z after a sixteenth, leaves c - z, exactly.
 struct Zero {
     uint32_t a, b;   // -(1024 + z) and -(64 + z), twice each
@@ -360,7 +360,7 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity) {
 // from there on.
 // Few rows are bound by the instructions that make codes operands, nine for the four registers of an MMA. 24576 x 8192,
 // groups of 128, one row: 26 us for 104 MB (59% of the copy rate, 59% of the issue slots, a quarter of the tensor cores'
-// cycles), 30 with the kernels around it; 8 bf16 rows 29, 16 37, 32 56 (MMAs and their operands), 64 in two passes 100. Equal
+// cycles), 30 with the kernels around it; 8 bf16 rows 29, 16 36, 32 53 (MMAs and their operands), 64 in two passes 94. Equal
 // steps: with whole tiles to a CTA the last ones run alone (49 us); a ring and warps of their own
 // instead of a barrier a step: 36; codes as whole numbers under a scale a group instead of scaled ones: 31. Codes that keep
 // their offset of 8, taken off the sum: an instruction less for two, but errors of 1e-6 instead of 9e-8.
