@@ -41,8 +41,8 @@ extern "C" {
  * Probabilities that decide (p and q of a draft near its border, all of the row that is
  * drawn from) are made to about 2^-29 of themselves and summed as whole numbers, in units
  * that cut off less than 2^-28 of a sum (those below 2^-70 of the row's largest count as 0,
- * and where q is taken off, those below 2^-62), so
- * neither a row's address nor the launch's shape changes a token; the sums of taken drafts'
+ * and where q is taken off, those below 2^-62; what is left of p then has the errors of both).
+ * So neither a row's address nor the launch's shape changes a token; the sums of taken drafts'
  * logprobs are f32.
  *
  * target: row i of sequence s lies at s * target_seq + i * target_row elements, vocab

@@ -109,7 +109,8 @@ typedef struct {
 /* Rotate the heads of n_sets (1 or 2, for example q and k; HOST array) sets of heads of
  * the same rows. positions: int32 [streams][rows], any value (negative ones rotate back). turns: device table.
  * dtype F32 or BF16 for all. Errors: EINVAL (null pointers, sizes below 0, head_dim not in 2..512,
- * rotary_dim odd or above head_dim, more than 16384 heads in a set, streams * rows above 2^30, several heads written at a stride of 0), ECUDA. */
+ * rotary_dim odd or above head_dim, more than 16384 heads in a set, streams * rows above 2^30, several
+ * heads written at a stride of 0), ECUDA. */
 talker_status talker_rotate(const uint64_t *turns, float amplitude, int head_dim, int rotary_dim, int interleaved,
                             const int32_t *positions, int streams, int rows, const talker_heads *sets, int n_sets,
                             int dtype, void *cuda_stream);

@@ -265,9 +265,9 @@ __global__ void __launch_bounds__(most_threads(C), 1) k_rms_norm(const NormArgs 
 // neighbouring values of it at a time, so that loads and stores touch whole sectors. STAGED: rows pass through shared
 // memory, where the next ones arrive while these are worked on, in whole 16 bytes but for their ends; otherwise (two rows
 // of more than 220 KB) they are read twice. What bounds it are the instructions, a value at a time (60 each; 69% of the
-// issue slots): 4001 x 5003 bf16 + f32 to e4m3 in blocks 51 us, 64% of the copy rate (as calls by themselves, 2 to 7 us more: 53; 148 from registers, without shared
-// memory; 74 with a thread's values as far apart as a row has threads, whose addresses take instructions), 2000 x 10001
-// bf16 + bf16 to f32 49 (207). A thread for 16 values (74 us then; for 8: 84, for 32: 82); of narrow rows 8 or 16 threads
+// issue slots): 4001 x 5003 bf16 + f32 to e4m3 in blocks 51 us, 64% of the copy rate. As calls by themselves, 2 to 7 us
+// more: 53 (148 from registers, without shared memory; 74 with a thread's values as far apart as a row has threads, whose
+// addresses take instructions), 2000 x 10001 bf16 + bf16 to f32 49 (207). A thread for 16 values (74 us then; for 8: 84, for 32: 82); of narrow rows 8 or 16 threads
 // (100000 x 47: a warp each 57 us, eight threads each 22), unless a warp's lanes have to be blocks.
 constexpr int kOddThreads = 512;
 constexpr int kMostStaged = 220 * 1024;

@@ -269,8 +269,9 @@ __device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-// Codes of one word as the operand's registers, by a widely published method (an integer under an fp16 power of two): fields 0 and 4 of v (or of v >> 8) under 1024, whose last place is 1, are
-// 1024 + c; fields 1 and 5 are 1024 + 16 c. Taking off 1024 + z, or 64 + z after a sixteenth, leaves c - z, exactly.
+// Codes of one word as the operand's registers, by a widely published method (an integer under an fp16 power of two): fields
+// 0 and 4 of v (or of v >> 8) under 1024, whose last place is 1, are 1024 + c; fields 1 and 5 are 1024 + 16 c. Taking off
+// 1024 + z, or 64 + z after a sixteenth, leaves c - z, exactly.
 struct Zero {
     uint32_t a, b;   // -(1024 + z) and -(64 + z), twice each
 };
